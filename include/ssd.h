@@ -234,6 +234,124 @@ typedef struct {
 ssd_status ssd_profile_begin(void);
 int32_t ssd_profile_end(ssd_kernel_time *out, int32_t max_entries);
 
+/* ======================= retention: linear attention with a decay for each head, and the norm behind it
+ *
+ * Linear attention.  Per query head h, with lam = exp(log_decay[h]) and kv = h / (nheads / nheads_kv), for the
+ * tokens t of one sequence in order:
+ *     S_t = lam S_{t-1} + k_{t,kv}^T v_{t,kv}      (headdim_k x headdim_v; S_{-1}: the initial state, or zero)
+ *     o_t = scale q_{t,h} S_t
+ * Sequences either all have dims.seqlen tokens (cu_seqlens NULL; token t of sequence s is row s * seqlen + t), or
+ * are packed into dims.total_tokens rows: sequence s covers rows [cu_seqlens[s], cu_seqlens[s+1]), cu_seqlens
+ * (nseq + 1) int32 device values, non-decreasing, from 0 to total_tokens (not checked on the host; values outside
+ * [0, total_tokens] are clamped, rows outside every sequence are neither read as data nor written).  Sequences may
+ * be empty or of one token; with no token the final state is the initial state.
+ * Tensors are token-major with their own token strides, heads and channels contiguous within a token:
+ *   q (T, nheads * headdim_k), k (T, nheads_kv * headdim_k), v (T, nheads_kv * headdim_v), o (T, nheads * headdim_v)
+ * in dims.dtype, 16-byte aligned, strides a multiple of 8 (bf16) or 4 (fp32) elements, so views into one
+ * projection output are read in place.  log_decay (nheads) fp32, at most 0 (-inf: the state forgets everything at
+ * each token).  States (nseq, nheads, headdim_k, headdim_v) fp32, contiguous, 16-byte aligned.
+ * Arithmetic: fp32; on the bf16 tensor-core path (headdim_k and headdim_v at most 128) the products take bf16
+ * operands with fp32 accumulation, and what reaches the state is split into three bf16 terms, so that states keep
+ * fp32 precision.  A NaN or infinity in a token can reach every output of the same 64-token block of its own
+ * sequence and head, and those of later tokens; other sequences are not affected.
+ * Envelope: headdim_k and headdim_v multiples of 8, at most 256; nheads * headdim and total rows as in ssd_dims;
+ * else SSD_ERR_UNSUPPORTED.  All sums have a fixed order: equal inputs give equal bits. */
+typedef struct {
+  int32_t nseq;
+  int32_t seqlen;       /* tokens of every sequence; ignored when packed */
+  int32_t total_tokens; /* packed: rows of the token-major tensors; else 0 or nseq * seqlen */
+  int32_t packed;       /* 1: cu_seqlens gives the sequences */
+  int32_t nheads, nheads_kv, headdim_k, headdim_v;
+  int32_t dtype; /* ssd_dtype of q, k, v, o and their gradients */
+} ssd_linear_attn_dims;
+
+typedef struct {
+  const void *q; int64_t q_tok_stride;
+  const void *k; int64_t k_tok_stride;
+  const void *v; int64_t v_tok_stride;
+  const float *log_decay;
+  const float *initial_states; /* or NULL: zero */
+  const int32_t *cu_seqlens;   /* exactly when dims.packed */
+  float scale;
+} ssd_linear_attn_inputs;
+
+/* Gradients, written (not accumulated).  dq, dk, dv: layout rules of q, k, v, own token strides; dk and dv are
+ * summed over the query heads that share a key/value head.  dinitial_states fp32: written when not NULL (it does
+ * not need initial_states to be given).  log_decay is a constant of the model and has no gradient. */
+typedef struct {
+  void *dq; int64_t dq_tok_stride;
+  void *dk; int64_t dk_tok_stride;
+  void *dv; int64_t dv_tok_stride;
+  float *dinitial_states;
+} ssd_linear_attn_grads;
+
+/* Bytes of device workspace of ssd_linear_attn_forward (backward = 0) or _backward (1); 0 if dims are invalid. */
+size_t ssd_linear_attn_workspace_size(const ssd_linear_attn_dims *dims, int backward);
+
+/* Forward.  final_states: the state after each sequence's last token, or NULL. */
+ssd_status ssd_linear_attn_forward(const ssd_linear_attn_dims *dims, const ssd_linear_attn_inputs *in, void *o,
+                                   int64_t o_tok_stride, float *final_states, void *workspace, size_t ws_bytes,
+                                   ssd_stream_t stream);
+
+/* Backward of <do, o> + <dfinal_states, final_states> (dfinal_states NULL: zero).  do is named dout here: layout
+ * rules of o.  Nothing but the inputs is needed from the forward pass. */
+ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims *dims, const ssd_linear_attn_inputs *in,
+                                    const void *dout, int64_t dout_tok_stride, const float *dfinal_states,
+                                    const ssd_linear_attn_grads *grads, void *workspace, size_t ws_bytes,
+                                    ssd_stream_t stream);
+
+/* One token of each of dims.nseq rows (dims.seqlen must be 1, dims.packed 0), against a cache of states
+ * (nslots, nheads, headdim_k, headdim_v) fp32, updated in place: row r uses slot slot_idx[r] (slot_idx NULL: slot
+ * r).  A row whose slot is outside [0, nslots) leaves the cache alone and writes zeros to its o; no two rows may
+ * share a slot (which of them would win is undefined).  in->initial_states and in->cu_seqlens must be NULL.  No
+ * workspace. */
+ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_linear_attn_inputs *in, float *states,
+                                int32_t nslots, const int32_t *slot_idx, void *o, int64_t o_tok_stride,
+                                ssd_stream_t stream);
+
+/* Group norm with an activation, channels last.  x (nsamples, nrows, channels): row r of sample n is row
+ * n * nrows + r of a row-major tensor with its own row stride (channels contiguous).  Per sample and group of
+ * channels / groups consecutive channels, over its nrows * channels / groups values:
+ *     u = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps)   (var: the mean squared deviation)
+ *     y = u (SSD_ACT_NONE), u sigmoid(u) (SSD_ACT_SILU), u z sigmoid(z) (SSD_ACT_GATE, z a tensor like x)
+ * nrows = 1 is the norm of each head of each token that retention uses.  weight and bias (channels) fp32, or NULL
+ * (1 and 0).  mean and rstd (nsamples, groups) fp32 are written by the forward pass (each may be NULL) and read by
+ * the backward pass.  Any number of channels per group; rows of 16-byte aligned tensors whose strides and group
+ * widths are multiples of 8 elements move as 16-byte vectors, others element by element. Statistics are summed
+ * in fp32 as deviations (no difference of large sums). */
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GATE = 2 } ssd_activation;
+
+typedef struct {
+  int32_t nsamples, nrows, channels, groups;
+  int32_t dtype;      /* ssd_dtype of x, z, y and their gradients */
+  int32_t activation; /* ssd_activation */
+} ssd_group_norm_dims;
+
+typedef struct {
+  const void *x; int64_t x_row_stride;
+  const void *z; int64_t z_row_stride; /* exactly with SSD_ACT_GATE */
+  const float *weight, *bias;
+  float eps;
+} ssd_group_norm_inputs;
+
+/* Gradients, written (not accumulated); dz exactly with SSD_ACT_GATE; dweight and dbias may be NULL. */
+typedef struct {
+  void *dx; int64_t dx_row_stride;
+  void *dz; int64_t dz_row_stride;
+  float *dweight, *dbias;
+} ssd_group_norm_grads;
+
+size_t ssd_group_norm_workspace_size(const ssd_group_norm_dims *dims, int backward);
+
+ssd_status ssd_group_norm_forward(const ssd_group_norm_dims *dims, const ssd_group_norm_inputs *in, void *y,
+                                  int64_t y_row_stride, float *mean, float *rstd, void *workspace, size_t ws_bytes,
+                                  ssd_stream_t stream);
+
+ssd_status ssd_group_norm_backward(const ssd_group_norm_dims *dims, const ssd_group_norm_inputs *in, const void *dy,
+                                   int64_t dy_row_stride, const float *mean, const float *rstd,
+                                   const ssd_group_norm_grads *grads, void *workspace, size_t ws_bytes,
+                                   ssd_stream_t stream);
+
 /* Static description of a status code. */
 const char *ssd_status_string(ssd_status status);
 

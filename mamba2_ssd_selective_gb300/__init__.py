@@ -2,9 +2,9 @@
 
 The functions below carry the C names (``ssd_forward``, ``ssd_backward``,
 ``ssd_workspace_size``, ``ssd_cu_seqlens_to_seq_idx``, ``ssd_device_status``,
-``ssd_status_string``) and only marshal arguments: torch tensors become device
-pointers, the current torch stream becomes the cudaStream_t.  Every step of the
-computation runs in libssd's CUDA kernels; there is no Python or CPU fallback,
+``ssd_status_string``; those of the retention operators are in ``retention.py``) and
+only marshal arguments: torch tensors become device pointers, the current torch
+stream becomes the cudaStream_t.  Every step of the computation runs in libssd's CUDA kernels; there is no Python or CPU fallback,
 and loading fails loudly when the compiled library is missing.
 """
 from __future__ import annotations
@@ -14,7 +14,10 @@ import os
 
 import torch
 
-__all__ = [
+from . import retention
+from .retention import *  # noqa: F401,F403
+
+__all__ = retention.__all__ + [
     "SsdError", "SsdDims", "SsdInputs", "SsdGrads", "load", "ssd_workspace_size", "ssd_forward", "ssd_backward",
     "ssd_forward_static", "STATIC_SCRATCH_BYTES", "ssd_forward_varlen",
     "ssd_cu_seqlens_to_seq_idx", "ssd_device_status", "ssd_set_wait_limit_ns", "DEFAULT_WAIT_LIMIT_NS",
@@ -103,6 +106,7 @@ def load():
         lib.ssd_profile_end.restype = ctypes.c_int32
         lib.ssd_status_string.argtypes = [I]
         lib.ssd_status_string.restype = ctypes.c_char_p
+        retention.declare(lib)
         _lib = lib
     return _lib
 

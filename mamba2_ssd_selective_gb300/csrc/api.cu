@@ -1,21 +1,16 @@
 // libssd C ABI: argument validation, workspace carving and the launch sequence
 // of the forward and backward passes.  Nothing here allocates or synchronises.
-#include <atomic>
-#include <cstring>
 #include <mutex>
 #include <type_traits>
 
 #include "kernels.h"
+#include "launch.h"
 #include "ssd.h"
 
 using namespace ssd;
 
 namespace {
 
-// limit of the kernels' bounded hand-off waits, for every later call
-std::atomic<unsigned long long> g_wait_limit_ns{sm100::kDefaultWaitLimitNs};
-
-int elem_bytes(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
 
 ssd_status check_dims(const ssd_dims *d) {
   if (!d) return SSD_ERR_NULL_PTR;
@@ -56,8 +51,6 @@ Problem problem_from(const ssd_dims *d) {
   pr.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   return pr;
 }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 ssd_status check_inputs(const ssd_dims *d, const ssd_inputs *in, Problem &pr) {
   if (!in) return SSD_ERR_NULL_PTR;
@@ -108,42 +101,6 @@ ssd_status check_inputs(const ssd_dims *d, const ssd_inputs *in, Problem &pr) {
 
 Workspace plan_for(const ssd_dims *d, const Problem &pr, bool backward) {
   return plan_workspace(pr, elem_bytes(d->dtype), backward, d->dtype == SSD_BF16 && tc_envelope(pr), d->gated_norm != 0);
-}
-
-// ---------------------------------------------------------------- profiling
-struct ProfRec {
-  const char *name;
-  int pair;
-};
-constexpr int kProfMax = 65536;
-bool g_prof_on = false;
-cudaEvent_t *g_prof_ev = nullptr;  // 2 * kProfMax events, created on first begin
-ProfRec g_prof_rec[kProfMax];
-int g_prof_n = 0;
-
-struct ProfScope {
-  int idx = -1;
-  cudaStream_t s;
-  ProfScope(const char *name, cudaStream_t st) : s(st) {
-    if (g_prof_on && g_prof_n < kProfMax) {
-      idx = g_prof_n++;
-      g_prof_rec[idx] = {name, idx};
-      cudaEventRecord(g_prof_ev[2 * idx], s);
-    }
-  }
-  ~ProfScope() {
-    if (idx >= 0) cudaEventRecord(g_prof_ev[2 * idx + 1], s);
-  }
-};
-#define SSD_LAUNCH(name, call) \
-  do {                         \
-    ProfScope _ps(name, s);    \
-    call;                      \
-  } while (0)
-
-ssd_status launch_status() {
-  const bool host_err = take_host_error();
-  return (cudaPeekAtLastError() == cudaSuccess && !host_err) ? SSD_OK : SSD_ERR_CUDA;
 }
 
 template <typename T>
@@ -489,42 +446,6 @@ ssd_status ssd_device_status(const void *workspace, ssd_stream_t stream) {
   if (cudaMemcpyAsync(&v, word, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess) return SSD_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return SSD_ERR_CUDA;
   return v == 0 ? SSD_OK : SSD_ERR_DEVICE_TIMEOUT;
-}
-
-uint64_t ssd_set_wait_limit_ns(uint64_t limit_ns) {
-  return g_wait_limit_ns.exchange(limit_ns);
-}
-
-ssd_status ssd_profile_begin(void) {
-  if (!g_prof_ev) {
-    g_prof_ev = new cudaEvent_t[2 * kProfMax];
-    for (int i = 0; i < 2 * kProfMax; ++i)
-      if (cudaEventCreate(&g_prof_ev[i]) != cudaSuccess) return SSD_ERR_CUDA;
-  }
-  g_prof_n = 0;
-  g_prof_on = true;
-  return SSD_OK;
-}
-
-int32_t ssd_profile_end(ssd_kernel_time *out, int32_t max_entries) {
-  g_prof_on = false;
-  if (!g_prof_ev) return 0;
-  int n = 0;
-  for (int i = 0; i < g_prof_n; ++i) {
-    if (cudaEventSynchronize(g_prof_ev[2 * i + 1]) != cudaSuccess) return SSD_ERR_CUDA;
-    float ms = 0.f;
-    if (cudaEventElapsedTime(&ms, g_prof_ev[2 * i], g_prof_ev[2 * i + 1]) != cudaSuccess) return SSD_ERR_CUDA;
-    int j = 0;
-    while (j < n && strcmp(out[j].name, g_prof_rec[i].name) != 0) ++j;
-    if (j == n) {
-      if (n >= max_entries) continue;
-      out[n++] = {g_prof_rec[i].name, 0, 0.f};
-    }
-    out[j].launches += 1;
-    out[j].total_ms += ms;
-  }
-  g_prof_n = 0;
-  return n;
 }
 
 const char *ssd_status_string(ssd_status status) {

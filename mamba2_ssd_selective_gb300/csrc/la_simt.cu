@@ -1,0 +1,347 @@
+// Linear attention with a decay for each head on the CUDA cores: fp32 tensors,
+// and widths outside the tensor-core kernel's envelope.
+//
+// A block of 128 threads takes one segment of one sequence, one query head and
+// 64 columns of v, and walks the segment in blocks of 32 tokens with the state's
+// columns S (dk x 64) in shared memory:
+//     A_ij = q_i . k_j lam^|i - j|          (j <= i; reverse: j >= i)
+//     o_i  = lam^a(i) q_i S + sum_j A_ij v_j
+//     S    = lam^nv S + sum_j lam^b(j) k_j^T v_j
+// q and k are staged transposed, so that every product reads its operands as
+// float4; sums are fp32 in a fixed order.
+#include "retention.h"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kC = 32;        // tokens of a block
+constexpr int kLdC = kC + 4;  // padded row of q, k, A (floats), float4 aligned
+constexpr int kTV = 64;       // columns of v
+constexpr int kLdV = kTV + 4;
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2 *>(p) =
+      make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// rows [0, nv) of a (kC x d) tile of a token-major tensor, transposed into dst[d][kLdC]; rows past nv are zero
+template <typename T>
+__device__ __forceinline__ void stage_transposed(float *dst, const T *src, long long stride, int nv, int d) {
+  const int r = threadIdx.x & 31;
+  for (int x = threadIdx.x >> 5; x < d / 8; x += kThreads / 32) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r < nv) load8(src + (long long)r * stride + 8 * x, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dst[(8 * x + i) * kLdC + r] = v[i];
+  }
+}
+
+template <typename T, bool REV, bool SUMMARY>
+__global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
+  extern __shared__ __align__(16) float sm[];
+  const int dkp = (p.dk + 63) & ~63;
+  float *Qt = sm, *Kt = Qt + dkp * kLdC, *S = Kt + dkp * kLdC, *V = S + dkp * kLdV, *At = V + kC * kLdV,
+        *pw = At + kC * kLdC;  // pw[0..kC]: lam^n
+  LaUnit u;
+  if (!la_find_unit(p, blockIdx.x, u)) return;  // every warp finds the same
+  const int h = blockIdx.y, c0 = blockIdx.z * kTV, tid = threadIdx.x, ncol = min(kTV, p.dv - c0);
+  const float g = __ldg(p.g + h);
+  const T *q = static_cast<const T *>(p.q) + u.t0 * p.qs + (h / p.gq) * p.dk;
+  const T *k = static_cast<const T *>(p.k) + u.t0 * p.ks + (h / p.gk) * p.dk;
+  const T *v = static_cast<const T *>(p.v) + u.t0 * p.vs + (h / p.gv) * p.dv + c0;
+  const size_t dd = (size_t)p.dk * p.dv;
+
+  if (tid <= kC) pw[tid] = la_pow(g, tid);
+  const float2 carry_full = la_pow2(g, kC);
+  // q and k rows past dk (up to the padded width) stay zero
+  for (int e = p.dk * kLdC + tid; e < dkp * kLdC; e += kThreads) Qt[e] = Kt[e] = 0.f;
+  {
+    const float *in = nullptr;
+    int sa = p.sa, sb = p.sb;
+    if (SUMMARY) {
+    } else if (p.split) {
+      in = p.seg_state + ((size_t)blockIdx.x * p.H + h) * dd;
+      sa = p.dv;
+      sb = 1;
+    } else if (p.init) {
+      in = p.init + ((size_t)u.seq * p.H + h) * dd;
+    }
+    for (int e = tid; e < dkp * kTV; e += kThreads) {
+      const int a = e / kTV, b = e % kTV;
+      S[a * kLdV + b] = in && a < p.dk && b < ncol ? in[(size_t)a * sa + (size_t)(c0 + b) * sb] : 0.f;
+    }
+  }
+  const int nb = (u.len + kC - 1) / kC;
+  for (int ib = 0; ib < nb; ++ib) {
+    const int blk = REV ? nb - 1 - ib : ib, r0 = blk * kC, nv = min(kC, u.len - r0);
+    __syncthreads();  // the previous block's operands have been read
+    if (!SUMMARY) stage_transposed(Qt, q + (long long)r0 * p.qs, p.qs, nv, p.dk);
+    stage_transposed(Kt, k + (long long)r0 * p.ks, p.ks, nv, p.dk);
+    for (int e = tid; e < kC * (kTV / 8); e += kThreads) {
+      const int r = e / (kTV / 8), x = e % (kTV / 8);
+      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (r < nv && 8 * x < ncol) load8(v + (long long)(r0 + r) * p.vs + 8 * x, w);
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<float4 *>(V + r * kLdV + 8 * x + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+    __syncthreads();
+    if (!SUMMARY) {
+      {  // A: 2 rows x 4 columns a thread, stored transposed
+        const int i0 = 2 * (tid >> 3), j0 = 4 * (tid & 7);
+        float acc[2][4] = {};
+#pragma unroll 4
+        for (int x = 0; x < p.dk; ++x) {
+          const float2 a = *reinterpret_cast<const float2 *>(Qt + x * kLdC + i0);
+          const float4 b = *reinterpret_cast<const float4 *>(Kt + x * kLdC + j0);
+          const float bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[0][j] = fmaf(a.x, bv[j], acc[0][j]);
+            acc[1][j] = fmaf(a.y, bv[j], acc[1][j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 out;
+          const int d0 = REV ? j0 + j - i0 : i0 - j0 - j, d1 = REV ? d0 - 1 : d0 + 1;
+          out.x = d0 >= 0 ? acc[0][j] * (pw[d0] * p.p_scale) : 0.f;
+          out.y = d1 >= 0 ? acc[1][j] * (pw[d1] * p.p_scale) : 0.f;
+          *reinterpret_cast<float2 *>(At + (j0 + j) * kLdC + i0) = out;
+        }
+      }
+      __syncthreads();
+      // o: 4 rows x 4 columns a thread
+      const int i0 = 4 * (tid >> 4), n0 = 4 * (tid & 15);
+      float acc[4][4] = {};
+#pragma unroll 4
+      for (int x = 0; x < p.dk; ++x) {
+        const float4 a = *reinterpret_cast<const float4 *>(Qt + x * kLdC + i0);
+        const float4 b = *reinterpret_cast<const float4 *>(S + x * kLdV + n0);
+        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = p.in_scale * pw[REV ? max(nv - 1 - i0 - i, 0) : i0 + i + 1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] *= w;
+      }
+#pragma unroll 4
+      for (int x = 0; x < kC; ++x) {
+        const float4 a = *reinterpret_cast<const float4 *>(At + x * kLdC + i0);
+        const float4 b = *reinterpret_cast<const float4 *>(V + x * kLdV + n0);
+        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+      }
+      if (n0 < ncol) {  // widths are multiples of 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i0 + i >= nv) break;
+          const long long at = (long long)(u.t0 + r0 + i0 + i) * p.os + (long long)h * p.dv + c0 + n0;
+          if (p.o_f32)
+            store4(static_cast<float *>(p.o) + at, acc[i]);
+          else
+            store4(static_cast<T *>(p.o) + at, acc[i]);
+        }
+      }
+      __syncthreads();  // S has been read
+    }
+    // S: 8 rows x 4 columns a thread, 64 rows at a time
+    const float2 carry = nv == kC ? carry_full : la_pow2(g, nv);
+    const int n0 = 4 * (tid & 15);
+    for (int a0 = 8 * (tid >> 4); a0 < dkp; a0 += 64) {
+      float acc[8][4] = {};
+#pragma unroll 2
+      for (int j0 = 0; j0 < kC; j0 += 4) {
+        float vv[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 b = *reinterpret_cast<const float4 *>(V + (j0 + j) * kLdV + n0);
+          const int r = j0 + j;
+          const float w = r < nv ? p.st_scale * pw[REV ? r + 1 : nv - 1 - r] : 0.f;
+          vv[j][0] = b.x * w; vv[j][1] = b.y * w; vv[j][2] = b.z * w; vv[j][3] = b.w * w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 a = *reinterpret_cast<const float4 *>(Kt + (a0 + i) * kLdC + j0);
+          const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][c] = fmaf(av[j], vv[j][c], acc[i][c]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float4 *sp = reinterpret_cast<float4 *>(S + (a0 + i) * kLdV + n0);
+        float4 t = *sp;
+        t.x = fmaf(t.x, carry.x, fmaf(t.x, carry.y, acc[i][0]));
+        t.y = fmaf(t.y, carry.x, fmaf(t.y, carry.y, acc[i][1]));
+        t.z = fmaf(t.z, carry.x, fmaf(t.z, carry.y, acc[i][2]));
+        t.w = fmaf(t.w, carry.x, fmaf(t.w, carry.y, acc[i][3]));
+        *sp = t;
+      }
+    }
+  }
+  __syncthreads();
+  float *out = nullptr;
+  int sa = p.sa, sb = p.sb;
+  if (SUMMARY) {
+    out = p.seg_state + ((size_t)blockIdx.x * p.H + h) * dd;
+    sa = p.dv;
+    sb = 1;
+  } else if (!p.split && p.fin) {
+    out = p.fin + ((size_t)u.seq * p.H + h) * dd;
+  }
+  if (out)
+    for (int e = tid; e < p.dk * kTV; e += kThreads) {
+      const int a = e / kTV, b = e % kTV;
+      if (b < ncol) out[(size_t)a * sa + (size_t)(c0 + b) * sb] = S[a * kLdV + b];
+    }
+}
+
+// The states between segments: per sequence and head, in processing order,
+//     next = lam^len S + W_seg,   W_seg (from a zero state) replaced by S,
+// and the last `next` is the final state.
+constexpr int kScanThreads = 256;
+template <bool REV>
+__global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPass p) {
+  __shared__ int first;
+  const int nblk = (p.dk * p.dv + kScanThreads - 1) / kScanThreads;
+  const int s = blockIdx.x / nblk, h = blockIdx.y;
+  int a, len;
+  la_seq_bounds(p, s, a, len);
+  const int n = la_segments(p, len);
+  // the sequence's first unit: segments of the sequences before it
+  if (threadIdx.x < 32) {
+    int c = 0;
+    if (!p.cu) {
+      c = s * n;
+    } else {
+      for (int x = threadIdx.x; x < s; x += 32) {
+        int xa, xl;
+        la_seq_bounds(p, x, xa, xl);
+        c += la_segments(p, xl);
+      }
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+    }
+    if (threadIdx.x == 0) first = c;
+  }
+  __syncthreads();
+  const int u0 = first;
+  if (u0 + n > p.nunits) return;  // cu_seqlens that do not partition the rows
+  const int dd = p.dk * p.dv, e = (blockIdx.x % nblk) * kScanThreads + threadIdx.x;
+  if (e >= dd) return;
+  const size_t user = ((size_t)s * p.H + h) * dd + (size_t)(e / p.dv) * p.sa + (size_t)(e % p.dv) * p.sb;
+  const float g = __ldg(p.g + h);
+  const float2 full = la_pow2(g, p.seg_len), tail = la_pow2(g, len - (n - 1) * p.seg_len);
+  float st = p.init ? p.init[user] : 0.f;
+  float *base = p.seg_state + ((size_t)u0 * p.H + h) * dd + e;
+  const size_t step = (size_t)p.H * dd;
+  constexpr int kAhead = 8;
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    float w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i < n) w[i] = base[(REV ? n - 1 - i0 - i : i0 + i) * step];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i < n) {
+        const int seg = REV ? n - 1 - i0 - i : i0 + i;
+        const float2 c = seg == n - 1 ? tail : full;
+        base[seg * step] = st;
+        st = fmaf(st, c.x, fmaf(st, c.y, w[i]));
+      }
+  }
+  if (p.fin) p.fin[user] = st;
+}
+
+// out(row, kv, c) = sum of in(row, kv * group + i, c) over i, in order
+template <typename T>
+__global__ void __launch_bounds__(256) la_sum_heads_kernel(const float *__restrict__ in, T *__restrict__ out,
+                                                           long long os, long long n4, int Hkv, int group, int d) {
+  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (e >= n4) return;
+  const int d4 = d / 4, c = (int)(e % d4);
+  const long long rk = e / d4, row = rk / Hkv;
+  const int kv = (int)(rk % Hkv);
+  const float4 *src = reinterpret_cast<const float4 *>(in) + (row * Hkv + kv) * (long long)group * d4 + c;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < group; ++i) {
+    const float4 x = __ldg(src + (long long)i * d4);
+    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+  }
+  store4(out + row * os + (long long)kv * d + 4 * c, acc);
+}
+
+template <typename T, bool REV, bool SUMMARY>
+void run_simt(const LaPass &p, cudaStream_t s) {
+  const int dkp = (p.dk + 63) & ~63;
+  const int bytes = 4 * (2 * dkp * kLdC + dkp * kLdV + kC * kLdV + kC * kLdC + kC + 4);
+  static bool once = (cudaFuncSetAttribute(la_simt_kernel<T, REV, SUMMARY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           4 * (2 * 256 * kLdC + 256 * kLdV + kC * kLdV + kC * kLdC + kC + 4)),
+                      true);
+  (void)once;
+  const dim3 grid(p.nunits, p.H, (p.dv + kTV - 1) / kTV);
+  la_simt_kernel<T, REV, SUMMARY><<<grid, kThreads, bytes, s>>>(p);
+}
+
+}  // namespace
+
+template <typename T>
+void launch_la_simt(const LaPass &p, bool reverse, bool summary, cudaStream_t s) {
+  if (reverse)
+    summary ? run_simt<T, true, true>(p, s) : run_simt<T, true, false>(p, s);
+  else
+    summary ? run_simt<T, false, true>(p, s) : run_simt<T, false, false>(p, s);
+}
+
+void launch_la_scan(const LaPass &p, bool reverse, cudaStream_t s) {
+  const dim3 grid((p.dk * p.dv + kScanThreads - 1) / kScanThreads * p.nseq, p.H);
+  if (reverse)
+    la_scan_kernel<true><<<grid, kScanThreads, 0, s>>>(p);
+  else
+    la_scan_kernel<false><<<grid, kScanThreads, 0, s>>>(p);
+}
+
+template <typename T>
+void launch_la_sum_heads(const float *in, void *out, long long os, long long rows, int Hkv, int group, int d,
+                         cudaStream_t s) {
+  const long long n4 = rows * Hkv * (d / 4);
+  la_sum_heads_kernel<T><<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(in, static_cast<T *>(out), os, n4, Hkv, group, d);
+}
+
+template void launch_la_simt<float>(const LaPass &, bool, bool, cudaStream_t);
+template void launch_la_simt<__nv_bfloat16>(const LaPass &, bool, bool, cudaStream_t);
+template void launch_la_sum_heads<float>(const float *, void *, long long, long long, int, int, int, cudaStream_t);
+template void launch_la_sum_heads<__nv_bfloat16>(const float *, void *, long long, long long, int, int, int,
+                                                 cudaStream_t);
+
+}  // namespace ssd
