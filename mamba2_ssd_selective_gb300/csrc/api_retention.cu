@@ -33,10 +33,15 @@ ssd_status la_check_dims(const ssd_linear_attn_dims *d) {
   const long long rows = la_rows(d);
   if (!d->packed && d->total_tokens != 0 && d->total_tokens != rows) return SSD_ERR_INVALID_DIMS;
   if (d->headdim_k % 8 || d->headdim_v % 8 || d->headdim_k > 256 || d->headdim_v > 256 || rows > kMaxRows ||
-      d->nseq > kMaxSeqs || (long long)d->nheads * d->headdim_k > kMaxChannels ||
+      d->nseq > kMaxSeqs || (long long)d->nseq * d->nheads > (1LL << 30) || (long long)d->nheads * d->headdim_k > kMaxChannels ||
       (long long)d->nheads * d->headdim_v > kMaxChannels)
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
+}
+
+// bf16 within its widths takes the tensor-core kernel, everything else the CUDA-core one
+bool la_use_tc(const ssd_linear_attn_dims *d) {
+  return d->dtype == SSD_BF16 && la_tc_envelope(d->headdim_k, d->headdim_v);
 }
 
 // Whether and where sequences are cut, and the workspace.  A cut sequence costs
@@ -44,13 +49,16 @@ ssd_status la_check_dims(const ssd_linear_attn_dims *d) {
 // it is only made when whole sequences leave most of the GPU without work.
 LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
   LaPlan pl{};
+  const bool tc = la_use_tc(d);
   const long long rows = la_rows(d), H = d->nheads, sms = 152;
-  const long long tiles = (d->headdim_v + 63) / 64, want = 4 * sms;  // blocks that fill the GPU
+  // blocks of a whole sequence, and blocks that fill the GPU (one or four on an SM)
+  const long long blocks = H * (tc ? 1 : (d->headdim_v + 63) / 64), want = tc ? sms : 4 * sms;
   const long long longest = d->packed ? rows : d->seqlen;
-  long long seg = (rows * H * tiles + want - 1) / want;
+  const long long cuts = want / (d->nseq * blocks);
+  long long seg = d->packed ? rows * blocks / want : cuts > 0 ? (longest + cuts - 1) / cuts : longest;
   seg = (seg + 63) / 64 * 64;
   if (seg < 256) seg = 256;
-  pl.split = seg < longest && d->nseq * H * tiles < want;
+  pl.split = seg < longest && cuts >= 2;
   if (!pl.split) seg = (longest + 63) / 64 * 64;
   pl.seg_len = (int)seg;
   pl.nunits = (int)(!pl.split ? d->nseq : d->packed ? rows / seg + d->nseq : d->nseq * ((longest + seg - 1) / seg));
@@ -147,11 +155,13 @@ void la_states(LaPass &p, const float *init, float *fin, bool transposed) {
 
 template <typename T>
 void la_run(const LaPass &p, bool reverse, cudaStream_t s) {
+  const bool tc = sizeof(T) == 2 && la_tc_envelope(p.dk, p.dv);
+  auto pass = [&](bool summary) { tc ? launch_la_tc(p, reverse, summary, s) : launch_la_simt<T>(p, reverse, summary, s); };
   if (p.split) {
-    SSD_LAUNCH("la_segment_states", launch_la_simt<T>(p, reverse, true, s));
+    SSD_LAUNCH("la_segment_states", pass(true));
     SSD_LAUNCH("la_scan", launch_la_scan(p, reverse, s));
   }
-  SSD_LAUNCH("la_pass", launch_la_simt<T>(p, reverse, false, s));
+  SSD_LAUNCH("la_pass", pass(false));
 }
 
 template <typename T>

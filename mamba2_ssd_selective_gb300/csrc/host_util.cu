@@ -61,6 +61,19 @@ bool encode_tmap_f32_2d(CUtensorMap *map, const void *base, uint64_t cols, uint6
   return encode_sw128_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, cols, rows, row_bytes, box_cols, box_rows);
 }
 
+bool encode_tmap_bf16_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t rows,
+                            uint64_t row_bytes, uint32_t box_rows) {
+  EncodeTiled fn = encoder();
+  if (!fn || (reinterpret_cast<uintptr_t>(base) & 15) || (row_bytes & 15) || (width * 2 & 15)) return false;
+  const cuuint64_t dims[3] = {width, heads, rows};
+  const cuuint64_t strides[2] = {width * 2, row_bytes};
+  const cuuint32_t box[3] = {64, 1, box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_sm_count() {
   static std::mutex mu;
   static int cache[64] = {0};

@@ -114,15 +114,19 @@ __device__ __forceinline__ bool la_find_unit(const LaPass &p, int u, LaUnit &out
 // lam^n in fp32; lam^0 is 1 even for a log decay of -inf
 __device__ __forceinline__ float la_pow(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
 // lam^n as a sum of two fp32 values: a state is multiplied by it once per block,
-// for as many blocks as it lives, so that an error of its own would add up
+// for as many blocks as it lives, so that an error of its own would add up.  A
+// state lives for about 1 / (1 - lam^n) blocks, so the error has to be small
+// against 1 - lam^n, which expm1 gives.
 __device__ __forceinline__ float2 la_pow2(float g, int n) {
-  const double d = n == 0 ? 1.0 : exp((double)g * n);
-  const float hi = (float)d;
-  return make_float2(hi, (float)(d - (double)hi));
+  const float e = n == 0 ? 0.f : expm1f(g * (float)n), hi = 1.f + e;
+  return make_float2(hi, e - (hi - 1.f));
 }
 
 // la_simt.cu: any type and width of the envelope
 template <typename T> void launch_la_simt(const LaPass &p, bool reverse, bool summary, cudaStream_t s);
+// la_tc.cu: bf16, both widths at most 128
+inline bool la_tc_envelope(int dk, int dv) { return dk <= 128 && dv <= 128; }
+void launch_la_tc(const LaPass &p, bool reverse, bool summary, cudaStream_t s);
 // segment states -> incoming segment states, in place, and the final states (either type's path)
 void launch_la_scan(const LaPass &p, bool reverse, cudaStream_t s);
 // sums fp32 (rows, H, d) over groups of query heads into (rows, Hkv, d)

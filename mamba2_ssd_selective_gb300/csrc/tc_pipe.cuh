@@ -158,6 +158,11 @@ bool encode_tmap_bf16_2d(CUtensorMap *map, const void *base, uint64_t cols, uint
 // Host: the same for fp32 (box_cols * 4 must be 128).
 bool encode_tmap_f32_2d(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
                         uint32_t box_cols, uint32_t box_rows);
+// Host: a token-major (rows, heads * width) bf16 tensor as (width, heads, rows), box
+// 64 columns of one head x box_rows rows, 128-byte swizzle; columns past a head's
+// width and rows past the last read as zeros.
+bool encode_tmap_bf16_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t rows,
+                            uint64_t row_bytes, uint32_t box_rows);
 // Host: SM count of the current device (cached per device).
 int device_sm_count();
 // Host: record an error found while preparing a launch; the pass then returns
