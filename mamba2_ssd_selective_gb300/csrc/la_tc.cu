@@ -46,39 +46,46 @@ constexpr uint32_t kTmQK = 0, kTmO = 64, kTmOi = 192, kTmW = 320, kTmS = 448, kT
 
 template <int KB, int VB, bool SUMMARY>
 struct Layout {
-  static constexpr int kStages = KB == 2 ? 3 : 4;
-  static constexpr uint32_t kQ = 0, kK = SUMMARY ? 0 : KB * kBox, kV = kK + KB * kBox, kStage = kV + VB * kBox;
-  static constexpr uint32_t kKt = kStages * kStage;                       // three terms of the weighted K
-  static constexpr uint32_t kP = kKt + 3 * KB * kBox;                     // two P buffers
-  static constexpr uint32_t kO = kP + (SUMMARY ? 0 : 2 * kBox);           // transposed output block
-  static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : VB * kBox);        // lam^n times each scale, n = 0..64
+  static constexpr int kStages = KB + VB == 2 ? 4 : 3;
+  // a stage: Q, later the block's outputs; K, later the first term of the weighted K; V
+  static constexpr int kQBoxes = SUMMARY ? 0 : KB > VB ? KB : VB;
+  static constexpr uint32_t kQ = 0, kK = kQBoxes * kBox, kV = kK + KB * kBox, kStage = kV + VB * kBox;
+  static constexpr uint32_t kLoad = ((SUMMARY ? 1 : 2) * KB + VB) * kBox;  // bytes loaded into a stage
+  static constexpr uint32_t kKt = kStages * kStage;                // two buffers of the other two terms
+  static constexpr uint32_t kP = kKt + 4 * KB * kBox;              // two P buffers
+  static constexpr uint32_t kTab = kP + (SUMMARY ? 0 : 2 * kBox);  // lam^n times each scale, n = 0..64
   static constexpr uint32_t kBar = kTab + 3 * 272 + 16;
-  static constexpr int kNumBars = 2 * kStages + 2 + 2 + 2 + 1 + 1 + 1 + 2 + 2 + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 + 1 + 1 + 2 + 2 + 1 + 2 + 1 + 2 + 2 + 1;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
+// The m-th use of a barrier that alternates between two is completion m / 2 of
+// barrier m & 1.  Alternation is needed wherever the arriving side may be a block
+// ahead of a waiter (k_done, kt_ready).
 template <int ST>
 struct Bars {
-  uint64_t *full, *free;        // [ST] stage loaded / read by every MMA of its block
-  uint64_t *qk_full, *qk_free;  // scores
+  uint64_t *full, *free;        // [ST] stage loaded / its operands and outputs read
+  uint64_t *k_done;             // [2] scores formed (for the state warps, which then overwrite K)
+  uint64_t *qk_full, *qk_free;  // scores (for the P warps)
   uint64_t *p_ready, *p_free;   // [2]
-  uint64_t *s_ready;            // S^T of the block in TMEM
-  uint64_t *kt_ready;           // weighted K in shared memory (and V's tail zeroed)
+  uint64_t *s_ready;            // S^T of the block in TMEM, and the previous W read
+  uint64_t *kt_ready;           // [2] weighted K in shared memory (and V's tail zeroed)
   uint64_t *w_full;             // W formed, weighted K and S^T read
   uint64_t *o_full, *o_free;    // [2]
   uint64_t *drain;
   __device__ explicit Bars(uint64_t *b) {
     full = b;
     free = full + ST;
-    qk_full = free + ST;
+    k_done = free + ST;
+    qk_full = k_done + 2;
     qk_free = qk_full + 1;
     p_ready = qk_free + 1;
     p_free = p_ready + 2;
     s_ready = p_free + 2;
     kt_ready = s_ready + 1;
-    w_full = kt_ready + 1;
+    w_full = kt_ready + 2;
     o_full = w_full + 1;
     o_free = o_full + 2;
     drain = o_free + 2;
@@ -88,20 +95,26 @@ struct Bars {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// two values as three bf16 pairs whose sums give them to 24 bits
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t &a, uint32_t &b, uint32_t &c) {
-  a = tc::pack_bf16x2(x0, x1);
-  x0 -= lo_f(a);
-  x1 -= hi_f(a);
-  b = tc::pack_bf16x2(x0, x1);
-  c = tc::pack_bf16x2(x0 - lo_f(b), x1 - hi_f(b));
+// Two values x as three bf16 pairs that add up to them: each term is the rest's
+// leading 8 bits (cut off, so that the rest is exact and packing is a byte
+// permute), the last one rounded.
+__device__ __forceinline__ void split3(uint64_t x, uint32_t &a, uint32_t &b, uint32_t &c) {
+  float f0, f1;
+  upk2(x, f0, f1);
+  uint32_t u0 = __float_as_uint(f0), u1 = __float_as_uint(f1);
+  a = __byte_perm(u0, u1, 0x7632);
+  x = add2(x, pk2(__uint_as_float((u0 & 0xffff0000u) ^ 0x80000000u), __uint_as_float((u1 & 0xffff0000u) ^ 0x80000000u)));
+  upk2(x, f0, f1);
+  u0 = __float_as_uint(f0), u1 = __float_as_uint(f1);
+  b = __byte_perm(u0, u1, 0x7632);
+  c = tc::pack_bf16x2(f0 - __uint_as_float(u0 & 0xffff0000u), f1 - __uint_as_float(u1 & 0xffff0000u));
 }
 
 // KB, VB: 64-column boxes of the q/k roles and of the v/o roles
 template <int KB, int VB, bool REV, bool SUMMARY>
 __global__ void __launch_bounds__(kThreads, 1)
     la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, LaPass p) {
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, LaPass p) {
   using L = Layout<KB, VB, SUMMARY>;
   constexpr int ST = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -121,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 64) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.free[i], 1);
+      mbar_init(&bar.free[i], SUMMARY ? 1 : 2);
     }
     mbar_init(bar.qk_full, 1);
     mbar_init(bar.qk_free, 2);
@@ -130,9 +143,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.p_free[i], 1);
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.o_free[i], 2 * VB);
+      mbar_init(&bar.k_done[i], 1);
+      mbar_init(&bar.kt_ready[i], kStateWarps);
     }
     mbar_init(bar.s_ready, kStateWarps);
-    mbar_init(bar.kt_ready, kStateWarps);
     mbar_init(bar.w_full, 1);
     mbar_init(bar.drain, 1);
     fence_mbar_init();
@@ -166,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = i % ST, row = u.t0 + block_of(i) * kC;
         if (i >= ST && !mbar_wait(&bar.free[st], parity(i / ST - 1), wait)) break;
         uint8_t *base = sm + st * L::kStage;
-        mbar_expect_tx(&bar.full[st], L::kStage);
+        mbar_expect_tx(&bar.full[st], L::kLoad);
         for (int b = 0; b < KB; ++b) {
           if (!SUMMARY) tma_load_3d(base + L::kQ + b * kBox, &tm_q, &bar.full[st], 64 * b, h / p.gq, row);
           tma_load_3d(base + L::kK + b * kBox, &tm_k, &bar.full[st], 64 * b, h / p.gk, row);
@@ -185,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows run past Q's 64 into the shared memory behind it; those rows of the
       // result (and the lanes past 64 when VB = 1) are not read.
       const uint64_t dQ = desc_sw128(s0 + L::kQ, 16, 1024), dK = desc_sw128(s0 + L::kK, 16, 1024),
-                     dV = desc_sw128(s0 + L::kV, kBox, 1024), dKt = desc_sw128(s0 + L::kKt, kBox, 1024),
+                     dV = desc_sw128(s0 + L::kV, kBox, 1024), dK1 = desc_sw128(s0 + L::kK, kBox, 1024),
+                     dKt = desc_sw128(s0 + L::kKt, kBox, 1024),
                      dP = desc_sw128(s0 + L::kP, 16, 1024);
       constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iPV = idesc_bf16(128, 64, true, false),
                          iQS = idesc_bf16(128, 64, false, false), iW = idesc_bf16(128, 64 * KB, true, true);
@@ -199,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pipe::umma_k<4>(tmem + kTmQK, dQ + stage(i) + b * (kBox / 16), dK + stage(i) + b * (kBox / 16), pipe::kStepK,
                           pipe::kStepK, iQK, b > 0);
         umma_commit(bar.qk_full);
+        umma_commit(&bar.k_done[i & 1]);
       };
       if (!SUMMARY && nb > 0) scores(0);
       for (int i = 0; i < nb; ++i) {
@@ -206,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!SUMMARY) {
           if (i + 1 < nb) scores(i + 1);
           if (i >= 2) mbar_wait(&bar.o_free[ob], parity(i / 2 - 1), wait);
-          if (rows_of(block_of(i)) < kC) mbar_wait(bar.kt_ready, parity(i), wait);  // V's tail is zeroed
+          if (rows_of(block_of(i)) < kC) mbar_wait(&bar.kt_ready[ob], parity(i / 2), wait);  // V's tail
           mbar_wait(&bar.p_ready[ob], parity(i / 2), wait);
           tc_fence_after();
           pipe::umma_k<4>(tmem + kTmO + 64 * ob, dV + stage(i), dP + ob * (kBox / 16), pipe::kStepMN, pipe::kStepK, iPV,
@@ -221,12 +237,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(&bar.o_full[ob]);
         } else {
           mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
+          mbar_wait(bar.s_ready, parity(i), wait);
         }
-        mbar_wait(bar.kt_ready, parity(i), wait);
+        mbar_wait(&bar.kt_ready[ob], parity(i / 2), wait);
         tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < 3; ++t)
-          pipe::umma_k<4>(tmem + kTmW, dV + stage(i), dKt + t * KB * (kBox / 16), pipe::kStepMN, pipe::kStepMN, iW, t > 0);
+        const uint64_t v = dV + stage(i), kt = dKt + (uint64_t)(ob * 2 * KB * (kBox / 16));
+        pipe::umma_k<4>(tmem + kTmW, v, dK1 + stage(i), pipe::kStepMN, pipe::kStepMN, iW, false);
+        pipe::umma_k<4>(tmem + kTmW, v, kt, pipe::kStepMN, pipe::kStepMN, iW, true);
+        pipe::umma_k<4>(tmem + kTmW, v, kt + KB * (kBox / 16), pipe::kStepMN, pipe::kStepMN, iW, true);
         umma_commit(bar.w_full);
         umma_commit(&bar.free[i % ST]);
       }
@@ -240,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) {
           mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
           mbar_wait_drain(&bar.o_full[m & 1], parity(m / 2));
+          mbar_wait_drain(&bar.k_done[m & 1], parity(m / 2));
         }
       }
     }
@@ -258,6 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         pipe::warp_arrive(bar.qk_free);
         if (i >= 2) mbar_wait(&bar.p_free[i & 1], parity(i / 2 - 1), wait);
         const uint32_t dst = smem_u32(sm + L::kP + (i & 1) * kBox);
+        // columns past the end: in order, only rows past it see them
+        const int jmax = REV ? nv : kC;
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           float v[8];
@@ -265,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 8; ++e) {
             const int j = 8 * x + e, d = REV ? j - r : r - j;
             // a select, not a factor of zero: masked scores may be NaN
-            v[e] = d >= 0 && j < nv ? s[j] * tab_p[d] : 0.f;
+            v[e] = d >= 0 && j < jmax ? s[j] * tab_p[d] : 0.f;
           }
           pipe::sts_u4(dst + sw128_offset(r, 8 * x), tc::pack8(v));
         }
@@ -277,58 +298,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ outputs
     if (!SUMMARY && warp < kOutWarp0 + 2 * VB) {
       constexpr int kOutThreads = 64 * VB;
-      const int tt = threadIdx.x - 32 * kOutWarp0, c = tt;  // c: column of v (TMEM lane)
-      const uint32_t so = smem_u32(sm + L::kO);
+      const int tt = threadIdx.x - 32 * kOutWarp0, quad = warp & 3;
+      // the address this lane gives to a group of four fragments: row i, columns of v
+      const int fi = 8 * (lane >> 4) + (lane & 7), fc = 32 * quad + 8 * ((lane >> 3) & 1);
       for (int i = 0; i < nb; ++i) {
-        const int ob = i & 1, blk = block_of(i), nv = rows_of(blk);
+        const int ob = i & 1, st = i % ST, blk = block_of(i), nv = rows_of(blk);
         const long long row0 = u.t0 + (long long)blk * kC;
+        const uint32_t so = smem_u32(sm + st * L::kStage + L::kQ);
+        float w[16];  // what the incoming state's part of this lane's columns i weighs
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * m + 2 * (lane & 3) + e;
+            w[2 * m + e] = tab_in[REV ? max(nv - 1 - r, 0) : r + 1];
+          }
         mbar_wait(&bar.o_full[ob], parity(i / 2), wait);
         tc_fence_after();
-        if (!p.o_f32 && i > 0) asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          float a[32], b[32];
-          tmem_ld32(pipe::tmem_quad(tmem + kTmO + 64 * ob, 32 * half), a);
-          tmem_ld32(pipe::tmem_quad(tmem + kTmOi + 64 * ob, 32 * half), b);
-          const float *w = tab_in + (REV ? nv - 1 - 32 * half : 1 + 32 * half);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int r = 32 * half + e;
-            if (r < nv) a[e] = fmaf(REV ? w[-e] : w[e], b[e], a[e]);
+        for (int half = 0; half < 2; ++half) {  // 16 lanes (columns of v) at a time
+          uint32_t a[32], b[32];
+          const uint32_t lanes = (uint32_t)(16 * half) << 16;
+          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmO + 64 * ob, 0) + lanes, a);
+          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmOi + 64 * ob, 0) + lanes, b);
+          tmem_wait_ld32(a);
+          tmem_wait_ld32(b);
+          if (half == 1) {
+            tc_fence_before();
+            pipe::warp_arrive(&bar.o_free[ob]);
           }
-          if (p.o_f32) {
-            if (c < p.dv) {
-              float *dst = static_cast<float *>(p.o) + (row0 + 32 * half) * p.os + (long long)h * p.dv + c;
+          float o[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * half + e < nv) dst[e * p.os] = a[e];
+          for (int x = 0; x < 32; ++x)
+            o[x] = fmaf(w[2 * (x >> 2) + (x & 1)], __uint_as_float(b[x]), __uint_as_float(a[x]));
+          if (p.o_f32) {
+            float *dst = static_cast<float *>(p.o) + row0 * p.os + (long long)h * p.dv;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const int r = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1), c = 32 * quad + 16 * half + (lane >> 2) + 4 * (x & 2);
+              if (r < nv && c < p.dv) dst[r * p.os + c] = o[x];
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(so + (32 * half + e) * (VB * 128) + 2 * c),
-                           "h"(__bfloat16_as_ushort(__float2bfloat16_rn(a[e])))
-                           : "memory");
-          }
-        }
-        tc_fence_before();
-        pipe::warp_arrive(&bar.o_free[ob]);
-        if (!p.o_f32) {
-          asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
-          bf16 *out = static_cast<bf16 *>(p.o) + row0 * p.os + (long long)h * p.dv;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int e = tt + kOutThreads * x, r = e / (8 * VB), cc = e % (8 * VB);
-            if (r < nv && 8 * cc < p.dv) {
-              uint4 v;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                           : "r"(so + r * (VB * 128) + 16 * cc));
-              *reinterpret_cast<uint4 *>(out + r * p.os + 8 * cc) = v;
+            for (int m = 0; m < 8; m += 2) {
+              const int r = 8 * m + fi, c = fc + 16 * half;
+              stmatrix4_trans(so + (uint32_t)(c >> 6) * kBox + sw128_offset(r, c & 63),
+                              tc::pack_bf16x2(o[4 * m], o[4 * m + 1]), tc::pack_bf16x2(o[4 * m + 2], o[4 * m + 3]),
+                              tc::pack_bf16x2(o[4 * m + 4], o[4 * m + 5]), tc::pack_bf16x2(o[4 * m + 6], o[4 * m + 7]));
             }
           }
         }
+        if (!p.o_f32) {
+          fence_async_smem();
+          asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
+          if (nv < kC) {  // rows past the end belong to another sequence: row by row
+            bf16 *out = static_cast<bf16 *>(p.o) + row0 * p.os + (long long)h * p.dv;
+            for (int e = tt; e < nv * 8 * VB; e += kOutThreads) {
+              const int r = e / (8 * VB), c = 8 * (e % (8 * VB));
+              if (c < p.dv) {
+                uint4 v;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(so + (uint32_t)(c >> 6) * kBox + sw128_offset(r, c & 63)));
+                *reinterpret_cast<uint4 *>(out + r * p.os + c) = v;
+              }
+            }
+            asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
+          } else if (tt == 0) {
+            for (int b = 0; b < VB; ++b)
+              if (64 * b < p.dv) tma_store_3d(&tm_o, so + b * kBox, 64 * b, h, (int)row0);
+            bulk_commit();
+            bulk_wait_read0();
+          }
+        }
+        if (tt == 0) mbar_arrive(&bar.free[st]);
       }
+      if (tt == 0) bulk_wait0();
     }
   } else {
     // ------------------------------------------------------------ state
@@ -337,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c = 32 * quad + lane, a0 = half * kCols;
     const bool holds = quad < 2 * VB;  // this warp's lanes are columns of the state (warp-uniform)
     const size_t dd = (size_t)p.dk * p.dv;
-    float S[kCols];
+    uint64_t S[kCols / 2];  // pairs along dk
     {
       const float *in = nullptr;
       int sa = p.sa, sb = p.sb;
@@ -350,30 +395,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool live = in && holds && c < p.dv;
 #pragma unroll
-      for (int a = 0; a < kCols; ++a)
-        S[a] = live && a0 + a < p.dk ? in[(size_t)(a0 + a) * sa + (size_t)c * sb] : 0.f;
+      for (int a = 0; a < kCols; a += 2) {  // dk is even
+        float x = 0.f, y = 0.f;
+        if (live && a0 + a < p.dk) {
+          x = in[(size_t)(a0 + a) * sa + (size_t)c * sb];
+          y = in[(size_t)(a0 + a + 1) * sa + (size_t)c * sb];
+        }
+        S[a / 2] = pk2(x, y);
+      }
     }
     auto publish = [&] {  // S^T as the A operand: lane = column of v, bf16 pairs along dk
-      if (holds) {
+      if (!SUMMARY && holds) {
 #pragma unroll
-        for (int x = 0; x < kCols; x += 32) {
+        for (int x = 0; x < kCols / 2; x += 16) {
           uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = tc::pack_bf16x2(S[x + 2 * e], S[x + 2 * e + 1]);
-          tmem_st16_async(pipe::tmem_quad(tmem + kTmS, (a0 + x) / 2), w);
+          for (int e = 0; e < 16; ++e) {
+            float f0, f1;
+            upk2(S[x + e], f0, f1);
+            w[e] = tc::pack_bf16x2(f0, f1);
+          }
+          tmem_st16_async(pipe::tmem_quad(tmem + kTmS, a0 / 2 + x), w);
         }
         tmem_wait_st();
       }
       tc_fence_before();
       pipe::warp_arrive(bar.s_ready);
     };
-    if (!SUMMARY && nb > 0) publish();
-    const float2 full = la_pow2(g, kC);
-    const uint32_t skt = smem_u32(sm + L::kKt);
-    for (int i = 0; i < nb; ++i) {
+    // the three terms of diag(lam^b) K of block i: the first over K itself
+    const uint32_t s0 = smem_u32(sm);
+    auto weigh = [&](int i) {
       const int st = i % ST, nv = rows_of(block_of(i));
+      const uint32_t sk = s0 + st * L::kStage + L::kK, sv = s0 + st * L::kStage + L::kV,
+                     skt = s0 + L::kKt + (uint32_t)(i & 1) * (2 * KB * kBox);
       mbar_wait(&bar.full[st], parity(i / ST), wait);
-      const uint32_t sk = smem_u32(sm + st * L::kStage + L::kK), sv = smem_u32(sm + st * L::kStage + L::kV);
+      if (!SUMMARY) mbar_wait(&bar.k_done[i & 1], parity(i / 2), wait);
 #pragma unroll
       for (int x = 0; x < 2 * KB; ++x) {
         const int e = tt + 256 * x, r = (e >> 3) & 63, cc = e & 7;
@@ -381,17 +437,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 raw, t0 = make_uint4(0, 0, 0, 0), t1 = t0, t2 = t0;
         if (r < nv) {
           const float w = tab_st[REV ? r + 1 : nv - 1 - r];
+          const uint64_t w2 = pk2(w, w);
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
                        : "r"(sk + off));
-          split3(w * lo_f(raw.x), w * hi_f(raw.x), t0.x, t1.x, t2.x);
-          split3(w * lo_f(raw.y), w * hi_f(raw.y), t0.y, t1.y, t2.y);
-          split3(w * lo_f(raw.z), w * hi_f(raw.z), t0.z, t1.z, t2.z);
-          split3(w * lo_f(raw.w), w * hi_f(raw.w), t0.w, t1.w, t2.w);
+          split3(mul2(w2, pk2(lo_f(raw.x), hi_f(raw.x))), t0.x, t1.x, t2.x);
+          split3(mul2(w2, pk2(lo_f(raw.y), hi_f(raw.y))), t0.y, t1.y, t2.y);
+          split3(mul2(w2, pk2(lo_f(raw.z), hi_f(raw.z))), t0.z, t1.z, t2.z);
+          split3(mul2(w2, pk2(lo_f(raw.w), hi_f(raw.w))), t0.w, t1.w, t2.w);
         }
-        pipe::sts_u4(skt + off, t0);
-        pipe::sts_u4(skt + KB * kBox + off, t1);
-        pipe::sts_u4(skt + 2 * KB * kBox + off, t2);
+        pipe::sts_u4(sk + off, t0);
+        pipe::sts_u4(skt + off, t1);
+        pipe::sts_u4(skt + KB * kBox + off, t2);
       }
       if (nv < kC) {
 #pragma unroll
@@ -401,8 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       fence_async_smem();
-      pipe::warp_arrive(bar.kt_ready);
+      pipe::warp_arrive(&bar.kt_ready[i & 1]);
+    };
+    const float2 full = la_pow2(g, kC);
+    if (nb > 0) {
+      publish();
+      weigh(0);
+    }
+    for (int i = 0; i < nb; ++i) {
+      if (i + 1 < nb) weigh(i + 1);  // while the tensor core works on block i
+      const int nv = rows_of(block_of(i));
       const float2 carry = nv == kC ? full : la_pow2(g, nv);
+      const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
       // W done: so are the MMAs issued before it, which read the weighted K and S^T
       mbar_wait(bar.w_full, parity(i), wait);
       tc_fence_after();
@@ -412,10 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           float w[32];
           tmem_ld32(pipe::tmem_quad(tmem + kTmW, a0 + x), w);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) S[x + e] = fmaf(S[x + e], carry.x, fmaf(S[x + e], carry.y, w[e]));
+          for (int e = 0; e < 16; ++e) {
+            uint64_t &t = S[x / 2 + e];
+            t = fma2(t, chi, fma2(t, clo, pk2(w[2 * e], w[2 * e + 1])));
+          }
         }
       }
-      if (!SUMMARY && i + 1 < nb) publish();
+      if (i + 1 < nb) publish();
     }
     float *out = nullptr;
     int sa = p.sa, sb = p.sb;
@@ -428,8 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (out && holds && c < p.dv) {
 #pragma unroll
-      for (int a = 0; a < kCols; ++a)
-        if (a0 + a < p.dk) out[(size_t)(a0 + a) * sa + (size_t)c * sb] = S[a];
+      for (int a = 0; a < kCols; a += 2) {
+        float x, y;
+        upk2(S[a / 2], x, y);
+        if (a0 + a < p.dk) {
+          out[(size_t)(a0 + a) * sa + (size_t)c * sb] = x;
+          out[(size_t)(a0 + a + 1) * sa + (size_t)c * sb] = y;
+        }
+      }
     }
   }
 
@@ -448,14 +524,15 @@ void run_tc(const LaPass &p, cudaStream_t s) {
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes),
                       true);
   (void)once;
-  CUtensorMap tq{}, tk, tv;
+  CUtensorMap tq{}, tk, tv, to{};
   if ((!SUMMARY && !encode_tmap_bf16_heads(&tq, p.q, p.dk, p.Hq, p.total, p.qs * 2, kC)) ||
+      (!SUMMARY && !p.o_f32 && !encode_tmap_bf16_heads(&to, p.o, p.dv, p.H, p.total, p.os * 2, kC)) ||
       !encode_tmap_bf16_heads(&tk, p.k, p.dk, p.Hk, p.total, p.ks * 2, kC) ||
       !encode_tmap_bf16_heads(&tv, p.v, p.dv, p.Hv, p.total, p.vs * 2, kC)) {
     note_host_error();
     return;
   }
-  la_tc_kernel<KB, VB, REV, SUMMARY><<<(unsigned)p.H * (unsigned)p.nunits, kThreads, L::kBytes, s>>>(tq, tk, tv, p);
+  la_tc_kernel<KB, VB, REV, SUMMARY><<<(unsigned)p.H * (unsigned)p.nunits, kThreads, L::kBytes, s>>>(tq, tk, tv, to, p);
 }
 
 template <int KB, int VB>
