@@ -1,29 +1,39 @@
 // Linear attention with a decay for each head on the 5th-generation tensor cores
-// (tcgen05, accumulators and the state operand in TMEM): bf16 tensors, widths up to 128.
+// (tcgen05, accumulators and A operands in TMEM): bf16 tensors, widths up to 128.
 //
 // One CTA takes one segment of one sequence and one query head, and walks it in
 // blocks of 64 tokens.  With P_ij = scale q_i . k_j lam^|i - j| inside the block
 // (j <= i; reverse: j >= i) and the incoming state S (dk x dv):
 //     O^T  = V^T P^T              Oi^T = S^T Q^T
 //     o_i  = O_i + lam^a(i) Oi_i
-//     S    = lam^nv S + (diag(lam^b) K)^T V
-// The outputs are formed transposed, so that dv (up to 128) fills the lanes of
-// the accumulators and the state, which its warps hold in registers as S^T (lane =
-// dv), goes into TMEM as the A operand of Oi without a detour through shared
-// memory.  P and S are rounded to bf16 as operands (the outputs are bf16 too);
-// what goes into the state is not: diag(lam^b) K is split into three bf16 terms
-// (24 bits), so that states keep fp32 precision over any length.
+//     S^T  = lam^nv S^T + W^T,    W^T = (V^T diag(lam^b)) K
+// Everything is formed transposed, so that dv (up to 128) fills the accumulators'
+// lanes, the state stays in its warps' registers (lane = dv) from block to
+// block, and every product but the scores takes its A operand from TMEM: S^T
+// from the registers, V^T and its weighted copies from shared memory through
+// transposing matrix loads.  That matters because shared memory is what bounds
+// the kernel before HBM does: with the weighted K kept there as a B operand
+// (three terms written and read back) a block of 64 tokens at widths of 128 moved
+// 340 KB through it and took 3560 cycles, and 1.5 of them were shared memory's.
+// P and S are rounded to bf16 as operands (the outputs are bf16 too); what goes
+// into the state is not: V diag(lam^b) is split into three bf16 terms (24 bits), so
+// that states keep fp32 precision over any length.
 //
 // Warps:
 //   0, 1    P: scores out of TMEM (lane = row i of the block), decay and mask, P into shared memory
 //   2       TMA producer: Q, K, V blocks [64 x 64 columns each], a ring of stages
 //   3       TMEM owner and MMA issuer
-//   4-7     outputs: O^T and Oi^T out of TMEM, combined, transposed through shared memory
-//   8-15    state: the three terms of diag(lam^b) K, then S = lam^nv S + W and S^T into TMEM
-// A block's scores are issued one block ahead, so that P is ready when the
-// tensor core gets to it.  The last block of a sequence is masked: rows past its
-// end belong to another sequence, so K's rows there are not used, V's are zeroed
-// (0 * NaN would be NaN), and nothing is stored there.
+//   4-7     outputs: O^T and Oi^T out of TMEM as fragments, combined, transposed by stmatrix into
+//           the block's Q tile, stored by TMA
+//   8-15    state: V^T and the three terms of V^T diag(lam^b) into TMEM, then S = lam^nv S + W and
+//           S^T into TMEM as the next block's operand
+// The tensor core's order is scores of block i + 1, W's first half (32 tokens),
+// Oi, O, W's second half: the halves' operands alternate between two buffers, so
+// that the state warps prepare one while the other is in use.
+// The last block of a sequence is masked: rows past its end belong to another
+// sequence, so V's are replaced by zeros on their way to TMEM and K's in shared
+// memory (0 * NaN would be NaN), scores with them are selected away, and nothing
+// is stored there.
 #include "retention.h"
 #include "tc_pipe.cuh"
 #include "tc_util.cuh"
@@ -38,76 +48,88 @@ using pipe::parity;
 
 constexpr int kC = 64;  // tokens of a block
 constexpr int kThreads = 512;
-constexpr int kStateWarp0 = 8, kStateWarps = 8, kOutWarp0 = 4;
+constexpr int kStateWarp0 = 8, kOutWarp0 = 4;
 constexpr uint32_t kBox = 8192;  // [64 tokens x 64 columns] bf16
 
-// TMEM columns
-constexpr uint32_t kTmQK = 0, kTmO = 64, kTmOi = 192, kTmW = 320, kTmS = 448, kTmCols = 512;
+// TMEM columns: scores, O, Oi, W, S^T (bf16), two buffers of the three terms of half a block, V^T
+constexpr uint32_t kTmQK = 0, kTmO = 64, kTmOi = 128, kTmW = 192, kTmS = 320, kTmT = 384, kTmV = 480, kTmCols = 512;
+constexpr uint32_t kTerm = 16, kHalf = 3 * kTerm;  // a term of half a block (32 tokens as bf16 pairs)
 
 template <int KB, int VB, bool SUMMARY>
 struct Layout {
-  static constexpr int kStages = KB + VB == 2 ? 4 : 3;
-  // a stage: Q, later the block's outputs; K, later the first term of the weighted K; V
+  static constexpr int kStages = KB + VB == 2 ? 6 : 4;
+  // a stage: Q, later the block's outputs; K; V
   static constexpr int kQBoxes = SUMMARY ? 0 : KB > VB ? KB : VB;
   static constexpr uint32_t kQ = 0, kK = kQBoxes * kBox, kV = kK + KB * kBox, kStage = kV + VB * kBox;
   static constexpr uint32_t kLoad = ((SUMMARY ? 1 : 2) * KB + VB) * kBox;  // bytes loaded into a stage
-  static constexpr uint32_t kKt = kStages * kStage;                // two buffers of the other two terms
-  static constexpr uint32_t kP = kKt + 4 * KB * kBox;              // two P buffers
+  static constexpr uint32_t kP = kStages * kStage;                 // two P buffers
   static constexpr uint32_t kTab = kP + (SUMMARY ? 0 : 2 * kBox);  // lam^n times each scale, n = 0..64
   static constexpr uint32_t kBar = kTab + 3 * 272 + 16;
-  static constexpr int kNumBars = 2 * kStages + 2 + 1 + 1 + 2 + 2 + 1 + 2 + 1 + 2 + 2 + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 1 + 1 + 4 + 1 + 2 + 1;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
-// The m-th use of a barrier that alternates between two is completion m / 2 of
-// barrier m & 1.  Alternation is needed wherever the arriving side may be a block
-// ahead of a waiter (k_done, kt_ready).
 template <int ST>
 struct Bars {
   uint64_t *full, *free;        // [ST] stage loaded / its operands and outputs read
-  uint64_t *k_done;             // [2] scores formed (for the state warps, which then overwrite K)
-  uint64_t *qk_full, *qk_free;  // scores (for the P warps)
+  uint64_t *qk_full, *qk_free;  // scores
   uint64_t *p_ready, *p_free;   // [2]
-  uint64_t *s_ready;            // S^T of the block in TMEM, and the previous W read
-  uint64_t *kt_ready;           // [2] weighted K in shared memory (and V's tail zeroed)
-  uint64_t *w_full;             // W formed, weighted K and S^T read
-  uint64_t *o_full, *o_free;    // [2]
+  uint64_t *s_ready;            // S^T of the block in TMEM
+  uint64_t *w_free;             // the previous block's W read out of TMEM
+  uint64_t *v_ready, *v_free;   // [2] half a block's V^T and terms in TMEM / read by its MMAs
+  uint64_t *w_full;             // W formed: v_free[1] and the end of the block's MMAs
+  uint64_t *o_full, *o_free;
   uint64_t *drain;
   __device__ explicit Bars(uint64_t *b) {
     full = b;
     free = full + ST;
-    k_done = free + ST;
-    qk_full = k_done + 2;
+    qk_full = free + ST;
     qk_free = qk_full + 1;
     p_ready = qk_free + 1;
     p_free = p_ready + 2;
     s_ready = p_free + 2;
-    kt_ready = s_ready + 1;
-    w_full = kt_ready + 2;
+    w_free = s_ready + 1;
+    v_ready = w_free + 1;
+    v_free = v_ready + 2;
+    w_full = v_free + 2;
     o_full = w_full + 1;
-    o_free = o_full + 2;
-    drain = o_free + 2;
+    o_free = o_full + 1;
+    drain = o_free + 1;
   }
 };
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// x minus the low (high) bf16 of w, exact where that is x's leading part: one
+// mixed-precision instruction on the FMA pipe, instead of a mask on the ALU
+__device__ __forceinline__ float minus_lo(float x, uint32_t w) {
+  float d;
+  asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %1;\n mov.b16 m, 0xbf80;\n fma.rn.f32.bf16 %0, l, m, %2;\n}"
+      : "=f"(d)
+      : "r"(w), "f"(x));
+  return d;
+}
+__device__ __forceinline__ float minus_hi(float x, uint32_t w) {
+  float d;
+  asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %1;\n mov.b16 m, 0xbf80;\n fma.rn.f32.bf16 %0, h, m, %2;\n}"
+      : "=f"(d)
+      : "r"(w), "f"(x));
+  return d;
+}
 // Two values x as three bf16 pairs that add up to them: each term is the rest's
 // leading 8 bits (cut off, so that the rest is exact and packing is a byte
 // permute), the last one rounded.
 __device__ __forceinline__ void split3(uint64_t x, uint32_t &a, uint32_t &b, uint32_t &c) {
   float f0, f1;
   upk2(x, f0, f1);
-  uint32_t u0 = __float_as_uint(f0), u1 = __float_as_uint(f1);
-  a = __byte_perm(u0, u1, 0x7632);
-  x = add2(x, pk2(__uint_as_float((u0 & 0xffff0000u) ^ 0x80000000u), __uint_as_float((u1 & 0xffff0000u) ^ 0x80000000u)));
-  upk2(x, f0, f1);
-  u0 = __float_as_uint(f0), u1 = __float_as_uint(f1);
-  b = __byte_perm(u0, u1, 0x7632);
-  c = tc::pack_bf16x2(f0 - __uint_as_float(u0 & 0xffff0000u), f1 - __uint_as_float(u1 & 0xffff0000u));
+  a = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
+  f0 = minus_lo(f0, a);
+  f1 = minus_hi(f1, a);
+  b = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
+  c = tc::pack_bf16x2(minus_lo(f0, b), minus_hi(f1, b));
 }
 
 // KB, VB: 64-column boxes of the q/k roles and of the v/o roles
@@ -141,13 +163,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.p_ready[i], 2);
       mbar_init(&bar.p_free[i], 1);
-      mbar_init(&bar.o_full[i], 1);
-      mbar_init(&bar.o_free[i], 2 * VB);
-      mbar_init(&bar.k_done[i], 1);
-      mbar_init(&bar.kt_ready[i], kStateWarps);
+      mbar_init(&bar.v_ready[i], 4 * VB);
     }
-    mbar_init(bar.s_ready, kStateWarps);
+    mbar_init(&bar.v_free[0], 1);
+    mbar_init(bar.s_ready, 4 * VB);
+    mbar_init(bar.w_free, 4 * VB);
     mbar_init(bar.w_full, 1);
+    mbar_init(bar.o_full, 1);
+    mbar_init(bar.o_free, 2 * VB);
     mbar_init(bar.drain, 1);
     fence_mbar_init();
   }
@@ -195,15 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t s0 = smem_u32(sm);
-      // K-major operands: Q (A and B), K, P; MN-major: V (A), weighted K (B).  A's 128
-      // rows run past Q's 64 into the shared memory behind it; those rows of the
-      // result (and the lanes past 64 when VB = 1) are not read.
+      // K-major: Q (A and B), K, P; MN-major: K as the B operand of W.  A's 128 rows run
+      // past Q's 64 into the shared memory behind it; those rows of the result (and
+      // the lanes past 64 when VB = 1) are not read.
       const uint64_t dQ = desc_sw128(s0 + L::kQ, 16, 1024), dK = desc_sw128(s0 + L::kK, 16, 1024),
-                     dV = desc_sw128(s0 + L::kV, kBox, 1024), dK1 = desc_sw128(s0 + L::kK, kBox, 1024),
-                     dKt = desc_sw128(s0 + L::kKt, kBox, 1024),
-                     dP = desc_sw128(s0 + L::kP, 16, 1024);
-      constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iPV = idesc_bf16(128, 64, true, false),
-                         iQS = idesc_bf16(128, 64, false, false), iW = idesc_bf16(128, 64 * KB, true, true);
+                     dKn = desc_sw128(s0 + L::kK, kBox, 1024), dP = desc_sw128(s0 + L::kP, 16, 1024);
+      constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iW = idesc_bf16(128, 64 * KB, false, true);
       auto stage = [&](int i) { return (uint64_t)((i % ST) * (L::kStage / 16)); };
       auto scores = [&](int i) {
         mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
@@ -214,37 +234,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           pipe::umma_k<4>(tmem + kTmQK, dQ + stage(i) + b * (kBox / 16), dK + stage(i) + b * (kBox / 16), pipe::kStepK,
                           pipe::kStepK, iQK, b > 0);
         umma_commit(bar.qk_full);
-        umma_commit(&bar.k_done[i & 1]);
+      };
+      // W of half a block: the three terms' two steps of 16 tokens each
+      auto half_w = [&](int i, int half) {
+        mbar_wait(&bar.v_ready[half], parity(i), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          pipe::umma_ts_k<2>(tmem + kTmW, tmem + kTmT + half * kHalf + t * kTerm, dKn + stage(i) + half * (4096 / 16), 8,
+                             pipe::kStepMN, iW, half > 0 || t > 0);
       };
       if (!SUMMARY && nb > 0) scores(0);
       for (int i = 0; i < nb; ++i) {
         const int ob = i & 1;
+        if (SUMMARY)
+          mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
+        else if (i + 1 < nb)
+          scores(i + 1);
+        if (i > 0) mbar_wait(bar.w_free, parity(i - 1), wait);
+        half_w(i, 0);
         if (!SUMMARY) {
-          if (i + 1 < nb) scores(i + 1);
-          if (i >= 2) mbar_wait(&bar.o_free[ob], parity(i / 2 - 1), wait);
-          if (rows_of(block_of(i)) < kC) mbar_wait(&bar.kt_ready[ob], parity(i / 2), wait);  // V's tail
-          mbar_wait(&bar.p_ready[ob], parity(i / 2), wait);
-          tc_fence_after();
-          pipe::umma_k<4>(tmem + kTmO + 64 * ob, dV + stage(i), dP + ob * (kBox / 16), pipe::kStepMN, pipe::kStepK, iPV,
-                          false);
-          umma_commit(&bar.p_free[ob]);
           mbar_wait(bar.s_ready, parity(i), wait);
+          if (i > 0) mbar_wait(bar.o_free, parity(i - 1), wait);
           tc_fence_after();
 #pragma unroll
           for (int b = 0; b < KB; ++b)
-            pipe::umma_ts_k<4>(tmem + kTmOi + 64 * ob, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8,
-                               pipe::kStepK, iQS, b > 0);
-          umma_commit(&bar.o_full[ob]);
-        } else {
-          mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
-          mbar_wait(bar.s_ready, parity(i), wait);
+            pipe::umma_ts_k<4>(tmem + kTmOi, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8, pipe::kStepK, iQK,
+                               b > 0);
+          mbar_wait(&bar.v_ready[1], parity(i), wait);
+          mbar_wait(&bar.p_ready[ob], parity(i / 2), wait);
+          tc_fence_after();
+          pipe::umma_ts_k<4>(tmem + kTmO, tmem + kTmV, dP + ob * (kBox / 16), 8, pipe::kStepK, iQK, false);
+          umma_commit(bar.o_full);
+          umma_commit(&bar.p_free[ob]);
         }
-        mbar_wait(&bar.kt_ready[ob], parity(i / 2), wait);
-        tc_fence_after();
-        const uint64_t v = dV + stage(i), kt = dKt + (uint64_t)(ob * 2 * KB * (kBox / 16));
-        pipe::umma_k<4>(tmem + kTmW, v, dK1 + stage(i), pipe::kStepMN, pipe::kStepMN, iW, false);
-        pipe::umma_k<4>(tmem + kTmW, v, kt, pipe::kStepMN, pipe::kStepMN, iW, true);
-        pipe::umma_k<4>(tmem + kTmW, v, kt + KB * (kBox / 16), pipe::kStepMN, pipe::kStepMN, iW, true);
+        umma_commit(&bar.v_free[0]);
+        half_w(i, 1);
         umma_commit(bar.w_full);
         umma_commit(&bar.free[i % ST]);
       }
@@ -252,14 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(bar.drain);
       mbar_wait_drain(bar.drain, 0);
       for (int m = nb > ST ? nb - ST : 0; m < nb; ++m) mbar_wait_drain(&bar.free[m % ST], parity(m / ST));
-      if (nb > 0) mbar_wait_drain(bar.w_full, parity(nb - 1));
+      if (nb > 0) {
+        mbar_wait_drain(bar.w_full, parity(nb - 1));
+        mbar_wait_drain(&bar.v_free[0], parity(nb - 1));
+      }
       if (!SUMMARY && nb > 0) {
         mbar_wait_drain(bar.qk_full, parity(nb - 1));
-        for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) {
-          mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
-          mbar_wait_drain(&bar.o_full[m & 1], parity(m / 2));
-          mbar_wait_drain(&bar.k_done[m & 1], parity(m / 2));
-        }
+        mbar_wait_drain(bar.o_full, parity(nb - 1));
+        for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
       }
     }
   } else if (warp < 2) {
@@ -268,28 +293,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = threadIdx.x;  // row of the block
       for (int i = 0; i < nb; ++i) {
         const int nv = rows_of(block_of(i));
+        if (i >= 2) mbar_wait(&bar.p_free[i & 1], parity(i / 2 - 1), wait);
         mbar_wait(bar.qk_full, parity(i), wait);
         tc_fence_after();
-        float s[64];
-        tmem_ld32(pipe::tmem_quad(tmem + kTmQK, 0), *reinterpret_cast<float(*)[32]>(s));
-        tmem_ld32(pipe::tmem_quad(tmem + kTmQK, 32), *reinterpret_cast<float(*)[32]>(s + 32));
-        tc_fence_before();
-        pipe::warp_arrive(bar.qk_free);
-        if (i >= 2) mbar_wait(&bar.p_free[i & 1], parity(i / 2 - 1), wait);
         const uint32_t dst = smem_u32(sm + L::kP + (i & 1) * kBox);
         // columns past the end: in order, only rows past it see them
         const int jmax = REV ? nv : kC;
+#pragma unroll 1
+        for (int j0 = 0; j0 < kC; j0 += 16) {
+          // 32 rows against 16 columns: all masked, all live, or in between
+          const int lo = REV ? j0 - (32 * warp + 31) : 32 * warp - (j0 + 15), hi = lo + 46;  // least and largest distance
+          uint4 p0 = make_uint4(0, 0, 0, 0), p1 = p0;
+          if (hi >= 0) {
+            float s[16], v[8];
+            tmem_ld16(pipe::tmem_quad(tmem + kTmQK, j0), s);
+            const float *w = tab_p + (REV ? j0 - r : r - j0);
+            if (lo >= 0 && j0 + 16 <= jmax) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          float v[8];
+              for (int e = 0; e < 16; ++e) s[e] *= w[REV ? e : -e];
+            } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int j = 8 * x + e, d = REV ? j - r : r - j;
-            // a select, not a factor of zero: masked scores may be NaN
-            v[e] = d >= 0 && j < jmax ? s[j] * tab_p[d] : 0.f;
+              for (int e = 0; e < 16; ++e) {
+                const int d = REV ? j0 + e - r : r - j0 - e;
+                // a select, not a factor of zero: masked scores may be NaN
+                s[e] = d >= 0 && j0 + e < jmax ? s[e] * w[REV ? e : -e] : 0.f;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = s[e];
+            p0 = tc::pack8(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = s[8 + e];
+            p1 = tc::pack8(v);
           }
-          pipe::sts_u4(dst + sw128_offset(r, 8 * x), tc::pack8(v));
+          pipe::sts_u4(dst + sw128_offset(r, j0), p0);
+          pipe::sts_u4(dst + sw128_offset(r, j0 + 8), p1);
         }
+        tc_fence_before();
+        pipe::warp_arrive(bar.qk_free);
         fence_async_smem();
         pipe::warp_arrive(&bar.p_ready[i & 1]);
       }
@@ -302,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the address this lane gives to a group of four fragments: row i, columns of v
       const int fi = 8 * (lane >> 4) + (lane & 7), fc = 32 * quad + 8 * ((lane >> 3) & 1);
       for (int i = 0; i < nb; ++i) {
-        const int ob = i & 1, st = i % ST, blk = block_of(i), nv = rows_of(blk);
+        const int st = i % ST, blk = block_of(i), nv = rows_of(blk);
         const long long row0 = u.t0 + (long long)blk * kC;
         const uint32_t so = smem_u32(sm + st * L::kStage + L::kQ);
         float w[16];  // what the incoming state's part of this lane's columns i weighs
@@ -313,19 +354,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 8 * m + 2 * (lane & 3) + e;
             w[2 * m + e] = tab_in[REV ? max(nv - 1 - r, 0) : r + 1];
           }
-        mbar_wait(&bar.o_full[ob], parity(i / 2), wait);
+        mbar_wait(bar.o_full, parity(i), wait);
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {  // 16 lanes (columns of v) at a time
           uint32_t a[32], b[32];
           const uint32_t lanes = (uint32_t)(16 * half) << 16;
-          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmO + 64 * ob, 0) + lanes, a);
-          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmOi + 64 * ob, 0) + lanes, b);
+          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmO, 0) + lanes, a);
+          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmOi, 0) + lanes, b);
           tmem_wait_ld32(a);
           tmem_wait_ld32(b);
           if (half == 1) {
             tc_fence_before();
-            pipe::warp_arrive(&bar.o_free[ob]);
+            pipe::warp_arrive(bar.o_free);
           }
           float o[32];
 #pragma unroll
@@ -375,12 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tt == 0) bulk_wait0();
     }
-  } else {
+  } else if ((warp & 3) < 2 * VB) {
     // ------------------------------------------------------------ state
     constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
-    const int tt = threadIdx.x - 32 * kStateWarp0, quad = warp & 3, half = (warp - kStateWarp0) >> 2;
-    const int c = 32 * quad + lane, a0 = half * kCols;
-    const bool holds = quad < 2 * VB;  // this warp's lanes are columns of the state (warp-uniform)
+    const int quad = warp & 3, sub = (warp - kStateWarp0) >> 2;  // two warps share a quadrant of lanes
+    const int c = 32 * quad + lane, a0 = sub * kCols;
     const size_t dd = (size_t)p.dk * p.dv;
     uint64_t S[kCols / 2];  // pairs along dk
     {
@@ -393,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (!SUMMARY && p.init) {
         in = p.init + ((size_t)u.seq * p.H + h) * dd;
       }
-      const bool live = in && holds && c < p.dv;
+      const bool live = in && c < p.dv;
 #pragma unroll
       for (int a = 0; a < kCols; a += 2) {  // dk is even
         float x = 0.f, y = 0.f;
@@ -405,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     auto publish = [&] {  // S^T as the A operand: lane = column of v, bf16 pairs along dk
-      if (!SUMMARY && holds) {
+      if (!SUMMARY) {
 #pragma unroll
         for (int x = 0; x < kCols / 2; x += 16) {
           uint32_t w[16];
@@ -418,75 +458,91 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16_async(pipe::tmem_quad(tmem + kTmS, a0 / 2 + x), w);
         }
         tmem_wait_st();
+        tc_fence_before();
+        pipe::warp_arrive(bar.s_ready);
       }
-      tc_fence_before();
-      pipe::warp_arrive(bar.s_ready);
     };
-    // the three terms of diag(lam^b) K of block i: the first over K itself
+    // V^T and its three weighted terms of this warp's 16 tokens of half a block: matrix
+    // loads of 8 tokens x 8 columns (lane: its address), 16 columns of v at a time
     const uint32_t s0 = smem_u32(sm);
-    auto weigh = [&](int i) {
-      const int st = i % ST, nv = rows_of(block_of(i));
-      const uint32_t sk = s0 + st * L::kStage + L::kK, sv = s0 + st * L::kStage + L::kV,
-                     skt = s0 + L::kKt + (uint32_t)(i & 1) * (2 * KB * kBox);
-      mbar_wait(&bar.full[st], parity(i / ST), wait);
-      if (!SUMMARY) mbar_wait(&bar.k_done[i & 1], parity(i / 2), wait);
-#pragma unroll
-      for (int x = 0; x < 2 * KB; ++x) {
-        const int e = tt + 256 * x, r = (e >> 3) & 63, cc = e & 7;
-        const uint32_t off = (uint32_t)(e >> 9) * kBox + sw128_offset(r, 8 * cc);
-        uint4 raw, t0 = make_uint4(0, 0, 0, 0), t1 = t0, t2 = t0;
-        if (r < nv) {
-          const float w = tab_st[REV ? r + 1 : nv - 1 - r];
-          const uint64_t w2 = pk2(w, w);
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
-                       : "r"(sk + off));
-          split3(mul2(w2, pk2(lo_f(raw.x), hi_f(raw.x))), t0.x, t1.x, t2.x);
-          split3(mul2(w2, pk2(lo_f(raw.y), hi_f(raw.y))), t0.y, t1.y, t2.y);
-          split3(mul2(w2, pk2(lo_f(raw.z), hi_f(raw.z))), t0.z, t1.z, t2.z);
-          split3(mul2(w2, pk2(lo_f(raw.w), hi_f(raw.w))), t0.w, t1.w, t2.w);
-        }
-        pipe::sts_u4(sk + off, t0);
-        pipe::sts_u4(skt + off, t1);
-        pipe::sts_u4(skt + KB * kBox + off, t2);
-      }
-      if (nv < kC) {
-#pragma unroll
-        for (int x = 0; x < 2 * VB; ++x) {
-          const int e = tt + 256 * x, r = (e >> 3) & 63, cc = e & 7;
-          if (r >= nv) pipe::sts_u4(sv + (uint32_t)(e >> 9) * kBox + sw128_offset(r, 8 * cc), make_uint4(0, 0, 0, 0));
+    const int lr = (lane & 7) + 8 * (lane >> 4), lc = 32 * (quad & 1) + 8 * ((lane >> 3) & 1);
+    auto weigh = [&](int i, int half) {
+      const int st = i % ST, nv = rows_of(block_of(i)), j0 = 32 * half + 16 * sub;
+      const uint32_t sv = s0 + st * L::kStage + L::kV + (uint32_t)(quad >> 1) * kBox;
+      if (half == 0) {
+        mbar_wait(&bar.full[st], parity(i / ST), wait);
+        if (nv < kC) {  // K's rows past the end become zeros too
+          const uint32_t sk = s0 + st * L::kStage + L::kK;
+          for (int e = (sub * 2 * VB + quad) * 32 + lane; e < (kC - nv) * 8 * KB; e += 128 * VB) {
+            const int x = e % (8 * KB), r = nv + e / (8 * KB);
+            pipe::sts_u4(sk + (uint32_t)(x >> 3) * kBox + sw128_offset(r, 8 * (x & 7)), make_uint4(0, 0, 0, 0));
+          }
+          fence_async_smem();
         }
       }
-      fence_async_smem();
-      pipe::warp_arrive(&bar.kt_ready[i & 1]);
+      uint64_t w[2];  // weights of tokens j0 + 8 x + 2 (lane % 4) and the next; whether they exist
+      uint32_t live[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = j0 + 8 * x + 2 * (lane & 3);
+        const int n0 = REV ? j + 1 : nv - 1 - j, n1 = REV ? j + 2 : nv - 2 - j;
+        w[x] = pk2(tab_st[min(max(n0, 0), kC)], tab_st[min(max(n1, 0), kC)]);
+        live[x] = (j < nv ? 0xffffu : 0u) | (j + 1 < nv ? 0xffff0000u : 0u);
+      }
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        uint32_t f[4], t0[4], t1[4], t2[4];
+        ldmatrix4_trans(sv + sw128_offset(j0 + lr, lc + 16 * q), f[0], f[1], f[2], f[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[e] &= live[e >> 1];
+          split3(mul2(w[e >> 1], pk2(lo_f(f[e]), hi_f(f[e]))), t0[e], t1[e], t2[e]);
+        }
+        const uint32_t lanes = (uint32_t)(16 * q) << 16, col = kTmT + half * kHalf + 8 * sub;
+        if (!SUMMARY) tmem_st_16x128_async(pipe::tmem_quad(tmem + kTmV, j0 / 2) + lanes, f[0], f[1], f[2], f[3]);
+        tmem_st_16x128_async(pipe::tmem_quad(tmem + col, 0) + lanes, t0[0], t0[1], t0[2], t0[3]);
+        tmem_st_16x128_async(pipe::tmem_quad(tmem + col, kTerm) + lanes, t1[0], t1[1], t1[2], t1[3]);
+        tmem_st_16x128_async(pipe::tmem_quad(tmem + col, 2 * kTerm) + lanes, t2[0], t2[1], t2[2], t2[3]);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      pipe::warp_arrive(&bar.v_ready[half]);
     };
     const float2 full = la_pow2(g, kC);
-    if (nb > 0) {
-      publish();
-      weigh(0);
-    }
-    for (int i = 0; i < nb; ++i) {
-      if (i + 1 < nb) weigh(i + 1);  // while the tensor core works on block i
+    auto update = [&](int i) {  // the state after block i
       const int nv = rows_of(block_of(i));
       const float2 carry = nv == kC ? full : la_pow2(g, nv);
       const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
-      // W done: so are the MMAs issued before it, which read the weighted K and S^T
+      // W done: so are the MMAs issued before it, which read the second half's terms and S^T
       mbar_wait(bar.w_full, parity(i), wait);
       tc_fence_after();
-      if (holds) {
+      float w[kCols];
 #pragma unroll
-        for (int x = 0; x < kCols; x += 32) {
-          float w[32];
-          tmem_ld32(pipe::tmem_quad(tmem + kTmW, a0 + x), w);
+      for (int x = 0; x < kCols; x += 32)
+        tmem_ld32(pipe::tmem_quad(tmem + kTmW, a0 + x), *reinterpret_cast<float(*)[32]>(w + x));
+      tc_fence_before();
+      pipe::warp_arrive(bar.w_free);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint64_t &t = S[x / 2 + e];
-            t = fma2(t, chi, fma2(t, clo, pk2(w[2 * e], w[2 * e + 1])));
-          }
-        }
+      for (int e = 0; e < kCols / 2; ++e) S[e] = fma2(S[e], chi, fma2(S[e], clo, pk2(w[2 * e], w[2 * e + 1])));
+    };
+    // Half-blocks in order: the first half's terms of a block while the tensor core works on
+    // the rest of the block before, then the state, then the second half's.  One
+    // copy of the code of each: the roles together are more than the instruction caches
+    // hold at speed (unrolled, a quarter of all warp cycles waited for instructions).
+#pragma unroll 1
+    for (int n = 0; n < 2 * nb; ++n) {
+      const int i = n >> 1, half = n & 1;
+      if (half == 0 && i > 0) {
+        mbar_wait(&bar.v_free[0], parity(i - 1), wait);
+        tc_fence_after();
       }
-      if (i + 1 < nb) publish();
+      if (half == 1) {
+        if (i > 0) update(i - 1);
+        publish();
+      }
+      weigh(i, half);
     }
+    if (nb > 0) update(nb - 1);
     float *out = nullptr;
     int sa = p.sa, sb = p.sb;
     if (SUMMARY) {
@@ -496,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (!p.split && p.fin) {
       out = p.fin + ((size_t)u.seq * p.H + h) * dd;
     }
-    if (out && holds && c < p.dv) {
+    if (out && c < p.dv) {
 #pragma unroll
       for (int a = 0; a < kCols; a += 2) {
         float x, y;

@@ -273,6 +273,21 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+// 8 consecutive 32-bit columns of 16 TMEM lanes (taddr's lane: the warp's first or 17th), without waiting: of lane
+// t, a and c go to lane t / 4, b and d to lane t / 4 + 8; a and b to column t % 4, c and d to column 4 + t % 4.
+__device__ __forceinline__ void tmem_st_16x128_async(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+// four 8 x 8 bf16 matrices out of shared memory (16-byte rows at the addresses of lanes 8q..8q+7), each transposed:
+// lane t gets of matrix q column t / 4, rows 2 (t % 4) and the next
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
 // four 8 x 8 bf16 fragments (lane t: row t / 4, columns 2 (t % 4) and the next) into shared memory, each
 // transposed: the 16-byte row at the address of lane 8q + i receives column i of fragment q
 __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
