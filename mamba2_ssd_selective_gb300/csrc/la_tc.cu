@@ -25,11 +25,12 @@
 //   3       TMEM owner and MMA issuer
 //   4-7     outputs: O^T and Oi^T out of TMEM as fragments, combined, transposed by stmatrix into
 //           the block's Q tile, stored by TMA
-//   8-15    state: V^T and the three terms of V^T diag(lam^b) into TMEM, then S = lam^nv S + W and
-//           S^T into TMEM as the next block's operand
+//   8-15    state: S = lam^nv S + W, and S^T into TMEM as the next block's operand
+//   16-19   V^T and the three terms of V^T diag(lam^b) into TMEM
 // The tensor core's order is scores of block i + 1, W's first half (32 tokens),
 // Oi, O, W's second half: the halves' operands alternate between two buffers, so
-// that the state warps prepare one while the other is in use.
+// that one is prepared while the other is in use, and W's read (not the whole
+// state update) is what the next block's first half waits for.
 // The last block of a sequence is masked: rows past its end belong to another
 // sequence, so V's are replaced by zeros on their way to TMEM and K's in shared
 // memory (0 * NaN would be NaN), scores with them are selected away, and nothing
@@ -47,8 +48,8 @@ using namespace sm100;
 using pipe::parity;
 
 constexpr int kC = 64;  // tokens of a block
-constexpr int kThreads = 512;
-constexpr int kStateWarp0 = 8, kOutWarp0 = 4;
+constexpr int kThreads = 640;
+constexpr int kOutWarp0 = 4, kStateWarp0 = 8, kWeighWarp0 = 16;
 constexpr uint32_t kBox = 8192;  // [64 tokens x 64 columns] bf16
 
 // TMEM columns: scores, O, Oi, W, S^T (bf16), two buffers of the three terms of half a block, V^T
@@ -79,7 +80,7 @@ struct Bars {
   uint64_t *s_ready;            // S^T of the block in TMEM
   uint64_t *w_free;             // the previous block's W read out of TMEM
   uint64_t *v_ready, *v_free;   // [2] half a block's V^T and terms in TMEM / read by its MMAs
-  uint64_t *w_full;             // W formed: v_free[1] and the end of the block's MMAs
+  uint64_t *w_full;             // W formed (and S^T read)
   uint64_t *o_full, *o_free;
   uint64_t *drain;
   __device__ explicit Bars(uint64_t *b) {
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtl wait{p.status, p.wait_ns};
   const Bars<ST> bar(reinterpret_cast<uint64_t *>(sm + L::kBar));
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + L::kNumBars * 8);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const int nb = (u.len + kC - 1) / kC;
   const float g = __ldg(p.g + h);
   // tables: lam^n, n = 0..64, times the scale of the products, the incoming state, the outgoing state
@@ -163,9 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.p_ready[i], 2);
       mbar_init(&bar.p_free[i], 1);
-      mbar_init(&bar.v_ready[i], 4 * VB);
+      mbar_init(&bar.v_free[i], 1);
+      mbar_init(&bar.v_ready[i], 2 * VB);
     }
-    mbar_init(&bar.v_free[0], 1);
     mbar_init(bar.s_ready, 4 * VB);
     mbar_init(bar.w_free, 4 * VB);
     mbar_init(bar.w_full, 1);
@@ -187,156 +188,165 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
   // processing order: block i is rows [64 blk, 64 blk + nv) of the segment
   auto block_of = [&](int i) { return REV ? nb - 1 - i : i; };
   auto rows_of = [&](int blk) { return min(kC, u.len - blk * kC); };
 
-  if (warp == 2) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0 && nb > 0) {
-      if (!SUMMARY) prefetch_tmap(&tm_q);
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-      int i = 0;
-      for (; i < nb; ++i) {
-        const int st = i % ST, row = u.t0 + block_of(i) * kC;
-        if (i >= ST && !mbar_wait(&bar.free[st], parity(i / ST - 1), wait)) break;
-        uint8_t *base = sm + st * L::kStage;
-        mbar_expect_tx(&bar.full[st], L::kLoad);
-        for (int b = 0; b < KB; ++b) {
-          if (!SUMMARY) tma_load_3d(base + L::kQ + b * kBox, &tm_q, &bar.full[st], 64 * b, h / p.gq, row);
-          tma_load_3d(base + L::kK + b * kBox, &tm_k, &bar.full[st], 64 * b, h / p.gk, row);
+  // The block is launched with 640 x 96 registers; the state warps, which hold 64 values of the state a
+  // thread, take what the others do not need: 128 x (72 + 88 + 2 * 112 + 88) = 60416 <= 61440.
+  if (warp < kOutWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 2) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0 && nb > 0) {
+        if (!SUMMARY) prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        int i = 0;
+        for (; i < nb; ++i) {
+          const int st = i % ST, row = u.t0 + block_of(i) * kC;
+          if (i >= ST && !mbar_wait(&bar.free[st], parity(i / ST - 1), wait)) break;
+          uint8_t *base = sm + st * L::kStage;
+          mbar_expect_tx(&bar.full[st], L::kLoad);
+          for (int b = 0; b < KB; ++b) {
+            if (!SUMMARY) tma_load_3d(base + L::kQ + b * kBox, &tm_q, &bar.full[st], 64 * b, h / p.gq, row);
+            tma_load_3d(base + L::kK + b * kBox, &tm_k, &bar.full[st], 64 * b, h / p.gk, row);
+          }
+          for (int b = 0; b < VB; ++b)
+            tma_load_3d(base + L::kV + b * kBox, &tm_v, &bar.full[st], 64 * b, h / p.gv, row);
         }
-        for (int b = 0; b < VB; ++b)
-          tma_load_3d(base + L::kV + b * kBox, &tm_v, &bar.full[st], 64 * b, h / p.gv, row);
+        // every load issued has landed before the CTA releases its shared memory
+        for (int m = i > ST ? i - ST : 0; m < i; ++m) mbar_wait_drain(&bar.full[m % ST], parity(m / ST));
       }
-      // every load issued has landed before the CTA releases its shared memory
-      for (int m = i > ST ? i - ST : 0; m < i; ++m) mbar_wait_drain(&bar.full[m % ST], parity(m / ST));
-    }
-  } else if (warp == 3) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t s0 = smem_u32(sm);
-      // K-major: Q (A and B), K, P; MN-major: K as the B operand of W.  A's 128 rows run
-      // past Q's 64 into the shared memory behind it; those rows of the result (and
-      // the lanes past 64 when VB = 1) are not read.
-      const uint64_t dQ = desc_sw128(s0 + L::kQ, 16, 1024), dK = desc_sw128(s0 + L::kK, 16, 1024),
-                     dKn = desc_sw128(s0 + L::kK, kBox, 1024), dP = desc_sw128(s0 + L::kP, 16, 1024);
-      constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iW = idesc_bf16(128, 64 * KB, false, true);
-      auto stage = [&](int i) { return (uint64_t)((i % ST) * (L::kStage / 16)); };
-      auto scores = [&](int i) {
-        mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
-        if (i > 0) mbar_wait(bar.qk_free, parity(i - 1), wait);
-        tc_fence_after();
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-          pipe::umma_k<4>(tmem + kTmQK, dQ + stage(i) + b * (kBox / 16), dK + stage(i) + b * (kBox / 16), pipe::kStepK,
-                          pipe::kStepK, iQK, b > 0);
-        umma_commit(bar.qk_full);
-      };
-      // W of half a block: the three terms' two steps of 16 tokens each
-      auto half_w = [&](int i, int half) {
-        mbar_wait(&bar.v_ready[half], parity(i), wait);
-        tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < 3; ++t)
-          pipe::umma_ts_k<2>(tmem + kTmW, tmem + kTmT + half * kHalf + t * kTerm, dKn + stage(i) + half * (4096 / 16), 8,
-                             pipe::kStepMN, iW, half > 0 || t > 0);
-      };
-      if (!SUMMARY && nb > 0) scores(0);
-      for (int i = 0; i < nb; ++i) {
-        const int ob = i & 1;
-        if (SUMMARY)
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ MMA issuer
+      {  // the whole warp, so that descriptors stay in uniform registers; one lane acts
+        const uint32_t el = elect_one();
+        const uint32_t s0 = smem_u32(sm);
+        // K-major: Q (A and B), K, P; MN-major: K as the B operand of W.  A's 128 rows run
+        // past Q's 64 into the shared memory behind it; those rows of the result (and
+        // the lanes past 64 when VB = 1) are not read.
+        const uint64_t dQ = desc_sw128(s0 + L::kQ, 16, 1024), dK = desc_sw128(s0 + L::kK, 16, 1024),
+                       dKn = desc_sw128(s0 + L::kK, kBox, 1024), dP = desc_sw128(s0 + L::kP, 16, 1024);
+        constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iW = idesc_bf16(128, 64 * KB, false, true);
+        auto stage = [&](int i) { return (uint64_t)((i % ST) * (L::kStage / 16)); };
+        auto scores = [&](int i) {
           mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
-        else if (i + 1 < nb)
-          scores(i + 1);
-        if (i > 0) mbar_wait(bar.w_free, parity(i - 1), wait);
-        half_w(i, 0);
-        if (!SUMMARY) {
-          mbar_wait(bar.s_ready, parity(i), wait);
-          if (i > 0) mbar_wait(bar.o_free, parity(i - 1), wait);
+          if (i > 0) mbar_wait(bar.qk_free, parity(i - 1), wait);
           tc_fence_after();
 #pragma unroll
           for (int b = 0; b < KB; ++b)
-            pipe::umma_ts_k<4>(tmem + kTmOi, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8, pipe::kStepK, iQK,
-                               b > 0);
-          mbar_wait(&bar.v_ready[1], parity(i), wait);
-          mbar_wait(&bar.p_ready[ob], parity(i / 2), wait);
+            pipe::umma_k_el<4>(el, tmem + kTmQK, dQ + stage(i) + b * (kBox / 16), dK + stage(i) + b * (kBox / 16), pipe::kStepK,
+                            pipe::kStepK, iQK, b > 0);
+          umma_commit_el(el, bar.qk_full);
+        };
+        // W of half a block: the three terms' two steps of 16 tokens each
+        auto half_w = [&](int i, int half) {
+          mbar_wait(&bar.v_ready[half], parity(i), wait);
           tc_fence_after();
-          pipe::umma_ts_k<4>(tmem + kTmO, tmem + kTmV, dP + ob * (kBox / 16), 8, pipe::kStepK, iQK, false);
-          umma_commit(bar.o_full);
-          umma_commit(&bar.p_free[ob]);
-        }
-        umma_commit(&bar.v_free[0]);
-        half_w(i, 1);
-        umma_commit(bar.w_full);
-        umma_commit(&bar.free[i % ST]);
-      }
-      // every MMA and every arrival of a commit has landed before the CTA ends
-      umma_commit(bar.drain);
-      mbar_wait_drain(bar.drain, 0);
-      for (int m = nb > ST ? nb - ST : 0; m < nb; ++m) mbar_wait_drain(&bar.free[m % ST], parity(m / ST));
-      if (nb > 0) {
-        mbar_wait_drain(bar.w_full, parity(nb - 1));
-        mbar_wait_drain(&bar.v_free[0], parity(nb - 1));
-      }
-      if (!SUMMARY && nb > 0) {
-        mbar_wait_drain(bar.qk_full, parity(nb - 1));
-        mbar_wait_drain(bar.o_full, parity(nb - 1));
-        for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
-      }
-    }
-  } else if (warp < 2) {
-    // ------------------------------------------------------------ P
-    if (!SUMMARY) {
-      const int r = threadIdx.x;  // row of the block
-      for (int i = 0; i < nb; ++i) {
-        const int nv = rows_of(block_of(i));
-        if (i >= 2) mbar_wait(&bar.p_free[i & 1], parity(i / 2 - 1), wait);
-        mbar_wait(bar.qk_full, parity(i), wait);
-        tc_fence_after();
-        const uint32_t dst = smem_u32(sm + L::kP + (i & 1) * kBox);
-        // columns past the end: in order, only rows past it see them
-        const int jmax = REV ? nv : kC;
-#pragma unroll 1
-        for (int j0 = 0; j0 < kC; j0 += 16) {
-          // 32 rows against 16 columns: all masked, all live, or in between
-          const int lo = REV ? j0 - (32 * warp + 31) : 32 * warp - (j0 + 15), hi = lo + 46;  // least and largest distance
-          uint4 p0 = make_uint4(0, 0, 0, 0), p1 = p0;
-          if (hi >= 0) {
-            float s[16], v[8];
-            tmem_ld16(pipe::tmem_quad(tmem + kTmQK, j0), s);
-            const float *w = tab_p + (REV ? j0 - r : r - j0);
-            if (lo >= 0 && j0 + 16 <= jmax) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) s[e] *= w[REV ? e : -e];
-            } else {
+          for (int t = 0; t < 3; ++t)
+            pipe::umma_ts_k_el<2>(el, tmem + kTmW, tmem + kTmT + half * kHalf + t * kTerm, dKn + stage(i) + half * (4096 / 16), 8,
+                               pipe::kStepMN, iW, half > 0 || t > 0);
+        };
+        if (!SUMMARY && nb > 0) scores(0);
+        for (int i = 0; i < nb; ++i) {
+          const int ob = i & 1;
+          if (SUMMARY)
+            mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
+          else if (i + 1 < nb)
+            scores(i + 1);
+          if (i > 0) mbar_wait(bar.w_free, parity(i - 1), wait);
+          half_w(i, 0);
+          if (!SUMMARY) {
+            mbar_wait(bar.s_ready, parity(i), wait);
+            if (i > 0) mbar_wait(bar.o_free, parity(i - 1), wait);
+            tc_fence_after();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int d = REV ? j0 + e - r : r - j0 - e;
-                // a select, not a factor of zero: masked scores may be NaN
-                s[e] = d >= 0 && j0 + e < jmax ? s[e] * w[REV ? e : -e] : 0.f;
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = s[e];
-            p0 = tc::pack8(v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = s[8 + e];
-            p1 = tc::pack8(v);
+            for (int b = 0; b < KB; ++b)
+              pipe::umma_ts_k_el<4>(el, tmem + kTmOi, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8, pipe::kStepK, iQK,
+                                 b > 0);
+            mbar_wait(&bar.v_ready[1], parity(i), wait);
+            mbar_wait(&bar.p_ready[ob], parity(i / 2), wait);
+            tc_fence_after();
+            pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmV, dP + ob * (kBox / 16), 8, pipe::kStepK, iQK, false);
+            umma_commit_el(el, bar.o_full);
+            umma_commit_el(el, &bar.p_free[ob]);
           }
-          pipe::sts_u4(dst + sw128_offset(r, j0), p0);
-          pipe::sts_u4(dst + sw128_offset(r, j0 + 8), p1);
+          umma_commit_el(el, &bar.v_free[0]);
+          half_w(i, 1);
+          umma_commit_el(el, bar.w_full);
+          umma_commit_el(el, &bar.v_free[1]);
+          umma_commit_el(el, &bar.free[i % ST]);
         }
-        tc_fence_before();
-        pipe::warp_arrive(bar.qk_free);
-        fence_async_smem();
-        pipe::warp_arrive(&bar.p_ready[i & 1]);
+        // every MMA and every arrival of a commit has landed before the CTA ends
+        umma_commit_el(el, bar.drain);
+        mbar_wait_drain(bar.drain, 0);
+        for (int m = nb > ST ? nb - ST : 0; m < nb; ++m) mbar_wait_drain(&bar.free[m % ST], parity(m / ST));
+        if (nb > 0) {
+          mbar_wait_drain(bar.w_full, parity(nb - 1));
+          mbar_wait_drain(&bar.v_free[0], parity(nb - 1));
+          mbar_wait_drain(&bar.v_free[1], parity(nb - 1));
+        }
+        if (!SUMMARY && nb > 0) {
+          mbar_wait_drain(bar.qk_full, parity(nb - 1));
+          mbar_wait_drain(bar.o_full, parity(nb - 1));
+          for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ P
+      if (!SUMMARY) {
+        const int r = threadIdx.x;  // row of the block
+        for (int i = 0; i < nb; ++i) {
+          const int nv = rows_of(block_of(i));
+          if (i >= 2) mbar_wait(&bar.p_free[i & 1], parity(i / 2 - 1), wait);
+          mbar_wait(bar.qk_full, parity(i), wait);
+          tc_fence_after();
+          const uint32_t dst = smem_u32(sm + L::kP + (i & 1) * kBox);
+          // columns past the end: in order, only rows past it see them
+          const int jmax = REV ? nv : kC;
+#pragma unroll 1
+          for (int j0 = 0; j0 < kC; j0 += 16) {
+            // 32 rows against 16 columns: all masked, all live, or in between
+            const int lo = REV ? j0 - (32 * warp + 31) : 32 * warp - (j0 + 15), hi = lo + 46;  // least and largest distance
+            uint4 p0 = make_uint4(0, 0, 0, 0), p1 = p0;
+            if (hi >= 0) {
+              float s[16], v[8];
+              tmem_ld16(pipe::tmem_quad(tmem + kTmQK, j0), s);
+              const float *w = tab_p + (REV ? j0 - r : r - j0);
+              if (lo >= 0 && j0 + 16 <= jmax) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] *= w[REV ? e : -e];
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int d = REV ? j0 + e - r : r - j0 - e;
+                  // a select, not a factor of zero: masked scores may be NaN
+                  s[e] = d >= 0 && j0 + e < jmax ? s[e] * w[REV ? e : -e] : 0.f;
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = s[e];
+              p0 = tc::pack8(v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = s[8 + e];
+              p1 = tc::pack8(v);
+            }
+            pipe::sts_u4(dst + sw128_offset(r, j0), p0);
+            pipe::sts_u4(dst + sw128_offset(r, j0 + 8), p1);
+          }
+          tc_fence_before();
+          pipe::warp_arrive(bar.qk_free);
+          fence_async_smem();
+          pipe::warp_arrive(&bar.p_ready[i & 1]);
+        }
       }
     }
   } else if (warp < kStateWarp0) {
     // ------------------------------------------------------------ outputs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (!SUMMARY && warp < kOutWarp0 + 2 * VB) {
       constexpr int kOutThreads = 64 * VB;
       const int tt = threadIdx.x - 32 * kOutWarp0, quad = warp & 3;
@@ -416,8 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tt == 0) bulk_wait0();
     }
-  } else if ((warp & 3) < 2 * VB) {
+  } else if (warp < kWeighWarp0) {
     // ------------------------------------------------------------ state
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    if ((warp & 3) < 2 * VB) {
     constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
     const int quad = warp & 3, sub = (warp - kStateWarp0) >> 2;  // two warps share a quadrant of lanes
     const int c = 32 * quad + lane, a0 = sub * kCols;
@@ -462,52 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         pipe::warp_arrive(bar.s_ready);
       }
     };
-    // V^T and its three weighted terms of this warp's 16 tokens of half a block: matrix
-    // loads of 8 tokens x 8 columns (lane: its address), 16 columns of v at a time
-    const uint32_t s0 = smem_u32(sm);
-    const int lr = (lane & 7) + 8 * (lane >> 4), lc = 32 * (quad & 1) + 8 * ((lane >> 3) & 1);
-    auto weigh = [&](int i, int half) {
-      const int st = i % ST, nv = rows_of(block_of(i)), j0 = 32 * half + 16 * sub;
-      const uint32_t sv = s0 + st * L::kStage + L::kV + (uint32_t)(quad >> 1) * kBox;
-      if (half == 0) {
-        mbar_wait(&bar.full[st], parity(i / ST), wait);
-        if (nv < kC) {  // K's rows past the end become zeros too
-          const uint32_t sk = s0 + st * L::kStage + L::kK;
-          for (int e = (sub * 2 * VB + quad) * 32 + lane; e < (kC - nv) * 8 * KB; e += 128 * VB) {
-            const int x = e % (8 * KB), r = nv + e / (8 * KB);
-            pipe::sts_u4(sk + (uint32_t)(x >> 3) * kBox + sw128_offset(r, 8 * (x & 7)), make_uint4(0, 0, 0, 0));
-          }
-          fence_async_smem();
-        }
-      }
-      uint64_t w[2];  // weights of tokens j0 + 8 x + 2 (lane % 4) and the next; whether they exist
-      uint32_t live[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int j = j0 + 8 * x + 2 * (lane & 3);
-        const int n0 = REV ? j + 1 : nv - 1 - j, n1 = REV ? j + 2 : nv - 2 - j;
-        w[x] = pk2(tab_st[min(max(n0, 0), kC)], tab_st[min(max(n1, 0), kC)]);
-        live[x] = (j < nv ? 0xffffu : 0u) | (j + 1 < nv ? 0xffff0000u : 0u);
-      }
-#pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        uint32_t f[4], t0[4], t1[4], t2[4];
-        ldmatrix4_trans(sv + sw128_offset(j0 + lr, lc + 16 * q), f[0], f[1], f[2], f[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[e] &= live[e >> 1];
-          split3(mul2(w[e >> 1], pk2(lo_f(f[e]), hi_f(f[e]))), t0[e], t1[e], t2[e]);
-        }
-        const uint32_t lanes = (uint32_t)(16 * q) << 16, col = kTmT + half * kHalf + 8 * sub;
-        if (!SUMMARY) tmem_st_16x128_async(pipe::tmem_quad(tmem + kTmV, j0 / 2) + lanes, f[0], f[1], f[2], f[3]);
-        tmem_st_16x128_async(pipe::tmem_quad(tmem + col, 0) + lanes, t0[0], t0[1], t0[2], t0[3]);
-        tmem_st_16x128_async(pipe::tmem_quad(tmem + col, kTerm) + lanes, t1[0], t1[1], t1[2], t1[3]);
-        tmem_st_16x128_async(pipe::tmem_quad(tmem + col, 2 * kTerm) + lanes, t2[0], t2[1], t2[2], t2[3]);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      pipe::warp_arrive(&bar.v_ready[half]);
-    };
     const float2 full = la_pow2(g, kC);
     auto update = [&](int i) {  // the state after block i
       const int nv = rows_of(block_of(i));
@@ -516,31 +482,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // W done: so are the MMAs issued before it, which read the second half's terms and S^T
       mbar_wait(bar.w_full, parity(i), wait);
       tc_fence_after();
-      float w[kCols];
 #pragma unroll
-      for (int x = 0; x < kCols; x += 32)
-        tmem_ld32(pipe::tmem_quad(tmem + kTmW, a0 + x), *reinterpret_cast<float(*)[32]>(w + x));
-      tc_fence_before();
-      pipe::warp_arrive(bar.w_free);
+      for (int x = 0; x < kCols; x += 32) {
+        float w[32];
+        tmem_ld32(pipe::tmem_quad(tmem + kTmW, a0 + x), w);
+        if (x + 32 == kCols) {
+          tc_fence_before();
+          pipe::warp_arrive(bar.w_free);
+        }
 #pragma unroll
-      for (int e = 0; e < kCols / 2; ++e) S[e] = fma2(S[e], chi, fma2(S[e], clo, pk2(w[2 * e], w[2 * e + 1])));
+        for (int e = 0; e < 16; ++e) {
+          uint64_t &t = S[x / 2 + e];
+          t = fma2(t, chi, fma2(t, clo, pk2(w[2 * e], w[2 * e + 1])));
+        }
+      }
     };
-    // Half-blocks in order: the first half's terms of a block while the tensor core works on
-    // the rest of the block before, then the state, then the second half's.  One
-    // copy of the code of each: the roles together are more than the instruction caches
-    // hold at speed (unrolled, a quarter of all warp cycles waited for instructions).
 #pragma unroll 1
-    for (int n = 0; n < 2 * nb; ++n) {
-      const int i = n >> 1, half = n & 1;
-      if (half == 0 && i > 0) {
-        mbar_wait(&bar.v_free[0], parity(i - 1), wait);
-        tc_fence_after();
-      }
-      if (half == 1) {
-        if (i > 0) update(i - 1);
-        publish();
-      }
-      weigh(i, half);
+    for (int i = 0; i < nb; ++i) {
+      if (i > 0) update(i - 1);
+      publish();
     }
     if (nb > 0) update(nb - 1);
     float *out = nullptr;
@@ -562,6 +522,66 @@ __global__ void __launch_bounds__(kThreads, 1)
           out[(size_t)(a0 + a + 1) * sa + (size_t)c * sb] = y;
         }
       }
+    }
+    }
+  } else {
+    // ------------------------------------------------------------ weighted V
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // half-blocks of 32 tokens in order; matrix loads of 8 tokens x 8 columns (lane: its
+    // address), 16 tokens and 16 columns of v at a time
+    const int quad = warp & 3;
+    const uint32_t s0 = smem_u32(sm);
+    const int lr = (lane & 7) + 8 * (lane >> 4), lc = 32 * (quad & 1) + 8 * ((lane >> 3) & 1);
+#pragma unroll 1
+    for (int n = 0; n < (quad < 2 * VB ? 2 * nb : 0); ++n) {
+      const int i = n >> 1, half = n & 1, st = i % ST, nv = rows_of(block_of(i));
+      const uint32_t sv = s0 + st * L::kStage + L::kV + (uint32_t)(quad >> 1) * kBox;
+      if (half == 0) {
+        mbar_wait(&bar.full[st], parity(i / ST), wait);
+        if (nv < kC) {  // K's rows past the end become zeros too
+          const uint32_t sk = s0 + st * L::kStage + L::kK;
+          for (int e = quad * 32 + lane; e < (kC - nv) * 8 * KB; e += 64 * VB) {
+            const int x = e % (8 * KB), r = nv + e / (8 * KB);
+            pipe::sts_u4(sk + (uint32_t)(x >> 3) * kBox + sw128_offset(r, 8 * (x & 7)), make_uint4(0, 0, 0, 0));
+          }
+          fence_async_smem();
+        }
+      }
+      if (i > 0) {
+        mbar_wait(&bar.v_free[half], parity(i - 1), wait);
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int sub = 0; sub < 2; ++sub) {
+        const int j0 = 32 * half + 16 * sub;
+        uint64_t w[2];  // weights of tokens j0 + 8 x + 2 (lane % 4) and the next; whether they exist
+        uint32_t live[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int j = j0 + 8 * x + 2 * (lane & 3);
+          const int n0 = REV ? j + 1 : nv - 1 - j, n1 = REV ? j + 2 : nv - 2 - j;
+          w[x] = pk2(tab_st[min(max(n0, 0), kC)], tab_st[min(max(n1, 0), kC)]);
+          live[x] = (j < nv ? 0xffffu : 0u) | (j + 1 < nv ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t f[4], t0[4], t1[4], t2[4];
+          ldmatrix4_trans(sv + sw128_offset(j0 + lr, lc + 16 * q), f[0], f[1], f[2], f[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] &= live[e >> 1];
+            split3(mul2(w[e >> 1], pk2(lo_f(f[e]), hi_f(f[e]))), t0[e], t1[e], t2[e]);
+          }
+          const uint32_t lanes = (uint32_t)(16 * q) << 16, col = kTmT + half * kHalf + 8 * sub;
+          if (!SUMMARY) tmem_st_16x128_async(pipe::tmem_quad(tmem + kTmV, j0 / 2) + lanes, f[0], f[1], f[2], f[3]);
+          tmem_st_16x128_async(pipe::tmem_quad(tmem + col, 0) + lanes, t0[0], t0[1], t0[2], t0[3]);
+          tmem_st_16x128_async(pipe::tmem_quad(tmem + col, kTerm) + lanes, t1[0], t1[1], t1[2], t1[3]);
+          tmem_st_16x128_async(pipe::tmem_quad(tmem + col, 2 * kTerm) + lanes, t2[0], t2[1], t2[2], t2[3]);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      pipe::warp_arrive(&bar.v_ready[half]);
     }
   }
 

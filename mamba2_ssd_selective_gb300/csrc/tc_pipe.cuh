@@ -143,6 +143,22 @@ __device__ __forceinline__ void umma_ts_k(uint32_t d, uint32_t a, uint64_t b, ui
   for (int kk = 1; kk < NK; ++kk) umma_bf16_ts(d, a + kk * sa, b + kk * sb, idesc, 1u);
 }
 
+// Both for a converged warp with one acting lane.
+template <int NK>
+__device__ __forceinline__ void umma_k_el(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint64_t sa, uint64_t sb,
+                                          uint32_t idesc, bool accumulate) {
+  umma_bf16_el(el, d, a, b, idesc, accumulate ? 1u : 0u);
+#pragma unroll
+  for (int kk = 1; kk < NK; ++kk) umma_bf16_el(el, d, a + kk * sa, b + kk * sb, idesc, 1u);
+}
+template <int NK>
+__device__ __forceinline__ void umma_ts_k_el(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint32_t sa, uint64_t sb,
+                                             uint32_t idesc, bool accumulate) {
+  umma_bf16_ts_el(el, d, a, b, idesc, accumulate ? 1u : 0u);
+#pragma unroll
+  for (int kk = 1; kk < NK; ++kk) umma_bf16_ts_el(el, d, a + kk * sa, b + kk * sb, idesc, 1u);
+}
+
 // TMEM address of (lane quadrant of this warp, column col)
 __device__ __forceinline__ uint32_t tmem_quad(uint32_t base, int col) {
   return base + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16) + (uint32_t)col;
