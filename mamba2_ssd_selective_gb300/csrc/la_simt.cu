@@ -63,28 +63,20 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
         *pw = At + kC * kLdC;  // pw[0..kC]: lam^n
   LaUnit u;
   if (!la_find_unit(p, blockIdx.x, u)) return;  // every warp finds the same
+  if (SUMMARY && (u.nseg == 1 || la_is_last(u, REV))) return;  // nothing follows
   const int h = blockIdx.y, c0 = blockIdx.z * kTV, tid = threadIdx.x, ncol = min(kTV, p.dv - c0);
   const float g = __ldg(p.g + h);
   const T *q = static_cast<const T *>(p.q) + u.t0 * p.qs + (h / p.gq) * p.dk;
   const T *k = static_cast<const T *>(p.k) + u.t0 * p.ks + (h / p.gk) * p.dk;
   const T *v = static_cast<const T *>(p.v) + u.t0 * p.vs + (h / p.gv) * p.dv + c0;
-  const size_t dd = (size_t)p.dk * p.dv;
 
   if (tid <= kC) pw[tid] = la_pow(g, tid);
   const float2 carry_full = la_pow2(g, kC);
   // q and k rows past dk (up to the padded width) stay zero
   for (int e = p.dk * kLdC + tid; e < dkp * kLdC; e += kThreads) Qt[e] = Kt[e] = 0.f;
   {
-    const float *in = nullptr;
-    int sa = p.sa, sb = p.sb;
-    if (SUMMARY) {
-    } else if (p.split) {
-      in = p.seg_state + ((size_t)blockIdx.x * p.H + h) * dd;
-      sa = p.dv;
-      sb = 1;
-    } else if (p.init) {
-      in = p.init + ((size_t)u.seq * p.H + h) * dd;
-    }
+    int sa, sb;
+    const float *in = SUMMARY ? nullptr : la_state_in(p, u, blockIdx.x, h, sa, sb);
     for (int e = tid; e < dkp * kTV; e += kThreads) {
       const int a = e / kTV, b = e % kTV;
       S[a * kLdV + b] = in && a < p.dk && b < ncol ? in[(size_t)a * sa + (size_t)(c0 + b) * sb] : 0.f;
@@ -210,15 +202,8 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
     }
   }
   __syncthreads();
-  float *out = nullptr;
-  int sa = p.sa, sb = p.sb;
-  if (SUMMARY) {
-    out = p.seg_state + ((size_t)blockIdx.x * p.H + h) * dd;
-    sa = p.dv;
-    sb = 1;
-  } else if (!p.split && p.fin) {
-    out = p.fin + ((size_t)u.seq * p.H + h) * dd;
-  }
+  int sa, sb;
+  float *out = la_state_out(p, u, blockIdx.x, h, REV, SUMMARY, sa, sb);
   if (out)
     for (int e = tid; e < p.dk * kTV; e += kThreads) {
       const int a = e / kTV, b = e % kTV;
@@ -226,9 +211,9 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
     }
 }
 
-// The states between segments: per sequence and head, in processing order,
-//     next = lam^len S + W_seg,   W_seg (from a zero state) replaced by S,
-// and the last `next` is the final state.
+// The states between segments of a cut sequence: per head, in processing order,
+//     next = lam^len S + W_seg,   W_seg (from a zero state) replaced by S.
+// The last segment has no W_seg: the pass that starts from its S writes the final state.
 constexpr int kScanThreads = 256;
 template <bool REV>
 __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPass p) {
@@ -238,6 +223,7 @@ __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPass p) {
   int a, len;
   la_seq_bounds(p, s, a, len);
   const int n = la_segments(p, len);
+  if (n == 1) return;
   // the sequence's first unit: segments of the sequences before it
   if (threadIdx.x < 32) {
     int c = 0;
@@ -270,17 +256,16 @@ __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPass p) {
     float w[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (i0 + i < n) w[i] = base[(REV ? n - 1 - i0 - i : i0 + i) * step];
+      if (i0 + i < n - 1) w[i] = base[(REV ? n - 1 - i0 - i : i0 + i) * step];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (i0 + i < n) {
         const int seg = REV ? n - 1 - i0 - i : i0 + i;
         const float2 c = seg == n - 1 ? tail : full;
         base[seg * step] = st;
-        st = fmaf(st, c.x, fmaf(st, c.y, w[i]));
+        if (i0 + i < n - 1) st = fmaf(st, c.x, fmaf(st, c.y, w[i]));
       }
   }
-  if (p.fin) p.fin[user] = st;
 }
 
 // out(row, kv, c) = sum of in(row, kv * group + i, c) over i, in order

@@ -23,8 +23,7 @@
 //   0, 1    P: scores out of TMEM (lane = row i of the block), decay and mask, P into shared memory
 //   2       TMA producer: Q, K, V blocks [64 x 64 columns each], a ring of stages
 //   3       TMEM owner and MMA issuer
-//   4-7     outputs: O^T and Oi^T out of TMEM as fragments, combined, transposed by stmatrix into
-//           the block's Q tile, stored by TMA
+//   4-7     outputs: O^T and Oi^T out of TMEM as fragments, combined, transposed by stmatrix, stored by TMA
 //   8-15    state: S = lam^nv S + W, and S^T into TMEM as the next block's operand
 //   16-19   V^T and the three terms of V^T diag(lam^b) into TMEM
 // The tensor core's order is scores of block i + 1, W's first half (32 tokens),
@@ -59,22 +58,30 @@ constexpr uint32_t kTerm = 16, kHalf = 3 * kTerm;  // a term of half a block (32
 template <int KB, int VB, bool SUMMARY>
 struct Layout {
   static constexpr int kStages = KB + VB == 2 ? 6 : 4;
-  // a stage: Q, later the block's outputs; K; V
-  static constexpr int kQBoxes = SUMMARY ? 0 : KB > VB ? KB : VB;
-  static constexpr uint32_t kQ = 0, kK = kQBoxes * kBox, kV = kK + KB * kBox, kStage = kV + VB * kBox;
-  static constexpr uint32_t kLoad = ((SUMMARY ? 1 : 2) * KB + VB) * kBox;  // bytes loaded into a stage
-  static constexpr uint32_t kP = kStages * kStage;                 // two P buffers
-  static constexpr uint32_t kTab = kP + (SUMMARY ? 0 : 2 * kBox);  // lam^n times each scale, n = 0..64
-  static constexpr uint32_t kBar = kTab + 3 * 272 + 16;
+  static constexpr uint32_t kQ = 0, kK = SUMMARY ? 0 : KB * kBox, kV = kK + KB * kBox, kStage = kV + VB * kBox;
+  static constexpr uint32_t kP = kStages * kStage;                  // two P buffers
+  static constexpr uint32_t kO = kP + (SUMMARY ? 0 : 2 * kBox);     // a block's outputs, on their way to TMA
+  static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : VB * kBox);  // weights, see Tables
+  static constexpr uint32_t kBar = kTab + 4 * 6 * kC;
   static constexpr int kNumBars = 2 * kStages + 2 + 4 + 1 + 1 + 4 + 1 + 2 + 1;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
+// Weights of a block's rows: of a full block, then of the sequence's last one, which
+// has fewer live rows (the others weigh nothing).
+struct Tables {
+  float st[2][kC];  // state scale lam^b(r)
+  float in[2][kC];  // incoming scale lam^a(r)
+  float below[kC];  // zeros, for the masked distances
+  float p[kC];      // product scale lam^n
+};
+static_assert(sizeof(Tables) <= 4 * 6 * kC, "table space");
+
 template <int ST>
 struct Bars {
-  uint64_t *full, *free;        // [ST] stage loaded / its operands and outputs read
+  uint64_t *full, *free;        // [ST] stage loaded / its operands read
   uint64_t *qk_full, *qk_free;  // scores
   uint64_t *p_ready, *p_free;   // [2]
   uint64_t *s_ready;            // S^T of the block in TMEM
@@ -144,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   LaUnit u;
   const int unit = blockIdx.x / p.H, h = blockIdx.x - unit * p.H;
   if (!la_find_unit(p, unit, u)) return;  // every warp finds the same
+  if (SUMMARY && (u.nseg == 1 || la_is_last(u, REV))) return;  // nothing follows
   uint8_t *sm = tc::aligned_smem(smem_raw);
   const WaitCtl wait{p.status, p.wait_ns};
   const Bars<ST> bar(reinterpret_cast<uint64_t *>(sm + L::kBar));
@@ -151,20 +159,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const int nb = (u.len + kC - 1) / kC;
   const float g = __ldg(p.g + h);
-  // tables: lam^n, n = 0..64, times the scale of the products, the incoming state, the outgoing state
-  float *tab_p = reinterpret_cast<float *>(sm + L::kTab), *tab_in = tab_p + 68, *tab_st = tab_in + 68;
+  Tables &tab = *reinterpret_cast<Tables *>(sm + L::kTab);
 
   if (threadIdx.x == 64) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.free[i], SUMMARY ? 1 : 2);
+      mbar_init(&bar.free[i], 1);
     }
     mbar_init(bar.qk_full, 1);
     mbar_init(bar.qk_free, 2);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.v_free[i], 1);
       mbar_init(&bar.p_ready[i], 2);
       mbar_init(&bar.p_free[i], 1);
-      mbar_init(&bar.v_free[i], 1);
       mbar_init(&bar.v_ready[i], 2 * VB);
     }
     mbar_init(bar.s_ready, 4 * VB);
@@ -179,11 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tslot, kTmCols);
     tmem_relinquish();
   }
-  if (threadIdx.x <= kC) {
-    const float w = la_pow(g, threadIdx.x);
-    tab_p[threadIdx.x] = p.p_scale * w;
-    tab_in[threadIdx.x] = p.in_scale * w;
-    tab_st[threadIdx.x] = p.st_scale * w;
+  if (threadIdx.x < 2 * kC) {
+    const int r = threadIdx.x & (kC - 1), last = threadIdx.x / kC, nv = last ? u.len - (nb - 1) * kC : kC;
+    const bool live = r < nv;
+    tab.st[last][r] = live ? p.st_scale * la_pow(g, REV ? r + 1 : nv - 1 - r) : 0.f;
+    tab.in[last][r] = live ? p.in_scale * la_pow(g, REV ? nv - 1 - r : r + 1) : 0.f;
+    (last ? tab.below : tab.p)[r] = last ? 0.f : p.p_scale * la_pow(g, r);
   }
   tc_fence_before();
   __syncthreads();
@@ -194,9 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto rows_of = [&](int blk) { return min(kC, u.len - blk * kC); };
 
   // The block is launched with 640 x 96 registers; the state warps, which hold 64 values of the state a
-  // thread, take what the others do not need: 128 x (72 + 88 + 2 * 112 + 88) = 60416 <= 61440.
+  // thread, take what the others do not need: 128 x (64 + 104 + 2 * 112 + 88) = 61440.
   if (warp < kOutWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 2) {
       // ------------------------------------------------------------ producer
       if (lane == 0 && nb > 0) {
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = i % ST, row = u.t0 + block_of(i) * kC;
           if (i >= ST && !mbar_wait(&bar.free[st], parity(i / ST - 1), wait)) break;
           uint8_t *base = sm + st * L::kStage;
-          mbar_expect_tx(&bar.full[st], L::kLoad);
+          mbar_expect_tx(&bar.full[st], L::kStage);
           for (int b = 0; b < KB; ++b) {
             if (!SUMMARY) tma_load_3d(base + L::kQ + b * kBox, &tm_q, &bar.full[st], 64 * b, h / p.gq, row);
             tma_load_3d(base + L::kK + b * kBox, &tm_k, &bar.full[st], 64 * b, h / p.gk, row);
@@ -252,7 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (!SUMMARY && nb > 0) scores(0);
         for (int i = 0; i < nb; ++i) {
-          const int ob = i & 1;
           if (SUMMARY)
             mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
           else if (i + 1 < nb)
@@ -268,11 +275,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               pipe::umma_ts_k_el<4>(el, tmem + kTmOi, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8, pipe::kStepK, iQK,
                                  b > 0);
             mbar_wait(&bar.v_ready[1], parity(i), wait);
-            mbar_wait(&bar.p_ready[ob], parity(i / 2), wait);
+            mbar_wait(&bar.p_ready[i & 1], parity(i / 2), wait);
             tc_fence_after();
-            pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmV, dP + ob * (kBox / 16), 8, pipe::kStepK, iQK, false);
+            pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmV, dP + (i & 1) * (kBox / 16), 8, pipe::kStepK, iQK, false);
             umma_commit_el(el, bar.o_full);
-            umma_commit_el(el, &bar.p_free[ob]);
+            umma_commit_el(el, &bar.p_free[i & 1]);
           }
           umma_commit_el(el, &bar.v_free[0]);
           half_w(i, 1);
@@ -299,40 +306,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ P
       if (!SUMMARY) {
         const int r = threadIdx.x;  // row of the block
+        // Masks of this row's bf16 pairs in the two 16-column groups that the diagonal
+        // crosses (columns 32 warp and 32 warp + 16): masked scores may be NaN, so they
+        // are cut off as bits.
+        uint32_t keep[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          keep[x] = ((REV ? 2 * x >= lane : 2 * x <= lane) ? 0xffffu : 0u) |
+                    ((REV ? 2 * x + 1 >= lane : 2 * x + 1 <= lane) ? 0xffff0000u : 0u);
         for (int i = 0; i < nb; ++i) {
           const int nv = rows_of(block_of(i));
           if (i >= 2) mbar_wait(&bar.p_free[i & 1], parity(i / 2 - 1), wait);
           mbar_wait(bar.qk_full, parity(i), wait);
           tc_fence_after();
           const uint32_t dst = smem_u32(sm + L::kP + (i & 1) * kBox);
-          // columns past the end: in order, only rows past it see them
-          const int jmax = REV ? nv : kC;
 #pragma unroll 1
           for (int j0 = 0; j0 < kC; j0 += 16) {
-            // 32 rows against 16 columns: all masked, all live, or in between
-            const int lo = REV ? j0 - (32 * warp + 31) : 32 * warp - (j0 + 15), hi = lo + 46;  // least and largest distance
+            const int at = j0 - 32 * warp;  // the group's place against the diagonal: 0 and 16 cross it
             uint4 p0 = make_uint4(0, 0, 0, 0), p1 = p0;
-            if (hi >= 0) {
+            if (REV ? at >= 0 : at < 32) {
               float s[16], v[8];
               tmem_ld16(pipe::tmem_quad(tmem + kTmQK, j0), s);
-              const float *w = tab_p + (REV ? j0 - r : r - j0);
-              if (lo >= 0 && j0 + 16 <= jmax) {
+              const float *w = tab.p + (REV ? j0 - r : r - j0);  // masked weights: zeros
+              if (REV && nv < kC) {  // columns past the end are masked for the rows before it too
 #pragma unroll
-                for (int e = 0; e < 16; ++e) s[e] *= w[REV ? e : -e];
-              } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int d = REV ? j0 + e - r : r - j0 - e;
-                  // a select, not a factor of zero: masked scores may be NaN
-                  s[e] = d >= 0 && j0 + e < jmax ? s[e] * w[REV ? e : -e] : 0.f;
-                }
+                for (int e = 0; e < 16; ++e) s[e] = j0 + e < nv ? s[e] : 0.f;
               }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) s[e] *= w[REV ? e : -e];
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = s[e];
               p0 = tc::pack8(v);
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = s[8 + e];
               p1 = tc::pack8(v);
+              if (at == 0) {
+                p0.x &= keep[0]; p0.y &= keep[1]; p0.z &= keep[2]; p0.w &= keep[3];
+                p1.x &= keep[4]; p1.y &= keep[5]; p1.z &= keep[6]; p1.w &= keep[7];
+              } else if (at == 16) {
+                p0.x &= keep[8]; p0.y &= keep[9]; p0.z &= keep[10]; p0.w &= keep[11];
+                p1.x &= keep[12]; p1.y &= keep[13]; p1.z &= keep[14]; p1.w &= keep[15];
+              }
             }
             pipe::sts_u4(dst + sw128_offset(r, j0), p0);
             pipe::sts_u4(dst + sw128_offset(r, j0 + 8), p1);
@@ -346,59 +360,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kStateWarp0) {
     // ------------------------------------------------------------ outputs
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     if (!SUMMARY && warp < kOutWarp0 + 2 * VB) {
       constexpr int kOutThreads = 64 * VB;
       const int tt = threadIdx.x - 32 * kOutWarp0, quad = warp & 3;
       // the address this lane gives to a group of four fragments: row i, columns of v
       const int fi = 8 * (lane >> 4) + (lane & 7), fc = 32 * quad + 8 * ((lane >> 3) & 1);
+      float w[16];  // what the incoming state's part of this lane's columns i weighs
       for (int i = 0; i < nb; ++i) {
-        const int st = i % ST, blk = block_of(i), nv = rows_of(blk);
+        const int blk = block_of(i), nv = rows_of(blk);
         const long long row0 = u.t0 + (long long)blk * kC;
-        const uint32_t so = smem_u32(sm + st * L::kStage + L::kQ);
-        float w[16];  // what the incoming state's part of this lane's columns i weighs
+        const uint32_t so = smem_u32(sm + L::kO);
+        if (i == 0 || (REV && i == 1)) {  // in order the weights of a shorter block are those of a full one
+          const float *t = tab.in[REV && nv < kC] + 2 * (lane & 3);
 #pragma unroll
-        for (int m = 0; m < 8; ++m)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 8 * m + 2 * (lane & 3) + e;
-            w[2 * m + e] = tab_in[REV ? max(nv - 1 - r, 0) : r + 1];
+          for (int m = 0; m < 8; ++m) {
+            const float2 x = *reinterpret_cast<const float2 *>(t + 8 * m);
+            w[2 * m] = x.x;
+            w[2 * m + 1] = x.y;
           }
-        mbar_wait(bar.o_full, parity(i), wait);
-        tc_fence_after();
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {  // 16 lanes (columns of v) at a time
-          uint32_t a[32], b[32];
-          const uint32_t lanes = (uint32_t)(16 * half) << 16;
-          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmO, 0) + lanes, a);
-          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmOi, 0) + lanes, b);
-          tmem_wait_ld32(a);
-          tmem_wait_ld32(b);
-          if (half == 1) {
-            tc_fence_before();
-            pipe::warp_arrive(bar.o_free);
-          }
-          float o[32];
+        }
+        // pieces of 16 lanes (columns of v) x 32 columns i: one is loaded while the one before is combined
+        auto load = [&](int piece, uint32_t(&a)[16], uint32_t(&b)[16]) {
+          const uint32_t at = ((uint32_t)(16 * (piece >> 1)) << 16) + 32 * (piece & 1);
+          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmO, 0) + at, a);
+          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmOi, 0) + at, b);
+        };
+        auto combine = [&](int piece, const uint32_t(&a)[16], const uint32_t(&b)[16]) {
+          const int half = piece >> 1, m0 = 4 * (piece & 1);
+          float o[16];
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            o[x] = fmaf(w[2 * (x >> 2) + (x & 1)], __uint_as_float(b[x]), __uint_as_float(a[x]));
+          for (int x = 0; x < 16; ++x)
+            o[x] = fmaf(w[2 * (m0 + (x >> 2)) + (x & 1)], __uint_as_float(b[x]), __uint_as_float(a[x]));
           if (p.o_f32) {
             float *dst = static_cast<float *>(p.o) + row0 * p.os + (long long)h * p.dv;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int r = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1), c = 32 * quad + 16 * half + (lane >> 2) + 4 * (x & 2);
+            for (int x = 0; x < 16; ++x) {
+              const int r = 8 * (m0 + (x >> 2)) + 2 * (lane & 3) + (x & 1),
+                        c = 32 * quad + 16 * half + (lane >> 2) + 4 * (x & 2);
               if (r < nv && c < p.dv) dst[r * p.os + c] = o[x];
             }
           } else {
 #pragma unroll
-            for (int m = 0; m < 8; m += 2) {
-              const int r = 8 * m + fi, c = fc + 16 * half;
+            for (int m = 0; m < 4; m += 2) {
+              const int r = 8 * (m0 + m) + fi, c = fc + 16 * half;
               stmatrix4_trans(so + (uint32_t)(c >> 6) * kBox + sw128_offset(r, c & 63),
                               tc::pack_bf16x2(o[4 * m], o[4 * m + 1]), tc::pack_bf16x2(o[4 * m + 2], o[4 * m + 3]),
                               tc::pack_bf16x2(o[4 * m + 4], o[4 * m + 5]), tc::pack_bf16x2(o[4 * m + 6], o[4 * m + 7]));
             }
           }
+        };
+        if (!p.o_f32 && i > 0) {  // the block before has been read out of the staging tile
+          if (tt == 0) bulk_wait_read0();
+          asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
         }
+        mbar_wait(bar.o_full, parity(i), wait);
+        tc_fence_after();
+        uint32_t a0[16], b0[16], a1[16], b1[16];
+        load(0, a0, b0);
+        tmem_wait_ld(a0, b0);
+        load(1, a1, b1);
+        combine(0, a0, b0);
+        tmem_wait_ld(a1, b1);
+        load(2, a0, b0);
+        combine(1, a1, b1);
+        tmem_wait_ld(a0, b0);
+        load(3, a1, b1);
+        combine(2, a0, b0);
+        tmem_wait_ld(a1, b1);
+        tc_fence_before();
+        pipe::warp_arrive(bar.o_free);
+        combine(3, a1, b1);
         if (!p.o_f32) {
           fence_async_smem();
           asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
@@ -414,15 +446,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4 *>(out + r * p.os + c) = v;
               }
             }
-            asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
           } else if (tt == 0) {
             for (int b = 0; b < VB; ++b)
               if (64 * b < p.dv) tma_store_3d(&tm_o, so + b * kBox, 64 * b, h, (int)row0);
             bulk_commit();
-            bulk_wait_read0();
           }
         }
-        if (tt == 0) mbar_arrive(&bar.free[st]);
       }
       if (tt == 0) bulk_wait0();
     }
@@ -433,18 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
     const int quad = warp & 3, sub = (warp - kStateWarp0) >> 2;  // two warps share a quadrant of lanes
     const int c = 32 * quad + lane, a0 = sub * kCols;
-    const size_t dd = (size_t)p.dk * p.dv;
     uint64_t S[kCols / 2];  // pairs along dk
     {
-      const float *in = nullptr;
-      int sa = p.sa, sb = p.sb;
-      if (!SUMMARY && p.split) {
-        in = p.seg_state + ((size_t)unit * p.H + h) * dd;
-        sa = p.dv;
-        sb = 1;
-      } else if (!SUMMARY && p.init) {
-        in = p.init + ((size_t)u.seq * p.H + h) * dd;
-      }
+      int sa, sb;
+      const float *in = SUMMARY ? nullptr : la_state_in(p, u, unit, h, sa, sb);
       const bool live = in && c < p.dv;
 #pragma unroll
       for (int a = 0; a < kCols; a += 2) {  // dk is even
@@ -503,15 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       publish();
     }
     if (nb > 0) update(nb - 1);
-    float *out = nullptr;
-    int sa = p.sa, sb = p.sb;
-    if (SUMMARY) {
-      out = p.seg_state + ((size_t)unit * p.H + h) * dd;
-      sa = p.dv;
-      sb = 1;
-    } else if (!p.split && p.fin) {
-      out = p.fin + ((size_t)u.seq * p.H + h) * dd;
-    }
+    int sa, sb;
+    float *out = la_state_out(p, u, unit, h, REV, SUMMARY, sa, sb);
     if (out && c < p.dv) {
 #pragma unroll
       for (int a = 0; a < kCols; a += 2) {
@@ -551,33 +565,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&bar.v_free[half], parity(i - 1), wait);
         tc_fence_after();
       }
+      // weights of tokens 8 x + 2 (lane % 4) and the next of this half
+      const float *tw = tab.st[nv < kC] + 32 * half + 2 * (lane & 3);
+      uint64_t w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) w[x] = *reinterpret_cast<const uint64_t *>(tw + 8 * x);
 #pragma unroll 1
-      for (int sub = 0; sub < 2; ++sub) {
-        const int j0 = 32 * half + 16 * sub;
-        uint64_t w[2];  // weights of tokens j0 + 8 x + 2 (lane % 4) and the next; whether they exist
-        uint32_t live[2];
+      for (int q = 0; q < 2; ++q) {
+        uint32_t f[8], t0[8], t1[8], t2[8];
+        const uint32_t row = sv + (32 * half + lr) * 128 + (uint32_t)((((lc >> 3) + 2 * q) ^ (lane & 7)) * 16);
+        ldmatrix4_trans(row, f[0], f[1], f[2], f[3]);
+        ldmatrix4_trans(row + 16 * 128, f[4], f[5], f[6], f[7]);
+        if (nv < kC) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int j = j0 + 8 * x + 2 * (lane & 3);
-          const int n0 = REV ? j + 1 : nv - 1 - j, n1 = REV ? j + 2 : nv - 2 - j;
-          w[x] = pk2(tab_st[min(max(n0, 0), kC)], tab_st[min(max(n1, 0), kC)]);
-          live[x] = (j < nv ? 0xffffu : 0u) | (j + 1 < nv ? 0xffff0000u : 0u);
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t f[4], t0[4], t1[4], t2[4];
-          ldmatrix4_trans(sv + sw128_offset(j0 + lr, lc + 16 * q), f[0], f[1], f[2], f[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[e] &= live[e >> 1];
-            split3(mul2(w[e >> 1], pk2(lo_f(f[e]), hi_f(f[e]))), t0[e], t1[e], t2[e]);
+          for (int e = 0; e < 8; ++e) {
+            const int j = 32 * half + 8 * (e >> 1) + 2 * (lane & 3);
+            f[e] &= (j < nv ? 0xffffu : 0u) | (j + 1 < nv ? 0xffff0000u : 0u);
           }
-          const uint32_t lanes = (uint32_t)(16 * q) << 16, col = kTmT + half * kHalf + 8 * sub;
-          if (!SUMMARY) tmem_st_16x128_async(pipe::tmem_quad(tmem + kTmV, j0 / 2) + lanes, f[0], f[1], f[2], f[3]);
-          tmem_st_16x128_async(pipe::tmem_quad(tmem + col, 0) + lanes, t0[0], t0[1], t0[2], t0[3]);
-          tmem_st_16x128_async(pipe::tmem_quad(tmem + col, kTerm) + lanes, t1[0], t1[1], t1[2], t1[3]);
-          tmem_st_16x128_async(pipe::tmem_quad(tmem + col, 2 * kTerm) + lanes, t2[0], t2[1], t2[2], t2[3]);
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split3(mul2(w[e >> 1], pk2(lo_f(f[e]), hi_f(f[e]))), t0[e], t1[e], t2[e]);
+        const uint32_t at = pipe::tmem_quad(tmem + kTmT + half * kHalf, 0) + ((uint32_t)(16 * q) << 16);
+        if (!SUMMARY) tmem_st_16x128_async(at + (kTmV + 16 * half - kTmT - half * kHalf), f);
+        tmem_st_16x128_async(at, t0);
+        tmem_st_16x128_async(at + kTerm, t1);
+        tmem_st_16x128_async(at + 2 * kTerm, t2);
       }
       tmem_wait_st();
       tc_fence_before();

@@ -39,7 +39,7 @@ struct LaPass {
   const int *cu;
   int seg_len;  // tokens of a segment (a multiple of the blocks' tokens)
   int nunits;   // upper bound of the segments of all sequences
-  bool split;   // sequences are cut: seg_state[u, h] holds segment states
+  bool split;   // sequences longer than seg_len are cut: seg_state[u, h] holds their segments' states
   float *seg_state;
   bool o_f32;  // o is fp32 whatever the inputs' type
   int *status;
@@ -48,8 +48,7 @@ struct LaPass {
 
 // One segment of a sequence: tokens [t0, t0 + len) of the rows, seg-th of its sequence.
 struct LaUnit {
-  int seq, seg, t0, len;
-  bool last;  // the sequence's last segment
+  int seq, seg, nseg, t0, len;
 };
 
 __device__ __forceinline__ void la_seq_bounds(const LaPass &p, int s, int &a, int &len) {
@@ -107,8 +106,33 @@ __device__ __forceinline__ bool la_find_unit(const LaPass &p, int u, LaUnit &out
   out.seg = seg;
   out.t0 = a + seg * p.seg_len;
   out.len = min(p.seg_len, len - seg * p.seg_len);
-  out.last = seg + 1 >= la_segments(p, len);
+  out.nseg = la_segments(p, len);
   return true;
+}
+
+// The state before the unit's first token in processing order, or null (zero), and its strides: the segment's, or
+// the user's for a sequence that is not cut.
+__device__ __forceinline__ const float *la_state_in(const LaPass &p, const LaUnit &u, int unit, int h, int &sa, int &sb) {
+  const size_t dd = (size_t)p.dk * p.dv;
+  sa = p.sa;
+  sb = p.sb;
+  if (u.nseg == 1) return p.init ? p.init + ((size_t)u.seq * p.H + h) * dd : nullptr;
+  sa = p.dv;
+  sb = 1;
+  return p.seg_state + ((size_t)unit * p.H + h) * dd;
+}
+// whether the unit is its sequence's last in processing order
+__device__ __forceinline__ bool la_is_last(const LaUnit &u, bool reverse) {
+  return reverse ? u.seg == 0 : u.seg == u.nseg - 1;
+}
+// Where the unit's state goes, or null: the summary's segment state, the user's final state of a sequence.
+__device__ __forceinline__ float *la_state_out(const LaPass &p, const LaUnit &u, int unit, int h, bool reverse,
+                                               bool summary, int &sa, int &sb) {
+  const size_t dd = (size_t)p.dk * p.dv;
+  sa = summary ? p.dv : p.sa;
+  sb = summary ? 1 : p.sb;
+  if (summary) return p.seg_state + ((size_t)unit * p.H + h) * dd;
+  return p.fin && la_is_last(u, reverse) ? p.fin + ((size_t)u.seq * p.H + h) * dd : nullptr;
 }
 
 // lam^n in fp32; lam^0 is 1 even for a log decay of -inf
@@ -127,7 +151,7 @@ template <typename T> void launch_la_simt(const LaPass &p, bool reverse, bool su
 // la_tc.cu: bf16, both widths at most 128
 inline bool la_tc_envelope(int dk, int dv) { return dk <= 128 && dv <= 128; }
 void launch_la_tc(const LaPass &p, bool reverse, bool summary, cudaStream_t s);
-// segment states -> incoming segment states, in place, and the final states (either type's path)
+// segment states -> incoming segment states, in place (either path)
 void launch_la_scan(const LaPass &p, bool reverse, cudaStream_t s);
 // sums fp32 (rows, H, d) over groups of query heads into (rows, Hkv, d)
 template <typename T>
