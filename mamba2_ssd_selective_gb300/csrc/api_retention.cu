@@ -179,8 +179,8 @@ ssd_status la_backward_impl(const ssd_linear_attn_dims *d, const ssd_linear_attn
   LaPass p = base;  // dq
   la_roles(p, o, v, k, dv, dk);
   la_states(p, in->initial_states, nullptr, true);
-  p.p_scale = p.in_scale = in->scale;
-  p.st_scale = 1.f;
+  p.o_scale = in->scale;
+  p.p_scale = p.st_scale = 1.f;
   p.o = g->dq;
   p.os = g->dq_tok_stride;
   la_run<T>(p, false, s);
@@ -189,7 +189,7 @@ ssd_status la_backward_impl(const ssd_linear_attn_dims *d, const ssd_linear_attn
   la_roles(p, v, o, q, dv, dk);
   la_states(p, dfinal, nullptr, true);
   p.p_scale = p.st_scale = in->scale;
-  p.in_scale = 1.f;
+  p.o_scale = 1.f;
   p.o_f32 = group > 1;
   p.o = group > 1 ? part : g->dk;
   p.os = group > 1 ? (long long)H * dk : g->dk_tok_stride;
@@ -201,7 +201,7 @@ ssd_status la_backward_impl(const ssd_linear_attn_dims *d, const ssd_linear_attn
   la_roles(p, k, q, o, dk, dv);
   la_states(p, dfinal, g->dinitial_states, false);
   p.p_scale = p.st_scale = in->scale;
-  p.in_scale = 1.f;
+  p.o_scale = 1.f;
   p.o_f32 = group > 1;
   p.o = group > 1 ? part : g->dv;
   p.os = group > 1 ? (long long)H * dv : g->dv_tok_stride;
@@ -294,8 +294,8 @@ ssd_status ssd_linear_attn_forward(const ssd_linear_attn_dims *dims, const ssd_l
   la_roles(p, Role{in->q, in->q_tok_stride, 1, dims->nheads}, Role{in->k, in->k_tok_stride, group, dims->nheads_kv},
            Role{in->v, in->v_tok_stride, group, dims->nheads_kv}, dims->headdim_k, dims->headdim_v);
   la_states(p, in->initial_states, final_states, false);
-  p.p_scale = p.in_scale = in->scale;
-  p.st_scale = 1.f;
+  p.o_scale = in->scale;
+  p.p_scale = p.st_scale = 1.f;
   p.o = o;
   p.os = o_tok_stride;
   cudaMemsetAsync(p.status, 0, 64, s);
@@ -350,7 +350,7 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_line
   LaPass p = la_base(dims, in, LaPlan{}, nullptr);
   la_roles(p, Role{in->q, in->q_tok_stride, 1, dims->nheads}, Role{in->k, in->k_tok_stride, group, dims->nheads_kv},
            Role{in->v, in->v_tok_stride, group, dims->nheads_kv}, dims->headdim_k, dims->headdim_v);
-  p.p_scale = in->scale;
+  p.o_scale = in->scale;
   p.o = o;
   p.os = o_tok_stride;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
   LaUnit u;
   if (!la_find_unit(p, blockIdx.x, u)) return;  // every warp finds the same
   if (SUMMARY && (u.nseg == 1 || la_is_last(u, REV))) return;  // nothing follows
+  const float p_scale = p.o_scale * p.p_scale;
   const int h = blockIdx.y, c0 = blockIdx.z * kTV, tid = threadIdx.x, ncol = min(kTV, p.dv - c0);
   const float g = __ldg(p.g + h);
   const T *q = static_cast<const T *>(p.q) + u.t0 * p.qs + (h / p.gq) * p.dk;
@@ -116,8 +117,8 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
         for (int j = 0; j < 4; ++j) {
           float2 out;
           const int d0 = REV ? j0 + j - i0 : i0 - j0 - j, d1 = REV ? d0 - 1 : d0 + 1;
-          out.x = d0 >= 0 ? acc[0][j] * (pw[d0] * p.p_scale) : 0.f;
-          out.y = d1 >= 0 ? acc[1][j] * (pw[d1] * p.p_scale) : 0.f;
+          out.x = d0 >= 0 ? acc[0][j] * (pw[d0] * p_scale) : 0.f;
+          out.y = d1 >= 0 ? acc[1][j] * (pw[d1] * p_scale) : 0.f;
           *reinterpret_cast<float2 *>(At + (j0 + j) * kLdC + i0) = out;
         }
       }
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float w = p.in_scale * pw[REV ? max(nv - 1 - i0 - i, 0) : i0 + i + 1];
+        const float w = p.o_scale * pw[REV ? max(nv - 1 - i0 - i, 0) : i0 + i + 1];
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] *= w;
       }

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) la_step_kernel(LaPass p, float *__re
     float o = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) o += part[w][tid];
-    static_cast<T *>(p.o)[r * p.os + (long long)h * p.dv + blockIdx.z * kCols + tid] = from_f<T>(o * p.p_scale);
+    static_cast<T *>(p.o)[r * p.os + (long long)h * p.dv + blockIdx.z * kCols + tid] = from_f<T>(o * p.o_scale);
   }
 }
 

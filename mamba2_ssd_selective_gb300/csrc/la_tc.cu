@@ -4,8 +4,7 @@
 // One CTA takes one segment of one sequence and one query head, and walks it in
 // blocks of 64 tokens.  With P_ij = scale q_i . k_j lam^|i - j| inside the block
 // (j <= i; reverse: j >= i) and the incoming state S (dk x dv):
-//     O^T  = V^T P^T              Oi^T = S^T Q^T
-//     o_i  = O_i + lam^a(i) Oi_i
+//     o_i  = lam^a(i) (S^T q_i + V^T P'_i),    P'_ij = P_ij lam^-a(i)
 //     S^T  = lam^nv S^T + W^T,    W^T = (V^T diag(lam^b)) K
 // Everything is formed transposed, so that dv (up to 128) fills the accumulators'
 // lanes, the state stays in its warps' registers (lane = dv) from block to
@@ -23,13 +22,17 @@
 //   0, 1    P: scores out of TMEM (lane = row i of the block), decay and mask, P into shared memory
 //   2       TMA producer: Q, K, V blocks [64 x 64 columns each], a ring of stages
 //   3       TMEM owner and MMA issuer
-//   4-7     outputs: O^T and Oi^T out of TMEM as fragments, combined, transposed by stmatrix, stored by TMA
+//   4-7     outputs: O^T out of TMEM as fragments, weighed, transposed by stmatrix, stored by TMA
 //   8-15    state: S = lam^nv S + W, and S^T into TMEM as the next block's operand
 //   16-19   V^T and the three terms of V^T diag(lam^b) into TMEM
 // The tensor core's order is scores of block i + 1, W's first half (32 tokens),
-// Oi, O, W's second half: the halves' operands alternate between two buffers, so
+// the outputs, W's second half: the halves' operands alternate between two buffers, so
 // that one is prepared while the other is in use, and W's read (not the whole
 // state update) is what the next block's first half waits for.
+// P' weighs a score with a power that depends on its column alone, lam^-(j + 1) (reverse:
+// lam^-(nv - 1 - j)), so that both products meet in one accumulator, which takes
+// turns between two.  It is up to lam^-64: heads whose lam^64 is below 2^-40 form
+// P and O beside Oi instead, and add lam^a Oi at the end.
 // The last block of a sequence is masked: rows past its end belong to another
 // sequence, so V's are replaced by zeros on their way to TMEM and K's in shared
 // memory (0 * NaN would be NaN), scores with them are selected away, and nothing
@@ -51,7 +54,7 @@ constexpr int kThreads = 640;
 constexpr int kOutWarp0 = 4, kStateWarp0 = 8, kWeighWarp0 = 16;
 constexpr uint32_t kBox = 8192;  // [64 tokens x 64 columns] bf16
 
-// TMEM columns: scores, O, Oi, W, S^T (bf16), two buffers of the three terms of half a block, V^T
+// TMEM columns: scores, two accumulators of outputs (or O and Oi), W, S^T (bf16), two buffers of the three terms of half a block, V^T
 constexpr uint32_t kTmQK = 0, kTmO = 64, kTmOi = 128, kTmW = 192, kTmS = 320, kTmT = 384, kTmV = 480, kTmCols = 512;
 constexpr uint32_t kTerm = 16, kHalf = 3 * kTerm;  // a term of half a block (32 tokens as bf16 pairs)
 
@@ -62,8 +65,8 @@ struct Layout {
   static constexpr uint32_t kP = kStages * kStage;                  // two P buffers
   static constexpr uint32_t kO = kP + (SUMMARY ? 0 : 2 * kBox);     // a block's outputs, on their way to TMA
   static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : VB * kBox);  // weights, see Tables
-  static constexpr uint32_t kBar = kTab + 4 * 6 * kC;
-  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 1 + 1 + 4 + 1 + 2 + 1;
+  static constexpr uint32_t kBar = kTab + 4 * 7 * kC;
+  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 1 + 1 + 4 + 1 + 4 + 1;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
@@ -73,11 +76,11 @@ struct Layout {
 // has fewer live rows (the others weigh nothing).
 struct Tables {
   float st[2][kC];  // state scale lam^b(r)
-  float in[2][kC];  // incoming scale lam^a(r)
-  float below[kC];  // zeros, for the masked distances
-  float p[kC];      // product scale lam^n
+  float out[2][kC]; // output scale lam^a(r)
+  float p[kC];      // output and product scale lam^n
+  float col[2][kC]; // product scale lam^-(what out gives the row of the same number)
 };
-static_assert(sizeof(Tables) <= 4 * 6 * kC, "table space");
+static_assert(sizeof(Tables) <= 4 * 7 * kC, "table space");
 
 template <int ST>
 struct Bars {
@@ -88,7 +91,7 @@ struct Bars {
   uint64_t *w_free;             // the previous block's W read out of TMEM
   uint64_t *v_ready, *v_free;   // [2] half a block's V^T and terms in TMEM / read by its MMAs
   uint64_t *w_full;             // W formed (and S^T read)
-  uint64_t *o_full, *o_free;
+  uint64_t *o_full, *o_free;    // [2]
   uint64_t *drain;
   __device__ explicit Bars(uint64_t *b) {
     full = b;
@@ -103,8 +106,8 @@ struct Bars {
     v_free = v_ready + 2;
     w_full = v_free + 2;
     o_full = w_full + 1;
-    o_free = o_full + 1;
-    drain = o_free + 1;
+    o_free = o_full + 2;
+    drain = o_free + 2;
   }
 };
 
@@ -161,6 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float g = __ldg(p.g + h);
   Tables &tab = *reinterpret_cast<Tables *>(sm + L::kTab);
 
+  // whether lam^-64 is out of reach: products and incoming state in accumulators of their own
+  const bool apart = !(g * kC > -40.f * 0.6931f);
   if (threadIdx.x == 64) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bar.full[i], 1);
@@ -172,13 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.v_free[i], 1);
       mbar_init(&bar.p_ready[i], 2);
       mbar_init(&bar.p_free[i], 1);
+      mbar_init(&bar.o_full[i], 1);
+      mbar_init(&bar.o_free[i], 2 * VB);
       mbar_init(&bar.v_ready[i], 2 * VB);
     }
     mbar_init(bar.s_ready, 4 * VB);
     mbar_init(bar.w_free, 4 * VB);
     mbar_init(bar.w_full, 1);
-    mbar_init(bar.o_full, 1);
-    mbar_init(bar.o_free, 2 * VB);
     mbar_init(bar.drain, 1);
     fence_mbar_init();
   }
@@ -190,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & (kC - 1), last = threadIdx.x / kC, nv = last ? u.len - (nb - 1) * kC : kC;
     const bool live = r < nv;
     tab.st[last][r] = live ? p.st_scale * la_pow(g, REV ? r + 1 : nv - 1 - r) : 0.f;
-    tab.in[last][r] = live ? p.in_scale * la_pow(g, REV ? nv - 1 - r : r + 1) : 0.f;
-    (last ? tab.below : tab.p)[r] = last ? 0.f : p.p_scale * la_pow(g, r);
+    tab.out[last][r] = live ? p.o_scale * la_pow(g, REV ? nv - 1 - r : r + 1) : 0.f;
+    tab.col[last][r] = live ? p.p_scale * la_pow(g, REV ? r + 1 - nv : -1 - r) : 0.f;
+    if (!last) tab.p[r] = p.o_scale * p.p_scale * la_pow(g, r);
   }
   tc_fence_before();
   __syncthreads();
@@ -268,17 +274,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           half_w(i, 0);
           if (!SUMMARY) {
             mbar_wait(bar.s_ready, parity(i), wait);
-            if (i > 0) mbar_wait(bar.o_free, parity(i - 1), wait);
+            // the accumulator of the incoming state's part and, unless apart, of the products
+            const uint32_t acc = tmem + (apart || (i & 1) ? kTmOi : kTmO);
+            if (apart ? i > 0 : i > 1) {
+              const int m = apart ? i - 1 : i - 2;
+              mbar_wait(&bar.o_free[m & 1], parity(m / 2), wait);
+            }
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < KB; ++b)
-              pipe::umma_ts_k_el<4>(el, tmem + kTmOi, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8, pipe::kStepK, iQK,
-                                 b > 0);
+              pipe::umma_ts_k_el<4>(el, acc, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8, pipe::kStepK, iQK,
+                                    b > 0);
             mbar_wait(&bar.v_ready[1], parity(i), wait);
             mbar_wait(&bar.p_ready[i & 1], parity(i / 2), wait);
             tc_fence_after();
-            pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmV, dP + (i & 1) * (kBox / 16), 8, pipe::kStepK, iQK, false);
-            umma_commit_el(el, bar.o_full);
+            pipe::umma_ts_k_el<4>(el, apart ? tmem + kTmO : acc, tmem + kTmV, dP + (i & 1) * (kBox / 16), 8, pipe::kStepK,
+                                  iQK, !apart);
+            umma_commit_el(el, &bar.o_full[i & 1]);
             umma_commit_el(el, &bar.p_free[i & 1]);
           }
           umma_commit_el(el, &bar.v_free[0]);
@@ -298,8 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!SUMMARY && nb > 0) {
           mbar_wait_drain(bar.qk_full, parity(nb - 1));
-          mbar_wait_drain(bar.o_full, parity(nb - 1));
-          for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
+          for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) {
+            mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
+            mbar_wait_drain(&bar.o_full[m & 1], parity(m / 2));
+          }
         }
       }
     } else {
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = threadIdx.x;  // row of the block
         // Masks of this row's bf16 pairs in the two 16-column groups that the diagonal
         // crosses (columns 32 warp and 32 warp + 16): masked scores may be NaN, so they
-        // are cut off as bits.
+        // are cut off as bits, after weights that need not be right there.
         uint32_t keep[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x)
@@ -327,13 +341,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (REV ? at >= 0 : at < 32) {
               float s[16], v[8];
               tmem_ld16(pipe::tmem_quad(tmem + kTmQK, j0), s);
-              const float *w = tab.p + (REV ? j0 - r : r - j0);  // masked weights: zeros
               if (REV && nv < kC) {  // columns past the end are masked for the rows before it too
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[e] = j0 + e < nv ? s[e] : 0.f;
               }
+              if (apart) {
+                const float *w = tab.p + (REV ? j0 - r : r - j0);  // where masked, whatever lies there
 #pragma unroll
-              for (int e = 0; e < 16; ++e) s[e] *= w[REV ? e : -e];
+                for (int e = 0; e < 16; ++e) s[e] *= w[REV ? e : -e];
+              } else {
+                const float4 *w = reinterpret_cast<const float4 *>(tab.col[REV && nv < kC] + j0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float4 t = w[e];
+                  s[4 * e] *= t.x;
+                  s[4 * e + 1] *= t.y;
+                  s[4 * e + 2] *= t.z;
+                  s[4 * e + 3] *= t.w;
+                }
+              }
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = s[e];
               p0 = tc::pack8(v);
@@ -366,13 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tt = threadIdx.x - 32 * kOutWarp0, quad = warp & 3;
       // the address this lane gives to a group of four fragments: row i, columns of v
       const int fi = 8 * (lane >> 4) + (lane & 7), fc = 32 * quad + 8 * ((lane >> 3) & 1);
-      float w[16];  // what the incoming state's part of this lane's columns i weighs
+      float w[16];  // what this lane's columns i weigh
       for (int i = 0; i < nb; ++i) {
         const int blk = block_of(i), nv = rows_of(blk);
         const long long row0 = u.t0 + (long long)blk * kC;
         const uint32_t so = smem_u32(sm + L::kO);
         if (i == 0 || (REV && i == 1)) {  // in order the weights of a shorter block are those of a full one
-          const float *t = tab.in[REV && nv < kC] + 2 * (lane & 3);
+          const float *t = tab.out[REV && nv < kC] + 2 * (lane & 3);
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
             const float2 x = *reinterpret_cast<const float2 *>(t + 8 * m);
@@ -380,57 +406,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[2 * m + 1] = x.y;
           }
         }
-        // pieces of 16 lanes (columns of v) x 32 columns i: one is loaded while the one before is combined
-        auto load = [&](int piece, uint32_t(&a)[16], uint32_t(&b)[16]) {
-          const uint32_t at = ((uint32_t)(16 * (piece >> 1)) << 16) + 32 * (piece & 1);
-          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmO, 0) + at, a);
-          tmem_ld_16x256_async(pipe::tmem_quad(tmem + kTmOi, 0) + at, b);
-        };
-        auto combine = [&](int piece, const uint32_t(&a)[16], const uint32_t(&b)[16]) {
-          const int half = piece >> 1, m0 = 4 * (piece & 1);
-          float o[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x)
-            o[x] = fmaf(w[2 * (m0 + (x >> 2)) + (x & 1)], __uint_as_float(b[x]), __uint_as_float(a[x]));
-          if (p.o_f32) {
-            float *dst = static_cast<float *>(p.o) + row0 * p.os + (long long)h * p.dv;
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const int r = 8 * (m0 + (x >> 2)) + 2 * (lane & 3) + (x & 1),
-                        c = 32 * quad + 16 * half + (lane >> 2) + 4 * (x & 2);
-              if (r < nv && c < p.dv) dst[r * p.os + c] = o[x];
-            }
-          } else {
-#pragma unroll
-            for (int m = 0; m < 4; m += 2) {
-              const int r = 8 * (m0 + m) + fi, c = fc + 16 * half;
-              stmatrix4_trans(so + (uint32_t)(c >> 6) * kBox + sw128_offset(r, c & 63),
-                              tc::pack_bf16x2(o[4 * m], o[4 * m + 1]), tc::pack_bf16x2(o[4 * m + 2], o[4 * m + 3]),
-                              tc::pack_bf16x2(o[4 * m + 4], o[4 * m + 5]), tc::pack_bf16x2(o[4 * m + 6], o[4 * m + 7]));
-            }
-          }
-        };
         if (!p.o_f32 && i > 0) {  // the block before has been read out of the staging tile
           if (tt == 0) bulk_wait_read0();
           asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
         }
-        mbar_wait(bar.o_full, parity(i), wait);
+        auto emit = [&](int half, const uint32_t(&a)[32]) {  // 16 lanes (columns of v) x 64 rows i
+          if (p.o_f32) {
+            float *dst = static_cast<float *>(p.o) + row0 * p.os + (long long)h * p.dv;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const int r = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1), c = 32 * quad + 16 * half + (lane >> 2) + 4 * (x & 2);
+              if (r < nv && c < p.dv) dst[r * p.os + c] = __uint_as_float(a[x]);
+            }
+          } else {
+            const int c = fc + 16 * half;
+            // 8 rows on it is the same place in the swizzle
+            const uint32_t to = so + (uint32_t)(c >> 6) * kBox + sw128_offset(fi, c & 63);
+#pragma unroll
+            for (int m = 0; m < 8; m += 2) {
+              uint32_t f[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                f[x] = tc::pack_bf16x2(__uint_as_float(a[4 * m + 2 * x]), __uint_as_float(a[4 * m + 2 * x + 1]));
+              stmatrix4_trans(to + m * 1024, f[0], f[1], f[2], f[3]);
+            }
+          }
+        };
+        const uint32_t lo = pipe::tmem_quad(tmem, apart || (i & 1) ? kTmOi : kTmO), hi = lo + (16u << 16);
+        mbar_wait(&bar.o_full[i & 1], parity(i / 2), wait);
         tc_fence_after();
-        uint32_t a0[16], b0[16], a1[16], b1[16];
-        load(0, a0, b0);
-        tmem_wait_ld(a0, b0);
-        load(1, a1, b1);
-        combine(0, a0, b0);
-        tmem_wait_ld(a1, b1);
-        load(2, a0, b0);
-        combine(1, a1, b1);
-        tmem_wait_ld(a0, b0);
-        load(3, a1, b1);
-        combine(2, a0, b0);
-        tmem_wait_ld(a1, b1);
+        uint32_t a[32], b[32];
+        tmem_ld_16x256_async(lo, a);
+        tmem_ld_16x256_async(hi, b);
+        tmem_wait_ld32(a);
+        tmem_wait_ld32(b);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const float t = w[2 * (x >> 2) + (x & 1)];
+          a[x] = __float_as_uint(t * __uint_as_float(a[x]));
+          b[x] = __float_as_uint(t * __uint_as_float(b[x]));
+        }
+        if (apart) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t t[16];
+            tmem_ld_16x256_x4_async(pipe::tmem_quad(tmem, kTmO) + ((uint32_t)(16 * (q >> 1)) << 16) + 32 * (q & 1), t);
+            tmem_wait_ld16(t);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              uint32_t &y = q < 2 ? a[16 * (q & 1) + x] : b[16 * (q & 1) + x];
+              y = __float_as_uint(__uint_as_float(y) + __uint_as_float(t[x]));
+            }
+          }
+        }
         tc_fence_before();
-        pipe::warp_arrive(bar.o_free);
-        combine(3, a1, b1);
+        pipe::warp_arrive(&bar.o_free[i & 1]);
+        emit(0, a);
+        emit(1, b);
         if (!p.o_f32) {
           fence_async_smem();
           asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");

@@ -26,8 +26,8 @@ struct LaPass {
   int gq, gk, gv;            // query heads that share one head of the role's tensor
   int dk, dv;                // widths of the q/k roles and of the v/o roles
   int H, Hq, Hk, Hv;         // query heads; heads of each role's tensor
-  float p_scale;             // factor of the products inside a block
-  float in_scale;            // factor of the incoming state's part
+  float o_scale;             // factor of the output
+  float p_scale;             // factor of the products inside a block, on top of it
   float st_scale;            // factor of what is added to the state
   const float *g;            // (H) log decays
   // states, element (a, b) of a (dk x dv) state at a * sa + b * sb

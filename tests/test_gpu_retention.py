@@ -152,6 +152,14 @@ def test_strong_and_absent_decay(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decays_about_the_reach_of_inverse_powers(dtype):
+    """lam^64 about 2^-40, where the tensor-core path changes how it weighs scores, and on both sides of it."""
+    decay = torch.tensor([-0.2, -0.43, -0.4332, -0.4333, -0.44, -0.8])
+    Case([200, 64, 7], 6, 2, 64, 64, dtype, seed=31, decay=decay).check()
+    Case([129], 6, 6, 128, 128, dtype, seed=32, decay=decay).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_other_sequences_do_not_see_nan(dtype):
     lens = [33, 40, 70]
     c = Case(lens, 2, 2, 64, 64, dtype, seed=8)
