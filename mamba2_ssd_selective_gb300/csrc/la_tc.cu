@@ -8,8 +8,8 @@
 //     S^T  = lam^nv S^T + W^T,    W^T = (V^T diag(lam^b)) K
 // Everything is formed transposed, so that dv (up to 128) fills the accumulators'
 // lanes, the state stays in its warps' registers (lane = dv) from block to
-// block, and every product but the scores takes its A operand from TMEM: S^T
-// from the registers, V^T and its weighted copies from shared memory through
+// block, and the products with the state take their A operands from TMEM: S^T
+// from the registers, the weighted copies of V^T from shared memory through
 // transposing matrix loads.  That matters because shared memory is what bounds
 // the kernel before HBM does: with the weighted K kept there as a B operand
 // (three terms written and read back) a block of 64 tokens at widths of 128 moved
@@ -24,19 +24,18 @@
 //   3       TMEM owner and MMA issuer
 //   4-7     outputs: O^T out of TMEM as fragments, weighed, transposed by stmatrix, stored by TMA
 //   8-15    state: S = lam^nv S + W, and S^T into TMEM as the next block's operand
-//   16-19   V^T and the three terms of V^T diag(lam^b) into TMEM
-// The tensor core's order is scores of block i + 1, W's first half (32 tokens),
-// the outputs, W's second half: the halves' operands alternate between two buffers, so
-// that one is prepared while the other is in use, and W's read (not the whole
-// state update) is what the next block's first half waits for.
+//   16-19   the three terms of V^T diag(lam^b) into TMEM
+// The tensor core's order is scores of block i + 1, W of block i (by halves of 32 tokens,
+// whose operands alternate between two buffers), outputs of block i.  So the chain
+// from state to state is W's products and W's read, and the state's update and
+// its way into TMEM run beside the next block's scores and W.
 // P' weighs a score with a power that depends on its column alone, lam^-(j + 1) (reverse:
 // lam^-(nv - 1 - j)), so that both products meet in one accumulator, which takes
 // turns between two.  It is up to lam^-64: heads whose lam^64 is below 2^-40 form
 // P and O beside Oi instead, and add lam^a Oi at the end.
 // The last block of a sequence is masked: rows past its end belong to another
-// sequence, so V's are replaced by zeros on their way to TMEM and K's in shared
-// memory (0 * NaN would be NaN), scores with them are selected away, and nothing
-// is stored there.
+// sequence, so K's and V's are replaced by zeros in shared memory (0 * NaN would be
+// NaN), scores with them are cut off, and nothing is stored there.
 #include "retention.h"
 #include "tc_pipe.cuh"
 #include "tc_util.cuh"
@@ -54,8 +53,8 @@ constexpr int kThreads = 640;
 constexpr int kOutWarp0 = 4, kStateWarp0 = 8, kWeighWarp0 = 16;
 constexpr uint32_t kBox = 8192;  // [64 tokens x 64 columns] bf16
 
-// TMEM columns: scores, two accumulators of outputs (or O and Oi), W, S^T (bf16), two buffers of the three terms of half a block, V^T
-constexpr uint32_t kTmQK = 0, kTmO = 64, kTmOi = 128, kTmW = 192, kTmS = 320, kTmT = 384, kTmV = 480, kTmCols = 512;
+// TMEM columns: scores, two accumulators of outputs (or O and Oi), W, S^T (bf16), two buffers of the three terms of half a block
+constexpr uint32_t kTmQK = 0, kTmO = 64, kTmOi = 128, kTmW = 192, kTmS = 320, kTmT = 384, kTmCols = 512;
 constexpr uint32_t kTerm = 16, kHalf = 3 * kTerm;  // a term of half a block (32 tokens as bf16 pairs)
 
 template <int KB, int VB, bool SUMMARY>
@@ -66,7 +65,7 @@ struct Layout {
   static constexpr uint32_t kO = kP + (SUMMARY ? 0 : 2 * kBox);     // a block's outputs, on their way to TMA
   static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : VB * kBox);  // weights, see Tables
   static constexpr uint32_t kBar = kTab + 4 * 7 * kC;
-  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 1 + 1 + 4 + 1 + 4 + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2 + 1 + 4 + 1 + 4 + 1;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
@@ -87,10 +86,10 @@ struct Bars {
   uint64_t *full, *free;        // [ST] stage loaded / its operands read
   uint64_t *qk_full, *qk_free;  // scores
   uint64_t *p_ready, *p_free;   // [2]
-  uint64_t *s_ready;            // S^T of the block in TMEM
+  uint64_t *s_ready, *s_free;   // S^T of the block in TMEM / read by its product
   uint64_t *w_free;             // the previous block's W read out of TMEM
-  uint64_t *v_ready, *v_free;   // [2] half a block's V^T and terms in TMEM / read by its MMAs
-  uint64_t *w_full;             // W formed (and S^T read)
+  uint64_t *v_ready, *v_free;   // [2] half a block's terms in TMEM / read by its MMAs
+  uint64_t *w_full;             // W formed
   uint64_t *o_full, *o_free;    // [2]
   uint64_t *drain;
   __device__ explicit Bars(uint64_t *b) {
@@ -101,7 +100,8 @@ struct Bars {
     p_ready = qk_free + 1;
     p_free = p_ready + 2;
     s_ready = p_free + 2;
-    w_free = s_ready + 1;
+    s_free = s_ready + 1;
+    w_free = s_free + 1;
     v_ready = w_free + 1;
     v_free = v_ready + 2;
     w_full = v_free + 2;
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar.s_ready, 4 * VB);
     mbar_init(bar.w_free, 4 * VB);
+    mbar_init(bar.s_free, 1);
     mbar_init(bar.w_full, 1);
     mbar_init(bar.drain, 1);
     fence_mbar_init();
@@ -238,12 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       {  // the whole warp, so that descriptors stay in uniform registers; one lane acts
         const uint32_t el = elect_one();
         const uint32_t s0 = smem_u32(sm);
-        // K-major: Q (A and B), K, P; MN-major: K as the B operand of W.  A's 128 rows run
+        // K-major: Q (A and B), K, P; MN-major: K as the B operand of W, V (A).  A's 128 rows run
         // past Q's 64 into the shared memory behind it; those rows of the result (and
         // the lanes past 64 when VB = 1) are not read.
         const uint64_t dQ = desc_sw128(s0 + L::kQ, 16, 1024), dK = desc_sw128(s0 + L::kK, 16, 1024),
-                       dKn = desc_sw128(s0 + L::kK, kBox, 1024), dP = desc_sw128(s0 + L::kP, 16, 1024);
-        constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iW = idesc_bf16(128, 64 * KB, false, true);
+                       dKn = desc_sw128(s0 + L::kK, kBox, 1024), dV = desc_sw128(s0 + L::kV, kBox, 1024), dP = desc_sw128(s0 + L::kP, 16, 1024);
+        constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iPV = idesc_bf16(128, 64, true, false), iW = idesc_bf16(128, 64 * KB, false, true);
         auto stage = [&](int i) { return (uint64_t)((i % ST) * (L::kStage / 16)); };
         auto scores = [&](int i) {
           mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
@@ -272,6 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             scores(i + 1);
           if (i > 0) mbar_wait(bar.w_free, parity(i - 1), wait);
           half_w(i, 0);
+          umma_commit_el(el, &bar.v_free[0]);
+          half_w(i, 1);
+          umma_commit_el(el, bar.w_full);
+          umma_commit_el(el, &bar.v_free[1]);
           if (!SUMMARY) {
             mbar_wait(bar.s_ready, parity(i), wait);
             // the accumulator of the incoming state's part and, unless apart, of the products
@@ -285,18 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < KB; ++b)
               pipe::umma_ts_k_el<4>(el, acc, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8, pipe::kStepK, iQK,
                                     b > 0);
-            mbar_wait(&bar.v_ready[1], parity(i), wait);
+            umma_commit_el(el, bar.s_free);
             mbar_wait(&bar.p_ready[i & 1], parity(i / 2), wait);
             tc_fence_after();
-            pipe::umma_ts_k_el<4>(el, apart ? tmem + kTmO : acc, tmem + kTmV, dP + (i & 1) * (kBox / 16), 8, pipe::kStepK,
-                                  iQK, !apart);
+            pipe::umma_k_el<4>(el, apart ? tmem + kTmO : acc, dV + stage(i), dP + (i & 1) * (kBox / 16), pipe::kStepMN,
+                               pipe::kStepK, iPV, !apart);
             umma_commit_el(el, &bar.o_full[i & 1]);
             umma_commit_el(el, &bar.p_free[i & 1]);
           }
-          umma_commit_el(el, &bar.v_free[0]);
-          half_w(i, 1);
-          umma_commit_el(el, bar.w_full);
-          umma_commit_el(el, &bar.v_free[1]);
           umma_commit_el(el, &bar.free[i % ST]);
         }
         // every MMA and every arrival of a commit has landed before the CTA ends
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!SUMMARY && nb > 0) {
           mbar_wait_drain(bar.qk_full, parity(nb - 1));
+          mbar_wait_drain(bar.s_free, parity(nb - 1));
           for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) {
             mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
             mbar_wait_drain(&bar.o_full[m & 1], parity(m / 2));
@@ -532,7 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nv = rows_of(block_of(i));
       const float2 carry = nv == kC ? full : la_pow2(g, nv);
       const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
-      // W done: so are the MMAs issued before it, which read the second half's terms and S^T
       mbar_wait(bar.w_full, parity(i), wait);
       tc_fence_after();
 #pragma unroll
@@ -552,7 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 #pragma unroll 1
     for (int i = 0; i < nb; ++i) {
-      if (i > 0) update(i - 1);
+      if (i > 0) {
+        update(i - 1);
+        if (!SUMMARY) mbar_wait(bar.s_free, parity(i - 1), wait);
+      }
       publish();
     }
     if (nb > 0) update(nb - 1);
@@ -584,10 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t sv = s0 + st * L::kStage + L::kV + (uint32_t)(quad >> 1) * kBox;
       if (half == 0) {
         mbar_wait(&bar.full[st], parity(i / ST), wait);
-        if (nv < kC) {  // K's rows past the end become zeros too
-          const uint32_t sk = s0 + st * L::kStage + L::kK;
-          for (int e = quad * 32 + lane; e < (kC - nv) * 8 * KB; e += 64 * VB) {
-            const int x = e % (8 * KB), r = nv + e / (8 * KB);
+        if (nv < kC) {  // rows past the end of K and V, which are operands as they are, become zeros
+          const uint32_t sk = s0 + st * L::kStage + L::kK;  // V's boxes follow K's
+          for (int e = quad * 32 + lane; e < (kC - nv) * 8 * (KB + VB); e += 64 * VB) {
+            const int x = e % (8 * (KB + VB)), r = nv + e / (8 * (KB + VB));
             pipe::sts_u4(sk + (uint32_t)(x >> 3) * kBox + sw128_offset(r, 8 * (x & 7)), make_uint4(0, 0, 0, 0));
           }
           fence_async_smem();
@@ -618,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) split3(mul2(w[e >> 1], pk2(lo_f(f[e]), hi_f(f[e]))), t0[e], t1[e], t2[e]);
         const uint32_t at = pipe::tmem_quad(tmem + kTmT + half * kHalf, 0) + ((uint32_t)(16 * q) << 16);
-        if (!SUMMARY) tmem_st_16x128_async(at + (kTmV + 16 * half - kTmT - half * kHalf), f);
         tmem_st_16x128_async(at, t0);
         tmem_st_16x128_async(at + kTerm, t1);
         tmem_st_16x128_async(at + 2 * kTerm, t2);
