@@ -247,6 +247,9 @@ ssd_status gn_check_inputs(const ssd_group_norm_dims *d, const ssd_group_norm_in
   return SSD_OK;
 }
 
+// whether rows of the tensor allow accesses of 8 channels (16 bytes of bf16, twice 16 of fp32)
+bool gn_vector(const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
+
 GnProblem gn_problem(const ssd_group_norm_dims *d, const ssd_group_norm_inputs *in) {
   GnProblem p{};
   p.n = d->nsamples;
@@ -255,7 +258,6 @@ GnProblem gn_problem(const ssd_group_norm_dims *d, const ssd_group_norm_inputs *
   p.G = d->groups;
   p.cg = d->channels / d->groups;
   p.act = d->activation;
-  p.eb = elem_bytes(d->dtype);
   if (in) {
     p.x = in->x;
     p.xs = in->x_row_stride;
@@ -363,7 +365,7 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_line
 
 size_t ssd_group_norm_workspace_size(const ssd_group_norm_dims *dims, int backward) {
   if (gn_check_dims(dims) != SSD_OK) return 0;
-  return gn_plan(gn_problem(dims, nullptr), backward != 0).total;
+  return gn_workspace(gn_problem(dims, nullptr), backward != 0);
 }
 
 ssd_status ssd_group_norm_forward(const ssd_group_norm_dims *dims, const ssd_group_norm_inputs *in, void *y,
@@ -375,9 +377,11 @@ ssd_status ssd_group_norm_forward(const ssd_group_norm_dims *dims, const ssd_gro
   if (st != SSD_OK) return st;
   if (!aligned(mean, 4) || !aligned(rstd, 4)) return SSD_ERR_ALIGNMENT;
   GnProblem p = gn_problem(dims, in);
-  const GnPlan pl = gn_plan(p, false);
-  if (!workspace || ws_bytes < pl.total) return SSD_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < gn_workspace(p, false)) return SSD_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SSD_ERR_ALIGNMENT;
+  const bool gate = dims->activation == SSD_ACT_GATE;
+  const GnPlan pl = gn_plan(p, false, gn_vector(in->x, in->x_row_stride) && gn_vector(y, y_row_stride) &&
+                                          (!gate || gn_vector(in->z, in->z_row_stride)));
   p.y = y;
   p.ys = y_row_stride;
   p.mean = mean;
@@ -406,9 +410,13 @@ ssd_status ssd_group_norm_backward(const ssd_group_norm_dims *dims, const ssd_gr
   if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(grads->dweight, 4) || !aligned(grads->dbias, 4))
     return SSD_ERR_ALIGNMENT;
   GnProblem p = gn_problem(dims, in);
-  const GnPlan pl = gn_plan(p, true);
-  if (!workspace || ws_bytes < pl.total) return SSD_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < gn_workspace(p, true)) return SSD_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SSD_ERR_ALIGNMENT;
+  const bool gate = dims->activation == SSD_ACT_GATE;
+  const GnPlan pl =
+      gn_plan(p, true, gn_vector(in->x, in->x_row_stride) && gn_vector(dy, dy_row_stride) &&
+                           gn_vector(grads->dx, grads->dx_row_stride) &&
+                           (!gate || (gn_vector(in->z, in->z_row_stride) && gn_vector(grads->dz, grads->dz_row_stride))));
   p.dy = dy;
   p.dys = dy_row_stride;
   p.mean = const_cast<float *>(mean);  // read only on this path

@@ -1,0 +1,104 @@
+// Group norm with an activation: which kernels a call takes, its workspace, and
+// the sum of the parameters' partial gradients.
+#include "group_norm.cuh"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kSms = 152;
+
+// Partials of one channel, 8 threads a channel: thread q adds partials q, q + 8, ... in order, then
+// the 8 sums are added in order.
+constexpr int kSumLanes = 8, kSumCols = gn::kThreads / kSumLanes;
+__global__ void __launch_bounds__(gn::kThreads) param_sum_kernel(int C, int partials, const float *__restrict__ dwp,
+                                                                 const float *__restrict__ dbp, float *dw, float *db) {
+  __shared__ float acc[2][kSumLanes][kSumCols];
+  const int cl = threadIdx.x % kSumCols, q = threadIdx.x / kSumCols, c = blockIdx.x * kSumCols + cl;
+  float sw = 0.f, sb = 0.f;
+  if (c < C) {
+#pragma unroll 4
+    for (int t = q; t < partials; t += kSumLanes) {
+      sw += dwp[(size_t)t * C + c];
+      sb += dbp[(size_t)t * C + c];
+    }
+  }
+  acc[0][q][cl] = sw;
+  acc[1][q][cl] = sb;
+  __syncthreads();
+  if (q == 0 && c < C) {
+    sw = sb = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSumLanes; ++i) {
+      sw += acc[0][i][cl];
+      sb += acc[1][i][cl];
+    }
+    if (dw) dw[c] = sw;
+    if (db) db[c] = sb;
+  }
+}
+
+}  // namespace
+
+void launch_gn_param_sum(int C, int partials, const float *dwp, const float *dbp, float *dw, float *db,
+                         cudaStream_t s) {
+  param_sum_kernel<<<(C + kSumCols - 1) / kSumCols, gn::kThreads, 0, s>>>(C, partials, dwp, dbp, dw, db);
+}
+
+GnPlan gn_plan(const GnProblem &p, bool backward, bool vectors) {
+  GnPlan pl{};
+  pl.vec = vectors && p.cg % 8 == 0 ? 8 : 1;
+  const int ncol = p.cg / pl.vec, block_places = pl.vec == 8 ? 4 : 8;
+  // the narrowest team that holds a group; backward teams also need a thread to keep its column
+  if (pl.vec == 8 && p.m == 1 && ncol <= 32) {
+    pl.team = ncol <= 8 ? 8 : ncol <= 16 ? 16 : 32;
+    pl.places = 1;
+  } else if (p.m <= gn::rows_of_team(ncol, 32, 4) && (!backward || ncol <= 32)) {
+    pl.team = 32;
+    pl.places = 4;
+  } else {
+    pl.team = gn::kThreads;
+    pl.places = block_places;
+    const long long rows = gn::rows_of_team(ncol, pl.team, pl.places);
+    if (p.m > rows || (backward && ncol > pl.team)) {
+      pl.tile_rows = (int)rows;
+      const long long tiles = ncol <= pl.team ? (p.m + rows - 1) / rows
+                                              : ((long long)p.m * ncol + pl.places * pl.team - 1) / (pl.places * pl.team);
+      pl.tiles = (int)tiles;
+    }
+  }
+  pl.own_columns = ncol <= pl.team;
+  if (pl.tiles == 0) {
+    const int teams = gn::kThreads / pl.team;
+    pl.groups_per_block = teams < p.G ? teams : p.G;
+    // blocks that fill the GPU a few times over, but no fewer samples than a block's teams take at once
+    const long long gblocks = (p.G + pl.groups_per_block - 1) / pl.groups_per_block, shares = teams / pl.groups_per_block;
+    const long long want = (backward ? 8 : 32) * kSms;  // a backward block writes a partial dw and db row
+    long long per = (p.n * gblocks + want - 1) / want;
+    per = (per + shares - 1) / shares * shares;
+    while ((p.n + per - 1) / per > 65535) per *= 2;
+    pl.samples_per_block = (int)per;
+  }
+  if (backward)
+    pl.partials = !pl.own_columns ? (int)(((long long)p.n * p.m + gn::kParamRows - 1) / gn::kParamRows)
+                  : pl.tiles      ? p.n * pl.tiles
+                                  : (p.n + pl.samples_per_block - 1) / pl.samples_per_block;
+  size_t off = 256;  // never empty
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  pl.part = take((size_t)p.n * p.G * pl.tiles * 8);
+  pl.dwp = take((size_t)pl.partials * p.C * 4);
+  pl.dbp = take((size_t)pl.partials * p.C * 4);
+  pl.total = off;
+  return pl;
+}
+
+size_t gn_workspace(const GnProblem &p, bool backward) {
+  const size_t a = gn_plan(p, backward, true).total, b = gn_plan(p, backward, false).total;
+  return a > b ? a : b;
+}
+
+}  // namespace ssd

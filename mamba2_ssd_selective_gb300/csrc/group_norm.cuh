@@ -1,0 +1,648 @@
+// Group norm with an activation, channels last.  Per sample and group, over its
+// m rows and cg channels (M = m cg values):
+//     xhat = (x - mean) rstd,  u = xhat w + b,  y = u | u sigmoid(u) | u z sigmoid(z)
+// and backwards, with du the gradient of u:
+//     dx = rstd (du w - A / M - xhat B / M),  A = sum du w,  B = sum du w xhat
+//     dw = sum du xhat,  db = sum du,  dz = dy u silu'(z)
+// Memory traffic bounds all of it.  A thread owns W consecutive channels (16 bytes
+// of bf16) of every RP-th row of a group's slab, so that its channels, and its
+// part of dw and db, stay in registers.
+//
+// A group that fits the registers of its team of NT threads (a part of a warp, a
+// warp, or a block) is read once: its mean, then its squared deviations, are
+// summed from registers.  With one row to a sample, a team is the narrowest
+// part of a warp that spans the group.  A larger group is cut into tiles of
+// rows: a first kernel gives each tile's count, mean and squared deviations (or
+// its part of A and B, and dz), a second one joins them, in order, and reads the
+// tile again, from L2 where the tensor fits it.
+// dw and db are sums of per-block partials in a fixed order.
+#pragma once
+
+#include "group_norm.h"
+
+namespace ssd {
+namespace gn {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------- vectors of W channels
+template <int W>
+__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float (&v)[W]) {
+  if constexpr (W == 8) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    v[0] = __bfloat162float(*p);
+  }
+}
+template <int W>
+__device__ __forceinline__ void load_vec(const float *p, float (&v)[W]) {
+  if constexpr (W == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4 *>(p + i));
+      v[i] = a.x;
+      v[i + 1] = a.y;
+      v[i + 2] = a.z;
+      v[i + 3] = a.w;
+    }
+  } else {
+    v[0] = __ldg(p);
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&v)[W]) {
+  if constexpr (W == 8) {
+    uint4 u;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = u;
+  } else {
+    *p = __float2bfloat16_rn(v[0]);
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_vec(float *p, const float (&v)[W]) {
+  if constexpr (W == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+    p[0] = v[0];
+  }
+}
+// W parameters of consecutive channels (c a multiple of W), or a constant where there are none
+template <int W>
+__device__ __forceinline__ void load_param(const float *p, int c, float none, float (&v)[W]) {
+  if (W == 8 && p && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    load_vec<W>(p + c, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < W; ++e) v[e] = p ? __ldg(p + c + e) : none;
+}
+
+// ---------------------------------------------------------------- sums over a team of NT threads
+template <int NT>
+__device__ __forceinline__ float2 team_sum(float a, float b, float *scratch) {
+#pragma unroll
+  for (int o = (NT < 32 ? NT : 32) / 2; o >= 1; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if constexpr (NT > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+      scratch[threadIdx.x >> 5] = a;
+      scratch[8 + (threadIdx.x >> 5)] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      a += scratch[w];
+      b += scratch[8 + w];
+    }
+  }
+  return make_float2(a, b);
+}
+
+// ---------------------------------------------------------------- a thread's places in a slab
+// V places among a group's rows [r0, rows): column vectors of W channels.  With at most
+// NT columns a thread keeps one column and takes every (NT / columns)-th row; with
+// more the group is one sequence of vectors, taken from e0 on.
+template <int W, int NT, int V>
+struct Places {
+  int row[V], col[V];  // row < 0: no such place
+  __device__ __forceinline__ Places(int tid, int ncol, int r0, long long e0, int rows) {
+    if constexpr (V == 1) {  // one row of at most NT columns
+      row[0] = rows > 0 && tid < ncol ? 0 : -1;
+      col[0] = tid * W;
+    } else if (ncol <= NT) {
+      const int rp = NT / ncol, ph = tid / ncol;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int r = r0 + ph + k * rp;
+        row[k] = ph < rp && r < rows ? r : -1;
+        col[k] = (tid - ph * ncol) * W;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const long long e = e0 + tid + k * NT, r = e / ncol;
+        row[k] = r < rows ? (int)r : -1;
+        col[k] = (int)(e - r * ncol) * W;
+      }
+    }
+  }
+};
+// rows that fit a team's places (0: not one)
+inline long long rows_of_team(int ncol, int nt, int v) {
+  return ncol <= nt ? (long long)v * (nt / ncol) : (long long)v * nt / ncol;
+}
+// Tile t of a group: rows [t tile_rows, ...) or, where a row has more columns than a block has threads,
+// vectors [t V NT, ...); and its number of values.
+template <int W, int V>
+struct Tile {
+  int n, g, t;
+  Places<W, kThreads, V> at;
+  __device__ __forceinline__ Tile(const GnProblem &p, const GnPlan &pl)
+      : n(blockIdx.x / p.G / pl.tiles), g(blockIdx.x % p.G), t(blockIdx.x / p.G % pl.tiles),
+        at(threadIdx.x, p.cg / W, t * pl.tile_rows, (long long)t * (V * kThreads), limit(p, pl)) {}
+  // (in rows mode a thread's last places may lie in the next tile)
+  __device__ __forceinline__ int limit(const GnProblem &p, const GnPlan &pl) const {
+    return pl.own_columns ? min(p.m, (t + 1) * pl.tile_rows) : p.m;
+  }
+  static __device__ __forceinline__ float count(const GnProblem &p, const GnPlan &pl, int i) {
+    if (pl.own_columns) return (float)min(pl.tile_rows, p.m - i * pl.tile_rows) * p.cg;
+    const long long left = (long long)p.m * (p.cg / W) - (long long)i * (V * kThreads);
+    return (float)(left < V * kThreads ? left : V * kThreads) * W;
+  }
+};
+
+__device__ __forceinline__ float silu_grad(float a, float s) { return s * (1.f + a * (1.f - s)); }
+
+// u -> y
+template <bool GATE>
+__device__ __forceinline__ float activate(float u, float z, bool silu) {
+  if (GATE) return u * (z * sigmoid_fast(z));
+  return silu ? u * sigmoid_fast(u) : u;
+}
+// dy -> du, and dz with the gate
+template <bool GATE>
+__device__ __forceinline__ float activate_grad(float dy, float u, float z, bool silu, float &dz) {
+  if (GATE) {
+    const float s = sigmoid_fast(z);
+    dz = dy * u * silu_grad(z, s);
+    return dy * (z * s);
+  }
+  return silu ? dy * silu_grad(u, sigmoid_fast(u)) : dy;
+}
+
+// one group of one sample: pointers to its first row's first channel
+template <typename T>
+struct Slab {
+  const T *x, *z, *dy;
+  T *y, *dx, *dz;
+  __device__ __forceinline__ Slab(const GnProblem &p, int n, int g) {
+    const long long r = (long long)n * p.m;
+    const int c = g * p.cg;
+    x = static_cast<const T *>(p.x) + r * p.xs + c;
+    z = static_cast<const T *>(p.z) + r * p.zs + c;
+    dy = static_cast<const T *>(p.dy) + r * p.dys + c;
+    y = static_cast<T *>(p.y) + r * p.ys + c;
+    dx = static_cast<T *>(p.dx) + r * p.dxs + c;
+    dz = static_cast<T *>(p.dz) + r * p.dzs + c;
+  }
+};
+
+template <typename T, int W, bool GATE>
+__device__ __forceinline__ void write_y(const GnProblem &p, const Slab<T> &s, int row, int col, const float (&w)[W],
+                                        const float (&b)[W], const float (&x)[W], const float (&z)[W], float mean,
+                                        float rstd) {
+  float y[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e)
+    y[e] = activate<GATE>(fmaf((x[e] - mean) * rstd, w[e], b[e]), GATE ? z[e] : 0.f, p.act == SSD_ACT_SILU);
+  store_vec<W>(s.y + row * p.ys + col, y);
+}
+
+// ---------------------------------------------------------------- forward, groups that fit a team
+// Teams that each keep one group and walk over samples, U at a time; block (groups of the block, samples of
+// the block).
+template <typename T, int W, int NT, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads) team_forward_kernel(GnProblem p, GnPlan pl) {
+  constexpr int kTeams = kThreads / NT, U = V == 1 ? 2 : 1;
+  __shared__ float red[16];
+  const int team = threadIdx.x / NT, tid = threadIdx.x % NT, gpb = pl.groups_per_block, shares = kTeams / gpb;
+  const int share = team / gpb, g = blockIdx.x * gpb + team % gpb;
+  const bool has = g < p.G && share < shares;
+  const int n0 = blockIdx.y * pl.samples_per_block, n1 = min(p.n, n0 + pl.samples_per_block), c0 = (has ? g : 0) * p.cg;
+  const float inv = 1.f / ((float)p.m * p.cg);
+  const Places<W, NT, V> at(tid, p.cg / W, 0, 0, has ? p.m : 0);
+  float w[W], b[W];
+  if (pl.own_columns && has && at.row[0] >= 0) {
+    load_param<W>(p.w, c0 + at.col[0], 1.f, w);
+    load_param<W>(p.b, c0 + at.col[0], 0.f, b);
+  }
+  // every thread of a warp makes the same number of turns (the sums are warp or block wide)
+  for (int nn = n0; nn < n1; nn += U * shares) {
+    float x[U][V][W], z[U][V][W];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = nn + u * shares + share;
+      const Slab<T> s(p, has && n < n1 ? n : 0, has ? g : 0);
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (has && n < n1 && at.row[k] >= 0) {
+          load_vec<W>(s.x + at.row[k] * p.xs + at.col[k], x[u][k]);
+          if (GATE) load_vec<W>(s.z + at.row[k] * p.zs + at.col[k], z[u][k]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < W; ++e) x[u][k][e] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = nn + u * shares + share;
+      const bool live = has && n < n1;
+      const Slab<T> s(p, live ? n : 0, has ? g : 0);
+      float sum = 0.f, dev = 0.f;
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < W; ++e) sum += x[u][k][e];
+      const float mean = team_sum<NT>(sum, 0.f, red).x * inv;
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (live && at.row[k] >= 0)
+#pragma unroll
+          for (int e = 0; e < W; ++e) dev = fmaf(x[u][k][e] - mean, x[u][k][e] - mean, dev);
+      const float rstd = 1.f / sqrtf(team_sum<NT>(dev, 0.f, red).x * inv + p.eps);
+      if (live && tid == 0) {
+        if (p.mean) p.mean[n * p.G + g] = mean;
+        if (p.rstd) p.rstd[n * p.G + g] = rstd;
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (live && at.row[k] >= 0) {
+          if (!pl.own_columns) {
+            load_param<W>(p.w, c0 + at.col[k], 1.f, w);
+            load_param<W>(p.b, c0 + at.col[k], 0.f, b);
+          }
+          write_y<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, x[u][k], z[u][k], mean, rstd);
+        }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- forward, groups in tiles of rows
+// Block (tile, group, sample): the tile's count, mean and squared deviations, joined over the threads
+// as pairs (each thread's from its own values, twice over registers).
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(kThreads) tile_stats_kernel(GnProblem p, GnPlan pl, float *part) {
+  __shared__ float red[16];
+  const Tile<W, V> tile(p, pl);
+  const Places<W, kThreads, V> &at = tile.at;
+  const int n = tile.n, g = tile.g, t = tile.t;
+  const Slab<T> s(p, n, g);
+  float x[V][W], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) {
+      load_vec<W>(s.x + at.row[k] * p.xs + at.col[k], x[k]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) x[k][e] = 0.f;
+    }
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+#pragma unroll
+    for (int e = 0; e < W; ++e) sum += x[k][e];
+  const float mean = team_sum<kThreads>(sum, 0.f, red).x / Tile<W, V>::count(p, pl, t);
+  float dev = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0)
+#pragma unroll
+      for (int e = 0; e < W; ++e) dev = fmaf(x[k][e] - mean, x[k][e] - mean, dev);
+  dev = team_sum<kThreads>(dev, 0.f, red).x;
+  if (threadIdx.x == 0) {
+    float *q = part + 2 * (((size_t)n * p.G + g) * pl.tiles + t);
+    q[0] = mean;
+    q[1] = dev;
+  }
+}
+
+template <typename T, int W, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads) tile_forward_kernel(GnProblem p, GnPlan pl, const float *part) {
+  __shared__ float red[16];
+  const Tile<W, V> tile(p, pl);
+  const Places<W, kThreads, V> &at = tile.at;
+  const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg;
+  const Slab<T> s(p, n, g);
+  float x[V][W];
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) load_vec<W>(s.x + at.row[k] * p.xs + at.col[k], x[k]);
+  // mean of the tiles' means by their counts, then the deviations about it
+  const float *q = part + 2 * ((size_t)n * p.G + g) * pl.tiles;
+  const float inv = 1.f / ((float)p.m * p.cg), base = q[0];
+  float sum = 0.f, dev = 0.f;
+  for (int i = threadIdx.x; i < pl.tiles; i += kThreads)
+    sum += (q[2 * i] - base) * Tile<W, V>::count(p, pl, i);
+  const float off = team_sum<kThreads>(sum, 0.f, red).x * inv, mean = base + off;
+  for (int i = threadIdx.x; i < pl.tiles; i += kThreads) {
+    const float d = (q[2 * i] - base) - off;
+    dev += fmaf(d * d, Tile<W, V>::count(p, pl, i), q[2 * i + 1]);
+  }
+  const float rstd = 1.f / sqrtf(team_sum<kThreads>(dev, 0.f, red).x * inv + p.eps);
+  if (t == 0 && threadIdx.x == 0) {
+    if (p.mean) p.mean[n * p.G + g] = mean;
+    if (p.rstd) p.rstd[n * p.G + g] = rstd;
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) {
+      float w[W], b[W], z[W];
+      load_param<W>(p.w, c0 + at.col[k], 1.f, w);
+      load_param<W>(p.b, c0 + at.col[k], 0.f, b);
+      if (GATE) load_vec<W>(s.z + at.row[k] * p.zs + at.col[k], z);
+      write_y<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, x[k], z, mean, rstd);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// What a place gives: du w (gradient of xhat) and xhat, its part of dw and db, and dz, which is written here.
+template <typename T, int W, bool GATE>
+__device__ __forceinline__ void place_grad(const GnProblem &p, const Slab<T> &s, int row, int col, const float (&w)[W],
+                                           const float (&b)[W], float mean, float rstd, float (&dxh)[W], float (&xh)[W],
+                                           float (&dw)[W], float (&db)[W], bool write_dz) {
+  float x[W], z[W], dy[W], dz[W];
+  load_vec<W>(s.x + row * p.xs + col, x);
+  load_vec<W>(s.dy + row * p.dys + col, dy);
+  if (GATE) load_vec<W>(s.z + row * p.zs + col, z);
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    xh[e] = (x[e] - mean) * rstd;
+    const float du =
+        activate_grad<GATE>(dy[e], fmaf(xh[e], w[e], b[e]), GATE ? z[e] : 0.f, p.act == SSD_ACT_SILU, dz[e]);
+    dw[e] = fmaf(du, xh[e], dw[e]);
+    db[e] += du;
+    dxh[e] = du * w[e];
+  }
+  if (GATE && write_dz) store_vec<W>(s.dz + row * p.dzs + col, dz);
+}
+
+// Teams that each keep one group and walk over samples; block (groups of the block, samples of the block).
+// ROWSUM: teams of a block that share a group, whose dw and db are added in order at the end.
+template <typename T, int W, int NT, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads) team_backward_kernel(GnProblem p, GnPlan pl, float *dwp, float *dbp) {
+  constexpr int kTeams = kThreads / NT;
+  __shared__ float red[16];
+  __shared__ float acc[2][kThreads * W];
+  const int team = threadIdx.x / NT, tid = threadIdx.x % NT, gpb = pl.groups_per_block, shares = kTeams / gpb;
+  const int gl = team % gpb, share = team / gpb, g = blockIdx.x * gpb + gl, ncol = p.cg / W;
+  const bool has = g < p.G && share < shares;
+  const int n0 = blockIdx.y * pl.samples_per_block, n1 = min(p.n, n0 + pl.samples_per_block), c0 = (has ? g : 0) * p.cg;
+  const float inv = 1.f / ((float)p.m * p.cg);
+  const Places<W, NT, V> at(tid, ncol, 0, 0, has ? p.m : 0);
+  float w[W], b[W], dw[W], db[W];  // with at most NT columns a thread keeps one
+  const int col = at.col[0];
+#pragma unroll
+  for (int e = 0; e < W; ++e) w[e] = dw[e] = db[e] = b[e] = 0.f;
+  if (has && at.row[0] >= 0) {
+    load_param<W>(p.w, c0 + col, 1.f, w);
+    load_param<W>(p.b, c0 + col, 0.f, b);
+  }
+  // every thread of a warp makes the same number of turns (the sums are warp or block wide)
+  for (int nn = n0; nn < n1; nn += shares) {
+    const int n = nn + share;
+    const bool live = has && n < n1;
+    const int at_stat = live ? n * p.G + g : 0;
+    const float mean = __ldg(p.mean + at_stat), rstd = __ldg(p.rstd + at_stat);
+    const Slab<T> s(p, live ? n : 0, has ? g : 0);
+    float dxh[V][W], xh[V][W], sa = 0.f, sb = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (live && at.row[k] >= 0) {
+        place_grad<T, W, GATE>(p, s, at.row[k], col, w, b, mean, rstd, dxh[k], xh[k], dw, db, true);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          sa += dxh[k][e];
+          sb = fmaf(dxh[k][e], xh[k][e], sb);
+        }
+      }
+    const float2 ab = team_sum<NT>(sa, sb, red);
+    const float a = ab.x * inv, bb = ab.y * inv;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (live && at.row[k] >= 0) {
+        float dx[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) dx[e] = rstd * (dxh[k][e] - a - xh[k][e] * bb);
+        store_vec<W>(s.dx + at.row[k] * p.dxs + col, dx);
+      }
+  }
+  if (!dwp) return;
+  // the threads of a block that hold the same channels: a team's row phases, then the teams of a group
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    acc[0][threadIdx.x * W + e] = dw[e];
+    acc[1][threadIdx.x * W + e] = db[e];
+  }
+  __syncthreads();
+  const int phases = V == 1 ? 1 : NT / ncol;
+  for (int e = threadIdx.x; e < gpb * p.cg; e += kThreads) {
+    const int q = e / p.cg, c = e % p.cg;
+    if (blockIdx.x * gpb + q >= p.G) continue;
+    float sw = 0.f, sb = 0.f;
+    for (int sh = 0; sh < shares; ++sh)
+      for (int ph = 0; ph < phases; ++ph) {
+        const int th = (sh * gpb + q) * NT + ph * ncol + c / W;
+        sw += acc[0][th * W + c % W];
+        sb += acc[1][th * W + c % W];
+      }
+    const size_t to = (size_t)blockIdx.y * p.C + (blockIdx.x * gpb + q) * p.cg + c;
+    dwp[to] = sw;
+    dbp[to] = sb;
+  }
+}
+
+// Tiles, first kernel: the tile's parts of A and B, of dw and db (when a thread keeps its column), and dz.
+template <typename T, int W, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads) tile_sums_kernel(GnProblem p, GnPlan pl, float *part, float *dwp,
+                                                             float *dbp) {
+  __shared__ float red[16];
+  __shared__ float acc[2][kThreads * W];
+  const Tile<W, V> tile(p, pl);
+  const Places<W, kThreads, V> &at = tile.at;
+  const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg, ncol = p.cg / W;
+  const Slab<T> s(p, n, g);
+  const float mean = __ldg(p.mean + n * p.G + g), rstd = __ldg(p.rstd + n * p.G + g);
+  float dw[W], db[W], sa = 0.f, sb = 0.f;
+#pragma unroll
+  for (int e = 0; e < W; ++e) dw[e] = db[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) {
+      float w[W], b[W], dxh[W], xh[W];
+      load_param<W>(p.w, c0 + at.col[k], 1.f, w);
+      load_param<W>(p.b, c0 + at.col[k], 0.f, b);
+      place_grad<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, mean, rstd, dxh, xh, dw, db, true);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        sa += dxh[e];
+        sb = fmaf(dxh[e], xh[e], sb);
+      }
+    }
+  const float2 ab = team_sum<kThreads>(sa, sb, red);
+  if (threadIdx.x == 0) {
+    float *q = part + 2 * (((size_t)n * p.G + g) * pl.tiles + t);
+    q[0] = ab.x;
+    q[1] = ab.y;
+  }
+  if (!dwp) return;
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    acc[0][threadIdx.x * W + e] = dw[e];
+    acc[1][threadIdx.x * W + e] = db[e];
+  }
+  __syncthreads();
+  const int phases = kThreads / ncol;
+  for (int c = threadIdx.x; c < p.cg; c += kThreads) {
+    float sw = 0.f, sd = 0.f;
+    for (int ph = 0; ph < phases; ++ph) {
+      sw += acc[0][(ph * ncol + c / W) * W + c % W];
+      sd += acc[1][(ph * ncol + c / W) * W + c % W];
+    }
+    const size_t to = ((size_t)n * pl.tiles + t) * p.C + c0 + c;
+    dwp[to] = sw;
+    dbp[to] = sd;
+  }
+}
+
+template <typename T, int W, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads) tile_backward_kernel(GnProblem p, GnPlan pl, const float *part) {
+  __shared__ float red[16];
+  const Tile<W, V> tile(p, pl);
+  const Places<W, kThreads, V> &at = tile.at;
+  const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg;
+  const Slab<T> s(p, n, g);
+  const float mean = __ldg(p.mean + n * p.G + g), rstd = __ldg(p.rstd + n * p.G + g);
+  const float *q = part + 2 * ((size_t)n * p.G + g) * pl.tiles;
+  float sa = 0.f, sb = 0.f;
+  for (int i = threadIdx.x; i < pl.tiles; i += kThreads) {
+    sa += q[2 * i];
+    sb += q[2 * i + 1];
+  }
+  const float inv = 1.f / ((float)p.m * p.cg);
+  const float2 ab = team_sum<kThreads>(sa, sb, red);
+  const float a = ab.x * inv, bb = ab.y * inv;
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) {
+      float w[W], b[W], dxh[W], xh[W], dw[W], db[W], dx[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) dw[e] = db[e] = 0.f;
+      load_param<W>(p.w, c0 + at.col[k], 1.f, w);
+      load_param<W>(p.b, c0 + at.col[k], 0.f, b);
+      place_grad<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, mean, rstd, dxh, xh, dw, db, false);
+#pragma unroll
+      for (int e = 0; e < W; ++e) dx[e] = rstd * (dxh[e] - a - xh[e] * bb);
+      store_vec<W>(s.dx + at.row[k] * p.dxs + at.col[k], dx);
+    }
+}
+
+// dw and db of rows of groups wider than a block (a thread then has no column of its own): a thread per
+// channel, a tile of rows per block
+constexpr int kParamRows = 256;
+template <typename T, bool GATE>
+__global__ void __launch_bounds__(kThreads) param_kernel(GnProblem p, float *dwp, float *dbp) {
+  const int c = blockIdx.y * kThreads + threadIdx.x;
+  if (c >= p.C) return;
+  const int g = c / p.cg;
+  const long long r0 = (long long)blockIdx.x * kParamRows, r1 = min((long long)p.n * p.m, r0 + kParamRows);
+  float w[1], b[1], sw = 0.f, sb = 0.f;
+  load_param<1>(p.w, c, 1.f, w);
+  load_param<1>(p.b, c, 0.f, b);
+  for (long long r = r0; r < r1; ++r) {
+    const size_t at = (size_t)(r / p.m) * p.G + g;
+    float x[1], dy[1], z[1], dz;
+    load_vec<1>(static_cast<const T *>(p.x) + r * p.xs + c, x);
+    load_vec<1>(static_cast<const T *>(p.dy) + r * p.dys + c, dy);
+    if (GATE) load_vec<1>(static_cast<const T *>(p.z) + r * p.zs + c, z);
+    const float xh = (x[0] - __ldg(p.mean + at)) * __ldg(p.rstd + at);
+    const float du =
+        activate_grad<GATE>(dy[0], fmaf(xh, w[0], b[0]), GATE ? z[0] : 0.f, p.act == SSD_ACT_SILU, dz);
+    sw = fmaf(du, xh, sw);
+    sb += du;
+  }
+  dwp[(size_t)blockIdx.x * p.C + c] = sw;
+  dbp[(size_t)blockIdx.x * p.C + c] = sb;
+}
+
+// ---------------------------------------------------------------- launches
+// f(W, NT, V) for the plan's variant
+template <class F>
+void with_team(const GnPlan &pl, F f) {
+  using std::integral_constant;
+  auto call = [&](auto w, auto nt, auto v) { f(w, nt, v); };
+  if (pl.vec == 8) {
+    if (pl.places == 1) {
+      if (pl.team == 8) return call(integral_constant<int, 8>{}, integral_constant<int, 8>{}, integral_constant<int, 1>{});
+      if (pl.team == 16) return call(integral_constant<int, 8>{}, integral_constant<int, 16>{}, integral_constant<int, 1>{});
+      return call(integral_constant<int, 8>{}, integral_constant<int, 32>{}, integral_constant<int, 1>{});
+    }
+    if (pl.team == 32) return call(integral_constant<int, 8>{}, integral_constant<int, 32>{}, integral_constant<int, 4>{});
+    return call(integral_constant<int, 8>{}, integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  }
+  if (pl.team == 32) return call(integral_constant<int, 1>{}, integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  return call(integral_constant<int, 1>{}, integral_constant<int, 256>{}, integral_constant<int, 8>{});
+}
+
+template <typename T, bool GATE>
+void forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
+  if (pl.tiles == 0) {
+    with_team(pl, [&](auto w, auto nt, auto v) {
+      const dim3 grid((p.G + pl.groups_per_block - 1) / pl.groups_per_block,
+                      (p.n + pl.samples_per_block - 1) / pl.samples_per_block);
+      SSD_LAUNCH("gn_forward",
+                 (team_forward_kernel<T, decltype(w)::value, decltype(nt)::value, decltype(v)::value, GATE>
+                  <<<grid, kThreads, 0, s>>>(p, pl)));
+    });
+    return;
+  }
+  float *part = reinterpret_cast<float *>(ws + pl.part);
+  const unsigned grid = (unsigned)p.n * pl.tiles * p.G;
+  if (pl.vec == 8) {
+    SSD_LAUNCH("gn_stats", (tile_stats_kernel<T, 8, 4><<<grid, kThreads, 0, s>>>(p, pl, part)));
+    SSD_LAUNCH("gn_forward", (tile_forward_kernel<T, 8, 4, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
+  } else {
+    SSD_LAUNCH("gn_stats", (tile_stats_kernel<T, 1, 8><<<grid, kThreads, 0, s>>>(p, pl, part)));
+    SSD_LAUNCH("gn_forward", (tile_forward_kernel<T, 1, 8, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
+  }
+}
+
+template <typename T, bool GATE>
+void backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
+  const bool params = p.dw || p.db, own_columns = pl.own_columns;
+  float *dwp = reinterpret_cast<float *>(ws + pl.dwp), *dbp = reinterpret_cast<float *>(ws + pl.dbp);
+  float *kw = params && own_columns ? dwp : nullptr;  // partials written by the gradient kernel itself
+  if (pl.tiles == 0) {
+    with_team(pl, [&](auto w, auto nt, auto v) {
+      const dim3 grid((p.G + pl.groups_per_block - 1) / pl.groups_per_block,
+                      (p.n + pl.samples_per_block - 1) / pl.samples_per_block);
+      SSD_LAUNCH("gn_backward",
+                 (team_backward_kernel<T, decltype(w)::value, decltype(nt)::value, decltype(v)::value, GATE>
+                  <<<grid, kThreads, 0, s>>>(p, pl, kw, dbp)));
+    });
+  } else {
+    float *part = reinterpret_cast<float *>(ws + pl.part);
+    const unsigned grid = (unsigned)p.n * pl.tiles * p.G;
+    if (pl.vec == 8) {
+      SSD_LAUNCH("gn_sums", (tile_sums_kernel<T, 8, 4, GATE><<<grid, kThreads, 0, s>>>(p, pl, part, kw, dbp)));
+      SSD_LAUNCH("gn_backward", (tile_backward_kernel<T, 8, 4, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
+    } else {
+      SSD_LAUNCH("gn_sums", (tile_sums_kernel<T, 1, 8, GATE><<<grid, kThreads, 0, s>>>(p, pl, part, kw, dbp)));
+      SSD_LAUNCH("gn_backward", (tile_backward_kernel<T, 1, 8, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
+    }
+  }
+  if (!params) return;
+  if (!own_columns) {
+    const dim3 grid(pl.partials, (p.C + kThreads - 1) / kThreads);
+    SSD_LAUNCH("gn_param", (param_kernel<T, GATE><<<grid, kThreads, 0, s>>>(p, dwp, dbp)));
+  }
+  SSD_LAUNCH("gn_param_sum", launch_gn_param_sum(p.C, pl.partials, dwp, dbp, p.dw, p.db, s));
+}
+
+}  // namespace gn
+}  // namespace ssd

@@ -8,7 +8,6 @@ namespace ssd {
 struct GnProblem {
   int n, m, C, G, cg;  // samples, rows of a sample, channels, groups, channels of a group
   int act;             // ssd_activation
-  int eb;              // bytes of an element
   const void *x, *z, *dy;
   void *y, *dx, *dz;
   long long xs, zs, dys, ys, dxs, dzs;  // row strides (elements)
@@ -18,13 +17,28 @@ struct GnProblem {
   float *dw, *db;      // (C), may be null
 };
 
+// How a call is cut up.  The workspace does not depend on alignments, so it is
+// laid out for either width of accesses.
 struct GnPlan {
-  int tiles;                 // row tiles that hold a partial dweight / dbias each
-  size_t dwp, dbp, total;    // (tiles, C) fp32 each
+  int vec;                // channels of an access: 8 (16 bytes of bf16) or 1
+  int team, places;       // threads of a group's team and places of a thread
+  int tiles, tile_rows;   // 0: a group fits its team; else tiles of rows of a sample
+  bool own_columns;       // a thread keeps one column of channels: dw and db come out of the gradient kernel
+  int groups_per_block, samples_per_block;  // of a block of teams
+  int partials;           // partial dw / db rows
+  size_t part, dwp, dbp, total;  // workspace: (n, G, tiles, 2) and (partials, C) fp32 twice
 };
 
-GnPlan gn_plan(const GnProblem &p, bool backward);
+// vectors: whether every tensor of the call allows accesses of 8 channels
+GnPlan gn_plan(const GnProblem &p, bool backward, bool vectors);
+size_t gn_workspace(const GnProblem &p, bool backward);
 template <typename T> void run_gn_forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s);
 template <typename T> void run_gn_backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s);
+template <> void run_gn_forward<float>(const GnProblem &, const GnPlan &, char *, cudaStream_t);
+template <> void run_gn_forward<__nv_bfloat16>(const GnProblem &, const GnPlan &, char *, cudaStream_t);
+template <> void run_gn_backward<float>(const GnProblem &, const GnPlan &, char *, cudaStream_t);
+template <> void run_gn_backward<__nv_bfloat16>(const GnProblem &, const GnPlan &, char *, cudaStream_t);
+// dw and db as sums of their partials, in order (gn_plan.cu)
+void launch_gn_param_sum(int C, int partials, const float *dwp, const float *dbp, float *dw, float *db, cudaStream_t s);
 
 }  // namespace ssd
