@@ -55,6 +55,34 @@ __device__ __forceinline__ void load_vec(const float *p, float (&v)[W]) {
     v[0] = __ldg(p);
   }
 }
+// W channels as they lie in memory: half the registers for bf16
+template <typename T, int W>
+struct Raw {
+  float f[W];
+  __device__ __forceinline__ void load(const T *p) { load_vec<W>(p, f); }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int e = 0; e < W; ++e) f[e] = 0.f;
+  }
+  __device__ __forceinline__ void get(float (&v)[W]) const {
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] = f[e];
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
 template <int W>
 __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&v)[W]) {
   if constexpr (W == 8) {
@@ -216,16 +244,22 @@ __device__ __forceinline__ void write_y(const GnProblem &p, const Slab<T> &s, in
 }
 
 // ---------------------------------------------------------------- forward, groups that fit a team
-// Teams that each keep one group and walk over samples, U at a time; block (groups of the block, samples of
-// the block).
+// Teams that each keep one group and walk over samples; block (groups of the block, samples of the block).
+// With one place to a thread the next sample's values are on their way while one is worked on, and
+// registers are held down to keep enough of them in flight on an SM.
+template <int V>
+constexpr int min_blocks(int one) { return V == 1 ? one : 1; }
 template <typename T, int W, int NT, int V, bool GATE>
-__global__ void __launch_bounds__(kThreads) team_forward_kernel(GnProblem p, GnPlan pl) {
-  constexpr int kTeams = kThreads / NT, U = V == 1 ? 2 : 1;
+__global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 5 : 4))
+    team_forward_kernel(GnProblem p, GnPlan pl) {
+  constexpr int kTeams = kThreads / NT;
   __shared__ float red[16];
   const int team = threadIdx.x / NT, tid = threadIdx.x % NT, gpb = pl.groups_per_block, shares = kTeams / gpb;
   const int share = team / gpb, g = blockIdx.x * gpb + team % gpb;
   const bool has = g < p.G && share < shares;
-  const int n0 = blockIdx.y * pl.samples_per_block, n1 = min(p.n, n0 + pl.samples_per_block), c0 = (has ? g : 0) * p.cg;
+  const int n0 = blockIdx.y * pl.samples_per_block + share;
+  const int n1 = min(p.n, (blockIdx.y + 1) * pl.samples_per_block), c0 = (has ? g : 0) * p.cg;
+  const int turns = (n1 - (int)blockIdx.y * pl.samples_per_block + shares - 1) / shares;
   const float inv = 1.f / ((float)p.m * p.cg);
   const Places<W, NT, V> at(tid, p.cg / W, 0, 0, has ? p.m : 0);
   float w[W], b[W];
@@ -233,54 +267,66 @@ __global__ void __launch_bounds__(kThreads) team_forward_kernel(GnProblem p, GnP
     load_param<W>(p.w, c0 + at.col[0], 1.f, w);
     load_param<W>(p.b, c0 + at.col[0], 0.f, b);
   }
-  // every thread of a warp makes the same number of turns (the sums are warp or block wide)
-  for (int nn = n0; nn < n1; nn += U * shares) {
-    float x[U][V][W], z[U][V][W];
+  Raw<T, W> xr[V], zr[V];
+  auto load = [&](int n) {
+    const Slab<T> s(p, has && n < n1 ? n : 0, has ? g : 0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int n = nn + u * shares + share;
-      const Slab<T> s(p, has && n < n1 ? n : 0, has ? g : 0);
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (has && n < n1 && at.row[k] >= 0) {
-          load_vec<W>(s.x + at.row[k] * p.xs + at.col[k], x[u][k]);
-          if (GATE) load_vec<W>(s.z + at.row[k] * p.zs + at.col[k], z[u][k]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < W; ++e) x[u][k][e] = 0.f;
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int n = nn + u * shares + share;
-      const bool live = has && n < n1;
-      const Slab<T> s(p, live ? n : 0, has ? g : 0);
-      float sum = 0.f, dev = 0.f;
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-#pragma unroll
-        for (int e = 0; e < W; ++e) sum += x[u][k][e];
-      const float mean = team_sum<NT>(sum, 0.f, red).x * inv;
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (live && at.row[k] >= 0)
-#pragma unroll
-          for (int e = 0; e < W; ++e) dev = fmaf(x[u][k][e] - mean, x[u][k][e] - mean, dev);
-      const float rstd = 1.f / sqrtf(team_sum<NT>(dev, 0.f, red).x * inv + p.eps);
-      if (live && tid == 0) {
-        if (p.mean) p.mean[n * p.G + g] = mean;
-        if (p.rstd) p.rstd[n * p.G + g] = rstd;
+    for (int k = 0; k < V; ++k)
+      if (has && n < n1 && at.row[k] >= 0) {
+        xr[k].load(s.x + at.row[k] * p.xs + at.col[k]);
+        if (GATE) zr[k].load(s.z + at.row[k] * p.zs + at.col[k]);
+      } else {
+        xr[k].clear();
       }
+  };
+  // every thread of a warp makes the same number of turns (the sums are warp or block wide)
+  if (V == 1) load(n0);
+  for (int i = 0; i < turns; ++i) {
+    const int n = n0 + i * shares;
+    const bool live = has && n < n1;
+    if (V > 1) load(n);
+    Raw<T, W> xc[V], zc[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (live && at.row[k] >= 0) {
-          if (!pl.own_columns) {
-            load_param<W>(p.w, c0 + at.col[k], 1.f, w);
-            load_param<W>(p.b, c0 + at.col[k], 0.f, b);
-          }
-          write_y<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, x[u][k], z[u][k], mean, rstd);
-        }
+    for (int k = 0; k < V; ++k) {
+      xc[k] = xr[k];
+      if (GATE) zc[k] = zr[k];
     }
+    if (V == 1) load(n + shares);
+    const Slab<T> s(p, live ? n : 0, has ? g : 0);
+    float sum = 0.f, dev = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float x[W];
+      xc[k].get(x);
+#pragma unroll
+      for (int e = 0; e < W; ++e) sum += x[e];
+    }
+    const float mean = team_sum<NT>(sum, 0.f, red).x * inv;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (live && at.row[k] >= 0) {
+        float x[W];
+        xc[k].get(x);
+#pragma unroll
+        for (int e = 0; e < W; ++e) dev = fmaf(x[e] - mean, x[e] - mean, dev);
+      }
+    const float rstd = 1.f / sqrtf(team_sum<NT>(dev, 0.f, red).x * inv + p.eps);
+    if (live && tid == 0) {
+      if (p.mean) p.mean[n * p.G + g] = mean;
+      if (p.rstd) p.rstd[n * p.G + g] = rstd;
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (live && at.row[k] >= 0) {
+        float x[W], z[W];
+        xc[k].get(x);
+        if (GATE) zc[k].get(z);
+        if (!pl.own_columns) {
+          load_param<W>(p.w, c0 + at.col[k], 1.f, w);
+          load_param<W>(p.b, c0 + at.col[k], 0.f, b);
+        }
+        write_y<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, x, z, mean, rstd);
+      }
   }
 }
 
@@ -361,15 +407,16 @@ __global__ void __launch_bounds__(kThreads) tile_forward_kernel(GnProblem p, GnP
 }
 
 // ---------------------------------------------------------------- backward
-// What a place gives: du w (gradient of xhat) and xhat, its part of dw and db, and dz, which is written here.
+// What a place gives: du w (gradient of xhat) and xhat, its part of dw and db, and dz.
 template <typename T, int W, bool GATE>
-__device__ __forceinline__ void place_grad(const GnProblem &p, const Slab<T> &s, int row, int col, const float (&w)[W],
-                                           const float (&b)[W], float mean, float rstd, float (&dxh)[W], float (&xh)[W],
-                                           float (&dw)[W], float (&db)[W], bool write_dz) {
-  float x[W], z[W], dy[W], dz[W];
-  load_vec<W>(s.x + row * p.xs + col, x);
-  load_vec<W>(s.dy + row * p.dys + col, dy);
-  if (GATE) load_vec<W>(s.z + row * p.zs + col, z);
+__device__ __forceinline__ void place_grad(const GnProblem &p, const Raw<T, W> &xr, const Raw<T, W> &zr,
+                                           const Raw<T, W> &dyr, const float (&w)[W], const float (&b)[W], float mean,
+                                           float rstd, float (&dxh)[W], float (&xh)[W], float (&dw)[W], float (&db)[W],
+                                           float (&dz)[W]) {
+  float x[W], z[W], dy[W];
+  xr.get(x);
+  dyr.get(dy);
+  if (GATE) zr.get(z);
 #pragma unroll
   for (int e = 0; e < W; ++e) {
     xh[e] = (x[e] - mean) * rstd;
@@ -379,20 +426,28 @@ __device__ __forceinline__ void place_grad(const GnProblem &p, const Slab<T> &s,
     db[e] += du;
     dxh[e] = du * w[e];
   }
-  if (GATE && write_dz) store_vec<W>(s.dz + row * p.dzs + col, dz);
+}
+template <typename T, int W, bool GATE>
+__device__ __forceinline__ void load_place(const GnProblem &p, const Slab<T> &s, int row, int col, Raw<T, W> &x,
+                                           Raw<T, W> &z, Raw<T, W> &dy) {
+  x.load(s.x + row * p.xs + col);
+  dy.load(s.dy + row * p.dys + col);
+  if (GATE) z.load(s.z + row * p.zs + col);
 }
 
-// Teams that each keep one group and walk over samples; block (groups of the block, samples of the block).
-// ROWSUM: teams of a block that share a group, whose dw and db are added in order at the end.
+// As the forward's teams; dw and db of the block's samples at the end.
 template <typename T, int W, int NT, int V, bool GATE>
-__global__ void __launch_bounds__(kThreads) team_backward_kernel(GnProblem p, GnPlan pl, float *dwp, float *dbp) {
+__global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2))
+    team_backward_kernel(GnProblem p, GnPlan pl, float *dwp, float *dbp) {
   constexpr int kTeams = kThreads / NT;
   __shared__ float red[16];
   __shared__ float acc[2][kThreads * W];
   const int team = threadIdx.x / NT, tid = threadIdx.x % NT, gpb = pl.groups_per_block, shares = kTeams / gpb;
   const int gl = team % gpb, share = team / gpb, g = blockIdx.x * gpb + gl, ncol = p.cg / W;
   const bool has = g < p.G && share < shares;
-  const int n0 = blockIdx.y * pl.samples_per_block, n1 = min(p.n, n0 + pl.samples_per_block), c0 = (has ? g : 0) * p.cg;
+  const int n0 = blockIdx.y * pl.samples_per_block + share;
+  const int n1 = min(p.n, (blockIdx.y + 1) * pl.samples_per_block), c0 = (has ? g : 0) * p.cg;
+  const int turns = (n1 - (int)blockIdx.y * pl.samples_per_block + shares - 1) / shares;
   const float inv = 1.f / ((float)p.m * p.cg);
   const Places<W, NT, V> at(tid, ncol, 0, 0, has ? p.m : 0);
   float w[W], b[W], dw[W], db[W];  // with at most NT columns a thread keeps one
@@ -403,24 +458,40 @@ __global__ void __launch_bounds__(kThreads) team_backward_kernel(GnProblem p, Gn
     load_param<W>(p.w, c0 + col, 1.f, w);
     load_param<W>(p.b, c0 + col, 0.f, b);
   }
-  // every thread of a warp makes the same number of turns (the sums are warp or block wide)
-  for (int nn = n0; nn < n1; nn += shares) {
-    const int n = nn + share;
+  Raw<T, W> xr, zr, dyr;
+  float mean_r = 0.f, rstd_r = 0.f;
+  auto load = [&](int n) {  // one place: the sample after the one in work
+    if (has && n < n1) {
+      mean_r = __ldg(p.mean + n * p.G + g);
+      rstd_r = __ldg(p.rstd + n * p.G + g);
+      if (at.row[0] >= 0) load_place<T, W, GATE>(p, Slab<T>(p, n, g), at.row[0], col, xr, zr, dyr);
+    }
+  };
+  if (V == 1) load(n0);
+  for (int i = 0; i < turns; ++i) {
+    const int n = n0 + i * shares;
     const bool live = has && n < n1;
-    const int at_stat = live ? n * p.G + g : 0;
-    const float mean = __ldg(p.mean + at_stat), rstd = __ldg(p.rstd + at_stat);
+    if (V > 1 && live) {
+      mean_r = __ldg(p.mean + n * p.G + g);
+      rstd_r = __ldg(p.rstd + n * p.G + g);
+    }
+    const float mean = mean_r, rstd = rstd_r;
     const Slab<T> s(p, live ? n : 0, has ? g : 0);
     float dxh[V][W], xh[V][W], sa = 0.f, sb = 0.f;
 #pragma unroll
     for (int k = 0; k < V; ++k)
       if (live && at.row[k] >= 0) {
-        place_grad<T, W, GATE>(p, s, at.row[k], col, w, b, mean, rstd, dxh[k], xh[k], dw, db, true);
+        float dz[W];
+        if (V > 1) load_place<T, W, GATE>(p, s, at.row[k], col, xr, zr, dyr);
+        place_grad<T, W, GATE>(p, xr, zr, dyr, w, b, mean, rstd, dxh[k], xh[k], dw, db, dz);
+        if (GATE) store_vec<W>(s.dz + at.row[k] * p.dzs + col, dz);
 #pragma unroll
         for (int e = 0; e < W; ++e) {
           sa += dxh[k][e];
           sb = fmaf(dxh[k][e], xh[k][e], sb);
         }
       }
+    if (V == 1) load(n + shares);
     const float2 ab = team_sum<NT>(sa, sb, red);
     const float a = ab.x * inv, bb = ab.y * inv;
 #pragma unroll
@@ -474,10 +545,13 @@ __global__ void __launch_bounds__(kThreads) tile_sums_kernel(GnProblem p, GnPlan
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0) {
-      float w[W], b[W], dxh[W], xh[W];
+      float w[W], b[W], dxh[W], xh[W], dz[W];
+      Raw<T, W> xr, zr, dyr;
+      load_place<T, W, GATE>(p, s, at.row[k], at.col[k], xr, zr, dyr);
       load_param<W>(p.w, c0 + at.col[k], 1.f, w);
       load_param<W>(p.b, c0 + at.col[k], 0.f, b);
-      place_grad<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, mean, rstd, dxh, xh, dw, db, true);
+      place_grad<T, W, GATE>(p, xr, zr, dyr, w, b, mean, rstd, dxh, xh, dw, db, dz);
+      if (GATE) store_vec<W>(s.dz + at.row[k] * p.dzs + at.col[k], dz);
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         sa += dxh[e];
@@ -530,12 +604,14 @@ __global__ void __launch_bounds__(kThreads) tile_backward_kernel(GnProblem p, Gn
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0) {
-      float w[W], b[W], dxh[W], xh[W], dw[W], db[W], dx[W];
+      float w[W], b[W], dxh[W], xh[W], dw[W], db[W], dz[W], dx[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) dw[e] = db[e] = 0.f;
+      Raw<T, W> xr, zr, dyr;
+      load_place<T, W, GATE>(p, s, at.row[k], at.col[k], xr, zr, dyr);
       load_param<W>(p.w, c0 + at.col[k], 1.f, w);
       load_param<W>(p.b, c0 + at.col[k], 0.f, b);
-      place_grad<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, mean, rstd, dxh, xh, dw, db, false);
+      place_grad<T, W, GATE>(p, xr, zr, dyr, w, b, mean, rstd, dxh, xh, dw, db, dz);
 #pragma unroll
       for (int e = 0; e < W; ++e) dx[e] = rstd * (dxh[e] - a - xh[e] * bb);
       store_vec<W>(s.dx + at.row[k] * p.dxs + at.col[k], dx);
