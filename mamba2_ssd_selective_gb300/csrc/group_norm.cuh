@@ -19,6 +19,7 @@
 #pragma once
 
 #include "group_norm.h"
+#include "sm100.cuh"
 
 namespace ssd {
 namespace gn {
@@ -107,20 +108,112 @@ __device__ __forceinline__ void store_vec(float *p, const float (&v)[W]) {
     p[0] = v[0];
   }
 }
+// ---------------------------------------------------------------- arithmetic on W channels
+// Eight channels go two to an instruction (packed fp32): once enough loads are in
+// flight, instructions bound these kernels before memory does.
+template <int W>
+struct Vec {
+  static constexpr int kPairs = (W + 1) / 2;
+  uint64_t q[kPairs];
+  __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ explicit Vec(float c) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) q[i] = sm100::pk2(c, c);
+  }
+  __device__ __forceinline__ explicit Vec(const float (&v)[W]) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) q[i] = sm100::pk2(v[2 * i], W == 1 ? 0.f : v[2 * i + (W > 1)]);
+  }
+  __device__ __forceinline__ void get(float (&v)[W]) const {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      float a, b;
+      sm100::upk2(q[i], a, b);
+      v[2 * i] = a;
+      if (W > 1) v[2 * i + (W > 1)] = b;
+    }
+  }
+  __device__ __forceinline__ float sum() const {
+    uint64_t t = q[0];
+#pragma unroll
+    for (int i = 1; i < kPairs; ++i) t = sm100::add2(t, q[i]);
+    float a, b;
+    sm100::upk2(t, a, b);
+    return W == 1 ? a : a + b;
+  }
+};
+template <int W> __device__ __forceinline__ Vec<W> operator+(const Vec<W> &a, const Vec<W> &b) {
+  Vec<W> r;
+#pragma unroll
+  for (int i = 0; i < Vec<W>::kPairs; ++i) r.q[i] = sm100::add2(a.q[i], b.q[i]);
+  return r;
+}
+template <int W> __device__ __forceinline__ Vec<W> operator*(const Vec<W> &a, const Vec<W> &b) {
+  Vec<W> r;
+#pragma unroll
+  for (int i = 0; i < Vec<W>::kPairs; ++i) r.q[i] = sm100::mul2(a.q[i], b.q[i]);
+  return r;
+}
+template <int W> __device__ __forceinline__ Vec<W> fma(const Vec<W> &a, const Vec<W> &b, const Vec<W> &c) {
+  Vec<W> r;
+#pragma unroll
+  for (int i = 0; i < Vec<W>::kPairs; ++i) r.q[i] = sm100::fma2(a.q[i], b.q[i], c.q[i]);
+  return r;
+}
+// 1 / (1 + e^-v) on the special-function unit: 2^x and 1 / x, each to about 2^-22
+template <int W> __device__ __forceinline__ Vec<W> sigmoid(const Vec<W> &v) {
+  float t[W];
+  (v * Vec<W>(-1.44269504f)).get(t);
+#pragma unroll
+  for (int e = 0; e < W; ++e) t[e] = sm100::ex2_approx(t[e]);
+  (Vec<W>(t) + Vec<W>(1.f)).get(t);
+#pragma unroll
+  for (int e = 0; e < W; ++e) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t[e]));
+  return Vec<W>(t);
+}
+// (a sigmoid(a))' given s = sigmoid(a)
+template <int W> __device__ __forceinline__ Vec<W> silu_grad(const Vec<W> &a, const Vec<W> &s) {
+  return s * fma(a, fma(s, Vec<W>(-1.f), Vec<W>(1.f)), Vec<W>(1.f));
+}
+
+// Vec of what lies in a Raw
+template <typename T, int W>
+__device__ __forceinline__ Vec<W> vec_of(const Raw<T, W> &r) {
+  float v[W];
+  r.get(v);
+  return Vec<W>(v);
+}
 // W parameters of consecutive channels (c a multiple of W), or a constant where there are none
 template <int W>
-__device__ __forceinline__ void load_param(const float *p, int c, float none, float (&v)[W]) {
+__device__ __forceinline__ Vec<W> load_param(const float *p, int c, float none) {
+  float v[W];
   if (W == 8 && p && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
     load_vec<W>(p + c, v);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int e = 0; e < W; ++e) v[e] = p ? __ldg(p + c + e) : none;
+    for (int e = 0; e < W; ++e) v[e] = p ? __ldg(p + c + e) : none;
+  }
+  return Vec<W>(v);
 }
 
 // ---------------------------------------------------------------- sums over a team of NT threads
 template <int NT>
-__device__ __forceinline__ float2 team_sum(float a, float b, float *scratch) {
+__device__ __forceinline__ float team_sum(float a, float *scratch) {
+#pragma unroll
+  for (int o = (NT < 32 ? NT : 32) / 2; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if constexpr (NT > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) a += scratch[w];
+  }
+  return a;
+}
+// two sums at once; scratch of 16 values
+template <int NT>
+__device__ __forceinline__ float2 team_sum2(float a, float b, float *scratch) {
 #pragma unroll
   for (int o = (NT < 32 ? NT : 32) / 2; o >= 1; o >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, o);
@@ -196,23 +289,21 @@ struct Tile {
   }
 };
 
-__device__ __forceinline__ float silu_grad(float a, float s) { return s * (1.f + a * (1.f - s)); }
-
 // u -> y
-template <bool GATE>
-__device__ __forceinline__ float activate(float u, float z, bool silu) {
-  if (GATE) return u * (z * sigmoid_fast(z));
-  return silu ? u * sigmoid_fast(u) : u;
+template <int W, bool GATE>
+__device__ __forceinline__ Vec<W> activate(const Vec<W> &u, const Vec<W> &z, bool silu) {
+  if (GATE) return u * (z * sigmoid(z));
+  return silu ? u * sigmoid(u) : u;
 }
 // dy -> du, and dz with the gate
-template <bool GATE>
-__device__ __forceinline__ float activate_grad(float dy, float u, float z, bool silu, float &dz) {
+template <int W, bool GATE>
+__device__ __forceinline__ Vec<W> activate_grad(const Vec<W> &dy, const Vec<W> &u, const Vec<W> &z, bool silu, Vec<W> &dz) {
   if (GATE) {
-    const float s = sigmoid_fast(z);
+    const Vec<W> s = sigmoid(z);
     dz = dy * u * silu_grad(z, s);
     return dy * (z * s);
   }
-  return silu ? dy * silu_grad(u, sigmoid_fast(u)) : dy;
+  return silu ? dy * silu_grad(u, sigmoid(u)) : dy;
 }
 
 // one group of one sample: pointers to its first row's first channel
@@ -233,14 +324,18 @@ struct Slab {
 };
 
 template <typename T, int W, bool GATE>
-__device__ __forceinline__ void write_y(const GnProblem &p, const Slab<T> &s, int row, int col, const float (&w)[W],
-                                        const float (&b)[W], const float (&x)[W], const float (&z)[W], float mean,
-                                        float rstd) {
+__device__ __forceinline__ void write_y(const GnProblem &p, const Slab<T> &s, int row, int col, const Vec<W> &w,
+                                        const Vec<W> &b, const Vec<W> &x, const Raw<T, W> &z, float mean, float rstd) {
+  const Vec<W> u = fma((x + Vec<W>(-mean)) * Vec<W>(rstd), w, b);
   float y[W];
-#pragma unroll
-  for (int e = 0; e < W; ++e)
-    y[e] = activate<GATE>(fmaf((x[e] - mean) * rstd, w[e], b[e]), GATE ? z[e] : 0.f, p.act == SSD_ACT_SILU);
+  activate<W, GATE>(u, GATE ? vec_of<T, W>(z) : u, p.act == SSD_ACT_SILU).get(y);
   store_vec<W>(s.y + row * p.ys + col, y);
+}
+// sum of (x - mean)^2
+template <int W>
+__device__ __forceinline__ float deviations(const Vec<W> &x, float mean) {
+  const Vec<W> d = x + Vec<W>(-mean);
+  return (d * d).sum();
 }
 
 // ---------------------------------------------------------------- forward, groups that fit a team
@@ -250,7 +345,7 @@ __device__ __forceinline__ void write_y(const GnProblem &p, const Slab<T> &s, in
 template <int V>
 constexpr int min_blocks(int one) { return V == 1 ? one : 1; }
 template <typename T, int W, int NT, int V, bool GATE>
-__global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 5 : 4))
+__global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 4 : 3))
     team_forward_kernel(GnProblem p, GnPlan pl) {
   constexpr int kTeams = kThreads / NT;
   __shared__ float red[16];
@@ -262,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 5 : 4
   const int turns = (n1 - (int)blockIdx.y * pl.samples_per_block + shares - 1) / shares;
   const float inv = 1.f / ((float)p.m * p.cg);
   const Places<W, NT, V> at(tid, p.cg / W, 0, 0, has ? p.m : 0);
-  float w[W], b[W];
+  Vec<W> w, b;
   if (pl.own_columns && has && at.row[0] >= 0) {
-    load_param<W>(p.w, c0 + at.col[0], 1.f, w);
-    load_param<W>(p.b, c0 + at.col[0], 0.f, b);
+    w = load_param<W>(p.w, c0 + at.col[0], 1.f);
+    b = load_param<W>(p.b, c0 + at.col[0], 0.f);
   }
   Raw<T, W> xr[V], zr[V];
   auto load = [&](int n) {
@@ -285,32 +380,23 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 5 : 4
     const int n = n0 + i * shares;
     const bool live = has && n < n1;
     if (V > 1) load(n);
-    Raw<T, W> xc[V], zc[V];
+    Vec<W> x[V];
+    Raw<T, W> z[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      xc[k] = xr[k];
-      if (GATE) zc[k] = zr[k];
+      x[k] = vec_of<T, W>(xr[k]);
+      if (GATE) z[k] = zr[k];
     }
     if (V == 1) load(n + shares);
     const Slab<T> s(p, live ? n : 0, has ? g : 0);
     float sum = 0.f, dev = 0.f;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      float x[W];
-      xc[k].get(x);
-#pragma unroll
-      for (int e = 0; e < W; ++e) sum += x[e];
-    }
-    const float mean = team_sum<NT>(sum, 0.f, red).x * inv;
+    for (int k = 0; k < V; ++k) sum += x[k].sum();
+    const float mean = team_sum<NT>(sum, red) * inv;
 #pragma unroll
     for (int k = 0; k < V; ++k)
-      if (live && at.row[k] >= 0) {
-        float x[W];
-        xc[k].get(x);
-#pragma unroll
-        for (int e = 0; e < W; ++e) dev = fmaf(x[e] - mean, x[e] - mean, dev);
-      }
-    const float rstd = 1.f / sqrtf(team_sum<NT>(dev, 0.f, red).x * inv + p.eps);
+      if (live && at.row[k] >= 0) dev += deviations<W>(x[k], mean);
+    const float rstd = 1.f / sqrtf(team_sum<NT>(dev, red) * inv + p.eps);
     if (live && tid == 0) {
       if (p.mean) p.mean[n * p.G + g] = mean;
       if (p.rstd) p.rstd[n * p.G + g] = rstd;
@@ -318,14 +404,11 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 5 : 4
 #pragma unroll
     for (int k = 0; k < V; ++k)
       if (live && at.row[k] >= 0) {
-        float x[W], z[W];
-        xc[k].get(x);
-        if (GATE) zc[k].get(z);
         if (!pl.own_columns) {
-          load_param<W>(p.w, c0 + at.col[k], 1.f, w);
-          load_param<W>(p.b, c0 + at.col[k], 0.f, b);
+          w = load_param<W>(p.w, c0 + at.col[k], 1.f);
+          b = load_param<W>(p.b, c0 + at.col[k], 0.f);
         }
-        write_y<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, x, z, mean, rstd);
+        write_y<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, x[k], z[k], mean, rstd);
       }
   }
 }
@@ -340,27 +423,21 @@ __global__ void __launch_bounds__(kThreads) tile_stats_kernel(GnProblem p, GnPla
   const Places<W, kThreads, V> &at = tile.at;
   const int n = tile.n, g = tile.g, t = tile.t;
   const Slab<T> s(p, n, g);
-  float x[V][W], sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0) {
-      load_vec<W>(s.x + at.row[k] * p.xs + at.col[k], x[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < W; ++e) x[k][e] = 0.f;
-    }
-#pragma unroll
-  for (int k = 0; k < V; ++k)
-#pragma unroll
-    for (int e = 0; e < W; ++e) sum += x[k][e];
-  const float mean = team_sum<kThreads>(sum, 0.f, red).x / Tile<W, V>::count(p, pl, t);
-  float dev = 0.f;
+  Raw<T, W> xr[V];
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0)
+      xr[k].load(s.x + at.row[k] * p.xs + at.col[k]);
+    else
+      xr[k].clear();
+  float sum = 0.f, dev = 0.f;
 #pragma unroll
-      for (int e = 0; e < W; ++e) dev = fmaf(x[k][e] - mean, x[k][e] - mean, dev);
-  dev = team_sum<kThreads>(dev, 0.f, red).x;
+  for (int k = 0; k < V; ++k) sum += vec_of<T, W>(xr[k]).sum();
+  const float mean = team_sum<kThreads>(sum, red) / Tile<W, V>::count(p, pl, t);
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) dev += deviations<W>(vec_of<T, W>(xr[k]), mean);
+  dev = team_sum<kThreads>(dev, red);
   if (threadIdx.x == 0) {
     float *q = part + 2 * (((size_t)n * p.G + g) * pl.tiles + t);
     q[0] = mean;
@@ -375,57 +452,62 @@ __global__ void __launch_bounds__(kThreads) tile_forward_kernel(GnProblem p, GnP
   const Places<W, kThreads, V> &at = tile.at;
   const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg;
   const Slab<T> s(p, n, g);
-  float x[V][W];
+  Raw<T, W> xr[V], zr[V];
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0) load_vec<W>(s.x + at.row[k] * p.xs + at.col[k], x[k]);
+    if (at.row[k] >= 0) {
+      xr[k].load(s.x + at.row[k] * p.xs + at.col[k]);
+      if (GATE) zr[k].load(s.z + at.row[k] * p.zs + at.col[k]);
+    }
   // mean of the tiles' means by their counts, then the deviations about it
   const float *q = part + 2 * ((size_t)n * p.G + g) * pl.tiles;
   const float inv = 1.f / ((float)p.m * p.cg), base = q[0];
   float sum = 0.f, dev = 0.f;
   for (int i = threadIdx.x; i < pl.tiles; i += kThreads)
     sum += (q[2 * i] - base) * Tile<W, V>::count(p, pl, i);
-  const float off = team_sum<kThreads>(sum, 0.f, red).x * inv, mean = base + off;
+  const float off = team_sum<kThreads>(sum, red) * inv, mean = base + off;
   for (int i = threadIdx.x; i < pl.tiles; i += kThreads) {
     const float d = (q[2 * i] - base) - off;
     dev += fmaf(d * d, Tile<W, V>::count(p, pl, i), q[2 * i + 1]);
   }
-  const float rstd = 1.f / sqrtf(team_sum<kThreads>(dev, 0.f, red).x * inv + p.eps);
+  const float rstd = 1.f / sqrtf(team_sum<kThreads>(dev, red) * inv + p.eps);
   if (t == 0 && threadIdx.x == 0) {
     if (p.mean) p.mean[n * p.G + g] = mean;
     if (p.rstd) p.rstd[n * p.G + g] = rstd;
   }
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0) {
-      float w[W], b[W], z[W];
-      load_param<W>(p.w, c0 + at.col[k], 1.f, w);
-      load_param<W>(p.b, c0 + at.col[k], 0.f, b);
-      if (GATE) load_vec<W>(s.z + at.row[k] * p.zs + at.col[k], z);
-      write_y<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, x[k], z, mean, rstd);
-    }
+    if (at.row[k] >= 0)
+      write_y<T, W, GATE>(p, s, at.row[k], at.col[k], load_param<W>(p.w, c0 + at.col[k], 1.f),
+                          load_param<W>(p.b, c0 + at.col[k], 0.f), vec_of<T, W>(xr[k]), zr[k], mean, rstd);
 }
 
 // ---------------------------------------------------------------- backward
-// What a place gives: du w (gradient of xhat) and xhat, its part of dw and db, and dz.
+// What a place gives: du w (gradient of xhat) and xhat, its part of dw and db, and dz, which is stored if asked for.
 template <typename T, int W, bool GATE>
 __device__ __forceinline__ void place_grad(const GnProblem &p, const Raw<T, W> &xr, const Raw<T, W> &zr,
-                                           const Raw<T, W> &dyr, const float (&w)[W], const float (&b)[W], float mean,
-                                           float rstd, float (&dxh)[W], float (&xh)[W], float (&dw)[W], float (&db)[W],
-                                           float (&dz)[W]) {
-  float x[W], z[W], dy[W];
-  xr.get(x);
-  dyr.get(dy);
-  if (GATE) zr.get(z);
-#pragma unroll
-  for (int e = 0; e < W; ++e) {
-    xh[e] = (x[e] - mean) * rstd;
-    const float du =
-        activate_grad<GATE>(dy[e], fmaf(xh[e], w[e], b[e]), GATE ? z[e] : 0.f, p.act == SSD_ACT_SILU, dz[e]);
-    dw[e] = fmaf(du, xh[e], dw[e]);
-    db[e] += du;
-    dxh[e] = du * w[e];
+                                           const Raw<T, W> &dyr, const Vec<W> &w, const Vec<W> &b, float mean, float rstd,
+                                           Vec<W> &dxh, Vec<W> &xh, Vec<W> &dw, Vec<W> &db, T *dz_to) {
+  Vec<W> dz;
+  xh = (vec_of<T, W>(xr) + Vec<W>(-mean)) * Vec<W>(rstd);
+  const Vec<W> dy = vec_of<T, W>(dyr);
+  const Vec<W> du =
+      activate_grad<W, GATE>(dy, fma(xh, w, b), GATE ? vec_of<T, W>(zr) : dy, p.act == SSD_ACT_SILU, dz);
+  dw = fma(du, xh, dw);
+  db = db + du;
+  dxh = du * w;
+  if (GATE && dz_to) {
+    float v[W];
+    dz.get(v);
+    store_vec<W>(dz_to, v);
   }
+}
+// dx = rstd (dxh - a - xh b)
+template <typename T, int W>
+__device__ __forceinline__ void write_dx(T *to, const Vec<W> &dxh, const Vec<W> &xh, float a, float b, float rstd) {
+  float v[W];
+  (Vec<W>(rstd) * fma(xh, Vec<W>(-b), dxh + Vec<W>(-a))).get(v);
+  store_vec<W>(to, v);
 }
 template <typename T, int W, bool GATE>
 __device__ __forceinline__ void load_place(const GnProblem &p, const Slab<T> &s, int row, int col, Raw<T, W> &x,
@@ -433,6 +515,18 @@ __device__ __forceinline__ void load_place(const GnProblem &p, const Slab<T> &s,
   x.load(s.x + row * p.xs + col);
   dy.load(s.dy + row * p.dys + col);
   if (GATE) z.load(s.z + row * p.zs + col);
+}
+
+template <int W>
+__device__ __forceinline__ void keep_params(float (&acc)[2][kThreads * W], const Vec<W> &dw, const Vec<W> &db) {
+  float a[W], b[W];
+  dw.get(a);
+  db.get(b);
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    acc[0][threadIdx.x * W + e] = a[e];
+    acc[1][threadIdx.x * W + e] = b[e];
+  }
 }
 
 // As the forward's teams; dw and db of the block's samples at the end.
@@ -450,13 +544,11 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
   const int turns = (n1 - (int)blockIdx.y * pl.samples_per_block + shares - 1) / shares;
   const float inv = 1.f / ((float)p.m * p.cg);
   const Places<W, NT, V> at(tid, ncol, 0, 0, has ? p.m : 0);
-  float w[W], b[W], dw[W], db[W];  // with at most NT columns a thread keeps one
+  Vec<W> w(0.f), b(0.f), dw(0.f), db(0.f);  // with at most NT columns a thread keeps one
   const int col = at.col[0];
-#pragma unroll
-  for (int e = 0; e < W; ++e) w[e] = dw[e] = db[e] = b[e] = 0.f;
   if (has && at.row[0] >= 0) {
-    load_param<W>(p.w, c0 + col, 1.f, w);
-    load_param<W>(p.b, c0 + col, 0.f, b);
+    w = load_param<W>(p.w, c0 + col, 1.f);
+    b = load_param<W>(p.b, c0 + col, 0.f);
   }
   Raw<T, W> xr, zr, dyr;
   float mean_r = 0.f, rstd_r = 0.f;
@@ -477,39 +569,27 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
     }
     const float mean = mean_r, rstd = rstd_r;
     const Slab<T> s(p, live ? n : 0, has ? g : 0);
-    float dxh[V][W], xh[V][W], sa = 0.f, sb = 0.f;
+    Vec<W> dxh[V], xh[V];
+    float sa = 0.f, sb = 0.f;
 #pragma unroll
     for (int k = 0; k < V; ++k)
       if (live && at.row[k] >= 0) {
-        float dz[W];
         if (V > 1) load_place<T, W, GATE>(p, s, at.row[k], col, xr, zr, dyr);
-        place_grad<T, W, GATE>(p, xr, zr, dyr, w, b, mean, rstd, dxh[k], xh[k], dw, db, dz);
-        if (GATE) store_vec<W>(s.dz + at.row[k] * p.dzs + col, dz);
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          sa += dxh[k][e];
-          sb = fmaf(dxh[k][e], xh[k][e], sb);
-        }
+        place_grad<T, W, GATE>(p, xr, zr, dyr, w, b, mean, rstd, dxh[k], xh[k], dw, db,
+                               s.dz + at.row[k] * p.dzs + col);
+        sa += dxh[k].sum();
+        sb += (dxh[k] * xh[k]).sum();
       }
     if (V == 1) load(n + shares);
-    const float2 ab = team_sum<NT>(sa, sb, red);
-    const float a = ab.x * inv, bb = ab.y * inv;
+    const float2 ab = team_sum2<NT>(sa, sb, red);
 #pragma unroll
     for (int k = 0; k < V; ++k)
-      if (live && at.row[k] >= 0) {
-        float dx[W];
-#pragma unroll
-        for (int e = 0; e < W; ++e) dx[e] = rstd * (dxh[k][e] - a - xh[k][e] * bb);
-        store_vec<W>(s.dx + at.row[k] * p.dxs + col, dx);
-      }
+      if (live && at.row[k] >= 0)
+        write_dx<T, W>(s.dx + at.row[k] * p.dxs + col, dxh[k], xh[k], ab.x * inv, ab.y * inv, rstd);
   }
   if (!dwp) return;
   // the threads of a block that hold the same channels: a team's row phases, then the teams of a group
-#pragma unroll
-  for (int e = 0; e < W; ++e) {
-    acc[0][threadIdx.x * W + e] = dw[e];
-    acc[1][threadIdx.x * W + e] = db[e];
-  }
+  keep_params<W>(acc, dw, db);
   __syncthreads();
   const int phases = V == 1 ? 1 : NT / ncol;
   for (int e = threadIdx.x; e < gpb * p.cg; e += kThreads) {
@@ -539,37 +619,30 @@ __global__ void __launch_bounds__(kThreads) tile_sums_kernel(GnProblem p, GnPlan
   const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg, ncol = p.cg / W;
   const Slab<T> s(p, n, g);
   const float mean = __ldg(p.mean + n * p.G + g), rstd = __ldg(p.rstd + n * p.G + g);
-  float dw[W], db[W], sa = 0.f, sb = 0.f;
+  Raw<T, W> xr[V], zr[V], dyr[V];
 #pragma unroll
-  for (int e = 0; e < W; ++e) dw[e] = db[e] = 0.f;
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) load_place<T, W, GATE>(p, s, at.row[k], at.col[k], xr[k], zr[k], dyr[k]);
+  Vec<W> dw(0.f), db(0.f);
+  float sa = 0.f, sb = 0.f;
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0) {
-      float w[W], b[W], dxh[W], xh[W], dz[W];
-      Raw<T, W> xr, zr, dyr;
-      load_place<T, W, GATE>(p, s, at.row[k], at.col[k], xr, zr, dyr);
-      load_param<W>(p.w, c0 + at.col[k], 1.f, w);
-      load_param<W>(p.b, c0 + at.col[k], 0.f, b);
-      place_grad<T, W, GATE>(p, xr, zr, dyr, w, b, mean, rstd, dxh, xh, dw, db, dz);
-      if (GATE) store_vec<W>(s.dz + at.row[k] * p.dzs + at.col[k], dz);
-#pragma unroll
-      for (int e = 0; e < W; ++e) {
-        sa += dxh[e];
-        sb = fmaf(dxh[e], xh[e], sb);
-      }
+      Vec<W> dxh, xh;
+      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], load_param<W>(p.w, c0 + at.col[k], 1.f),
+                             load_param<W>(p.b, c0 + at.col[k], 0.f), mean, rstd, dxh, xh, dw, db,
+                             s.dz + at.row[k] * p.dzs + at.col[k]);
+      sa += dxh.sum();
+      sb += (dxh * xh).sum();
     }
-  const float2 ab = team_sum<kThreads>(sa, sb, red);
+  const float2 ab = team_sum2<kThreads>(sa, sb, red);
   if (threadIdx.x == 0) {
     float *q = part + 2 * (((size_t)n * p.G + g) * pl.tiles + t);
     q[0] = ab.x;
     q[1] = ab.y;
   }
   if (!dwp) return;
-#pragma unroll
-  for (int e = 0; e < W; ++e) {
-    acc[0][threadIdx.x * W + e] = dw[e];
-    acc[1][threadIdx.x * W + e] = db[e];
-  }
+  keep_params<W>(acc, dw, db);
   __syncthreads();
   const int phases = kThreads / ncol;
   for (int c = threadIdx.x; c < p.cg; c += kThreads) {
@@ -592,6 +665,10 @@ __global__ void __launch_bounds__(kThreads) tile_backward_kernel(GnProblem p, Gn
   const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg;
   const Slab<T> s(p, n, g);
   const float mean = __ldg(p.mean + n * p.G + g), rstd = __ldg(p.rstd + n * p.G + g);
+  Raw<T, W> xr[V], zr[V], dyr[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) load_place<T, W, GATE>(p, s, at.row[k], at.col[k], xr[k], zr[k], dyr[k]);
   const float *q = part + 2 * ((size_t)n * p.G + g) * pl.tiles;
   float sa = 0.f, sb = 0.f;
   for (int i = threadIdx.x; i < pl.tiles; i += kThreads) {
@@ -599,22 +676,16 @@ __global__ void __launch_bounds__(kThreads) tile_backward_kernel(GnProblem p, Gn
     sb += q[2 * i + 1];
   }
   const float inv = 1.f / ((float)p.m * p.cg);
-  const float2 ab = team_sum<kThreads>(sa, sb, red);
-  const float a = ab.x * inv, bb = ab.y * inv;
+  const float2 ab = team_sum2<kThreads>(sa, sb, red);
+  Vec<W> dw(0.f), db(0.f);
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0) {
-      float w[W], b[W], dxh[W], xh[W], dw[W], db[W], dz[W], dx[W];
-#pragma unroll
-      for (int e = 0; e < W; ++e) dw[e] = db[e] = 0.f;
-      Raw<T, W> xr, zr, dyr;
-      load_place<T, W, GATE>(p, s, at.row[k], at.col[k], xr, zr, dyr);
-      load_param<W>(p.w, c0 + at.col[k], 1.f, w);
-      load_param<W>(p.b, c0 + at.col[k], 0.f, b);
-      place_grad<T, W, GATE>(p, xr, zr, dyr, w, b, mean, rstd, dxh, xh, dw, db, dz);
-#pragma unroll
-      for (int e = 0; e < W; ++e) dx[e] = rstd * (dxh[e] - a - xh[e] * bb);
-      store_vec<W>(s.dx + at.row[k] * p.dxs + at.col[k], dx);
+      Vec<W> dxh, xh;
+      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], load_param<W>(p.w, c0 + at.col[k], 1.f),
+                             load_param<W>(p.b, c0 + at.col[k], 0.f), mean, rstd, dxh, xh, dw, db,
+                             static_cast<T *>(nullptr));
+      write_dx<T, W>(s.dx + at.row[k] * p.dxs + at.col[k], dxh, xh, ab.x * inv, ab.y * inv, rstd);
     }
 }
 
@@ -627,23 +698,20 @@ __global__ void __launch_bounds__(kThreads) param_kernel(GnProblem p, float *dwp
   if (c >= p.C) return;
   const int g = c / p.cg;
   const long long r0 = (long long)blockIdx.x * kParamRows, r1 = min((long long)p.n * p.m, r0 + kParamRows);
-  float w[1], b[1], sw = 0.f, sb = 0.f;
-  load_param<1>(p.w, c, 1.f, w);
-  load_param<1>(p.b, c, 0.f, b);
+  const Vec<1> w = load_param<1>(p.w, c, 1.f), b = load_param<1>(p.b, c, 0.f);
+  Vec<1> sw(0.f), sb(0.f);
   for (long long r = r0; r < r1; ++r) {
     const size_t at = (size_t)(r / p.m) * p.G + g;
-    float x[1], dy[1], z[1], dz;
-    load_vec<1>(static_cast<const T *>(p.x) + r * p.xs + c, x);
-    load_vec<1>(static_cast<const T *>(p.dy) + r * p.dys + c, dy);
-    if (GATE) load_vec<1>(static_cast<const T *>(p.z) + r * p.zs + c, z);
-    const float xh = (x[0] - __ldg(p.mean + at)) * __ldg(p.rstd + at);
-    const float du =
-        activate_grad<GATE>(dy[0], fmaf(xh, w[0], b[0]), GATE ? z[0] : 0.f, p.act == SSD_ACT_SILU, dz);
-    sw = fmaf(du, xh, sw);
-    sb += du;
+    Raw<T, 1> x, z, dy;
+    Vec<1> dxh, xh;
+    x.load(static_cast<const T *>(p.x) + r * p.xs + c);
+    dy.load(static_cast<const T *>(p.dy) + r * p.dys + c);
+    if (GATE) z.load(static_cast<const T *>(p.z) + r * p.zs + c);
+    place_grad<T, 1, GATE>(p, x, z, dy, w, b, __ldg(p.mean + at), __ldg(p.rstd + at), dxh, xh, sw, sb,
+                           static_cast<T *>(nullptr));
   }
-  dwp[(size_t)blockIdx.x * p.C + c] = sw;
-  dbp[(size_t)blockIdx.x * p.C + c] = sb;
+  dwp[(size_t)blockIdx.x * p.C + c] = sw.sum();
+  dbp[(size_t)blockIdx.x * p.C + c] = sb.sum();
 }
 
 // ---------------------------------------------------------------- launches
