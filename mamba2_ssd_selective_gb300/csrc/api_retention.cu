@@ -247,8 +247,11 @@ ssd_status gn_check_inputs(const ssd_group_norm_dims *d, const ssd_group_norm_in
   return SSD_OK;
 }
 
-// whether rows of the tensor allow accesses of 8 channels (16 bytes of bf16, twice 16 of fp32)
-bool gn_vector(const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
+// channels that rows of the tensor allow at once, at most `widest`: 8 (16 bytes of bf16, twice 16 of fp32), 2 or 1
+int gn_width(const void *p, int64_t stride, int eb, int widest) {
+  const int w = aligned(p, 16) && stride % 8 == 0 ? 8 : aligned(p, 2 * eb) && stride % 2 == 0 ? 2 : 1;
+  return w < widest ? w : widest;
+}
 
 GnProblem gn_problem(const ssd_group_norm_dims *d, const ssd_group_norm_inputs *in) {
   GnProblem p{};
@@ -379,9 +382,10 @@ ssd_status ssd_group_norm_forward(const ssd_group_norm_dims *dims, const ssd_gro
   GnProblem p = gn_problem(dims, in);
   if (!workspace || ws_bytes < gn_workspace(p, false)) return SSD_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SSD_ERR_ALIGNMENT;
-  const bool gate = dims->activation == SSD_ACT_GATE;
-  const GnPlan pl = gn_plan(p, false, gn_vector(in->x, in->x_row_stride) && gn_vector(y, y_row_stride) &&
-                                          (!gate || gn_vector(in->z, in->z_row_stride)));
+  const int eb = elem_bytes(dims->dtype);
+  int widest = gn_width(y, y_row_stride, eb, gn_width(in->x, in->x_row_stride, eb, 8));
+  if (dims->activation == SSD_ACT_GATE) widest = gn_width(in->z, in->z_row_stride, eb, widest);
+  const GnPlan pl = gn_plan(p, false, widest);
   p.y = y;
   p.ys = y_row_stride;
   p.mean = mean;
@@ -412,11 +416,12 @@ ssd_status ssd_group_norm_backward(const ssd_group_norm_dims *dims, const ssd_gr
   GnProblem p = gn_problem(dims, in);
   if (!workspace || ws_bytes < gn_workspace(p, true)) return SSD_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SSD_ERR_ALIGNMENT;
-  const bool gate = dims->activation == SSD_ACT_GATE;
-  const GnPlan pl =
-      gn_plan(p, true, gn_vector(in->x, in->x_row_stride) && gn_vector(dy, dy_row_stride) &&
-                           gn_vector(grads->dx, grads->dx_row_stride) &&
-                           (!gate || (gn_vector(in->z, in->z_row_stride) && gn_vector(grads->dz, grads->dz_row_stride))));
+  const int eb = elem_bytes(dims->dtype);
+  int widest = gn_width(in->x, in->x_row_stride, eb, gn_width(dy, dy_row_stride, eb, 8));
+  widest = gn_width(grads->dx, grads->dx_row_stride, eb, widest);
+  if (dims->activation == SSD_ACT_GATE)
+    widest = gn_width(in->z, in->z_row_stride, eb, gn_width(grads->dz, grads->dz_row_stride, eb, widest));
+  const GnPlan pl = gn_plan(p, true, widest);
   p.dy = dy;
   p.dys = dy_row_stride;
   p.mean = const_cast<float *>(mean);  // read only on this path

@@ -8,16 +8,16 @@ namespace {
 
 constexpr int kSms = 152;
 
-// Partials of one channel, 8 threads a channel: thread q adds partials q, q + 8, ... in order, then
-// the 8 sums are added in order.
-constexpr int kSumLanes = 8, kSumCols = gn::kThreads / kSumLanes;
+// Partials of one channel, 16 threads a channel: thread q adds partials q, q + 16, ... in order, then
+// the 16 sums are added in order.
+constexpr int kSumLanes = 16, kSumCols = gn::kThreads / kSumLanes;
 __global__ void __launch_bounds__(gn::kThreads) param_sum_kernel(int C, int partials, const float *__restrict__ dwp,
                                                                  const float *__restrict__ dbp, float *dw, float *db) {
   __shared__ float acc[2][kSumLanes][kSumCols];
   const int cl = threadIdx.x % kSumCols, q = threadIdx.x / kSumCols, c = blockIdx.x * kSumCols + cl;
   float sw = 0.f, sb = 0.f;
   if (c < C) {
-#pragma unroll 4
+#pragma unroll 8
     for (int t = q; t < partials; t += kSumLanes) {
       sw += dwp[(size_t)t * C + c];
       sb += dbp[(size_t)t * C + c];
@@ -45,10 +45,10 @@ void launch_gn_param_sum(int C, int partials, const float *dwp, const float *dbp
   param_sum_kernel<<<(C + kSumCols - 1) / kSumCols, gn::kThreads, 0, s>>>(C, partials, dwp, dbp, dw, db);
 }
 
-GnPlan gn_plan(const GnProblem &p, bool backward, bool vectors) {
+GnPlan gn_plan(const GnProblem &p, bool backward, int widest) {
   GnPlan pl{};
-  pl.vec = vectors && p.cg % 8 == 0 ? 8 : 1;
-  const int ncol = p.cg / pl.vec, block_places = pl.vec == 8 ? 4 : 8;
+  pl.vec = widest >= 8 && p.cg % 8 == 0 ? 8 : widest >= 2 && p.cg % 2 == 0 ? 2 : 1;
+  const int ncol = p.cg / pl.vec, block_places = pl.vec == 8 ? 4 : 12;
   // the narrowest team that holds a group; backward teams also need a thread to keep its column
   if (pl.vec == 8 && p.m == 1 && ncol <= 32) {
     pl.team = ncol <= 8 ? 8 : ncol <= 16 ? 16 : 32;
@@ -73,7 +73,8 @@ GnPlan gn_plan(const GnProblem &p, bool backward, bool vectors) {
     pl.groups_per_block = teams < p.G ? teams : p.G;
     // blocks that fill the GPU a few times over, but no fewer samples than a block's teams take at once
     const long long gblocks = (p.G + pl.groups_per_block - 1) / pl.groups_per_block, shares = teams / pl.groups_per_block;
-    const long long want = (backward ? 8 : 32) * kSms;  // a backward block writes a partial dw and db row
+    // (a backward block writes a partial row of dw and db, and as many are resident at once)
+    const long long want = (backward ? (pl.places == 1 ? 3 : 2) : 8) * kSms;
     long long per = (p.n * gblocks + want - 1) / want;
     per = (per + shares - 1) / shares * shares;
     while ((p.n + per - 1) / per > 65535) per *= 2;
@@ -97,8 +98,12 @@ GnPlan gn_plan(const GnProblem &p, bool backward, bool vectors) {
 }
 
 size_t gn_workspace(const GnProblem &p, bool backward) {
-  const size_t a = gn_plan(p, backward, true).total, b = gn_plan(p, backward, false).total;
-  return a > b ? a : b;
+  size_t most = 0;
+  for (int widest : {8, 2, 1}) {
+    const size_t t = gn_plan(p, backward, widest).total;
+    if (t > most) most = t;
+  }
+  return most;
 }
 
 }  // namespace ssd

@@ -18,6 +18,8 @@
 // dw and db are sums of per-block partials in a fixed order.
 #pragma once
 
+#include <type_traits>
+
 #include "group_norm.h"
 #include "sm100.cuh"
 
@@ -37,6 +39,10 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float (&v)[W]) 
       v[2 * i] = __uint_as_float(w[i] << 16);
       v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+  } else if constexpr (W == 2) {
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(p));
+    v[0] = __uint_as_float(u << 16);
+    v[1] = __uint_as_float(u & 0xffff0000u);
   } else {
     v[0] = __bfloat162float(*p);
   }
@@ -52,6 +58,10 @@ __device__ __forceinline__ void load_vec(const float *p, float (&v)[W]) {
       v[i + 2] = a.z;
       v[i + 3] = a.w;
     }
+  } else if constexpr (W == 2) {
+    const float2 a = __ldg(reinterpret_cast<const float2 *>(p));
+    v[0] = a.x;
+    v[1] = a.y;
   } else {
     v[0] = __ldg(p);
   }
@@ -95,6 +105,8 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&v)[W])
       w[i] = *reinterpret_cast<uint32_t *>(&h);
     }
     *reinterpret_cast<uint4 *>(p) = u;
+  } else if constexpr (W == 2) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
   } else {
     *p = __float2bfloat16_rn(v[0]);
   }
@@ -104,6 +116,8 @@ __device__ __forceinline__ void store_vec(float *p, const float (&v)[W]) {
   if constexpr (W == 8) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else if constexpr (W == 2) {
+    *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
   } else {
     p[0] = v[0];
   }
@@ -517,6 +531,37 @@ __device__ __forceinline__ void load_place(const GnProblem &p, const Slab<T> &s,
   if (GATE) z.load(s.z + row * p.zs + col);
 }
 
+// dw and db of a block's `channels` channels: each is held by `holders` threads (thread_of(channel, holder), element
+// channel % W of theirs) and added over them in a fixed order: in up to kThreads / channels runs, then the runs.
+template <int W, class TH, class WR>
+__device__ __forceinline__ void sum_params(float (&acc)[2][kThreads * W], int channels, int holders, TH thread_of,
+                                           WR write) {
+  __shared__ float run[2][kThreads];
+  __syncthreads();
+  const int runs = min(holders, max(1, kThreads / channels)), per = (holders + runs - 1) / runs;
+  for (int c0 = 0; c0 < channels; c0 += kThreads) {
+    const int c = c0 + threadIdx.x % min(channels, kThreads), q = threadIdx.x / min(channels, kThreads);
+    float sw = 0.f, sb = 0.f;
+    if (c < channels && q < runs)
+      for (int j = q * per; j < min(holders, (q + 1) * per); ++j) {
+        const int at = thread_of(c, j) * W + c % W;
+        sw += acc[0][at];
+        sb += acc[1][at];
+      }
+    if (runs > 1) {  // then all channels are in this one turn
+      run[0][threadIdx.x] = sw;
+      run[1][threadIdx.x] = sb;
+      __syncthreads();
+      if (q == 0)
+        for (int i = 1; i < runs; ++i) {
+          sw += run[0][i * channels + c];
+          sb += run[1][i * channels + c];
+        }
+    }
+    if (q == 0 && c < channels) write(c, sw, sb);
+  }
+}
+
 template <int W>
 __device__ __forceinline__ void keep_params(float (&acc)[2][kThreads * W], const Vec<W> &dw, const Vec<W> &db) {
   float a[W], b[W];
@@ -588,24 +633,19 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
         write_dx<T, W>(s.dx + at.row[k] * p.dxs + col, dxh[k], xh[k], ab.x * inv, ab.y * inv, rstd);
   }
   if (!dwp) return;
-  // the threads of a block that hold the same channels: a team's row phases, then the teams of a group
+  // the threads of a block that hold the same channels: the teams of a group, each team's row phases
   keep_params<W>(acc, dw, db);
-  __syncthreads();
   const int phases = V == 1 ? 1 : NT / ncol;
-  for (int e = threadIdx.x; e < gpb * p.cg; e += kThreads) {
-    const int q = e / p.cg, c = e % p.cg;
-    if (blockIdx.x * gpb + q >= p.G) continue;
-    float sw = 0.f, sb = 0.f;
-    for (int sh = 0; sh < shares; ++sh)
-      for (int ph = 0; ph < phases; ++ph) {
-        const int th = (sh * gpb + q) * NT + ph * ncol + c / W;
-        sw += acc[0][th * W + c % W];
-        sb += acc[1][th * W + c % W];
-      }
-    const size_t to = (size_t)blockIdx.y * p.C + (blockIdx.x * gpb + q) * p.cg + c;
-    dwp[to] = sw;
-    dbp[to] = sb;
-  }
+  sum_params<W>(
+      acc, gpb * p.cg, shares * phases,
+      [&](int c, int j) { return (j / phases * gpb + c / p.cg) * NT + j % phases * ncol + c % p.cg / W; },
+      [&](int c, float sw, float sb) {
+        const int ch = blockIdx.x * gpb * p.cg + c;
+        if (ch < p.C) {
+          dwp[(size_t)blockIdx.y * p.C + ch] = sw;
+          dbp[(size_t)blockIdx.y * p.C + ch] = sb;
+        }
+      });
 }
 
 // Tiles, first kernel: the tile's parts of A and B, of dw and db (when a thread keeps its column), and dz.
@@ -643,18 +683,13 @@ __global__ void __launch_bounds__(kThreads) tile_sums_kernel(GnProblem p, GnPlan
   }
   if (!dwp) return;
   keep_params<W>(acc, dw, db);
-  __syncthreads();
-  const int phases = kThreads / ncol;
-  for (int c = threadIdx.x; c < p.cg; c += kThreads) {
-    float sw = 0.f, sd = 0.f;
-    for (int ph = 0; ph < phases; ++ph) {
-      sw += acc[0][(ph * ncol + c / W) * W + c % W];
-      sd += acc[1][(ph * ncol + c / W) * W + c % W];
-    }
-    const size_t to = ((size_t)n * pl.tiles + t) * p.C + c0 + c;
-    dwp[to] = sw;
-    dbp[to] = sd;
-  }
+  sum_params<W>(
+      acc, p.cg, kThreads / ncol, [&](int c, int j) { return j * ncol + c / W; },
+      [&](int c, float sw, float sd) {
+        const size_t to = ((size_t)n * pl.tiles + t) * p.C + c0 + c;
+        dwp[to] = sw;
+        dbp[to] = sd;
+      });
 }
 
 template <typename T, int W, int V, bool GATE>
@@ -715,22 +750,26 @@ __global__ void __launch_bounds__(kThreads) param_kernel(GnProblem p, float *dwp
 }
 
 // ---------------------------------------------------------------- launches
-// f(W, NT, V) for the plan's variant
+template <int X> using Int = std::integral_constant<int, X>;
+// f(W, NT, V) for the plan's team
 template <class F>
 void with_team(const GnPlan &pl, F f) {
-  using std::integral_constant;
-  auto call = [&](auto w, auto nt, auto v) { f(w, nt, v); };
   if (pl.vec == 8) {
     if (pl.places == 1) {
-      if (pl.team == 8) return call(integral_constant<int, 8>{}, integral_constant<int, 8>{}, integral_constant<int, 1>{});
-      if (pl.team == 16) return call(integral_constant<int, 8>{}, integral_constant<int, 16>{}, integral_constant<int, 1>{});
-      return call(integral_constant<int, 8>{}, integral_constant<int, 32>{}, integral_constant<int, 1>{});
+      if (pl.team == 8) return f(Int<8>{}, Int<8>{}, Int<1>{});
+      if (pl.team == 16) return f(Int<8>{}, Int<16>{}, Int<1>{});
+      return f(Int<8>{}, Int<32>{}, Int<1>{});
     }
-    if (pl.team == 32) return call(integral_constant<int, 8>{}, integral_constant<int, 32>{}, integral_constant<int, 4>{});
-    return call(integral_constant<int, 8>{}, integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    return pl.team == 32 ? f(Int<8>{}, Int<32>{}, Int<4>{}) : f(Int<8>{}, Int<256>{}, Int<4>{});
   }
-  if (pl.team == 32) return call(integral_constant<int, 1>{}, integral_constant<int, 32>{}, integral_constant<int, 4>{});
-  return call(integral_constant<int, 1>{}, integral_constant<int, 256>{}, integral_constant<int, 8>{});
+  if (pl.vec == 2) return pl.team == 32 ? f(Int<2>{}, Int<32>{}, Int<4>{}) : f(Int<2>{}, Int<256>{}, Int<12>{});
+  return pl.team == 32 ? f(Int<1>{}, Int<32>{}, Int<4>{}) : f(Int<1>{}, Int<256>{}, Int<12>{});
+}
+// f(W, V) for the plan's tiles
+template <class F>
+void with_tile(const GnPlan &pl, F f) {
+  if (pl.vec == 8) return f(Int<8>{}, Int<4>{});
+  return pl.vec == 2 ? f(Int<2>{}, Int<12>{}) : f(Int<1>{}, Int<12>{});
 }
 
 template <typename T, bool GATE>
@@ -747,13 +786,11 @@ void forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
   }
   float *part = reinterpret_cast<float *>(ws + pl.part);
   const unsigned grid = (unsigned)p.n * pl.tiles * p.G;
-  if (pl.vec == 8) {
-    SSD_LAUNCH("gn_stats", (tile_stats_kernel<T, 8, 4><<<grid, kThreads, 0, s>>>(p, pl, part)));
-    SSD_LAUNCH("gn_forward", (tile_forward_kernel<T, 8, 4, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
-  } else {
-    SSD_LAUNCH("gn_stats", (tile_stats_kernel<T, 1, 8><<<grid, kThreads, 0, s>>>(p, pl, part)));
-    SSD_LAUNCH("gn_forward", (tile_forward_kernel<T, 1, 8, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
-  }
+  with_tile(pl, [&](auto w, auto v) {
+    constexpr int W = decltype(w)::value, V = decltype(v)::value;
+    SSD_LAUNCH("gn_stats", (tile_stats_kernel<T, W, V><<<grid, kThreads, 0, s>>>(p, pl, part)));
+    SSD_LAUNCH("gn_forward", (tile_forward_kernel<T, W, V, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
+  });
 }
 
 template <typename T, bool GATE>
@@ -772,13 +809,11 @@ void backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
   } else {
     float *part = reinterpret_cast<float *>(ws + pl.part);
     const unsigned grid = (unsigned)p.n * pl.tiles * p.G;
-    if (pl.vec == 8) {
-      SSD_LAUNCH("gn_sums", (tile_sums_kernel<T, 8, 4, GATE><<<grid, kThreads, 0, s>>>(p, pl, part, kw, dbp)));
-      SSD_LAUNCH("gn_backward", (tile_backward_kernel<T, 8, 4, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
-    } else {
-      SSD_LAUNCH("gn_sums", (tile_sums_kernel<T, 1, 8, GATE><<<grid, kThreads, 0, s>>>(p, pl, part, kw, dbp)));
-      SSD_LAUNCH("gn_backward", (tile_backward_kernel<T, 1, 8, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
-    }
+    with_tile(pl, [&](auto w, auto v) {
+      constexpr int W = decltype(w)::value, V = decltype(v)::value;
+      SSD_LAUNCH("gn_sums", (tile_sums_kernel<T, W, V, GATE><<<grid, kThreads, 0, s>>>(p, pl, part, kw, dbp)));
+      SSD_LAUNCH("gn_backward", (tile_backward_kernel<T, W, V, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
+    });
   }
   if (!params) return;
   if (!own_columns) {

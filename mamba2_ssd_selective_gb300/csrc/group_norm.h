@@ -17,10 +17,10 @@ struct GnProblem {
   float *dw, *db;      // (C), may be null
 };
 
-// How a call is cut up.  The workspace does not depend on alignments, so it is
-// laid out for either width of accesses.
+// How a call is cut up.  The workspace's size does not depend on alignments: it
+// suffices for any width of accesses.
 struct GnPlan {
-  int vec;                // channels of an access: 8 (16 bytes of bf16) or 1
+  int vec;                // channels of an access: 8 (16 bytes of bf16), 2 or 1
   int team, places;       // threads of a group's team and places of a thread
   int tiles, tile_rows;   // 0: a group fits its team; else tiles of rows of a sample
   bool own_columns;       // a thread keeps one column of channels: dw and db come out of the gradient kernel
@@ -29,8 +29,8 @@ struct GnPlan {
   size_t part, dwp, dbp, total;  // workspace: (n, G, tiles, 2) and (partials, C) fp32 twice
 };
 
-// vectors: whether every tensor of the call allows accesses of 8 channels
-GnPlan gn_plan(const GnProblem &p, bool backward, bool vectors);
+// widest: channels that every tensor of the call allows at once (8, 2 or 1)
+GnPlan gn_plan(const GnProblem &p, bool backward, int widest);
 size_t gn_workspace(const GnProblem &p, bool backward);
 template <typename T> void run_gn_forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s);
 template <typename T> void run_gn_backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s);
