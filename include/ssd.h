@@ -315,7 +315,7 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_line
  *     u = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps)   (var: the mean squared deviation)
  *     y = u (SSD_ACT_NONE), u sigmoid(u) (SSD_ACT_SILU), u z sigmoid(z) (SSD_ACT_GATE, z a tensor like x)
  * nrows = 1 is the norm of each head of each token that retention uses.  weight and bias (channels) fp32, or NULL
- * (1 and 0).  mean and rstd (nsamples, groups) fp32 are written by the forward pass (each may be NULL) and read by
+ * (1 and 0).  Row strides below 2^31 elements.  mean and rstd (nsamples, groups) fp32 are written by the forward pass (each may be NULL) and read by
  * the backward pass.  Any number of channels per group; rows of 16-byte aligned tensors whose strides and group
  * widths are multiples of 8 elements move as 16-byte vectors, others element by element. Statistics are summed
  * in fp32 as deviations (no difference of large sums). */

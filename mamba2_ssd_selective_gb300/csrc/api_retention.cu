@@ -229,6 +229,7 @@ ssd_status gn_check_dims(const ssd_group_norm_dims *d) {
 ssd_status gn_check_rows(const ssd_group_norm_dims *d, const void *p, int64_t stride) {
   if (!p) return SSD_ERR_NULL_PTR;
   if (stride < d->channels) return SSD_ERR_INVALID_DIMS;
+  if (stride > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   return aligned(p, elem_bytes(d->dtype)) ? SSD_OK : SSD_ERR_ALIGNMENT;
 }
 
@@ -263,9 +264,9 @@ GnProblem gn_problem(const ssd_group_norm_dims *d, const ssd_group_norm_inputs *
   p.act = d->activation;
   if (in) {
     p.x = in->x;
-    p.xs = in->x_row_stride;
+    p.xs = (int)in->x_row_stride;
     p.z = in->z;
-    p.zs = in->z_row_stride;
+    p.zs = (int)in->z_row_stride;
     p.w = in->weight;
     p.b = in->bias;
     p.eps = in->eps;
@@ -387,7 +388,7 @@ ssd_status ssd_group_norm_forward(const ssd_group_norm_dims *dims, const ssd_gro
   if (dims->activation == SSD_ACT_GATE) widest = gn_width(in->z, in->z_row_stride, eb, widest);
   const GnPlan pl = gn_plan(p, false, widest);
   p.y = y;
-  p.ys = y_row_stride;
+  p.ys = (int)y_row_stride;
   p.mean = mean;
   p.rstd = rstd;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -423,13 +424,13 @@ ssd_status ssd_group_norm_backward(const ssd_group_norm_dims *dims, const ssd_gr
     widest = gn_width(in->z, in->z_row_stride, eb, gn_width(grads->dz, grads->dz_row_stride, eb, widest));
   const GnPlan pl = gn_plan(p, true, widest);
   p.dy = dy;
-  p.dys = dy_row_stride;
+  p.dys = (int)dy_row_stride;
   p.mean = const_cast<float *>(mean);  // read only on this path
   p.rstd = const_cast<float *>(rstd);
   p.dx = grads->dx;
-  p.dxs = grads->dx_row_stride;
+  p.dxs = (int)grads->dx_row_stride;
   p.dz = grads->dz;
-  p.dzs = grads->dz_row_stride;
+  p.dzs = (int)grads->dz_row_stride;
   p.dw = grads->dweight;
   p.db = grads->dbias;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

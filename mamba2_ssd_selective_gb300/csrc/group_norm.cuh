@@ -12,13 +12,17 @@
 // warp, or a block) is read once: its mean, then its squared deviations, are
 // summed from registers.  With one row to a sample, a team is the narrowest
 // part of a warp that spans the group.  A larger group is cut into tiles of
-// rows: a first kernel gives each tile's count, mean and squared deviations (or
-// its part of A and B, and dz), a second one joins them, in order, and reads the
-// tile again, from L2 where the tensor fits it.
+// rows, a block each.  Up to eight tiles are a cluster, whose blocks keep their
+// tile in registers while they exchange its mean and squared deviations (or its
+// part of A and B) through distributed shared memory.  Beyond that a first kernel
+// writes what a tile gives, and dz, and a second one joins the tiles, in order,
+// and reads its own again, from L2 where the tensor fits it.
 // dw and db are sums of per-block partials in a fixed order.
 #pragma once
 
 #include <type_traits>
+
+#include <cooperative_groups.h>
 
 #include "group_norm.h"
 #include "sm100.cuh"
@@ -211,12 +215,13 @@ __device__ __forceinline__ Vec<W> load_param(const float *p, int c, float none) 
 }
 
 // ---------------------------------------------------------------- sums over a team of NT threads
+// (`fresh`: the scratch has not been used since a barrier)
 template <int NT>
-__device__ __forceinline__ float team_sum(float a, float *scratch) {
+__device__ __forceinline__ float team_sum(float a, float *scratch, bool fresh = false) {
 #pragma unroll
   for (int o = (NT < 32 ? NT : 32) / 2; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   if constexpr (NT > 32) {
-    __syncthreads();
+    if (!fresh) __syncthreads();
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = a;
     __syncthreads();
     a = 0.f;
@@ -227,14 +232,14 @@ __device__ __forceinline__ float team_sum(float a, float *scratch) {
 }
 // two sums at once; scratch of 16 values
 template <int NT>
-__device__ __forceinline__ float2 team_sum2(float a, float b, float *scratch) {
+__device__ __forceinline__ float2 team_sum2(float a, float b, float *scratch, bool fresh = false) {
 #pragma unroll
   for (int o = (NT < 32 ? NT : 32) / 2; o >= 1; o >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, o);
     b += __shfl_xor_sync(0xffffffffu, b, o);
   }
   if constexpr (NT > 32) {
-    __syncthreads();
+    if (!fresh) __syncthreads();
     if ((threadIdx.x & 31) == 0) {
       scratch[threadIdx.x >> 5] = a;
       scratch[8 + (threadIdx.x >> 5)] = b;
@@ -284,22 +289,24 @@ inline long long rows_of_team(int ncol, int nt, int v) {
   return ncol <= nt ? (long long)v * (nt / ncol) : (long long)v * nt / ncol;
 }
 // Tile t of a group: rows [t tile_rows, ...) or, where a row has more columns than a block has threads,
-// vectors [t V NT, ...); and its number of values.
+// vectors [t V NT, ...); and its number of values.  (A cluster's last blocks may have no tile: no rows.)
 template <int W, int V>
 struct Tile {
   int n, g, t;
   Places<W, kThreads, V> at;
   __device__ __forceinline__ Tile(const GnProblem &p, const GnPlan &pl)
-      : n(blockIdx.x / p.G / pl.tiles), g(blockIdx.x % p.G), t(blockIdx.x / p.G % pl.tiles),
+      : n(pl.cluster ? blockIdx.x / pl.cluster / p.G : blockIdx.x / p.G / pl.tiles),
+        g(pl.cluster ? blockIdx.x / pl.cluster % p.G : blockIdx.x % p.G),
+        t(pl.cluster ? blockIdx.x % pl.cluster : blockIdx.x / p.G % pl.tiles),
         at(threadIdx.x, p.cg / W, t * pl.tile_rows, (long long)t * (V * kThreads), limit(p, pl)) {}
   // (in rows mode a thread's last places may lie in the next tile)
   __device__ __forceinline__ int limit(const GnProblem &p, const GnPlan &pl) const {
     return pl.own_columns ? min(p.m, (t + 1) * pl.tile_rows) : p.m;
   }
   static __device__ __forceinline__ float count(const GnProblem &p, const GnPlan &pl, int i) {
-    if (pl.own_columns) return (float)min(pl.tile_rows, p.m - i * pl.tile_rows) * p.cg;
+    if (pl.own_columns) return (float)max(0, min(pl.tile_rows, p.m - i * pl.tile_rows)) * p.cg;
     const long long left = (long long)p.m * (p.cg / W) - (long long)i * (V * kThreads);
-    return (float)(left < V * kThreads ? left : V * kThreads) * W;
+    return (float)max(0LL, left < V * kThreads ? left : (long long)(V * kThreads)) * W;
   }
 };
 
@@ -319,6 +326,8 @@ __device__ __forceinline__ Vec<W> activate_grad(const Vec<W> &dy, const Vec<W> &
   }
   return silu ? dy * silu_grad(u, sigmoid(u)) : dy;
 }
+
+__device__ __forceinline__ long long off(int row, int stride) { return (long long)row * stride; }
 
 // one group of one sample: pointers to its first row's first channel
 template <typename T>
@@ -343,7 +352,7 @@ __device__ __forceinline__ void write_y(const GnProblem &p, const Slab<T> &s, in
   const Vec<W> u = fma((x + Vec<W>(-mean)) * Vec<W>(rstd), w, b);
   float y[W];
   activate<W, GATE>(u, GATE ? vec_of<T, W>(z) : u, p.act == SSD_ACT_SILU).get(y);
-  store_vec<W>(s.y + row * p.ys + col, y);
+  store_vec<W>(s.y + off(row, p.ys) + col, y);
 }
 // sum of (x - mean)^2
 template <int W>
@@ -382,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 4 : 3
 #pragma unroll
     for (int k = 0; k < V; ++k)
       if (has && n < n1 && at.row[k] >= 0) {
-        xr[k].load(s.x + at.row[k] * p.xs + at.col[k]);
-        if (GATE) zr[k].load(s.z + at.row[k] * p.zs + at.col[k]);
+        xr[k].load(s.x + off(at.row[k], p.xs) + at.col[k]);
+        if (GATE) zr[k].load(s.z + off(at.row[k], p.zs) + at.col[k]);
       } else {
         xr[k].clear();
       }
@@ -427,6 +436,26 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 4 : 3
   }
 }
 
+// weight and bias of a thread's places: loaded once where it keeps its column
+template <int W>
+struct Params {
+  Vec<W> wv, bv;
+  bool own;
+  __device__ __forceinline__ Params(const GnProblem &p, const GnPlan &pl, int c0, int col, bool live)
+      : wv(1.f), bv(0.f), own(pl.own_columns) {
+    if (own && live) {
+      wv = load_param<W>(p.w, c0 + col, 1.f);
+      bv = load_param<W>(p.b, c0 + col, 0.f);
+    }
+  }
+  __device__ __forceinline__ Vec<W> w(const GnProblem &p, int c0, int col) const {
+    return own ? wv : load_param<W>(p.w, c0 + col, 1.f);
+  }
+  __device__ __forceinline__ Vec<W> b(const GnProblem &p, int c0, int col) const {
+    return own ? bv : load_param<W>(p.b, c0 + col, 0.f);
+  }
+};
+
 // ---------------------------------------------------------------- forward, groups in tiles of rows
 // Block (tile, group, sample): the tile's count, mean and squared deviations, joined over the threads
 // as pairs (each thread's from its own values, twice over registers).
@@ -441,7 +470,7 @@ __global__ void __launch_bounds__(kThreads) tile_stats_kernel(GnProblem p, GnPla
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0)
-      xr[k].load(s.x + at.row[k] * p.xs + at.col[k]);
+      xr[k].load(s.x + off(at.row[k], p.xs) + at.col[k]);
     else
       xr[k].clear();
   float sum = 0.f, dev = 0.f;
@@ -459,6 +488,82 @@ __global__ void __launch_bounds__(kThreads) tile_stats_kernel(GnProblem p, GnPla
   }
 }
 
+// The joined mean and 1 / sqrt(variance + eps) of a group's tiles, whose own means and squared deviations come
+// from get(tile): the tiles' means by their counts, then the deviations about the joined mean.  A warp's lanes take
+// up to 32 tiles, each warp for itself; more go to the block's threads.
+template <int W, int V, class GET>
+__device__ __forceinline__ float2 join_stats(const GnProblem &p, const GnPlan &pl, float *red, GET get) {
+  const float inv = 1.f / ((float)p.m * p.cg);
+  if (pl.tiles <= 32) {
+    const int i = threadIdx.x & 31;
+    const float2 q = i < pl.tiles ? get(i) : make_float2(0.f, 0.f);
+    const float c = i < pl.tiles ? Tile<W, V>::count(p, pl, i) : 0.f, base = __shfl_sync(0xffffffffu, q.x, 0);
+    const float off = team_sum<32>((q.x - base) * c, red) * inv, d = (q.x - base) - off;
+    return make_float2(base + off, 1.f / sqrtf(team_sum<32>(fmaf(d * d, c, q.y), red) * inv + p.eps));
+  }
+  const float base = get(0).x;
+  float sum = 0.f, dev = 0.f;
+  for (int i = threadIdx.x; i < pl.tiles; i += kThreads) sum += (get(i).x - base) * Tile<W, V>::count(p, pl, i);
+  const float off = team_sum<kThreads>(sum, red) * inv;
+  for (int i = threadIdx.x; i < pl.tiles; i += kThreads) {
+    const float2 q = get(i);
+    const float d = (q.x - base) - off;
+    dev += fmaf(d * d, Tile<W, V>::count(p, pl, i), q.y);
+  }
+  return make_float2(base + off, 1.f / sqrtf(team_sum<kThreads>(dev, red) * inv + p.eps));
+}
+
+// Before a block of a cluster ends, the others have to have read its shared memory: they arrive after their
+// reads (which orders nothing else: no waiting for stores) and wait at their end.
+__device__ __forceinline__ void cluster_done_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
+__device__ __forceinline__ void cluster_done_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+// A cluster of blocks per group: loaded once, the tiles' statistics exchanged between the blocks.
+template <typename T, int W, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads) cluster_forward_kernel(GnProblem p, GnPlan pl) {
+  namespace cg = cooperative_groups;
+  __shared__ float red[2][8];
+  __shared__ float2 mine;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const Tile<W, V> tile(p, pl);
+  const Places<W, kThreads, V> &at = tile.at;
+  const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg;
+  const Slab<T> s(p, n, g);
+  const Params<W> params(p, pl, c0, at.col[0], at.row[0] >= 0);
+  Raw<T, W> xr[V], zr[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) {
+      xr[k].load(s.x + off(at.row[k], p.xs) + at.col[k]);
+      if (GATE) zr[k].load(s.z + off(at.row[k], p.zs) + at.col[k]);
+    } else {
+      xr[k].clear();
+    }
+  float sum = 0.f, dev = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) sum += vec_of<T, W>(xr[k]).sum();
+  const float own = team_sum<kThreads>(sum, red[0], true) / fmaxf(Tile<W, V>::count(p, pl, t), 1.f);
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) dev += deviations<W>(vec_of<T, W>(xr[k]), own);
+  dev = team_sum<kThreads>(dev, red[1], true);
+  if (threadIdx.x == 0) mine = make_float2(own, dev);
+  cluster.sync();
+  const float2 st = join_stats<W, V>(p, pl, red[0], [&](int i) { return *cluster.map_shared_rank(&mine, i); });
+  __syncwarp();
+  cluster_done_arrive();
+  if (t == 0 && threadIdx.x == 0) {
+    if (p.mean) p.mean[n * p.G + g] = st.x;
+    if (p.rstd) p.rstd[n * p.G + g] = st.y;
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0)
+      write_y<T, W, GATE>(p, s, at.row[k], at.col[k], params.w(p, c0, at.col[k]), params.b(p, c0, at.col[k]),
+                          vec_of<T, W>(xr[k]), zr[k], st.x, st.y);
+  cluster_done_wait();
+}
+
 template <typename T, int W, int V, bool GATE>
 __global__ void __launch_bounds__(kThreads) tile_forward_kernel(GnProblem p, GnPlan pl, const float *part) {
   __shared__ float red[16];
@@ -466,25 +571,17 @@ __global__ void __launch_bounds__(kThreads) tile_forward_kernel(GnProblem p, GnP
   const Places<W, kThreads, V> &at = tile.at;
   const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg;
   const Slab<T> s(p, n, g);
+  const Params<W> params(p, pl, c0, at.col[0], at.row[0] >= 0);
   Raw<T, W> xr[V], zr[V];
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0) {
-      xr[k].load(s.x + at.row[k] * p.xs + at.col[k]);
-      if (GATE) zr[k].load(s.z + at.row[k] * p.zs + at.col[k]);
+      xr[k].load(s.x + off(at.row[k], p.xs) + at.col[k]);
+      if (GATE) zr[k].load(s.z + off(at.row[k], p.zs) + at.col[k]);
     }
-  // mean of the tiles' means by their counts, then the deviations about it
-  const float *q = part + 2 * ((size_t)n * p.G + g) * pl.tiles;
-  const float inv = 1.f / ((float)p.m * p.cg), base = q[0];
-  float sum = 0.f, dev = 0.f;
-  for (int i = threadIdx.x; i < pl.tiles; i += kThreads)
-    sum += (q[2 * i] - base) * Tile<W, V>::count(p, pl, i);
-  const float off = team_sum<kThreads>(sum, red) * inv, mean = base + off;
-  for (int i = threadIdx.x; i < pl.tiles; i += kThreads) {
-    const float d = (q[2 * i] - base) - off;
-    dev += fmaf(d * d, Tile<W, V>::count(p, pl, i), q[2 * i + 1]);
-  }
-  const float rstd = 1.f / sqrtf(team_sum<kThreads>(dev, red) * inv + p.eps);
+  const float2 *q = reinterpret_cast<const float2 *>(part) + ((size_t)n * p.G + g) * pl.tiles;
+  const float2 st = join_stats<W, V>(p, pl, red, [&](int i) { return q[i]; });
+  const float mean = st.x, rstd = st.y;
   if (t == 0 && threadIdx.x == 0) {
     if (p.mean) p.mean[n * p.G + g] = mean;
     if (p.rstd) p.rstd[n * p.G + g] = rstd;
@@ -492,8 +589,8 @@ __global__ void __launch_bounds__(kThreads) tile_forward_kernel(GnProblem p, GnP
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0)
-      write_y<T, W, GATE>(p, s, at.row[k], at.col[k], load_param<W>(p.w, c0 + at.col[k], 1.f),
-                          load_param<W>(p.b, c0 + at.col[k], 0.f), vec_of<T, W>(xr[k]), zr[k], mean, rstd);
+      write_y<T, W, GATE>(p, s, at.row[k], at.col[k], params.w(p, c0, at.col[k]), params.b(p, c0, at.col[k]),
+                          vec_of<T, W>(xr[k]), zr[k], mean, rstd);
 }
 
 // ---------------------------------------------------------------- backward
@@ -526,9 +623,9 @@ __device__ __forceinline__ void write_dx(T *to, const Vec<W> &dxh, const Vec<W> 
 template <typename T, int W, bool GATE>
 __device__ __forceinline__ void load_place(const GnProblem &p, const Slab<T> &s, int row, int col, Raw<T, W> &x,
                                            Raw<T, W> &z, Raw<T, W> &dy) {
-  x.load(s.x + row * p.xs + col);
-  dy.load(s.dy + row * p.dys + col);
-  if (GATE) z.load(s.z + row * p.zs + col);
+  x.load(s.x + off(row, p.xs) + col);
+  dy.load(s.dy + off(row, p.dys) + col);
+  if (GATE) z.load(s.z + off(row, p.zs) + col);
 }
 
 // dw and db of a block's `channels` channels: each is held by `holders` threads (thread_of(channel, holder), element
@@ -621,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
       if (live && at.row[k] >= 0) {
         if (V > 1) load_place<T, W, GATE>(p, s, at.row[k], col, xr, zr, dyr);
         place_grad<T, W, GATE>(p, xr, zr, dyr, w, b, mean, rstd, dxh[k], xh[k], dw, db,
-                               s.dz + at.row[k] * p.dzs + col);
+                               s.dz + off(at.row[k], p.dzs) + col);
         sa += dxh[k].sum();
         sb += (dxh[k] * xh[k]).sum();
       }
@@ -630,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
 #pragma unroll
     for (int k = 0; k < V; ++k)
       if (live && at.row[k] >= 0)
-        write_dx<T, W>(s.dx + at.row[k] * p.dxs + col, dxh[k], xh[k], ab.x * inv, ab.y * inv, rstd);
+        write_dx<T, W>(s.dx + off(at.row[k], p.dxs) + col, dxh[k], xh[k], ab.x * inv, ab.y * inv, rstd);
   }
   if (!dwp) return;
   // the threads of a block that hold the same channels: the teams of a group, each team's row phases
@@ -659,6 +756,7 @@ __global__ void __launch_bounds__(kThreads) tile_sums_kernel(GnProblem p, GnPlan
   const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg, ncol = p.cg / W;
   const Slab<T> s(p, n, g);
   const float mean = __ldg(p.mean + n * p.G + g), rstd = __ldg(p.rstd + n * p.G + g);
+  const Params<W> params(p, pl, c0, at.col[0], at.row[0] >= 0);
   Raw<T, W> xr[V], zr[V], dyr[V];
 #pragma unroll
   for (int k = 0; k < V; ++k)
@@ -669,9 +767,9 @@ __global__ void __launch_bounds__(kThreads) tile_sums_kernel(GnProblem p, GnPlan
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0) {
       Vec<W> dxh, xh;
-      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], load_param<W>(p.w, c0 + at.col[k], 1.f),
-                             load_param<W>(p.b, c0 + at.col[k], 0.f), mean, rstd, dxh, xh, dw, db,
-                             s.dz + at.row[k] * p.dzs + at.col[k]);
+      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], params.w(p, c0, at.col[k]),
+                             params.b(p, c0, at.col[k]), mean, rstd, dxh, xh, dw, db,
+                             s.dz + off(at.row[k], p.dzs) + at.col[k]);
       sa += dxh.sum();
       sb += (dxh * xh).sum();
     }
@@ -692,6 +790,63 @@ __global__ void __launch_bounds__(kThreads) tile_sums_kernel(GnProblem p, GnPlan
       });
 }
 
+// A cluster of blocks per group: loaded once, the parts of A and B exchanged between the blocks.
+template <typename T, int W, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads) cluster_backward_kernel(GnProblem p, GnPlan pl, float *dwp, float *dbp) {
+  namespace cg = cooperative_groups;
+  __shared__ float red[16];
+  __shared__ float2 mine;
+  __shared__ float acc[2][kThreads * W];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const Tile<W, V> tile(p, pl);
+  const Places<W, kThreads, V> &at = tile.at;
+  const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg, ncol = p.cg / W;
+  const Slab<T> s(p, n, g);
+  const float mean = __ldg(p.mean + n * p.G + g), rstd = __ldg(p.rstd + n * p.G + g);
+  const float inv = 1.f / ((float)p.m * p.cg);
+  const Params<W> params(p, pl, c0, at.col[0], at.row[0] >= 0);
+  Raw<T, W> xr[V], zr[V], dyr[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) load_place<T, W, GATE>(p, s, at.row[k], at.col[k], xr[k], zr[k], dyr[k]);
+  Vec<W> dw(0.f), db(0.f), dxh[V];
+  float sa = 0.f, sb = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0) {
+      Vec<W> xh;
+      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], params.w(p, c0, at.col[k]),
+                             params.b(p, c0, at.col[k]), mean, rstd, dxh[k], xh, dw, db,
+                             s.dz + off(at.row[k], p.dzs) + at.col[k]);
+      sa += dxh[k].sum();
+      sb += (dxh[k] * xh).sum();
+    }
+  const float2 own = team_sum2<kThreads>(sa, sb, red, true);
+  if (threadIdx.x == 0) mine = own;
+  cluster.sync();
+  const int lane = threadIdx.x & 31;  // each warp for itself
+  const float2 q = lane < pl.tiles ? *cluster.map_shared_rank(&mine, lane) : make_float2(0.f, 0.f);
+  const float2 ab = team_sum2<32>(q.x, q.y, red);
+  __syncwarp();
+  cluster_done_arrive();
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (at.row[k] >= 0)
+      write_dx<T, W>(s.dx + off(at.row[k], p.dxs) + at.col[k], dxh[k],
+                     (vec_of<T, W>(xr[k]) + Vec<W>(-mean)) * Vec<W>(rstd), ab.x * inv, ab.y * inv, rstd);
+  if (dwp && t < pl.tiles) {
+    keep_params<W>(acc, dw, db);
+    sum_params<W>(
+        acc, p.cg, kThreads / ncol, [&](int c, int j) { return j * ncol + c / W; },
+        [&](int c, float sw, float sd) {
+          const size_t to = ((size_t)n * pl.tiles + t) * p.C + c0 + c;
+          dwp[to] = sw;
+          dbp[to] = sd;
+        });
+  }
+  cluster_done_wait();
+}
+
 template <typename T, int W, int V, bool GATE>
 __global__ void __launch_bounds__(kThreads) tile_backward_kernel(GnProblem p, GnPlan pl, const float *part) {
   __shared__ float red[16];
@@ -700,6 +855,7 @@ __global__ void __launch_bounds__(kThreads) tile_backward_kernel(GnProblem p, Gn
   const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg;
   const Slab<T> s(p, n, g);
   const float mean = __ldg(p.mean + n * p.G + g), rstd = __ldg(p.rstd + n * p.G + g);
+  const Params<W> params(p, pl, c0, at.col[0], at.row[0] >= 0);
   Raw<T, W> xr[V], zr[V], dyr[V];
 #pragma unroll
   for (int k = 0; k < V; ++k)
@@ -717,10 +873,10 @@ __global__ void __launch_bounds__(kThreads) tile_backward_kernel(GnProblem p, Gn
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0) {
       Vec<W> dxh, xh;
-      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], load_param<W>(p.w, c0 + at.col[k], 1.f),
-                             load_param<W>(p.b, c0 + at.col[k], 0.f), mean, rstd, dxh, xh, dw, db,
+      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], params.w(p, c0, at.col[k]),
+                             params.b(p, c0, at.col[k]), mean, rstd, dxh, xh, dw, db,
                              static_cast<T *>(nullptr));
-      write_dx<T, W>(s.dx + at.row[k] * p.dxs + at.col[k], dxh, xh, ab.x * inv, ab.y * inv, rstd);
+      write_dx<T, W>(s.dx + off(at.row[k], p.dxs) + at.col[k], dxh, xh, ab.x * inv, ab.y * inv, rstd);
     }
 }
 
@@ -772,6 +928,22 @@ void with_tile(const GnPlan &pl, F f) {
   return pl.vec == 2 ? f(Int<2>{}, Int<12>{}) : f(Int<1>{}, Int<12>{});
 }
 
+// a launch of clusters of pl.cluster blocks
+template <class... P, class... A>
+void launch_clusters(void (*kernel)(P...), unsigned grid, const GnPlan &pl, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)pl.cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) note_host_error();
+}
+
 template <typename T, bool GATE>
 void forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
   if (pl.tiles == 0) {
@@ -785,9 +957,13 @@ void forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
     return;
   }
   float *part = reinterpret_cast<float *>(ws + pl.part);
-  const unsigned grid = (unsigned)p.n * pl.tiles * p.G;
+  const unsigned grid = (unsigned)p.n * (pl.cluster ? pl.cluster : pl.tiles) * p.G;
   with_tile(pl, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
+    if (pl.cluster) {
+      SSD_LAUNCH("gn_forward", launch_clusters(cluster_forward_kernel<T, W, V, GATE>, grid, pl, s, p, pl));
+      return;
+    }
     SSD_LAUNCH("gn_stats", (tile_stats_kernel<T, W, V><<<grid, kThreads, 0, s>>>(p, pl, part)));
     SSD_LAUNCH("gn_forward", (tile_forward_kernel<T, W, V, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
   });
@@ -808,9 +984,13 @@ void backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
     });
   } else {
     float *part = reinterpret_cast<float *>(ws + pl.part);
-    const unsigned grid = (unsigned)p.n * pl.tiles * p.G;
+    const unsigned grid = (unsigned)p.n * (pl.cluster ? pl.cluster : pl.tiles) * p.G;
     with_tile(pl, [&](auto w, auto v) {
       constexpr int W = decltype(w)::value, V = decltype(v)::value;
+      if (pl.cluster) {
+        SSD_LAUNCH("gn_backward", launch_clusters(cluster_backward_kernel<T, W, V, GATE>, grid, pl, s, p, pl, kw, dbp));
+        return;
+      }
       SSD_LAUNCH("gn_sums", (tile_sums_kernel<T, W, V, GATE><<<grid, kThreads, 0, s>>>(p, pl, part, kw, dbp)));
       SSD_LAUNCH("gn_backward", (tile_backward_kernel<T, W, V, GATE><<<grid, kThreads, 0, s>>>(p, pl, part)));
     });

@@ -10,7 +10,7 @@ struct GnProblem {
   int act;             // ssd_activation
   const void *x, *z, *dy;
   void *y, *dx, *dz;
-  long long xs, zs, dys, ys, dxs, dzs;  // row strides (elements)
+  int xs, zs, dys, ys, dxs, dzs;  // row strides (elements)
   const float *w, *b;                   // or null: 1 and 0
   float eps;
   float *mean, *rstd;  // (n, G): written by the forward pass (may be null), read by the backward pass
@@ -23,6 +23,7 @@ struct GnPlan {
   int vec;                // channels of an access: 8 (16 bytes of bf16), 2 or 1
   int team, places;       // threads of a group's team and places of a thread
   int tiles, tile_rows;   // 0: a group fits its team; else tiles of rows of a sample
+  int cluster;            // blocks of a cluster that holds a group's tiles, or 0: the tiles are read twice
   bool own_columns;       // a thread keeps one column of channels: dw and db come out of the gradient kernel
   int groups_per_block, samples_per_block;  // of a block of teams
   int partials;           // partial dw / db rows

@@ -151,35 +151,43 @@ def ssd_group_norm_backward(dims, inputs, dy, dy_row_stride, mean, rstd, grads, 
 
 def _rows(x, name: str, rows: int, width: int, dtype, device) -> tuple[int, int]:
     """(address, row stride) of a (..., width) tensor whose leading dimensions flatten to `rows` evenly spaced rows."""
+    strides = x.stride()
+    # the usual case first: a small call's time is mostly spent on the host
+    if len(strides) == 2 and strides[1] == 1 and x.dtype is dtype and x.shape == (rows, width) and x.device == device:
+        return x.data_ptr(), strides[0] if rows > 1 else max(width, strides[0])
     shape = x.shape
     if x.dtype != dtype or x.device != device:
         raise ValueError(f"{name}: expected {dtype} on {device}, got {x.dtype} on {x.device}")
     if x.dim() < 2 or shape[-1] != width or x.numel() != rows * width:
         raise ValueError(f"{name}: expected {rows} rows of {width} channels, got {tuple(shape)}")
-    strides = x.stride()
     if width > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: channels must be contiguous")
-    step, count = strides[-2], shape[-2]
-    if count == 1:
-        step = max(width, step)
-    for i in range(x.dim() - 3, -1, -1):
-        if shape[i] == 1:
+    step, count = 0, 1  # rows seen so far, innermost first, and their spacing
+    for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        if size == 1:
             continue
         if count == 1:
-            step = strides[i]
-        elif strides[i] != step * count:
+            step = stride
+        elif stride != step * count:
             raise ValueError(f"{name}: rows must be evenly spaced")
-        count *= shape[i]
-    return x.data_ptr(), step
+        count *= size
+    return x.data_ptr(), step if count > 1 else width
 
 
 def _exact(x, name: str, shape: tuple, dtype, device):
     if x is None:
         return None
-    if x.dtype != dtype or x.device != device or tuple(x.shape) != shape or not x.is_contiguous():
+    if x.dtype is not dtype or x.shape != shape or x.device != device or not x.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {device}, "
                          f"got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x.data_ptr()
+
+
+def _current(device, stream):
+    """Handle of the given stream, or of the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _device(device) -> torch.device:
@@ -214,6 +222,7 @@ class LinearAttnRunner:
         self._widths = (nheads * headdim_k, self.nheads_kv * headdim_k, self.nheads_kv * headdim_v,
                         nheads * headdim_v)
         self._scale = headdim_k ** -0.5
+        self._heads, self._bounds = (nheads,), (nseq + 1,)
 
     def _inputs(self, q, k, v, log_decay, scale, init, cu) -> SsdLinearAttnInputs:
         wq, wk, wv, _ = self._widths
@@ -223,10 +232,10 @@ class LinearAttnRunner:
         vp, vs = _rows(v, "v", rows, wv, tdtype, device)
         if (cu is not None) != self.packed:
             raise ValueError("cu_seqlens goes with packed=True")
-        return SsdLinearAttnInputs(qp, qs, kp, ks, vp, vs,
-                                   _exact(log_decay, "log_decay", (self.nheads,), torch.float32, device),
-                                   _exact(init, "initial_state", self.state_shape, torch.float32, device),
-                                   _exact(cu, "cu_seqlens", (self.nseq + 1,), torch.int32, device),
+        f32 = torch.float32
+        return SsdLinearAttnInputs(qp, qs, kp, ks, vp, vs, _exact(log_decay, "log_decay", self._heads, f32, device),
+                                   _exact(init, "initial_state", self.state_shape, f32, device),
+                                   _exact(cu, "cu_seqlens", self._bounds, torch.int32, device),
                                    self._scale if scale is None else scale)
 
     def forward(self, q, k, v, log_decay, *, scale=None, initial_state=None, cu_seqlens=None, final_state=True,
@@ -238,7 +247,7 @@ class LinearAttnRunner:
         o = torch.empty(self.rows, wo, dtype=self.tdtype, device=self.device) if out is None else out
         op, os = _rows(o, "out", self.rows, wo, self.tdtype, self.device)
         fin = torch.empty(self.state_shape, dtype=torch.float32, device=self.device) if final_state else None
-        ssd_linear_attn_forward(self.dims, inputs, op, os, fin, self.workspace, stream=stream)
+        ssd_linear_attn_forward(self.dims, inputs, op, os, fin, self.workspace, stream=_current(self.device, stream))
         return o, fin
 
     def backward(self, q, k, v, log_decay, do, *, scale=None, initial_state=None, dfinal_state=None, cu_seqlens=None,
@@ -260,7 +269,7 @@ class LinearAttnRunner:
                                                                               device=device)}
         grads = SsdLinearAttnGrads(g["dq"].data_ptr(), wq, g["dk"].data_ptr(), wk, g["dv"].data_ptr(), wv,
                                    _ptr(g["dinitial_state"]))
-        ssd_linear_attn_backward(self.dims, inputs, dop, dos, dfin, grads, self.workspace, stream=stream)
+        ssd_linear_attn_backward(self.dims, inputs, dop, dos, dfin, grads, self.workspace, stream=_current(self.device, stream))
         return g
 
     def step(self, q, k, v, log_decay, states, *, slot_idx=None, scale=None, out=None, stream=None):
@@ -273,7 +282,7 @@ class LinearAttnRunner:
         idx = _exact(slot_idx, "slot_idx", (self.nseq,), torch.int32, self.device)
         o = torch.empty(self.rows, wo, dtype=self.tdtype, device=self.device) if out is None else out
         op, os = _rows(o, "out", self.rows, wo, self.tdtype, self.device)
-        ssd_linear_attn_step(self.dims, inputs, states, states.shape[0], idx, op, os, stream)
+        ssd_linear_attn_step(self.dims, inputs, states, states.shape[0], idx, op, os, _current(self.device, stream))
         return o
 
 
@@ -313,7 +322,7 @@ class GroupNormRunner:
         yp, ys = self._row(y, "out")
         stats = torch.empty((2,) + self.stat_shape, dtype=torch.float32, device=self.device)
         mean, rstd = stats[0], stats[1]
-        ssd_group_norm_forward(self.dims, inputs, yp, ys, mean, rstd, self.workspace, stream=stream)
+        ssd_group_norm_forward(self.dims, inputs, yp, ys, mean, rstd, self.workspace, stream=_current(self.device, stream))
         return y, mean, rstd
 
     def backward(self, dy, x, weight, bias, mean, rstd, *, z=None, stream=None) -> dict:
@@ -333,5 +342,5 @@ class GroupNormRunner:
              "dbias": torch.empty(self.channels, dtype=torch.float32, device=device)}
         grads = SsdGroupNormGrads(g["dx"].data_ptr(), self.channels, _ptr(g["dz"]), self.channels,
                                   g["dweight"].data_ptr(), g["dbias"].data_ptr())
-        ssd_group_norm_backward(self.dims, inputs, dyp, dys, mp, rp, grads, self.workspace, stream=stream)
+        ssd_group_norm_backward(self.dims, inputs, dyp, dys, mp, rp, grads, self.workspace, stream=_current(self.device, stream))
         return g
