@@ -14,10 +14,14 @@ constexpr int kMaxSeqs = 1 << 20;
 // ---------------------------------------------------------------- linear attention
 
 struct LaPlan {
-  bool split;
-  int seg_len, nunits;
-  size_t status, seg, part, total;  // workspace offsets
+  enum Cut { kWhole, kChained, kSideBySide } cut;
+  bool table;
+  int seg_len, units, passes;
+  size_t status, flags, table_at, seg, part, total;  // workspace offsets
+  size_t seg_bytes;                                  // of one pass
 };
+// words at the start of the workspace: the status, the work counters, the table's number of units
+constexpr int kLaCounters = 16, kLaTableUnits = kLaCounters + kLaCounterWords;
 
 long long la_rows(const ssd_linear_attn_dims *d) {
   return d->packed ? d->total_tokens : (long long)d->nseq * d->seqlen;
@@ -33,7 +37,7 @@ ssd_status la_check_dims(const ssd_linear_attn_dims *d) {
   const long long rows = la_rows(d);
   if (!d->packed && d->total_tokens != 0 && d->total_tokens != rows) return SSD_ERR_INVALID_DIMS;
   if (d->headdim_k % 8 || d->headdim_v % 8 || d->headdim_k > 256 || d->headdim_v > 256 || rows > kMaxRows ||
-      d->nseq > kMaxSeqs || (long long)d->nseq * d->nheads > (1LL << 30) || (long long)d->nheads * d->headdim_k > kMaxChannels ||
+      d->nseq > kMaxSeqs || (long long)d->nseq * d->nheads > (1LL << 28) || (long long)d->nheads * d->headdim_k > kMaxChannels ||
       (long long)d->nheads * d->headdim_v > kMaxChannels)
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
@@ -44,24 +48,46 @@ bool la_use_tc(const ssd_linear_attn_dims *d) {
   return d->dtype == SSD_BF16 && la_tc_envelope(d->headdim_k, d->headdim_v);
 }
 
-// Whether and where sequences are cut, and the workspace.  A cut sequence costs
-// a second read of k and v (the segments' own states) and two more launches, so
-// it is only made when whole sequences leave most of the GPU without work.
+// Whether and where sequences are cut, and the workspace.
+//
+// Cut side by side, a sequence's segments run at once: their own states first (a second
+// read of k and v), a scan, then the pass.  That pays where whole sequences
+// leave at least half of the GPU idle: one sequence of 31991 tokens, 16 heads of 128,
+// takes 950 us whole, 160 us in 9 segments.
+// Chained (tensor cores), segments of all sequences are items of a queue in order of
+// their level, a segment's state handed to the next: nothing is done twice, and SMs
+// that finish early take over.  That pays where there are more sequences than SMs
+// but not a multiple of them, or of different lengths.
 LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
   LaPlan pl{};
   const bool tc = la_use_tc(d);
-  const long long rows = la_rows(d), H = d->nheads, sms = 152;
-  // blocks of a whole sequence, and blocks that fill the GPU (one or four on an SM)
-  const long long blocks = H * (tc ? 1 : (d->headdim_v + 63) / 64), want = tc ? sms : 4 * sms;
+  pl.passes = backward ? 3 : 1;
+  const int wide = d->headdim_k > d->headdim_v ? d->headdim_k : d->headdim_v;
+  const long long rows = la_rows(d), H = d->nheads, n = d->nseq, sms = 152;
+  // blocks of a whole sequence, and blocks that fill the GPU (CUDA cores: 4 resident on an SM, twice over)
+  const long long blocks = H * pl.passes * (tc ? 1 : (wide + 63) / 64), want = tc ? sms : 8 * sms;
   const long long longest = d->packed ? rows : d->seqlen;
-  const long long cuts = want / (d->nseq * blocks);
-  long long seg = d->packed ? rows * blocks / want : cuts > 0 ? (longest + cuts - 1) / cuts : longest;
-  seg = (seg + 63) / 64 * 64;
-  if (seg < 256) seg = 256;
-  pl.split = seg < longest && cuts >= 2;
-  if (!pl.split) seg = (longest + 63) / 64 * 64;
+  long long seg = 0;
+  if (d->packed && n > kLaMaxCutSeqs) {
+    pl.cut = LaPlan::kWhole;
+  } else if (n * blocks >= want) {
+    seg = (rows * blocks / (4 * sms) + 63) / 64 * 64;
+    if (seg < 1024) seg = 1024;
+    const bool fits = (rows / seg + n) * blocks < (1LL << 28);  // item numbers are 32-bit
+    pl.cut = tc && fits && 2 * longest > 3 * seg && (d->packed || n * blocks % sms) ? LaPlan::kChained : LaPlan::kWhole;
+  } else {
+    const long long cuts = want / (n * blocks);
+    seg = d->packed ? rows * blocks / want : (longest + cuts - 1) / cuts;
+    seg = (seg + 63) / 64 * 64;
+    const long long least = tc ? 256 : 64;
+    if (seg < least) seg = least;
+    pl.cut = seg < longest && (cuts >= 2 || d->packed) ? LaPlan::kSideBySide : LaPlan::kWhole;
+  }
+  if (pl.cut == LaPlan::kWhole) seg = (longest + 63) / 64 * 64;
+  const bool cut = pl.cut != LaPlan::kWhole;
   pl.seg_len = (int)seg;
-  pl.nunits = (int)(!pl.split ? d->nseq : d->packed ? rows / seg + d->nseq : d->nseq * ((longest + seg - 1) / seg));
+  pl.table = cut && d->packed;
+  pl.units = (int)(!cut ? n : d->packed ? rows / seg + n : n * ((longest + seg - 1) / seg));
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -69,9 +95,11 @@ LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
     return o;
   };
   pl.status = take(256);
-  pl.seg = take(pl.split ? (size_t)pl.nunits * H * d->headdim_k * d->headdim_v * 4 : 0);
-  const int wide = d->headdim_k > d->headdim_v ? d->headdim_k : d->headdim_v;
-  pl.part = take(backward && d->nheads != d->nheads_kv ? (size_t)rows * H * wide * 4 : 0);
+  pl.flags = take(pl.cut == LaPlan::kChained ? (size_t)pl.passes * pl.units * H * 4 : 0);
+  pl.table_at = take(pl.table ? (size_t)pl.units * sizeof(LaEntry) : 0);
+  pl.seg_bytes = align_up((size_t)pl.units * H * d->headdim_k * d->headdim_v * 4, 256);
+  pl.seg = take(cut ? pl.passes * pl.seg_bytes : 0);
+  pl.part = take(backward && d->nheads != d->nheads_kv ? (size_t)rows * H * (d->headdim_k + d->headdim_v) * 4 : 0);
   pl.total = off;
   return pl;
 }
@@ -105,21 +133,32 @@ ssd_status la_check_workspace(const LaPlan &pl, const void *ws, size_t bytes) {
   return aligned(ws, 256) ? SSD_OK : SSD_ERR_ALIGNMENT;
 }
 
-// what every pass of a call has in common
-LaPass la_base(const ssd_linear_attn_dims *d, const ssd_linear_attn_inputs *in, const LaPlan &pl, char *ws) {
+LaPlanDev la_plan_dev(const ssd_linear_attn_dims *d, const ssd_linear_attn_inputs *in, const LaPlan &pl, char *ws) {
+  LaPlanDev v{};
+  v.nseq = d->nseq;
+  v.seqlen = d->seqlen;
+  v.total = (int)la_rows(d);
+  v.H = d->nheads;
+  v.cu = in->cu_seqlens;
+  v.seg_len = pl.seg_len;
+  v.units = pl.units;
+  v.status = reinterpret_cast<int *>(ws + pl.status);
+  v.counters = v.status + kLaCounters;
+  if (pl.table) {
+    v.table = reinterpret_cast<const LaEntry *>(ws + pl.table_at);
+    v.table_units = v.status + kLaTableUnits;
+  }
+  if (pl.cut == LaPlan::kChained) v.flags = reinterpret_cast<int *>(ws + pl.flags);
+  v.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return v;
+}
+
+// pass i of a call; the tensors, scales and states follow
+LaPass la_pass(const ssd_linear_attn_dims *d, const ssd_linear_attn_inputs *in, const LaPlan &pl, char *ws, int i) {
   LaPass p{};
   p.H = d->nheads;
   p.g = in->log_decay;
-  p.nseq = d->nseq;
-  p.seqlen = d->seqlen;
-  p.total = (int)la_rows(d);
-  p.cu = in->cu_seqlens;
-  p.seg_len = pl.seg_len;
-  p.nunits = pl.nunits;
-  p.split = pl.split;
-  p.seg_state = ws ? reinterpret_cast<float *>(ws + pl.seg) : nullptr;
-  p.status = ws ? reinterpret_cast<int *>(ws + pl.status) : nullptr;
-  p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  p.seg_state = reinterpret_cast<float *>(ws + pl.seg + i * pl.seg_bytes);
   return p;
 }
 
@@ -153,15 +192,32 @@ void la_states(LaPass &p, const float *init, float *fin, bool transposed) {
   p.sb = transposed ? p.dk : 1;
 }
 
+// The passes of a call: status, counters and flags cleared (and the table of units written), then the passes, in
+// batches that share a kernel.
 template <typename T>
-void la_run(const LaPass &p, bool reverse, cudaStream_t s) {
-  const bool tc = sizeof(T) == 2 && la_tc_envelope(p.dk, p.dv);
-  auto pass = [&](bool summary) { tc ? launch_la_tc(p, reverse, summary, s) : launch_la_simt<T>(p, reverse, summary, s); };
-  if (p.split) {
-    SSD_LAUNCH("la_segment_states", pass(true));
-    SSD_LAUNCH("la_scan", launch_la_scan(p, reverse, s));
+void la_run(const ssd_linear_attn_dims *d, const LaPlan &pl, const LaPlanDev &dev, const LaPass *p, int n, char *ws,
+            cudaStream_t s) {
+  const int nflags = pl.cut == LaPlan::kChained ? pl.passes * pl.units * d->nheads : 0;
+  if (pl.table)
+    SSD_LAUNCH("la_table", launch_la_table(dev, reinterpret_cast<LaEntry *>(ws + pl.table_at),
+                                           dev.status + kLaTableUnits, nflags, s));
+  else
+    cudaMemsetAsync(ws, 0, pl.flags + (size_t)nflags * 4, s);
+  const bool tc = sizeof(T) == 2 && la_use_tc(d);
+  for (int done = 0, batch = 0; done < n; ++batch) {
+    LaBatch b{};
+    LaPlanDev v = dev;
+    v.counters += 2 * batch;
+    if (v.flags) v.flags += (size_t)done * pl.units * d->nheads;
+    auto kernel = [](const LaPass &x) { return 4 * la_tc_boxes(x.dk) + 2 * la_tc_boxes(x.dv) + x.o_f32; };
+    while (done < n && (b.n == 0 || !tc || kernel(p[done]) == kernel(b.p[0]))) b.p[b.n++] = p[done++];
+    auto pass = [&](bool summary) { tc ? launch_la_tc(v, b, summary, s) : launch_la_simt<T>(v, b, summary, s); };
+    if (pl.cut == LaPlan::kSideBySide) {
+      SSD_LAUNCH("la_segment_states", pass(true));
+      SSD_LAUNCH("la_scan", launch_la_scan(v, b, s));
+    }
+    SSD_LAUNCH("la_pass", pass(false));
   }
-  SSD_LAUNCH("la_pass", pass(false));
 }
 
 template <typename T>
@@ -172,42 +228,37 @@ ssd_status la_backward_impl(const ssd_linear_attn_dims *d, const ssd_linear_attn
             dv = d->headdim_v;
   const Role q{in->q, in->q_tok_stride, 1, H}, k{in->k, in->k_tok_stride, group, Hkv},
       v{in->v, in->v_tok_stride, group, Hkv}, o{dout, dout_stride, 1, H};
-  float *part = reinterpret_cast<float *>(ws + pl.part);
   const long long rows = la_rows(d);
-  const LaPass base = la_base(d, in, pl, ws);
-
-  LaPass p = base;  // dq
-  la_roles(p, o, v, k, dv, dk);
-  la_states(p, in->initial_states, nullptr, true);
-  p.o_scale = in->scale;
-  p.p_scale = p.st_scale = 1.f;
-  p.o = g->dq;
-  p.os = g->dq_tok_stride;
-  la_run<T>(p, false, s);
-
-  p = base;  // dk
-  la_roles(p, v, o, q, dv, dk);
-  la_states(p, dfinal, nullptr, true);
-  p.p_scale = p.st_scale = in->scale;
-  p.o_scale = 1.f;
-  p.o_f32 = group > 1;
-  p.o = group > 1 ? part : g->dk;
-  p.os = group > 1 ? (long long)H * dk : g->dk_tok_stride;
-  la_run<T>(p, true, s);
-  if (group > 1)
-    SSD_LAUNCH("la_sum_heads", launch_la_sum_heads<T>(part, g->dk, g->dk_tok_stride, rows, Hkv, group, dk, s));
-
-  p = base;  // dv, and the gradient of the initial states
-  la_roles(p, k, q, o, dk, dv);
-  la_states(p, dfinal, g->dinitial_states, false);
-  p.p_scale = p.st_scale = in->scale;
-  p.o_scale = 1.f;
-  p.o_f32 = group > 1;
-  p.o = group > 1 ? part : g->dv;
-  p.os = group > 1 ? (long long)H * dv : g->dv_tok_stride;
-  la_run<T>(p, true, s);
-  if (group > 1)
-    SSD_LAUNCH("la_sum_heads", launch_la_sum_heads<T>(part, g->dv, g->dv_tok_stride, rows, Hkv, group, dv, s));
+  float *part_k = reinterpret_cast<float *>(ws + pl.part), *part_v = part_k + (size_t)rows * H * dk;
+  LaPass p[3] = {la_pass(d, in, pl, ws, 0), la_pass(d, in, pl, ws, 1), la_pass(d, in, pl, ws, 2)};
+  // dq
+  la_roles(p[0], o, v, k, dv, dk);
+  la_states(p[0], in->initial_states, nullptr, true);
+  p[0].o_scale = in->scale;
+  p[0].p_scale = p[0].st_scale = 1.f;
+  p[0].o = g->dq;
+  p[0].os = g->dq_tok_stride;
+  // dk
+  la_roles(p[1], v, o, q, dv, dk);
+  la_states(p[1], dfinal, nullptr, true);
+  p[1].o = group > 1 ? part_k : g->dk;
+  p[1].os = group > 1 ? (long long)H * dk : g->dk_tok_stride;
+  // dv, and the gradient of the initial states
+  la_roles(p[2], k, q, o, dk, dv);
+  la_states(p[2], dfinal, g->dinitial_states, false);
+  p[2].o = group > 1 ? part_v : g->dv;
+  p[2].os = group > 1 ? (long long)H * dv : g->dv_tok_stride;
+  for (int i = 1; i < 3; ++i) {
+    p[i].reverse = true;
+    p[i].o_scale = 1.f;
+    p[i].p_scale = p[i].st_scale = in->scale;
+    p[i].o_f32 = group > 1;
+  }
+  la_run<T>(d, pl, la_plan_dev(d, in, pl, ws), p, 3, ws, s);
+  if (group > 1) {
+    SSD_LAUNCH("la_sum_heads", launch_la_sum_heads<T>(part_k, g->dk, g->dk_tok_stride, rows, Hkv, group, dk, s));
+    SSD_LAUNCH("la_sum_heads", launch_la_sum_heads<T>(part_v, g->dv, g->dv_tok_stride, rows, Hkv, group, dv, s));
+  }
   return launch_status();
 }
 
@@ -296,7 +347,8 @@ ssd_status ssd_linear_attn_forward(const ssd_linear_attn_dims *dims, const ssd_l
   if (st != SSD_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int group = dims->nheads / dims->nheads_kv;
-  LaPass p = la_base(dims, in, pl, static_cast<char *>(workspace));
+  char *ws = static_cast<char *>(workspace);
+  LaPass p = la_pass(dims, in, pl, ws, 0);
   la_roles(p, Role{in->q, in->q_tok_stride, 1, dims->nheads}, Role{in->k, in->k_tok_stride, group, dims->nheads_kv},
            Role{in->v, in->v_tok_stride, group, dims->nheads_kv}, dims->headdim_k, dims->headdim_v);
   la_states(p, in->initial_states, final_states, false);
@@ -304,11 +356,11 @@ ssd_status ssd_linear_attn_forward(const ssd_linear_attn_dims *dims, const ssd_l
   p.p_scale = p.st_scale = 1.f;
   p.o = o;
   p.os = o_tok_stride;
-  cudaMemsetAsync(p.status, 0, 64, s);
+  const LaPlanDev dev = la_plan_dev(dims, in, pl, ws);
   if (dims->dtype == SSD_BF16)
-    la_run<__nv_bfloat16>(p, false, s);
+    la_run<__nv_bfloat16>(dims, pl, dev, &p, 1, ws, s);
   else
-    la_run<float>(p, false, s);
+    la_run<float>(dims, pl, dev, &p, 1, ws, s);
   return launch_status();
 }
 
@@ -333,7 +385,6 @@ ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims *dims, const ssd_
   if (st != SSD_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
-  cudaMemsetAsync(ws + pl.status, 0, 64, s);
   if (dims->dtype == SSD_BF16)
     return la_backward_impl<__nv_bfloat16>(dims, in, dout, dout_tok_stride, dfinal_states, grads, ws, pl, s);
   return la_backward_impl<float>(dims, in, dout, dout_tok_stride, dfinal_states, grads, ws, pl, s);
@@ -353,7 +404,9 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_line
   if (nslots <= 0) return SSD_ERR_INVALID_DIMS;
   if (!aligned(states, 16) || !aligned(slot_idx, 4)) return SSD_ERR_ALIGNMENT;
   const int group = dims->nheads / dims->nheads_kv;
-  LaPass p = la_base(dims, in, LaPlan{}, nullptr);
+  LaPass p{};
+  p.H = dims->nheads;
+  p.g = in->log_decay;
   la_roles(p, Role{in->q, in->q_tok_stride, 1, dims->nheads}, Role{in->k, in->k_tok_stride, group, dims->nheads_kv},
            Role{in->v, in->v_tok_stride, group, dims->nheads_kv}, dims->headdim_k, dims->headdim_v);
   p.o_scale = in->scale;
@@ -361,9 +414,9 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_line
   p.os = o_tok_stride;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dims->dtype == SSD_BF16)
-    SSD_LAUNCH("la_step", launch_la_step<__nv_bfloat16>(p, states, nslots, slot_idx, s));
+    SSD_LAUNCH("la_step", launch_la_step<__nv_bfloat16>(p, dims->nseq, states, nslots, slot_idx, s));
   else
-    SSD_LAUNCH("la_step", launch_la_step<float>(p, states, nslots, slot_idx, s));
+    SSD_LAUNCH("la_step", launch_la_step<float>(p, dims->nseq, states, nslots, slot_idx, s));
   return launch_status();
 }
 

@@ -1,0 +1,61 @@
+// Linear attention: the table of units of packed sequences, and the words that a
+// call's kernels share (status, work counters, flags) cleared in the same launch.
+#include "retention.h"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Thread y takes unit y in sequence order, finds its sequence and segment, and
+// its place in the order by levels:
+//     sum_s min(segments_s, level) + (sequences before its own with more segments than level).
+__global__ void __launch_bounds__(kThreads) la_table_kernel(LaPlanDev pl, LaEntry *table, int *table_units, int nflags) {
+  __shared__ int nseg[kLaMaxCutSeqs];
+  const int y = blockIdx.x * kThreads + threadIdx.x, stride = gridDim.x * kThreads;
+  if (y == 0) *pl.status = 0;
+  if (y < kLaCounterWords) pl.counters[y] = 0;
+  for (int i = y; i < nflags; i += stride) pl.flags[i] = 0;
+  if (!table) return;
+  for (int s = threadIdx.x; s < pl.nseq; s += kThreads) {
+    int a, len;
+    la_seq_bounds(pl, s, a, len);
+    nseg[s] = la_segments(len, pl.seg_len);
+  }
+  __syncthreads();
+  int seq = 0, first = 0;
+  while (seq < pl.nseq && first + nseg[seq] <= y) first += nseg[seq++];
+  if (y == 0) {
+    int n = 0;
+    for (int s = 0; s < pl.nseq; ++s) n += nseg[s];
+    // bounds that overlap could name more units than there is room for; the last ones are then left out
+    *table_units = min(n, pl.units);
+  }
+  if (y >= pl.units || seq == pl.nseq) return;
+  const int level = y - first;
+  int at = 0, next = 0;  // places of this level and of the next
+  for (int s = 0; s < pl.nseq; ++s) {
+    at += min(nseg[s], level) + (s < seq && nseg[s] > level);
+    next += min(nseg[s], level + 1) + (s < seq && nseg[s] > level + 1);
+  }
+  if (at >= pl.units) return;
+  LaEntry e;
+  e.seq = seq;
+  e.level = level;
+  e.nseg = nseg[seq];
+  la_seq_bounds(pl, seq, e.a, e.len);
+  e.next = level + 1 < nseg[seq] && next < pl.units ? next : -1;
+  table[at] = e;
+}
+
+}  // namespace
+
+void launch_la_table(const LaPlanDev &pl, LaEntry *table, int *table_units, int nflags, cudaStream_t s) {
+  const long long work = table ? pl.units : 1;
+  long long blocks = (work + kThreads - 1) / kThreads;
+  if (blocks < (nflags + 4095) / 4096) blocks = (nflags + 4095) / 4096;
+  la_table_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(pl, table, table_units, nflags);
+}
+
+}  // namespace ssd

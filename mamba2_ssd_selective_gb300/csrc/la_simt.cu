@@ -55,17 +55,22 @@ __device__ __forceinline__ void stage_transposed(float *dst, const T *src, long 
   }
 }
 
-template <typename T, bool REV, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
+template <typename T, bool SUMMARY>
+__global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPlanDev pl, const __grid_constant__ LaBatch batch) {
   extern __shared__ __align__(16) float sm[];
+  const int unit = blockIdx.x;
+  if (unit >= la_units(pl)) return;
+  const LaPass &p = batch.p[blockIdx.z % batch.n];
+  const int tile = blockIdx.z / batch.n, c0 = tile * kTV;
+  if (c0 >= p.dv) return;  // passes of a batch may differ in width
+  const bool rev = p.reverse;
+  const LaUnit u = la_unit(pl, unit, rev);
+  if (SUMMARY && u.next < 0) return;  // nothing follows
   const int dkp = (p.dk + 63) & ~63;
   float *Qt = sm, *Kt = Qt + dkp * kLdC, *S = Kt + dkp * kLdC, *V = S + dkp * kLdV, *At = V + kC * kLdV,
         *pw = At + kC * kLdC;  // pw[0..kC]: lam^n
-  LaUnit u;
-  if (!la_find_unit(p, blockIdx.x, u)) return;  // every warp finds the same
-  if (SUMMARY && (u.nseg == 1 || la_is_last(u, REV))) return;  // nothing follows
   const float p_scale = p.o_scale * p.p_scale;
-  const int h = blockIdx.y, c0 = blockIdx.z * kTV, tid = threadIdx.x, ncol = min(kTV, p.dv - c0);
+  const int h = blockIdx.y, tid = threadIdx.x, ncol = min(kTV, p.dv - c0);
   const float g = __ldg(p.g + h);
   const T *q = static_cast<const T *>(p.q) + u.t0 * p.qs + (h / p.gq) * p.dk;
   const T *k = static_cast<const T *>(p.k) + u.t0 * p.ks + (h / p.gk) * p.dk;
@@ -77,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
   for (int e = p.dk * kLdC + tid; e < dkp * kLdC; e += kThreads) Qt[e] = Kt[e] = 0.f;
   {
     int sa, sb;
-    const float *in = SUMMARY ? nullptr : la_state_in(p, u, blockIdx.x, h, sa, sb);
+    const float *in = SUMMARY ? nullptr : la_state_in(p, u, unit, h, sa, sb);
     for (int e = tid; e < dkp * kTV; e += kThreads) {
       const int a = e / kTV, b = e % kTV;
       S[a * kLdV + b] = in && a < p.dk && b < ncol ? in[(size_t)a * sa + (size_t)(c0 + b) * sb] : 0.f;
@@ -85,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
   }
   const int nb = (u.len + kC - 1) / kC;
   for (int ib = 0; ib < nb; ++ib) {
-    const int blk = REV ? nb - 1 - ib : ib, r0 = blk * kC, nv = min(kC, u.len - r0);
+    const int blk = rev ? nb - 1 - ib : ib, r0 = blk * kC, nv = min(kC, u.len - r0);
     __syncthreads();  // the previous block's operands have been read
     if (!SUMMARY) stage_transposed(Qt, q + (long long)r0 * p.qs, p.qs, nv, p.dk);
     stage_transposed(Kt, k + (long long)r0 * p.ks, p.ks, nv, p.dk);
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float2 out;
-          const int d0 = REV ? j0 + j - i0 : i0 - j0 - j, d1 = REV ? d0 - 1 : d0 + 1;
+          const int d0 = rev ? j0 + j - i0 : i0 - j0 - j, d1 = rev ? d0 - 1 : d0 + 1;
           out.x = d0 >= 0 ? acc[0][j] * (pw[d0] * p_scale) : 0.f;
           out.y = d1 >= 0 ? acc[1][j] * (pw[d1] * p_scale) : 0.f;
           *reinterpret_cast<float2 *>(At + (j0 + j) * kLdC + i0) = out;
@@ -138,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float w = p.o_scale * pw[REV ? max(nv - 1 - i0 - i, 0) : i0 + i + 1];
+        const float w = p.o_scale * pw[rev ? max(nv - 1 - i0 - i, 0) : i0 + i + 1];
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] *= w;
       }
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
         for (int j = 0; j < 4; ++j) {
           const float4 b = *reinterpret_cast<const float4 *>(V + (j0 + j) * kLdV + n0);
           const int r = j0 + j;
-          const float w = r < nv ? p.st_scale * pw[REV ? r + 1 : nv - 1 - r] : 0.f;
+          const float w = r < nv ? p.st_scale * pw[rev ? r + 1 : nv - 1 - r] : 0.f;
           vv[j][0] = b.x * w; vv[j][1] = b.y * w; vv[j][2] = b.z * w; vv[j][3] = b.w * w;
         }
 #pragma unroll
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
   }
   __syncthreads();
   int sa, sb;
-  float *out = la_state_out(p, u, blockIdx.x, h, REV, SUMMARY, sa, sb);
+  float *out = la_state_out(p, u, h, SUMMARY, sa, sb);
   if (out)
     for (int e = tid; e < p.dk * kTV; e += kThreads) {
       const int a = e / kTV, b = e % kTV;
@@ -213,59 +218,62 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPass p) {
 }
 
 // The states between segments of a cut sequence: per head, in processing order,
-//     next = lam^len S + W_seg,   W_seg (from a zero state) replaced by S.
+//     next = lam^len S + W_seg,   W_seg (from a zero state, where S belongs) replaced by S.
 // The last segment has no W_seg: the pass that starts from its S writes the final state.
-constexpr int kScanThreads = 256;
-template <bool REV>
-__global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPass p) {
-  __shared__ int first;
-  const int nblk = (p.dk * p.dv + kScanThreads - 1) / kScanThreads;
+constexpr int kScanThreads = 256, kScanMax = 512;
+__global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPlanDev pl, const __grid_constant__ LaBatch batch) {
+  __shared__ int units[kScanMax];
+  const LaPass &p = batch.p[blockIdx.z];
+  const int dd = p.dk * p.dv, nblk = (batch.p[0].dk * batch.p[0].dv + kScanThreads - 1) / kScanThreads;
   const int s = blockIdx.x / nblk, h = blockIdx.y;
   int a, len;
-  la_seq_bounds(p, s, a, len);
-  const int n = la_segments(p, len);
+  la_seq_bounds(pl, s, a, len);
+  const int n = la_segments(len, pl.seg_len);
   if (n == 1) return;
-  // the sequence's first unit: segments of the sequences before it
-  if (threadIdx.x < 32) {
-    int c = 0;
-    if (!p.cu) {
-      c = s * n;
-    } else {
-      for (int x = threadIdx.x; x < s; x += 32) {
-        int xa, xl;
-        la_seq_bounds(p, x, xa, xl);
-        c += la_segments(p, xl);
-      }
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
-    }
-    if (threadIdx.x == 0) first = c;
-  }
-  __syncthreads();
-  const int u0 = first;
-  if (u0 + n > p.nunits) return;  // cu_seqlens that do not partition the rows
-  const int dd = p.dk * p.dv, e = (blockIdx.x % nblk) * kScanThreads + threadIdx.x;
-  if (e >= dd) return;
+  const int e = blockIdx.x % nblk * kScanThreads + threadIdx.x;
+  const bool live = e < dd;
   const size_t user = ((size_t)s * p.H + h) * dd + (size_t)(e / p.dv) * p.sa + (size_t)(e % p.dv) * p.sb;
   const float g = __ldg(p.g + h);
-  const float2 full = la_pow2(g, p.seg_len), tail = la_pow2(g, len - (n - 1) * p.seg_len);
-  float st = p.init ? p.init[user] : 0.f;
-  float *base = p.seg_state + ((size_t)u0 * p.H + h) * dd + e;
+  const float2 full = la_pow2(g, pl.seg_len), tail = la_pow2(g, len - (n - 1) * pl.seg_len);
+  float st = live && p.init ? p.init[user] : 0.f;
+  float *base = p.seg_state + (size_t)h * dd + e;
   const size_t step = (size_t)p.H * dd;
   constexpr int kAhead = 8;
-  for (int i0 = 0; i0 < n; i0 += kAhead) {
-    float w[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (i0 + i < n - 1) w[i] = base[(REV ? n - 1 - i0 - i : i0 + i) * step];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (i0 + i < n) {
-        const int seg = REV ? n - 1 - i0 - i : i0 + i;
-        const float2 c = seg == n - 1 ? tail : full;
-        base[seg * step] = st;
-        if (i0 + i < n - 1) st = fmaf(st, c.x, fmaf(st, c.y, w[i]));
+  // level i + 1 holds what level i's segment gives, then the state after it
+  for (int l0 = 1; l0 < n; l0 += kScanMax) {
+    const int m = min(kScanMax, n - l0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < m; i += kScanThreads) {
+      const int level = l0 + i;
+      int at = 0;
+      if (!pl.table) {
+        at = level * pl.nseq + s;
+      } else {
+        for (int x = 0; x < pl.nseq; ++x) {
+          int xa, xl;
+          la_seq_bounds(pl, x, xa, xl);
+          const int xn = la_segments(xl, pl.seg_len);
+          at += min(xn, level) + (x < s && xn > level);
+        }
       }
+      units[i] = at < la_units(pl) ? at : -1;
+    }
+    __syncthreads();
+    if (!live) continue;
+    for (int i0 = 0; i0 < m; i0 += kAhead) {
+      float w[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i0 + i < m && units[i0 + i] >= 0) w[i] = base[units[i0 + i] * step];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i0 + i < m && units[i0 + i] >= 0) {
+          // the segment before this level: the sequence's tail comes first in reverse
+          const float2 c = p.reverse && l0 + i0 + i == 1 ? tail : full;
+          st = fmaf(st, c.x, fmaf(st, c.y, w[i]));
+          base[units[i0 + i] * step] = st;
+        }
+    }
   }
 }
 
@@ -287,34 +295,36 @@ __global__ void __launch_bounds__(256) la_sum_heads_kernel(const float *__restri
   store4(out + row * os + (long long)kv * d + 4 * c, acc);
 }
 
-template <typename T, bool REV, bool SUMMARY>
-void run_simt(const LaPass &p, cudaStream_t s) {
-  const int dkp = (p.dk + 63) & ~63;
-  const int bytes = 4 * (2 * dkp * kLdC + dkp * kLdV + kC * kLdV + kC * kLdC + kC + 4);
-  static bool once = (cudaFuncSetAttribute(la_simt_kernel<T, REV, SUMMARY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           4 * (2 * 256 * kLdC + 256 * kLdV + kC * kLdV + kC * kLdC + kC + 4)),
+constexpr int smem_bytes(int dk) {
+  const int dkp = (dk + 63) & ~63;
+  return 4 * (2 * dkp * kLdC + dkp * kLdV + kC * kLdV + kC * kLdC + kC + 4);
+}
+
+template <typename T, bool SUMMARY>
+void run_simt(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
+  static bool once = (cudaFuncSetAttribute(la_simt_kernel<T, SUMMARY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           smem_bytes(256)),
                       true);
   (void)once;
-  const dim3 grid(p.nunits, p.H, (p.dv + kTV - 1) / kTV);
-  la_simt_kernel<T, REV, SUMMARY><<<grid, kThreads, bytes, s>>>(p);
+  int dk = 0, dv = 0;
+  for (int i = 0; i < b.n; ++i) {
+    dk = b.p[i].dk > dk ? b.p[i].dk : dk;
+    dv = b.p[i].dv > dv ? b.p[i].dv : dv;
+  }
+  const dim3 grid(pl.units, pl.H, (dv + kTV - 1) / kTV * b.n);
+  la_simt_kernel<T, SUMMARY><<<grid, kThreads, smem_bytes(dk), s>>>(pl, b);
 }
 
 }  // namespace
 
 template <typename T>
-void launch_la_simt(const LaPass &p, bool reverse, bool summary, cudaStream_t s) {
-  if (reverse)
-    summary ? run_simt<T, true, true>(p, s) : run_simt<T, true, false>(p, s);
-  else
-    summary ? run_simt<T, false, true>(p, s) : run_simt<T, false, false>(p, s);
+void launch_la_simt(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s) {
+  summary ? run_simt<T, true>(pl, b, s) : run_simt<T, false>(pl, b, s);
 }
 
-void launch_la_scan(const LaPass &p, bool reverse, cudaStream_t s) {
-  const dim3 grid((p.dk * p.dv + kScanThreads - 1) / kScanThreads * p.nseq, p.H);
-  if (reverse)
-    la_scan_kernel<true><<<grid, kScanThreads, 0, s>>>(p);
-  else
-    la_scan_kernel<false><<<grid, kScanThreads, 0, s>>>(p);
+void launch_la_scan(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
+  const int nblk = (b.p[0].dk * b.p[0].dv + kScanThreads - 1) / kScanThreads;  // the same for every pass
+  la_scan_kernel<<<dim3(nblk * pl.nseq, pl.H, b.n), kScanThreads, 0, s>>>(pl, b);
 }
 
 template <typename T>
@@ -324,8 +334,8 @@ void launch_la_sum_heads(const float *in, void *out, long long os, long long row
   la_sum_heads_kernel<T><<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(in, static_cast<T *>(out), os, n4, Hkv, group, d);
 }
 
-template void launch_la_simt<float>(const LaPass &, bool, bool, cudaStream_t);
-template void launch_la_simt<__nv_bfloat16>(const LaPass &, bool, bool, cudaStream_t);
+template void launch_la_simt<float>(const LaPlanDev &, const LaBatch &, bool, cudaStream_t);
+template void launch_la_simt<__nv_bfloat16>(const LaPlanDev &, const LaBatch &, bool, cudaStream_t);
 template void launch_la_sum_heads<float>(const float *, void *, long long, long long, int, int, int, cudaStream_t);
 template void launch_la_sum_heads<__nv_bfloat16>(const float *, void *, long long, long long, int, int, int,
                                                  cudaStream_t);

@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(kThreads) la_step_kernel(LaPass p, float *__re
 }  // namespace
 
 template <typename T>
-void launch_la_step(const LaPass &p, float *states, int nslots, const int *slot_idx, cudaStream_t s) {
-  const dim3 grid(p.nseq, p.H, (p.dv + kCols - 1) / kCols);
+void launch_la_step(const LaPass &p, int rows, float *states, int nslots, const int *slot_idx, cudaStream_t s) {
+  const dim3 grid(rows, p.H, (p.dv + kCols - 1) / kCols);
   if (p.dk <= 2 * kRows)
     la_step_kernel<T, 2><<<grid, kThreads, 0, s>>>(p, states, nslots, slot_idx);
   else if (p.dk <= 4 * kRows)
@@ -94,7 +94,7 @@ void launch_la_step(const LaPass &p, float *states, int nslots, const int *slot_
     la_step_kernel<T, 8><<<grid, kThreads, 0, s>>>(p, states, nslots, slot_idx);
 }
 
-template void launch_la_step<float>(const LaPass &, float *, int, const int *, cudaStream_t);
-template void launch_la_step<__nv_bfloat16>(const LaPass &, float *, int, const int *, cudaStream_t);
+template void launch_la_step<float>(const LaPass &, int, float *, int, const int *, cudaStream_t);
+template void launch_la_step<__nv_bfloat16>(const LaPass &, int, float *, int, const int *, cudaStream_t);
 
 }  // namespace ssd

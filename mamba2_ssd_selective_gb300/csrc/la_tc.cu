@@ -1,9 +1,10 @@
 // Linear attention with a decay for each head on the 5th-generation tensor cores
 // (tcgen05, accumulators and A operands in TMEM): bf16 tensors, widths up to 128.
 //
-// One CTA takes one segment of one sequence and one query head, and walks it in
-// blocks of 64 tokens.  With P_ij = scale q_i . k_j lam^|i - j| inside the block
-// (j <= i; reverse: j >= i) and the incoming state S (dk x dv):
+// Persistent CTAs, one on an SM, take items (a segment of one sequence, one pass of
+// the call, one query head) from a counter and walk each in blocks of 64 tokens.
+// With P_ij = p_scale q_i . k_j lam^|i - j| inside the block (j <= i; reverse: j >= i) and
+// the incoming state S (dk x dv):
 //     o_i  = lam^a(i) (S^T q_i + V^T P'_i),    P'_ij = P_ij lam^-a(i)
 //     S^T  = lam^nv S^T + W^T,    W^T = (V^T diag(lam^b)) K
 // Everything is formed transposed, so that dv (up to 128) fills the accumulators'
@@ -33,6 +34,10 @@
 // lam^-(nv - 1 - j)), so that both products meet in one accumulator, which takes
 // turns between two.  It is up to lam^-64: heads whose lam^64 is below 2^-40 form
 // P and O beside Oi instead, and add lam^a Oi at the end.
+// Segments of a cut sequence either start from states that a scan has joined before
+// (few sequences: the segments run side by side), or hand their state on: the
+// next segment's state warps wait for its flag, and as items are taken level by
+// level, whatever an item waits for was taken before it.
 // The last block of a sequence is masked: rows past its end belong to another
 // sequence, so K's and V's are replaced by zeros in shared memory (0 * NaN would be
 // NaN), scores with them are cut off, and nothing is stored there.
@@ -57,6 +62,13 @@ constexpr uint32_t kBox = 8192;  // [64 tokens x 64 columns] bf16
 constexpr uint32_t kTmQK = 0, kTmO = 64, kTmOi = 128, kTmW = 192, kTmS = 320, kTmT = 384, kTmCols = 512;
 constexpr uint32_t kTerm = 16, kHalf = 3 * kTerm;  // a term of half a block (32 tokens as bf16 pairs)
 
+// Weights of a block's rows, each filled by the role that reads it.
+struct Tables {
+  float st[kC];   // weighted V: state scale lam^b(row)
+  float out[kC];  // outputs: output scale lam^a(row)
+  float p[kC];    // P: product scale lam^-a of the column, or (heads that stand apart) both scales lam^distance
+};
+
 template <int KB, int VB, bool SUMMARY>
 struct Layout {
   static constexpr int kStages = KB + VB == 2 ? 6 : 4;
@@ -64,22 +76,12 @@ struct Layout {
   static constexpr uint32_t kP = kStages * kStage;                  // two P buffers
   static constexpr uint32_t kO = kP + (SUMMARY ? 0 : 2 * kBox);     // a block's outputs, on their way to TMA
   static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : VB * kBox);  // weights, see Tables
-  static constexpr uint32_t kBar = kTab + 4 * 7 * kC;
-  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2 + 1 + 4 + 1 + 4 + 1;
-  static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
+  static constexpr uint32_t kBar = kTab + sizeof(Tables);
+  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2 + 1 + 4 + 1 + 4 + 4 + 1;
+  static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;  // and the TMEM address, two item slots
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
-
-// Weights of a block's rows: of a full block, then of the sequence's last one, which
-// has fewer live rows (the others weigh nothing).
-struct Tables {
-  float st[2][kC];  // state scale lam^b(r)
-  float out[2][kC]; // output scale lam^a(r)
-  float p[kC];      // output and product scale lam^n
-  float col[2][kC]; // product scale lam^-(what out gives the row of the same number)
-};
-static_assert(sizeof(Tables) <= 4 * 7 * kC, "table space");
 
 template <int ST>
 struct Bars {
@@ -91,8 +93,9 @@ struct Bars {
   uint64_t *v_ready, *v_free;   // [2] half a block's terms in TMEM / read by its MMAs
   uint64_t *w_full;             // W formed
   uint64_t *o_full, *o_free;    // [2]
+  pipe::UnitRing items;
   uint64_t *drain;
-  __device__ explicit Bars(uint64_t *b) {
+  __device__ explicit Bars(uint64_t *b, int *slot) {
     full = b;
     free = full + ST;
     qk_full = free + ST;
@@ -107,7 +110,10 @@ struct Bars {
     w_full = v_free + 2;
     o_full = w_full + 1;
     o_free = o_full + 2;
-    drain = o_free + 2;
+    items.full = o_free + 2;
+    items.free = items.full + 2;
+    items.slot = slot;
+    drain = items.free + 2;
   }
 };
 
@@ -143,29 +149,104 @@ __device__ __forceinline__ void split3(uint64_t x, uint32_t &a, uint32_t &b, uin
   c = tc::pack_bf16x2(minus_lo(f0, b), minus_hi(f1, b));
 }
 
+// Branches that a block of the usual kind does not take are kept out of the loops' code: the roles' loops
+// together are about what the instruction caches hold (with such branches in line, half
+// of all warp cycles waited for instructions).
+__device__ __forceinline__ bool unlikely(bool c) { return __builtin_expect(c, 0); }
+// barrier among a role's warps
+template <int ID, int THREADS>
+__device__ __forceinline__ void role_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+
+// a chained segment waits for its incoming state (bounded like every hand-off)
+__device__ __forceinline__ bool wait_flag(const int *flag, const WaitCtl &w) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+    if (v) return true;
+    if ((i & 15u) == 15u) {
+      if (*reinterpret_cast<volatile int *>(w.status) != 0) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0)
+        t0 = t;
+      else if (t - t0 > w.limit_ns)
+        break;
+    }
+    __nanosleep(100);
+  }
+  atomicExch(w.status, 1);
+  return false;
+}
+
+struct Maps {
+  CUtensorMap q, k, v, o;
+};
+struct Args {
+  Maps maps[3];
+  LaBatch batch;
+  LaPlanDev pl;
+};
+
+// One item: a unit, a pass, a query head.
+struct Item {
+  int pass, unit, h, nb;
+  bool rev;
+  float g;
+  LaUnit u;
+  template <bool SUMMARY>
+  static __device__ __forceinline__ Item get(const Args &a, int x) {
+    Item it;
+    const int y = x / a.pl.H;
+    it.h = x - y * a.pl.H;
+    it.unit = y / a.batch.n;
+    it.pass = y - it.unit * a.batch.n;
+    const LaPass &p = a.batch.p[it.pass];
+    it.rev = p.reverse;
+    it.g = __ldg(p.g + it.h);
+    it.u = la_unit(a.pl, it.unit, it.rev);
+    it.nb = SUMMARY && it.u.next < 0 ? 0 : (it.u.len + kC - 1) / kC;  // nothing follows a last segment
+    return it;
+  }
+  // The same for a converged warp.  What comes from memory goes through a shuffle, which tells
+  // the compiler that it is the same in all lanes: else every loop and operand that
+  // depends on it leaves the uniform registers (the kernel then took twice as long).
+  template <bool SUMMARY>
+  static __device__ __forceinline__ Item get_uniform(const Args &a, int x) {
+    Item it = get<SUMMARY>(a, x);
+    it.g = __shfl_sync(0xffffffffu, it.g, 0);
+    it.nb = __shfl_sync(0xffffffffu, it.nb, 0);
+    it.u.t0 = __shfl_sync(0xffffffffu, it.u.t0, 0);
+    it.u.len = __shfl_sync(0xffffffffu, it.u.len, 0);
+    it.u.level = __shfl_sync(0xffffffffu, it.u.level, 0);
+    it.u.next = __shfl_sync(0xffffffffu, it.u.next, 0);
+    it.u.seq = __shfl_sync(0xffffffffu, it.u.seq, 0);
+    return it;
+  }
+  // processing order: block i is rows [64 blk, 64 blk + nv) of the segment
+  __device__ __forceinline__ int block(int i) const { return rev ? nb - 1 - i : i; }
+  __device__ __forceinline__ int rows(int i) const { return min(kC, u.len - block(i) * kC); }
+  // whether lam^-64 is out of reach: products and incoming state in accumulators of their own
+  __device__ __forceinline__ bool apart() const { return !(g * kC > -40.f * 0.6931f); }
+};
+
 // KB, VB: 64-column boxes of the q/k roles and of the v/o roles
-template <int KB, int VB, bool REV, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads, 1)
-    la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, LaPass p) {
+// F32: fp32 outputs
+template <int KB, int VB, bool SUMMARY, bool F32>
+__global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constant__ Args args) {
   using L = Layout<KB, VB, SUMMARY>;
   constexpr int ST = L::kStages;
   extern __shared__ uint8_t smem_raw[];
-  LaUnit u;
-  const int unit = blockIdx.x / p.H, h = blockIdx.x - unit * p.H;
-  if (!la_find_unit(p, unit, u)) return;  // every warp finds the same
-  if (SUMMARY && (u.nseg == 1 || la_is_last(u, REV))) return;  // nothing follows
   uint8_t *sm = tc::aligned_smem(smem_raw);
-  const WaitCtl wait{p.status, p.wait_ns};
-  const Bars<ST> bar(reinterpret_cast<uint64_t *>(sm + L::kBar));
+  const LaPlanDev &pl = args.pl;
+  const WaitCtl wait{pl.status, pl.wait_ns};
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + L::kNumBars * 8);
+  const Bars<ST> bar(reinterpret_cast<uint64_t *>(sm + L::kBar), reinterpret_cast<int *>(tslot + 1));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
-  const int nb = (u.len + kC - 1) / kC;
-  const float g = __ldg(p.g + h);
   Tables &tab = *reinterpret_cast<Tables *>(sm + L::kTab);
+  const int nitems = __shfl_sync(0xffffffffu, la_units(pl), 0) * args.batch.n * pl.H;
 
-  // whether lam^-64 is out of reach: products and incoming state in accumulators of their own
-  const bool apart = !(g * kC > -40.f * 0.6931f);
   if (threadIdx.x == 64) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bar.full[i], 1);
@@ -180,6 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.o_free[i], 2 * VB);
       mbar_init(&bar.v_ready[i], 2 * VB);
+      mbar_init(&bar.items.full[i], 1);
+      mbar_init(&bar.items.free[i], SUMMARY ? 1 + 6 * VB : 3 + 8 * VB);  // every warp but the producer's that takes part
     }
     mbar_init(bar.s_ready, 4 * VB);
     mbar_init(bar.w_free, 4 * VB);
@@ -192,167 +275,191 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tslot, kTmCols);
     tmem_relinquish();
   }
-  if (threadIdx.x < 2 * kC) {
-    const int r = threadIdx.x & (kC - 1), last = threadIdx.x / kC, nv = last ? u.len - (nb - 1) * kC : kC;
-    const bool live = r < nv;
-    tab.st[last][r] = live ? p.st_scale * la_pow(g, REV ? r + 1 : nv - 1 - r) : 0.f;
-    tab.out[last][r] = live ? p.o_scale * la_pow(g, REV ? nv - 1 - r : r + 1) : 0.f;
-    tab.col[last][r] = live ? p.p_scale * la_pow(g, REV ? r + 1 - nv : -1 - r) : 0.f;
-    if (!last) tab.p[r] = p.o_scale * p.p_scale * la_pow(g, r);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
-  // processing order: block i is rows [64 blk, 64 blk + nv) of the segment
-  auto block_of = [&](int i) { return REV ? nb - 1 - i : i; };
-  auto rows_of = [&](int blk) { return min(kC, u.len - blk * kC); };
 
+  // Every role counts the blocks it has been through (m): the m-th use of a barrier is
+  // its m-th completion, or for pairs and rings completion m / 2 or m / ST of one of them.
   // The block is launched with 640 x 96 registers; the state warps, which hold 64 values of the state a
   // thread, take what the others do not need: 128 x (64 + 104 + 2 * 112 + 88) = 61440.
   if (warp < kOutWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 2) {
       // ------------------------------------------------------------ producer
-      if (lane == 0 && nb > 0) {
-        if (!SUMMARY) prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
-        int i = 0;
-        for (; i < nb; ++i) {
-          const int st = i % ST, row = u.t0 + block_of(i) * kC;
-          if (i >= ST && !mbar_wait(&bar.free[st], parity(i / ST - 1), wait)) break;
-          uint8_t *base = sm + st * L::kStage;
-          mbar_expect_tx(&bar.full[st], L::kStage);
-          for (int b = 0; b < KB; ++b) {
-            if (!SUMMARY) tma_load_3d(base + L::kQ + b * kBox, &tm_q, &bar.full[st], 64 * b, h / p.gq, row);
-            tma_load_3d(base + L::kK + b * kBox, &tm_k, &bar.full[st], 64 * b, h / p.gk, row);
+      if (lane == 0) {
+        int *counter = pl.counters + (SUMMARY ? 0 : 1);
+        uint32_t m = 0;
+        bool ok = true;
+        int next = atomicAdd(counter, 1);
+        for (uint32_t n = 0;; ++n) {
+          const int x = pipe::publish_unit(bar.items, n, ok && (uint32_t)next < (uint32_t)nitems ? next : nitems, nitems);
+          if (x >= nitems) break;
+          next = atomicAdd(counter, 1);
+          const Item it = Item::get<SUMMARY>(args, x);
+          const LaPass &p = args.batch.p[it.pass];
+          const Maps &mp = args.maps[it.pass];
+          const int hq = it.h / p.gq, hk = it.h / p.gk, hv = it.h / p.gv;
+          for (int i = 0; i < it.nb; ++i) {
+            const int st = m % ST, row = it.u.t0 + it.block(i) * kC;
+            if (m >= ST && !mbar_wait(&bar.free[st], parity(m / ST - 1), wait)) {
+              ok = false;
+              break;
+            }
+            uint8_t *base = sm + st * L::kStage;
+            mbar_expect_tx(&bar.full[st], L::kStage);
+            for (int b = 0; b < KB; ++b) {
+              if (!SUMMARY) tma_load_3d(base + L::kQ + b * kBox, &mp.q, &bar.full[st], 64 * b, hq, row);
+              tma_load_3d(base + L::kK + b * kBox, &mp.k, &bar.full[st], 64 * b, hk, row);
+            }
+            for (int b = 0; b < VB; ++b) tma_load_3d(base + L::kV + b * kBox, &mp.v, &bar.full[st], 64 * b, hv, row);
+            ++m;
           }
-          for (int b = 0; b < VB; ++b)
-            tma_load_3d(base + L::kV + b * kBox, &tm_v, &bar.full[st], 64 * b, h / p.gv, row);
         }
         // every load issued has landed before the CTA releases its shared memory
-        for (int m = i > ST ? i - ST : 0; m < i; ++m) mbar_wait_drain(&bar.full[m % ST], parity(m / ST));
+        for (uint32_t x = m > ST ? m - ST : 0; x < m; ++x) mbar_wait_drain(&bar.full[x % ST], parity(x / ST));
       }
     } else if (warp == 3) {
       // ------------------------------------------------------------ MMA issuer
-      {  // the whole warp, so that descriptors stay in uniform registers; one lane acts
-        const uint32_t el = elect_one();
-        const uint32_t s0 = smem_u32(sm);
-        // K-major: Q (A and B), K, P; MN-major: K as the B operand of W, V (A).  A's 128 rows run
-        // past Q's 64 into the shared memory behind it; those rows of the result (and
-        // the lanes past 64 when VB = 1) are not read.
-        const uint64_t dQ = desc_sw128(s0 + L::kQ, 16, 1024), dK = desc_sw128(s0 + L::kK, 16, 1024),
-                       dKn = desc_sw128(s0 + L::kK, kBox, 1024), dV = desc_sw128(s0 + L::kV, kBox, 1024), dP = desc_sw128(s0 + L::kP, 16, 1024);
-        constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iPV = idesc_bf16(128, 64, true, false), iW = idesc_bf16(128, 64 * KB, false, true);
-        auto stage = [&](int i) { return (uint64_t)((i % ST) * (L::kStage / 16)); };
-        auto scores = [&](int i) {
-          mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
-          if (i > 0) mbar_wait(bar.qk_free, parity(i - 1), wait);
-          tc_fence_after();
+      // the whole warp, so that descriptors stay in uniform registers; one lane acts
+      const uint32_t el = elect_one();
+      const uint32_t s0 = smem_u32(sm);
+      // K-major: Q (A and B), K, P; MN-major: K as the B operand of W, V (A).  A's 128 rows run
+      // past Q's 64 into the shared memory behind it; those rows of the result (and
+      // the lanes past 64 when VB = 1) are not read.
+      const uint64_t dQ = desc_sw128(s0 + L::kQ, 16, 1024), dK = desc_sw128(s0 + L::kK, 16, 1024),
+                     dKn = desc_sw128(s0 + L::kK, kBox, 1024), dV = desc_sw128(s0 + L::kV, kBox, 1024),
+                     dP = desc_sw128(s0 + L::kP, 16, 1024);
+      constexpr uint32_t iQK = idesc_bf16(128, 64, false, false), iPV = idesc_bf16(128, 64, true, false),
+                         iW = idesc_bf16(128, 64 * KB, false, true);
+      auto stage = [&](uint32_t m) { return (uint64_t)((m % ST) * (L::kStage / 16)); };
+      auto scores = [&](uint32_t m) {
+        mbar_wait(&bar.full[m % ST], parity(m / ST), wait);
+        if (m > 0) mbar_wait(bar.qk_free, parity(m - 1), wait);
+        tc_fence_after();
 #pragma unroll
-          for (int b = 0; b < KB; ++b)
-            pipe::umma_k_el<4>(el, tmem + kTmQK, dQ + stage(i) + b * (kBox / 16), dK + stage(i) + b * (kBox / 16), pipe::kStepK,
-                            pipe::kStepK, iQK, b > 0);
-          umma_commit_el(el, bar.qk_full);
-        };
-        // W of half a block: the three terms' two steps of 16 tokens each
-        auto half_w = [&](int i, int half) {
-          mbar_wait(&bar.v_ready[half], parity(i), wait);
-          tc_fence_after();
+        for (int b = 0; b < KB; ++b)
+          pipe::umma_k_el<4>(el, tmem + kTmQK, dQ + stage(m) + b * (kBox / 16), dK + stage(m) + b * (kBox / 16),
+                             pipe::kStepK, pipe::kStepK, iQK, b > 0);
+        umma_commit_el(el, bar.qk_full);
+      };
+      // W of half a block: the three terms' two steps of 16 tokens each
+      auto half_w = [&](uint32_t m, int half) {
+        mbar_wait(&bar.v_ready[half], parity(m), wait);
+        tc_fence_after();
 #pragma unroll
-          for (int t = 0; t < 3; ++t)
-            pipe::umma_ts_k_el<2>(el, tmem + kTmW, tmem + kTmT + half * kHalf + t * kTerm, dKn + stage(i) + half * (4096 / 16), 8,
-                               pipe::kStepMN, iW, half > 0 || t > 0);
-        };
-        if (!SUMMARY && nb > 0) scores(0);
-        for (int i = 0; i < nb; ++i) {
+        for (int t = 0; t < 3; ++t)
+          pipe::umma_ts_k_el<2>(el, tmem + kTmW, tmem + kTmT + half * kHalf + t * kTerm,
+                                dKn + stage(m) + half * (4096 / 16), 8, pipe::kStepMN, iW, half > 0 || t > 0);
+      };
+      uint32_t m = 0;
+      bool was_apart = false;
+      for (uint32_t n = 0;; ++n) {
+        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        if (x >= nitems) break;
+        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const bool apart = __shfl_sync(0xffffffffu, (int)it.apart(), 0);
+        if (!SUMMARY && it.nb > 0) scores(m);
+        for (int i = 0; i < it.nb; ++i, ++m) {
           if (SUMMARY)
-            mbar_wait(&bar.full[i % ST], parity(i / ST), wait);
-          else if (i + 1 < nb)
-            scores(i + 1);
-          if (i > 0) mbar_wait(bar.w_free, parity(i - 1), wait);
-          half_w(i, 0);
+            mbar_wait(&bar.full[m % ST], parity(m / ST), wait);
+          else if (i + 1 < it.nb)
+            scores(m + 1);
+          if (m > 0) mbar_wait(bar.w_free, parity(m - 1), wait);
+          half_w(m, 0);
           umma_commit_el(el, &bar.v_free[0]);
-          half_w(i, 1);
+          half_w(m, 1);
           umma_commit_el(el, bar.w_full);
           umma_commit_el(el, &bar.v_free[1]);
           if (!SUMMARY) {
-            mbar_wait(bar.s_ready, parity(i), wait);
-            // the accumulator of the incoming state's part and, unless apart, of the products
-            const uint32_t acc = tmem + (apart || (i & 1) ? kTmOi : kTmO);
-            if (apart ? i > 0 : i > 1) {
-              const int m = apart ? i - 1 : i - 2;
-              mbar_wait(&bar.o_free[m & 1], parity(m / 2), wait);
-            }
+            mbar_wait(bar.s_ready, parity(m), wait);
+            // the accumulator of the incoming state's part and, unless apart, of the products:
+            // the one of two blocks ago, or after or before a block that uses both the last one's
+            const uint32_t acc = tmem + (apart || (m & 1) ? kTmOi : kTmO);
+            const uint32_t back = apart || was_apart ? 1 : 2;
+            if (m >= back) mbar_wait(&bar.o_free[(m - back) & 1], parity((m - back) / 2), wait);
+            was_apart = apart;
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < KB; ++b)
-              pipe::umma_ts_k_el<4>(el, acc, tmem + kTmS + 32 * b, dQ + stage(i) + b * (kBox / 16), 8, pipe::kStepK, iQK,
+              pipe::umma_ts_k_el<4>(el, acc, tmem + kTmS + 32 * b, dQ + stage(m) + b * (kBox / 16), 8, pipe::kStepK, iQK,
                                     b > 0);
             umma_commit_el(el, bar.s_free);
-            mbar_wait(&bar.p_ready[i & 1], parity(i / 2), wait);
+            mbar_wait(&bar.p_ready[m & 1], parity(m / 2), wait);
             tc_fence_after();
-            pipe::umma_k_el<4>(el, apart ? tmem + kTmO : acc, dV + stage(i), dP + (i & 1) * (kBox / 16), pipe::kStepMN,
+            pipe::umma_k_el<4>(el, apart ? tmem + kTmO : acc, dV + stage(m), dP + (m & 1) * (kBox / 16), pipe::kStepMN,
                                pipe::kStepK, iPV, !apart);
-            umma_commit_el(el, &bar.o_full[i & 1]);
-            umma_commit_el(el, &bar.p_free[i & 1]);
+            umma_commit_el(el, &bar.o_full[m & 1]);
+            umma_commit_el(el, &bar.p_free[m & 1]);
           }
-          umma_commit_el(el, &bar.free[i % ST]);
-        }
-        // every MMA and every arrival of a commit has landed before the CTA ends
-        umma_commit_el(el, bar.drain);
-        mbar_wait_drain(bar.drain, 0);
-        for (int m = nb > ST ? nb - ST : 0; m < nb; ++m) mbar_wait_drain(&bar.free[m % ST], parity(m / ST));
-        if (nb > 0) {
-          mbar_wait_drain(bar.w_full, parity(nb - 1));
-          mbar_wait_drain(&bar.v_free[0], parity(nb - 1));
-          mbar_wait_drain(&bar.v_free[1], parity(nb - 1));
-        }
-        if (!SUMMARY && nb > 0) {
-          mbar_wait_drain(bar.qk_full, parity(nb - 1));
-          mbar_wait_drain(bar.s_free, parity(nb - 1));
-          for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) {
-            mbar_wait_drain(&bar.p_free[m & 1], parity(m / 2));
-            mbar_wait_drain(&bar.o_full[m & 1], parity(m / 2));
-          }
+          umma_commit_el(el, &bar.free[m % ST]);
         }
       }
-    } else {
+      // every MMA and every arrival of a commit has landed before the CTA ends
+      umma_commit_el(el, bar.drain);
+      mbar_wait_drain(bar.drain, 0);
+      for (uint32_t x = m > ST ? m - ST : 0; x < m; ++x) mbar_wait_drain(&bar.free[x % ST], parity(x / ST));
+      if (m > 0) {
+        mbar_wait_drain(bar.w_full, parity(m - 1));
+        mbar_wait_drain(&bar.v_free[0], parity(m - 1));
+        mbar_wait_drain(&bar.v_free[1], parity(m - 1));
+      }
+      if (!SUMMARY && m > 0) {
+        mbar_wait_drain(bar.qk_full, parity(m - 1));
+        mbar_wait_drain(bar.s_free, parity(m - 1));
+        for (uint32_t x = m > 2 ? m - 2 : 0; x < m; ++x) {
+          mbar_wait_drain(&bar.p_free[x & 1], parity(x / 2));
+          mbar_wait_drain(&bar.o_full[x & 1], parity(x / 2));
+        }
+      }
+    } else if (!SUMMARY) {
       // ------------------------------------------------------------ P
-      if (!SUMMARY) {
-        const int r = threadIdx.x;  // row of the block
+      const int r = threadIdx.x;  // row of the block
+      uint32_t m = 0;
+      for (uint32_t n = 0;; ++n) {
+        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        if (x >= nitems) break;
+        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const LaPass &p = args.batch.p[it.pass];
+        const bool rev = it.rev, apart = it.apart();
         // Masks of this row's bf16 pairs in the two 16-column groups that the diagonal
         // crosses (columns 32 warp and 32 warp + 16): masked scores may be NaN, so they
         // are cut off as bits, after weights that need not be right there.
         uint32_t keep[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          keep[x] = ((REV ? 2 * x >= lane : 2 * x <= lane) ? 0xffffu : 0u) |
-                    ((REV ? 2 * x + 1 >= lane : 2 * x + 1 <= lane) ? 0xffff0000u : 0u);
-        for (int i = 0; i < nb; ++i) {
-          const int nv = rows_of(block_of(i));
-          if (i >= 2) mbar_wait(&bar.p_free[i & 1], parity(i / 2 - 1), wait);
-          mbar_wait(bar.qk_full, parity(i), wait);
+        for (int y = 0; y < 16; ++y)
+          keep[y] = ((rev ? 2 * y >= lane : 2 * y <= lane) ? 0xffffu : 0u) |
+                    ((rev ? 2 * y + 1 >= lane : 2 * y + 1 <= lane) ? 0xffff0000u : 0u);
+        for (int i = 0; i < it.nb; ++i, ++m) {
+          const int nv = it.rows(i);
+          if (unlikely(i == 0 || (rev && i == 1))) {  // in order the weights do not depend on nv
+            role_sync<4, 64>();
+            tab.p[r] = p.p_scale * (apart ? p.o_scale * la_pow(it.g, r) : la_pow(it.g, rev ? r + 1 - nv : -1 - r));
+            role_sync<4, 64>();
+          }
+          if (m >= 2) mbar_wait(&bar.p_free[m & 1], parity(m / 2 - 1), wait);
+          mbar_wait(bar.qk_full, parity(m), wait);
           tc_fence_after();
-          const uint32_t dst = smem_u32(sm + L::kP + (i & 1) * kBox);
+          const uint32_t dst = smem_u32(sm + L::kP + (m & 1) * kBox);
 #pragma unroll 1
           for (int j0 = 0; j0 < kC; j0 += 16) {
             const int at = j0 - 32 * warp;  // the group's place against the diagonal: 0 and 16 cross it
             uint4 p0 = make_uint4(0, 0, 0, 0), p1 = p0;
-            if (REV ? at >= 0 : at < 32) {
+            if (rev ? at >= 0 : at < 32) {
               float s[16], v[8];
               tmem_ld16(pipe::tmem_quad(tmem + kTmQK, j0), s);
-              if (REV && nv < kC) {  // columns past the end are masked for the rows before it too
+              if (unlikely(rev && nv < kC)) {  // columns past the end are masked for the rows before it too
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[e] = j0 + e < nv ? s[e] : 0.f;
               }
-              if (apart) {
-                const float *w = tab.p + (REV ? j0 - r : r - j0);  // where masked, whatever lies there
+              if (unlikely(apart)) {
+                const float *w = tab.p + (rev ? j0 - r : r - j0);  // where masked, whatever lies there
+                const int step = rev ? 1 : -1;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) s[e] *= w[REV ? e : -e];
+                for (int e = 0; e < 16; ++e) s[e] *= w[step * e];
               } else {
-                const float4 *w = reinterpret_cast<const float4 *>(tab.col[REV && nv < kC] + j0);
+                const float4 *w = reinterpret_cast<const float4 *>(tab.p + j0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float4 t = w[e];
@@ -382,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           pipe::warp_arrive(bar.qk_free);
           fence_async_smem();
-          pipe::warp_arrive(&bar.p_ready[i & 1]);
+          pipe::warp_arrive(&bar.p_ready[m & 1]);
         }
       }
     }
@@ -394,96 +501,104 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tt = threadIdx.x - 32 * kOutWarp0, quad = warp & 3;
       // the address this lane gives to a group of four fragments: row i, columns of v
       const int fi = 8 * (lane >> 4) + (lane & 7), fc = 32 * quad + 8 * ((lane >> 3) & 1);
-      float w[16];  // what this lane's columns i weigh
-      for (int i = 0; i < nb; ++i) {
-        const int blk = block_of(i), nv = rows_of(blk);
-        const long long row0 = u.t0 + (long long)blk * kC;
-        const uint32_t so = smem_u32(sm + L::kO);
-        if (i == 0 || (REV && i == 1)) {  // in order the weights of a shorter block are those of a full one
-          const float *t = tab.out[REV && nv < kC] + 2 * (lane & 3);
+      const uint32_t so = smem_u32(sm + L::kO);
+      uint32_t m = 0;
+      for (uint32_t n = 0;; ++n) {
+        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        if (x >= nitems) break;
+        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const LaPass &p = args.batch.p[it.pass];
+        const bool rev = it.rev, apart = it.apart();
+        float w[16];  // what this lane's columns i weigh
+        for (int i = 0; i < it.nb; ++i, ++m) {
+          const int nv = it.rows(i);
+          const long long row0 = it.u.t0 + (long long)it.block(i) * kC;
+          if (!F32 && m > 0 && tt == 0) bulk_wait_read0();  // the block before has been read out of the staging tile
+          role_sync<2, kOutThreads>();
+          if (unlikely(i == 0 || (rev && i == 1))) {  // in order the weights of a shorter block are those of a full one
+            for (int r = tt; r < kC; r += kOutThreads)
+              tab.out[r] = p.o_scale * la_pow(it.g, rev ? max(nv - 1 - r, 0) : r + 1);
+            role_sync<2, kOutThreads>();
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            const float2 x = *reinterpret_cast<const float2 *>(t + 8 * m);
-            w[2 * m] = x.x;
-            w[2 * m + 1] = x.y;
-          }
-        }
-        if (!p.o_f32 && i > 0) {  // the block before has been read out of the staging tile
-          if (tt == 0) bulk_wait_read0();
-          asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
-        }
-        auto emit = [&](int half, const uint32_t(&a)[32]) {  // 16 lanes (columns of v) x 64 rows i
-          if (p.o_f32) {
-            float *dst = static_cast<float *>(p.o) + row0 * p.os + (long long)h * p.dv;
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int r = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1), c = 32 * quad + 16 * half + (lane >> 2) + 4 * (x & 2);
-              if (r < nv && c < p.dv) dst[r * p.os + c] = __uint_as_float(a[x]);
-            }
-          } else {
-            const int c = fc + 16 * half;
-            // 8 rows on it is the same place in the swizzle
-            const uint32_t to = so + (uint32_t)(c >> 6) * kBox + sw128_offset(fi, c & 63);
-#pragma unroll
-            for (int m = 0; m < 8; m += 2) {
-              uint32_t f[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                f[x] = tc::pack_bf16x2(__uint_as_float(a[4 * m + 2 * x]), __uint_as_float(a[4 * m + 2 * x + 1]));
-              stmatrix4_trans(to + m * 1024, f[0], f[1], f[2], f[3]);
+            for (int e = 0; e < 8; ++e) {
+              const float2 t = *reinterpret_cast<const float2 *>(tab.out + 8 * e + 2 * (lane & 3));
+              w[2 * e] = t.x;
+              w[2 * e + 1] = t.y;
             }
           }
-        };
-        const uint32_t lo = pipe::tmem_quad(tmem, apart || (i & 1) ? kTmOi : kTmO), hi = lo + (16u << 16);
-        mbar_wait(&bar.o_full[i & 1], parity(i / 2), wait);
-        tc_fence_after();
-        uint32_t a[32], b[32];
-        tmem_ld_16x256_async(lo, a);
-        tmem_ld_16x256_async(hi, b);
-        tmem_wait_ld32(a);
-        tmem_wait_ld32(b);
+          auto emit = [&](int half, const uint32_t(&a)[32]) {  // 16 lanes (columns of v) x 64 rows i
+            if (F32) {
+              float *dst = static_cast<float *>(p.o) + row0 * p.os + (long long)it.h * p.dv;
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float t = w[2 * (x >> 2) + (x & 1)];
-          a[x] = __float_as_uint(t * __uint_as_float(a[x]));
-          b[x] = __float_as_uint(t * __uint_as_float(b[x]));
-        }
-        if (apart) {
+              for (int e = 0; e < 32; ++e) {
+                const int r = 8 * (e >> 2) + 2 * (lane & 3) + (e & 1), c = 32 * quad + 16 * half + (lane >> 2) + 4 * (e & 2);
+                if (r < nv && c < p.dv) dst[r * p.os + c] = __uint_as_float(a[e]);
+              }
+            } else {
+              const int c = fc + 16 * half;
+              // 8 rows on it is the same place in the swizzle
+              const uint32_t to = so + (uint32_t)(c >> 6) * kBox + sw128_offset(fi, c & 63);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t t[16];
-            tmem_ld_16x256_x4_async(pipe::tmem_quad(tmem, kTmO) + ((uint32_t)(16 * (q >> 1)) << 16) + 32 * (q & 1), t);
-            tmem_wait_ld16(t);
+              for (int e = 0; e < 8; e += 2) {
+                uint32_t f[4];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              uint32_t &y = q < 2 ? a[16 * (q & 1) + x] : b[16 * (q & 1) + x];
-              y = __float_as_uint(__uint_as_float(y) + __uint_as_float(t[x]));
-            }
-          }
-        }
-        tc_fence_before();
-        pipe::warp_arrive(&bar.o_free[i & 1]);
-        emit(0, a);
-        emit(1, b);
-        if (!p.o_f32) {
-          fence_async_smem();
-          asm volatile("bar.sync 2, %0;" ::"n"(kOutThreads) : "memory");
-          if (nv < kC) {  // rows past the end belong to another sequence: row by row
-            bf16 *out = static_cast<bf16 *>(p.o) + row0 * p.os + (long long)h * p.dv;
-            for (int e = tt; e < nv * 8 * VB; e += kOutThreads) {
-              const int r = e / (8 * VB), c = 8 * (e % (8 * VB));
-              if (c < p.dv) {
-                uint4 v;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(so + (uint32_t)(c >> 6) * kBox + sw128_offset(r, c & 63)));
-                *reinterpret_cast<uint4 *>(out + r * p.os + c) = v;
+                for (int y = 0; y < 4; ++y)
+                  f[y] = tc::pack_bf16x2(__uint_as_float(a[4 * e + 2 * y]), __uint_as_float(a[4 * e + 2 * y + 1]));
+                stmatrix4_trans(to + e * 1024, f[0], f[1], f[2], f[3]);
               }
             }
-          } else if (tt == 0) {
-            for (int b = 0; b < VB; ++b)
-              if (64 * b < p.dv) tma_store_3d(&tm_o, so + b * kBox, 64 * b, h, (int)row0);
-            bulk_commit();
+          };
+          const uint32_t lo = pipe::tmem_quad(tmem, apart || (m & 1) ? kTmOi : kTmO), hi = lo + (16u << 16);
+          mbar_wait(&bar.o_full[m & 1], parity(m / 2), wait);
+          tc_fence_after();
+          uint32_t a[32], b[32];
+          tmem_ld_16x256_async(lo, a);
+          tmem_ld_16x256_async(hi, b);
+          tmem_wait_ld32(a);
+          tmem_wait_ld32(b);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float t = w[2 * (e >> 2) + (e & 1)];
+            a[e] = __float_as_uint(t * __uint_as_float(a[e]));
+            b[e] = __float_as_uint(t * __uint_as_float(b[e]));
+          }
+          if (unlikely(apart)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t t[16];
+              tmem_ld_16x256_x4_async(pipe::tmem_quad(tmem, kTmO) + ((uint32_t)(16 * (q >> 1)) << 16) + 32 * (q & 1), t);
+              tmem_wait_ld16(t);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                uint32_t &y = q < 2 ? a[16 * (q & 1) + e] : b[16 * (q & 1) + e];
+                y = __float_as_uint(__uint_as_float(y) + __uint_as_float(t[e]));
+              }
+            }
+          }
+          tc_fence_before();
+          pipe::warp_arrive(&bar.o_free[m & 1]);
+          emit(0, a);
+          emit(1, b);
+          if (!F32) {
+            fence_async_smem();
+            role_sync<2, kOutThreads>();
+            if (unlikely(nv < kC)) {  // rows past the end belong to another sequence: row by row
+              bf16 *out = static_cast<bf16 *>(p.o) + row0 * p.os + (long long)it.h * p.dv;
+              for (int e = tt; e < nv * 8 * VB; e += kOutThreads) {
+                const int r = e / (8 * VB), c = 8 * (e % (8 * VB));
+                if (c < p.dv) {
+                  uint4 v;
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                               : "r"(so + (uint32_t)(c >> 6) * kBox + sw128_offset(r, c & 63)));
+                  *reinterpret_cast<uint4 *>(out + r * p.os + c) = v;
+                }
+              }
+            } else if (tt == 0) {
+              for (int b2 = 0; b2 < VB; ++b2)
+                if (64 * b2 < p.dv) tma_store_3d(&args.maps[it.pass].o, so + b2 * kBox, 64 * b2, it.h, (int)row0);
+              bulk_commit();
+            }
           }
         }
       }
@@ -493,142 +608,168 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ state
     asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     if ((warp & 3) < 2 * VB) {
-    constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
-    const int quad = warp & 3, sub = (warp - kStateWarp0) >> 2;  // two warps share a quadrant of lanes
-    const int c = 32 * quad + lane, a0 = sub * kCols;
-    uint64_t S[kCols / 2];  // pairs along dk
-    {
-      int sa, sb;
-      const float *in = SUMMARY ? nullptr : la_state_in(p, u, unit, h, sa, sb);
-      const bool live = in && c < p.dv;
+      constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
+      const int quad = warp & 3, sub = (warp - kStateWarp0) >> 2;  // two warps share a quadrant of lanes
+      const int c = 32 * quad + lane, a0 = sub * kCols;
+      uint64_t S[kCols / 2];  // pairs along dk
+      uint32_t m = 0;
+      auto publish = [&] {  // S^T as the A operand: lane = column of v, bf16 pairs along dk
+        if (!SUMMARY) {
+          if (m > 0) mbar_wait(bar.s_free, parity(m - 1), wait);
 #pragma unroll
-      for (int a = 0; a < kCols; a += 2) {  // dk is even
-        float x = 0.f, y = 0.f;
-        if (live && a0 + a < p.dk) {
-          x = in[(size_t)(a0 + a) * sa + (size_t)c * sb];
-          y = in[(size_t)(a0 + a + 1) * sa + (size_t)c * sb];
-        }
-        S[a / 2] = pk2(x, y);
-      }
-    }
-    auto publish = [&] {  // S^T as the A operand: lane = column of v, bf16 pairs along dk
-      if (!SUMMARY) {
+          for (int x = 0; x < kCols / 2; x += 16) {
+            uint32_t w[16];
 #pragma unroll
-        for (int x = 0; x < kCols / 2; x += 16) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float f0, f1;
-            upk2(S[x + e], f0, f1);
-            w[e] = tc::pack_bf16x2(f0, f1);
+            for (int e = 0; e < 16; ++e) {
+              float f0, f1;
+              upk2(S[x + e], f0, f1);
+              w[e] = tc::pack_bf16x2(f0, f1);
+            }
+            tmem_st16_async(pipe::tmem_quad(tmem + kTmS, a0 / 2 + x), w);
           }
-          tmem_st16_async(pipe::tmem_quad(tmem + kTmS, a0 / 2 + x), w);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        pipe::warp_arrive(bar.s_ready);
-      }
-    };
-    const float2 full = la_pow2(g, kC);
-    auto update = [&](int i) {  // the state after block i
-      const int nv = rows_of(block_of(i));
-      const float2 carry = nv == kC ? full : la_pow2(g, nv);
-      const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
-      mbar_wait(bar.w_full, parity(i), wait);
-      tc_fence_after();
-#pragma unroll
-      for (int x = 0; x < kCols; x += 32) {
-        float w[32];
-        tmem_ld32(pipe::tmem_quad(tmem + kTmW, a0 + x), w);
-        if (x + 32 == kCols) {
+          tmem_wait_st();
           tc_fence_before();
-          pipe::warp_arrive(bar.w_free);
+          pipe::warp_arrive(bar.s_ready);
         }
+      };
+      for (uint32_t n = 0;; ++n) {
+        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        if (x >= nitems) break;
+        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const LaPass &p = args.batch.p[it.pass];
+        // this item's place among the flags of the units' incoming states
+        auto flag = [&](int unit) { return pl.flags + ((size_t)it.pass * pl.units + unit) * pl.H + it.h; };
+        {
+          int sa, sb;
+          const float *in = SUMMARY ? nullptr : la_state_in(p, it.u, it.unit, it.h, sa, sb);
+          if (!SUMMARY && pl.flags && it.u.level > 0) wait_flag(flag(it.unit), wait);
+          const bool live = in && c < p.dv;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          uint64_t &t = S[x / 2 + e];
-          t = fma2(t, chi, fma2(t, clo, pk2(w[2 * e], w[2 * e + 1])));
+          for (int a = 0; a < kCols; a += 2) {  // dk is even
+            float f0 = 0.f, f1 = 0.f;
+            if (live && a0 + a < p.dk) {
+              f0 = in[(size_t)(a0 + a) * sa + (size_t)c * sb];
+              f1 = in[(size_t)(a0 + a + 1) * sa + (size_t)c * sb];
+            }
+            S[a / 2] = pk2(f0, f1);
+          }
         }
-      }
-    };
+        const float2 full = la_pow2(it.g, kC);
 #pragma unroll 1
-    for (int i = 0; i < nb; ++i) {
-      if (i > 0) {
-        update(i - 1);
-        if (!SUMMARY) mbar_wait(bar.s_free, parity(i - 1), wait);
-      }
-      publish();
-    }
-    if (nb > 0) update(nb - 1);
-    int sa, sb;
-    float *out = la_state_out(p, u, unit, h, REV, SUMMARY, sa, sb);
-    if (out && c < p.dv) {
+        for (int i = 0; i < it.nb; ++i, ++m) {
+          publish();
+          const int nv = it.rows(i);
+          const float2 carry = nv == kC ? full : la_pow2(it.g, nv);
+          const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
+          mbar_wait(bar.w_full, parity(m), wait);
+          tc_fence_after();
 #pragma unroll
-      for (int a = 0; a < kCols; a += 2) {
-        float x, y;
-        upk2(S[a / 2], x, y);
-        if (a0 + a < p.dk) {
-          out[(size_t)(a0 + a) * sa + (size_t)c * sb] = x;
-          out[(size_t)(a0 + a + 1) * sa + (size_t)c * sb] = y;
+          for (int x2 = 0; x2 < kCols; x2 += 32) {
+            float w[32];
+            tmem_ld32(pipe::tmem_quad(tmem + kTmW, a0 + x2), w);
+            if (x2 + 32 == kCols) {
+              tc_fence_before();
+              pipe::warp_arrive(bar.w_free);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              uint64_t &t = S[x2 / 2 + e];
+              t = fma2(t, chi, fma2(t, clo, pk2(w[2 * e], w[2 * e + 1])));
+            }
+          }
+        }
+        int sa, sb;
+        const bool hand_on = SUMMARY || pl.flags;
+        float *out = la_state_out(p, it.u, it.h, hand_on, sa, sb);
+        if (out && c < p.dv && (!SUMMARY || it.u.next >= 0)) {
+#pragma unroll
+          for (int a = 0; a < kCols; a += 2) {
+            float f0, f1;
+            upk2(S[a / 2], f0, f1);
+            if (a0 + a < p.dk) {
+              out[(size_t)(a0 + a) * sa + (size_t)c * sb] = f0;
+              out[(size_t)(a0 + a + 1) * sa + (size_t)c * sb] = f1;
+            }
+          }
+        }
+        if (!SUMMARY && pl.flags && it.u.next >= 0) {  // the state warps' stores, then the flag
+          __threadfence();
+          role_sync<3, 128 * VB>();
+          if (warp == kStateWarp0 && lane == 0)
+            asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(flag(it.u.next)) : "memory");
         }
       }
-    }
     }
   } else {
     // ------------------------------------------------------------ weighted V
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    // half-blocks of 32 tokens in order; matrix loads of 8 tokens x 8 columns (lane: its
-    // address), 16 tokens and 16 columns of v at a time
     const int quad = warp & 3;
-    const uint32_t s0 = smem_u32(sm);
-    const int lr = (lane & 7) + 8 * (lane >> 4), lc = 32 * (quad & 1) + 8 * ((lane >> 3) & 1);
-#pragma unroll 1
-    for (int n = 0; n < (quad < 2 * VB ? 2 * nb : 0); ++n) {
-      const int i = n >> 1, half = n & 1, st = i % ST, nv = rows_of(block_of(i));
-      const uint32_t sv = s0 + st * L::kStage + L::kV + (uint32_t)(quad >> 1) * kBox;
-      if (half == 0) {
-        mbar_wait(&bar.full[st], parity(i / ST), wait);
-        if (nv < kC) {  // rows past the end of K and V, which are operands as they are, become zeros
-          const uint32_t sk = s0 + st * L::kStage + L::kK;  // V's boxes follow K's
-          for (int e = quad * 32 + lane; e < (kC - nv) * 8 * (KB + VB); e += 64 * VB) {
-            const int x = e % (8 * (KB + VB)), r = nv + e / (8 * (KB + VB));
-            pipe::sts_u4(sk + (uint32_t)(x >> 3) * kBox + sw128_offset(r, 8 * (x & 7)), make_uint4(0, 0, 0, 0));
+    if (quad < 2 * VB) {
+      // half-blocks of 32 tokens in order; matrix loads of 8 tokens x 8 columns (lane: its
+      // address), 16 tokens and 16 columns of v at a time
+      const uint32_t s0 = smem_u32(sm);
+      const int lr = (lane & 7) + 8 * (lane >> 4), lc = 32 * (quad & 1) + 8 * ((lane >> 3) & 1);
+      uint32_t m = 0;
+      for (uint32_t n = 0;; ++n) {
+        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        if (x >= nitems) break;
+        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const float st_scale = args.batch.p[it.pass].st_scale;
+        for (int i = 0; i < it.nb; ++i, ++m) {
+          const int st = m % ST, nv = it.rows(i);
+          if (unlikely(i == 0 || nv < kC)) {
+            role_sync<5, 64 * VB>();
+            for (int j = quad * 32 + lane; j < kC; j += 64 * VB)
+              tab.st[j] = st_scale * la_pow(it.g, it.rev ? j + 1 : max(nv - 1 - j, 0));
+            role_sync<5, 64 * VB>();
           }
-          fence_async_smem();
+          const uint32_t sv = s0 + st * L::kStage + L::kV + (uint32_t)(quad >> 1) * kBox;
+          mbar_wait(&bar.full[st], parity(m / ST), wait);
+          if (unlikely(nv < kC)) {  // rows past the end of K and V, which are operands as they are, become zeros
+            const uint32_t sk = s0 + st * L::kStage + L::kK;  // V's boxes follow K's
+            for (int e = quad * 32 + lane; e < (kC - nv) * 8 * (KB + VB); e += 64 * VB) {
+              const int y = e % (8 * (KB + VB)), r = nv + e / (8 * (KB + VB));
+              pipe::sts_u4(sk + (uint32_t)(y >> 3) * kBox + sw128_offset(r, 8 * (y & 7)), make_uint4(0, 0, 0, 0));
+            }
+            fence_async_smem();
+          }
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (m > 0) {
+              mbar_wait(&bar.v_free[half], parity(m - 1), wait);
+              tc_fence_after();
+            }
+            uint64_t w[4];  // weights of tokens 8 y + 2 (lane % 4) and the next of this half
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              w[y] = *reinterpret_cast<const uint64_t *>(tab.st + 32 * half + 8 * y + 2 * (lane & 3));
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              uint32_t f[8], t0[8], t1[8], t2[8];
+              const uint32_t row = sv + (32 * half + lr) * 128 + (uint32_t)((((lc >> 3) + 2 * q) ^ (lane & 7)) * 16);
+              ldmatrix4_trans(row, f[0], f[1], f[2], f[3]);
+              ldmatrix4_trans(row + 16 * 128, f[4], f[5], f[6], f[7]);
+              if (unlikely(nv < kC)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int j = 32 * half + 8 * (e >> 1) + 2 * (lane & 3);
+                  f[e] &= (j < nv ? 0xffffu : 0u) | (j + 1 < nv ? 0xffff0000u : 0u);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                split3(mul2(w[e >> 1], pk2(lo_f(f[e]), hi_f(f[e]))), t0[e], t1[e], t2[e]);
+              const uint32_t at = pipe::tmem_quad(tmem + kTmT + half * kHalf, 0) + ((uint32_t)(16 * q) << 16);
+              tmem_st_16x128_async(at, t0);
+              tmem_st_16x128_async(at + kTerm, t1);
+              tmem_st_16x128_async(at + 2 * kTerm, t2);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            pipe::warp_arrive(&bar.v_ready[half]);
+          }
         }
       }
-      if (i > 0) {
-        mbar_wait(&bar.v_free[half], parity(i - 1), wait);
-        tc_fence_after();
-      }
-      // weights of tokens 8 x + 2 (lane % 4) and the next of this half
-      const float *tw = tab.st[nv < kC] + 32 * half + 2 * (lane & 3);
-      uint64_t w[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) w[x] = *reinterpret_cast<const uint64_t *>(tw + 8 * x);
-#pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        uint32_t f[8], t0[8], t1[8], t2[8];
-        const uint32_t row = sv + (32 * half + lr) * 128 + (uint32_t)((((lc >> 3) + 2 * q) ^ (lane & 7)) * 16);
-        ldmatrix4_trans(row, f[0], f[1], f[2], f[3]);
-        ldmatrix4_trans(row + 16 * 128, f[4], f[5], f[6], f[7]);
-        if (nv < kC) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int j = 32 * half + 8 * (e >> 1) + 2 * (lane & 3);
-            f[e] &= (j < nv ? 0xffffu : 0u) | (j + 1 < nv ? 0xffff0000u : 0u);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split3(mul2(w[e >> 1], pk2(lo_f(f[e]), hi_f(f[e]))), t0[e], t1[e], t2[e]);
-        const uint32_t at = pipe::tmem_quad(tmem + kTmT + half * kHalf, 0) + ((uint32_t)(16 * q) << 16);
-        tmem_st_16x128_async(at, t0);
-        tmem_st_16x128_async(at + kTerm, t1);
-        tmem_st_16x128_async(at + 2 * kTerm, t2);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      pipe::warp_arrive(&bar.v_ready[half]);
     }
   }
 
@@ -640,39 +781,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int KB, int VB, bool REV, bool SUMMARY>
-void run_tc(const LaPass &p, cudaStream_t s) {
+template <int KB, int VB, bool SUMMARY, bool F32>
+void run_tc(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
   using L = Layout<KB, VB, SUMMARY>;
-  static bool once = (cudaFuncSetAttribute(la_tc_kernel<KB, VB, REV, SUMMARY>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes),
+  static bool once = (cudaFuncSetAttribute(la_tc_kernel<KB, VB, SUMMARY, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           L::kBytes),
                       true);
   (void)once;
-  CUtensorMap tq{}, tk, tv, to{};
-  if ((!SUMMARY && !encode_tmap_bf16_heads(&tq, p.q, p.dk, p.Hq, p.total, p.qs * 2, kC)) ||
-      (!SUMMARY && !p.o_f32 && !encode_tmap_bf16_heads(&to, p.o, p.dv, p.H, p.total, p.os * 2, kC)) ||
-      !encode_tmap_bf16_heads(&tk, p.k, p.dk, p.Hk, p.total, p.ks * 2, kC) ||
-      !encode_tmap_bf16_heads(&tv, p.v, p.dv, p.Hv, p.total, p.vs * 2, kC)) {
-    note_host_error();
-    return;
+  Args args;
+  args.batch = b;
+  args.pl = pl;
+  for (int i = 0; i < b.n; ++i) {
+    const LaPass &p = b.p[i];
+    Maps &mp = args.maps[i];
+    if ((!SUMMARY && !encode_tmap_bf16_heads(&mp.q, p.q, p.dk, p.Hq, pl.total, p.qs * 2, kC)) ||
+        (!SUMMARY && !F32 && !encode_tmap_bf16_heads(&mp.o, p.o, p.dv, p.H, pl.total, p.os * 2, kC)) ||
+        !encode_tmap_bf16_heads(&mp.k, p.k, p.dk, p.Hk, pl.total, p.ks * 2, kC) ||
+        !encode_tmap_bf16_heads(&mp.v, p.v, p.dv, p.Hv, pl.total, p.vs * 2, kC)) {
+      note_host_error();
+      return;
+    }
   }
-  la_tc_kernel<KB, VB, REV, SUMMARY><<<(unsigned)p.H * (unsigned)p.nunits, kThreads, L::kBytes, s>>>(tq, tk, tv, to, p);
+  const long long items = (long long)pl.units * b.n * pl.H;
+  const int grid = items < device_sm_count() ? (int)items : device_sm_count();
+  la_tc_kernel<KB, VB, SUMMARY, F32><<<grid, kThreads, L::kBytes, s>>>(args);
 }
 
 template <int KB, int VB>
-void run_tc_mode(const LaPass &p, bool reverse, bool summary, cudaStream_t s) {
-  if (reverse)
-    summary ? run_tc<KB, VB, true, true>(p, s) : run_tc<KB, VB, true, false>(p, s);
+void run_tc_mode(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s) {
+  if (summary)
+    run_tc<KB, VB, true, false>(pl, b, s);
   else
-    summary ? run_tc<KB, VB, false, true>(p, s) : run_tc<KB, VB, false, false>(p, s);
+    b.p[0].o_f32 ? run_tc<KB, VB, false, true>(pl, b, s) : run_tc<KB, VB, false, false>(pl, b, s);
 }
 
 }  // namespace
 
-void launch_la_tc(const LaPass &p, bool reverse, bool summary, cudaStream_t s) {
-  if (p.dk <= 64)
-    p.dv <= 64 ? run_tc_mode<1, 1>(p, reverse, summary, s) : run_tc_mode<1, 2>(p, reverse, summary, s);
+void launch_la_tc(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s) {
+  const int kb = la_tc_boxes(b.p[0].dk), vb = la_tc_boxes(b.p[0].dv);
+  if (kb == 1)
+    vb == 1 ? run_tc_mode<1, 1>(pl, b, summary, s) : run_tc_mode<1, 2>(pl, b, summary, s);
   else
-    p.dv <= 64 ? run_tc_mode<2, 1>(p, reverse, summary, s) : run_tc_mode<2, 2>(p, reverse, summary, s);
+    vb == 1 ? run_tc_mode<2, 1>(pl, b, summary, s) : run_tc_mode<2, 2>(pl, b, summary, s);
 }
 
 }  // namespace ssd

@@ -19,6 +19,11 @@
 
 namespace ssd {
 
+// packed calls of more sequences are never cut
+constexpr int kLaMaxCutSeqs = 1024;
+// work counters of a call: two for each of up to three batches of passes
+constexpr int kLaCounterWords = 6;
+
 struct LaPass {
   const void *q, *k, *v;
   void *o;
@@ -26,113 +31,106 @@ struct LaPass {
   int gq, gk, gv;            // query heads that share one head of the role's tensor
   int dk, dv;                // widths of the q/k roles and of the v/o roles
   int H, Hq, Hk, Hv;         // query heads; heads of each role's tensor
-  float o_scale;             // factor of the output
-  float p_scale;             // factor of the products inside a block, on top of it
-  float st_scale;            // factor of what is added to the state
-  const float *g;            // (H) log decays
+  bool reverse;
+  float o_scale;   // factor of the output
+  float p_scale;   // factor of the products inside a block, on top of it
+  float st_scale;  // factor of what is added to the state
+  const float *g;  // (H) log decays
   // states, element (a, b) of a (dk x dv) state at a * sa + b * sb
   const float *init;
   float *fin;
   int sa, sb;
-  // sequences
-  int nseq, seqlen, total;
+  float *seg_state;  // (units, H, dk, dv): a cut sequence's segment states
+  bool o_f32;        // o is fp32 whatever the inputs' type
+};
+
+// A unit is one segment of one sequence: its level-th in processing order.  Units are
+// numbered level by level (all first segments, then all second ones, ...), so
+// that whoever takes them in order never waits for a unit that nobody has taken.
+struct LaEntry {
+  int seq, level, nseg, a, len, next;  // a, len: the sequence's rows; next: the unit after it, or -1
+};
+// The sequences and how they are cut; common to the passes of a call.
+struct LaPlanDev {
+  int nseq, seqlen, total, H;
   const int *cu;
-  int seg_len;  // tokens of a segment (a multiple of the blocks' tokens)
-  int nunits;   // upper bound of the segments of all sequences
-  bool split;   // sequences longer than seg_len are cut: seg_state[u, h] holds their segments' states
-  float *seg_state;
-  bool o_f32;  // o is fp32 whatever the inputs' type
-  int *status;
+  int seg_len;            // tokens of a segment, a multiple of the blocks' tokens
+  int units;              // units, or with a table an upper bound of them
+  const LaEntry *table;   // packed sequences that may be cut: written by la_table_kernel
+  const int *table_units; // and their number
+  int *status;            // status word
+  int *counters;          // work counters of the persistent kernels: two for each batch of passes
+  int *flags;             // (passes, units, H): the unit's incoming state is written (chained segments), or null
   unsigned long long wait_ns;
 };
-
-// One segment of a sequence: tokens [t0, t0 + len) of the rows, seg-th of its sequence.
-struct LaUnit {
-  int seq, seg, nseg, t0, len;
+// Passes that one launch works on.
+struct LaBatch {
+  LaPass p[3];
+  int n;
 };
 
-__device__ __forceinline__ void la_seq_bounds(const LaPass &p, int s, int &a, int &len) {
-  if (p.cu) {
-    a = min(max(__ldg(p.cu + s), 0), p.total);
-    len = max(min(max(__ldg(p.cu + s + 1), 0), p.total) - a, 0);
+__device__ __forceinline__ void la_seq_bounds(const LaPlanDev &pl, int s, int &a, int &len) {
+  if (pl.cu) {
+    a = min(max(__ldg(pl.cu + s), 0), pl.total);
+    len = max(min(max(__ldg(pl.cu + s + 1), 0), pl.total) - a, 0);
   } else {
-    a = s * p.seqlen;
-    len = p.seqlen;
+    a = s * pl.seqlen;
+    len = pl.seqlen;
   }
 }
 // segments of a sequence (an empty one has one empty segment, so that its state is passed on)
-__device__ __forceinline__ int la_segments(const LaPass &p, int len) {
-  return len <= p.seg_len ? 1 : (len - 1) / p.seg_len + 1;
+__host__ __device__ __forceinline__ int la_segments(int len, int seg_len) {
+  return len <= seg_len ? 1 : (len - 1) / seg_len + 1;
 }
+__device__ __forceinline__ int la_units(const LaPlanDev &pl) { return pl.table ? *pl.table_units : pl.units; }
 
-// Segment u of all sequences in order; by a full warp.  false: there is no such segment.
-__device__ __forceinline__ bool la_find_unit(const LaPass &p, int u, LaUnit &out) {
-  int s, seg, a, len;
-  if (!p.cu) {
-    const int per = la_segments(p, p.seqlen);
-    s = u / per;
-    seg = u - s * per;
-    if (s >= p.nseq) return false;
+struct LaUnit {
+  int seq, level, nseg, next, t0, len;  // rows [t0, t0 + len)
+};
+__device__ __forceinline__ LaUnit la_unit(const LaPlanDev &pl, int unit, bool reverse) {
+  LaUnit u;
+  int a, len;
+  if (pl.table) {
+    const LaEntry &e = pl.table[unit];
+    u.seq = e.seq;
+    u.level = e.level;
+    u.nseg = e.nseg;
+    u.next = e.next;
+    a = e.a;
+    len = e.len;
   } else {
-    const int lane = threadIdx.x & 31;
-    int base = 0;
-    s = -1;
-    seg = 0;
-    for (int s0 = 0; s0 < p.nseq; s0 += 32) {
-      int n = 0;
-      if (s0 + lane < p.nseq) {
-        la_seq_bounds(p, s0 + lane, a, len);
-        n = la_segments(p, len);
-      }
-      int inc = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += x;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, base + inc > u);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        s = s0 + l;
-        seg = u - base - __shfl_sync(0xffffffffu, inc - n, l);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (s < 0) return false;
+    u.level = unit / pl.nseq;
+    u.seq = unit - u.level * pl.nseq;
+    la_seq_bounds(pl, u.seq, a, len);
+    u.nseg = pl.cu ? 1 : la_segments(len, pl.seg_len);
+    u.next = u.level + 1 < u.nseg ? unit + pl.nseq : -1;
   }
-  la_seq_bounds(p, s, a, len);
-  out.seq = s;
-  out.seg = seg;
-  out.t0 = a + seg * p.seg_len;
-  out.len = min(p.seg_len, len - seg * p.seg_len);
-  out.nseg = la_segments(p, len);
-  return true;
+  const int seg = reverse ? u.nseg - 1 - u.level : u.level;
+  u.t0 = a + seg * pl.seg_len;
+  u.len = u.nseg == 1 ? len : min(pl.seg_len, len - seg * pl.seg_len);
+  return u;
 }
 
 // The state before the unit's first token in processing order, or null (zero), and its strides: the segment's, or
-// the user's for a sequence that is not cut.
+// the user's for a sequence's first segment.
 __device__ __forceinline__ const float *la_state_in(const LaPass &p, const LaUnit &u, int unit, int h, int &sa, int &sb) {
   const size_t dd = (size_t)p.dk * p.dv;
   sa = p.sa;
   sb = p.sb;
-  if (u.nseg == 1) return p.init ? p.init + ((size_t)u.seq * p.H + h) * dd : nullptr;
+  if (u.level == 0) return p.init ? p.init + ((size_t)u.seq * p.H + h) * dd : nullptr;
   sa = p.dv;
   sb = 1;
   return p.seg_state + ((size_t)unit * p.H + h) * dd;
 }
-// whether the unit is its sequence's last in processing order
-__device__ __forceinline__ bool la_is_last(const LaUnit &u, bool reverse) {
-  return reverse ? u.seg == 0 : u.seg == u.nseg - 1;
-}
-// Where the unit's state goes, or null: the summary's segment state, the user's final state of a sequence.
-__device__ __forceinline__ float *la_state_out(const LaPass &p, const LaUnit &u, int unit, int h, bool reverse,
-                                               bool summary, int &sa, int &sb) {
+// Where the unit's state goes, or null: with to_next the next unit's incoming state, else (and for the last
+// segment) the user's final state.
+__device__ __forceinline__ float *la_state_out(const LaPass &p, const LaUnit &u, int h, bool to_next, int &sa, int &sb) {
   const size_t dd = (size_t)p.dk * p.dv;
-  sa = summary ? p.dv : p.sa;
-  sb = summary ? 1 : p.sb;
-  if (summary) return p.seg_state + ((size_t)unit * p.H + h) * dd;
-  return p.fin && la_is_last(u, reverse) ? p.fin + ((size_t)u.seq * p.H + h) * dd : nullptr;
+  const bool last = u.next < 0;
+  sa = last ? p.sa : p.dv;
+  sb = last ? p.sb : 1;
+  if (!last) return to_next ? p.seg_state + ((size_t)u.next * p.H + h) * dd : nullptr;
+  return p.fin ? p.fin + ((size_t)u.seq * p.H + h) * dd : nullptr;
 }
 
 // lam^n in fp32; lam^0 is 1 even for a log decay of -inf
@@ -146,19 +144,23 @@ __device__ __forceinline__ float2 la_pow2(float g, int n) {
   return make_float2(hi, e - (hi - 1.f));
 }
 
-// la_simt.cu: any type and width of the envelope
-template <typename T> void launch_la_simt(const LaPass &p, bool reverse, bool summary, cudaStream_t s);
-// la_tc.cu: bf16, both widths at most 128
+// la_plan.cu: clears status, counters and flags; writes the table of units
+void launch_la_table(const LaPlanDev &pl, LaEntry *table, int *table_units, int nflags, cudaStream_t s);
+// la_simt.cu: any type and width of the envelope.  summary: the segments' own states
+// (from zero), each where the next segment's incoming state will be
+template <typename T> void launch_la_simt(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s);
+// la_tc.cu: bf16, both widths at most 128 (all passes of a batch of the same boxes and output type)
 inline bool la_tc_envelope(int dk, int dv) { return dk <= 128 && dv <= 128; }
-void launch_la_tc(const LaPass &p, bool reverse, bool summary, cudaStream_t s);
-// segment states -> incoming segment states, in place (either path)
-void launch_la_scan(const LaPass &p, bool reverse, cudaStream_t s);
+inline int la_tc_boxes(int width) { return width <= 64 ? 1 : 2; }
+void launch_la_tc(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s);
+// segments' own states -> incoming states, in place (either path)
+void launch_la_scan(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s);
 // sums fp32 (rows, H, d) over groups of query heads into (rows, Hkv, d)
 template <typename T>
 void launch_la_sum_heads(const float *in, void *out, long long os, long long rows, int Hkv, int group, int d,
                          cudaStream_t s);
 // la_step.cu
 template <typename T>
-void launch_la_step(const LaPass &p, float *states, int nslots, const int *slot_idx, cudaStream_t s);
+void launch_la_step(const LaPass &p, int rows, float *states, int nslots, const int *slot_idx, cudaStream_t s);
 
 }  // namespace ssd
