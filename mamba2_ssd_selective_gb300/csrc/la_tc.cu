@@ -153,6 +153,19 @@ __device__ __forceinline__ void split3(uint64_t x, uint32_t &a, uint32_t &b, uin
 // together are about what the instruction caches hold (with such branches in line, half
 // of all warp cycles waited for instructions).
 __device__ __forceinline__ bool unlikely(bool c) { return __builtin_expect(c, 0); }
+// A hand-off wait as mbar_wait, kept short for the same reason: the usual case (the phase completes while the
+// warp is parked) is one instruction.
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
+  const uint32_t hint = w.limit_ns < kWaitHintNs ? (uint32_t)w.limit_ns : kWaitHintNs;
+  if (__builtin_expect(mbar_try_wait_hint(bar, parity, hint), 1)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  do {
+    if (mbar_try_wait_hint(bar, parity, hint)) return true;
+    if (*reinterpret_cast<volatile int *>(w.status) != 0) return false;
+  } while (globaltimer_ns() - t0 <= w.limit_ns);
+  atomicExch(w.status, 1);
+  return false;
+}
 // barrier among a role's warps
 template <int ID, int THREADS>
 __device__ __forceinline__ void role_sync() {
@@ -303,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const int hq = it.h / p.gq, hk = it.h / p.gk, hv = it.h / p.gv;
           for (int i = 0; i < it.nb; ++i) {
             const int st = m % ST, row = it.u.t0 + it.block(i) * kC;
-            if (m >= ST && !mbar_wait(&bar.free[st], parity(m / ST - 1), wait)) {
+            if (m >= ST && !wait_on(&bar.free[st], parity(m / ST - 1), wait)) {
               ok = false;
               break;
             }
@@ -335,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                          iW = idesc_bf16(128, 64 * KB, false, true);
       auto stage = [&](uint32_t m) { return (uint64_t)((m % ST) * (L::kStage / 16)); };
       auto scores = [&](uint32_t m) {
-        mbar_wait(&bar.full[m % ST], parity(m / ST), wait);
-        if (m > 0) mbar_wait(bar.qk_free, parity(m - 1), wait);
+        wait_on(&bar.full[m % ST], parity(m / ST), wait);
+        if (m > 0) wait_on(bar.qk_free, parity(m - 1), wait);
         tc_fence_after();
 #pragma unroll
         for (int b = 0; b < KB; ++b)
@@ -346,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       };
       // W of half a block: the three terms' two steps of 16 tokens each
       auto half_w = [&](uint32_t m, int half) {
-        mbar_wait(&bar.v_ready[half], parity(m), wait);
+        wait_on(&bar.v_ready[half], parity(m), wait);
         tc_fence_after();
 #pragma unroll
         for (int t = 0; t < 3; ++t)
@@ -363,22 +376,22 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         if (!SUMMARY && it.nb > 0) scores(m);
         for (int i = 0; i < it.nb; ++i, ++m) {
           if (SUMMARY)
-            mbar_wait(&bar.full[m % ST], parity(m / ST), wait);
+            wait_on(&bar.full[m % ST], parity(m / ST), wait);
           else if (i + 1 < it.nb)
             scores(m + 1);
-          if (m > 0) mbar_wait(bar.w_free, parity(m - 1), wait);
+          if (m > 0) wait_on(bar.w_free, parity(m - 1), wait);
           half_w(m, 0);
           umma_commit_el(el, &bar.v_free[0]);
           half_w(m, 1);
           umma_commit_el(el, bar.w_full);
           umma_commit_el(el, &bar.v_free[1]);
           if (!SUMMARY) {
-            mbar_wait(bar.s_ready, parity(m), wait);
+            wait_on(bar.s_ready, parity(m), wait);
             // the accumulator of the incoming state's part and, unless apart, of the products:
             // the one of two blocks ago, or after or before a block that uses both the last one's
             const uint32_t acc = tmem + (apart || (m & 1) ? kTmOi : kTmO);
             const uint32_t back = apart || was_apart ? 1 : 2;
-            if (m >= back) mbar_wait(&bar.o_free[(m - back) & 1], parity((m - back) / 2), wait);
+            if (m >= back) wait_on(&bar.o_free[(m - back) & 1], parity((m - back) / 2), wait);
             was_apart = apart;
             tc_fence_after();
 #pragma unroll
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
               pipe::umma_ts_k_el<4>(el, acc, tmem + kTmS + 32 * b, dQ + stage(m) + b * (kBox / 16), 8, pipe::kStepK, iQK,
                                     b > 0);
             umma_commit_el(el, bar.s_free);
-            mbar_wait(&bar.p_ready[m & 1], parity(m / 2), wait);
+            wait_on(&bar.p_ready[m & 1], parity(m / 2), wait);
             tc_fence_after();
             pipe::umma_k_el<4>(el, apart ? tmem + kTmO : acc, dV + stage(m), dP + (m & 1) * (kBox / 16), pipe::kStepMN,
                                pipe::kStepK, iPV, !apart);
@@ -438,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             tab.p[r] = p.p_scale * (apart ? p.o_scale * la_pow(it.g, r) : la_pow(it.g, rev ? r + 1 - nv : -1 - r));
             role_sync<4, 64>();
           }
-          if (m >= 2) mbar_wait(&bar.p_free[m & 1], parity(m / 2 - 1), wait);
-          mbar_wait(bar.qk_full, parity(m), wait);
+          if (m >= 2) wait_on(&bar.p_free[m & 1], parity(m / 2 - 1), wait);
+          wait_on(bar.qk_full, parity(m), wait);
           tc_fence_after();
           const uint32_t dst = smem_u32(sm + L::kP + (m & 1) * kBox);
 #pragma unroll 1
@@ -549,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             }
           };
           const uint32_t lo = pipe::tmem_quad(tmem, apart || (m & 1) ? kTmOi : kTmO), hi = lo + (16u << 16);
-          mbar_wait(&bar.o_full[m & 1], parity(m / 2), wait);
+          wait_on(&bar.o_full[m & 1], parity(m / 2), wait);
           tc_fence_after();
           uint32_t a[32], b[32];
           tmem_ld_16x256_async(lo, a);
@@ -615,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       uint32_t m = 0;
       auto publish = [&] {  // S^T as the A operand: lane = column of v, bf16 pairs along dk
         if (!SUMMARY) {
-          if (m > 0) mbar_wait(bar.s_free, parity(m - 1), wait);
+          if (m > 0) wait_on(bar.s_free, parity(m - 1), wait);
 #pragma unroll
           for (int x = 0; x < kCols / 2; x += 16) {
             uint32_t w[16];
@@ -661,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const int nv = it.rows(i);
           const float2 carry = nv == kC ? full : la_pow2(it.g, nv);
           const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
-          mbar_wait(bar.w_full, parity(m), wait);
+          wait_on(bar.w_full, parity(m), wait);
           tc_fence_after();
 #pragma unroll
           for (int x2 = 0; x2 < kCols; x2 += 32) {
@@ -724,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             role_sync<5, 64 * VB>();
           }
           const uint32_t sv = s0 + st * L::kStage + L::kV + (uint32_t)(quad >> 1) * kBox;
-          mbar_wait(&bar.full[st], parity(m / ST), wait);
+          wait_on(&bar.full[st], parity(m / ST), wait);
           if (unlikely(nv < kC)) {  // rows past the end of K and V, which are operands as they are, become zeros
             const uint32_t sk = s0 + st * L::kStage + L::kK;  // V's boxes follow K's
             for (int e = quad * 32 + lane; e < (kC - nv) * 8 * (KB + VB); e += 64 * VB) {
@@ -736,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             if (m > 0) {
-              mbar_wait(&bar.v_free[half], parity(m - 1), wait);
+              wait_on(&bar.v_free[half], parity(m - 1), wait);
               tc_fence_after();
             }
             uint64_t w[4];  // weights of tokens 8 y + 2 (lane % 4) and the next of this half
