@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPlanDev pl, const _
   for (int e = p.dk * kLdC + tid; e < dkp * kLdC; e += kThreads) Qt[e] = Kt[e] = 0.f;
   {
     int sa, sb;
-    const float *in = SUMMARY ? nullptr : la_state_in(p, u, unit, h, sa, sb);
+    const float *in = SUMMARY ? nullptr : la_state_in(p, u.level, u.seq, unit, h, sa, sb);
     for (int e = tid; e < dkp * kTV; e += kThreads) {
       const int a = e / kTV, b = e % kTV;
       S[a * kLdV + b] = in && a < p.dk && b < ncol ? in[(size_t)a * sa + (size_t)(c0 + b) * sb] : 0.f;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPlanDev pl, const _
   }
   __syncthreads();
   int sa, sb;
-  float *out = la_state_out(p, u, h, SUMMARY, sa, sb);
+  float *out = la_state_out(p, u.next, u.seq, h, SUMMARY, sa, sb);
   if (out)
     for (int e = tid; e < p.dk * kTV; e += kThreads) {
       const int a = e / kTV, b = e % kTV;

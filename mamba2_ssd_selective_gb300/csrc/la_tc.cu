@@ -41,6 +41,8 @@
 // The last block of a sequence is masked: rows past its end belong to another
 // sequence, so K's and V's are replaced by zeros in shared memory (0 * NaN would be
 // NaN), scores with them are cut off, and nothing is stored there.
+#include <type_traits>
+
 #include "retention.h"
 #include "tc_pipe.cuh"
 #include "tc_util.cuh"
@@ -78,7 +80,7 @@ struct Layout {
   static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : VB * kBox);  // weights, see Tables
   static constexpr uint32_t kBar = kTab + sizeof(Tables);
   static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2 + 1 + 4 + 1 + 4 + 4 + 1;
-  static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;  // and the TMEM address, two item slots
+  static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16 + 2 * 48;  // and the TMEM address, two item numbers, two items
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -149,9 +151,9 @@ __device__ __forceinline__ void split3(uint64_t x, uint32_t &a, uint32_t &b, uin
   c = tc::pack_bf16x2(minus_lo(f0, b), minus_hi(f1, b));
 }
 
-// Branches that a block of the usual kind does not take are kept out of the loops' code: the roles' loops
-// together are about what the instruction caches hold (with such branches in line, half
-// of all warp cycles waited for instructions).
+// The roles' loops together are about what the instruction caches hold: blocks of the
+// usual kind have code of their own, without the branches of the others (with those
+// in line, half of all warp cycles waited for instructions).
 __device__ __forceinline__ bool unlikely(bool c) { return __builtin_expect(c, 0); }
 // A hand-off wait as mbar_wait, kept short for the same reason: the usual case (the phase completes while the
 // warp is parked) is one instruction.
@@ -165,6 +167,12 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, const Wa
   } while (globaltimer_ns() - t0 <= w.limit_ns);
   atomicExch(w.status, 1);
   return false;
+}
+// The n-th item's number, or `stop`: as pipe::next_unit, but the slot is given back by the caller, after it has
+// read the item.
+__device__ __forceinline__ int next_item(const pipe::UnitRing &r, uint32_t n, int stop) {
+  const bool ok = mbar_wait_drain(&r.full[n & 1], parity(n / 2));
+  return __shfl_sync(0xffffffffu, ok ? *reinterpret_cast<volatile int *>(&r.slot[n & 1]) : stop, 0);
 }
 // barrier among a role's warps
 template <int ID, int THREADS>
@@ -202,46 +210,45 @@ struct Args {
   LaPlanDev pl;
 };
 
-// One item: a unit, a pass, a query head.
+// One item: a unit, a pass, a query head.  The producer works it out and leaves it in shared memory for the
+// other roles.
 struct Item {
-  int pass, unit, h, nb;
-  bool rev;
+  int pass, unit, h, nb;  // nb: blocks
+  int rev, apart;         // apart: lam^-64 is out of reach, products and incoming state have accumulators of their own
   float g;
-  LaUnit u;
+  int seq, level, next, t0, len;  // of the unit
   template <bool SUMMARY>
-  static __device__ __forceinline__ Item get(const Args &a, int x) {
-    Item it;
+  __device__ __forceinline__ void find(const Args &a, int x) {
     const int y = x / a.pl.H;
-    it.h = x - y * a.pl.H;
-    it.unit = y / a.batch.n;
-    it.pass = y - it.unit * a.batch.n;
-    const LaPass &p = a.batch.p[it.pass];
-    it.rev = p.reverse;
-    it.g = __ldg(p.g + it.h);
-    it.u = la_unit(a.pl, it.unit, it.rev);
-    it.nb = SUMMARY && it.u.next < 0 ? 0 : (it.u.len + kC - 1) / kC;  // nothing follows a last segment
-    return it;
+    h = x - y * a.pl.H;
+    unit = y / a.batch.n;
+    pass = y - unit * a.batch.n;
+    const LaPass &p = a.batch.p[pass];
+    rev = p.reverse;
+    g = __ldg(p.g + h);
+    apart = !(g * kC > -40.f * 0.6931f);
+    const LaUnit u = la_unit(a.pl, unit, rev);
+    seq = u.seq;
+    level = u.level;
+    next = u.next;
+    t0 = u.t0;
+    len = u.len;
+    nb = SUMMARY && next < 0 ? 0 : (len + kC - 1) / kC;  // nothing follows a last segment
   }
-  // The same for a converged warp.  What comes from memory goes through a shuffle, which tells
-  // the compiler that it is the same in all lanes: else every loop and operand that
-  // depends on it leaves the uniform registers (the kernel then took twice as long).
-  template <bool SUMMARY>
-  static __device__ __forceinline__ Item get_uniform(const Args &a, int x) {
-    Item it = get<SUMMARY>(a, x);
-    it.g = __shfl_sync(0xffffffffu, it.g, 0);
-    it.nb = __shfl_sync(0xffffffffu, it.nb, 0);
-    it.u.t0 = __shfl_sync(0xffffffffu, it.u.t0, 0);
-    it.u.len = __shfl_sync(0xffffffffu, it.u.len, 0);
-    it.u.level = __shfl_sync(0xffffffffu, it.u.level, 0);
-    it.u.next = __shfl_sync(0xffffffffu, it.u.next, 0);
-    it.u.seq = __shfl_sync(0xffffffffu, it.u.seq, 0);
-    return it;
+  // A converged warp's copy.  What comes from memory goes through a shuffle, which tells the
+  // compiler that it is the same in all lanes: else loops and operands that depend on
+  // it leave the uniform registers.
+  __device__ __forceinline__ Item uniform() const {
+    Item r;
+    const volatile int *from = reinterpret_cast<const volatile int *>(this);
+    int *to = reinterpret_cast<int *>(&r);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) to[i] = __shfl_sync(0xffffffffu, from[i], 0);
+    return r;
   }
   // processing order: block i is rows [64 blk, 64 blk + nv) of the segment
   __device__ __forceinline__ int block(int i) const { return rev ? nb - 1 - i : i; }
-  __device__ __forceinline__ int rows(int i) const { return min(kC, u.len - block(i) * kC); }
-  // whether lam^-64 is out of reach: products and incoming state in accumulators of their own
-  __device__ __forceinline__ bool apart() const { return !(g * kC > -40.f * 0.6931f); }
+  __device__ __forceinline__ int rows(int i) const { return min(kC, len - block(i) * kC); }
 };
 
 // KB, VB: 64-column boxes of the q/k roles and of the v/o roles
@@ -258,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   const Bars<ST> bar(reinterpret_cast<uint64_t *>(sm + L::kBar), reinterpret_cast<int *>(tslot + 1));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   Tables &tab = *reinterpret_cast<Tables *>(sm + L::kTab);
+  Item *slots = reinterpret_cast<Item *>(tslot + 4);  // [2]
   const int nitems = __shfl_sync(0xffffffffu, la_units(pl), 0) * args.batch.n * pl.H;
 
   if (threadIdx.x == 64) {
@@ -306,16 +314,22 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         uint32_t m = 0;
         bool ok = true;
         int next = atomicAdd(counter, 1);
+#pragma unroll 1
         for (uint32_t n = 0;; ++n) {
-          const int x = pipe::publish_unit(bar.items, n, ok && (uint32_t)next < (uint32_t)nitems ? next : nitems, nitems);
-          if (x >= nitems) break;
+          const int x = ok && (uint32_t)next < (uint32_t)nitems ? next : nitems;
+          Item it;
+          if (x < nitems) it.find<SUMMARY>(args, x);
+          // the slot of two items ago has been read
+          if (n >= 2 && !mbar_wait_drain(&bar.items.free[n & 1], parity(n / 2 - 1))) ok = false;
+          slots[n & 1] = it;
+          if (pipe::publish_unit(bar.items, n, ok ? x : nitems, nitems) >= nitems) break;
           next = atomicAdd(counter, 1);
-          const Item it = Item::get<SUMMARY>(args, x);
           const LaPass &p = args.batch.p[it.pass];
           const Maps &mp = args.maps[it.pass];
           const int hq = it.h / p.gq, hk = it.h / p.gk, hv = it.h / p.gv;
+#pragma unroll 1
           for (int i = 0; i < it.nb; ++i) {
-            const int st = m % ST, row = it.u.t0 + it.block(i) * kC;
+            const int st = m % ST, row = it.t0 + it.block(i) * kC;
             if (m >= ST && !wait_on(&bar.free[st], parity(m / ST - 1), wait)) {
               ok = false;
               break;
@@ -331,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           }
         }
         // every load issued has landed before the CTA releases its shared memory
+#pragma unroll 1
         for (uint32_t x = m > ST ? m - ST : 0; x < m; ++x) mbar_wait_drain(&bar.full[x % ST], parity(x / ST));
       }
     } else if (warp == 3) {
@@ -368,12 +383,15 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       };
       uint32_t m = 0;
       bool was_apart = false;
+#pragma unroll 1
       for (uint32_t n = 0;; ++n) {
-        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        const int x = next_item(bar.items, n, nitems);
         if (x >= nitems) break;
-        const Item it = Item::get_uniform<SUMMARY>(args, x);
-        const bool apart = __shfl_sync(0xffffffffu, (int)it.apart(), 0);
+        const Item it = slots[n & 1].uniform();
+        pipe::warp_arrive(&bar.items.free[n & 1]);
+        const bool apart = it.apart;
         if (!SUMMARY && it.nb > 0) scores(m);
+#pragma unroll 1
         for (int i = 0; i < it.nb; ++i, ++m) {
           if (SUMMARY)
             wait_on(&bar.full[m % ST], parity(m / ST), wait);
@@ -412,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       // every MMA and every arrival of a commit has landed before the CTA ends
       umma_commit_el(el, bar.drain);
       mbar_wait_drain(bar.drain, 0);
+#pragma unroll 1
       for (uint32_t x = m > ST ? m - ST : 0; x < m; ++x) mbar_wait_drain(&bar.free[x % ST], parity(x / ST));
       if (m > 0) {
         mbar_wait_drain(bar.w_full, parity(m - 1));
@@ -421,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       if (!SUMMARY && m > 0) {
         mbar_wait_drain(bar.qk_full, parity(m - 1));
         mbar_wait_drain(bar.s_free, parity(m - 1));
+#pragma unroll 1
         for (uint32_t x = m > 2 ? m - 2 : 0; x < m; ++x) {
           mbar_wait_drain(&bar.p_free[x & 1], parity(x / 2));
           mbar_wait_drain(&bar.o_full[x & 1], parity(x / 2));
@@ -430,12 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       // ------------------------------------------------------------ P
       const int r = threadIdx.x;  // row of the block
       uint32_t m = 0;
+#pragma unroll 1
       for (uint32_t n = 0;; ++n) {
-        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        const int x = next_item(bar.items, n, nitems);
         if (x >= nitems) break;
-        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const Item it = slots[n & 1].uniform();
+        pipe::warp_arrive(&bar.items.free[n & 1]);
         const LaPass &p = args.batch.p[it.pass];
-        const bool rev = it.rev, apart = it.apart();
+        const bool rev = it.rev, apart = it.apart;
         // Masks of this row's bf16 pairs in the two 16-column groups that the diagonal
         // crosses (columns 32 warp and 32 warp + 16): masked scores may be NaN, so they
         // are cut off as bits, after weights that need not be right there.
@@ -444,13 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         for (int y = 0; y < 16; ++y)
           keep[y] = ((rev ? 2 * y >= lane : 2 * y <= lane) ? 0xffffu : 0u) |
                     ((rev ? 2 * y + 1 >= lane : 2 * y + 1 <= lane) ? 0xffff0000u : 0u);
-        for (int i = 0; i < it.nb; ++i, ++m) {
-          const int nv = it.rows(i);
-          if (unlikely(i == 0 || (rev && i == 1))) {  // in order the weights do not depend on nv
-            role_sync<4, 64>();
-            tab.p[r] = p.p_scale * (apart ? p.o_scale * la_pow(it.g, r) : la_pow(it.g, rev ? r + 1 - nv : -1 - r));
-            role_sync<4, 64>();
-          }
+        auto fill = [&](int nv) {  // the weights of blocks of nv rows (in order they do not depend on it)
+          role_sync<4, 64>();
+          tab.p[r] = p.p_scale * (apart ? p.o_scale * la_pow(it.g, r) : la_pow(it.g, rev ? r + 1 - nv : -1 - r));
+          role_sync<4, 64>();
+        };
+        // usual: not apart, all rows live
+        auto block = [&](auto usual, int nv) {
+          constexpr bool kUsual = decltype(usual)::value;
           if (m >= 2) wait_on(&bar.p_free[m & 1], parity(m / 2 - 1), wait);
           wait_on(bar.qk_full, parity(m), wait);
           tc_fence_after();
@@ -462,11 +485,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (rev ? at >= 0 : at < 32) {
               float s[16], v[8];
               tmem_ld16(pipe::tmem_quad(tmem + kTmQK, j0), s);
-              if (unlikely(rev && nv < kC)) {  // columns past the end are masked for the rows before it too
+              if (!kUsual && rev) {  // columns past the end are masked for the rows before it too
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[e] = j0 + e < nv ? s[e] : 0.f;
               }
-              if (unlikely(apart)) {
+              if (!kUsual && apart) {
                 const float *w = tab.p + (rev ? j0 - r : r - j0);  // where masked, whatever lies there
                 const int step = rev ? 1 : -1;
 #pragma unroll
@@ -503,6 +526,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           pipe::warp_arrive(bar.qk_free);
           fence_async_smem();
           pipe::warp_arrive(&bar.p_ready[m & 1]);
+        };
+        fill(kC);
+#pragma unroll 1
+        for (int i = 0; i < it.nb; ++i, ++m) {
+          const int nv = it.rows(i);
+          if (!apart && nv == kC) {
+            block(std::true_type{}, kC);
+          } else {
+            if (nv < kC) fill(nv);
+            block(std::false_type{}, nv);
+            if (nv < kC) fill(kC);
+          }
         }
       }
     }
@@ -516,28 +551,33 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       const int fi = 8 * (lane >> 4) + (lane & 7), fc = 32 * quad + 8 * ((lane >> 3) & 1);
       const uint32_t so = smem_u32(sm + L::kO);
       uint32_t m = 0;
+#pragma unroll 1
       for (uint32_t n = 0;; ++n) {
-        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        const int x = next_item(bar.items, n, nitems);
         if (x >= nitems) break;
-        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const Item it = slots[n & 1].uniform();
+        pipe::warp_arrive(&bar.items.free[n & 1]);
         const LaPass &p = args.batch.p[it.pass];
-        const bool rev = it.rev, apart = it.apart();
+        const bool rev = it.rev, apart = it.apart;
         float w[16];  // what this lane's columns i weigh
-        for (int i = 0; i < it.nb; ++i, ++m) {
-          const int nv = it.rows(i);
-          const long long row0 = it.u.t0 + (long long)it.block(i) * kC;
-          if (!F32 && m > 0 && tt == 0) bulk_wait_read0();  // the block before has been read out of the staging tile
+        auto fill = [&](int nv) {  // the weights of blocks of nv rows (in order those of a full one will do)
           role_sync<2, kOutThreads>();
-          if (unlikely(i == 0 || (rev && i == 1))) {  // in order the weights of a shorter block are those of a full one
-            for (int r = tt; r < kC; r += kOutThreads)
-              tab.out[r] = p.o_scale * la_pow(it.g, rev ? max(nv - 1 - r, 0) : r + 1);
-            role_sync<2, kOutThreads>();
+          for (int r = tt; r < kC; r += kOutThreads)
+            tab.out[r] = p.o_scale * la_pow(it.g, rev ? max(nv - 1 - r, 0) : r + 1);
+          role_sync<2, kOutThreads>();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 t = *reinterpret_cast<const float2 *>(tab.out + 8 * e + 2 * (lane & 3));
-              w[2 * e] = t.x;
-              w[2 * e + 1] = t.y;
-            }
+          for (int e = 0; e < 8; ++e) {
+            const float2 t = *reinterpret_cast<const float2 *>(tab.out + 8 * e + 2 * (lane & 3));
+            w[2 * e] = t.x;
+            w[2 * e + 1] = t.y;
+          }
+        };
+        // usual: not apart, all rows live
+        auto block = [&](auto usual, int nv, long long row0) {
+          constexpr bool kUsual = decltype(usual)::value;
+          if (!F32) {  // the block before has been read out of the staging tile
+            if (tt == 0) bulk_wait_read0();
+            role_sync<2, kOutThreads>();
           }
           auto emit = [&](int half, const uint32_t(&a)[32]) {  // 16 lanes (columns of v) x 64 rows i
             if (F32) {
@@ -545,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const int r = 8 * (e >> 2) + 2 * (lane & 3) + (e & 1), c = 32 * quad + 16 * half + (lane >> 2) + 4 * (e & 2);
-                if (r < nv && c < p.dv) dst[r * p.os + c] = __uint_as_float(a[e]);
+                if ((kUsual || r < nv) && c < p.dv) dst[r * p.os + c] = __uint_as_float(a[e]);
               }
             } else {
               const int c = fc + 16 * half;
@@ -561,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
               }
             }
           };
-          const uint32_t lo = pipe::tmem_quad(tmem, apart || (m & 1) ? kTmOi : kTmO), hi = lo + (16u << 16);
+          const uint32_t lo = pipe::tmem_quad(tmem, (!kUsual && apart) || (m & 1) ? kTmOi : kTmO), hi = lo + (16u << 16);
           wait_on(&bar.o_full[m & 1], parity(m / 2), wait);
           tc_fence_after();
           uint32_t a[32], b[32];
@@ -575,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             a[e] = __float_as_uint(t * __uint_as_float(a[e]));
             b[e] = __float_as_uint(t * __uint_as_float(b[e]));
           }
-          if (unlikely(apart)) {
+          if (!kUsual && apart) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t t[16];
@@ -595,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (!F32) {
             fence_async_smem();
             role_sync<2, kOutThreads>();
-            if (unlikely(nv < kC)) {  // rows past the end belong to another sequence: row by row
+            if (!kUsual && nv < kC) {  // rows past the end belong to another sequence: row by row
               bf16 *out = static_cast<bf16 *>(p.o) + row0 * p.os + (long long)it.h * p.dv;
               for (int e = tt; e < nv * 8 * VB; e += kOutThreads) {
                 const int r = e / (8 * VB), c = 8 * (e % (8 * VB));
@@ -608,10 +648,23 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 }
               }
             } else if (tt == 0) {
-              for (int b2 = 0; b2 < VB; ++b2)
-                if (64 * b2 < p.dv) tma_store_3d(&args.maps[it.pass].o, so + b2 * kBox, 64 * b2, it.h, (int)row0);
+              for (int y = 0; y < VB; ++y)
+                if (64 * y < p.dv) tma_store_3d(&args.maps[it.pass].o, so + y * kBox, 64 * y, it.h, (int)row0);
               bulk_commit();
             }
+          }
+        };
+        fill(kC);
+#pragma unroll 1
+        for (int i = 0; i < it.nb; ++i, ++m) {
+          const int nv = it.rows(i);
+          const long long row0 = it.t0 + (long long)it.block(i) * kC;
+          if (!apart && nv == kC) {
+            block(std::true_type{}, kC, row0);
+          } else {
+            if (rev && nv < kC) fill(nv);
+            block(std::false_type{}, nv, row0);
+            if (rev && nv < kC) fill(kC);
           }
         }
       }
@@ -645,17 +698,19 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           pipe::warp_arrive(bar.s_ready);
         }
       };
+#pragma unroll 1
       for (uint32_t n = 0;; ++n) {
-        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        const int x = next_item(bar.items, n, nitems);
         if (x >= nitems) break;
-        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const Item it = slots[n & 1].uniform();
+        pipe::warp_arrive(&bar.items.free[n & 1]);
         const LaPass &p = args.batch.p[it.pass];
         // this item's place among the flags of the units' incoming states
         auto flag = [&](int unit) { return pl.flags + ((size_t)it.pass * pl.units + unit) * pl.H + it.h; };
         {
           int sa, sb;
-          const float *in = SUMMARY ? nullptr : la_state_in(p, it.u, it.unit, it.h, sa, sb);
-          if (!SUMMARY && pl.flags && it.u.level > 0) wait_flag(flag(it.unit), wait);
+          const float *in = SUMMARY ? nullptr : la_state_in(p, it.level, it.seq, it.unit, it.h, sa, sb);
+          if (!SUMMARY && pl.flags && it.level > 0) wait_flag(flag(it.unit), wait);
           const bool live = in && c < p.dv;
 #pragma unroll
           for (int a = 0; a < kCols; a += 2) {  // dk is even
@@ -672,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         for (int i = 0; i < it.nb; ++i, ++m) {
           publish();
           const int nv = it.rows(i);
-          const float2 carry = nv == kC ? full : la_pow2(it.g, nv);
+          float2 carry = full;
+          if (unlikely(nv < kC)) carry = la_pow2(it.g, nv);
           const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
           wait_on(bar.w_full, parity(m), wait);
           tc_fence_after();
@@ -693,8 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         }
         int sa, sb;
         const bool hand_on = SUMMARY || pl.flags;
-        float *out = la_state_out(p, it.u, it.h, hand_on, sa, sb);
-        if (out && c < p.dv && (!SUMMARY || it.u.next >= 0)) {
+        float *out = la_state_out(p, it.next, it.seq, it.h, hand_on, sa, sb);
+        if (out && c < p.dv && (!SUMMARY || it.next >= 0)) {
 #pragma unroll
           for (int a = 0; a < kCols; a += 2) {
             float f0, f1;
@@ -705,11 +761,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             }
           }
         }
-        if (!SUMMARY && pl.flags && it.u.next >= 0) {  // the state warps' stores, then the flag
+        if (!SUMMARY && pl.flags && it.next >= 0) {  // the state warps' stores, then the flag
           __threadfence();
           role_sync<3, 128 * VB>();
           if (warp == kStateWarp0 && lane == 0)
-            asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(flag(it.u.next)) : "memory");
+            asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(flag(it.next)) : "memory");
         }
       }
     }
@@ -723,22 +779,26 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       const uint32_t s0 = smem_u32(sm);
       const int lr = (lane & 7) + 8 * (lane >> 4), lc = 32 * (quad & 1) + 8 * ((lane >> 3) & 1);
       uint32_t m = 0;
+#pragma unroll 1
       for (uint32_t n = 0;; ++n) {
-        const int x = __shfl_sync(0xffffffffu, pipe::next_unit(bar.items, n, nitems, true), 0);
+        const int x = next_item(bar.items, n, nitems);
         if (x >= nitems) break;
-        const Item it = Item::get_uniform<SUMMARY>(args, x);
+        const Item it = slots[n & 1].uniform();
+        pipe::warp_arrive(&bar.items.free[n & 1]);
         const float st_scale = args.batch.p[it.pass].st_scale;
-        for (int i = 0; i < it.nb; ++i, ++m) {
-          const int st = m % ST, nv = it.rows(i);
-          if (unlikely(i == 0 || nv < kC)) {
-            role_sync<5, 64 * VB>();
-            for (int j = quad * 32 + lane; j < kC; j += 64 * VB)
-              tab.st[j] = st_scale * la_pow(it.g, it.rev ? j + 1 : max(nv - 1 - j, 0));
-            role_sync<5, 64 * VB>();
-          }
+        auto fill = [&](int nv) {  // the weights of blocks of nv rows
+          role_sync<5, 64 * VB>();
+          for (int j = quad * 32 + lane; j < kC; j += 64 * VB)
+            tab.st[j] = st_scale * la_pow(it.g, it.rev ? j + 1 : max(nv - 1 - j, 0));
+          role_sync<5, 64 * VB>();
+        };
+        // usual: all rows live
+        auto block = [&](auto usual, int nv) {
+          constexpr bool kUsual = decltype(usual)::value;
+          const int st = m % ST;
           const uint32_t sv = s0 + st * L::kStage + L::kV + (uint32_t)(quad >> 1) * kBox;
           wait_on(&bar.full[st], parity(m / ST), wait);
-          if (unlikely(nv < kC)) {  // rows past the end of K and V, which are operands as they are, become zeros
+          if (!kUsual) {  // rows past the end of K and V, which are operands as they are, become zeros
             const uint32_t sk = s0 + st * L::kStage + L::kK;  // V's boxes follow K's
             for (int e = quad * 32 + lane; e < (kC - nv) * 8 * (KB + VB); e += 64 * VB) {
               const int y = e % (8 * (KB + VB)), r = nv + e / (8 * (KB + VB));
@@ -762,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
               const uint32_t row = sv + (32 * half + lr) * 128 + (uint32_t)((((lc >> 3) + 2 * q) ^ (lane & 7)) * 16);
               ldmatrix4_trans(row, f[0], f[1], f[2], f[3]);
               ldmatrix4_trans(row + 16 * 128, f[4], f[5], f[6], f[7]);
-              if (unlikely(nv < kC)) {
+              if (!kUsual) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                   const int j = 32 * half + 8 * (e >> 1) + 2 * (lane & 3);
@@ -780,6 +840,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             tmem_wait_st();
             tc_fence_before();
             pipe::warp_arrive(&bar.v_ready[half]);
+          }
+        };
+        fill(kC);
+#pragma unroll 1
+        for (int i = 0; i < it.nb; ++i, ++m) {
+          const int nv = it.rows(i);
+          if (nv == kC) {
+            block(std::true_type{}, kC);
+          } else {
+            fill(nv);
+            block(std::false_type{}, nv);
+            fill(kC);
           }
         }
       }

@@ -113,24 +113,25 @@ __device__ __forceinline__ LaUnit la_unit(const LaPlanDev &pl, int unit, bool re
 
 // The state before the unit's first token in processing order, or null (zero), and its strides: the segment's, or
 // the user's for a sequence's first segment.
-__device__ __forceinline__ const float *la_state_in(const LaPass &p, const LaUnit &u, int unit, int h, int &sa, int &sb) {
+__device__ __forceinline__ const float *la_state_in(const LaPass &p, int level, int seq, int unit, int h, int &sa,
+                                                       int &sb) {
   const size_t dd = (size_t)p.dk * p.dv;
   sa = p.sa;
   sb = p.sb;
-  if (u.level == 0) return p.init ? p.init + ((size_t)u.seq * p.H + h) * dd : nullptr;
+  if (level == 0) return p.init ? p.init + ((size_t)seq * p.H + h) * dd : nullptr;
   sa = p.dv;
   sb = 1;
   return p.seg_state + ((size_t)unit * p.H + h) * dd;
 }
 // Where the unit's state goes, or null: with to_next the next unit's incoming state, else (and for the last
 // segment) the user's final state.
-__device__ __forceinline__ float *la_state_out(const LaPass &p, const LaUnit &u, int h, bool to_next, int &sa, int &sb) {
+__device__ __forceinline__ float *la_state_out(const LaPass &p, int next, int seq, int h, bool to_next, int &sa, int &sb) {
   const size_t dd = (size_t)p.dk * p.dv;
-  const bool last = u.next < 0;
+  const bool last = next < 0;
   sa = last ? p.sa : p.dv;
   sb = last ? p.sb : 1;
-  if (!last) return to_next ? p.seg_state + ((size_t)u.next * p.H + h) * dd : nullptr;
-  return p.fin ? p.fin + ((size_t)u.seq * p.H + h) * dd : nullptr;
+  if (!last) return to_next ? p.seg_state + ((size_t)next * p.H + h) * dd : nullptr;
+  return p.fin ? p.fin + ((size_t)seq * p.H + h) * dd : nullptr;
 }
 
 // lam^n in fp32; lam^0 is 1 even for a log decay of -inf
