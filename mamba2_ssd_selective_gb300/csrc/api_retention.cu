@@ -1,6 +1,8 @@
 // C ABI of linear attention with a decay for each head and of group norm with
 // an activation: argument checks, workspace carving and launch sequences.
 // Nothing here allocates or synchronises.
+#include <cmath>
+
 #include "group_norm.h"
 #include "retention.h"
 
@@ -52,12 +54,18 @@ bool la_use_tc(const ssd_linear_attn_dims *d) {
 //
 // Cut side by side, a sequence's segments run at once: their own states first (a second
 // read of k and v), a scan, then the pass.  That pays where whole sequences
-// leave at least half of the GPU idle: one sequence of 31991 tokens, 16 heads of 128,
-// takes 950 us whole, 160 us in 9 segments.
+// leave at least half of the GPU idle.
 // Chained (tensor cores), segments of all sequences are items of a queue in order of
 // their level, a segment's state handed to the next: nothing is done twice, and SMs
-// that finish early take over.  That pays where there are more sequences than SMs
-// but not a multiple of them, or of different lengths.
+// that finish early take over.  Handing over costs the time of about three blocks of 64
+// tokens, so that a call of c segments a sequence takes
+//     max(c, items c / SMs, rounded up) x (blocks of a segment + 3)
+// and the c of the least is taken: 192 items of 8192 tokens of 128 (two sequences' backward pass, 32
+// heads) took 349 us whole (two rounds of 128 + 3 blocks), 288 us in 4 segments (210 blocks by the formula),
+// 301 us in 8 (209), and 3 (184) are taken: 262 us.
+// Lengths of packed sequences are not known here.  There a segment is long enough for its hand-over to
+// be small, at the least 2048 tokens: 24 sequences of 1 to 4487 tokens, 16 heads, took 107 us
+// whole, 104 us in segments of 1024, 94 us in segments of 2048.
 LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
   LaPlan pl{};
   const bool tc = la_use_tc(d);
@@ -71,10 +79,24 @@ LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
   if (d->packed && n > kLaMaxCutSeqs) {
     pl.cut = LaPlan::kWhole;
   } else if (n * blocks >= want) {
-    seg = (rows * blocks / (4 * sms) + 63) / 64 * 64;
-    if (seg < 1024) seg = 1024;
-    const bool fits = (rows / seg + n) * blocks < (1LL << 28);  // item numbers are 32-bit
-    pl.cut = tc && fits && 2 * longest > 3 * seg && (d->packed || n * blocks % sms) ? LaPlan::kChained : LaPlan::kWhole;
+    if (tc && d->packed) {
+      // hand-overs in all against the last items' idle SMs
+      seg = (long long)std::sqrt(384. * (double)(rows * blocks / sms)) / 64 * 64;
+      if (seg < 2048) seg = 2048;
+    } else if (tc) {
+      const long long tiles = (longest + 63) / 64;
+      long long best = 0;
+      for (long long c = 1; c <= 32 && c <= tiles; ++c) {
+        const long long rounds = (n * blocks * c + sms - 1) / sms, each = (tiles + c - 1) / c;
+        const long long cost = (rounds > c ? rounds : c) * (each + 3);
+        if (c == 1 || cost < best) {
+          best = cost;
+          seg = each * 64;
+        }
+      }
+    }
+    const bool fits = tc && (rows / seg + n) * blocks < (1LL << 28);  // item numbers are 32-bit
+    pl.cut = fits && seg < longest ? LaPlan::kChained : LaPlan::kWhole;
   } else {
     const long long cuts = want / (n * blocks);
     seg = d->packed ? rows * blocks / want : (longest + cuts - 1) / cuts;

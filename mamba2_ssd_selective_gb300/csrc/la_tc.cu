@@ -527,17 +527,15 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           fence_async_smem();
           pipe::warp_arrive(&bar.p_ready[m & 1]);
         };
-        fill(kC);
+        int have = 0;  // rows that the weights are for
 #pragma unroll 1
         for (int i = 0; i < it.nb; ++i, ++m) {
           const int nv = it.rows(i);
-          if (!apart && nv == kC) {
+          if (nv != have) fill(have = nv);
+          if (!apart && nv == kC)
             block(std::true_type{}, kC);
-          } else {
-            if (nv < kC) fill(nv);
+          else
             block(std::false_type{}, nv);
-            if (nv < kC) fill(kC);
-          }
         }
       }
     }
@@ -654,18 +652,16 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             }
           }
         };
-        fill(kC);
+        int have = 0;  // rows that the weights are for
 #pragma unroll 1
         for (int i = 0; i < it.nb; ++i, ++m) {
           const int nv = it.rows(i);
           const long long row0 = it.t0 + (long long)it.block(i) * kC;
-          if (!apart && nv == kC) {
+          if (nv != have) fill(have = nv);
+          if (!apart && nv == kC)
             block(std::true_type{}, kC, row0);
-          } else {
-            if (rev && nv < kC) fill(nv);
+          else
             block(std::false_type{}, nv, row0);
-            if (rev && nv < kC) fill(kC);
-          }
         }
       }
       if (tt == 0) bulk_wait0();
@@ -722,13 +718,13 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             S[a / 2] = pk2(f0, f1);
           }
         }
-        const float2 full = la_pow2(it.g, kC);
+        float2 carry = make_float2(0.f, 0.f);
+        int have = 0;  // rows that carry is for
 #pragma unroll 1
         for (int i = 0; i < it.nb; ++i, ++m) {
           publish();
           const int nv = it.rows(i);
-          float2 carry = full;
-          if (unlikely(nv < kC)) carry = la_pow2(it.g, nv);
+          if (nv != have) carry = la_pow2(it.g, have = nv);
           const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
           wait_on(bar.w_full, parity(m), wait);
           tc_fence_after();
@@ -842,17 +838,15 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             pipe::warp_arrive(&bar.v_ready[half]);
           }
         };
-        fill(kC);
+        int have = 0;  // rows that the weights are for
 #pragma unroll 1
         for (int i = 0; i < it.nb; ++i, ++m) {
           const int nv = it.rows(i);
-          if (nv == kC) {
+          if (nv != have) fill(have = nv);
+          if (nv == kC)
             block(std::true_type{}, kC);
-          } else {
-            fill(nv);
+          else
             block(std::false_type{}, nv);
-            fill(kC);
-          }
         }
       }
     }
