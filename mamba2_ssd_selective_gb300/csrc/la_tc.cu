@@ -62,6 +62,7 @@ constexpr uint32_t kBox = 8192;  // [64 tokens x 64 columns] bf16
 
 // TMEM columns: scores, two accumulators of outputs (or O and Oi), W, S^T (bf16), two buffers of the three terms of half a block
 constexpr uint32_t kTmQK = 0, kTmO = 64, kTmOi = 128, kTmW = 192, kTmS = 320, kTmT = 384, kTmCols = 512;
+constexpr uint32_t kTmW1 = 0;  // summaries, which need nothing else: W's second buffer
 constexpr uint32_t kTerm = 16, kHalf = 3 * kTerm;  // a term of half a block (32 tokens as bf16 pairs)
 
 // Weights of a block's rows, each filled by the role that reads it.
@@ -79,7 +80,7 @@ struct Layout {
   static constexpr uint32_t kO = kP + (SUMMARY ? 0 : 2 * kBox);     // a block's outputs, on their way to TMA
   static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : VB * kBox);  // weights, see Tables
   static constexpr uint32_t kBar = kTab + sizeof(Tables);
-  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2 + 1 + 4 + 1 + 4 + 4 + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2 + 2 + 4 + 2 + 4 + 4 + 1;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16 + 2 * 48;  // and the TMEM address, two item numbers, two items
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
@@ -91,9 +92,8 @@ struct Bars {
   uint64_t *qk_full, *qk_free;  // scores
   uint64_t *p_ready, *p_free;   // [2]
   uint64_t *s_ready, *s_free;   // S^T of the block in TMEM / read by its product
-  uint64_t *w_free;             // the previous block's W read out of TMEM
   uint64_t *v_ready, *v_free;   // [2] half a block's terms in TMEM / read by its MMAs
-  uint64_t *w_full;             // W formed
+  uint64_t *w_full, *w_free;    // [2] W formed / read out of TMEM (summaries: two buffers, else one)
   uint64_t *o_full, *o_free;    // [2]
   pipe::UnitRing items;
   uint64_t *drain;
@@ -107,10 +107,10 @@ struct Bars {
     s_ready = p_free + 2;
     s_free = s_ready + 1;
     w_free = s_free + 1;
-    v_ready = w_free + 1;
+    v_ready = w_free + 2;
     v_free = v_ready + 2;
     w_full = v_free + 2;
-    o_full = w_full + 1;
+    o_full = w_full + 2;
     o_free = o_full + 2;
     items.full = o_free + 2;
     items.free = items.full + 2;
@@ -151,10 +151,11 @@ __device__ __forceinline__ void split3(uint64_t x, uint32_t &a, uint32_t &b, uin
   c = tc::pack_bf16x2(minus_lo(f0, b), minus_hi(f1, b));
 }
 
-// The roles' loops together are about what the instruction caches hold: blocks of the
-// usual kind have code of their own, without the branches of the others (with those
-// in line, half of all warp cycles waited for instructions).
-__device__ __forceinline__ bool unlikely(bool c) { return __builtin_expect(c, 0); }
+// The roles' loops together are more than the instruction caches hold at once, and code
+// that all of them hold in line is what made them so: items are worked out by the producer alone, weights are
+// filled at one place of a role, blocks of the usual kind have code of their own without the branches of the
+// others.  32 heads of 4 sequences of 8192 tokens, widths of 128: 263 us with each role working out its
+// items, 202 us with the producer, 181 us with one fill, 190 us without the split of the usual blocks.
 // A hand-off wait as mbar_wait, kept short for the same reason: the usual case (the phase completes while the
 // warp is parked) is one instruction.
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
@@ -283,12 +284,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       mbar_init(&bar.o_free[i], 2 * VB);
       mbar_init(&bar.v_ready[i], 2 * VB);
       mbar_init(&bar.items.full[i], 1);
-      mbar_init(&bar.items.free[i], SUMMARY ? 1 + 6 * VB : 3 + 8 * VB);  // every warp but the producer's that takes part
+      mbar_init(&bar.items.free[i], SUMMARY ? 1 + 8 * VB : 3 + 8 * VB);  // every warp but the producer's that takes part
+      mbar_init(&bar.w_full[i], 1);
+      mbar_init(&bar.w_free[i], 4 * VB);
     }
     mbar_init(bar.s_ready, 4 * VB);
-    mbar_init(bar.w_free, 4 * VB);
     mbar_init(bar.s_free, 1);
-    mbar_init(bar.w_full, 1);
     mbar_init(bar.drain, 1);
     fence_mbar_init();
   }
@@ -300,6 +301,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
+
+  // W's buffer of block m, and its use of it
+  auto w_at = [&](uint32_t m) { return SUMMARY ? m & 1 : 0u; };
+  auto w_use = [&](uint32_t m) { return SUMMARY ? m / 2 : m; };
+  constexpr uint32_t kWBufs = SUMMARY ? 2 : 1;
 
   // Every role counts the blocks it has been through (m): the m-th use of a barrier is
   // its m-th completion, or for pairs and rings completion m / 2 or m / ST of one of them.
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 #pragma unroll 1
         for (uint32_t n = 0;; ++n) {
           const int x = ok && (uint32_t)next < (uint32_t)nitems ? next : nitems;
-          Item it;
+          Item it{};
           if (x < nitems) it.find<SUMMARY>(args, x);
           // the slot of two items ago has been read
           if (n >= 2 && !mbar_wait_drain(&bar.items.free[n & 1], parity(n / 2 - 1))) ok = false;
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         tc_fence_after();
 #pragma unroll
         for (int t = 0; t < 3; ++t)
-          pipe::umma_ts_k_el<2>(el, tmem + kTmW, tmem + kTmT + half * kHalf + t * kTerm,
+          pipe::umma_ts_k_el<2>(el, tmem + (w_at(m) ? kTmW1 : kTmW), tmem + kTmT + half * kHalf + t * kTerm,
                                 dKn + stage(m) + half * (4096 / 16), 8, pipe::kStepMN, iW, half > 0 || t > 0);
       };
       uint32_t m = 0;
@@ -397,11 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             wait_on(&bar.full[m % ST], parity(m / ST), wait);
           else if (i + 1 < it.nb)
             scores(m + 1);
-          if (m > 0) wait_on(bar.w_free, parity(m - 1), wait);
+          if (m >= kWBufs) wait_on(&bar.w_free[w_at(m)], parity(w_use(m) - 1), wait);
           half_w(m, 0);
           umma_commit_el(el, &bar.v_free[0]);
           half_w(m, 1);
-          umma_commit_el(el, bar.w_full);
+          umma_commit_el(el, &bar.w_full[w_at(m)]);
           umma_commit_el(el, &bar.v_free[1]);
           if (!SUMMARY) {
             wait_on(bar.s_ready, parity(m), wait);
@@ -433,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 #pragma unroll 1
       for (uint32_t x = m > ST ? m - ST : 0; x < m; ++x) mbar_wait_drain(&bar.free[x % ST], parity(x / ST));
       if (m > 0) {
-        mbar_wait_drain(bar.w_full, parity(m - 1));
+#pragma unroll 1
+        for (uint32_t x = m > kWBufs ? m - kWBufs : 0; x < m; ++x) mbar_wait_drain(&bar.w_full[w_at(x)], parity(w_use(x)));
         mbar_wait_drain(&bar.v_free[0], parity(m - 1));
         mbar_wait_drain(&bar.v_free[1], parity(m - 1));
       }
@@ -539,10 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         }
       }
     }
-  } else if (warp < kStateWarp0) {
+  } else if (!SUMMARY && warp < kStateWarp0) {
     // ------------------------------------------------------------ outputs
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if (!SUMMARY && warp < kOutWarp0 + 2 * VB) {
+    if (warp < kOutWarp0 + 2 * VB) {
       constexpr int kOutThreads = 64 * VB;
       const int tt = threadIdx.x - 32 * kOutWarp0, quad = warp & 3;
       // the address this lane gives to a group of four fragments: row i, columns of v
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       }
       if (tt == 0) bulk_wait0();
     }
-  } else if (warp < kWeighWarp0) {
+  } else if (warp >= kStateWarp0 && warp < kWeighWarp0) {
     // ------------------------------------------------------------ state
     asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     if ((warp & 3) < 2 * VB) {
@@ -726,15 +733,15 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const int nv = it.rows(i);
           if (nv != have) carry = la_pow2(it.g, have = nv);
           const uint64_t chi = pk2(carry.x, carry.x), clo = pk2(carry.y, carry.y);
-          wait_on(bar.w_full, parity(m), wait);
+          wait_on(&bar.w_full[w_at(m)], parity(w_use(m)), wait);
           tc_fence_after();
 #pragma unroll
           for (int x2 = 0; x2 < kCols; x2 += 32) {
             float w[32];
-            tmem_ld32(pipe::tmem_quad(tmem + kTmW, a0 + x2), w);
+            tmem_ld32(pipe::tmem_quad(tmem + (w_at(m) ? kTmW1 : kTmW), a0 + x2), w);
             if (x2 + 32 == kCols) {
               tc_fence_before();
-              pipe::warp_arrive(bar.w_free);
+              pipe::warp_arrive(&bar.w_free[w_at(m)]);
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -767,8 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     }
   } else {
     // ------------------------------------------------------------ weighted V
+    // summaries: with the warps that have no outputs to write, each half of a block by warps of its own
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    const int quad = warp & 3;
+    constexpr int kTeam = SUMMARY ? 128 * VB : 64 * VB;
+    const int quad = warp & 3, first = SUMMARY && warp >= kWeighWarp0 ? 1 : 0, tt = quad * 32 + lane + first * 64 * VB;
     if (quad < 2 * VB) {
       // half-blocks of 32 tokens in order; matrix loads of 8 tokens x 8 columns (lane: its
       // address), 16 tokens and 16 columns of v at a time
@@ -783,10 +792,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         pipe::warp_arrive(&bar.items.free[n & 1]);
         const float st_scale = args.batch.p[it.pass].st_scale;
         auto fill = [&](int nv) {  // the weights of blocks of nv rows
-          role_sync<5, 64 * VB>();
-          for (int j = quad * 32 + lane; j < kC; j += 64 * VB)
+          role_sync<5, kTeam>();
+          for (int j = tt; j < kC; j += kTeam)
             tab.st[j] = st_scale * la_pow(it.g, it.rev ? j + 1 : max(nv - 1 - j, 0));
-          role_sync<5, 64 * VB>();
+          role_sync<5, kTeam>();
         };
         // usual: all rows live
         auto block = [&](auto usual, int nv) {
@@ -803,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             fence_async_smem();
           }
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
+          for (int half = first; half < (SUMMARY ? first + 1 : 2); ++half) {
             if (m > 0) {
               wait_on(&bar.v_free[half], parity(m - 1), wait);
               tc_fence_after();
