@@ -226,20 +226,33 @@ void la_run(const ssd_linear_attn_dims *d, const LaPlan &pl, const LaPlanDev &de
   else
     cudaMemsetAsync(ws, 0, pl.flags + (size_t)nflags * 4, s);
   const bool tc = sizeof(T) == 2 && la_use_tc(d);
-  for (int done = 0, batch = 0; done < n; ++batch) {
-    LaBatch b{};
-    LaPlanDev v = dev;
-    v.counters += 2 * batch;
-    if (v.flags) v.flags += (size_t)done * pl.units * d->nheads;
-    auto kernel = [](const LaPass &x) { return 4 * la_tc_boxes(x.dk) + 2 * la_tc_boxes(x.dv) + x.o_f32; };
-    while (done < n && (b.n == 0 || !tc || kernel(p[done]) == kernel(b.p[0]))) b.p[b.n++] = p[done++];
-    auto pass = [&](bool summary) { tc ? launch_la_tc(v, b, summary, s) : launch_la_simt<T>(v, b, summary, s); };
-    if (pl.cut == LaPlan::kSideBySide) {
-      SSD_LAUNCH("la_segment_states", pass(true));
-      SSD_LAUNCH("la_scan", launch_la_scan(v, b, s));
+  // batches of passes that one kernel takes: on the tensor cores those of the same boxes and output type
+  auto batches = [&](bool summary, auto launch) {
+    int number = 0;
+    for (int done = 0; done < n;) {
+      LaBatch b{};
+      LaPlanDev v = dev;
+      v.counters += 2 * number++;
+      if (v.flags) v.flags += (size_t)done * pl.units * d->nheads;
+      auto kernel = [&](const LaPass &x) {
+        return 4 * la_tc_boxes(x.dk) + 2 * la_tc_boxes(x.dv) + (!summary && x.o_f32);
+      };
+      for (; done < n; ++done) {
+        if (summary && p[done].seg_shared) continue;
+        if (tc && b.n > 0 && kernel(p[done]) != kernel(b.p[0])) break;
+        b.p[b.n++] = p[done];
+      }
+      launch(v, b);
     }
-    SSD_LAUNCH("la_pass", pass(false));
-  }
+  };
+  if (pl.cut == LaPlan::kSideBySide)
+    batches(true, [&](const LaPlanDev &v, const LaBatch &b) {
+      SSD_LAUNCH("la_segment_states", tc ? launch_la_tc(v, b, true, s) : launch_la_simt<T>(v, b, true, s));
+      SSD_LAUNCH("la_scan", launch_la_scan(v, b, s));
+    });
+  batches(false, [&](const LaPlanDev &v, const LaBatch &b) {
+    SSD_LAUNCH("la_pass", tc ? launch_la_tc(v, b, false, s) : launch_la_simt<T>(v, b, false, s));
+  });
 }
 
 template <typename T>
@@ -276,11 +289,14 @@ ssd_status la_backward_impl(const ssd_linear_attn_dims *d, const ssd_linear_attn
     p[i].p_scale = p[i].st_scale = in->scale;
     p[i].o_f32 = group > 1;
   }
-  la_run<T>(d, pl, la_plan_dev(d, in, pl, ws), p, 3, ws, s);
-  if (group > 1) {
-    SSD_LAUNCH("la_sum_heads", launch_la_sum_heads<T>(part_k, g->dk, g->dk_tok_stride, rows, Hkv, group, dk, s));
-    SSD_LAUNCH("la_sum_heads", launch_la_sum_heads<T>(part_v, g->dv, g->dv_tok_stride, rows, Hkv, group, dv, s));
+  if (pl.cut == LaPlan::kSideBySide) {  // both reverse passes carry the same state, one of them transposed
+    p[1].seg_state = p[2].seg_state;
+    p[1].seg_shared = true;
   }
+  la_run<T>(d, pl, la_plan_dev(d, in, pl, ws), p, 3, ws, s);
+  if (group > 1)
+    SSD_LAUNCH("la_sum_heads", launch_la_sum_heads<T>({part_k, g->dk, g->dk_tok_stride, dk},
+                                                      {part_v, g->dv, g->dv_tok_stride, dv}, rows, Hkv, group, s));
   return launch_status();
 }
 

@@ -56,7 +56,7 @@ __device__ __forceinline__ void stage_transposed(float *dst, const T *src, long 
 }
 
 template <typename T, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPlanDev pl, const __grid_constant__ LaBatch batch) {
+__global__ void __launch_bounds__(kThreads, SUMMARY ? 5 : 4) la_simt_kernel(LaPlanDev pl, const __grid_constant__ LaBatch batch) {
   extern __shared__ __align__(16) float sm[];
   const int unit = blockIdx.x;
   if (unit >= la_units(pl)) return;
@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPlanDev pl, const _
   const LaUnit u = la_unit(pl, unit, rev);
   if (SUMMARY && u.next < 0) return;  // nothing follows
   const int dkp = (p.dk + 63) & ~63;
-  float *Qt = sm, *Kt = Qt + dkp * kLdC, *S = Kt + dkp * kLdC, *V = S + dkp * kLdV, *At = V + kC * kLdV,
-        *pw = At + kC * kLdC;  // pw[0..kC]: lam^n
+  float *Qt = sm, *Kt = SUMMARY ? sm : Qt + dkp * kLdC, *S = Kt + dkp * kLdC, *V = S + dkp * kLdV, *At = V + kC * kLdV,
+        *pw = SUMMARY ? At : At + kC * kLdC;  // pw[0..kC]: lam^n
   const float p_scale = p.o_scale * p.p_scale;
   const int h = blockIdx.y, tid = threadIdx.x, ncol = min(kTV, p.dv - c0);
   const float g = __ldg(p.g + h);
@@ -79,7 +79,10 @@ __global__ void __launch_bounds__(kThreads) la_simt_kernel(LaPlanDev pl, const _
   if (tid <= kC) pw[tid] = la_pow(g, tid);
   const float2 carry_full = la_pow2(g, kC);
   // q and k rows past dk (up to the padded width) stay zero
-  for (int e = p.dk * kLdC + tid; e < dkp * kLdC; e += kThreads) Qt[e] = Kt[e] = 0.f;
+  for (int e = p.dk * kLdC + tid; e < dkp * kLdC; e += kThreads) {
+    if (!SUMMARY) Qt[e] = 0.f;
+    Kt[e] = 0.f;
+  }
   {
     int sa, sb;
     const float *in = SUMMARY ? nullptr : la_state_in(p, u.level, u.seq, unit, h, sa, sb);
@@ -277,33 +280,34 @@ __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPlanDev pl, con
   }
 }
 
-// out(row, kv, c) = sum of in(row, kv * group + i, c) over i, in order
+// out(row, kv, c) = sum of in(row, kv * group + i, c) over i, in order; blockIdx.y: which of two tensors
 template <typename T>
-__global__ void __launch_bounds__(256) la_sum_heads_kernel(const float *__restrict__ in, T *__restrict__ out,
-                                                           long long os, long long n4, int Hkv, int group, int d) {
+__global__ void __launch_bounds__(256) la_sum_heads_kernel(const LaHeadSum x, const LaHeadSum y, long long rows, int Hkv,
+                                                           int group) {
+  const LaHeadSum &p = blockIdx.y ? y : x;
   const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (e >= n4) return;
-  const int d4 = d / 4, c = (int)(e % d4);
+  const int d4 = p.d / 4, c = (int)(e % d4);
   const long long rk = e / d4, row = rk / Hkv;
+  if (row >= rows) return;
   const int kv = (int)(rk % Hkv);
-  const float4 *src = reinterpret_cast<const float4 *>(in) + (row * Hkv + kv) * (long long)group * d4 + c;
+  const float4 *src = reinterpret_cast<const float4 *>(p.in) + (row * Hkv + kv) * (long long)group * d4 + c;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   for (int i = 0; i < group; ++i) {
-    const float4 x = __ldg(src + (long long)i * d4);
-    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+    const float4 t = __ldg(src + (long long)i * d4);
+    acc[0] += t.x; acc[1] += t.y; acc[2] += t.z; acc[3] += t.w;
   }
-  store4(out + row * os + (long long)kv * d + 4 * c, acc);
+  store4(static_cast<T *>(p.out) + row * p.os + (long long)kv * p.d + 4 * c, acc);
 }
 
-constexpr int smem_bytes(int dk) {
+constexpr int smem_bytes(int dk, bool summary) {
   const int dkp = (dk + 63) & ~63;
-  return 4 * (2 * dkp * kLdC + dkp * kLdV + kC * kLdV + kC * kLdC + kC + 4);
+  return 4 * ((summary ? 1 : 2) * dkp * kLdC + dkp * kLdV + kC * kLdV + (summary ? 0 : kC * kLdC) + kC + 4);
 }
 
 template <typename T, bool SUMMARY>
 void run_simt(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
   static bool once = (cudaFuncSetAttribute(la_simt_kernel<T, SUMMARY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           smem_bytes(256)),
+                                           smem_bytes(256, SUMMARY)),
                       true);
   (void)once;
   int dk = 0, dv = 0;
@@ -312,7 +316,7 @@ void run_simt(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
     dv = b.p[i].dv > dv ? b.p[i].dv : dv;
   }
   const dim3 grid(pl.units, pl.H, (dv + kTV - 1) / kTV * b.n);
-  la_simt_kernel<T, SUMMARY><<<grid, kThreads, smem_bytes(dk), s>>>(pl, b);
+  la_simt_kernel<T, SUMMARY><<<grid, kThreads, smem_bytes(dk, SUMMARY), s>>>(pl, b);
 }
 
 }  // namespace
@@ -328,16 +332,14 @@ void launch_la_scan(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
 }
 
 template <typename T>
-void launch_la_sum_heads(const float *in, void *out, long long os, long long rows, int Hkv, int group, int d,
-                         cudaStream_t s) {
-  const long long n4 = rows * Hkv * (d / 4);
-  la_sum_heads_kernel<T><<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(in, static_cast<T *>(out), os, n4, Hkv, group, d);
+void launch_la_sum_heads(const LaHeadSum &x, const LaHeadSum &y, long long rows, int Hkv, int group, cudaStream_t s) {
+  const long long n4 = rows * Hkv * ((x.d > y.d ? x.d : y.d) / 4);
+  la_sum_heads_kernel<T><<<dim3((unsigned)((n4 + 255) / 256), 2), 256, 0, s>>>(x, y, rows, Hkv, group);
 }
 
 template void launch_la_simt<float>(const LaPlanDev &, const LaBatch &, bool, cudaStream_t);
 template void launch_la_simt<__nv_bfloat16>(const LaPlanDev &, const LaBatch &, bool, cudaStream_t);
-template void launch_la_sum_heads<float>(const float *, void *, long long, long long, int, int, int, cudaStream_t);
-template void launch_la_sum_heads<__nv_bfloat16>(const float *, void *, long long, long long, int, int, int,
-                                                 cudaStream_t);
+template void launch_la_sum_heads<float>(const LaHeadSum &, const LaHeadSum &, long long, int, int, cudaStream_t);
+template void launch_la_sum_heads<__nv_bfloat16>(const LaHeadSum &, const LaHeadSum &, long long, int, int, cudaStream_t);
 
 }  // namespace ssd

@@ -41,6 +41,7 @@ struct LaPass {
   float *fin;
   int sa, sb;
   float *seg_state;  // (units, H, dk, dv): a cut sequence's segment states
+  bool seg_shared;   // they are another pass's, transposed: (units, H, dv, dk), read only
   bool o_f32;        // o is fp32 whatever the inputs' type
 };
 
@@ -119,8 +120,8 @@ __device__ __forceinline__ const float *la_state_in(const LaPass &p, int level, 
   sa = p.sa;
   sb = p.sb;
   if (level == 0) return p.init ? p.init + ((size_t)seq * p.H + h) * dd : nullptr;
-  sa = p.dv;
-  sb = 1;
+  sa = p.seg_shared ? 1 : p.dv;
+  sb = p.seg_shared ? p.dk : 1;
   return p.seg_state + ((size_t)unit * p.H + h) * dd;
 }
 // Where the unit's state goes, or null: with to_next the next unit's incoming state, else (and for the last
@@ -156,10 +157,15 @@ inline int la_tc_boxes(int width) { return width <= 64 ? 1 : 2; }
 void launch_la_tc(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s);
 // segments' own states -> incoming states, in place (either path)
 void launch_la_scan(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s);
-// sums fp32 (rows, H, d) over groups of query heads into (rows, Hkv, d)
+// sums fp32 (rows, H, d) over groups of query heads into (rows, Hkv, d), for two tensors
+struct LaHeadSum {
+  const float *in;
+  void *out;
+  long long os;
+  int d;
+};
 template <typename T>
-void launch_la_sum_heads(const float *in, void *out, long long os, long long rows, int Hkv, int group, int d,
-                         cudaStream_t s);
+void launch_la_sum_heads(const LaHeadSum &x, const LaHeadSum &y, long long rows, int Hkv, int group, cudaStream_t s);
 // la_step.cu
 template <typename T>
 void launch_la_step(const LaPass &p, int rows, float *states, int nslots, const int *slot_idx, cudaStream_t s);
