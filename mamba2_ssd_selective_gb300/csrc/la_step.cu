@@ -2,11 +2,14 @@
 // cache of states:
 //     S[slot] = lam S[slot] + k^T v,   o = scale q S[slot]
 // The state is read and written once, and that traffic is the bound.  A block
-// of 256 threads takes 32 columns of one state: 8 threads span a row of 128
-// bytes, 32 rows at a time, all of a thread's rows loaded before the first is
-// used; the sum over rows goes through the warps' lanes, then shared memory, in
-// a fixed order.  The columns are split over blocks so that a single row's few
-// states still spread over many SMs.
+// of 256 threads takes 64 or 32 columns of one state, all of a thread's elements
+// loaded before the first is used; the sum over rows goes through the warps'
+// lanes, then shared memory, in a fixed order.  Blocks of one state are
+// neighbours in the grid, so that its memory is read as one piece (with rows of the cache next to one
+// another instead: 209 us where it is 199).  256 rows, 32 heads of 128 x 128 (1.07 GB): 64 columns
+// 178 us (6.0 TB/s), 32 columns 202 us, 128 columns 223 us, which leave a thread 16 loads and the SM few
+// warps; dk of 256 takes 32 columns for the same reason (211 us against 509).  Where 64 columns leave SMs
+// without a block, 32 spread a single row's few states over more of them (16 heads: 8.3 us against 9.0).
 #include "retention.h"
 
 namespace ssd {
@@ -14,18 +17,19 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCols = 32;
-constexpr int kRows = kThreads / (kCols / 4);  // state rows of one sweep
 
 template <typename T> __device__ __forceinline__ float load1(const T *p) { return to_f<T>(*p); }
 
-// SWEEPS * 32 rows cover the state's dk
-template <typename T, int SWEEPS>
+template <int COLS> constexpr int kRows = kThreads / (COLS / 4);  // state rows of one sweep
+
+// SWEEPS sweeps cover the state's dk
+template <typename T, int COLS, int SWEEPS>
 __global__ void __launch_bounds__(kThreads) la_step_kernel(LaPass p, float *__restrict__ states, int nslots,
                                                            const int *__restrict__ slot_idx) {
-  __shared__ float part[kThreads / 32][kCols];
-  const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  const int c = blockIdx.z * kCols + 4 * (tid & 7), a0 = tid >> 3;
+  constexpr int kLanes = COLS / 4;  // threads of a state row
+  __shared__ float part[kThreads / 32][COLS];
+  const int nz = (p.dv + COLS - 1) / COLS, r = blockIdx.x / nz, h = blockIdx.y, tid = threadIdx.x;
+  const int z = blockIdx.x - r * nz, c = z * COLS + 4 * (tid % kLanes), a0 = tid / kLanes;
   const bool col = c < p.dv;
   const int slot = slot_idx ? __ldg(slot_idx + r) : r;
   const bool live = slot >= 0 && slot < nslots;
@@ -39,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) la_step_kernel(LaPass p, float *__re
     float qv[SWEEPS], kv[SWEEPS];
 #pragma unroll
     for (int i = 0; i < SWEEPS; ++i) {
-      const int a = a0 + kRows * i;
+      const int a = a0 + kRows<COLS> * i;
       if (a < p.dk) {
         x[i] = *reinterpret_cast<const float4 *>(st + (size_t)a * p.dv);
         qv[i] = load1(q + a);
@@ -50,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) la_step_kernel(LaPass p, float *__re
     const float lam = expf(__ldg(p.g + h));
 #pragma unroll
     for (int i = 0; i < SWEEPS; ++i) {
-      const int a = a0 + kRows * i;
+      const int a = a0 + kRows<COLS> * i;
       if (a < p.dk) {
         x[i].x = fmaf(lam, x[i].x, kv[i] * vv[0]);
         x[i].y = fmaf(lam, x[i].y, kv[i] * vv[1]);
@@ -65,33 +69,38 @@ __global__ void __launch_bounds__(kThreads) la_step_kernel(LaPass p, float *__re
     }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 8);
-    acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 16);
-  }
-  if ((tid & 31) < 8)
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) part[tid >> 5][4 * (tid & 7) + j] = acc[j];
+    for (int o = kLanes; o < 32; o *= 2) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+  if ((tid & 31) < kLanes)
+    *reinterpret_cast<float4 *>(&part[tid >> 5][4 * (tid % kLanes)]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
   __syncthreads();
-  if (tid < kCols && blockIdx.z * kCols + tid < p.dv) {
+  if (tid < COLS && z * COLS + tid < p.dv) {
     float o = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) o += part[w][tid];
-    static_cast<T *>(p.o)[r * p.os + (long long)h * p.dv + blockIdx.z * kCols + tid] = from_f<T>(o * p.o_scale);
+    static_cast<T *>(p.o)[r * p.os + (long long)h * p.dv + z * COLS + tid] = from_f<T>(o * p.o_scale);
   }
+}
+
+template <typename T, int COLS, int SWEEPS>
+void run_step(const LaPass &p, int rows, float *states, int nslots, const int *slot_idx, cudaStream_t s) {
+  static_assert(SWEEPS <= 8, "registers");
+  const dim3 grid((unsigned)rows * ((p.dv + COLS - 1) / COLS), p.H);
+  la_step_kernel<T, COLS, SWEEPS><<<grid, kThreads, 0, s>>>(p, states, nslots, slot_idx);
 }
 
 }  // namespace
 
 template <typename T>
 void launch_la_step(const LaPass &p, int rows, float *states, int nslots, const int *slot_idx, cudaStream_t s) {
-  const dim3 grid(rows, p.H, (p.dv + kCols - 1) / kCols);
-  if (p.dk <= 2 * kRows)
-    la_step_kernel<T, 2><<<grid, kThreads, 0, s>>>(p, states, nslots, slot_idx);
-  else if (p.dk <= 4 * kRows)
-    la_step_kernel<T, 4><<<grid, kThreads, 0, s>>>(p, states, nslots, slot_idx);
+  const bool wide = p.dv > 32 && p.dk <= 128 && (long long)rows * p.H * ((p.dv + 63) / 64) >= 152;
+  if (p.dk <= 64)
+    wide ? run_step<T, 64, 4>(p, rows, states, nslots, slot_idx, s) : run_step<T, 32, 2>(p, rows, states, nslots, slot_idx, s);
+  else if (p.dk <= 128)
+    wide ? run_step<T, 64, 8>(p, rows, states, nslots, slot_idx, s) : run_step<T, 32, 4>(p, rows, states, nslots, slot_idx, s);
   else
-    la_step_kernel<T, 8><<<grid, kThreads, 0, s>>>(p, states, nslots, slot_idx);
+    run_step<T, 32, 8>(p, rows, states, nslots, slot_idx, s);
 }
 
 template void launch_la_step<float>(const LaPass &, int, float *, int, const int *, cudaStream_t);
