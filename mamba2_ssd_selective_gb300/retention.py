@@ -197,6 +197,16 @@ def _device(device) -> torch.device:
     return device
 
 
+def _grow(runner, workspace_size) -> None:
+    """The workspace that backward passes need, from the first one on.  The forward pass's stays alive: a stream that
+    is not the allocator's may still be using it."""
+    if runner._forward_workspace is None:
+        size = workspace_size(runner.dims, True)
+        runner._forward_workspace = runner.workspace
+        if runner.workspace.numel() < size:
+            runner.workspace = torch.empty(size, dtype=torch.uint8, device=runner.device)
+
+
 class LinearAttnRunner:
     """Linear attention of one shape: S_t = lam S_(t-1) + k_t^T v_t, o_t = scale q_t S_t per head.
 
@@ -223,6 +233,10 @@ class LinearAttnRunner:
                         nheads * headdim_v)
         self._scale = headdim_k ** -0.5
         self._heads, self._bounds = (nheads,), (nseq + 1,)
+        self._forward_workspace = None
+
+    def _grow(self):
+        _grow(self, ssd_linear_attn_workspace_size)
 
     def _inputs(self, q, k, v, log_decay, scale, init, cu) -> SsdLinearAttnInputs:
         wq, wk, wv, _ = self._widths
@@ -259,9 +273,7 @@ class LinearAttnRunner:
         inputs = self._inputs(q, k, v, log_decay, scale, initial_state, cu_seqlens)
         dop, dos = _rows(do, "do", rows, wo, tdtype, device)
         dfin = _exact(dfinal_state, "dfinal_state", self.state_shape, torch.float32, device)
-        size = ssd_linear_attn_workspace_size(self.dims, True)
-        if self.workspace.numel() < size:
-            self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        self._grow()
         g = {"dq": torch.empty(rows, wq, dtype=tdtype, device=device),
              "dk": torch.empty(rows, wk, dtype=tdtype, device=device),
              "dv": torch.empty(rows, wv, dtype=tdtype, device=device),
@@ -302,6 +314,10 @@ class GroupNormRunner:
         if size == 0:
             raise ValueError("invalid dims for libssd")
         self.workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+        self._forward_workspace = None
+
+    def _grow(self):
+        _grow(self, ssd_group_norm_workspace_size)
 
     def _row(self, x, name):
         return _rows(x, name, self.rows, self.channels, self.tdtype, self.device)
@@ -333,9 +349,7 @@ class GroupNormRunner:
         dyp, dys = self._row(dy, "dy")
         mp = _exact(mean, "mean", self.stat_shape, torch.float32, device)
         rp = _exact(rstd, "rstd", self.stat_shape, torch.float32, device)
-        size = ssd_group_norm_workspace_size(self.dims, True)
-        if self.workspace.numel() < size:
-            self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        self._grow()
         g = {"dx": torch.empty(x.shape, dtype=self.tdtype, device=device),
              "dz": None if z is None else torch.empty(x.shape, dtype=self.tdtype, device=device),
              "dweight": torch.empty(self.channels, dtype=torch.float32, device=device),
