@@ -162,10 +162,10 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, const Wa
   const uint32_t hint = w.limit_ns < kWaitHintNs ? (uint32_t)w.limit_ns : kWaitHintNs;
   if (__builtin_expect(mbar_try_wait_hint(bar, parity, hint), 1)) return true;
   const uint64_t t0 = globaltimer_ns();
-  do {
+  while (globaltimer_ns() - t0 < w.limit_ns) {
     if (mbar_try_wait_hint(bar, parity, hint)) return true;
     if (*reinterpret_cast<volatile int *>(w.status) != 0) return false;
-  } while (globaltimer_ns() - t0 <= w.limit_ns);
+  }
   atomicExch(w.status, 1);
   return false;
 }
@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const int x = ok && (uint32_t)next < (uint32_t)nitems ? next : nitems;
           Item it{};
           if (x < nitems) it.find<SUMMARY>(args, x);
-          // the slot of two items ago has been read
+          // the slot of two items ago has been read (if not, it is left alone: an item is never torn)
           if (n >= 2 && !mbar_wait_drain(&bar.items.free[n & 1], parity(n / 2 - 1))) ok = false;
-          slots[n & 1] = it;
+          if (ok) slots[n & 1] = it;
           if (pipe::publish_unit(bar.items, n, ok ? x : nitems, nitems) >= nitems) break;
           next = atomicAdd(counter, 1);
           const LaPass &p = args.batch.p[it.pass];
