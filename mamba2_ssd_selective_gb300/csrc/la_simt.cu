@@ -43,15 +43,34 @@ __device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
   *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// rows [0, nv) of a (kC x d) tile of a token-major tensor, transposed into dst[d][kLdC]; rows past nv are zero
-template <typename T>
-__device__ __forceinline__ void stage_transposed(float *dst, const T *src, long long stride, int nv, int d) {
+// Rows [0, nv) of (kC x d) tiles of two token-major tensors (SUMMARY: of the second only), transposed into
+// dst[d][kLdC]; rows past nv are zero.  All of a turn's loads are issued before the first is used.
+template <typename T, bool SUMMARY>
+__device__ __forceinline__ void stage_transposed(float *qt, const T *q, long long qs, float *kt, const T *k, long long ks,
+                                                 int nv, int d) {
+  constexpr int kWarps = kThreads / 32;
   const int r = threadIdx.x & 31;
-  for (int x = threadIdx.x >> 5; x < d / 8; x += kThreads / 32) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (r < nv) load8(src + (long long)r * stride + 8 * x, v);
+  for (int x0 = threadIdx.x >> 5; x0 < d / 8; x0 += 2 * kWarps) {
+    float a[2][8] = {}, b[2][8] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dst[(8 * x + i) * kLdC + r] = v[i];
+    for (int y = 0; y < 2; ++y) {
+      const int x = x0 + y * kWarps;
+      if (r < nv && x < d / 8) {
+        if (!SUMMARY) load8(q + (long long)r * qs + 8 * x, a[y]);
+        load8(k + (long long)r * ks + 8 * x, b[y]);
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int x = x0 + y * kWarps;
+      if (x < d / 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (!SUMMARY) qt[(8 * x + i) * kLdC + r] = a[y][i];
+          kt[(8 * x + i) * kLdC + r] = b[y][i];
+        }
+      }
+    }
   }
 }
 
@@ -95,15 +114,20 @@ __global__ void __launch_bounds__(kThreads, SUMMARY ? 5 : 4) la_simt_kernel(LaPl
   for (int ib = 0; ib < nb; ++ib) {
     const int blk = rev ? nb - 1 - ib : ib, r0 = blk * kC, nv = min(kC, u.len - r0);
     __syncthreads();  // the previous block's operands have been read
-    if (!SUMMARY) stage_transposed(Qt, q + (long long)r0 * p.qs, p.qs, nv, p.dk);
-    stage_transposed(Kt, k + (long long)r0 * p.ks, p.ks, nv, p.dk);
-    for (int e = tid; e < kC * (kTV / 8); e += kThreads) {
-      const int r = e / (kTV / 8), x = e % (kTV / 8);
-      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (r < nv && 8 * x < ncol) load8(v + (long long)(r0 + r) * p.vs + 8 * x, w);
+    stage_transposed<T, SUMMARY>(Qt, q + (long long)r0 * p.qs, p.qs, Kt, k + (long long)r0 * p.ks, p.ks, nv, p.dk);
+    {
+      constexpr int kTurns = kC * (kTV / 8) / kThreads, kRowsATurn = kThreads / (kTV / 8);
+      const int r = tid / (kTV / 8), x = tid % (kTV / 8);
+      float w[kTurns][8] = {};
 #pragma unroll
-      for (int i = 0; i < 8; i += 4)
-        *reinterpret_cast<float4 *>(V + r * kLdV + 8 * x + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+      for (int y = 0; y < kTurns; ++y)
+        if (r + y * kRowsATurn < nv && 8 * x < ncol) load8(v + (long long)(r0 + r + y * kRowsATurn) * p.vs + 8 * x, w[y]);
+#pragma unroll
+      for (int y = 0; y < kTurns; ++y)
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+          *reinterpret_cast<float4 *>(V + (r + y * kRowsATurn) * kLdV + 8 * x + i) =
+              make_float4(w[y][i], w[y][i + 1], w[y][i + 2], w[y][i + 3]);
     }
     __syncthreads();
     if (!SUMMARY) {
