@@ -53,8 +53,11 @@ bool la_use_tc(const ssd_linear_attn_dims *d) {
 // Whether and where sequences are cut, and the workspace.
 //
 // Cut side by side, a sequence's segments run at once: their own states first (a second
-// read of k and v), a scan, then the pass.  That pays where whole sequences
-// leave at least half of the GPU idle.
+// read of k and v), a scan, then the pass.  That pays where whole sequences leave most of the GPU's places
+// for blocks empty (half of them, where lengths differ or a segment's state is cheap beside the pass): one sequence of
+// 31991 tokens, 16 heads of 128, bf16, took 616 us whole, 165 us in 9 segments; four of 8192 (64 of 152
+// places) took 169 us whole, 170 us in 2.  fp32, 4 x 2048 tokens, 12 heads
+// of 64: 460 us whole, 171 us cut; 8 x 4096, 32 heads of 128 (all places taken): 4440 us whole, 5560 us cut.
 // Chained (tensor cores), segments of all sequences are items of a queue in order of
 // their level, a segment's state handed to the next: nothing is done twice, and SMs
 // that finish early take over.  Handing over costs the time of about three blocks of 64
@@ -72,18 +75,27 @@ LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
   pl.passes = backward ? 3 : 1;
   const int wide = d->headdim_k > d->headdim_v ? d->headdim_k : d->headdim_v;
   const long long rows = la_rows(d), H = d->nheads, n = d->nseq, sms = 152;
-  // blocks of a whole sequence, and blocks that fill the GPU (CUDA cores: 4 resident on an SM, twice over)
-  const long long blocks = H * pl.passes * (tc ? 1 : (wide + 63) / 64), want = tc ? sms : 8 * sms;
+  // blocks of a whole sequence, blocks that the GPU holds at once (CUDA cores: by their shared memory), and blocks to
+  // cut into (CUDA cores: twice over, as their segments are short)
+  const long long blocks = H * pl.passes * (tc ? 1 : (wide + 63) / 64);
+  const long long places = sms * (tc ? 1 : wide <= 64 ? 4 : wide <= 128 ? 2 : 1), want = tc ? places : 2 * places;
   const long long longest = d->packed ? rows : d->seqlen;
   long long seg = 0;
   if (d->packed && n > kLaMaxCutSeqs) {
     pl.cut = LaPlan::kWhole;
-  } else if (n * blocks >= want) {
-    if (tc && d->packed) {
+  } else if ((tc && !d->packed ? 3 : 2) * n * blocks <= places) {
+    const long long cuts = want / (n * blocks);
+    seg = d->packed ? rows * blocks / want : (longest + cuts - 1) / cuts;
+    seg = (seg + 63) / 64 * 64;
+    const long long least = tc ? 256 : 64;
+    if (seg < least) seg = least;
+    pl.cut = seg < longest ? LaPlan::kSideBySide : LaPlan::kWhole;
+  } else if (tc) {
+    if (d->packed) {
       // hand-overs in all against the last items' idle SMs
       seg = (long long)std::sqrt(384. * (double)(rows * blocks / sms)) / 64 * 64;
       if (seg < 2048) seg = 2048;
-    } else if (tc) {
+    } else {
       const long long tiles = (longest + 63) / 64;
       long long best = 0;
       for (long long c = 1; c <= 32 && c <= tiles; ++c) {
@@ -95,15 +107,8 @@ LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
         }
       }
     }
-    const bool fits = tc && (rows / seg + n) * blocks < (1LL << 28);  // item numbers are 32-bit
+    const bool fits = (rows / seg + n) * blocks < (1LL << 28);  // item numbers are 32-bit
     pl.cut = fits && seg < longest ? LaPlan::kChained : LaPlan::kWhole;
-  } else {
-    const long long cuts = want / (n * blocks);
-    seg = d->packed ? rows * blocks / want : (longest + cuts - 1) / cuts;
-    seg = (seg + 63) / 64 * 64;
-    const long long least = tc ? 256 : 64;
-    if (seg < least) seg = least;
-    pl.cut = seg < longest && (cuts >= 2 || d->packed) ? LaPlan::kSideBySide : LaPlan::kWhole;
   }
   if (pl.cut == LaPlan::kWhole) seg = (longest + 63) / 64 * 64;
   const bool cut = pl.cut != LaPlan::kWhole;

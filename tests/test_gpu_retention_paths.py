@@ -15,22 +15,22 @@ TIMEOUT = -9  # SSD_ERR_DEVICE_TIMEOUT
 
 
 # at least as many items (sequences x heads, three times as many backward) as SMs, and rounds that segments fill
-# better: (sequences' lengths, heads, key/value heads, packed, is backward cut too)
+# better: (sequences' lengths, heads, key/value heads, packed, is forward cut, is backward)
 CHAINED = [
-    ([650] * 10, 16, 16, False, False),
-    ([750] * 4, 16, 4, False, True),
-    ([64 * 9 + 1] * 20, 8, 8, False, False),
-    ([2300, 1, 0, 64, 5, 63, 2049, 0, 130, 17], 16, 4, True, True),
+    ([650] * 10, 16, 16, False, True, False),
+    ([750] * 4, 16, 4, False, False, True),
+    ([64 * 9 + 1] * 20, 8, 8, False, True, False),
+    ([2300, 1, 0, 64, 5, 63, 2049, 0, 130, 17], 16, 4, True, True, True),
 ]
 
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (64, 72)])
-@pytest.mark.parametrize("lens,H,K,packed,backward", CHAINED)
-def test_chained_segments(lens, H, K, packed, backward, dk, dv):
+@pytest.mark.parametrize("lens,H,K,packed,forward,backward", CHAINED)
+def test_chained_segments(lens, H, K, packed, forward, backward, dk, dv):
     c = Case(lens, H, K, dk, dv, packed=packed, seed=sum(lens) + dv)
     # room for a state of each head that is handed over, so that this case takes the path it is meant for
     state, heads = H * dk * dv * 4, c.T * H * (dk + dv) * 4 if K < H else 0
-    assert ssd.ssd_linear_attn_workspace_size(c.runner().dims, False) > state
+    assert (ssd.ssd_linear_attn_workspace_size(c.runner().dims, False) > state) == forward
     assert (ssd.ssd_linear_attn_workspace_size(c.runner().dims, True) - heads > 3 * state) == backward
     c.check()
 
