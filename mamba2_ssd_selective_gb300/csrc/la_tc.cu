@@ -11,10 +11,9 @@
 // lanes, the state stays in its warps' registers (lane = dv) from block to
 // block, and the products with the state take their A operands from TMEM: S^T
 // from the registers, the weighted copies of V^T from shared memory through
-// transposing matrix loads.  That matters because shared memory is what bounds
-// the kernel before HBM does: with the weighted K kept there as a B operand
-// (three terms written and read back) a block of 64 tokens at widths of 128 moved
-// 340 KB through it and took 3560 cycles, and 1.5 of them were shared memory's.
+// transposing matrix loads, so that shared memory carries the inputs, P and the outputs only.  (With
+// the weighted K as a B operand in shared memory, three terms written and read back, a call of 128 items
+// of 8192 tokens at widths of 128 took 325 us; as it is, 178.)
 // P and S are rounded to bf16 as operands (the outputs are bf16 too); what goes
 // into the state is not: V diag(lam^b) is split into three bf16 terms (24 bits), so
 // that states keep fp32 precision over any length.
@@ -34,6 +33,11 @@
 // lam^-(nv - 1 - j)), so that both products meet in one accumulator, which takes
 // turns between two.  It is up to lam^-64: heads whose lam^64 is below 2^-40 form
 // P and O beside Oi instead, and add lam^a Oi at the end.
+// What bounds it: with an item on every SM, HBM (144 items of 8192 tokens at widths of 128: 190 us, 6.3 TB/s of a
+// copy's 6.8).  An item by itself is bounded by its chain of blocks, 1.3 us a block of 64 tokens at widths of 128
+// (1.2 us at 64, where half of the lanes have nothing to do): the tensor core's 1600 cycles (of them 770 for the
+// three terms of W), the roles' hand-offs, and instructions that are not in the caches (1.2 of 9 cycles that a
+// warp waits for each of its instructions).
 // Segments of a cut sequence either start from states that a scan has joined before
 // (few sequences: the segments run side by side), or hand their state on: the
 // next segment's state warps wait for its flag, and as items are taken level by
@@ -237,8 +241,8 @@ struct Item {
     nb = SUMMARY && next < 0 ? 0 : (len + kC - 1) / kC;  // nothing follows a last segment
   }
   // A converged warp's copy.  What comes from memory goes through a shuffle, which tells the
-  // compiler that it is the same in all lanes: else loops and operands that depend on
-  // it leave the uniform registers.
+  // compiler that it is the same in all lanes, so that loops and operands that depend on it may stay in
+  // uniform registers.
   __device__ __forceinline__ Item uniform() const {
     Item r;
     const volatile int *from = reinterpret_cast<const volatile int *>(this);
