@@ -361,10 +361,33 @@ __device__ __forceinline__ float deviations(const Vec<W> &x, float mean) {
   return (d * d).sum();
 }
 
+// ---------------------------------------------------------------- a thread's own ring of values on their way
+// Teams of one place copy their next samples' values into shared memory, each thread its own and for itself alone
+// (no barrier), so that the loads in flight do not cost registers.
+template <typename T, int W, int TENSORS>
+struct Ring {
+  static constexpr int kChunks = W == 8 ? (int)sizeof(T) / 2 : 1, kStages = TENSORS * kChunks <= 2 ? 4 : 3;
+  static constexpr int kBytes = kStages * TENSORS * kChunks * kThreads * 16;
+  uint4 (*slot)[TENSORS][kChunks][kThreads];
+  __device__ __forceinline__ explicit Ring(void *smem) : slot(static_cast<uint4(*)[TENSORS][kChunks][kThreads]>(smem)) {}
+  __device__ __forceinline__ void load(int stage, int t, const T *from) const {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      sm100::cp_async16(sm100::smem_u32(&slot[stage][t][c][threadIdx.x]), reinterpret_cast<const uint4 *>(from) + c);
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // all but the last kStages - 2 groups have landed
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory"); }
+  __device__ __forceinline__ void get(int stage, int t, Raw<T, W> &to) const {
+    uint4 *u = reinterpret_cast<uint4 *>(&to);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) u[c] = slot[stage][t][c][threadIdx.x];
+  }
+};
+
 // ---------------------------------------------------------------- forward, groups that fit a team
 // Teams that each keep one group and walk over samples; block (groups of the block, samples of the block).
-// With one place to a thread the next sample's values are on their way while one is worked on, and
-// registers are held down to keep enough of them in flight on an SM.
+// With one place to a thread the next samples' values are on their way while one is worked on.
 template <int V>
 constexpr int min_blocks(int one) { return V == 1 ? one : 1; }
 template <typename T, int W, int NT, int V, bool GATE>
@@ -385,33 +408,45 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 4 : 3
     w = load_param<W>(p.w, c0 + at.col[0], 1.f);
     b = load_param<W>(p.b, c0 + at.col[0], 0.f);
   }
-  Raw<T, W> xr[V], zr[V];
-  auto load = [&](int n) {
-    const Slab<T> s(p, has && n < n1 ? n : 0, has ? g : 0);
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (has && n < n1 && at.row[k] >= 0) {
-        xr[k].load(s.x + off(at.row[k], p.xs) + at.col[k]);
-        if (GATE) zr[k].load(s.z + off(at.row[k], p.zs) + at.col[k]);
-      } else {
-        xr[k].clear();
-      }
+  using R = Ring<T, W, GATE ? 2 : 1>;
+  extern __shared__ uint4 ring_smem[];
+  const R ring(ring_smem);
+  auto ahead = [&](int i) {  // turn i's values on their way
+    const int n = n0 + i * shares;
+    if (has && n < n1 && at.row[0] >= 0) {
+      const Slab<T> s(p, n, g);
+      ring.load(i % R::kStages, 0, s.x + at.col[0]);
+      if (GATE) ring.load(i % R::kStages, 1, s.z + at.col[0]);
+    }
+    R::commit();
   };
+  if constexpr (V == 1)
+    for (int i = 0; i < R::kStages - 1; ++i) ahead(i);
   // every thread of a warp makes the same number of turns (the sums are warp or block wide)
-  if (V == 1) load(n0);
   for (int i = 0; i < turns; ++i) {
     const int n = n0 + i * shares;
     const bool live = has && n < n1;
-    if (V > 1) load(n);
+    const Slab<T> s(p, live ? n : 0, has ? g : 0);
     Vec<W> x[V];
     Raw<T, W> z[V];
+    if constexpr (V == 1) R::wait();
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      x[k] = vec_of<T, W>(xr[k]);
-      if (GATE) z[k] = zr[k];
+      Raw<T, W> xr;
+      if (live && at.row[k] >= 0) {
+        if constexpr (V == 1) {
+          ring.get(i % R::kStages, 0, xr);
+          if (GATE) ring.get(i % R::kStages, 1, z[0]);
+        } else {
+          xr.load(s.x + off(at.row[k], p.xs) + at.col[k]);
+          if (GATE) z[k].load(s.z + off(at.row[k], p.zs) + at.col[k]);
+        }
+      } else {
+        xr.clear();
+      }
+      x[k] = vec_of<T, W>(xr);
     }
-    if (V == 1) load(n + shares);
-    const Slab<T> s(p, live ? n : 0, has ? g : 0);
+    if constexpr (V == 1) ahead(i + R::kStages - 1);
     float sum = 0.f, dev = 0.f;
 #pragma unroll
     for (int k = 0; k < V; ++k) sum += x[k].sum();
@@ -677,7 +712,11 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
     team_backward_kernel(GnProblem p, GnPlan pl, float *dwp, float *dbp) {
   constexpr int kTeams = kThreads / NT;
   __shared__ float red[16];
-  __shared__ float acc[2][kThreads * W];
+  using R = Ring<T, W, GATE ? 3 : 2>;
+  using Acc = float[2][kThreads * W];
+  extern __shared__ uint4 ring_smem[];  // the ring, then what the threads have of dw and db
+  const R ring(ring_smem);
+  Acc &acc = *reinterpret_cast<Acc *>(ring_smem);
   const int team = threadIdx.x / NT, tid = threadIdx.x % NT, gpb = pl.groups_per_block, shares = kTeams / gpb;
   const int gl = team % gpb, share = team / gpb, g = blockIdx.x * gpb + gl, ncol = p.cg / W;
   const bool has = g < p.G && share < shares;
@@ -692,24 +731,43 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
     w = load_param<W>(p.w, c0 + col, 1.f);
     b = load_param<W>(p.b, c0 + col, 0.f);
   }
-  Raw<T, W> xr, zr, dyr;
   float mean_r = 0.f, rstd_r = 0.f;
-  auto load = [&](int n) {  // one place: the sample after the one in work
+  auto stats = [&](int n) {
     if (has && n < n1) {
       mean_r = __ldg(p.mean + n * p.G + g);
       rstd_r = __ldg(p.rstd + n * p.G + g);
-      if (at.row[0] >= 0) load_place<T, W, GATE>(p, Slab<T>(p, n, g), at.row[0], col, xr, zr, dyr);
     }
   };
-  if (V == 1) load(n0);
+  auto ahead = [&](int i) {  // turn i's values on their way
+    const int n = n0 + i * shares;
+    if (has && n < n1 && at.row[0] >= 0) {
+      const Slab<T> s(p, n, g);
+      ring.load(i % R::kStages, 0, s.x + col);
+      ring.load(i % R::kStages, 1, s.dy + col);
+      if (GATE) ring.load(i % R::kStages, 2, s.z + col);
+    }
+    R::commit();
+  };
+  if constexpr (V == 1) {
+    for (int i = 0; i < R::kStages - 1; ++i) ahead(i);
+    stats(n0);
+  }
   for (int i = 0; i < turns; ++i) {
     const int n = n0 + i * shares;
     const bool live = has && n < n1;
-    if (V > 1 && live) {
-      mean_r = __ldg(p.mean + n * p.G + g);
-      rstd_r = __ldg(p.rstd + n * p.G + g);
-    }
+    if (V > 1) stats(n);
     const float mean = mean_r, rstd = rstd_r;
+    Raw<T, W> xr, zr, dyr;
+    if constexpr (V == 1) {
+      R::wait();
+      if (live && at.row[0] >= 0) {
+        ring.get(i % R::kStages, 0, xr);
+        ring.get(i % R::kStages, 1, dyr);
+        if (GATE) ring.get(i % R::kStages, 2, zr);
+      }
+      ahead(i + R::kStages - 1);
+      stats(n + shares);
+    }
     const Slab<T> s(p, live ? n : 0, has ? g : 0);
     Vec<W> dxh[V], xh[V];
     float sa = 0.f, sb = 0.f;
@@ -722,7 +780,6 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
         sa += dxh[k].sum();
         sb += (dxh[k] * xh[k]).sum();
       }
-    if (V == 1) load(n + shares);
     const float2 ab = team_sum2<NT>(sa, sb, red);
 #pragma unroll
     for (int k = 0; k < V; ++k)
@@ -730,6 +787,10 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 3 : 2
         write_dx<T, W>(s.dx + off(at.row[k], p.dxs) + col, dxh[k], xh[k], ab.x * inv, ab.y * inv, rstd);
   }
   if (!dwp) return;
+  if constexpr (V == 1) {  // the ring is done with
+    sm100::cp_async_wait_all();
+    __syncthreads();
+  }
   // the threads of a block that hold the same channels: the teams of a group, each team's row phases
   keep_params<W>(acc, dw, db);
   const int phases = V == 1 ? 1 : NT / ncol;
@@ -928,6 +989,14 @@ void with_tile(const GnPlan &pl, F f) {
   return pl.vec == 2 ? f(Int<2>{}, Int<12>{}) : f(Int<1>{}, Int<12>{});
 }
 
+// a launch with `bytes` of dynamic shared memory (with what a kernel has of its own they may pass the 48 KB of a plain
+// launch)
+template <class... P, class... A>
+void launch_smem(void (*kernel)(P...), dim3 grid, int bytes, cudaStream_t s, A... args) {
+  if (bytes > 32 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  kernel<<<grid, kThreads, bytes, s>>>(args...);
+}
+
 // a launch of clusters of pl.cluster blocks
 template <class... P, class... A>
 void launch_clusters(void (*kernel)(P...), unsigned grid, const GnPlan &pl, cudaStream_t s, A... args) {
@@ -950,9 +1019,9 @@ void forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
     with_team(pl, [&](auto w, auto nt, auto v) {
       const dim3 grid((p.G + pl.groups_per_block - 1) / pl.groups_per_block,
                       (p.n + pl.samples_per_block - 1) / pl.samples_per_block);
-      SSD_LAUNCH("gn_forward",
-                 (team_forward_kernel<T, decltype(w)::value, decltype(nt)::value, decltype(v)::value, GATE>
-                  <<<grid, kThreads, 0, s>>>(p, pl)));
+      constexpr int W = decltype(w)::value, NT = decltype(nt)::value, V = decltype(v)::value;
+      constexpr int ring = V == 1 ? Ring<T, W, GATE ? 2 : 1>::kBytes : 0;
+      SSD_LAUNCH("gn_forward", launch_smem(team_forward_kernel<T, W, NT, V, GATE>, grid, ring, s, p, pl));
     });
     return;
   }
@@ -978,9 +1047,10 @@ void backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
     with_team(pl, [&](auto w, auto nt, auto v) {
       const dim3 grid((p.G + pl.groups_per_block - 1) / pl.groups_per_block,
                       (p.n + pl.samples_per_block - 1) / pl.samples_per_block);
-      SSD_LAUNCH("gn_backward",
-                 (team_backward_kernel<T, decltype(w)::value, decltype(nt)::value, decltype(v)::value, GATE>
-                  <<<grid, kThreads, 0, s>>>(p, pl, kw, dbp)));
+      constexpr int W = decltype(w)::value, NT = decltype(nt)::value, V = decltype(v)::value;
+      constexpr int ring = V == 1 ? Ring<T, W, GATE ? 3 : 2>::kBytes : 0, acc = 2 * kThreads * W * 4;
+      SSD_LAUNCH("gn_backward", launch_smem(team_backward_kernel<T, W, NT, V, GATE>, grid, ring > acc ? ring : acc, s, p,
+                                            pl, kw, dbp));
     });
   } else {
     float *part = reinterpret_cast<float *>(ws + pl.part);
