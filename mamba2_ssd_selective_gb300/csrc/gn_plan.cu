@@ -49,7 +49,9 @@ GnPlan gn_plan(const GnProblem &p, bool backward, int widest) {
   GnPlan pl{};
   pl.vec = widest >= 8 && p.cg % 8 == 0 ? 8 : widest >= 2 && p.cg % 2 == 0 ? 2 : 1;
   const int ncol = p.cg / pl.vec, block_places = pl.vec == 8 ? 4 : 12;
-  // the narrowest team that holds a group; backward teams also need a thread to keep its column
+  // Widths: rows of 16 bytes where a group allows it; pairs of channels halve the accesses of groups that eight do
+  // not divide (6 samples of 4099 rows of 32 groups of 10 channels, fp32: 51 us one by one, 37 us in pairs).
+  // The narrowest team that holds a group; backward teams also need a thread to keep its column.
   if (pl.vec == 8 && p.m == 1 && ncol <= 32) {
     pl.team = ncol <= 8 ? 8 : ncol <= 16 ? 16 : 32;
     pl.places = 1;

@@ -18,6 +18,16 @@
 // writes what a tile gives, and dz, and a second one joins the tiles, in order,
 // and reads its own again, from L2 where the tensor fits it.
 // dw and db are sums of per-block partials in a fixed order.
+//
+// Measured (kernel times): 32768 rows of 32 groups of 128 channels with a gate, bf16 (805 MB): 131 us, 6.1 TB/s;
+// the backward pass of 16384 rows (671 MB): 117 us and 8 us for the parameters' sums.  Both are near HBM's rate
+// once enough loads are in flight (the next samples' values held in registers instead of shared memory: 141 us
+// and 135 us).  Groups of a cluster are bound by the latency of their phases, not by any unit (DRAM 15% of
+// its rate, 1.5 to 1.8 of 4 instructions a cycle): 6 samples of 4099 rows of 32 groups of 10 channels, fp32
+// (63 MB): 29 us (two kernels: 37 us); the backward pass of 8 samples of 2048 rows of 32 groups of 16, bf16 (50 MB):
+// 31 us and 6 us for the parameters' sums (two kernels: 44 us).  Clusters that stay and copy their next group's tile
+// ahead into shared memory took 42 us and 35 us: the GPU holds fewer of them, and 192 or 256 groups do not fill
+// their rounds.
 #pragma once
 
 #include <type_traits>
@@ -366,6 +376,7 @@ __device__ __forceinline__ float deviations(const Vec<W> &x, float mean) {
 // (no barrier), so that the loads in flight do not cost registers.
 template <typename T, int W, int TENSORS>
 struct Ring {
+  // (forward with a gate: 131 us with 4 stages, 136 us with 6; backward: 117 us with 3, 118 us with 4)
   static constexpr int kChunks = W == 8 ? (int)sizeof(T) / 2 : 1, kStages = TENSORS * kChunks <= 2 ? 4 : 3;
   static constexpr int kBytes = kStages * TENSORS * kChunks * kThreads * 16;
   uint4 (*slot)[TENSORS][kChunks][kThreads];
