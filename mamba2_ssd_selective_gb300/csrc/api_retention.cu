@@ -52,63 +52,80 @@ bool la_use_tc(const ssd_linear_attn_dims *d) {
 
 // Whether and where sequences are cut, and the workspace.
 //
-// Cut side by side, a sequence's segments run at once: their own states first (a second
-// read of k and v), a scan, then the pass.  That pays where whole sequences leave most of the GPU's places
-// for blocks empty (half of them, where lengths differ or a segment's state is cheap beside the pass): one sequence of
-// 31991 tokens, 16 heads of 128, bf16, took 616 us whole, 165 us in 9 segments; four of 8192 (64 of 152
-// places) took 169 us whole, 170 us in 2.  fp32, 4 x 2048 tokens, 12 heads
-// of 64: 460 us whole, 171 us cut; 8 x 4096, 32 heads of 128 (all places taken): 4440 us whole, 5560 us cut.
-// Chained (tensor cores), segments of all sequences are items of a queue in order of
-// their level, a segment's state handed to the next: nothing is done twice, and SMs
-// that finish early take over.  Handing over costs the time of about three blocks of 64
-// tokens, so that a call of c segments a sequence takes
-//     max(c, items c / SMs, rounded up) x (blocks of a segment + 3)
-// and the c of the least is taken: 192 items of 8192 tokens of 128 (two sequences' backward pass, 32
-// heads) took 349 us whole (two rounds of 128 + 3 blocks), 288 us in 4 segments (210 blocks by the formula),
-// 301 us in 8 (209), and 3 (184) are taken: 262 us.
-// Lengths of packed sequences are not known here.  There a segment is long enough for its hand-over to
-// be small, at the least 2048 tokens: 24 sequences of 1 to 4487 tokens, 16 heads, took 107 us
-// whole, 104 us in segments of 1024, 94 us in segments of 2048.
+// Cut side by side, a sequence's segments run at once: their own states first (a second read of k and v), a scan,
+// then the pass.  Chained (tensor cores), segments of all sequences are items of a queue in order of their
+// level, a segment's state handed to the next: nothing is done twice, and SMs that finish early take over, but a
+// sequence still takes its time.  Which one, and the length of a segment, are those of the least cost by the
+// times measured here, in us:
+//   tensor cores, a block of 64 tokens on an SM: 1.3 (1.33 at widths of 128, 1.19 at 64); of segments' states 0.9;
+//   CUDA cores, a block of 32 tokens and 64 columns: 6.3 for one by itself, 5 where the SM has others;
+//   handing a state on: 3 blocks; a scan and a launch more: 17; the table of packed sequences' segments: 8.
+// Lengths of packed sequences are not known here: the longest of n is taken for its mean where
+// sequences end at random, (1 + 1/2 + ... + 1/n) / n of all tokens.
+// Whole against side by side: one sequence of 31991 tokens, 16 heads of 128, bf16, 616 us against 165 in 9 segments;
+// four of 8192, 169 against 170 in 2; fp32, 4 x 2048 tokens, 12 heads of 64, 460 us against 171; 8 x 4096, 32
+// heads of 128, 4440 us against 5560.
+// Whole against chained: 192 items of 8192 tokens of 128 (two sequences' backward pass, 32 heads) 349 us against 288 in
+// 4 segments, 301 in 8 and 262 in 3; 24 packed sequences of 1 to 4487 tokens, 16 heads, 107 us against 104 in
+// segments of 1024 and 94 in segments of 2048.
 LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
   LaPlan pl{};
   const bool tc = la_use_tc(d);
   pl.passes = backward ? 3 : 1;
-  const int wide = d->headdim_k > d->headdim_v ? d->headdim_k : d->headdim_v;
+  const int wide = d->headdim_k > d->headdim_v ? d->headdim_k : d->headdim_v, wide64 = (wide + 63) / 64;
   const long long rows = la_rows(d), H = d->nheads, n = d->nseq, sms = 152;
-  // blocks of a whole sequence, blocks that the GPU holds at once (CUDA cores: by their shared memory), and blocks to
-  // cut into (CUDA cores: twice over, as their segments are short)
-  const long long blocks = H * pl.passes * (tc ? 1 : (wide + 63) / 64);
-  const long long places = sms * (tc ? 1 : wide <= 64 ? 4 : wide <= 128 ? 2 : 1), want = tc ? places : 2 * places;
   const long long longest = d->packed ? rows : d->seqlen;
+  // blocks (CTAs or items) of a whole sequence of every head and pass, all of them, and those with states to sum
+  // (both reverse passes share theirs)
+  const long long each = H * pl.passes * (tc ? 1 : wide64), all = n * each;
+  const double summing = backward ? 2. / 3. : 1.;
+  const int kb = tc ? 64 : 32;
+  // in blocks of kb tokens: an SM's share of all work, and the longest sequence
+  const double share = (double)(d->packed ? rows * each : longest * all) / sms / kb;
+  const double part = d->packed ? (std::log((double)n) + 0.577 + 0.5 / (double)n) / (double)n : 1.;
+  const double chain = (double)longest / kb * (part < 1. ? part : 1.);
+  const bool cuttable = !d->packed || n <= kLaMaxCutSeqs;
+  const double table = d->packed ? 8. : 0.;
+  auto up = [](long long x, long long y) { return (x + y - 1) / y; };
   long long seg = 0;
-  if (d->packed && n > kLaMaxCutSeqs) {
-    pl.cut = LaPlan::kWhole;
-  } else if ((tc && !d->packed ? 3 : 2) * n * blocks <= places) {
-    const long long cuts = want / (n * blocks);
-    seg = d->packed ? rows * blocks / want : (longest + cuts - 1) / cuts;
-    seg = (seg + 63) / 64 * 64;
-    const long long least = tc ? 256 : 64;
-    if (seg < least) seg = least;
-    pl.cut = seg < longest ? LaPlan::kSideBySide : LaPlan::kWhole;
-  } else if (tc) {
-    if (d->packed) {
-      // hand-overs in all against the last items' idle SMs
-      seg = (long long)std::sqrt(384. * (double)(rows * blocks / sms)) / 64 * 64;
-      if (seg < 2048) seg = 2048;
-    } else {
-      const long long tiles = (longest + 63) / 64;
-      long long best = 0;
-      for (long long c = 1; c <= 32 && c <= tiles; ++c) {
-        const long long rounds = (n * blocks * c + sms - 1) / sms, each = (tiles + c - 1) / c;
-        const long long cost = (rounds > c ? rounds : c) * (each + 3);
-        if (c == 1 || cost < best) {
-          best = cost;
-          seg = each * 64;
-        }
-      }
+  double best = 0.;
+  auto take_if = [&](LaPlan::Cut cut, long long length, double cost) {
+    const bool fits = length < longest && (rows / length + n) * each < (1LL << 28);  // item numbers are 32-bit
+    if (cut == LaPlan::kWhole || (fits && cuttable && cost < best)) {
+      pl.cut = cut;
+      seg = length;
+      best = cost;
     }
-    const bool fits = (rows / seg + n) * blocks < (1LL << 28);  // item numbers are 32-bit
-    pl.cut = fits && seg < longest ? LaPlan::kChained : LaPlan::kWhole;
+  };
+  if (tc && !d->packed) {
+    const long long tiles = up(longest, kb);
+    take_if(LaPlan::kWhole, longest, 1.3 * (double)(up(all, sms) * (tiles + 3)));
+    for (long long c = 2; c <= 152 && 4 * c <= tiles; ++c) {
+      const long long len = up(tiles, c), rounds = up(all * c, sms);
+      take_if(LaPlan::kChained, len * kb, 1.3 * (double)((rounds > c ? rounds : c) * (len + 3)));
+      const double sums = (double)up((long long)((double)(all * (c - 1)) * summing), sms);
+      take_if(LaPlan::kSideBySide, len * kb, 1.3 * ((double)(rounds * (len + 3)) + sums * (0.7 * (double)len + 3.)) + 17.);
+    }
+  } else if (tc) {
+    const double longer = share > chain ? share : chain;
+    take_if(LaPlan::kWhole, longest, 1.3 * (longer + 0.5 * share));
+    // hand-overs in all against the last items' idle SMs
+    long long len = (long long)std::sqrt(6. * share) * kb;
+    if (len < 2048) len = 2048;
+    take_if(LaPlan::kChained, len, 1.3 * (longer + 3. * chain * kb / (double)len) + table);
+    len = ((long long)share + 1) * kb;
+    if (len < 512) len = 512;
+    const double of = share > (double)len / kb ? share : (double)len / kb;
+    take_if(LaPlan::kSideBySide, len, 1.3 * (of + 3.) * (1. + 0.7 * summing) + 17. + table);
+  } else {
+    const double alone = 6.3 * wide64, among = 5. * wide64;
+    auto time = [&](double blocks) { return alone * blocks > among * share ? alone * blocks : among * share; };
+    take_if(LaPlan::kWhole, longest, time(chain));
+    // segments enough for every SM's places (by shared memory), twice over as they are short
+    const long long want = 2 * sms * (wide64 == 1 ? 4 : wide64 == 2 ? 2 : 1);
+    long long len = up(d->packed ? rows * each / want : up(longest * all, want), 64) * 64;
+    if (len < 64) len = 64;
+    take_if(LaPlan::kSideBySide, len, time((double)len / kb) * (1. + 0.5 * summing) + 17. + table);
   }
   if (pl.cut == LaPlan::kWhole) seg = (longest + 63) / 64 * 64;
   const bool cut = pl.cut != LaPlan::kWhole;

@@ -333,7 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (n >= 2 && !mbar_wait_drain(&bar.items.free[n & 1], parity(n / 2 - 1))) ok = false;
           if (ok) slots[n & 1] = it;
           if (pipe::publish_unit(bar.items, n, ok ? x : nitems, nitems) >= nitems) break;
-          next = atomicAdd(counter, 1);
           const LaPass &p = args.batch.p[it.pass];
           const Maps &mp = args.maps[it.pass];
           const int hq = it.h / p.gq, hk = it.h / p.gk, hv = it.h / p.gv;
@@ -353,6 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             for (int b = 0; b < VB; ++b) tma_load_3d(base + L::kV + b * kBox, &mp.v, &bar.full[st], 64 * b, hv, row);
             ++m;
           }
+          // not earlier: an item that is claimed waits for this one, while other CTAs may be done; the ring is some
+          // blocks ahead, which hides the claim
+          next = atomicAdd(counter, 1);
         }
         // every load issued has landed before the CTA releases its shared memory
 #pragma unroll 1

@@ -134,11 +134,13 @@ def test_packed_sequences(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens,packed", [([1500], False), ([700, 700], False), ([3, 1400, 0, 257], True)])
+@pytest.mark.parametrize("lens,packed", [([1500], False), ([700, 700], False), ([3, 1400, 0, 257], True),
+                                         ([5000], False), ([3, 8000, 0, 257], True)])
 def test_sequences_cut_into_segments(lens, packed, dtype):
     c = Case(lens, 2, 2, 64, 72, dtype, packed=packed, seed=11)
-    # the segments' states are in the workspace, so that this case takes the path it is meant for
-    assert ssd.ssd_linear_attn_workspace_size(c.runner().dims, False) > 2 * 2 * 64 * 72 * 4
+    if max(lens) > 4000:  # a shorter one is cut only where that pays
+        # the segments' states are in the workspace, so that this case takes the path it is meant for
+        assert ssd.ssd_linear_attn_workspace_size(c.runner().dims, False) > 2 * 2 * 64 * 72 * 4
     c.check()
     c.check(init=False)
 

@@ -20,7 +20,8 @@ CHAINED = [
     ([650] * 10, 16, 16, False, True, False),
     ([750] * 4, 16, 4, False, False, True),
     ([64 * 9 + 1] * 20, 8, 8, False, True, False),
-    ([2300, 1, 0, 64, 5, 63, 2049, 0, 130, 17], 16, 4, True, True, True),
+    ([2300, 1, 0, 64, 5, 63, 2049, 0, 130, 17], 16, 4, True, False, True),
+    ([2300, 1, 0, 64, 5, 63, 2049, 0, 130, 17] + [260] * 14, 32, 8, True, True, True),
 ]
 
 
@@ -46,7 +47,7 @@ def test_chained_decays():
 
 
 def test_chained_repeats_give_equal_bits():
-    c = Case([2300, 1, 700, 64, 5, 63, 2049, 0, 130, 17], 16, 4, 64, 64, seed=9)
+    c = Case([2300, 1, 700, 64, 5, 63, 2049, 0, 130, 17] + [260] * 14, 32, 8, 64, 64, seed=9)
     a, b = c.gpu(), c.gpu()
     for x, y in zip([a[0], a[1], *a[2].values()], [b[0], b[1], *b[2].values()]):
         assert torch.equal(x, y)
@@ -56,8 +57,11 @@ def test_chained_repeats_give_equal_bits():
 @pytest.mark.parametrize("dk,dv", [(64, 128), (128, 40), (8, 64)])
 def test_side_by_side_states_of_both_reverse_passes(dk, dv, dtype):
     """dk and dv read one state, one of them transposed: widths that differ, shared heads, a last segment that is short."""
-    Case([901, 2, 0, 640], 4, 2, dk, dv, dtype, seed=dk).check()
-    Case([1000], 3, 3, dk, dv, dtype, packed=False, seed=dv).check(init=False)
+    long = 6000 if dtype == "bf16" else 901
+    for c in (Case([long, 2, 0, 640], 4, 2, dk, dv, dtype, seed=dk), Case([long], 3, 3, dk, dv, dtype, packed=False, seed=dv)):
+        heads = c.T * c.H * (dk + dv) * 4 if c.K < c.H else 0
+        assert ssd.ssd_linear_attn_workspace_size(c.runner().dims, True) - heads > 6 * c.H * dk * dv * 4
+        c.check(init=c.packed)
 
 
 @pytest.mark.parametrize("lens,H,packed", [([200, 200], 4, False), ([1500], 2, False), ([650] * 10, 16, False),
