@@ -74,6 +74,19 @@ bool encode_tmap_bf16_heads(CUtensorMap *map, const void *base, uint64_t width, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_f32_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t rows,
+                           uint64_t row_bytes, uint32_t box_rows) {
+  EncodeTiled fn = encoder();
+  if (!fn || (reinterpret_cast<uintptr_t>(base) & 15) || (row_bytes & 15) || (width * 4 & 15)) return false;
+  const cuuint64_t dims[3] = {width, heads, rows};
+  const cuuint64_t strides[2] = {width * 4, row_bytes};
+  const cuuint32_t box[3] = {16, 1, box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_sm_count() {
   static std::mutex mu;
   static int cache[64] = {0};

@@ -76,13 +76,13 @@ struct Tables {
   float p[kC];    // P: product scale lam^-a of the column, or (heads that stand apart) both scales lam^distance
 };
 
-template <int KB, int VB, bool SUMMARY>
+template <int KB, int VB, bool SUMMARY, bool F32>
 struct Layout {
-  static constexpr int kStages = KB + VB == 2 ? 6 : 4;
+  static constexpr int kStages = KB + VB == 2 ? 6 : KB + VB == 4 && F32 ? 3 : 4;
   static constexpr uint32_t kQ = 0, kK = SUMMARY ? 0 : KB * kBox, kV = kK + KB * kBox, kStage = kV + VB * kBox;
   static constexpr uint32_t kP = kStages * kStage;                  // two P buffers
   static constexpr uint32_t kO = kP + (SUMMARY ? 0 : 2 * kBox);     // a block's outputs, on their way to TMA
-  static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : VB * kBox);  // weights, see Tables
+  static constexpr uint32_t kTab = kO + (SUMMARY ? 0 : (F32 ? 2 : 1) * VB * kBox);  // weights, see Tables
   static constexpr uint32_t kBar = kTab + sizeof(Tables);
   static constexpr int kNumBars = 2 * kStages + 2 + 4 + 2 + 2 + 4 + 2 + 4 + 4 + 1;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16 + 2 * 48;  // and the TMEM address, two item numbers, two items
@@ -260,7 +260,7 @@ struct Item {
 // F32: fp32 outputs
 template <int KB, int VB, bool SUMMARY, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constant__ Args args) {
-  using L = Layout<KB, VB, SUMMARY>;
+  using L = Layout<KB, VB, SUMMARY, F32>;
   constexpr int ST = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = tc::aligned_smem(smem_raw);
@@ -586,17 +586,28 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         // usual: not apart, all rows live
         auto block = [&](auto usual, int nv, long long row0) {
           constexpr bool kUsual = decltype(usual)::value;
-          if (!F32) {  // the block before has been read out of the staging tile
+          if (F32) {  // the block before has been read out of the staging tile (fp32: the warp's own part)
+            if (lane == 0) bulk_wait_read0();
+            __syncwarp();
+          } else {
             if (tt == 0) bulk_wait_read0();
             role_sync<2, kOutThreads>();
           }
           auto emit = [&](int half, const uint32_t(&a)[32]) {  // 16 lanes (columns of v) x 64 rows i
-            if (F32) {
+            if (F32 && kUsual) {  // a box of 16 columns x 64 rows of 64 bytes, in their swizzle
+              const uint32_t to = so + (2 * (tt >> 5) + half) * 4096;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int r = 8 * (e >> 2) + 2 * (lane & 3) + (e & 1), c = (lane >> 2) + 4 * (e & 2);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + r * 64 + (((c >> 2) ^ (lane & 3)) << 4) + (c & 3) * 4), "r"(a[e])
+                             : "memory");
+              }
+            } else if (F32) {
               float *dst = static_cast<float *>(p.o) + row0 * p.os + (long long)it.h * p.dv;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const int r = 8 * (e >> 2) + 2 * (lane & 3) + (e & 1), c = 32 * quad + 16 * half + (lane >> 2) + 4 * (e & 2);
-                if ((kUsual || r < nv) && c < p.dv) dst[r * p.os + c] = __uint_as_float(a[e]);
+                if (r < nv && c < p.dv) dst[r * p.os + c] = __uint_as_float(a[e]);
               }
             } else {
               const int c = fc + 16 * half;
@@ -643,6 +654,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           pipe::warp_arrive(&bar.o_free[m & 1]);
           emit(0, a);
           emit(1, b);
+          if (F32 && kUsual) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int c = 32 * quad + 16 * half;
+                if (c < p.dv) tma_store_3d(&args.maps[it.pass].o, so + (2 * (tt >> 5) + half) * 4096, c, it.h, (int)row0);
+              }
+              bulk_commit();
+            }
+          }
           if (!F32) {
             fence_async_smem();
             role_sync<2, kOutThreads>();
@@ -677,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             block(std::false_type{}, nv, row0);
         }
       }
-      if (tt == 0) bulk_wait0();
+      if (F32 ? lane == 0 : tt == 0) bulk_wait0();
     }
   } else if (warp >= kStateWarp0 && warp < kWeighWarp0) {
     // ------------------------------------------------------------ state
@@ -877,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 
 template <int KB, int VB, bool SUMMARY, bool F32>
 void run_tc(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
-  using L = Layout<KB, VB, SUMMARY>;
+  using L = Layout<KB, VB, SUMMARY, F32>;
   static bool once = (cudaFuncSetAttribute(la_tc_kernel<KB, VB, SUMMARY, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            L::kBytes),
                       true);
@@ -890,6 +913,7 @@ void run_tc(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
     Maps &mp = args.maps[i];
     if ((!SUMMARY && !encode_tmap_bf16_heads(&mp.q, p.q, p.dk, p.Hq, pl.total, p.qs * 2, kC)) ||
         (!SUMMARY && !F32 && !encode_tmap_bf16_heads(&mp.o, p.o, p.dv, p.H, pl.total, p.os * 2, kC)) ||
+        (F32 && !encode_tmap_f32_heads(&mp.o, p.o, p.dv, p.H, pl.total, p.os * 4, kC)) ||
         !encode_tmap_bf16_heads(&mp.k, p.k, p.dk, p.Hk, pl.total, p.ks * 2, kC) ||
         !encode_tmap_bf16_heads(&mp.v, p.v, p.dv, p.Hv, pl.total, p.vs * 2, kC)) {
       note_host_error();

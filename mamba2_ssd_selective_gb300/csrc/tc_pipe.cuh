@@ -179,6 +179,9 @@ bool encode_tmap_f32_2d(CUtensorMap *map, const void *base, uint64_t cols, uint6
 // width and rows past the last read as zeros.
 bool encode_tmap_bf16_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t rows,
                             uint64_t row_bytes, uint32_t box_rows);
+// Host: the same for fp32, a box of 16 columns, 64-byte swizzle.
+bool encode_tmap_f32_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t rows,
+                           uint64_t row_bytes, uint32_t box_rows);
 // Host: SM count of the current device (cached per device).
 int device_sm_count();
 // Host: record an error found while preparing a launch; the pass then returns
