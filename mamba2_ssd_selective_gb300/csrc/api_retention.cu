@@ -248,7 +248,7 @@ void la_run(const ssd_linear_attn_dims *d, const LaPlan &pl, const LaPlanDev &de
   else
     cudaMemsetAsync(ws, 0, pl.flags + (size_t)nflags * 4, s);
   const bool tc = sizeof(T) == 2 && la_use_tc(d);
-  // batches of passes that one kernel takes: on the tensor cores those of the same boxes and output type
+  // batches of passes that one kernel takes: on the tensor cores those of the same boxes
   auto batches = [&](bool summary, auto launch) {
     int number = 0;
     for (int done = 0; done < n;) {
@@ -256,9 +256,7 @@ void la_run(const ssd_linear_attn_dims *d, const LaPlan &pl, const LaPlanDev &de
       LaPlanDev v = dev;
       v.counters += 2 * number++;
       if (v.flags) v.flags += (size_t)done * pl.units * d->nheads;
-      auto kernel = [&](const LaPass &x) {
-        return 4 * la_tc_boxes(x.dk) + 2 * la_tc_boxes(x.dv) + (!summary && x.o_f32);
-      };
+      auto kernel = [](const LaPass &x) { return 2 * la_tc_boxes(x.dk) + la_tc_boxes(x.dv); };
       for (; done < n; ++done) {
         if (summary && p[done].seg_shared) continue;
         if (tc && b.n > 0 && kernel(p[done]) != kernel(b.p[0])) break;

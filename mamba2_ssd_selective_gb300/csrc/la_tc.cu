@@ -257,7 +257,7 @@ struct Item {
 };
 
 // KB, VB: 64-column boxes of the q/k roles and of the v/o roles
-// F32: fp32 outputs
+// F32: passes with fp32 outputs among them
 template <int KB, int VB, bool SUMMARY, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constant__ Args args) {
   using L = Layout<KB, VB, SUMMARY, F32>;
@@ -569,7 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const Item it = slots[n & 1].uniform();
         pipe::warp_arrive(&bar.items.free[n & 1]);
         const LaPass &p = args.batch.p[it.pass];
-        const bool rev = it.rev, apart = it.apart;
+        const bool rev = it.rev, apart = it.apart, f32 = F32 && p.o_f32;
+        // (the kinds of output share the staging tile; the warps meet in fill)
+        if (F32 && lane == 0) bulk_wait_read0();
         float w[16];  // what this lane's columns i weigh
         auto fill = [&](int nv) {  // the weights of blocks of nv rows (in order those of a full one will do)
           role_sync<2, kOutThreads>();
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         // usual: not apart, all rows live
         auto block = [&](auto usual, int nv, long long row0) {
           constexpr bool kUsual = decltype(usual)::value;
-          if (F32) {  // the block before has been read out of the staging tile (fp32: the warp's own part)
+          if (f32) {  // the block before has been read out of the staging tile (fp32: the warp's own part)
             if (lane == 0) bulk_wait_read0();
             __syncwarp();
           } else {
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             role_sync<2, kOutThreads>();
           }
           auto emit = [&](int half, const uint32_t(&a)[32]) {  // 16 lanes (columns of v) x 64 rows i
-            if (F32 && kUsual) {  // a box of 16 columns x 64 rows of 64 bytes, in their swizzle
+            if (f32 && kUsual) {  // a box of 16 columns x 64 rows of 64 bytes, in their swizzle
               const uint32_t to = so + (2 * (tt >> 5) + half) * 4096;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + r * 64 + (((c >> 2) ^ (lane & 3)) << 4) + (c & 3) * 4), "r"(a[e])
                              : "memory");
               }
-            } else if (F32) {
+            } else if (f32) {
               float *dst = static_cast<float *>(p.o) + row0 * p.os + (long long)it.h * p.dv;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
@@ -654,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           pipe::warp_arrive(&bar.o_free[m & 1]);
           emit(0, a);
           emit(1, b);
-          if (F32 && kUsual) {
+          if (f32 && kUsual) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
               bulk_commit();
             }
           }
-          if (!F32) {
+          if (!f32) {
             fence_async_smem();
             role_sync<2, kOutThreads>();
             if (!kUsual && nv < kC) {  // rows past the end belong to another sequence: row by row
@@ -912,8 +914,8 @@ void run_tc(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
     const LaPass &p = b.p[i];
     Maps &mp = args.maps[i];
     if ((!SUMMARY && !encode_tmap_bf16_heads(&mp.q, p.q, p.dk, p.Hq, pl.total, p.qs * 2, kC)) ||
-        (!SUMMARY && !F32 && !encode_tmap_bf16_heads(&mp.o, p.o, p.dv, p.H, pl.total, p.os * 2, kC)) ||
-        (F32 && !encode_tmap_f32_heads(&mp.o, p.o, p.dv, p.H, pl.total, p.os * 4, kC)) ||
+        (!SUMMARY && !(p.o_f32 ? encode_tmap_f32_heads(&mp.o, p.o, p.dv, p.H, pl.total, p.os * 4, kC)
+                               : encode_tmap_bf16_heads(&mp.o, p.o, p.dv, p.H, pl.total, p.os * 2, kC))) ||
         !encode_tmap_bf16_heads(&mp.k, p.k, p.dk, p.Hk, pl.total, p.ks * 2, kC) ||
         !encode_tmap_bf16_heads(&mp.v, p.v, p.dv, p.Hv, pl.total, p.vs * 2, kC)) {
       note_host_error();
@@ -929,8 +931,11 @@ template <int KB, int VB>
 void run_tc_mode(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s) {
   if (summary)
     run_tc<KB, VB, true, false>(pl, b, s);
-  else
-    b.p[0].o_f32 ? run_tc<KB, VB, false, true>(pl, b, s) : run_tc<KB, VB, false, false>(pl, b, s);
+  else {
+    bool f32 = false;
+    for (int i = 0; i < b.n; ++i) f32 = f32 || b.p[i].o_f32;
+    f32 ? run_tc<KB, VB, false, true>(pl, b, s) : run_tc<KB, VB, false, false>(pl, b, s);
+  }
 }
 
 }  // namespace

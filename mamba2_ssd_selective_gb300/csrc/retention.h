@@ -151,7 +151,7 @@ void launch_la_table(const LaPlanDev &pl, LaEntry *table, int *table_units, int 
 // la_simt.cu: any type and width of the envelope.  summary: the segments' own states
 // (from zero), each where the next segment's incoming state will be
 template <typename T> void launch_la_simt(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s);
-// la_tc.cu: bf16, both widths at most 128 (all passes of a batch of the same boxes and output type)
+// la_tc.cu: bf16, both widths at most 128 (all passes of a batch of the same boxes)
 inline bool la_tc_envelope(int dk, int dv) { return dk <= 128 && dv <= 128; }
 inline int la_tc_boxes(int width) { return width <= 64 ? 1 : 2; }
 void launch_la_tc(const LaPlanDev &pl, const LaBatch &b, bool summary, cudaStream_t s);
