@@ -376,23 +376,46 @@ __device__ __forceinline__ float deviations(const Vec<W> &x, float mean) {
 // (no barrier), so that the loads in flight do not cost registers.
 template <typename T, int W, int TENSORS>
 struct Ring {
+  // a piece is a thread's W channels, copied in chunks of at most 16 bytes
   // (forward with a gate: 131 us with 4 stages, 136 us with 6; backward: 117 us with 3, 118 us with 4)
-  static constexpr int kChunks = W == 8 ? (int)sizeof(T) / 2 : 1, kStages = TENSORS * kChunks <= 2 ? 4 : 3;
-  static constexpr int kBytes = kStages * TENSORS * kChunks * kThreads * 16;
-  uint4 (*slot)[TENSORS][kChunks][kThreads];
-  __device__ __forceinline__ explicit Ring(void *smem) : slot(static_cast<uint4(*)[TENSORS][kChunks][kThreads]>(smem)) {}
+  static constexpr int kPiece = W * (int)sizeof(T), kStep = kPiece < 16 ? kPiece : 16, kChunks = kPiece / kStep,
+                       kStages = TENSORS * kChunks <= 2 ? 4 : 3;
+  static constexpr int kBytes = kStages * TENSORS * kPiece * kThreads;
+  unsigned char *base;
+  __device__ __forceinline__ explicit Ring(void *smem) : base(static_cast<unsigned char *>(smem)) {}
+  __device__ __forceinline__ unsigned char *at(int stage, int t, int c) const {
+    return base + (((stage * TENSORS + t) * kChunks + c) * kThreads + threadIdx.x) * kStep;
+  }
   __device__ __forceinline__ void load(int stage, int t, const T *from) const {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-      sm100::cp_async16(sm100::smem_u32(&slot[stage][t][c][threadIdx.x]), reinterpret_cast<const uint4 *>(from) + c);
+    for (int c = 0; c < kChunks; ++c) {
+      unsigned char *to = at(stage, t, c);
+      const unsigned char *src = reinterpret_cast<const unsigned char *>(from) + c * kStep;
+      if constexpr (kStep == 16)
+        sm100::cp_async16(sm100::smem_u32(to), src);
+      else if constexpr (kStep >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(sm100::smem_u32(to)), "l"(src), "n"(kStep) : "memory");
+      else  // less than an asynchronous copy moves
+        *reinterpret_cast<T *>(to) = *from;
+    }
   }
   static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   // all but the last kStages - 2 groups have landed
   static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory"); }
   __device__ __forceinline__ void get(int stage, int t, Raw<T, W> &to) const {
-    uint4 *u = reinterpret_cast<uint4 *>(&to);
+    if constexpr (W == 8) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) u[c] = slot[stage][t][c][threadIdx.x];
+      for (int c = 0; c < kChunks; ++c) reinterpret_cast<uint4 *>(&to)[c] = *reinterpret_cast<const uint4 *>(at(stage, t, c));
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) to.f[e] = reinterpret_cast<const float *>(at(stage, t, 0))[e];
+    } else if constexpr (W == 2) {
+      const uint32_t u = *reinterpret_cast<const uint32_t *>(at(stage, t, 0));
+      to.f[0] = __uint_as_float(u << 16);
+      to.f[1] = __uint_as_float(u & 0xffff0000u);
+    } else {
+      to.f[0] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(at(stage, t, 0)));
+    }
   }
 };
 
@@ -982,14 +1005,13 @@ template <int X> using Int = std::integral_constant<int, X>;
 // f(W, NT, V) for the plan's team
 template <class F>
 void with_team(const GnPlan &pl, F f) {
-  if (pl.vec == 8) {
-    if (pl.places == 1) {
-      if (pl.team == 8) return f(Int<8>{}, Int<8>{}, Int<1>{});
-      if (pl.team == 16) return f(Int<8>{}, Int<16>{}, Int<1>{});
-      return f(Int<8>{}, Int<32>{}, Int<1>{});
-    }
-    return pl.team == 32 ? f(Int<8>{}, Int<32>{}, Int<4>{}) : f(Int<8>{}, Int<256>{}, Int<4>{});
-  }
+  auto narrow = [&](auto w) {
+    if (pl.team == 8) return f(w, Int<8>{}, Int<1>{});
+    if (pl.team == 16) return f(w, Int<16>{}, Int<1>{});
+    return f(w, Int<32>{}, Int<1>{});
+  };
+  if (pl.places == 1) return pl.vec == 8 ? narrow(Int<8>{}) : pl.vec == 2 ? narrow(Int<2>{}) : narrow(Int<1>{});
+  if (pl.vec == 8) return pl.team == 32 ? f(Int<8>{}, Int<32>{}, Int<4>{}) : f(Int<8>{}, Int<256>{}, Int<4>{});
   if (pl.vec == 2) return pl.team == 32 ? f(Int<2>{}, Int<32>{}, Int<4>{}) : f(Int<2>{}, Int<256>{}, Int<12>{});
   return pl.team == 32 ? f(Int<1>{}, Int<32>{}, Int<4>{}) : f(Int<1>{}, Int<256>{}, Int<12>{});
 }
