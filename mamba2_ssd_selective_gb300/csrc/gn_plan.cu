@@ -67,7 +67,7 @@ GnPlan gn_plan(const GnProblem &p, bool backward, int widest) {
       const long long tiles = ncol <= pl.team ? (p.m + rows - 1) / rows
                                               : ((long long)p.m * ncol + pl.places * pl.team - 1) / (pl.places * pl.team);
       pl.tiles = (int)tiles;
-      pl.cluster = tiles <= 2 ? 2 : tiles <= 4 ? 4 : tiles <= 8 ? 8 : 0;  // 8: the largest portable cluster
+      pl.cluster = ncol > pl.team ? 0 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : tiles <= 8 ? 8 : 0;  // 8: the largest portable cluster
     }
   }
   pl.own_columns = ncol <= pl.team;

@@ -294,6 +294,22 @@ struct Places {
     }
   }
 };
+// The same with at most NT columns, without arrays: a thread's live places are the first `n`, `step` rows apart.
+template <int W, int NT, int V>
+struct ColumnPlaces {
+  int row, step, col, n;
+  __device__ __forceinline__ ColumnPlaces(int tid, int ncol, int r0, int rows) {
+    step = NT / ncol;
+    const int ph = tid / ncol;
+    row = r0 + ph;
+    col = (tid - ph * ncol) * W;
+    n = ph < step && row < rows ? min(V, (rows - row + step - 1) / step) : 0;
+  }
+  // a tensor's pointer at place k
+  template <typename U> __device__ __forceinline__ U *at(U *slab, int stride, int k) const {
+    return slab + ((long long)row * stride + col) + (long long)k * ((long long)step * stride);
+  }
+};
 // rows that fit a team's places (0: not one)
 inline long long rows_of_team(int ncol, int nt, int v) {
   return ncol <= nt ? (long long)v * (nt / ncol) : (long long)v * nt / ncol;
@@ -357,12 +373,12 @@ struct Slab {
 };
 
 template <typename T, int W, bool GATE>
-__device__ __forceinline__ void write_y(const GnProblem &p, const Slab<T> &s, int row, int col, const Vec<W> &w,
-                                        const Vec<W> &b, const Vec<W> &x, const Raw<T, W> &z, float mean, float rstd) {
+__device__ __forceinline__ void write_y(const GnProblem &p, T *to, const Vec<W> &w, const Vec<W> &b, const Vec<W> &x,
+                                        const Raw<T, W> &z, float mean, float rstd) {
   const Vec<W> u = fma((x + Vec<W>(-mean)) * Vec<W>(rstd), w, b);
   float y[W];
   activate<W, GATE>(u, GATE ? vec_of<T, W>(z) : u, p.act == SSD_ACT_SILU).get(y);
-  store_vec<W>(s.y + off(row, p.ys) + col, y);
+  store_vec<W>(to, y);
 }
 // sum of (x - mean)^2
 template <int W>
@@ -500,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<V>(sizeof(T) == 2 ? 4 : 3
           w = load_param<W>(p.w, c0 + at.col[k], 1.f);
           b = load_param<W>(p.b, c0 + at.col[k], 0.f);
         }
-        write_y<T, W, GATE>(p, s, at.row[k], at.col[k], w, b, x[k], z[k], mean, rstd);
+        write_y<T, W, GATE>(p, s.y + off(at.row[k], p.ys) + at.col[k], w, b, x[k], z[k], mean, rstd);
       }
   }
 }
@@ -594,27 +610,30 @@ __global__ void __launch_bounds__(kThreads) cluster_forward_kernel(GnProblem p, 
   __shared__ float red[2][8];
   __shared__ float2 mine;
   const cg::cluster_group cluster = cg::this_cluster();
-  const Tile<W, V> tile(p, pl);
-  const Places<W, kThreads, V> &at = tile.at;
-  const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg;
+  const int pair = blockIdx.x / pl.cluster, t = blockIdx.x % pl.cluster, n = pair / p.G, g = pair % p.G;
+  const ColumnPlaces<W, kThreads, V> at(threadIdx.x, p.cg / W, t * pl.tile_rows, min(p.m, (t + 1) * pl.tile_rows));
   const Slab<T> s(p, n, g);
-  const Params<W> params(p, pl, c0, at.col[0], at.row[0] >= 0);
   Raw<T, W> xr[V], zr[V];
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0) {
-      xr[k].load(s.x + off(at.row[k], p.xs) + at.col[k]);
-      if (GATE) zr[k].load(s.z + off(at.row[k], p.zs) + at.col[k]);
+    if (k < at.n) {
+      xr[k].load(at.at(s.x, p.xs, k));
+      if (GATE) zr[k].load(at.at(s.z, p.zs, k));
     } else {
       xr[k].clear();
     }
+  Vec<W> w(1.f), b(0.f);
+  if (at.n > 0) {
+    w = load_param<W>(p.w, g * p.cg + at.col, 1.f);
+    b = load_param<W>(p.b, g * p.cg + at.col, 0.f);
+  }
   float sum = 0.f, dev = 0.f;
 #pragma unroll
   for (int k = 0; k < V; ++k) sum += vec_of<T, W>(xr[k]).sum();
   const float own = team_sum<kThreads>(sum, red[0], true) / fmaxf(Tile<W, V>::count(p, pl, t), 1.f);
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0) dev += deviations<W>(vec_of<T, W>(xr[k]), own);
+    if (k < at.n) dev += deviations<W>(vec_of<T, W>(xr[k]), own);
   dev = team_sum<kThreads>(dev, red[1], true);
   if (threadIdx.x == 0) mine = make_float2(own, dev);
   cluster.sync();
@@ -622,14 +641,12 @@ __global__ void __launch_bounds__(kThreads) cluster_forward_kernel(GnProblem p, 
   __syncwarp();
   cluster_done_arrive();
   if (t == 0 && threadIdx.x == 0) {
-    if (p.mean) p.mean[n * p.G + g] = st.x;
-    if (p.rstd) p.rstd[n * p.G + g] = st.y;
+    if (p.mean) p.mean[pair] = st.x;
+    if (p.rstd) p.rstd[pair] = st.y;
   }
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0)
-      write_y<T, W, GATE>(p, s, at.row[k], at.col[k], params.w(p, c0, at.col[k]), params.b(p, c0, at.col[k]),
-                          vec_of<T, W>(xr[k]), zr[k], st.x, st.y);
+    if (k < at.n) write_y<T, W, GATE>(p, at.at(s.y, p.ys, k), w, b, vec_of<T, W>(xr[k]), zr[k], st.x, st.y);
   cluster_done_wait();
 }
 
@@ -658,7 +675,7 @@ __global__ void __launch_bounds__(kThreads) tile_forward_kernel(GnProblem p, GnP
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (at.row[k] >= 0)
-      write_y<T, W, GATE>(p, s, at.row[k], at.col[k], params.w(p, c0, at.col[k]), params.b(p, c0, at.col[k]),
+      write_y<T, W, GATE>(p, s.y + off(at.row[k], p.ys) + at.col[k], params.w(p, c0, at.col[k]), params.b(p, c0, at.col[k]),
                           vec_of<T, W>(xr[k]), zr[k], mean, rstd);
 }
 
@@ -893,26 +910,33 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(GnProblem p,
   __shared__ float2 mine;
   __shared__ float acc[2][kThreads * W];
   const cg::cluster_group cluster = cg::this_cluster();
-  const Tile<W, V> tile(p, pl);
-  const Places<W, kThreads, V> &at = tile.at;
-  const int n = tile.n, g = tile.g, t = tile.t, c0 = g * p.cg, ncol = p.cg / W;
+  const int pair = blockIdx.x / pl.cluster, t = blockIdx.x % pl.cluster, n = pair / p.G, g = pair % p.G;
+  const int c0 = g * p.cg, ncol = p.cg / W;
+  const ColumnPlaces<W, kThreads, V> at(threadIdx.x, ncol, t * pl.tile_rows, min(p.m, (t + 1) * pl.tile_rows));
   const Slab<T> s(p, n, g);
-  const float mean = __ldg(p.mean + n * p.G + g), rstd = __ldg(p.rstd + n * p.G + g);
+  const float mean = __ldg(p.mean + pair), rstd = __ldg(p.rstd + pair);
   const float inv = 1.f / ((float)p.m * p.cg);
-  const Params<W> params(p, pl, c0, at.col[0], at.row[0] >= 0);
   Raw<T, W> xr[V], zr[V], dyr[V];
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0) load_place<T, W, GATE>(p, s, at.row[k], at.col[k], xr[k], zr[k], dyr[k]);
+    if (k < at.n) {
+      xr[k].load(at.at(s.x, p.xs, k));
+      dyr[k].load(at.at(s.dy, p.dys, k));
+      if (GATE) zr[k].load(at.at(s.z, p.zs, k));
+    }
+  Vec<W> w(1.f), b(0.f);
+  if (at.n > 0) {
+    w = load_param<W>(p.w, c0 + at.col, 1.f);
+    b = load_param<W>(p.b, c0 + at.col, 0.f);
+  }
   Vec<W> dw(0.f), db(0.f), dxh[V];
   float sa = 0.f, sb = 0.f;
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0) {
+    if (k < at.n) {
       Vec<W> xh;
-      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], params.w(p, c0, at.col[k]),
-                             params.b(p, c0, at.col[k]), mean, rstd, dxh[k], xh, dw, db,
-                             s.dz + off(at.row[k], p.dzs) + at.col[k]);
+      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], w, b, mean, rstd, dxh[k], xh, dw, db,
+                             at.at(s.dz, p.dzs, k));
       sa += dxh[k].sum();
       sb += (dxh[k] * xh).sum();
     }
@@ -926,9 +950,9 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(GnProblem p,
   cluster_done_arrive();
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (at.row[k] >= 0)
-      write_dx<T, W>(s.dx + off(at.row[k], p.dxs) + at.col[k], dxh[k],
-                     (vec_of<T, W>(xr[k]) + Vec<W>(-mean)) * Vec<W>(rstd), ab.x * inv, ab.y * inv, rstd);
+    if (k < at.n)
+      write_dx<T, W>(at.at(s.dx, p.dxs, k), dxh[k], (vec_of<T, W>(xr[k]) + Vec<W>(-mean)) * Vec<W>(rstd), ab.x * inv,
+                     ab.y * inv, rstd);
   if (dwp && t < pl.tiles) {
     keep_params<W>(acc, dw, db);
     sum_params<W>(
