@@ -48,12 +48,12 @@ void launch_gn_param_sum(int C, int partials, const float *dwp, const float *dbp
 GnPlan gn_plan(const GnProblem &p, bool backward, int widest) {
   GnPlan pl{};
   pl.vec = widest >= 8 && p.cg % 8 == 0 ? 8 : widest >= 2 && p.cg % 2 == 0 ? 2 : 1;
-  const int ncol = p.cg / pl.vec, block_places = pl.vec == 8 ? 4 : 12;
+  const int ncol = p.cg / pl.vec, block_places = pl.vec == 8 ? (backward ? kBackwardPlaces : kForwardPlaces) : 12;
   // Widths: rows of 16 bytes where a group allows it; pairs of channels halve the accesses of groups that eight do
   // not divide (6 samples of 4099 rows of 32 groups of 10 channels, fp32: 51 us one by one, 37 us in pairs).
   // The narrowest team that holds a group; backward teams also need a thread to keep its column.
   if (p.m == 1 && ncol <= 32) {
-    pl.team = ncol <= 8 ? 8 : ncol <= 16 ? 16 : 32;
+    pl.team = ncol <= 4 ? 4 : ncol <= 8 ? 8 : ncol <= 16 ? 16 : 32;
     pl.places = 1;
   } else if (p.m <= gn::rows_of_team(ncol, 32, 4) && (!backward || ncol <= 32)) {
     pl.team = 32;

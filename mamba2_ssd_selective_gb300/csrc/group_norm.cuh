@@ -1026,23 +1026,23 @@ __global__ void __launch_bounds__(kThreads) param_kernel(GnProblem p, float *dwp
 
 // ---------------------------------------------------------------- launches
 template <int X> using Int = std::integral_constant<int, X>;
-// f(W, NT, V) for the plan's team
-template <class F>
+// f(W, NT, V) for the plan's team; PLACES: of a thread of a block that takes a group, 16 bytes at a time
+template <int PLACES, class F>
 void with_team(const GnPlan &pl, F f) {
-  auto narrow = [&](auto w) {
+  auto width = [&](auto w, auto places) {
+    if (pl.places > 1) return pl.team == 32 ? f(w, Int<32>{}, Int<4>{}) : f(w, Int<256>{}, places);
+    if (pl.team == 4) return f(w, Int<4>{}, Int<1>{});
     if (pl.team == 8) return f(w, Int<8>{}, Int<1>{});
     if (pl.team == 16) return f(w, Int<16>{}, Int<1>{});
     return f(w, Int<32>{}, Int<1>{});
   };
-  if (pl.places == 1) return pl.vec == 8 ? narrow(Int<8>{}) : pl.vec == 2 ? narrow(Int<2>{}) : narrow(Int<1>{});
-  if (pl.vec == 8) return pl.team == 32 ? f(Int<8>{}, Int<32>{}, Int<4>{}) : f(Int<8>{}, Int<256>{}, Int<4>{});
-  if (pl.vec == 2) return pl.team == 32 ? f(Int<2>{}, Int<32>{}, Int<4>{}) : f(Int<2>{}, Int<256>{}, Int<12>{});
-  return pl.team == 32 ? f(Int<1>{}, Int<32>{}, Int<4>{}) : f(Int<1>{}, Int<256>{}, Int<12>{});
+  if (pl.vec == 8) return width(Int<8>{}, Int<PLACES>{});
+  return pl.vec == 2 ? width(Int<2>{}, Int<12>{}) : width(Int<1>{}, Int<12>{});
 }
 // f(W, V) for the plan's tiles
-template <class F>
+template <int PLACES, class F>
 void with_tile(const GnPlan &pl, F f) {
-  if (pl.vec == 8) return f(Int<8>{}, Int<4>{});
+  if (pl.vec == 8) return f(Int<8>{}, Int<PLACES>{});
   return pl.vec == 2 ? f(Int<2>{}, Int<12>{}) : f(Int<1>{}, Int<12>{});
 }
 
@@ -1073,7 +1073,7 @@ void launch_clusters(void (*kernel)(P...), unsigned grid, const GnPlan &pl, cuda
 template <typename T, bool GATE>
 void forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
   if (pl.tiles == 0) {
-    with_team(pl, [&](auto w, auto nt, auto v) {
+    with_team<kForwardPlaces>(pl, [&](auto w, auto nt, auto v) {
       const dim3 grid((p.G + pl.groups_per_block - 1) / pl.groups_per_block,
                       (p.n + pl.samples_per_block - 1) / pl.samples_per_block);
       constexpr int W = decltype(w)::value, NT = decltype(nt)::value, V = decltype(v)::value;
@@ -1084,7 +1084,7 @@ void forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
   }
   float *part = reinterpret_cast<float *>(ws + pl.part);
   const unsigned grid = (unsigned)p.n * (pl.cluster ? pl.cluster : pl.tiles) * p.G;
-  with_tile(pl, [&](auto w, auto v) {
+  with_tile<kForwardPlaces>(pl, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     if (pl.cluster) {
       SSD_LAUNCH("gn_forward", launch_clusters(cluster_forward_kernel<T, W, V, GATE>, grid, pl, s, p, pl));
@@ -1101,7 +1101,7 @@ void backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
   float *dwp = reinterpret_cast<float *>(ws + pl.dwp), *dbp = reinterpret_cast<float *>(ws + pl.dbp);
   float *kw = params && own_columns ? dwp : nullptr;  // partials written by the gradient kernel itself
   if (pl.tiles == 0) {
-    with_team(pl, [&](auto w, auto nt, auto v) {
+    with_team<kBackwardPlaces>(pl, [&](auto w, auto nt, auto v) {
       const dim3 grid((p.G + pl.groups_per_block - 1) / pl.groups_per_block,
                       (p.n + pl.samples_per_block - 1) / pl.samples_per_block);
       constexpr int W = decltype(w)::value, NT = decltype(nt)::value, V = decltype(v)::value;
@@ -1112,7 +1112,7 @@ void backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
   } else {
     float *part = reinterpret_cast<float *>(ws + pl.part);
     const unsigned grid = (unsigned)p.n * (pl.cluster ? pl.cluster : pl.tiles) * p.G;
-    with_tile(pl, [&](auto w, auto v) {
+    with_tile<kBackwardPlaces>(pl, [&](auto w, auto v) {
       constexpr int W = decltype(w)::value, V = decltype(v)::value;
       if (pl.cluster) {
         SSD_LAUNCH("gn_backward", launch_clusters(cluster_backward_kernel<T, W, V, GATE>, grid, pl, s, p, pl, kw, dbp));

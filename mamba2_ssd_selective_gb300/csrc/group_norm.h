@@ -17,6 +17,10 @@ struct GnProblem {
   float *dw, *db;      // (C), may be null
 };
 
+// Places of 8 channels of a thread whose block takes a group or a tile of one: forward keeps x alone (57 samples of 771 rows
+// of 16 groups of 64 channels, bf16: 68 us with 8, 78 us with 4), backward three tensors and their gradients.
+constexpr int kForwardPlaces = 8, kBackwardPlaces = 4;
+
 // How a call is cut up.  The workspace's size does not depend on alignments: it
 // suffices for any width of accesses.
 struct GnPlan {
