@@ -19,15 +19,14 @@
 // and reads its own again, from L2 where the tensor fits it.
 // dw and db are sums of per-block partials in a fixed order.
 //
-// Measured (kernel times): 32768 rows of 32 groups of 128 channels with a gate, bf16 (805 MB): 131 us, 6.1 TB/s;
-// the backward pass of 16384 rows (671 MB): 117 us and 8 us for the parameters' sums.  Both are near HBM's rate
-// once enough loads are in flight (the next samples' values held in registers instead of shared memory: 141 us
-// and 135 us).  Groups of a cluster are bound by the latency of their phases, not by any unit (DRAM 15% of
-// its rate, 1.5 to 1.8 of 4 instructions a cycle): 6 samples of 4099 rows of 32 groups of 10 channels, fp32
-// (63 MB): 29 us (two kernels: 37 us); the backward pass of 8 samples of 2048 rows of 32 groups of 16, bf16 (50 MB):
-// 31 us and 6 us for the parameters' sums (two kernels: 44 us).  Clusters that stay and copy their next group's tile
-// ahead into shared memory took 42 us and 35 us: the GPU holds fewer of them, and 192 or 256 groups do not fill
-// their rounds.
+// Measured (kernel times): 32768 rows of 32 groups of 128 channels with a gate, bf16 (805 MB): 132 us, 6.1 TB/s;
+// the backward pass of 16384 rows (671 MB): 116 us and 8 us for the parameters' sums.  Both are near HBM's rate
+// once enough loads are in flight (the next samples' values in registers instead of shared memory: 141 us
+// and 135 us).  Groups of a cluster are bound by instructions and the latency of their phases, not by memory (DRAM
+// 15% of its rate): 6 samples of 4099 rows of 32 groups of 10 channels, fp32 (63 MB): 27 us (two kernels: 37 us);
+// the backward pass of 8 samples of 2048 rows of 32 groups of 16, bf16 (50 MB): 31 us and 6 us for the
+// parameters' sums (two kernels: 44 us).  Clusters that stay and copy their next group's tile ahead took 42 us and
+// 35 us: the GPU holds fewer of them, and 192 or 256 groups do not fill their rounds.
 #pragma once
 
 #include <type_traits>
@@ -387,25 +386,22 @@ __device__ __forceinline__ float deviations(const Vec<W> &x, float mean) {
   return (d * d).sum();
 }
 
-// ---------------------------------------------------------------- a thread's own ring of values on their way
-// Teams of one place copy their next samples' values into shared memory, each thread its own and for itself alone
-// (no barrier), so that the loads in flight do not cost registers.
-template <typename T, int W, int TENSORS>
-struct Ring {
-  // a piece is a thread's W channels, copied in chunks of at most 16 bytes
-  // (forward with a gate: 131 us with 4 stages, 136 us with 6; backward: 117 us with 3, 118 us with 4)
-  static constexpr int kPiece = W * (int)sizeof(T), kStep = kPiece < 16 ? kPiece : 16, kChunks = kPiece / kStep,
-                       kStages = TENSORS * kChunks <= 2 ? 4 : 3;
-  static constexpr int kBytes = kStages * TENSORS * kPiece * kThreads;
+// ---------------------------------------------------------------- a thread's own values on their way
+// COUNT slots in shared memory for a thread's W channels, which it copies and reads for itself alone (no barrier), so
+// that loads in flight do not cost registers.
+template <typename T, int W, int COUNT>
+struct Slots {
+  static constexpr int kPiece = W * (int)sizeof(T), kStep = kPiece < 16 ? kPiece : 16, kChunks = kPiece / kStep;
+  static constexpr int kBytes = COUNT * kPiece * kThreads;
   unsigned char *base;
-  __device__ __forceinline__ explicit Ring(void *smem) : base(static_cast<unsigned char *>(smem)) {}
-  __device__ __forceinline__ unsigned char *at(int stage, int t, int c) const {
-    return base + (((stage * TENSORS + t) * kChunks + c) * kThreads + threadIdx.x) * kStep;
+  __device__ __forceinline__ explicit Slots(void *smem) : base(static_cast<unsigned char *>(smem)) {}
+  __device__ __forceinline__ unsigned char *at(int i, int c) const {
+    return base + ((i * kChunks + c) * kThreads + threadIdx.x) * kStep;
   }
-  __device__ __forceinline__ void load(int stage, int t, const T *from) const {
+  __device__ __forceinline__ void load(int i, const T *from) const {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      unsigned char *to = at(stage, t, c);
+      unsigned char *to = at(i, c);
       const unsigned char *src = reinterpret_cast<const unsigned char *>(from) + c * kStep;
       if constexpr (kStep == 16)
         sm100::cp_async16(sm100::smem_u32(to), src);
@@ -415,24 +411,36 @@ struct Ring {
         *reinterpret_cast<T *>(to) = *from;
     }
   }
-  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-  // all but the last kStages - 2 groups have landed
-  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory"); }
-  __device__ __forceinline__ void get(int stage, int t, Raw<T, W> &to) const {
+  __device__ __forceinline__ void get(int i, Raw<T, W> &to) const {
     if constexpr (W == 8) {
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) reinterpret_cast<uint4 *>(&to)[c] = *reinterpret_cast<const uint4 *>(at(stage, t, c));
+      for (int c = 0; c < kChunks; ++c) reinterpret_cast<uint4 *>(&to)[c] = *reinterpret_cast<const uint4 *>(at(i, c));
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int e = 0; e < W; ++e) to.f[e] = reinterpret_cast<const float *>(at(stage, t, 0))[e];
+      for (int e = 0; e < W; ++e) to.f[e] = reinterpret_cast<const float *>(at(i, 0))[e];
     } else if constexpr (W == 2) {
-      const uint32_t u = *reinterpret_cast<const uint32_t *>(at(stage, t, 0));
+      const uint32_t u = *reinterpret_cast<const uint32_t *>(at(i, 0));
       to.f[0] = __uint_as_float(u << 16);
       to.f[1] = __uint_as_float(u & 0xffff0000u);
     } else {
-      to.f[0] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(at(stage, t, 0)));
+      to.f[0] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(at(i, 0)));
     }
   }
+};
+// Teams of one place keep their next samples' values in a ring of stages.
+// (forward with a gate: 131 us with 4 stages, 136 us with 6; backward: 117 us with 3, 118 us with 4)
+template <typename T, int W, int TENSORS>
+constexpr int kRingStages = TENSORS * Slots<T, W, 1>::kChunks <= 2 ? 4 : 3;
+template <typename T, int W, int TENSORS>
+struct Ring : Slots<T, W, kRingStages<T, W, TENSORS> * TENSORS> {
+  using Base = Slots<T, W, kRingStages<T, W, TENSORS> * TENSORS>;
+  static constexpr int kStages = kRingStages<T, W, TENSORS>;
+  using Base::Base;
+  __device__ __forceinline__ void load(int stage, int t, const T *from) const { Base::load(stage * TENSORS + t, from); }
+  __device__ __forceinline__ void get(int stage, int t, Raw<T, W> &to) const { Base::get(stage * TENSORS + t, to); }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // all but the last kStages - 2 groups have landed
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory"); }
 };
 
 // ---------------------------------------------------------------- forward, groups that fit a team
@@ -903,12 +911,16 @@ __global__ void __launch_bounds__(kThreads) tile_sums_kernel(GnProblem p, GnPlan
 }
 
 // A cluster of blocks per group: loaded once, the parts of A and B exchanged between the blocks.
+// The inputs wait in shared memory, so that three blocks fit an SM: 57 samples of 771 rows of 16 groups of 64
+// channels, bf16, 127 us (in registers, two blocks: 140 us; 8 samples of 2048 rows of 32 groups of 16: 31 us and 29 us).
 template <typename T, int W, int V, bool GATE>
-__global__ void __launch_bounds__(kThreads) cluster_backward_kernel(GnProblem p, GnPlan pl, float *dwp, float *dbp) {
+__global__ void __launch_bounds__(kThreads, W == 8 && sizeof(T) == 4 ? 2 : 3) cluster_backward_kernel(GnProblem p, GnPlan pl, float *dwp, float *dbp) {
   namespace cg = cooperative_groups;
   __shared__ float red[16];
   __shared__ float2 mine;
   __shared__ float acc[2][kThreads * W];
+  extern __shared__ uint4 slot_smem[];
+  const Slots<T, W, (GATE ? 3 : 2) * V> slots(slot_smem);  // x, dy, z of each place
   const cg::cluster_group cluster = cg::this_cluster();
   const int pair = blockIdx.x / pl.cluster, t = blockIdx.x % pl.cluster, n = pair / p.G, g = pair % p.G;
   const int c0 = g * p.cg, ncol = p.cg / W;
@@ -916,13 +928,12 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(GnProblem p,
   const Slab<T> s(p, n, g);
   const float mean = __ldg(p.mean + pair), rstd = __ldg(p.rstd + pair);
   const float inv = 1.f / ((float)p.m * p.cg);
-  Raw<T, W> xr[V], zr[V], dyr[V];
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (k < at.n) {
-      xr[k].load(at.at(s.x, p.xs, k));
-      dyr[k].load(at.at(s.dy, p.dys, k));
-      if (GATE) zr[k].load(at.at(s.z, p.zs, k));
+      slots.load(k, at.at(s.x, p.xs, k));
+      slots.load(V + k, at.at(s.dy, p.dys, k));
+      if (GATE) slots.load(2 * V + k, at.at(s.z, p.zs, k));
     }
   Vec<W> w(1.f), b(0.f);
   if (at.n > 0) {
@@ -931,17 +942,23 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(GnProblem p,
   }
   Vec<W> dw(0.f), db(0.f), dxh[V];
   float sa = 0.f, sb = 0.f;
+  sm100::cp_async_wait_all();
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (k < at.n) {
       Vec<W> xh;
-      place_grad<T, W, GATE>(p, xr[k], zr[k], dyr[k], w, b, mean, rstd, dxh[k], xh, dw, db,
+      Raw<T, W> x, z, dy;
+      slots.get(k, x);
+      slots.get(V + k, dy);
+      if (GATE) slots.get(2 * V + k, z);
+      place_grad<T, W, GATE>(p, x, z, dy, w, b, mean, rstd, dxh[k], xh, dw, db,
                              at.at(s.dz, p.dzs, k));
       sa += dxh[k].sum();
       sb += (dxh[k] * xh).sum();
     }
   const float2 own = team_sum2<kThreads>(sa, sb, red, true);
   if (threadIdx.x == 0) mine = own;
+  if (dwp) keep_params<W>(acc, dw, db);
   cluster.sync();
   const int lane = threadIdx.x & 31;  // each warp for itself
   const float2 q = lane < pl.tiles ? *cluster.map_shared_rank(&mine, lane) : make_float2(0.f, 0.f);
@@ -950,11 +967,13 @@ __global__ void __launch_bounds__(kThreads) cluster_backward_kernel(GnProblem p,
   cluster_done_arrive();
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (k < at.n)
-      write_dx<T, W>(at.at(s.dx, p.dxs, k), dxh[k], (vec_of<T, W>(xr[k]) + Vec<W>(-mean)) * Vec<W>(rstd), ab.x * inv,
+    if (k < at.n) {
+      Raw<T, W> x;
+      slots.get(k, x);
+      write_dx<T, W>(at.at(s.dx, p.dxs, k), dxh[k], (vec_of<T, W>(x) + Vec<W>(-mean)) * Vec<W>(rstd), ab.x * inv,
                      ab.y * inv, rstd);
+    }
   if (dwp && t < pl.tiles) {
-    keep_params<W>(acc, dw, db);
     sum_params<W>(
         acc, p.cg, kThreads / ncol, [&](int c, int j) { return j * ncol + c / W; },
         [&](int c, float sw, float sd) {
@@ -1056,10 +1075,11 @@ void launch_smem(void (*kernel)(P...), dim3 grid, int bytes, cudaStream_t s, A..
 
 // a launch of clusters of pl.cluster blocks
 template <class... P, class... A>
-void launch_clusters(void (*kernel)(P...), unsigned grid, const GnPlan &pl, cudaStream_t s, A... args) {
+void launch_clusters(void (*kernel)(P...), unsigned grid, const GnPlan &pl, int bytes, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -1067,6 +1087,7 @@ void launch_clusters(void (*kernel)(P...), unsigned grid, const GnPlan &pl, cuda
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
+  if (bytes > 16 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) note_host_error();
 }
 
@@ -1087,7 +1108,7 @@ void forward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
   with_tile<kForwardPlaces>(pl, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     if (pl.cluster) {
-      SSD_LAUNCH("gn_forward", launch_clusters(cluster_forward_kernel<T, W, V, GATE>, grid, pl, s, p, pl));
+      SSD_LAUNCH("gn_forward", launch_clusters(cluster_forward_kernel<T, W, V, GATE>, grid, pl, 0, s, p, pl));
       return;
     }
     SSD_LAUNCH("gn_stats", (tile_stats_kernel<T, W, V><<<grid, kThreads, 0, s>>>(p, pl, part)));
@@ -1115,7 +1136,8 @@ void backward(const GnProblem &p, const GnPlan &pl, char *ws, cudaStream_t s) {
     with_tile<kBackwardPlaces>(pl, [&](auto w, auto v) {
       constexpr int W = decltype(w)::value, V = decltype(v)::value;
       if (pl.cluster) {
-        SSD_LAUNCH("gn_backward", launch_clusters(cluster_backward_kernel<T, W, V, GATE>, grid, pl, s, p, pl, kw, dbp));
+        SSD_LAUNCH("gn_backward", launch_clusters(cluster_backward_kernel<T, W, V, GATE>, grid, pl,
+                                                  Slots<T, W, (GATE ? 3 : 2) * V>::kBytes, s, p, pl, kw, dbp));
         return;
       }
       SSD_LAUNCH("gn_sums", (tile_sums_kernel<T, W, V, GATE><<<grid, kThreads, 0, s>>>(p, pl, part, kw, dbp)));
