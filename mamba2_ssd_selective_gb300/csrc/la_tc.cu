@@ -273,6 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   Item *slots = reinterpret_cast<Item *>(tslot + 4);  // [2]
   const int nitems = __shfl_sync(0xffffffffu, la_units(pl), 0) * args.batch.n * pl.H;
 
+  if (warp == 0 && lane < args.batch.n) {
+    const Maps &mp = args.maps[lane];
+    prefetch_tmap(&mp.k);
+    prefetch_tmap(&mp.v);
+    if (!SUMMARY) prefetch_tmap(&mp.q);
+    if (!SUMMARY) prefetch_tmap(&mp.o);
+  }
   if (threadIdx.x == 64) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bar.full[i], 1);

@@ -77,10 +77,16 @@ def declare(lib) -> None:
     lib.ssd_group_norm_backward.restype = ctypes.c_int
 
 
-def _lib():
-    from . import load
+_loaded = None
 
-    return load()
+
+def _lib():
+    global _loaded
+    if _loaded is None:
+        from . import load
+
+        _loaded = load()
+    return _loaded
 
 
 def _check(status: int, what: str) -> None:
@@ -153,7 +159,8 @@ def _rows(x, name: str, rows: int, width: int, dtype, device) -> tuple[int, int]
     """(address, row stride) of a (..., width) tensor whose leading dimensions flatten to `rows` evenly spaced rows."""
     strides = x.stride()
     # the usual case first: a small call's time is mostly spent on the host
-    if len(strides) == 2 and strides[1] == 1 and x.dtype is dtype and x.shape == (rows, width) and x.device == device:
+    if (len(strides) == 2 and strides[1] == 1 and x.dtype is dtype and x.shape == (rows, width)
+            and x.get_device() == device.index and x.is_cuda):
         return x.data_ptr(), strides[0] if rows > 1 else max(width, strides[0])
     shape = x.shape
     if x.dtype != dtype or x.device != device:
@@ -177,7 +184,8 @@ def _rows(x, name: str, rows: int, width: int, dtype, device) -> tuple[int, int]
 def _exact(x, name: str, shape: tuple, dtype, device):
     if x is None:
         return None
-    if x.dtype is not dtype or x.shape != shape or x.device != device or not x.is_contiguous():
+    if (x.dtype is not dtype or x.shape != shape or x.get_device() != device.index or not x.is_cuda
+            or not x.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {device}, "
                          f"got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x.data_ptr()

@@ -101,3 +101,49 @@ def test_waits_that_give_up_are_reported_and_the_next_call_is_clean(lens, H, pac
     assert st == (0, 0)
     for x, y in zip(first, again):
         assert torch.equal(x, y)
+
+
+def _operators(c, r, step, norm, cache):
+    """One call of each operator; its outputs."""
+    q, k, v = c.parts("cuda")
+    decay = c.decay.cuda()
+    slots = torch.tensor([3, 0, -1, 2], dtype=torch.int32, device="cuda")
+    do, init, cu = c.do.cuda(), c.init.cuda(), c.cu.cuda()
+
+    def call():
+        o, fin = r.forward(q, k, v, decay, initial_state=init, cu_seqlens=cu)
+        y, mean, rstd = norm.forward(o, None, None, z=do)
+        n = norm.backward(do, o, None, None, mean, rstd, z=do)
+        g = r.backward(q, k, v, decay, n["dx"], initial_state=init, cu_seqlens=cu)
+        t = step.step(q[:4], k[:4], v[:4], decay, cache, slot_idx=slots)
+        return [o, fin, y, t, *n.values(), *g.values()]
+
+    return call
+
+
+@pytest.mark.parametrize("how", ["graph", "stream"])
+def test_captured_and_on_another_stream(how):
+    c = Case([700, 3, 0, 900], 4, 2, 64, 64, seed=19)
+    cache = torch.zeros(5, 4, 64, 64, device="cuda")
+    call = _operators(c, c.runner(), ssd.LinearAttnRunner(4, 1, 4, 64, 64, nheads_kv=2), ssd.GroupNormRunner(c.T, 1, 256, 4, "gate"),
+                      cache)
+    want = [x.clone() for x in call()]
+    state = cache.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            cache.zero_()
+            got = call()
+    torch.cuda.current_stream().wait_stream(side)
+    if how == "graph":
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call()
+        for _ in range(2):
+            cache.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cache, state)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
