@@ -184,8 +184,7 @@ def _rows(x, name: str, rows: int, width: int, dtype, device) -> tuple[int, int]
 def _exact(x, name: str, shape: tuple, dtype, device):
     if x is None:
         return None
-    if (x.dtype is not dtype or x.shape != shape or x.get_device() != device.index or not x.is_cuda
-            or not x.is_contiguous()):
+    if x.dtype is not dtype or x.shape != shape or x.device != device or not x.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {device}, "
                          f"got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x.data_ptr()
@@ -266,8 +265,12 @@ class LinearAttnRunner:
         None with final_state=False.  ``out``: a tensor for o."""
         wo = self._widths[3]
         inputs = self._inputs(q, k, v, log_decay, scale, initial_state, cu_seqlens)
-        o = torch.empty(self.rows, wo, dtype=self.tdtype, device=self.device) if out is None else out
-        op, os = _rows(o, "out", self.rows, wo, self.tdtype, self.device)
+        if out is None:
+            o = torch.empty(self.rows, wo, dtype=self.tdtype, device=self.device)
+            op, os = o.data_ptr(), wo
+        else:
+            o = out
+            op, os = _rows(o, "out", self.rows, wo, self.tdtype, self.device)
         fin = torch.empty(self.state_shape, dtype=torch.float32, device=self.device) if final_state else None
         ssd_linear_attn_forward(self.dims, inputs, op, os, fin, self.workspace, stream=_current(self.device, stream))
         return o, fin
@@ -300,8 +303,12 @@ class LinearAttnRunner:
         inputs = self._inputs(q, k, v, log_decay, scale, None, None)
         _exact(states, "states", (states.shape[0],) + self.state_shape[1:], torch.float32, self.device)
         idx = _exact(slot_idx, "slot_idx", (self.nseq,), torch.int32, self.device)
-        o = torch.empty(self.rows, wo, dtype=self.tdtype, device=self.device) if out is None else out
-        op, os = _rows(o, "out", self.rows, wo, self.tdtype, self.device)
+        if out is None:
+            o = torch.empty(self.rows, wo, dtype=self.tdtype, device=self.device)
+            op, os = o.data_ptr(), wo
+        else:
+            o = out
+            op, os = _rows(o, "out", self.rows, wo, self.tdtype, self.device)
         ssd_linear_attn_step(self.dims, inputs, states, states.shape[0], idx, op, os, _current(self.device, stream))
         return o
 
