@@ -515,14 +515,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[e] *= w[step * e];
               } else {
-                const float4 *w = reinterpret_cast<const float4 *>(tab.p + j0);
+                const ulonglong2 *w = reinterpret_cast<const ulonglong2 *>(tab.p + j0);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 t = w[e];
-                  s[4 * e] *= t.x;
-                  s[4 * e + 1] *= t.y;
-                  s[4 * e + 2] *= t.z;
-                  s[4 * e + 3] *= t.w;
+                for (int e = 0; e < 16; e += 4) {
+                  const ulonglong2 t = w[e / 4];
+                  upk2(mul2(t.x, pk2(s[e], s[e + 1])), s[e], s[e + 1]);
+                  upk2(mul2(t.y, pk2(s[e + 2], s[e + 3])), s[e + 2], s[e + 3]);
                 }
               }
 #pragma unroll
@@ -579,18 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const bool rev = it.rev, apart = it.apart, f32 = F32 && p.o_f32;
         // (the kinds of output share the staging tile; the warps meet in fill)
         if (F32 && lane == 0) bulk_wait_read0();
-        float w[16];  // what this lane's columns i weigh
+        uint64_t w[8];  // what this lane's columns i weigh, in pairs
         auto fill = [&](int nv) {  // the weights of blocks of nv rows (in order those of a full one will do)
           role_sync<2, kOutThreads>();
           for (int r = tt; r < kC; r += kOutThreads)
             tab.out[r] = p.o_scale * la_pow(it.g, rev ? max(nv - 1 - r, 0) : r + 1);
           role_sync<2, kOutThreads>();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 t = *reinterpret_cast<const float2 *>(tab.out + 8 * e + 2 * (lane & 3));
-            w[2 * e] = t.x;
-            w[2 * e + 1] = t.y;
-          }
+          for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint64_t *>(tab.out + 8 * e + 2 * (lane & 3));
         };
         // usual: not apart, all rows live
         auto block = [&](auto usual, int nv, long long row0) {
@@ -641,10 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           tmem_wait_ld32(a);
           tmem_wait_ld32(b);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float t = w[2 * (e >> 2) + (e & 1)];
-            a[e] = __float_as_uint(t * __uint_as_float(a[e]));
-            b[e] = __float_as_uint(t * __uint_as_float(b[e]));
+          for (int e = 0; e < 32; e += 2) {
+            float f0, f1;
+            upk2(mul2(w[e >> 2], pk2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]))), f0, f1);
+            a[e] = __float_as_uint(f0);
+            a[e + 1] = __float_as_uint(f1);
+            upk2(mul2(w[e >> 2], pk2(__uint_as_float(b[e]), __uint_as_float(b[e + 1]))), f0, f1);
+            b[e] = __float_as_uint(f0);
+            b[e + 1] = __float_as_uint(f1);
           }
           if (!kUsual && apart) {
 #pragma unroll
