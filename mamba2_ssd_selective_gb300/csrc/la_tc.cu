@@ -13,7 +13,7 @@
 // from the registers, the weighted copies of V^T from shared memory through
 // transposing matrix loads, so that shared memory carries the inputs, P and the outputs only.  (With
 // the weighted K as a B operand in shared memory, three terms written and read back, a call of 128 items
-// of 8192 tokens at widths of 128 took 325 us; as it is, 178.)
+// of 8192 tokens at widths of 128 took 325 us; as it is, 176.)
 // P and S are rounded to bf16 as operands (the outputs are bf16 too); what goes
 // into the state is not: V diag(lam^b) is split into three bf16 terms (24 bits), so
 // that states keep fp32 precision over any length.
