@@ -243,7 +243,8 @@ int32_t ssd_profile_end(ssd_kernel_time *out, int32_t max_entries);
  * Sequences either all have dims.seqlen tokens (cu_seqlens NULL; token t of sequence s is row s * seqlen + t), or
  * are packed into dims.total_tokens rows: sequence s covers rows [cu_seqlens[s], cu_seqlens[s+1]), cu_seqlens
  * (nseq + 1) int32 device values, non-decreasing, from 0 to total_tokens (not checked on the host; values outside
- * [0, total_tokens] are clamped, rows outside every sequence are neither read as data nor written).  Sequences may
+ * [0, total_tokens] are clamped, a bound below the one before gives an empty sequence, what rows of several
+ * sequences get is undefined, rows outside every sequence are neither read as data nor written).  Sequences may
  * be empty or of one token; with no token the final state is the initial state.
  * Tensors are token-major with their own token strides, heads and channels contiguous within a token:
  *   q (T, nheads * headdim_k), k (T, nheads_kv * headdim_k), v (T, nheads_kv * headdim_v), o (T, nheads * headdim_v)

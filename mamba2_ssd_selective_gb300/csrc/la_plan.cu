@@ -26,28 +26,32 @@ __global__ void __launch_bounds__(kThreads) la_table_kernel(LaPlanDev pl, LaEntr
     nseg[s] = la_segments(len, pl.seg_len);
   }
   __syncthreads();
-  int seq = 0, first = 0;
-  while (seq < pl.nseq && first + nseg[seq] <= y) first += nseg[seq++];
-  if (y == 0) {
-    int n = 0;
-    for (int s = 0; s < pl.nseq; ++s) n += nseg[s];
-    // bounds that overlap could name more units than there is room for; the last ones are then left out
-    *table_units = min(n, pl.units);
+  long long n = 0;
+  for (int s = 0; s < pl.nseq; ++s) n += nseg[s];
+  if (n > pl.units) {
+    // Only sequences that overlap have more units than there is room for: each is then taken whole, so that every
+    // entry below the number of units is written and names rows of its own sequence.
+    __syncthreads();
+    for (int s = threadIdx.x; s < pl.nseq; s += kThreads) nseg[s] = 1;
+    __syncthreads();
+    n = pl.nseq;
   }
-  if (y >= pl.units || seq == pl.nseq) return;
+  if (y == 0) *table_units = (int)n;
+  if (y >= n) return;
+  int seq = 0, first = 0;
+  while (first + nseg[seq] <= y) first += nseg[seq++];
   const int level = y - first;
   int at = 0, next = 0;  // places of this level and of the next
   for (int s = 0; s < pl.nseq; ++s) {
     at += min(nseg[s], level) + (s < seq && nseg[s] > level);
     next += min(nseg[s], level + 1) + (s < seq && nseg[s] > level + 1);
   }
-  if (at >= pl.units) return;
   LaEntry e;
   e.seq = seq;
   e.level = level;
   e.nseg = nseg[seq];
   la_seq_bounds(pl, seq, e.a, e.len);
-  e.next = level + 1 < nseg[seq] && next < pl.units ? next : -1;
+  e.next = level + 1 < nseg[seq] ? next : -1;
   table[at] = e;
 }
 

@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPlanDev pl, con
   const int s = blockIdx.x / nblk, h = blockIdx.y;
   int a, len;
   la_seq_bounds(pl, s, a, len);
-  const int n = la_segments(len, pl.seg_len);
+  // (unit s of a table is the first segment of sequence s)
+  const int n = pl.table ? pl.table[s].nseg : la_segments(len, pl.seg_len);
   if (n == 1) return;
   const int e = blockIdx.x % nblk * kScanThreads + threadIdx.x;
   const bool live = e < dd;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPlanDev pl, con
           at += min(xn, level) + (x < s && xn > level);
         }
       }
-      units[i] = at < la_units(pl) ? at : -1;
+      units[i] = at;
     }
     __syncthreads();
     if (!live) continue;
@@ -296,10 +297,10 @@ __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPlanDev pl, con
       float w[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (i0 + i < m && units[i0 + i] >= 0) w[i] = base[units[i0 + i] * step];
+        if (i0 + i < m) w[i] = base[units[i0 + i] * step];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (i0 + i < m && units[i0 + i] >= 0) {
+        if (i0 + i < m) {
           // the segment before this level: the sequence's tail comes first in reverse
           const float2 c = p.reverse && l0 + i0 + i == 1 ? tail : full;
           st = fmaf(st, c.x, fmaf(st, c.y, w[i]));
