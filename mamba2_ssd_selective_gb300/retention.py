@@ -5,6 +5,11 @@ with an activation behind it.  Python binding of the ``ssd_linear_attn_*`` and
 The functions carry the C names and only marshal arguments.  The runners hold
 what a program keeps between calls (the dimensions and the workspace) and check
 the tensors they are given; a runner's workspace belongs to one stream at a time.
+
+A call runs on ``stream`` (a stream, or its handle, which then has to outlive the runner) or, without one, on the
+current stream.  What it allocates, outputs and a larger workspace, belongs to that stream as it would to a current one, and a workspace
+that another stream used is kept for it.  That inputs are ready on the stream, and that they outlive the call
+there, is the caller's affair, as it is under torch.cuda.stream.
 """
 from __future__ import annotations
 
@@ -190,11 +195,20 @@ def _exact(x, name: str, shape: tuple, dtype, device):
     return x.data_ptr()
 
 
-def _current(device, stream):
-    """Handle of the given stream, or of the device's current one."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _current(runner):
+    """Handle of the current stream, for which the runner's workspace is kept from now on."""
+    handle = torch._C._cuda_getCurrentRawStream(runner.device.index)
+    if handle != runner._stream:
+        runner.workspace.record_stream(torch.cuda.current_stream(runner.device))
+        runner._stream = handle
+    return handle
+
+
+def _on(runner, stream):
+    """Makes the given stream the current one, so that what a call allocates belongs to the stream it is written on."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=runner.device)
+    return torch.cuda.stream(stream)
 
 
 def _device(device) -> torch.device:
@@ -236,6 +250,7 @@ class LinearAttnRunner:
             raise ValueError("invalid dims for libssd")
         self.state_shape = (nseq, nheads, headdim_k, headdim_v)
         self.workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+        self._stream = None  # the last one that used the workspace
         self._widths = (nheads * headdim_k, self.nheads_kv * headdim_k, self.nheads_kv * headdim_v,
                         nheads * headdim_v)
         self._scale = headdim_k ** -0.5
@@ -263,6 +278,10 @@ class LinearAttnRunner:
                 out=None, stream=None):
         """(o, final_state): o (rows, nheads * headdim_v); final_state (nseq, nheads, headdim_k, headdim_v) fp32, or
         None with final_state=False.  ``out``: a tensor for o."""
+        if stream is not None:
+            with _on(self, stream):
+                return self.forward(q, k, v, log_decay, scale=scale, initial_state=initial_state,
+                                    cu_seqlens=cu_seqlens, final_state=final_state, out=out)
         wo = self._widths[3]
         inputs = self._inputs(q, k, v, log_decay, scale, initial_state, cu_seqlens)
         if out is None:
@@ -272,13 +291,17 @@ class LinearAttnRunner:
             o = out
             op, os = _rows(o, "out", self.rows, wo, self.tdtype, self.device)
         fin = torch.empty(self.state_shape, dtype=torch.float32, device=self.device) if final_state else None
-        ssd_linear_attn_forward(self.dims, inputs, op, os, fin, self.workspace, stream=_current(self.device, stream))
+        ssd_linear_attn_forward(self.dims, inputs, op, os, fin, self.workspace, stream=_current(self))
         return o, fin
 
     def backward(self, q, k, v, log_decay, do, *, scale=None, initial_state=None, dfinal_state=None, cu_seqlens=None,
                  stream=None) -> dict:
         """Gradients of <do, o> + <dfinal_state, final_state>: dq, dk, dv, and dinitial_state (None without an
         initial state)."""
+        if stream is not None:
+            with _on(self, stream):
+                return self.backward(q, k, v, log_decay, do, scale=scale, initial_state=initial_state,
+                                     dfinal_state=dfinal_state, cu_seqlens=cu_seqlens)
         wq, wk, wv, wo = self._widths
         rows, tdtype, device = self.rows, self.tdtype, self.device
         inputs = self._inputs(q, k, v, log_decay, scale, initial_state, cu_seqlens)
@@ -292,13 +315,16 @@ class LinearAttnRunner:
                                                                               device=device)}
         grads = SsdLinearAttnGrads(g["dq"].data_ptr(), wq, g["dk"].data_ptr(), wk, g["dv"].data_ptr(), wv,
                                    _ptr(g["dinitial_state"]))
-        ssd_linear_attn_backward(self.dims, inputs, dop, dos, dfin, grads, self.workspace, stream=_current(self.device, stream))
+        ssd_linear_attn_backward(self.dims, inputs, dop, dos, dfin, grads, self.workspace, stream=_current(self))
         return g
 
     def step(self, q, k, v, log_decay, states, *, slot_idx=None, scale=None, out=None, stream=None):
         """One token of each of ``nseq`` rows (a runner with tokens=1): updates ``states`` (slots, nheads, headdim_k,
         headdim_v) in place at ``slot_idx`` (int32; None: row r uses slot r; a negative one leaves the cache alone and
         gives zeros) and returns o (rows, nheads * headdim_v)."""
+        if stream is not None:
+            with _on(self, stream):
+                return self.step(q, k, v, log_decay, states, slot_idx=slot_idx, scale=scale, out=out)
         wo = self._widths[3]
         inputs = self._inputs(q, k, v, log_decay, scale, None, None)
         _exact(states, "states", (states.shape[0],) + self.state_shape[1:], torch.float32, self.device)
@@ -309,7 +335,7 @@ class LinearAttnRunner:
         else:
             o = out
             op, os = _rows(o, "out", self.rows, wo, self.tdtype, self.device)
-        ssd_linear_attn_step(self.dims, inputs, states, states.shape[0], idx, op, os, _current(self.device, stream))
+        ssd_linear_attn_step(self.dims, inputs, states, states.shape[0], idx, op, os, _current(self))
         return o
 
 
@@ -329,6 +355,7 @@ class GroupNormRunner:
         if size == 0:
             raise ValueError("invalid dims for libssd")
         self.workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+        self._stream = None  # the last one that used the workspace
         self._forward_workspace = None
 
     def _grow(self):
@@ -348,17 +375,23 @@ class GroupNormRunner:
 
     def forward(self, x, weight=None, bias=None, *, z=None, eps: float = 1e-5, out=None, stream=None):
         """(y, mean, rstd): y shaped like x; mean and rstd (nsamples, groups) fp32, for backward."""
+        if stream is not None:
+            with _on(self, stream):
+                return self.forward(x, weight, bias, z=z, eps=eps, out=out)
         inputs = self._inputs(x, weight, bias, z, eps)
         y = torch.empty(x.shape, dtype=self.tdtype, device=self.device) if out is None else out
         yp, ys = self._row(y, "out")
         stats = torch.empty((2,) + self.stat_shape, dtype=torch.float32, device=self.device)
         mean, rstd = stats[0], stats[1]
-        ssd_group_norm_forward(self.dims, inputs, yp, ys, mean, rstd, self.workspace, stream=_current(self.device, stream))
+        ssd_group_norm_forward(self.dims, inputs, yp, ys, mean, rstd, self.workspace, stream=_current(self))
         return y, mean, rstd
 
     def backward(self, dy, x, weight, bias, mean, rstd, *, z=None, stream=None) -> dict:
         """dx, dweight, dbias, and dz with the gate (else None).  dweight and dbias are also given for the constant 1
         and 0 that stand for an absent weight and bias."""
+        if stream is not None:
+            with _on(self, stream):
+                return self.backward(dy, x, weight, bias, mean, rstd, z=z)
         device = self.device
         inputs = self._inputs(x, weight, bias, z, 0.0)
         dyp, dys = self._row(dy, "dy")
@@ -371,5 +404,5 @@ class GroupNormRunner:
              "dbias": torch.empty(self.channels, dtype=torch.float32, device=device)}
         grads = SsdGroupNormGrads(g["dx"].data_ptr(), self.channels, _ptr(g["dz"]), self.channels,
                                   g["dweight"].data_ptr(), g["dbias"].data_ptr())
-        ssd_group_norm_backward(self.dims, inputs, dyp, dys, mp, rp, grads, self.workspace, stream=_current(self.device, stream))
+        ssd_group_norm_backward(self.dims, inputs, dyp, dys, mp, rp, grads, self.workspace, stream=_current(self))
         return g

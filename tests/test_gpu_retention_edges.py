@@ -51,3 +51,65 @@ def test_bounds_in_any_order(T, n, H, dtype):
         lens = (c.cu[1:].clamp(0, T) - c.cu[:-1].clamp(0, T)).clamp(min=0)
         for s in (lens == 0).nonzero()[:, 0].tolist():
             assert torch.equal(fin[s].cpu(), c.init[s]) and torch.equal(g["dinitial_state"][s].cpu(), c.dfin[s])
+
+
+# ------------------------------------------------------------------ streams
+
+def _calls():
+    """(runner, a call of it on a given stream that returns its outputs) for each operator and direction.  (The step's
+    rows have no slot, so that calls leave nothing behind.)"""
+    c = Case([500], 4, 2, 64, 64, packed=False, seed=23)
+    q, k, v = c.parts("cuda")
+    decay, do, x = c.decay.cuda(), c.do.cuda(), torch.randn(500, 256, device="cuda").bfloat16()
+    kw = dict(initial_state=c.init.cuda())
+    r, tok, norm = c.runner(), ssd.LinearAttnRunner(500, 1, 4, 64, 64, nheads_kv=2), ssd.GroupNormRunner(500, 1, 256, 4)
+    cache, slots = torch.zeros(1, 4, 64, 64, device="cuda"), torch.full((500,), -1, dtype=torch.int32, device="cuda")
+    _, mean, rstd = norm.forward(x)
+    torch.cuda.synchronize()
+    return [(r, lambda s: list(r.forward(q, k, v, decay, **kw, stream=s))),
+            (r, lambda s: list(r.backward(q, k, v, decay, do, **kw, stream=s).values())),
+            (tok, lambda s: [tok.step(q, k, v, decay, cache, slot_idx=slots, stream=s)]),
+            (norm, lambda s: list(norm.forward(x, stream=s))),
+            (norm, lambda s: [t for t in norm.backward(x, x, None, None, mean, rstd, stream=s).values() if t is not None])]
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("which", range(5))
+def test_outputs_belong_to_the_given_stream(which, handle):
+    """Outputs that are dropped while their stream has yet to write them are not what other tensors get."""
+    _, call = _calls()[which]
+    want = [x.clone() for x in call(None)]
+    side = torch.cuda.Stream()
+    for keep in range(len(want)):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)  # some 50 ms
+        got = call(side.cuda_stream if handle else side)
+        kept, dropped = got[keep], [(x.data_ptr(), x.shape, x.dtype) for i, x in enumerate(got) if i != keep]
+        del got
+        others = [torch.full(shape, 7.0, dtype=dtype, device="cuda") for _, shape, dtype in dropped for _ in range(2)]
+        assert not {x.data_ptr() for x in others} & {p for p, _, _ in dropped}
+        torch.cuda.synchronize()
+        assert all((x == 7).all() for x in others)
+        assert torch.equal(kept, want[keep])
+
+
+@pytest.mark.parametrize("which", [0, 1, 3, 4])
+def test_workspaces_outlive_their_calls(which):
+    """A runner that is dropped while another stream has yet to work in its workspace."""
+    side = torch.cuda.Stream()
+    for current in (False, True):  # stream= and torch.cuda.stream
+        calls = _calls()
+        r, call = calls[which]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+            if current:
+                call(None)
+        if not current:
+            call(side)
+        used, size = r.workspace.data_ptr(), r.workspace.numel()
+        del calls, r, call
+        others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert used not in {x.data_ptr() for x in others}
+        torch.cuda.synchronize()
