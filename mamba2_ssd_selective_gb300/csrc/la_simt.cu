@@ -336,10 +336,8 @@ constexpr int smem_bytes(int dk, bool summary) {
 
 template <typename T, bool SUMMARY>
 void run_simt(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
-  static bool once = (cudaFuncSetAttribute(la_simt_kernel<T, SUMMARY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           smem_bytes(256, SUMMARY)),
-                      true);
-  (void)once;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(la_simt_kernel<T, SUMMARY>), smem_bytes(256, SUMMARY), allowed);
   int dk = 0, dv = 0;
   for (int i = 0; i < b.n; ++i) {
     dk = b.p[i].dk > dk ? b.p[i].dk : dk;

@@ -908,10 +908,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 template <int KB, int VB, bool SUMMARY, bool F32>
 void run_tc(const LaPlanDev &pl, const LaBatch &b, cudaStream_t s) {
   using L = Layout<KB, VB, SUMMARY, F32>;
-  static bool once = (cudaFuncSetAttribute(la_tc_kernel<KB, VB, SUMMARY, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           L::kBytes),
-                      true);
-  (void)once;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(la_tc_kernel<KB, VB, SUMMARY, F32>), L::kBytes, allowed);
   Args args;
   args.batch = b;
   args.pl = pl;

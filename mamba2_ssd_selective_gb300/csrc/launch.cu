@@ -34,6 +34,15 @@ ssd_status launch_status() {
   return (cudaPeekAtLastError() == cudaSuccess && !host_err) ? SSD_OK : SSD_ERR_CUDA;
 }
 
+void allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  // the attribute belongs to the current device; past the 64th it is set in every call
+  const uint64_t bit = cudaGetDevice(&dev) == cudaSuccess && dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess)
+    done.fetch_or(bit, std::memory_order_relaxed);
+}
+
 }  // namespace ssd
 
 using namespace ssd;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <cstdint>
 
 #include "kernels.h"
 #include "ssd.h"
@@ -29,5 +30,8 @@ struct ProfScope {
   } while (0)
 
 ssd_status launch_status();
+
+// Lets a kernel take that much dynamic shared memory; `done` (the kernel's own) keeps the devices where it may already.
+void allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done);
 
 }  // namespace ssd

@@ -6,8 +6,8 @@ The functions carry the C names and only marshal arguments.  The runners hold
 what a program keeps between calls (the dimensions and the workspace) and check
 the tensors they are given; a runner's workspace belongs to one stream at a time.
 
-A call runs on ``stream`` (a stream, or its handle, which then has to outlive the runner) or, without one, on the
-current stream.  What it allocates, outputs and a larger workspace, belongs to that stream as it would to a current one, and a workspace
+A call runs on the runner's device, on ``stream`` (a stream, or its handle, which then has to outlive the runner)
+or, without one, on the device's current stream.  What it allocates, outputs and a larger workspace, belongs to that stream as it would to a current one, and a workspace
 that another stream used is kept for it.  That inputs are ready on the stream, and that they outlive the call
 there, is the caller's affair, as it is under torch.cuda.stream.
 """
@@ -204,10 +204,16 @@ def _current(runner):
     return handle
 
 
-def _on(runner, stream):
-    """Makes the given stream the current one, so that what a call allocates belongs to the stream it is written on."""
+def _elsewhere(runner, stream):
+    """What makes the runner's device and the given stream the current ones, so that a call is launched there and what it
+    allocates belongs to the stream it is written on; None where they are current already."""
+    index = runner.device.index
+    if stream is None:
+        return None if index is None or index == torch._C._cuda_getDevice() else torch.cuda.device(runner.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=runner.device)
+    if stream.device != runner.device:
+        raise ValueError(f"stream: expected one of {runner.device}, got one of {stream.device}")
     return torch.cuda.stream(stream)
 
 
@@ -278,8 +284,9 @@ class LinearAttnRunner:
                 out=None, stream=None):
         """(o, final_state): o (rows, nheads * headdim_v); final_state (nseq, nheads, headdim_k, headdim_v) fp32, or
         None with final_state=False.  ``out``: a tensor for o."""
-        if stream is not None:
-            with _on(self, stream):
+        there = _elsewhere(self, stream)
+        if there is not None:
+            with there:
                 return self.forward(q, k, v, log_decay, scale=scale, initial_state=initial_state,
                                     cu_seqlens=cu_seqlens, final_state=final_state, out=out)
         wo = self._widths[3]
@@ -298,8 +305,9 @@ class LinearAttnRunner:
                  stream=None) -> dict:
         """Gradients of <do, o> + <dfinal_state, final_state>: dq, dk, dv, and dinitial_state (None without an
         initial state)."""
-        if stream is not None:
-            with _on(self, stream):
+        there = _elsewhere(self, stream)
+        if there is not None:
+            with there:
                 return self.backward(q, k, v, log_decay, do, scale=scale, initial_state=initial_state,
                                      dfinal_state=dfinal_state, cu_seqlens=cu_seqlens)
         wq, wk, wv, wo = self._widths
@@ -322,8 +330,9 @@ class LinearAttnRunner:
         """One token of each of ``nseq`` rows (a runner with tokens=1): updates ``states`` (slots, nheads, headdim_k,
         headdim_v) in place at ``slot_idx`` (int32; None: row r uses slot r; a negative one leaves the cache alone and
         gives zeros) and returns o (rows, nheads * headdim_v)."""
-        if stream is not None:
-            with _on(self, stream):
+        there = _elsewhere(self, stream)
+        if there is not None:
+            with there:
                 return self.step(q, k, v, log_decay, states, slot_idx=slot_idx, scale=scale, out=out)
         wo = self._widths[3]
         inputs = self._inputs(q, k, v, log_decay, scale, None, None)
@@ -375,8 +384,9 @@ class GroupNormRunner:
 
     def forward(self, x, weight=None, bias=None, *, z=None, eps: float = 1e-5, out=None, stream=None):
         """(y, mean, rstd): y shaped like x; mean and rstd (nsamples, groups) fp32, for backward."""
-        if stream is not None:
-            with _on(self, stream):
+        there = _elsewhere(self, stream)
+        if there is not None:
+            with there:
                 return self.forward(x, weight, bias, z=z, eps=eps, out=out)
         inputs = self._inputs(x, weight, bias, z, eps)
         y = torch.empty(x.shape, dtype=self.tdtype, device=self.device) if out is None else out
@@ -389,8 +399,9 @@ class GroupNormRunner:
     def backward(self, dy, x, weight, bias, mean, rstd, *, z=None, stream=None) -> dict:
         """dx, dweight, dbias, and dz with the gate (else None).  dweight and dbias are also given for the constant 1
         and 0 that stand for an absent weight and bias."""
-        if stream is not None:
-            with _on(self, stream):
+        there = _elsewhere(self, stream)
+        if there is not None:
+            with there:
                 return self.backward(dy, x, weight, bias, mean, rstd, z=z)
         device = self.device
         inputs = self._inputs(x, weight, bias, z, 0.0)
