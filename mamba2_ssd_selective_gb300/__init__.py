@@ -221,10 +221,12 @@ class SsdRunner:
 
     ``t`` is a dict of device tensors as produced by ``inputs.make_inputs`` (moved
     to the GPU): xBC (b, L, Cd) with x, B, C as token-strided views, dt_raw,
-    parameters and optional seq_idx, init, z / norm_weight (gated_norm=True)."""
+    parameters and optional seq_idx, init, z / norm_weight (gated_norm=True).
+    Calls run on the runner's device and what they allocate belongs to their
+    stream, as for the runners of retention.py."""
 
     def __init__(self, shape, dtype: str, device="cuda", gated_norm: bool = False):
-        self.shape, self.dtype, self.device = shape, dtype, torch.device(device)
+        self.shape, self.dtype, self.device = shape, dtype, retention._device(device)
         self.gated_norm = gated_norm
         self.dims = make_dims(shape, dtype, gated_norm)
         self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
@@ -233,6 +235,7 @@ class SsdRunner:
         if self.ws_fwd == 0:
             raise ValueError("invalid dims for libssd")
         self.workspace = torch.empty(max(self.ws_fwd, self.ws_bwd), dtype=torch.uint8, device=self.device)
+        self._stream = None  # the last one that used the workspace
 
     def inputs(self, t: dict) -> SsdInputs:
         s = self.shape
@@ -287,20 +290,33 @@ class SsdRunner:
     def forward_varlen(self, t: dict, out=None, stream=None):
         """Forward of a packed row (t["cu_seqlens"], t["seq_idx"]); returns y,
         final_state, seg_init_states and the per-sequence final states."""
+        there = retention._elsewhere(self, stream)
+        if there is not None:
+            with there:
+                return self.forward_varlen(t, out)
         y, fin, seg = out if out is not None else self.alloc_outputs()
         cu = t["cu_seqlens"]
         s = self.shape
         sf = torch.empty(cu.numel() - 1, s.nheads, s.headdim, s.dstate, dtype=torch.float32, device=self.device)
-        ssd_forward_varlen(self.dims, self.inputs(t), y, fin, seg, cu, sf, self.workspace, stream=stream)
+        ssd_forward_varlen(self.dims, self.inputs(t), y, fin, seg, cu, sf, self.workspace,
+                           stream=retention._current(self))
         return y, fin, seg, sf
 
     def forward(self, t: dict, out=None, stream=None):
+        there = retention._elsewhere(self, stream)
+        if there is not None:
+            with there:
+                return self.forward(t, out)
         y, fin, seg = out if out is not None else self.alloc_outputs()
-        ssd_forward(self.dims, self.inputs(t), y, fin, seg, self.workspace, stream=stream)
+        ssd_forward(self.dims, self.inputs(t), y, fin, seg, self.workspace, stream=retention._current(self))
         return y, fin, seg
 
     def backward(self, t: dict, dy, dfinal=None, seg=None, grads=None, stream=None):
+        there = retention._elsewhere(self, stream)
+        if there is not None:
+            with there:
+                return self.backward(t, dy, dfinal, seg, grads)
         g = grads if grads is not None else self.alloc_grads(init=t.get("init") is not None)
         ssd_backward(self.dims, self.inputs(t), dy, dfinal, seg, self.grads_struct(g), self.workspace,
-                     stream=stream)
+                     stream=retention._current(self))
         return g

@@ -9,6 +9,7 @@
 // parallelism in the mixer").  Taps that cross a packed-sequence boundary are
 // zero (seq_idx, NeMo Automodel PR #1441 "feat: context-parallel with nemotron v3").
 #include "kernels.h"
+#include "launch.h"
 
 namespace ssd {
 
@@ -281,8 +282,8 @@ template <typename T> constexpr int conv_fwd_smem() {
 
 template <typename T> void launch_conv_fwd(const Problem &pr, T *u, float *dtv, float *acs, cudaStream_t s) {
   constexpr int smem = conv_fwd_smem<T>();
-  static bool once = (cudaFuncSetAttribute(conv_fwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), true);
-  (void)once;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(conv_fwd_kernel<T>), smem, allowed);
   const int conv_x = chan_tiles(pr, kFwdCh), ny = (pr.L + kFwdTok - 1) / kFwdTok;
   const int dt_hg = (pr.H + kDtHeads - 1) / kDtHeads, dt_x = (pr.nc * dt_hg + ny - 1) / ny;
   conv_fwd_kernel<T><<<dim3(conv_x + dt_x, ny, pr.b), 256, smem, s>>>(pr, u, dtv, acs, conv_x, dt_hg);
@@ -507,15 +508,11 @@ template <typename T>
 void launch_conv_bwd(const Problem &pr, const float *du, const BcParts &bc, const GradOut &go, float *convp, int ntb,
                      cudaStream_t s) {
   constexpr int smem = conv_bwd_smem<T>();
-  static bool once = (cudaFuncSetAttribute(conv_bwd_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                      cudaFuncSetAttribute(conv_bwd_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                      true);
-  (void)once;
+  static std::atomic<uint64_t> allowed[2] = {};
+  auto *kernel = pr.seq_idx ? conv_bwd_kernel<T, true> : conv_bwd_kernel<T, false>;
+  allow_smem(reinterpret_cast<const void *>(kernel), smem, allowed[pr.seq_idx != nullptr]);
   dim3 grid(chan_tiles(pr, kBwdCh), ntb, pr.b);
-  if (pr.seq_idx)
-    conv_bwd_kernel<T, true><<<grid, 256, smem, s>>>(pr, du, bc, go, convp, ntb);
-  else
-    conv_bwd_kernel<T, false><<<grid, 256, smem, s>>>(pr, du, bc, go, convp, ntb);
+  kernel<<<grid, 256, smem, s>>>(pr, du, bc, go, convp, ntb);
 }
 
 // Parameter gradients: fixed-order sums of per-chunk / per-block partials.

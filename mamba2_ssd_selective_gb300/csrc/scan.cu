@@ -12,6 +12,7 @@
 // thread owns a few elements and walks the chunks (or segments) in order: the
 // result is bit-identical from run to run.
 #include "kernels.h"
+#include "launch.h"
 #include "simt_gemm.cuh"
 
 namespace ssd {
@@ -386,10 +387,8 @@ void launch_combine_bwd(const Problem &pr, const float *sc, const float *segin, 
   if (m == 4) {
     combine_bwd_kernel<4><<<grid, 256, smem, s>>>(pr, sc, segin, dsl, gout, sin16, dse16, sdp);
   } else if (m == 8) {
-    static bool once = (cudaFuncSetAttribute(combine_bwd_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             8 * kScanVec4 * 256 * (int)sizeof(float4)),
-                        true);
-    (void)once;
+    static std::atomic<uint64_t> allowed{0};
+    allow_smem(reinterpret_cast<const void *>(combine_bwd_kernel<8>), smem, allowed);
     combine_bwd_kernel<8><<<grid, 256, smem, s>>>(pr, sc, segin, dsl, gout, sin16, dse16, sdp);
   } else {
     combine_bwd_kernel<0><<<grid, 256, 0, s>>>(pr, sc, segin, dsl, gout, sin16, dse16, sdp);

@@ -26,6 +26,7 @@
 // store, so the rows leave as whole lines rather than as one line per thread.
 #include "chunk_common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "tc_util.cuh"
 #include "tc_pipe.cuh"
 
@@ -695,10 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 void launch_tc_bwd_col(const Problem &pr, const bf16 *u, const bf16 *dy, const float *dtv, const float *acs,
                        const bf16 *dse16, float *du, float *dbp, float *tok, int *status, cudaStream_t s) {
-  static bool once = (cudaFuncSetAttribute(tc_bwd_col_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kSmemBytes),
-                      true);
-  (void)once;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(tc_bwd_col_kernel), kSmemBytes, allowed);
   CUtensorMap tm_u, tm_dy, tm_ds, tm_du, tm_db;
   const uint64_t HP = (uint64_t)pr.H * pr.P;
   const int HB = tc_head_subset(pr);

@@ -19,6 +19,7 @@
 //                [320, 384) Y_off = C_I S_in^T | [384, 512) dC.
 #include "chunk_common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "tc_util.cuh"
 #include "tc_pipe.cuh"
 
@@ -565,10 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 void launch_tc_bwd_row(const Problem &pr, const bf16 *u, const bf16 *dy, const float *dtv, const float *acs,
                        const bf16 *sin16, float *dcp, float *tok, int *status, cudaStream_t s) {
-  static bool once = (cudaFuncSetAttribute(tc_bwd_row_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kSmemBytes),
-                      true);
-  (void)once;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(tc_bwd_row_kernel), kSmemBytes, allowed);
   CUtensorMap tm_u, tm_dy, tm_s;
   const uint64_t HP = (uint64_t)pr.H * pr.P;
   if (!encode_tmap_bf16_2d(&tm_u, u, pr.Cd, (uint64_t)pr.b * pr.L, (uint64_t)pr.Cd * 2, 64, 64) ||

@@ -31,6 +31,7 @@
 // Envelope (checked on the host): bf16 activations, headdim 64, dstate 128,
 // chunk 128 or 256, an even number of heads per group.
 #include "kernels.h"
+#include "launch.h"
 #include "tc_util.cuh"
 #include "tc_pipe.cuh"
 
@@ -376,9 +377,8 @@ int sz_head_block(const Problem &pr) {
 template <bool kZ>
 void launch_sz(const Problem &pr, const bf16 *u, const bf16 *xsrc, const float *dtv, const float *acs, float *out,
                DecayTabs tab, int *status, cudaStream_t s) {
-  static bool once = (cudaFuncSetAttribute(tc_sz_kernel<kZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes),
-                      true);
-  (void)once;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(tc_sz_kernel<kZ>), kSmemBytes, allowed);
   CUtensorMap tm_u, tm_x;
   const uint64_t HP = (uint64_t)pr.H * pr.P;
   const uint64_t xcols = kZ ? HP : (uint64_t)pr.Cd;

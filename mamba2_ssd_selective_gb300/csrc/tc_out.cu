@@ -33,6 +33,7 @@
 // slices never leave tensor memory.
 #include "chunk_common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "tc_util.cuh"
 #include "tc_pipe.cuh"
 
@@ -517,9 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 void launch_tc_out(const Problem &pr, const bf16 *u, const float *dtv, const float *acs, const bf16 *sin16, bf16 *y,
                    int *status, cudaStream_t s) {
   int *counter = status + kCounterOut;  // zeroed with the status word
-  static bool once = (cudaFuncSetAttribute(tc_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes),
-                      true);
-  (void)once;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(tc_out_kernel), kSmemBytes, allowed);
   CUtensorMap tm_u, tm_s;
   if (!encode_tmap_bf16_2d(&tm_u, u, pr.Cd, (uint64_t)pr.b * pr.L, (uint64_t)pr.Cd * 2, 64, 64) ||
       !encode_tmap_bf16_2d(&tm_s, sin16, pr.N, (uint64_t)pr.b * pr.nc * pr.H * pr.P, (uint64_t)pr.N * 2, 64, 64)) {

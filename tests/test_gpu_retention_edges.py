@@ -8,6 +8,8 @@ import pytest
 import torch
 
 import mamba2_ssd_selective_gb300 as ssd
+from mamba2_ssd_selective_gb300.inputs import SsdShape, make_inputs
+from tests.gpu_util import to_dev
 from tests.test_gpu_retention import BF16, F32, Case, _built, close  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -92,6 +94,29 @@ def test_outputs_belong_to_the_given_stream(which, handle):
         torch.cuda.synchronize()
         assert all((x == 7).all() for x in others)
         assert torch.equal(kept, want[keep])
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_outputs_of_the_ssd_runner_belong_to_the_given_stream(backward):
+    shape = SsdShape(1, 256, 2, 64, 64, 1, 64, 2)
+    t = to_dev(make_inputs(shape, 5, "bf16"))
+    r = ssd.SsdRunner(shape, "bf16")
+
+    def call(stream):
+        return list(r.backward(t, t["dy"], t["dfinal"], stream=stream).values()) if backward else list(r.forward(t, stream=stream))
+
+    want = [x.clone() for x in call(None)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    got = call(side)
+    kept, dropped = got[0], [(x.data_ptr(), x.shape, x.dtype) for x in got[1:]]
+    del got
+    others = [torch.full(shape, 7.0, dtype=dtype, device="cuda") for _, shape, dtype in dropped for _ in range(2)]
+    assert not {x.data_ptr() for x in others} & {p for p, _, _ in dropped}
+    torch.cuda.synchronize()
+    assert all((x == 7).all() for x in others) and torch.equal(kept, want[0])
 
 
 @pytest.mark.parametrize("which", [0, 1, 3, 4])

@@ -6,6 +6,7 @@ import torch
 
 import mamba2_ssd_selective_gb300 as ssd
 from mamba2_ssd_selective_gb300.build import build
+from mamba2_ssd_selective_gb300.inputs import SsdShape
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -61,3 +62,19 @@ def test_streams_of_another_device_are_refused(which):
     runner.device = torch.device("cuda", 0)
     with pytest.raises(ValueError, match="stream: expected one of cuda:0"):
         call(stream=Stream())
+
+
+@pytest.mark.parametrize("call", [lambda r: r.forward({}), lambda r: r.forward_varlen({}), lambda r: r.backward({}, None)])
+def test_calls_of_the_ssd_runner_enter_its_device(call, monkeypatch):
+    class Entered(Exception):
+        pass
+
+    def guard(device):
+        raise Entered(str(device))
+
+    runner = ssd.SsdRunner(SsdShape(1, 256, 2, 64, 64, 1, 64, 2), "bf16", device="cpu")
+    runner.device = torch.device("cuda", 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", guard)
+    with pytest.raises(Entered, match="cuda:1"):
+        call(runner)
