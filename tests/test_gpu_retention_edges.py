@@ -138,3 +138,27 @@ def test_workspaces_outlive_their_calls(which):
         others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
         assert used not in {x.data_ptr() for x in others}
         torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ single tokens
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_states_of_many_steps(dtype):
+    """6000 steps with decays that live about as long or longer, half a unit in the last place between two fp32 values: an
+    error of lam itself would add up to 6000 * 2^-25 of what the state had at first."""
+    L, H, d, rows = 6000, 3, 16, 2
+    decay = torch.log1p(-torch.tensor([2.**-12 + 2.**-25, 2.**-16 + 2.**-25, 2.**-14 + 2.**-25], dtype=torch.float64)).float()
+    c = Case([L] * rows, H, H, d, d, dtype, packed=False, seed=12, decay=decay)
+    q, k, v = (x.reshape(rows, L, -1) for x in c.parts("cuda"))
+    cache, g = c.init.cuda(), decay.cuda()
+    tok = ssd.LinearAttnRunner(rows, 1, H, d, d, dtype=dtype)
+    outs = [tok.step(q[:, t], k[:, t], v[:, t], g, cache) for t in range(L)]
+    k64, v64 = (x.double().cpu().view(rows, L, H, d) for x in (k, v))
+    left = torch.exp(decay.double() * torch.arange(L - 1, -1, -1, dtype=torch.float64)[:, None])  # (L, H)
+    want = torch.einsum("rlhk,lh,rlhv->rhkv", k64, left, v64) + c.init.double() * torch.exp(decay.double() * L)[:, None, None]
+    close(cache, want, F32, "state")
+    o64 = torch.einsum("rhk,rhkv->rhv", q[:, -1].double().cpu().view(rows, H, d), want) * d ** -0.5
+    close(outs[-1], o64.reshape(rows, -1), BF16 if dtype == "bf16" else F32, "last token")
+    # and what one prompt of all tokens gives
+    _, fin = c.runner().forward(*(x.reshape(rows * L, -1) for x in (q, k, v)), g, initial_state=c.init.cuda())
+    close(cache, fin.cpu(), 2 * F32, "prompt")
