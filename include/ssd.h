@@ -289,7 +289,8 @@ typedef struct {
 /* Bytes of device workspace of ssd_linear_attn_forward (backward = 0) or _backward (1); 0 if dims are invalid. */
 size_t ssd_linear_attn_workspace_size(const ssd_linear_attn_dims *dims, int backward);
 
-/* Forward.  final_states: the state after each sequence's last token, or NULL. */
+/* Forward.  final_states: the state after each sequence's last token, or NULL; it may be initial_states itself, which
+ * are then updated in place. */
 ssd_status ssd_linear_attn_forward(const ssd_linear_attn_dims *dims, const ssd_linear_attn_inputs *in, void *o,
                                    int64_t o_tok_stride, float *final_states, void *workspace, size_t ws_bytes,
                                    ssd_stream_t stream);

@@ -412,6 +412,7 @@ ssd_status ssd_linear_attn_forward(const ssd_linear_attn_dims *dims, const ssd_l
   la_states(p, in->initial_states, final_states, false);
   p.o_scale = in->scale;
   p.p_scale = p.st_scale = 1.f;
+  p.init_kept = pl.cut == LaPlan::kSideBySide && final_states && final_states == in->initial_states;
   p.o = o;
   p.os = o_tok_stride;
   const LaPlanDev dev = la_plan_dev(dims, in, pl, ws);

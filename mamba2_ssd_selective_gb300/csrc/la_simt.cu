@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, SUMMARY ? 5 : 4) la_simt_kernel(LaPl
   }
   {
     int sa, sb;
-    const float *in = SUMMARY ? nullptr : la_state_in(p, u.level, u.seq, unit, h, sa, sb);
+    const float *in = SUMMARY ? nullptr : la_state_in(p, u.level, u.next, u.seq, unit, h, sa, sb);
     for (int e = tid; e < dkp * kTV; e += kThreads) {
       const int a = e / kTV, b = e % kTV;
       S[a * kLdV + b] = in && a < p.dk && b < ncol ? in[(size_t)a * sa + (size_t)(c0 + b) * sb] : 0.f;
@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(kScanThreads) la_scan_kernel(LaPlanDev pl, con
   float st = live && p.init ? p.init[user] : 0.f;
   float *base = p.seg_state + (size_t)h * dd + e;
   const size_t step = (size_t)p.H * dd;
+  if (live && p.init_kept) base[s * step] = st;  // (unit s is the first of sequence s)
   constexpr int kAhead = 8;
   // level i + 1 holds what level i's segment gives, then the state after it
   for (int l0 = 1; l0 < n; l0 += kScanMax) {

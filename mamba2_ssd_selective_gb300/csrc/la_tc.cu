@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         auto flag = [&](int unit) { return pl.flags + ((size_t)it.pass * pl.units + unit) * pl.H + it.h; };
         {
           int sa, sb;
-          const float *in = SUMMARY ? nullptr : la_state_in(p, it.level, it.seq, it.unit, it.h, sa, sb);
+          const float *in = SUMMARY ? nullptr : la_state_in(p, it.level, it.next, it.seq, it.unit, it.h, sa, sb);
           if (!SUMMARY && pl.flags && it.level > 0) wait_flag(flag(it.unit), wait);
           const bool live = in && c < p.dv;
 #pragma unroll

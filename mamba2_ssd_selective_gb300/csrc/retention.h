@@ -42,6 +42,7 @@ struct LaPass {
   int sa, sb;
   float *seg_state;  // (units, H, dk, dv): a cut sequence's segment states
   bool seg_shared;   // they are another pass's, transposed: (units, H, dv, dk), read only
+  bool init_kept;    // fin is init, and the scan keeps what cut sequences start from in their first units' places
   bool o_f32;        // o is fp32 whatever the inputs' type
 };
 
@@ -113,13 +114,13 @@ __device__ __forceinline__ LaUnit la_unit(const LaPlanDev &pl, int unit, bool re
 }
 
 // The state before the unit's first token in processing order, or null (zero), and its strides: the segment's, or
-// the user's for a sequence's first segment.
-__device__ __forceinline__ const float *la_state_in(const LaPass &p, int level, int seq, int unit, int h, int &sa,
-                                                       int &sb) {
+// the user's for a sequence's first segment (unless that is where its last segment's state goes).
+__device__ __forceinline__ const float *la_state_in(const LaPass &p, int level, int next, int seq, int unit, int h,
+                                                    int &sa, int &sb) {
   const size_t dd = (size_t)p.dk * p.dv;
   sa = p.sa;
   sb = p.sb;
-  if (level == 0) return p.init ? p.init + ((size_t)seq * p.H + h) * dd : nullptr;
+  if (level == 0 && !(p.init_kept && next >= 0)) return p.init ? p.init + ((size_t)seq * p.H + h) * dd : nullptr;
   sa = p.seg_shared ? 1 : p.dv;
   sb = p.seg_shared ? p.dk : 1;
   return p.seg_state + ((size_t)unit * p.H + h) * dd;

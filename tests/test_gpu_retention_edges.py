@@ -55,6 +55,26 @@ def test_bounds_in_any_order(T, n, H, dtype):
             assert torch.equal(fin[s].cpu(), c.init[s]) and torch.equal(g["dinitial_state"][s].cpu(), c.dfin[s])
 
 
+# whole, chained, side by side
+@pytest.mark.parametrize("lens,H,packed,dtype", [([200, 70, 0], 2, True, "bf16"), ([650] * 10, 16, False, "bf16"), ([8000], 2, False, "bf16"),
+                                                 ([3, 8000, 0, 257], 2, True, "bf16"), ([1500, 1500], 2, False, "f32"),
+                                                 ([3, 1400, 0, 257], 2, True, "f32")])
+def test_states_in_place(lens, H, packed, dtype):
+    """final_states may be initial_states: the same bits, wherever sequences are cut."""
+    c = Case(lens, H, H, 64, 64, dtype, packed=packed, seed=len(lens))
+    r = c.runner()
+    want_o, want, _ = c.gpu(backward=False, runner=r)
+    q, k, v = c.parts("cuda")
+    decay, cu = c.decay.cuda(), c.cu.cuda()
+    for _ in range(10):
+        states, o = c.init.cuda(), torch.empty_like(want_o)
+        inputs = ssd.SsdLinearAttnInputs(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+                                         decay.data_ptr(), states.data_ptr(), cu.data_ptr() if packed else None, c.scale)
+        ssd.ssd_linear_attn_forward(r.dims, inputs, o, o.stride(0), states, r.workspace)
+        assert ssd.ssd_device_status(r.workspace) == 0
+        assert torch.equal(o, want_o) and torch.equal(states, want)
+
+
 # ------------------------------------------------------------------ streams
 
 def _calls():
