@@ -290,13 +290,15 @@ typedef struct {
 size_t ssd_linear_attn_workspace_size(const ssd_linear_attn_dims *dims, int backward);
 
 /* Forward.  final_states: the state after each sequence's last token, or NULL; it may be initial_states itself, which
- * are then updated in place. */
+ * are then updated in place.  o must not overlap an input: one that starts where an input does is refused
+ * (SSD_ERR_INVALID_DIMS). */
 ssd_status ssd_linear_attn_forward(const ssd_linear_attn_dims *dims, const ssd_linear_attn_inputs *in, void *o,
                                    int64_t o_tok_stride, float *final_states, void *workspace, size_t ws_bytes,
                                    ssd_stream_t stream);
 
 /* Backward of <do, o> + <dfinal_states, final_states> (dfinal_states NULL: zero).  do is named dout here: layout
- * rules of o.  Nothing but the inputs is needed from the forward pass. */
+ * rules of o.  Nothing but the inputs is needed from the forward pass.  Gradients must not overlap what is read:
+ * dinitial_states = dfinal_states is refused (SSD_ERR_INVALID_DIMS), as is any output that starts where an input does. */
 ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims *dims, const ssd_linear_attn_inputs *in,
                                     const void *dout, int64_t dout_tok_stride, const float *dfinal_states,
                                     const ssd_linear_attn_grads *grads, void *workspace, size_t ws_bytes,
@@ -305,8 +307,8 @@ ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims *dims, const ssd_
 /* One token of each of dims.nseq rows (dims.seqlen must be 1, dims.packed 0), against a cache of states
  * (nslots, nheads, headdim_k, headdim_v) fp32, updated in place: row r uses slot slot_idx[r] (slot_idx NULL: slot
  * r).  A row whose slot is outside [0, nslots) leaves the cache alone and writes zeros to its o; no two rows may
- * share a slot (which of them would win is undefined).  in->initial_states and in->cu_seqlens must be NULL.  No
- * workspace. */
+ * share a slot (which of them would win is undefined).  in->initial_states and in->cu_seqlens must be NULL.  o must
+ * not overlap an input, as in the forward pass.  No workspace. */
 ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_linear_attn_inputs *in, float *states,
                                 int32_t nslots, const int32_t *slot_idx, void *o, int64_t o_tok_stride,
                                 ssd_stream_t stream);
@@ -320,7 +322,9 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_line
  * (1 and 0).  Row strides below 2^31 elements.  mean and rstd (nsamples, groups) fp32 are written by the forward pass (each may be NULL) and read by
  * the backward pass.  Any number of channels per group; rows of 16-byte aligned tensors whose strides and group
  * widths are multiples of 8 elements move as 16-byte vectors, others element by element. Statistics are summed
- * in fp32 as deviations (no difference of large sums). */
+ * in fp32 as deviations (no difference of large sums).  y may be x or z itself, with its row stride; gradients must not
+ * overlap what the backward pass reads (tiles are read twice): what starts where an input does is refused otherwise
+ * (SSD_ERR_INVALID_DIMS). */
 typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GATE = 2 } ssd_activation;
 
 typedef struct {

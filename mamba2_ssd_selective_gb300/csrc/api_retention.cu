@@ -2,6 +2,7 @@
 // an activation: argument checks, workspace carving and launch sequences.
 // Nothing here allocates or synchronises.
 #include <cmath>
+#include <initializer_list>
 
 #include "group_norm.h"
 #include "retention.h"
@@ -12,6 +13,13 @@ namespace {
 
 constexpr long long kMaxRows = 1LL << 30, kMaxChannels = 1 << 16;
 constexpr int kMaxSeqs = 1 << 20;
+
+// an output that starts where one of these inputs does
+bool on_input(const void *out, std::initializer_list<const void *> inputs) {
+  for (const void *p : inputs)
+    if (out && out == p) return true;
+  return false;
+}
 
 // ---------------------------------------------------------------- linear attention
 
@@ -403,6 +411,7 @@ ssd_status ssd_linear_attn_forward(const ssd_linear_attn_dims *dims, const ssd_l
   const LaPlan pl = la_plan(dims, false);
   st = la_check_workspace(pl, workspace, ws_bytes);
   if (st != SSD_OK) return st;
+  if (on_input(o, {in->q, in->k, in->v})) return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int group = dims->nheads / dims->nheads_kv;
   char *ws = static_cast<char *>(workspace);
@@ -442,6 +451,9 @@ ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims *dims, const ssd_
   const LaPlan pl = la_plan(dims, true);
   st = la_check_workspace(pl, workspace, ws_bytes);
   if (st != SSD_OK) return st;
+  for (const void *out : {grads->dq, grads->dk, grads->dv})
+    if (on_input(out, {in->q, in->k, in->v, dout})) return SSD_ERR_INVALID_DIMS;
+  if (on_input(grads->dinitial_states, {in->initial_states, dfinal_states})) return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   if (dims->dtype == SSD_BF16)
@@ -462,6 +474,7 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_line
   if (!states) return SSD_ERR_NULL_PTR;
   if (nslots <= 0) return SSD_ERR_INVALID_DIMS;
   if (!aligned(states, 16) || !aligned(slot_idx, 4)) return SSD_ERR_ALIGNMENT;
+  if (on_input(o, {in->q, in->k, in->v})) return SSD_ERR_INVALID_DIMS;
   const int group = dims->nheads / dims->nheads_kv;
   LaPass p{};
   p.H = dims->nheads;
@@ -495,6 +508,8 @@ ssd_status ssd_group_norm_forward(const ssd_group_norm_dims *dims, const ssd_gro
   GnProblem p = gn_problem(dims, in);
   if (!workspace || ws_bytes < gn_workspace(p, false)) return SSD_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SSD_ERR_ALIGNMENT;
+  if ((y == in->x && y_row_stride != in->x_row_stride) || (y == in->z && y_row_stride != in->z_row_stride))
+    return SSD_ERR_INVALID_DIMS;  // in place, but at other places
   const int eb = elem_bytes(dims->dtype);
   int widest = gn_width(y, y_row_stride, eb, gn_width(in->x, in->x_row_stride, eb, 8));
   if (dims->activation == SSD_ACT_GATE) widest = gn_width(in->z, in->z_row_stride, eb, widest);
@@ -529,6 +544,8 @@ ssd_status ssd_group_norm_backward(const ssd_group_norm_dims *dims, const ssd_gr
   GnProblem p = gn_problem(dims, in);
   if (!workspace || ws_bytes < gn_workspace(p, true)) return SSD_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SSD_ERR_ALIGNMENT;
+  if (on_input(grads->dx, {in->x, in->z, dy, grads->dz}) || on_input(grads->dz, {in->x, in->z, dy}))
+    return SSD_ERR_INVALID_DIMS;
   const int eb = elem_bytes(dims->dtype);
   int widest = gn_width(in->x, in->x_row_stride, eb, gn_width(dy, dy_row_stride, eb, 8));
   widest = gn_width(grads->dx, grads->dx_row_stride, eb, widest);

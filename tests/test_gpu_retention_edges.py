@@ -10,7 +10,7 @@ import torch
 import mamba2_ssd_selective_gb300 as ssd
 from mamba2_ssd_selective_gb300.inputs import SsdShape, make_inputs
 from tests.gpu_util import to_dev
-from tests.test_gpu_retention import BF16, F32, Case, _built, close  # noqa: F401
+from tests.test_gpu_retention import BF16, F32, Case, _built, close, gn_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -182,3 +182,18 @@ def test_states_of_many_steps(dtype):
     # and what one prompt of all tokens gives
     _, fin = c.runner().forward(*(x.reshape(rows * L, -1) for x in (q, k, v)), g, initial_state=c.init.cuda())
     close(cache, fin.cpu(), 2 * F32, "prompt")
+
+
+# ------------------------------------------------------------------ group norm
+
+@pytest.mark.parametrize("act", ["silu", "gate"])
+@pytest.mark.parametrize("n,m,C,G", [(700, 1, 512, 8), (5, 60, 96, 2), (3, 4000, 96, 4), (2, 20000, 16, 2), (3, 1, 8192, 1)])
+def test_group_norm_in_place(n, m, C, G, act):
+    """y may be x or z: a team's groups, a cluster's, tiles, rows wider than a block."""
+    x, _, w, b, z = (None if t is None else t.cuda() for t in gn_case(n, m, C, G, act, "bf16", 3))
+    r = ssd.GroupNormRunner(n, m, C, G, act)
+    want = r.forward(x, w, b, z=z)
+    for over in ("x", "z") if act == "gate" else ("x",):
+        t = {"x": x.clone(), "z": None if z is None else z.clone()}
+        got = r.forward(t["x"], w, b, z=t["z"], out=t[over])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[0] is t[over]

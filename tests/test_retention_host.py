@@ -78,3 +78,47 @@ def test_calls_of_the_ssd_runner_enter_its_device(call, monkeypatch):
     monkeypatch.setattr(torch.cuda, "device", guard)
     with pytest.raises(Entered, match="cuda:1"):
         call(runner)
+
+
+# ------------------------------------------------------------------ outputs on inputs (addresses are never read)
+
+def _refused(call, *args):
+    """Status of a call that has all that it needs but for the place of an output."""
+    with pytest.raises(ssd.SsdError) as e:
+        call(*args, stream=0)
+    return e.value.status
+
+
+INVALID, WS = -1, (4096 * 100, 1 << 40)
+
+
+def test_linear_attn_outputs_on_inputs_are_refused():
+    dims = ssd.SsdLinearAttnDims(2, 100, 0, 0, 4, 4, 64, 64, 0)
+    q, k, v, do, s0, s1 = (4096 * i for i in range(1, 7))
+    inputs = ssd.SsdLinearAttnInputs(q, 256, k, 256, v, 256, 4096 * 9, s0, None, 0.1)
+    for out in (q, k, v):
+        assert _refused(ssd.ssd_linear_attn_forward, dims, inputs, out, 256, None, *WS) == INVALID
+
+    def backward(dq=4096 * 10, dk=4096 * 11, dv=4096 * 12, dinit=4096 * 13):
+        return _refused(ssd.ssd_linear_attn_backward, dims, inputs, do, 256, s1,
+                        ssd.SsdLinearAttnGrads(dq, 256, dk, 256, dv, 256, dinit), *WS)
+
+    for x in (q, k, v, do):
+        assert backward(dq=x) == backward(dk=x) == backward(dv=x) == INVALID
+    assert backward(dinit=s0) == backward(dinit=s1) == INVALID
+    one = ssd.SsdLinearAttnDims(2, 1, 0, 0, 4, 4, 64, 64, 0)
+    inputs.initial_states = None
+    for out in (q, k, v):
+        assert _refused(ssd.ssd_linear_attn_step, one, inputs, s0, 2, None, out, 256) == INVALID
+
+
+def test_group_norm_outputs_on_inputs_are_refused():
+    dims = ssd.SsdGroupNormDims(2, 5, 48, 3, 0, ssd.SSD_ACT_GATE)
+    x, z, dy, m, r, dx, dz = (4096 * i for i in range(1, 8))
+    inputs = ssd.SsdGroupNormInputs(x, 48, z, 64, None, None, 1e-5)
+    for y, stride in ((x, 48), (z, 64)):  # in place only at the same places
+        assert _refused(ssd.ssd_group_norm_forward, dims, inputs, y, stride + 8, m, r, *WS) == INVALID
+    for bad in [dict(dx=t) for t in (x, z, dy, dz)] + [dict(dz=t) for t in (x, z, dy)]:
+        p = {"dx": dx, "dz": dz, **bad}
+        grads = ssd.SsdGroupNormGrads(p["dx"], 48, p["dz"], 48, None, None)
+        assert _refused(ssd.ssd_group_norm_backward, dims, inputs, dy, 48, m, r, grads, *WS) == INVALID
