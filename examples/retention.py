@@ -13,13 +13,14 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import mamba2_ssd_selective_gb300 as ssd  # noqa: E402
 
 
 class _Mix(torch.autograd.Function):
-    """Linear attention, then the norm of each head times silu of a gate."""
+    """Linear attention, then the norm of each head times silu of a gate.  Its gradients have no derivatives of their own."""
 
     @staticmethod
     def forward(ctx, q, k, v, z, weight, log_decay, attn, norm):
@@ -30,6 +31,7 @@ class _Mix(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         q, k, v, z, weight, log_decay, o, mean, rstd = ctx.saved_tensors
         attn, norm = ctx.runners
