@@ -19,7 +19,6 @@ __global__ void __launch_bounds__(kThreads) la_table_kernel(LaPlanDev pl, LaEntr
   if (y == 0) *pl.status = 0;
   if (y < kLaCounterWords) pl.counters[y] = 0;
   for (int i = y; i < nflags; i += stride) pl.flags[i] = 0;
-  if (!table) return;
   for (int s = threadIdx.x; s < pl.nseq; s += kThreads) {
     int a, len;
     la_seq_bounds(pl, s, a, len);
@@ -58,8 +57,7 @@ __global__ void __launch_bounds__(kThreads) la_table_kernel(LaPlanDev pl, LaEntr
 }  // namespace
 
 void launch_la_table(const LaPlanDev &pl, LaEntry *table, int *table_units, int nflags, cudaStream_t s) {
-  const long long work = table ? pl.units : 1;
-  long long blocks = (work + kThreads - 1) / kThreads;
+  long long blocks = ((long long)pl.units + kThreads - 1) / kThreads;
   if (blocks < (nflags + 4095) / 4096) blocks = (nflags + 4095) / 4096;
   la_table_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(pl, table, table_units, nflags);
 }
