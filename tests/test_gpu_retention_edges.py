@@ -10,7 +10,7 @@ import torch
 import mamba2_ssd_selective_gb300 as ssd
 from mamba2_ssd_selective_gb300.inputs import SsdShape, make_inputs
 from tests.gpu_util import to_dev
-from tests.test_gpu_retention import BF16, F32, Case, _built, close, gn_case  # noqa: F401
+from tests.test_gpu_retention import BF16, F32, Case, _built, close, gn_case, gn_check  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +197,64 @@ def test_group_norm_in_place(n, m, C, G, act):
         t = {"x": x.clone(), "z": None if z is None else z.clone()}
         got = r.forward(t["x"], w, b, z=t["z"], out=t[over])
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[0] is t[over]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,m,C,G", [(2, 5000, 512, 2), (3, 20000, 16, 2),  # tiles: more than 32 of a group, and fewer
+                                     (50, 1, 48, 8), (37, 1, 320, 32), (41, 1, 104, 4), (33, 1, 200, 4),  # pairs: teams of 4 to 32
+                                     (9, 5, 60, 6), (3, 90, 60, 6), (2, 4099, 20, 2),  # pairs: a warp, a block, a cluster
+                                     (41, 1, 15, 5), (41, 1, 63, 3), (2, 3000, 9, 3)])  # single channels: teams, a cluster
+def test_group_norm_kernels(n, m, C, G, dtype):
+    gn_check(n, m, C, G, "gate", dtype, seed=n + C)
+
+
+# ------------------------------------------------------------------ linear attention: batches of tokens, many sequences, scales
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv,H,K", [(64, 64, 4, 4), (128, 128, 4, 2), (40, 72, 6, 2), (128, 40, 8, 8), (256, 64, 4, 1)])
+def test_steps_of_a_batch(dk, dv, H, K, dtype):
+    """Rows enough for the kernels that take 64 columns of a state, in slots in no order, with a scale, into a view."""
+    rows, L, scale = 40, 3, 0.3
+    decay = torch.log1p(-torch.exp2(torch.linspace(-1, -12, H)))
+    decay[0] = -float("inf")
+    c = Case([L] * rows, H, K, dk, dv, dtype, packed=False, seed=dk + dv, decay=decay)
+    c.scale = scale
+    ro, rfin = c.ref()[:2]
+    q, k, v = (x.reshape(rows, L, -1) for x in c.parts("cuda"))
+    slots = torch.randperm(rows + 3, generator=torch.Generator().manual_seed(1))[:rows].to(torch.int32)
+    cache = torch.full((rows + 3, H, dk, dv), 3.0, device="cuda")
+    cache[slots.long().cuda()] = c.init.cuda()
+    tok = ssd.LinearAttnRunner(rows, 1, H, dk, dv, nheads_kv=K, dtype=dtype)
+    for t in range(L):
+        buf = torch.full((rows, H * dv + 16), 7.0, dtype=c.qkv.dtype, device="cuda")
+        o = tok.step(q[:, t], k[:, t], v[:, t], decay.cuda(), cache, slot_idx=slots.cuda(), scale=scale, out=buf[:, 8:-8])
+        close(o, ro.view(rows, L, -1)[:, t], BF16 if dtype == "bf16" else F32, f"token {t}")
+        assert (buf[:, :8] == 7).all() and (buf[:, -8:] == 7).all()
+    close(cache[slots.long().cuda()], rfin, F32, "state")
+    rest = sorted(set(range(rows + 3)) - set(slots.tolist()))
+    assert (cache[rest] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_sequences_than_are_cut(dtype):
+    lens = torch.randint(0, 4, (1100,), generator=torch.Generator().manual_seed(2)).tolist()
+    Case(lens, 2, 1, 32, 40, dtype, seed=2).check()
+
+
+@pytest.mark.parametrize("scale", [0.3, -2.0, 0.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scales(scale, dtype):
+    c = Case([130, 0, 70], 4, 2, 64, 64, dtype, seed=6)
+    c.scale = scale
+    r = c.runner()
+    x = [*c.parts("cuda"), c.decay.cuda()]
+    kw = dict(scale=scale, initial_state=c.init.cuda(), cu_seqlens=c.cu.cuda())
+    o, fin = r.forward(*x, **kw)
+    g = r.backward(*x, c.do.cuda(), dfinal_state=c.dfin.cuda(), **kw)
+    ro, rfin, rdq, rdk, rdv, rdinit = c.ref()
+    tol = BF16 if dtype == "bf16" else F32
+    flat = lambda t: t.reshape(c.T, -1)  # noqa: E731
+    for got, want, t, name in ((o, flat(ro), tol, "o"), (fin, rfin, F32, "final state"), (g["dq"], flat(rdq), tol, "dq"),
+                               (g["dk"], flat(rdk), tol, "dk"), (g["dv"], flat(rdv), tol, "dv"),
+                               (g["dinitial_state"], rdinit, F32, "dinitial_state")):
+        close(got, want, t, name)
