@@ -253,7 +253,8 @@ int32_t ssd_profile_end(ssd_kernel_time *out, int32_t max_entries);
  * each token).  States (nseq, nheads, headdim_k, headdim_v) fp32, contiguous, 16-byte aligned.
  * Arithmetic: fp32; on the bf16 tensor-core path (headdim_k and headdim_v at most 128) the products take bf16
  * operands with fp32 accumulation, and what reaches the state is split into three bf16 terms, so that states keep
- * fp32 precision.  A NaN or infinity in a token can reach every output of the same 64-token block of its own
+ * fp32 precision.  There a head's scores q.k (backward: do.v, and with the scale) are weighed by up to 2^40 before they
+ * are rounded, so scores beyond 2^87 overflow; elsewhere the limit is that of fp32.  A NaN or infinity in a token can reach every output of the same 64-token block of its own
  * sequence and head, and those of later tokens; other sequences are not affected.
  * Envelope: headdim_k and headdim_v multiples of 8, at most 256; nheads * headdim and total rows as in ssd_dims; at
  * most 2^20 sequences and 2^28 sequences x heads; else SSD_ERR_UNSUPPORTED.  All sums have a fixed order: equal inputs give equal bits. */
@@ -321,8 +322,8 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_dims *dims, const ssd_line
  * nrows = 1 is the norm of each head of each token that retention uses.  weight and bias (channels) fp32, or NULL
  * (1 and 0).  Row strides below 2^31 elements.  mean and rstd (nsamples, groups) fp32 are written by the forward pass (each may be NULL) and read by
  * the backward pass.  Any number of channels per group; rows of 16-byte aligned tensors whose strides and group
- * widths are multiples of 8 elements move as 16-byte vectors, others element by element. Statistics are summed
- * in fp32 as deviations (no difference of large sums).  y may be x or z itself, with its row stride; gradients must not
+ * widths are multiples of 8 elements move as 16-byte vectors, even ones two elements at a time, others one by one.
+ * Statistics are summed in fp32 as deviations (no difference of large sums).  y may be x or z itself, with its row stride; gradients must not
  * overlap what the backward pass reads (tiles are read twice): what starts where an input does is refused otherwise
  * (SSD_ERR_INVALID_DIMS). */
 typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GATE = 2 } ssd_activation;

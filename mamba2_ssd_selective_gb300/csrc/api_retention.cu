@@ -81,6 +81,7 @@ LaPlan la_plan(const ssd_linear_attn_dims *d, bool backward) {
   const bool tc = la_use_tc(d);
   pl.passes = backward ? 3 : 1;
   const int wide = d->headdim_k > d->headdim_v ? d->headdim_k : d->headdim_v, wide64 = (wide + 63) / 64;
+  // (the SMs are not asked for: a workspace's size may be, where there is no GPU, and is that of the same plan)
   const long long rows = la_rows(d), H = d->nheads, n = d->nseq, sms = 152;
   const long long longest = d->packed ? rows : d->seqlen;
   // blocks (CTAs or items) of a whole sequence of every head and pass, all of them, and those with states to sum

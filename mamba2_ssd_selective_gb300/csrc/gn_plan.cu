@@ -6,7 +6,7 @@ namespace ssd {
 
 namespace {
 
-constexpr int kSms = 152;
+constexpr int kSms = 152;  // not asked for: a workspace's size may be, where there is no GPU
 
 // Partials of one channel, 16 threads a channel: thread q adds partials q, q + 16, ... in order, then
 // the 16 sums are added in order.
