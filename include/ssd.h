@@ -254,8 +254,9 @@ int32_t ssd_profile_end(ssd_kernel_time *out, int32_t max_entries);
  * Arithmetic: fp32; on the bf16 tensor-core path (headdim_k and headdim_v at most 128) the products take bf16
  * operands with fp32 accumulation, and what reaches the state is split into three bf16 terms, so that states keep
  * fp32 precision.  There a head's scores q.k (backward: do.v, and with the scale) are weighed by up to 2^40 before they
- * are rounded, so scores beyond 2^87 overflow; elsewhere the limit is that of fp32.  A NaN or infinity in a token can reach every output of the same 64-token block of its own
- * sequence and head, and those of later tokens; other sequences are not affected.
+ * are rounded, so scores beyond 2^87 overflow; elsewhere the limit is that of fp32.  A NaN or infinity in a token can
+ * reach every output of the same 64-token block of its own sequence and head, and those of later tokens (dk and dv:
+ * of earlier ones); other sequences are not affected.
  * Envelope: headdim_k and headdim_v multiples of 8, at most 256; nheads * headdim and total rows as in ssd_dims; at
  * most 2^20 sequences and 2^28 sequences x heads; else SSD_ERR_UNSUPPORTED.  All sums have a fixed order: equal inputs give equal bits. */
 typedef struct {
