@@ -360,6 +360,146 @@ ssd_status ssd_group_norm_backward(const ssd_group_norm_dims *dims, const ssd_gr
                                    const ssd_group_norm_grads *grads, void *workspace, size_t ws_bytes,
                                    ssd_stream_t stream);
 
+/* ======================= the gated delta rule, and the norms around a block
+ *
+ * Gated delta rule.  Per state head h, with a_t = exp(log_decay_t), b_t = beta_t and the rows k and q of head
+ * h / (nheads / nheads_qk), for the tokens t of one sequence in order:
+ *     S' = a_t S_{t-1},   S_t = S' + b_t k_t^T (v_t - k_t S')     (headdim_k x headdim_v; S_{-1}: the initial state, or zero)
+ *     o_t = scale q_t S_t
+ * With dims.qk_norm, q and k are divided by sqrt(|.|^2 + norm_eps) first (gradients go through the division); without
+ * it the keys should be short (b |k|^2 at most 2), or states grow from token to token.
+ * Sequences, cu_seqlens, empty sequences and rows outside every sequence are as in ssd_linear_attn_dims, and so are the
+ * layouts: token-major tensors with their own token strides, heads and channels contiguous within a token,
+ *   q, k (T, nheads_qk * headdim_k), v, o (T, nheads * headdim_v), log_decay, beta (T, nheads)
+ * all in dims.dtype; q, k, v, o 16-byte aligned with strides a multiple of 8 (bf16) or 4 (fp32) elements, log_decay and
+ * beta element aligned with any stride of at least nheads.  log_decay is at most 0 (below -256 it counts as -256, which
+ * forgets everything; -inf is allowed).  States (nseq, nheads, headdim_k, headdim_v) fp32, contiguous, 16-byte aligned.
+ * A NaN or infinity in a token can reach every output of the same 64-token chunk of its own sequence and head, and those
+ * of later tokens (gradients: of all tokens); other sequences are not affected.
+ * Envelope: headdim_k and headdim_v multiples of 8, at most 256; otherwise as linear attention, else
+ * SSD_ERR_UNSUPPORTED.  All sums have a fixed order: equal inputs give equal bits. */
+typedef struct {
+  int32_t nseq;
+  int32_t seqlen;       /* tokens of every sequence; ignored when packed */
+  int32_t total_tokens; /* packed: rows of the token-major tensors; else 0 or nseq * seqlen */
+  int32_t packed;       /* 1: cu_seqlens gives the sequences */
+  int32_t nheads, nheads_qk, headdim_k, headdim_v;
+  int32_t dtype;   /* ssd_dtype of q, k, v, log_decay, beta, o and their gradients */
+  int32_t qk_norm; /* 1: q and k of each head are divided by their length */
+} ssd_delta_rule_dims;
+
+typedef struct {
+  const void *q; int64_t q_tok_stride;
+  const void *k; int64_t k_tok_stride;
+  const void *v; int64_t v_tok_stride;
+  const void *log_decay; int64_t log_decay_tok_stride;
+  const void *beta; int64_t beta_tok_stride;
+  const float *initial_states; /* or NULL: zero */
+  const int32_t *cu_seqlens;   /* exactly when dims.packed */
+  float scale;
+  float norm_eps; /* with qk_norm: at least 0 */
+} ssd_delta_rule_inputs;
+
+/* Gradients, written (not accumulated), layout rules of the tensors they belong to, own token strides; dq and dk are
+ * summed over the states that share a head.  dinitial_states fp32: written when not NULL (it does not need
+ * initial_states to be given). */
+typedef struct {
+  void *dq; int64_t dq_tok_stride;
+  void *dk; int64_t dk_tok_stride;
+  void *dv; int64_t dv_tok_stride;
+  void *dlog_decay; int64_t dlog_decay_tok_stride;
+  void *dbeta; int64_t dbeta_tok_stride;
+  float *dinitial_states;
+} ssd_delta_rule_grads;
+
+/* Bytes of device workspace of ssd_delta_rule_forward (backward = 0) or _backward (1); 0 if dims are invalid. */
+size_t ssd_delta_rule_workspace_size(const ssd_delta_rule_dims *dims, int backward);
+
+/* Forward.  final_states: the state after each sequence's last token, or NULL; it may be initial_states itself, which
+ * are then updated in place.  o must not overlap an input: one that starts where an input does is refused
+ * (SSD_ERR_INVALID_DIMS). */
+ssd_status ssd_delta_rule_forward(const ssd_delta_rule_dims *dims, const ssd_delta_rule_inputs *in, void *o,
+                                  int64_t o_tok_stride, float *final_states, void *workspace, size_t ws_bytes,
+                                  ssd_stream_t stream);
+
+/* Backward of <do, o> + <dfinal_states, final_states> (dfinal_states NULL: zero).  do is named dout here: layout rules
+ * of o.  Nothing but the inputs is needed from the forward pass.  Gradients must not overlap what is read: an output
+ * that starts where an input does is refused (SSD_ERR_INVALID_DIMS). */
+ssd_status ssd_delta_rule_backward(const ssd_delta_rule_dims *dims, const ssd_delta_rule_inputs *in, const void *dout,
+                                   int64_t dout_tok_stride, const float *dfinal_states,
+                                   const ssd_delta_rule_grads *grads, void *workspace, size_t ws_bytes,
+                                   ssd_stream_t stream);
+
+/* One token of each of dims.nseq rows (dims.seqlen must be 1, dims.packed 0), against a cache of states (nslots, nheads,
+ * headdim_k, headdim_v) fp32, updated in place: slots, rows without one, and refusals are those of
+ * ssd_linear_attn_step.  No workspace. */
+ssd_status ssd_delta_rule_step(const ssd_delta_rule_dims *dims, const ssd_delta_rule_inputs *in, float *states,
+                               int32_t nslots, const int32_t *slot_idx, void *o, int64_t o_tok_stride,
+                               ssd_stream_t stream);
+
+/* Block norm: the norms behind and before a block, joined with its gate, its scale and the residual stream.  Per row of
+ * `channels` values, rms(v) = sqrt(mean of v^2 + eps):
+ *     u = x / rms(x) * post_weight          (dims.post_norm; else u = x)
+ *     t = u z sigmoid(z)                    (dims.gate, z a tensor like x; else t = u)
+ *     h = residual + branch_scale t         (dims.residual; else h = branch_scale t)
+ *     y = h / rms(h) * pre_weight           (dims.pre_norm: the input of the next block)
+ * x, z, y in dims.dtype, residual and h in dims.residual_dtype (that of x, or fp32), rows with their own strides
+ * (channels contiguous), element aligned; tensors that are 16-byte aligned with strides and channels a multiple of 8
+ * move as 16-byte vectors, even ones two elements at a time, others one by one.  post_weight, branch_scale, pre_weight
+ * (channels) fp32, or NULL (1).  y is made of h before it is rounded.
+ * h: may be NULL with pre_norm, and may be the residual itself, with its stride (the stream updated in place); other
+ * outputs that start where an input does are refused (SSD_ERR_INVALID_DIMS).  rstd_post (rows) and rstd_pre (rows) fp32,
+ * 1 / rms, are written with their norm, each may be NULL; the backward pass reads them.
+ * Envelope: at most 16384 channels and 2^30 rows, row strides below 2^31 elements; else SSD_ERR_UNSUPPORTED.  All sums
+ * have a fixed order. */
+typedef struct {
+  int32_t rows, channels;
+  int32_t dtype;          /* ssd_dtype of x, z, y and their gradients */
+  int32_t residual_dtype; /* ssd_dtype of residual, h and their gradients */
+  int32_t post_norm, gate, residual, pre_norm; /* each 0 or 1 */
+} ssd_block_norm_dims;
+
+typedef struct {
+  const void *x; int64_t x_row_stride;
+  const void *z; int64_t z_row_stride;               /* exactly with dims.gate */
+  const void *residual; int64_t residual_row_stride; /* forward: exactly with dims.residual; backward: NULL */
+  const float *post_weight;  /* NULL without post_norm */
+  const float *branch_scale;
+  const float *pre_weight;   /* NULL without pre_norm */
+  float eps;
+} ssd_block_norm_inputs;
+
+/* What the backward pass reads besides the inputs.  h: the forward pass's h (without post_norm, gate, residual and
+ * branch_scale that is x, of the same type), needed with pre_norm.  dh: the gradient of h from elsewhere, or NULL
+ * (zero).  dy: the gradient of y, exactly with pre_norm. */
+typedef struct {
+  const void *h; int64_t h_row_stride;
+  const void *dh; int64_t dh_row_stride;
+  const void *dy; int64_t dy_row_stride;
+  const float *rstd_post, *rstd_pre;
+} ssd_block_norm_saved;
+
+/* Gradients, written (not accumulated).  dz exactly with dims.gate, dresidual exactly with dims.residual; dresidual may
+ * be dh itself, with its stride.  Parameter gradients (channels) fp32, each may be NULL; dpost_weight only with
+ * post_norm, dpre_weight only with pre_norm. */
+typedef struct {
+  void *dx; int64_t dx_row_stride;
+  void *dz; int64_t dz_row_stride;
+  void *dresidual; int64_t dresidual_row_stride;
+  float *dpost_weight, *dbranch_scale, *dpre_weight;
+} ssd_block_norm_grads;
+
+/* Bytes of device workspace of ssd_block_norm_backward; the forward pass needs none. */
+size_t ssd_block_norm_workspace_size(const ssd_block_norm_dims *dims);
+
+ssd_status ssd_block_norm_forward(const ssd_block_norm_dims *dims, const ssd_block_norm_inputs *in, void *h,
+                                  int64_t h_row_stride, void *y, int64_t y_row_stride, float *rstd_post,
+                                  float *rstd_pre, ssd_stream_t stream);
+
+ssd_status ssd_block_norm_backward(const ssd_block_norm_dims *dims, const ssd_block_norm_inputs *in,
+                                   const ssd_block_norm_saved *saved, const ssd_block_norm_grads *grads,
+                                   void *workspace, size_t ws_bytes, ssd_stream_t stream);
+
 /* Static description of a status code. */
 const char *ssd_status_string(ssd_status status);
 

@@ -2,7 +2,6 @@
 // an activation: argument checks, workspace carving and launch sequences.
 // Nothing here allocates or synchronises.
 #include <cmath>
-#include <initializer_list>
 
 #include "group_norm.h"
 #include "retention.h"
@@ -10,16 +9,6 @@
 using namespace ssd;
 
 namespace {
-
-constexpr long long kMaxRows = 1LL << 30, kMaxChannels = 1 << 16;
-constexpr int kMaxSeqs = 1 << 20;
-
-// an output that starts where one of these inputs does
-bool on_input(const void *out, std::initializer_list<const void *> inputs) {
-  for (const void *p : inputs)
-    if (out && out == p) return true;
-  return false;
-}
 
 // ---------------------------------------------------------------- linear attention
 

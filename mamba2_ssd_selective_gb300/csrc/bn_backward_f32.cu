@@ -1,0 +1,7 @@
+#include "block_norm.cuh"
+
+namespace ssd {
+
+template void launch_bn_backward<float, float>(const BnProblem &, int, cudaStream_t);
+
+}  // namespace ssd

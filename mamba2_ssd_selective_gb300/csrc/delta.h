@@ -1,0 +1,115 @@
+// The gated delta rule, internal: a call's description, the chunks' tables and their launchers.
+//
+// Per state head, with a_t = exp(log_decay_t), b_t = beta_t and k, q of length 1 where qk_norm says so:
+//     S' = a_t S_{t-1},   S_t = S' + b_t k_t^T (v_t - k_t S'),   o_t = scale q_t S_t
+// Chunks of 64 tokens.  G_i: the sum of the chunk's log decays up to token i, S: the state before the chunk.
+//     A_ij = e^(G_i - G_j) k_i.k_j (j < i),    N = (I + A diag(b))^-1 A    (strictly lower triangular, as A)
+//     P_ij = scale e^(G_i - G_j) q_i.k_j (j <= i)
+//     Y = V - diag(e^G) K S,   E = Y - N (b Y),   D = b E
+//     O = scale diag(e^G) Q S + P D,   S_next = e^Gall S + K^T diag(e^(Gall - G)) D
+// N and P do not depend on the state: they are made for all chunks side by side, and what runs from chunk
+// to chunk is four products.  Writing the inverse as I - N diag(b) keeps its identity exact, and b = 0 harmless.
+// Backward, dS: the gradient of the state behind the chunk:
+//     dD = P^T dO + diag(e^(Gall - G)) K dS,   Z = dD - N^T (b dD),   dV = b Z,   dbeta_i = E_i.Z_i
+//     dS_prev = e^Gall dS + scale Q^T diag(e^G) dO - K^T diag(e^G) dV
+//     dA = -dV D^T,   dP = dO D^T (each where its matrix is not zero), and with L_ij = e^(G_i - G_j)
+//     dQ = scale diag(e^G) dO S^T + (scale dP L) K
+//     dK = diag(e^(Gall - G)) D dS^T - diag(e^G) dV S^T + (scale dP L)^T Q + (dA L) K + (dA L)^T K
+//     dlog_decay_t = sum_{i >= t} (q_i.dq_i - v_i.dv_i) + <S_next, dS>
+// The last line: a decay at t scales all that passes from before t to t and later, and both sums count it: q.dq
+// what tokens read, v.dv what they would have read of their own chunk's additions.
+// q and k stay as they are (exact as bf16 operands): 1 / |q| and 1 / |k| are part of the rows' factors and of A, P.
+#pragma once
+
+#include "retention.h"
+
+namespace ssd {
+
+constexpr int kDrC = 64;  // tokens of a chunk
+
+// Factors of a chunk's rows.  Rows past the sequence's end have zeros.
+struct alignas(16) DrRows {
+  float kin[kDrC];   // e^G / |k|
+  float kout[kDrC];  // e^(Gall - G) / |k|
+  float qin[kDrC];   // scale e^G / |q|
+  float beta[kDrC];
+  float rk[kDrC], rq[kDrC];      // 1 / |k|, 1 / |q| (1 without qk_norm)
+  float ghi[kDrC], glo[kDrC];    // G as a sum of two values
+  float all_hi, all_lo, pad[2];  // e^Gall, likewise: a state is multiplied by it in every chunk that it lives
+};
+static_assert(sizeof(DrRows) % 16 == 0, "moved in units of 16 bytes");
+
+struct DrProblem {
+  int nseq, seqlen, total, H, Hk, group, dk, dv;
+  int slots;      // places for chunks: those of sequence s start at dr_slot0
+  const int *cu;  // or null: sequences of seqlen tokens
+  const void *q, *k, *v, *g, *b;
+  long long qs, ks, vs, gs, bs;  // token strides (elements)
+  float scale, eps;
+  int norm;
+  const float *init;
+  // tables, of chunk (slot, head) at slot * H + head
+  DrRows *rows;
+  float *N, *P;  // CUDA cores: (64, 64) fp32, element (i, j) at 64 i + j
+  // backward: the states before the chunks and the gradients of those behind them (dk, dv); E and Z (total, H, dv)
+  float *S, *dS, *E, *Z;
+  float *dqp, *dkp;  // (total, H, dk): gradients of the unit q and k of each state head
+};
+
+__host__ __device__ __forceinline__ int dr_slots(long long rows, int nseq, int seqlen, bool packed) {
+  return packed ? (int)(rows / kDrC) + nseq : nseq * ((seqlen + kDrC - 1) / kDrC);
+}
+// A sequence's rows, and the place of its first chunk.  Packed: ceil(len / 64) chunks fit between the places of
+// sequences that start at a and a + len, a / 64 + s and (a + len) / 64 + s + 1, whatever the lengths are.
+__device__ __forceinline__ void dr_seq(const DrProblem &p, int s, int &a, int &len, int &slot0) {
+  if (p.cu) {
+    a = min(max(__ldg(p.cu + s), 0), p.total);
+    len = max(min(max(__ldg(p.cu + s + 1), 0), p.total) - a, 0);
+    slot0 = a / kDrC + s;
+  } else {
+    a = s * p.seqlen;
+    len = p.seqlen;
+    slot0 = s * ((p.seqlen + kDrC - 1) / kDrC);
+  }
+}
+// The rows of the chunk at a place: [t0, t0 + n), n = 0 where there is none
+__device__ __forceinline__ void dr_chunk(const DrProblem &p, int slot, int &t0, int &n) {
+  int a, len, slot0, s = 0;
+  if (p.cu) {  // the last sequence whose place is not behind this one
+    int lo = 0, hi = p.nseq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (min(max(__ldg(p.cu + mid), 0), p.total) / kDrC + mid <= slot)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    s = lo;
+  } else {
+    s = slot / ((p.seqlen + kDrC - 1) / kDrC);
+  }
+  dr_seq(p, s, a, len, slot0);
+  const long long off = (long long)(slot - slot0) * kDrC;
+  t0 = a + (int)(off < 0 || off > len ? len : off);
+  n = off < 0 || off >= len ? 0 : min(kDrC, len - (int)off);
+}
+
+// dr_prep.cu: rows' factors, N and P of every chunk
+template <typename T> void launch_dr_prep(const DrProblem &p, cudaStream_t s);
+// dr_simt.cu: the chain of chunks (o null: only S and E, for backward), its reverse, and the gradients
+template <typename T> void launch_dr_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);
+template <typename T>
+void launch_dr_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s);
+struct DrGrads {
+  void *dq, *dk, *dv, *dg, *db;
+  long long dqs, dks, dvs, dgs, dbs;
+};
+template <typename T>
+void launch_dr_grads(const DrProblem &p, const void *dout, long long dos, const DrGrads &g, cudaStream_t s);
+// dq and dk out of their parts: summed over the states that share a head, and through the division by the length
+template <typename T> void launch_dr_finish(const DrProblem &p, const DrGrads &g, cudaStream_t s);
+// dr_step.cu
+template <typename T>
+void launch_dr_step(const DrProblem &p, void *o, long long os, float *states, int nslots, const int *slot_idx, cudaStream_t s);
+
+}  // namespace ssd

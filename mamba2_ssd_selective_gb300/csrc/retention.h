@@ -147,6 +147,15 @@ __device__ __forceinline__ float2 la_pow2(float g, int n) {
   return make_float2(hi, e - (hi - 1.f));
 }
 
+// lam as a sum of two fp32 values where it is near 1: one rounded value, up to 2^-25 off, would multiply the state at
+// every token, for 1 / (1 - lam) tokens and more (6000 tokens of heads that live as long: states off by 9e-5).
+// e^g - 1 by its series, whose fifth term is below 2^-25 of the first at 1/32; below, a state lives for 32 tokens at
+// most, and the error adds up to 1e-6.  (la_pow2, with a call of expm1, costs 2% more where dk is small.)
+__device__ __forceinline__ float2 step_decay(float g) {
+  const float lam = expf(g), e = g * fmaf(g, fmaf(g, fmaf(g, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f), hi = 1.f + e;
+  return g > -0.03125f ? make_float2(hi, e - (hi - 1.f)) : make_float2(lam, 0.f);
+}
+
 // la_plan.cu: clears status, counters and flags; writes the table of units
 void launch_la_table(const LaPlanDev &pl, LaEntry *table, int *table_units, int nflags, cudaStream_t s);
 // la_simt.cu: any type and width of the envelope.  summary: the segments' own states
