@@ -10,8 +10,9 @@ namespace {
 // ---------------------------------------------------------------- gated delta rule
 
 struct DrPlan {
+  bool tc;
   int slots;
-  size_t rows, N, P, S, dS, E, Z, dqp, dkp, total;  // workspace offsets
+  size_t status, rows, N, P, S, dS, E, Z, dqp, dkp, total;  // workspace offsets
 };
 
 long long dr_rows(const ssd_delta_rule_dims *d) { return d->packed ? d->total_tokens : (long long)d->nseq * d->seqlen; }
@@ -32,8 +33,12 @@ ssd_status dr_check_dims(const ssd_delta_rule_dims *d) {
   return SSD_OK;
 }
 
+// bf16 within its widths takes the tensor-core kernels, everything else the CUDA-core ones
+bool dr_use_tc(const ssd_delta_rule_dims *d) { return d->dtype == SSD_BF16 && la_tc_envelope(d->headdim_k, d->headdim_v); }
+
 DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
   DrPlan pl{};
+  pl.tc = dr_use_tc(d) && !backward;
   pl.slots = dr_slots(dr_rows(d), d->nseq, d->seqlen, d->packed != 0);
   const size_t chunks = (size_t)pl.slots * d->nheads, state = (size_t)d->headdim_k * d->headdim_v,
                tokens = (size_t)dr_rows(d) * d->nheads;
@@ -43,9 +48,10 @@ DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
     off = align_up(off + bytes, 256);
     return o;
   };
+  pl.status = take(256);
   pl.rows = take(chunks * sizeof(DrRows));
-  pl.N = take(chunks * kDrC * kDrC * 4);
-  pl.P = take(chunks * kDrC * kDrC * 4);
+  pl.N = take(chunks * (pl.tc ? 4 * kDrTile : kDrC * kDrC * 4));
+  pl.P = take(pl.tc ? 0 : chunks * kDrC * kDrC * 4);
   if (backward) {
     pl.S = take(chunks * state * 4);
     pl.dS = take(chunks * state * 4);
@@ -115,6 +121,8 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
   p.init = in->initial_states;
   if (pl) {
     p.slots = pl->slots;
+    p.status = reinterpret_cast<int *>(ws + pl->status);
+    p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
     p.rows = reinterpret_cast<DrRows *>(ws + pl->rows);
     auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
     p.N = at(pl->N), p.P = at(pl->P);
@@ -125,9 +133,9 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
 }
 
 template <typename T>
-ssd_status dr_forward_impl(const DrProblem &p, void *o, int64_t os, float *fin, cudaStream_t s) {
-  SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, s));
-  SSD_LAUNCH("dr_chain", launch_dr_chain<T>(p, o, os, fin, s));
+ssd_status dr_forward_impl(const DrProblem &p, bool tc, void *o, int64_t os, float *fin, cudaStream_t s) {
+  SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, tc, s));
+  SSD_LAUNCH("dr_chain", tc ? launch_dr_tc_chain(p, o, os, fin, s) : launch_dr_chain<T>(p, o, os, fin, s));
   return launch_status();
 }
 
@@ -136,7 +144,7 @@ ssd_status dr_backward_impl(const DrProblem &p, const void *dout, int64_t dos, c
                             const ssd_delta_rule_grads *g, cudaStream_t s) {
   const DrGrads out{g->dq, g->dk, g->dv, g->dlog_decay, g->dbeta, g->dq_tok_stride, g->dk_tok_stride, g->dv_tok_stride,
                     g->dlog_decay_tok_stride, g->dbeta_tok_stride};
-  SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, s));
+  SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, false, s));
   SSD_LAUNCH("dr_chain", launch_dr_chain<T>(p, nullptr, 0, nullptr, s));
   SSD_LAUNCH("dr_reverse", launch_dr_reverse<T>(p, dout, dos, dfin, g->dinitial_states, s));
   SSD_LAUNCH("dr_grads", launch_dr_grads<T>(p, dout, dos, out, s));
@@ -228,8 +236,8 @@ ssd_status ssd_delta_rule_forward(const ssd_delta_rule_dims *dims, const ssd_del
   if (on_input(o, {in->q, in->k, in->v, in->log_decay, in->beta})) return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const DrProblem p = dr_problem(dims, in, &pl, static_cast<char *>(workspace));
-  return dims->dtype == SSD_BF16 ? dr_forward_impl<__nv_bfloat16>(p, o, o_tok_stride, final_states, s)
-                                 : dr_forward_impl<float>(p, o, o_tok_stride, final_states, s);
+  return dims->dtype == SSD_BF16 ? dr_forward_impl<__nv_bfloat16>(p, pl.tc, o, o_tok_stride, final_states, s)
+                                 : dr_forward_impl<float>(p, pl.tc, o, o_tok_stride, final_states, s);
 }
 
 ssd_status ssd_delta_rule_backward(const ssd_delta_rule_dims *dims, const ssd_delta_rule_inputs *in, const void *dout,

@@ -26,6 +26,7 @@
 namespace ssd {
 
 constexpr int kDrC = 64;  // tokens of a chunk
+constexpr uint32_t kDrTile = kDrC * kDrC * 2;  // bytes of a (64, 64) bf16 tile
 
 // Factors of a chunk's rows.  Rows past the sequence's end have zeros.
 struct alignas(16) DrRows {
@@ -51,9 +52,13 @@ struct DrProblem {
   // tables, of chunk (slot, head) at slot * H + head
   DrRows *rows;
   float *N, *P;  // CUDA cores: (64, 64) fp32, element (i, j) at 64 i + j
-  // backward: the states before the chunks and the gradients of those behind them (dk, dv); E and Z (total, H, dv)
+  // backward: the states before the chunks and the gradients of those behind them (dk, dv), E and Z (total, H, dv).
+  // Tensor cores: N's and P's two bf16 terms as four tiles of (64, 64) in the 128-byte swizzle, at N; the states
+  // (dv, dk), E and Z are bf16.
   float *S, *dS, *E, *Z;
   float *dqp, *dkp;  // (total, H, dk): gradients of the unit q and k of each state head
+  int *status;       // device status word, cleared by the first kernel
+  unsigned long long wait_ns;
 };
 
 __host__ __device__ __forceinline__ int dr_slots(long long rows, int nseq, int seqlen, bool packed) {
@@ -94,8 +99,11 @@ __device__ __forceinline__ void dr_chunk(const DrProblem &p, int slot, int &t0, 
   n = off < 0 || off >= len ? 0 : min(kDrC, len - (int)off);
 }
 
-// dr_prep.cu: rows' factors, N and P of every chunk
-template <typename T> void launch_dr_prep(const DrProblem &p, cudaStream_t s);
+// dr_prep.cu: rows' factors, N and P of every chunk; tc: for the tensor-core chains
+template <typename T> void launch_dr_prep(const DrProblem &p, bool tc, cudaStream_t s);
+// dr_tc.cu: the chains for bf16, both widths at most 128
+void launch_dr_tc_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);
+void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s);
 // dr_simt.cu: the chain of chunks (o null: only S and E, for backward), its reverse, and the gradients
 template <typename T> void launch_dr_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);
 template <typename T>

@@ -82,12 +82,21 @@ __device__ __forceinline__ void fill_rows(const DrProblem &p, PrepShared &sm, in
   }
 }
 
-template <typename T>
+// a value as two bf16 terms, element (i, j) of their tiles in the 128-byte swizzle
+__device__ __forceinline__ void store_terms(uint8_t *tile, int i, int j, float v) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  const uint32_t at = sm100::sw128_offset(i, j);
+  *reinterpret_cast<__nv_bfloat16 *>(tile + at) = hi;
+  *reinterpret_cast<__nv_bfloat16 *>(tile + kDrTile + at) = __float2bfloat16_rn(v - __bfloat162float(hi));
+}
+
+template <typename T, bool TC>
 __global__ void __launch_bounds__(kThreads) dr_prep_kernel(DrProblem p) {
   extern __shared__ __align__(16) uint8_t raw[];
   PrepShared &sm = *reinterpret_cast<PrepShared *>(raw);
   const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, tm = tid >> 4, tn = tid & 15;
   int t0, n;
+  if (slot == 0 && hk == 0 && tid == 0) *p.status = 0;
   dr_chunk(p, slot, t0, n);
   if (n == 0) return;
   const T *q = static_cast<const T *>(p.q) + (size_t)t0 * p.qs + (size_t)hk * p.dk;
@@ -123,12 +132,17 @@ __global__ void __launch_bounds__(kThreads) dr_prep_kernel(DrProblem p) {
     __syncthreads();
     const size_t at = (size_t)slot * p.H + h;
     const float nan = __int_as_float(0x7fffffff);
+    uint8_t *tiles = reinterpret_cast<uint8_t *>(p.N) + at * (4 * kDrTile);
     for (int e = tid; e < kDrC * kDrC; e += kThreads) {
       const int i = e >> 6, j = e & 63;
       float l = j <= i ? expf((sm.rows.ghi[i] - sm.rows.ghi[j]) + (sm.rows.glo[i] - sm.rows.glo[j])) : 0.f;
       if (j <= i && i >= sm.nan_at && j < sm.nan_at) l = nan;
       const float rk = sm.rows.rk[j];
-      p.P[at * (kDrC * kDrC) + e] = j <= i ? l * sm.qk[i][j] * (sm.rows.rq[i] * rk * p.scale) : 0.f;
+      const float w = j <= i ? l * sm.qk[i][j] * (sm.rows.rq[i] * rk * p.scale) : 0.f;
+      if (TC)
+        store_terms(tiles + 2 * kDrTile, i, j, w);
+      else
+        p.P[at * (kDrC * kDrC) + e] = w;
       sm.at[j][i] = j < i ? l * sm.kk[i][j] * (sm.rows.rk[i] * rk) : 0.f;
     }
     const uint32_t *from = reinterpret_cast<const uint32_t *>(&sm.rows);
@@ -155,20 +169,32 @@ __global__ void __launch_bounds__(kThreads) dr_prep_kernel(DrProblem p) {
         }
       }
 #pragma unroll
-      for (int i = 0; i < kDrC; ++i) p.N[at * (kDrC * kDrC) + i * kDrC + tid] = x[i];
+      for (int i = 0; i < kDrC; ++i) {
+        if (TC)
+          store_terms(tiles, i, tid, x[i]);
+        else
+          p.N[at * (kDrC * kDrC) + i * kDrC + tid] = x[i];
+      }
     }
   }
 }
 
-}  // namespace
-
-template <typename T> void launch_dr_prep(const DrProblem &p, cudaStream_t s) {
+template <typename T, bool TC> void run_prep(const DrProblem &p, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  allow_smem(reinterpret_cast<const void *>(dr_prep_kernel<T>), sizeof(PrepShared), allowed);
-  dr_prep_kernel<T><<<dim3((unsigned)p.slots, (unsigned)p.Hk), kThreads, sizeof(PrepShared), s>>>(p);
+  allow_smem(reinterpret_cast<const void *>(dr_prep_kernel<T, TC>), sizeof(PrepShared), allowed);
+  dr_prep_kernel<T, TC><<<dim3((unsigned)p.slots, (unsigned)p.Hk), kThreads, sizeof(PrepShared), s>>>(p);
 }
 
-template void launch_dr_prep<float>(const DrProblem &, cudaStream_t);
-template void launch_dr_prep<__nv_bfloat16>(const DrProblem &, cudaStream_t);
+}  // namespace
+
+template <typename T> void launch_dr_prep(const DrProblem &p, bool tc, cudaStream_t s) {
+  if (sizeof(T) == 2 && tc)
+    run_prep<__nv_bfloat16, true>(p, s);
+  else
+    run_prep<T, false>(p, s);
+}
+
+template void launch_dr_prep<float>(const DrProblem &, bool, cudaStream_t);
+template void launch_dr_prep<__nv_bfloat16>(const DrProblem &, bool, cudaStream_t);
 
 }  // namespace ssd

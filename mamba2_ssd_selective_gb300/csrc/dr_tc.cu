@@ -1,0 +1,677 @@
+// The gated delta rule on the 5th-generation tensor cores (tcgen05, accumulators and A operands in TMEM): bf16 tensors,
+// widths up to 128.  The chain of chunks, forward and in reverse; the formulas are at delta.h.
+//
+// A CTA takes one sequence and head and walks its chunks.  Everything is formed transposed, so that dv (up to 128)
+// fills the accumulators' lanes and the state stays in its warps' registers (lane = dv):
+//     X^T = S^T K^T,   Y = V - kin X,   E = Y - N (b Y),   S = e^Gall S + W,   W^T = (kout b E)^T K
+//     O^T = (qin S^T Q^T) + (b E)^T P^T
+// In reverse the same four steps, with the gradient of the state for the state:
+//     X^T = dS^T K^T,   dD = kout X + P^T dO,   Z = dD - N^T (b dD),   dS = e^Gall dS + W,
+//     W^T = (qin dO)^T Q - (kin b Z)^T K
+// What ends in a state keeps fp32 precision: an operand that is not a bf16 tensor of the user's is a sum of two bf16 terms
+// (16 bits; products of the two low terms are left out), which leaves a relative error of about 3e-6 a product.
+//
+// Warps:
+//   0       TMA producer: K, Q, V (reverse: dO), and the chunk's N, P and row factors, two stages
+//   1       MMA issuer
+//   2, 3    a sequence's last chunk: rows past its end become zeros in shared memory
+//   4-11    Y and E (reverse: dD and Z), as fragments of 16 lanes x 32 tokens
+//   12-19   state
+//   20-23   outputs; in reverse the two terms of (qin dO)^T
+// What bounds it: the chain from state to state, its products (16 of X, 12 of N, 8 of W, 46 to 66 cycles each) and
+// five hand-offs between tensor core and warps.
+#include "delta.h"
+#include "tc_pipe.cuh"
+#include "tc_util.cuh"
+
+namespace ssd {
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+using namespace sm100;
+using pipe::parity;
+
+constexpr int kThreads = 768;
+constexpr int kElemWarp0 = 4, kStateWarp0 = 12, kOutWarp0 = 20;
+constexpr uint32_t kBox = 8192;  // [64 rows x 64 columns] bf16
+constexpr int kStages = 2;
+
+// TMEM columns: the state's terms (64 each), X and then N's product, outputs (reverse: P^T dO), the terms of b Y and then
+// of the additions (32 each), b E for the outputs or the terms of qin dO, W
+constexpr uint32_t kTmS = 0, kTmX = 128, kTmO = 192, kTmY = 256, kTmD = 320, kTmW = 384, kTmCols = 512;
+
+enum Mode { kOut, kStates, kReverse };  // outputs; states and E for the backward pass; the reverse chain
+
+template <int KB, int VB, int MODE> struct Layout {
+  static constexpr uint32_t kK = 0, kQ = KB * kBox, kV = kQ + KB * kBox, kN = kV + VB * kBox, kP = kN + 2 * kBox;
+  static constexpr uint32_t kRows = kP + 2 * kBox, kStage = (kRows + sizeof(DrRows) + 1023) / 1024 * 1024;
+  static constexpr uint32_t kO = kStages * kStage;  // a chunk's outputs, on their way to TMA
+  static constexpr uint32_t kBar = kO + VB * kBox;
+  static constexpr int kNumBars = 2 * kStages + 14;
+  static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
+  static constexpr int kBytes = (int)kEnd + 1024;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+struct Bars {
+  uint64_t *full, *free;  // [stages] loaded / read
+  uint64_t *patched;      // the last chunk's rows past the end are zeros
+  uint64_t *s_ready;      // the state's terms in TMEM
+  uint64_t *x_full;       // X
+  uint64_t *y_ready;      // b Y's terms in TMEM
+  uint64_t *n_full;       // N's product
+  uint64_t *d_ready;      // the additions' terms in TMEM
+  uint64_t *w_full;       // W
+  uint64_t *q_full, *q_ready;  // outputs' part of the state formed / scaled; reverse: W's part of dO formed / its terms in TMEM
+  uint64_t *o_full, *o_free;   // outputs formed / read; reverse: P^T dO
+  uint64_t *drain;
+  __device__ explicit Bars(uint64_t *b) {
+    full = b;
+    free = b + kStages;
+    patched = b + 2 * kStages;
+    s_ready = patched + 1;
+    x_full = patched + 2;
+    y_ready = patched + 3;
+    n_full = patched + 4;
+    d_ready = patched + 5;
+    w_full = patched + 6;
+    q_full = patched + 7;
+    q_ready = patched + 8;
+    o_full = patched + 9;
+    o_free = patched + 10;
+    drain = patched + 11;
+  }
+};
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// two values as two bf16 pairs that add up to them to 16 bits
+__device__ __forceinline__ void split2(float x, float y, uint32_t &a, uint32_t &b) {
+  a = tc::pack_bf16x2(x, y);
+  b = tc::pack_bf16x2(x - lo_f(a), y - hi_f(a));
+}
+
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t par, const WaitCtl &w) {
+  const uint32_t hint = w.limit_ns < kWaitHintNs ? (uint32_t)w.limit_ns : kWaitHintNs;
+  if (__builtin_expect(mbar_try_wait_hint(bar, par, hint), 1)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < w.limit_ns) {
+    if (mbar_try_wait_hint(bar, par, hint)) return true;
+    if (*reinterpret_cast<volatile int *>(w.status) != 0) return false;
+  }
+  atomicExch(w.status, 1);
+  return false;
+}
+template <int ID, int THREADS> __device__ __forceinline__ void role_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+
+struct Args {
+  CUtensorMap q, k, v, o;  // v: dO in reverse; o: outputs, E or Z
+  DrProblem p;
+  const float *first;  // states (gradients of final states) that the chain starts from, or null
+  float *last;         // and where it ends, or null
+  bf16 *out;           // o's rows
+  long long os;
+  bf16 *kept;  // (chunk, dv, dk): the state before each chunk, the gradient of the one behind
+  WaitCtl wait;
+};
+
+template <int KB, int VB, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constant__ Args args) {
+  using L = Layout<KB, VB, MODE>;
+  constexpr bool kRev = MODE == kReverse;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = tc::aligned_smem(smem_raw);
+  const DrProblem &p = args.p;
+  const WaitCtl wait = args.wait;
+  const Bars bar(reinterpret_cast<uint64_t *>(sm + L::kBar));
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + L::kNumBars * 8);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int seq = blockIdx.x / p.H, h = blockIdx.x - seq * p.H;
+  int a, len, slot0;
+  dr_seq(p, seq, a, len, slot0);
+  const int nc = __shfl_sync(0xffffffffu, (len + kDrC - 1) / kDrC, 0);
+  // processing order: the i-th chunk, its rows
+  auto chunk = [&](int i) { return kRev ? nc - 1 - i : i; };
+  auto live = [&](int i) { return min(kDrC, len - chunk(i) * kDrC); };
+  const int tail = kRev ? 0 : nc - 1;
+  const bool partial = len % kDrC != 0;  // the tail is
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&args.k);
+    prefetch_tmap(&args.q);
+    prefetch_tmap(&args.v);
+    prefetch_tmap(&args.o);
+  }
+  if (threadIdx.x == 64) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar.full[i], 1);
+      // the issuer's commit, the Y and state warps, the outputs' warps and those of a partial chunk where there are any
+      mbar_init(&bar.free[i], 1 + 8 * VB + (MODE == kStates ? 0 : 2 * VB) + (partial ? 2 : 0));
+    }
+    mbar_init(bar.patched, 2);
+    mbar_init(bar.s_ready, 4 * VB);
+    mbar_init(bar.x_full, 1);
+    mbar_init(bar.y_ready, 4 * VB);
+    mbar_init(bar.n_full, 1);
+    mbar_init(bar.d_ready, 4 * VB);
+    mbar_init(bar.w_full, 1);
+    mbar_init(bar.q_full, 1);
+    mbar_init(bar.q_ready, 2 * VB);
+    mbar_init(bar.o_full, 1);
+    mbar_init(bar.o_free, kRev ? 4 * VB : 2 * VB);
+    mbar_init(bar.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tslot, kTmCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
+  const uint32_t s0 = smem_u32(sm);
+  auto stage = [&](int i) { return (uint32_t)(i % kStages) * L::kStage; };
+  auto rows_of = [&](int i) { return s0 + stage(i) + L::kRows; };
+  auto wait_full = [&](int i) {
+    wait_on(&bar.full[i % kStages], parity(i / kStages), wait);
+    if (partial && i == tail) wait_on(bar.patched, 0, wait);
+  };
+
+  // The block is launched with 768 x 80 registers; the state's warps take what the first four do not need:
+  // 128 x (48 + 2 * 80 + 2 * 96 + 80) = 61440.
+  if (warp < kElemWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        const int hk = h / p.group;
+        int i = 0;
+#pragma unroll 1
+        for (; i < nc; ++i) {
+          const int st = i % kStages, row = a + chunk(i) * kDrC;
+          if (i >= kStages && !wait_on(&bar.free[st], parity(i / kStages - 1), wait)) break;
+          uint8_t *base = sm + stage(i);
+          const size_t at = (size_t)(slot0 + chunk(i)) * p.H + h;
+          const uint8_t *tiles = reinterpret_cast<const uint8_t *>(p.N) + at * (4 * kBox);
+          constexpr uint32_t kQBytes = MODE == kStates ? 0 : KB * kBox;
+          constexpr uint32_t kMats = MODE == kOut ? 3 * kBox : MODE == kStates ? 2 * kBox : 4 * kBox;
+          mbar_expect_tx(&bar.full[st], KB * kBox + kQBytes + VB * kBox + kMats + (uint32_t)sizeof(DrRows));
+          for (int b = 0; b < KB; ++b) tma_load_3d(base + L::kK + b * kBox, &args.k, &bar.full[st], 64 * b, hk, row);
+          for (int b = 0; b < VB; ++b) tma_load_3d(base + L::kV + b * kBox, &args.v, &bar.full[st], 64 * b, h, row);
+          pipe::bulk_load(base + L::kRows, p.rows + at, sizeof(DrRows), &bar.full[st]);
+          pipe::bulk_load(base + L::kN, tiles, kMats, &bar.full[st]);  // N's terms, P's behind them
+          if (MODE != kStates)
+            for (int b = 0; b < KB; ++b) tma_load_3d(base + L::kQ + b * kBox, &args.q, &bar.full[st], 64 * b, hk, row);
+        }
+        // every load issued has landed before the CTA releases its shared memory
+#pragma unroll 1
+        for (int x = i > kStages ? i - kStages : 0; x < i; ++x) mbar_wait_drain(&bar.full[x % kStages], parity(x / kStages));
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t el = elect_one();
+      const uint64_t dK = desc_sw128(s0 + L::kK, 16, 1024), dQ = desc_sw128(s0 + L::kQ, 16, 1024);   // K-major
+      const uint64_t dKn = desc_sw128(s0 + L::kK, kBox, 1024), dQn = desc_sw128(s0 + L::kQ, kBox, 1024);  // MN-major
+      const uint64_t dV = desc_sw128(s0 + L::kV, kBox, 1024), dN = desc_sw128(s0 + L::kN, 16, 1024),
+                     dP = desc_sw128(s0 + L::kP, 16, 1024);
+      constexpr uint32_t iKK = idesc_bf16(128, 64, false, false), iKM = idesc_bf16(128, 64, false, true),
+                         iMM = idesc_bf16(128, 64, true, true), iW = idesc_bf16(128, 64 * KB, false, true);
+      constexpr uint64_t kB = kBox / 16;
+      constexpr uint64_t kStepN = kRev ? pipe::kStepMN : pipe::kStepK;  // N transposed in reverse
+      constexpr uint32_t iN = kRev ? iKM : iKK;
+      auto at = [&](int i) { return (uint64_t)(stage(i) / 16); };
+      auto dO_part = [&](int i) {  // P^T dO of chunk i
+        wait_full(i);
+        if (i > 0) wait_on(bar.o_free, parity(i - 1), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          pipe::umma_k_el<4>(el, tmem + kTmO, dV + at(i), dP + at(i) + t * kB, pipe::kStepMN, pipe::kStepMN, iMM, t > 0);
+        umma_commit_el(el, bar.o_full);
+      };
+      if (kRev && nc > 0) dO_part(0);
+#pragma unroll 1
+      for (int i = 0; i < nc; ++i) {
+        wait_full(i);
+        wait_on(bar.s_ready, parity(i), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+            pipe::umma_ts_k_el<4>(el, tmem + kTmX, tmem + kTmS + 64 * t + 32 * b, dK + at(i) + b * kB, 8, pipe::kStepK, iKK,
+                                  t + b > 0);
+        umma_commit_el(el, bar.x_full);
+        if (MODE == kOut) {
+          if (i > 0) {
+            wait_on(bar.o_free, parity(i - 1), wait);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+            pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmS + 32 * b, dQ + at(i) + b * kB, 8, pipe::kStepK, iKK, b > 0);
+          umma_commit_el(el, bar.q_full);
+        }
+        if (kRev) {
+          wait_on(bar.q_ready, parity(i), wait);
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            pipe::umma_ts_k_el<4>(el, tmem + kTmW, tmem + kTmD + 32 * t, dQn + at(i), 8, pipe::kStepMN, iW, t > 0);
+          umma_commit_el(el, bar.q_full);
+        }
+        wait_on(bar.y_ready, parity(i), wait);
+        tc_fence_after();
+        pipe::umma_ts_k_el<4>(el, tmem + kTmX, tmem + kTmY, dN + at(i), 8, kStepN, iN, false);
+        pipe::umma_ts_k_el<4>(el, tmem + kTmX, tmem + kTmY + 32, dN + at(i), 8, kStepN, iN, true);
+        pipe::umma_ts_k_el<4>(el, tmem + kTmX, tmem + kTmY, dN + at(i) + kB, 8, kStepN, iN, true);
+        umma_commit_el(el, bar.n_full);
+        wait_on(bar.d_ready, parity(i), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          pipe::umma_ts_k_el<4>(el, tmem + kTmW, tmem + kTmY + 32 * t, dKn + at(i), 8, pipe::kStepMN, iW, kRev || t > 0);
+        umma_commit_el(el, bar.w_full);
+        if (MODE == kOut) {
+          wait_on(bar.q_ready, parity(i), wait);
+          tc_fence_after();
+          pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmD, dP + at(i), 8, pipe::kStepK, iKK, true);
+          umma_commit_el(el, bar.o_full);
+        }
+        umma_commit_el(el, &bar.free[i % kStages]);
+        if (kRev && i + 1 < nc) dO_part(i + 1);
+      }
+      // every MMA and every arrival of a commit has landed before the CTA ends
+      umma_commit_el(el, bar.drain);
+      mbar_wait_drain(bar.drain, 0);
+#pragma unroll 1
+      for (int x = nc > kStages ? nc - kStages : 0; x < nc; ++x) mbar_wait_drain(&bar.free[x % kStages], parity(x / kStages));
+      if (nc > 0) {
+        mbar_wait_drain(bar.x_full, parity(nc - 1));
+        mbar_wait_drain(bar.n_full, parity(nc - 1));
+        mbar_wait_drain(bar.w_full, parity(nc - 1));
+        if (MODE != kStates) {
+          mbar_wait_drain(bar.q_full, parity(nc - 1));
+          mbar_wait_drain(bar.o_full, parity(nc - 1));
+        }
+      }
+    } else if (partial) {
+      // ------------------------------------------------------------ rows past the end
+      const int t = threadIdx.x - 64;
+      constexpr int kBoxes = 2 * KB + VB;  // K, Q and V follow each other
+#pragma unroll 1
+      for (int i = 0; i < nc; ++i) {
+        wait_on(&bar.full[i % kStages], parity(i / kStages), wait);
+        if (i == tail) {
+          const int nv = live(i);
+          for (int e = t; e < (kDrC - nv) * 8 * kBoxes; e += 64) {
+            const int y = e % (8 * kBoxes), r = nv + e / (8 * kBoxes);
+            pipe::sts_u4(s0 + stage(i) + L::kK + (uint32_t)(y >> 3) * kBox + sw128_offset(r, 8 * (y & 7)), make_uint4(0, 0, 0, 0));
+          }
+          fence_async_smem();
+          pipe::warp_arrive(bar.patched);
+        }
+        pipe::warp_arrive(&bar.free[i % kStages]);
+      }
+    }
+  } else if (warp < kStateWarp0) {
+    // ------------------------------------------------------------ Y and E
+    const int quad = warp & 3, sub = (warp - kElemWarp0) >> 2;
+    if (quad < 2 * VB) {
+      const int tok = 32 * sub + 2 * (lane & 3);  // this lane's tokens: tok + 8 m and the next
+      // addresses of the transposing loads of V: 16 tokens and 16 lanes (columns of v) at a time
+      const uint32_t lr = (lane & 7) + 8 * (lane >> 4), lc = 4 * (quad & 1) + ((lane >> 3) & 1);
+      const uint32_t v_at = L::kV + (uint32_t)(quad >> 1) * kBox + (32 * sub + lr) * 128;
+      // and of the stores of E: row i, columns of v
+      const int fi = 8 * (lane >> 4) + (lane & 7), fc = 32 * quad + 8 * ((lane >> 3) & 1);
+      const uint32_t so = s0 + L::kO;
+      const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+      constexpr int kTeam = 128 * VB;
+      const int tt = 64 * VB * sub + 32 * quad + lane;
+#pragma unroll 1
+      for (int i = 0; i < nc; ++i) {
+        wait_full(i);
+        const uint32_t rows = rows_of(i);
+        auto factors = [&](uint32_t which, float2(&f)[4]) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[m].x), "=f"(f[m].y) : "r"(rows + which + (tok + 8 * m) * 4));
+        };
+        constexpr uint32_t kIn = offsetof(DrRows, kin), kOutF = offsetof(DrRows, kout), kBeta = offsetof(DrRows, beta);
+        float y[2][16];
+        float2 f[4], beta[4];
+        factors(kRev ? kOutF : kIn, f);
+        factors(kBeta, beta);
+        if (!kRev) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[8];
+            const uint32_t at = s0 + stage(i) + v_at + (((lc + 2 * q) ^ (lane & 7)) * 16);
+            ldmatrix4_trans(at, w[0], w[1], w[2], w[3]);
+            ldmatrix4_trans(at + 16 * 128, w[4], w[5], w[6], w[7]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              y[q][2 * e] = lo_f(w[e]);
+              y[q][2 * e + 1] = hi_f(w[e]);
+            }
+          }
+        }
+        wait_on(bar.x_full, parity(i), wait);
+        if (kRev) wait_on(bar.o_full, parity(i), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t at = lanes + ((uint32_t)(16 * q) << 16);
+          uint32_t x[16];
+          tmem_ld_16x256_x4_async(at + kTmX + 32 * sub, x);
+          if (kRev) {
+            uint32_t g[16];
+            tmem_ld_16x256_x4_async(at + kTmO + 32 * sub, g);
+            tmem_wait_ld16(g);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[q][e] = __uint_as_float(g[e]);
+          }
+          tmem_wait_ld16(x);
+          uint32_t t0[8], t1[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 &w = f[e >> 1], &b = beta[e >> 1];
+            float &y0 = y[q][2 * e], &y1 = y[q][2 * e + 1];
+            y0 = fmaf(kRev ? w.x : -w.x, __uint_as_float(x[2 * e]), y0);
+            y1 = fmaf(kRev ? w.y : -w.y, __uint_as_float(x[2 * e + 1]), y1);
+            split2(b.x * y0, b.y * y1, t0[e], t1[e]);
+          }
+          tmem_st_16x128_async(at + kTmY + 16 * sub, t0);
+          tmem_st_16x128_async(at + kTmY + 32 + 16 * sub, t1);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        if (kRev) pipe::warp_arrive(bar.o_free);
+        pipe::warp_arrive(bar.y_ready);
+        factors(kRev ? kIn : kOutF, f);
+        if (MODE != kOut) {  // the chunk before has been read out of the staging tile
+          if (tt == 0) bulk_wait_read0();
+          role_sync<2, kTeam>();
+        }
+        wait_on(bar.n_full, parity(i), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t at = lanes + ((uint32_t)(16 * q) << 16);
+          uint32_t x[16];
+          tmem_ld_16x256_x4_async(at + kTmX + 32 * sub, x);
+          tmem_wait_ld16(x);
+          uint32_t t0[8], t1[8], t2[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 &w = f[e >> 1], &b = beta[e >> 1];
+            const float e0 = y[q][2 * e] - __uint_as_float(x[2 * e]), e1 = y[q][2 * e + 1] - __uint_as_float(x[2 * e + 1]);
+            const float d0 = b.x * e0, d1 = b.y * e1;
+            t2[e] = MODE == kOut ? tc::pack_bf16x2(d0, d1) : tc::pack_bf16x2(e0, e1);
+            split2(kRev ? -w.x * d0 : w.x * d0, kRev ? -w.y * d1 : w.y * d1, t0[e], t1[e]);
+          }
+          tmem_st_16x128_async(at + kTmY + 16 * sub, t0);
+          tmem_st_16x128_async(at + kTmY + 32 + 16 * sub, t1);
+          if (MODE == kOut) {
+            tmem_st_16x128_async(at + kTmD + 16 * sub, t2);
+          } else {  // E or Z, rows of tokens, into the staging tile
+            const int c = fc + 16 * q;
+            const uint32_t to = so + (uint32_t)(c >> 6) * kBox + sw128_offset(32 * sub + fi, c & 63);
+            stmatrix4_trans(to, t2[0], t2[1], t2[2], t2[3]);
+            stmatrix4_trans(to + 16 * 128, t2[4], t2[5], t2[6], t2[7]);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        pipe::warp_arrive(bar.d_ready);
+        pipe::warp_arrive(&bar.free[i % kStages]);
+        if (MODE != kOut) {
+          fence_async_smem();
+          role_sync<2, kTeam>();
+          const int nv = live(i);
+          const long long row0 = a + (long long)chunk(i) * kDrC;
+          if (nv < kDrC) {  // rows past the end belong to another sequence: row by row
+            bf16 *out = args.out + row0 * args.os + (size_t)h * p.dv;
+            for (int e = tt; e < nv * 8 * VB; e += kTeam) {
+              const int r = e / (8 * VB), c = 8 * (e % (8 * VB));
+              if (c < p.dv) *reinterpret_cast<uint4 *>(out + r * args.os + c) = pipe::lds_sw128(so + (uint32_t)(c >> 6) * kBox, r, (c & 63) / 8);
+            }
+          } else if (tt == 0) {
+            for (int b = 0; b < VB; ++b)
+              if (64 * b < p.dv) tma_store_3d(&args.o, so + b * kBox, 64 * b, h, (int)row0);
+            bulk_commit();
+          }
+        }
+      }
+      if (MODE != kOut && tt == 0) bulk_wait0();
+    }
+  } else if (warp < kOutWarp0) {
+    // ------------------------------------------------------------ state
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    const int quad = warp & 3, sub = (warp - kStateWarp0) >> 2;
+    if (quad < 2 * VB) {
+      constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
+      const int c = 32 * quad + lane, a0 = sub * kCols;
+      const size_t dd = (size_t)p.dk * p.dv, item = (size_t)seq * p.H + h;
+      float S[kCols];
+      {
+        const float *in = args.first ? args.first + item * dd + c : nullptr;
+        const bool col = in && c < p.dv;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) S[x] = col && a0 + x < p.dk ? in[(size_t)(a0 + x) * p.dv] : 0.f;
+      }
+#pragma unroll 1
+      for (int i = 0; i < nc; ++i) {
+        // the state's terms as A operands: lane = column of v, bf16 pairs along dk
+        bf16 *kept = MODE == kOut ? nullptr : args.kept + ((size_t)(slot0 + chunk(i)) * p.H + h) * dd + (size_t)c * p.dk + a0;
+#pragma unroll
+        for (int x = 0; x < kCols; x += 32) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) split2(S[x + 2 * e], S[x + 2 * e + 1], hi[e], lo[e]);
+          tmem_st16_async(pipe::tmem_quad(tmem + kTmS, (a0 + x) / 2), hi);
+          tmem_st16_async(pipe::tmem_quad(tmem + kTmS + 64, (a0 + x) / 2), lo);
+          if (MODE != kOut && c < p.dv) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              if (a0 + x + 2 * e < p.dk)
+                *reinterpret_cast<uint4 *>(kept + x + 2 * e) = make_uint4(hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        pipe::warp_arrive(bar.s_ready);
+        wait_full(i);
+        const float all_hi = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_hi)), all_lo = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_lo));
+        pipe::warp_arrive(&bar.free[i % kStages]);
+        wait_on(bar.w_full, parity(i), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < kCols; x += 16) {
+          float w[16];
+          tmem_ld16(pipe::tmem_quad(tmem + kTmW, a0 + x), w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[x + e] = fmaf(S[x + e], all_hi, fmaf(S[x + e], all_lo, w[e]));
+        }
+        tc_fence_before();
+      }
+      if (args.last && c < p.dv) {
+        float *out = args.last + item * dd + c;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x)
+          if (a0 + x < p.dk) out[(size_t)(a0 + x) * p.dv] = S[x];
+      }
+    }
+  } else if (MODE == kOut) {
+    // ------------------------------------------------------------ outputs
+    const int quad = warp & 3, tt = threadIdx.x - 32 * kOutWarp0;
+    if (quad < 2 * VB) {
+      constexpr int kTeam = 64 * VB;
+      const int fi = 8 * (lane >> 4) + (lane & 7), fc = 32 * quad + 8 * ((lane >> 3) & 1);
+      const uint32_t so = s0 + L::kO, lanes = tmem + ((uint32_t)(32 * quad) << 16);
+#pragma unroll 1
+      for (int i = 0; i < nc; ++i) {
+        wait_full(i);
+        wait_on(bar.q_full, parity(i), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kDrC; j += 32) {  // S^T q by e^G scale / |q|, in place
+          float x[32];
+          tmem_ld32(lanes + kTmO + j, x);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 f = pipe::lds_f4(rows_of(i) + offsetof(DrRows, qin) + (j + e) * 4);
+            x[e] *= f.x, x[e + 1] *= f.y, x[e + 2] *= f.z, x[e + 3] *= f.w;
+          }
+          tmem_st32(lanes + kTmO + j, x);
+        }
+        tc_fence_before();
+        pipe::warp_arrive(bar.q_ready);
+        pipe::warp_arrive(&bar.free[i % kStages]);
+        if (tt == 0) bulk_wait_read0();
+        role_sync<3, kTeam>();
+        wait_on(bar.o_full, parity(i), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t x[32];
+          tmem_ld_16x256_async(lanes + ((uint32_t)(16 * q) << 16) + kTmO, x);
+          tmem_wait_ld32(x);
+          const int c = fc + 16 * q;
+          const uint32_t to = so + (uint32_t)(c >> 6) * kBox + sw128_offset(fi, c & 63);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            uint32_t f[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              f[y] = tc::pack_bf16x2(__uint_as_float(x[4 * e + 2 * y]), __uint_as_float(x[4 * e + 2 * y + 1]));
+            stmatrix4_trans(to + e * 1024, f[0], f[1], f[2], f[3]);
+          }
+        }
+        tc_fence_before();
+        pipe::warp_arrive(bar.o_free);
+        fence_async_smem();
+        role_sync<3, kTeam>();
+        const int nv = live(i);
+        const long long row0 = a + (long long)chunk(i) * kDrC;
+        if (nv < kDrC) {
+          bf16 *out = args.out + row0 * args.os + (size_t)h * p.dv;
+          for (int e = tt; e < nv * 8 * VB; e += kTeam) {
+            const int r = e / (8 * VB), c = 8 * (e % (8 * VB));
+            if (c < p.dv) *reinterpret_cast<uint4 *>(out + r * args.os + c) = pipe::lds_sw128(so + (uint32_t)(c >> 6) * kBox, r, (c & 63) / 8);
+          }
+        } else if (tt == 0) {
+          for (int b = 0; b < VB; ++b)
+            if (64 * b < p.dv) tma_store_3d(&args.o, so + b * kBox, 64 * b, h, (int)row0);
+          bulk_commit();
+        }
+      }
+      if (tt == 0) bulk_wait0();
+    }
+  } else if (kRev) {
+    // ------------------------------------------------------------ the terms of (qin dO)^T
+    const int quad = warp & 3;
+    if (quad < 2 * VB) {
+      const uint32_t lr = (lane & 7) + 8 * (lane >> 4), lc = 4 * (quad & 1) + ((lane >> 3) & 1);
+      const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+#pragma unroll 1
+      for (int i = 0; i < nc; ++i) {
+        wait_full(i);
+        if (i > 0) {
+          wait_on(bar.q_full, parity(i - 1), wait);
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float2 f[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(f[m].x), "=f"(f[m].y)
+                         : "r"(rows_of(i) + (uint32_t)offsetof(DrRows, qin) + (32 * half + 2 * (lane & 3) + 8 * m) * 4));
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[8], t0[8], t1[8];
+            const uint32_t at = s0 + stage(i) + L::kV + (uint32_t)(quad >> 1) * kBox + (32 * half + lr) * 128 +
+                                (((lc + 2 * q) ^ (lane & 7)) * 16);
+            ldmatrix4_trans(at, w[0], w[1], w[2], w[3]);
+            ldmatrix4_trans(at + 16 * 128, w[4], w[5], w[6], w[7]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split2(f[e >> 1].x * lo_f(w[e]), f[e >> 1].y * hi_f(w[e]), t0[e], t1[e]);
+            const uint32_t to = lanes + ((uint32_t)(16 * q) << 16) + kTmD + 16 * half;
+            tmem_st_16x128_async(to, t0);
+            tmem_st_16x128_async(to + 32, t1);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        pipe::warp_arrive(bar.q_ready);
+        pipe::warp_arrive(&bar.free[i % kStages]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmCols);
+  }
+}
+
+template <int KB, int VB, int MODE> void run(Args &args, cudaStream_t s) {
+  using L = Layout<KB, VB, MODE>;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(dr_tc_kernel<KB, VB, MODE>), L::kBytes, allowed);
+  dr_tc_kernel<KB, VB, MODE><<<args.p.nseq * args.p.H, kThreads, L::kBytes, s>>>(args);
+}
+template <int MODE> void run_boxes(Args &args, cudaStream_t s) {
+  const int kb = la_tc_boxes(args.p.dk), vb = la_tc_boxes(args.p.dv);
+  if (kb == 1)
+    vb == 1 ? run<1, 1, MODE>(args, s) : run<1, 2, MODE>(args, s);
+  else
+    vb == 1 ? run<2, 1, MODE>(args, s) : run<2, 2, MODE>(args, s);
+}
+
+// the tensor maps that every chain has; v: its values or dO, with v's heads
+bool fill_args(Args &args, const DrProblem &p, const void *v, long long vs, void *out, long long os) {
+  args.p = p;
+  args.out = static_cast<bf16 *>(out);
+  args.os = os;
+  args.wait = {p.status, p.wait_ns};
+  if (!encode_tmap_bf16_heads(&args.q, p.q, p.dk, p.Hk, p.total, p.qs * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&args.k, p.k, p.dk, p.Hk, p.total, p.ks * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&args.v, v, p.dv, p.H, p.total, vs * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&args.o, out, p.dv, p.H, p.total, os * 2, kDrC)) {
+    note_host_error();
+    return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+void launch_dr_tc_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s) {
+  Args args;
+  const long long es = (long long)p.H * p.dv;
+  if (!fill_args(args, p, p.v, p.vs, o ? o : p.E, o ? os : es)) return;
+  args.first = p.init;
+  args.last = o ? fin : nullptr;
+  args.kept = reinterpret_cast<bf16 *>(p.S);
+  o ? run_boxes<kOut>(args, s) : run_boxes<kStates>(args, s);
+}
+
+void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s) {
+  Args args;
+  if (!fill_args(args, p, dout, dos, p.Z, (long long)p.H * p.dv)) return;
+  args.first = dfin;
+  args.last = dinit;
+  args.kept = reinterpret_cast<bf16 *>(p.dS);
+  run_boxes<kReverse>(args, s);
+}
+
+}  // namespace ssd
