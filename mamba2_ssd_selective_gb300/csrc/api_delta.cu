@@ -134,7 +134,7 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
 
 template <typename T>
 ssd_status dr_forward_impl(const DrProblem &p, bool tc, void *o, int64_t os, float *fin, cudaStream_t s) {
-  SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, tc, s));
+  SSD_LAUNCH("dr_prep", tc ? launch_dr_prep_tc(p, false, s) : launch_dr_prep<T>(p, s));
   SSD_LAUNCH("dr_chain", tc ? launch_dr_tc_chain(p, o, os, fin, s) : launch_dr_chain<T>(p, o, os, fin, s));
   return launch_status();
 }
@@ -144,7 +144,7 @@ ssd_status dr_backward_impl(const DrProblem &p, const void *dout, int64_t dos, c
                             const ssd_delta_rule_grads *g, cudaStream_t s) {
   const DrGrads out{g->dq, g->dk, g->dv, g->dlog_decay, g->dbeta, g->dq_tok_stride, g->dk_tok_stride, g->dv_tok_stride,
                     g->dlog_decay_tok_stride, g->dbeta_tok_stride};
-  SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, false, s));
+  SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, s));
   SSD_LAUNCH("dr_chain", launch_dr_chain<T>(p, nullptr, 0, nullptr, s));
   SSD_LAUNCH("dr_reverse", launch_dr_reverse<T>(p, dout, dos, dfin, g->dinitial_states, s));
   SSD_LAUNCH("dr_grads", launch_dr_grads<T>(p, dout, dos, out, s));

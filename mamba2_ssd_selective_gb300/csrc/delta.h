@@ -99,8 +99,10 @@ __device__ __forceinline__ void dr_chunk(const DrProblem &p, int slot, int &t0, 
   n = off < 0 || off >= len ? 0 : min(kDrC, len - (int)off);
 }
 
-// dr_prep.cu: rows' factors, N and P of every chunk; tc: for the tensor-core chains
-template <typename T> void launch_dr_prep(const DrProblem &p, bool tc, cudaStream_t s);
+// dr_prep.cu: rows' factors, N and P of every chunk
+template <typename T> void launch_dr_prep(const DrProblem &p, cudaStream_t s);
+// dr_prep_tc.cu: the same for the tensor-core chains (P's second term for backward only)
+void launch_dr_prep_tc(const DrProblem &p, bool backward, cudaStream_t s);
 // dr_tc.cu: the chains for bf16, both widths at most 128
 void launch_dr_tc_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);
 void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s);

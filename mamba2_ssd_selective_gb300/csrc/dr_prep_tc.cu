@@ -1,0 +1,265 @@
+// What the tensor-core chains of the gated delta rule need of every chunk before the state is known: the rows' factors, and
+// N and P as tiles of two bf16 terms (delta.h has the formulas).
+//
+// A block takes a chunk and a head of q and k; K K^T and Q K^T serve every state that shares the head and stay in
+// registers.  Four warps make A and N, the other four make P meanwhile.
+// N = (I + A diag(b))^-1 A in blocks, without a division by b: diagonal blocks of 16 column by column, a thread to a
+// column, then twice the block below two that are done (b1, b2: theirs),
+//     N21 = M - N22 (b2 M),   M = A21 - A21 (b1 N11),
+// in place, since A's blocks are not read again.  Sums of log decays are whole numbers of 2^-32 (dr_rows.cuh).
+#include "delta.h"
+#include "dr_rows.cuh"
+#include "tc_pipe.cuh"
+#include "tc_util.cuh"
+
+namespace ssd {
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+using namespace sm100;
+
+constexpr int kThreads = 256, kLd = kDrC + 4;
+constexpr uint32_t kBox = 8192;
+
+struct Work {
+  float m[kDrC][kLd];  // A, then N
+  DrRows rows;
+  float rk[kDrC], rq[kDrC];
+  int nan_at;
+  uint64_t full;
+};
+template <int KB> constexpr int smem_bytes() { return (KB == 1 ? 4 : 2 * KB) * (int)kBox + (int)sizeof(Work) + 1024; }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float square_sum(uint32_t w) {
+  const float x = __uint_as_float(w << 16), y = __uint_as_float(w & 0xffff0000u);
+  return fmaf(x, x, y * y);
+}
+template <int ID> __device__ __forceinline__ void half_sync() { asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory"); }
+
+// x[r][c] -= sum_k A[r][k] b[k] B[k][c]: ROWS x 2 values a thread, from rows A and B of the matrix
+template <int K, int ROWS>
+__device__ __forceinline__ void minus_product(float (&x)[ROWS][2], const float *A, const float *b, const float *B) {
+#pragma unroll
+  for (int k = 0; k < K; k += 4) {
+    const float4 bb = *reinterpret_cast<const float4 *>(b + k);
+    float2 y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const float2 *>(B + (k + e) * kLd);
+    y[0].x *= -bb.x, y[0].y *= -bb.x, y[1].x *= -bb.y, y[1].y *= -bb.y;
+    y[2].x *= -bb.z, y[2].y *= -bb.z, y[3].x *= -bb.w, y[3].y *= -bb.w;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const float4 a = *reinterpret_cast<const float4 *>(A + r * kLd + k);
+      x[r][0] = fmaf(a.x, y[0].x, fmaf(a.y, y[1].x, fmaf(a.z, y[2].x, fmaf(a.w, y[3].x, x[r][0]))));
+      x[r][1] = fmaf(a.x, y[0].y, fmaf(a.y, y[1].y, fmaf(a.z, y[2].y, fmaf(a.w, y[3].y, x[r][1]))));
+    }
+  }
+}
+// the block below two done ones: rows [at + S, at + 2S), columns [at, at + S); the thread has ROWS rows from r, columns c, c + 1
+template <int S, int ROWS> __device__ __forceinline__ void below(Work &w, int at, int r, int c) {
+  float x[ROWS][2];
+  const int row = at + S + r, col = at + c;
+  auto put = [&] {
+#pragma unroll
+    for (int e = 0; e < ROWS; ++e) *reinterpret_cast<float2 *>(&w.m[row + e][col]) = make_float2(x[e][0], x[e][1]);
+  };
+#pragma unroll
+  for (int e = 0; e < ROWS; ++e) {
+    const float2 t = *reinterpret_cast<const float2 *>(&w.m[row + e][col]);
+    x[e][0] = t.x, x[e][1] = t.y;
+  }
+  minus_product<S, ROWS>(x, &w.m[row][at], w.rows.beta + at, &w.m[at][col]);
+  half_sync<1>();
+  put();
+  half_sync<1>();
+  minus_product<S, ROWS>(x, &w.m[row][at + S], w.rows.beta + at + S, &w.m[at + S][col]);
+  half_sync<1>();
+  put();
+  half_sync<1>();
+}
+
+// a pair of values of a row, as two terms, into a tile and the one behind it
+__device__ __forceinline__ void put_terms(uint32_t tile, int i, int j, float x, float y) {
+  const uint32_t hi = tc::pack_bf16x2(x, y);
+  const uint32_t lo = tc::pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+  const uint32_t at = tile + sw128_offset(i, j);
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hi) : "memory");
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + kBox), "r"(lo) : "memory");
+}
+
+// NP: tiles that go out, N's two terms and one or two of P
+template <int KB, int NP>
+__global__ void __launch_bounds__(kThreads, 3) dr_prep_tc_kernel(const __grid_constant__ CUtensorMap tq,
+                                                                   const __grid_constant__ CUtensorMap tk, const DrProblem p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = tc::aligned_smem(smem_raw);
+  // K's and Q's boxes, and once their products are made, the tiles on their way out
+  Work &w = *reinterpret_cast<Work *>(sm + (KB == 1 ? 4 : 2 * KB) * kBox);
+  const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (slot == 0 && hk == 0 && tid == 0) *p.status = 0;
+  int t0, n;
+  dr_chunk(p, slot, t0, n);
+  if (n == 0) return;
+  const uint32_t s0 = smem_u32(sm);
+  if (tid == 0) {
+    mbar_init(&w.full, 1);
+    fence_mbar_init();
+    mbar_expect_tx(&w.full, 2 * KB * kBox);
+    for (int b = 0; b < KB; ++b) {
+      tma_load_3d(sm + b * kBox, &tk, &w.full, 64 * b, hk, t0);
+      tma_load_3d(sm + (KB + b) * kBox, &tq, &w.full, 64 * b, hk, t0);
+    }
+  }
+  __syncthreads();
+  mbar_wait_drain(&w.full, 0);
+  // rows 16 (warp % 4) on of K K^T (warps 0-3) or Q K^T: columns 8 y + 2 (lane % 4), rows lane / 4 and 8 more
+  const bool is_q = warp >= 4;
+  const int i0 = 16 * (warp & 3);
+  float acc[8][4], qq[2] = {0.f, 0.f};
+#pragma unroll
+  for (int y = 0; y < 8; ++y) acc[y][0] = acc[y][1] = acc[y][2] = acc[y][3] = 0.f;
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+    const uint32_t ta = s0 + ((is_q ? KB : 0) + b) * kBox, tb = s0 + b * kBox;
+#pragma unroll
+    for (int kk = 0; kk < 64; kk += 16) {
+      uint32_t fa[4];
+      ldmatrix4(ta + sw128_offset(i0 + (lane & 15), kk + 8 * (lane >> 4)), fa);
+      qq[0] += square_sum(fa[0]) + square_sum(fa[2]);
+      qq[1] += square_sum(fa[1]) + square_sum(fa[3]);
+#pragma unroll
+      for (int y = 0; y < 8; y += 2) {
+        if (8 * y > i0 + 15) continue;  // above the diagonal
+        uint32_t fb[4];
+        ldmatrix4(tb + sw128_offset(8 * y + (lane & 7) + 8 * (lane >> 4), kk + 8 * ((lane >> 3) & 1)), fb);
+        mma16816(acc[y], fa, fb[0], fb[1]);
+        mma16816(acc[y + 1], fa, fb[2], fb[3]);
+      }
+    }
+  }
+  const int r0 = i0 + (lane >> 2), c0 = 2 * (lane & 3);  // the thread's values: rows r0, r0 + 8, columns 8 y + c0 and the next
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {  // squared lengths, K's from the same sums
+    qq[e] += __shfl_xor_sync(0xffffffffu, qq[e], 1);
+    qq[e] += __shfl_xor_sync(0xffffffffu, qq[e], 2);
+    if ((lane & 3) == 0) (is_q ? w.rq : w.rk)[r0 + 8 * e] = p.norm ? 1.f / sqrtf(qq[e] + p.eps) : 1.f;
+  }
+  bool sent = false;
+  for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
+    if (sent && tid == 0) bulk_wait_read0();
+    __syncthreads();
+    if (warp == 0) dr_fill_rows<bf16>(p, w.rows, w.rk, w.rq, w.nan_at, h, t0, n, lane);
+    __syncthreads();
+    const float nan = __int_as_float(0x7fffffff);
+    const int nan_at = w.nan_at;
+    // e^(G_i - G_j) / |.| / |k_j| of the thread's values
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = r0 + 8 * e;
+      const float hi = w.rows.ghi[i], lo = w.rows.glo[i], ri = is_q ? w.rows.rq[i] * p.scale : w.rows.rk[i];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const int j = 8 * y + c0;
+        float v[2] = {0.f, 0.f};
+        if (8 * y <= i0 + 15) {
+          const float2 gh = *reinterpret_cast<const float2 *>(w.rows.ghi + j), gl = *reinterpret_cast<const float2 *>(w.rows.glo + j),
+                       rk = *reinterpret_cast<const float2 *>(w.rows.rk + j);
+          v[0] = __expf((hi - gh.x) + (lo - gl.x)) * acc[y][2 * e] * (ri * rk.x);
+          v[1] = __expf((hi - gh.y) + (lo - gl.y)) * acc[y][2 * e + 1] * (ri * rk.y);
+          const int last = is_q ? i : i - 1;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (i >= nan_at && j + x < nan_at) v[x] = nan;
+            if (j + x > last || i >= n) v[x] = 0.f;
+          }
+        }
+        if (is_q) {
+          if (NP == 4)
+            put_terms(s0 + 2 * kBox, i, j, v[0], v[1]);
+          else
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(s0 + 2 * kBox + sw128_offset(i, j)), "r"(tc::pack_bf16x2(v[0], v[1])) : "memory");
+        } else {
+          *reinterpret_cast<float2 *>(&w.m[i][j]) = make_float2(v[0], v[1]);
+        }
+      }
+    }
+    const size_t at = (size_t)slot * p.H + h;
+    if (is_q) {
+      const float4 *from = reinterpret_cast<const float4 *>(&w.rows);
+      float4 *to = reinterpret_cast<float4 *>(p.rows + at);
+      for (int e = tid - 128; e < (int)(sizeof(DrRows) / 16); e += 128) to[e] = from[e];
+    } else {
+      half_sync<1>();
+      float x[16];
+      const int d0 = tid & 48, c = tid & 15;  // column c of the diagonal block from d0
+      if (tid < kDrC) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = w.m[d0 + i][d0 + c];  // zeros up to the diagonal
+#pragma unroll
+        for (int m = 1; m < 15; ++m) {
+          const float f = -w.rows.beta[d0 + m] * x[m];
+#pragma unroll
+          for (int i = m + 1; i < 16; ++i) x[i] = fmaf(f, w.m[d0 + i][d0 + m], x[i]);
+        }
+      }
+      half_sync<1>();
+      if (tid < kDrC) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) w.m[d0 + i][d0 + c] = x[i];
+      }
+      half_sync<1>();
+      below<16, 2>(w, tid >> 6 ? 32 : 0, 2 * ((tid & 63) >> 3), 2 * (tid & 7));
+      below<32, 4>(w, 0, 4 * (tid >> 4), 2 * (tid & 15));
+      for (int e = tid; e < kDrC * kDrC / 2; e += 128) {
+        const int i = e >> 5, j = 2 * (e & 31);
+        const float2 v = *reinterpret_cast<const float2 *>(&w.m[i][j]);
+        put_terms(s0, i, j, v.x, v.y);
+      }
+    }
+    fence_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      pipe::bulk_store(reinterpret_cast<uint8_t *>(p.N) + at * (4 * kDrTile), s0, NP * kBox);
+      bulk_commit();
+    }
+    sent = true;
+  }
+  if (tid == 0) bulk_wait0();
+}
+
+template <int KB, int NP> void run(const DrProblem &p, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  constexpr int bytes = smem_bytes<KB>();
+  allow_smem(reinterpret_cast<const void *>(dr_prep_tc_kernel<KB, NP>), bytes, allowed);
+  CUtensorMap tq, tk;
+  if (!encode_tmap_bf16_heads(&tq, p.q, p.dk, p.Hk, p.total, p.qs * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&tk, p.k, p.dk, p.Hk, p.total, p.ks * 2, kDrC)) {
+    note_host_error();
+    return;
+  }
+  dr_prep_tc_kernel<KB, NP><<<dim3((unsigned)p.slots, (unsigned)p.Hk), kThreads, bytes, s>>>(tq, tk, p);
+}
+
+}  // namespace
+
+void launch_dr_prep_tc(const DrProblem &p, bool backward, cudaStream_t s) {
+  if (la_tc_boxes(p.dk) == 1)
+    backward ? run<1, 4>(p, s) : run<1, 3>(p, s);
+  else
+    backward ? run<2, 4>(p, s) : run<2, 3>(p, s);
+}
+
+}  // namespace ssd

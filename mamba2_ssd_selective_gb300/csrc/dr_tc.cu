@@ -252,8 +252,11 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
             tc_fence_after();
           }
 #pragma unroll
-          for (int b = 0; b < KB; ++b)
-            pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmS + 32 * b, dQ + at(i) + b * kB, 8, pipe::kStepK, iKK, b > 0);
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+              pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmS + 64 * t + 32 * b, dQ + at(i) + b * kB, 8, pipe::kStepK, iKK,
+                                    t + b > 0);
           umma_commit_el(el, bar.q_full);
         }
         if (kRev) {

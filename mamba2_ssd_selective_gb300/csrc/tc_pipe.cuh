@@ -28,6 +28,11 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                : "memory");
 }
 
+// and back, tracked by the issuing thread's bulk async-group
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ uint32_t parity(uint32_t m) { return m & 1u; }
 
 // explicit shared-memory accesses (32-bit shared addresses)
