@@ -63,7 +63,11 @@ __global__ void __launch_bounds__(kThreads) dr_prep_kernel(DrProblem p) {
   }
   for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
     __syncthreads();
-    if (tid < 32) dr_fill_rows<T>(p, sm.rows, sm.rk, sm.rq, sm.nan_at, h, t0, n, tid);
+    if (tid < 32) {
+      const DrSums sums = dr_sums<T>(p, h, t0, n, tid);
+      dr_put_rows(sm.rows, sums, sm.rk, sm.rq, p.scale, n, tid);
+      if (tid == 0) sm.nan_at = sums.first_nan;
+    }
     __syncthreads();
     const size_t at = (size_t)slot * p.H + h;
     const float nan = __int_as_float(0x7fffffff);

@@ -1,8 +1,8 @@
 // What the tensor-core chains of the gated delta rule need of every chunk before the state is known: the rows' factors, and
 // N and P as tiles of two bf16 terms (delta.h has the formulas).
 //
-// A block takes a chunk and a head of q and k; K K^T and Q K^T serve every state that shares the head and stay in
-// registers.  Four warps make A and N, the other four make P meanwhile.
+// A block of four warps takes a chunk and a state head: K K^T and Q K^T by matrix instructions, a warp's 16 rows of both in its
+// registers, so that A and P share their exponentials.
 // N = (I + A diag(b))^-1 A in blocks, without a division by b: diagonal blocks of 16 column by column, a thread to a
 // column, then twice the block below two that are done (b1, b2: theirs),
 //     N21 = M - N22 (b2 M),   M = A21 - A21 (b1 N11),
@@ -19,7 +19,7 @@ namespace {
 using bf16 = __nv_bfloat16;
 using namespace sm100;
 
-constexpr int kThreads = 256, kLd = kDrC + 4;
+constexpr int kThreads = 128, kLd = kDrC + 4;
 constexpr uint32_t kBox = 8192;
 
 struct Work {
@@ -47,13 +47,11 @@ __device__ __forceinline__ float square_sum(uint32_t w) {
   const float x = __uint_as_float(w << 16), y = __uint_as_float(w & 0xffff0000u);
   return fmaf(x, x, y * y);
 }
-template <int ID> __device__ __forceinline__ void half_sync() { asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory"); }
-
-// x[r][c] -= sum_k A[r][k] b[k] B[k][c]: ROWS x 2 values a thread, from rows A and B of the matrix
-template <int K, int ROWS>
-__device__ __forceinline__ void minus_product(float (&x)[ROWS][2], const float *A, const float *b, const float *B) {
-#pragma unroll
-  for (int k = 0; k < K; k += 4) {
+// x[r][c] -= sum_k A[r][k] b[k] B[k][c], k from k0 to k1: ROWS rows STEP apart x 2 values a thread
+template <int ROWS, int STEP>
+__device__ __forceinline__ void minus_product(float (&x)[ROWS][2], const float *A, const float *b, const float *B, int k0, int k1) {
+#pragma unroll 2
+  for (int k = k0; k < k1; k += 4) {
     const float4 bb = *reinterpret_cast<const float4 *>(b + k);
     float2 y[4];
 #pragma unroll
@@ -62,33 +60,22 @@ __device__ __forceinline__ void minus_product(float (&x)[ROWS][2], const float *
     y[2].x *= -bb.z, y[2].y *= -bb.z, y[3].x *= -bb.w, y[3].y *= -bb.w;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const float4 a = *reinterpret_cast<const float4 *>(A + r * kLd + k);
+      const float4 a = *reinterpret_cast<const float4 *>(A + r * STEP * kLd + k);
       x[r][0] = fmaf(a.x, y[0].x, fmaf(a.y, y[1].x, fmaf(a.z, y[2].x, fmaf(a.w, y[3].x, x[r][0]))));
       x[r][1] = fmaf(a.x, y[0].y, fmaf(a.y, y[1].y, fmaf(a.z, y[2].y, fmaf(a.w, y[3].y, x[r][1]))));
     }
   }
 }
-// the block below two done ones: rows [at + S, at + 2S), columns [at, at + S); the thread has ROWS rows from r, columns c, c + 1
-template <int S, int ROWS> __device__ __forceinline__ void below(Work &w, int at, int r, int c) {
-  float x[ROWS][2];
-  const int row = at + S + r, col = at + c;
-  auto put = [&] {
-#pragma unroll
-    for (int e = 0; e < ROWS; ++e) *reinterpret_cast<float2 *>(&w.m[row + e][col]) = make_float2(x[e][0], x[e][1]);
-  };
+template <int ROWS, int STEP> __device__ __forceinline__ void get(float (&x)[ROWS][2], const float *m) {
 #pragma unroll
   for (int e = 0; e < ROWS; ++e) {
-    const float2 t = *reinterpret_cast<const float2 *>(&w.m[row + e][col]);
+    const float2 t = *reinterpret_cast<const float2 *>(m + e * STEP * kLd);
     x[e][0] = t.x, x[e][1] = t.y;
   }
-  minus_product<S, ROWS>(x, &w.m[row][at], w.rows.beta + at, &w.m[at][col]);
-  half_sync<1>();
-  put();
-  half_sync<1>();
-  minus_product<S, ROWS>(x, &w.m[row][at + S], w.rows.beta + at + S, &w.m[at + S][col]);
-  half_sync<1>();
-  put();
-  half_sync<1>();
+}
+template <int ROWS, int STEP> __device__ __forceinline__ void put(const float (&x)[ROWS][2], float *m) {
+#pragma unroll
+  for (int e = 0; e < ROWS; ++e) *reinterpret_cast<float2 *>(m + e * STEP * kLd) = make_float2(x[e][0], x[e][1]);
 }
 
 // a pair of values of a row, as two terms, into a tile and the one behind it
@@ -102,14 +89,14 @@ __device__ __forceinline__ void put_terms(uint32_t tile, int i, int j, float x, 
 
 // NP: tiles that go out, N's two terms and one or two of P
 template <int KB, int NP>
-__global__ void __launch_bounds__(kThreads, 3) dr_prep_tc_kernel(const __grid_constant__ CUtensorMap tq,
-                                                                   const __grid_constant__ CUtensorMap tk, const DrProblem p) {
+__global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_constant__ CUtensorMap tq,
+                                                                 const __grid_constant__ CUtensorMap tk, const DrProblem p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = tc::aligned_smem(smem_raw);
   // K's and Q's boxes, and once their products are made, the tiles on their way out
   Work &w = *reinterpret_cast<Work *>(sm + (KB == 1 ? 4 : 2 * KB) * kBox);
-  const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (slot == 0 && hk == 0 && tid == 0) *p.status = 0;
+  const int slot = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (slot == 0 && h == 0 && tid == 0) *p.status = 0;
   int t0, n;
   dr_chunk(p, slot, t0, n);
   if (n == 0) return;
@@ -119,125 +106,164 @@ __global__ void __launch_bounds__(kThreads, 3) dr_prep_tc_kernel(const __grid_co
     fence_mbar_init();
     mbar_expect_tx(&w.full, 2 * KB * kBox);
     for (int b = 0; b < KB; ++b) {
-      tma_load_3d(sm + b * kBox, &tk, &w.full, 64 * b, hk, t0);
-      tma_load_3d(sm + (KB + b) * kBox, &tq, &w.full, 64 * b, hk, t0);
+      tma_load_3d(sm + b * kBox, &tk, &w.full, 64 * b, h / p.group, t0);
+      tma_load_3d(sm + (KB + b) * kBox, &tq, &w.full, 64 * b, h / p.group, t0);
     }
   }
+  DrSums sums;
+  if (warp == 0) sums = dr_sums<bf16>(p, h, t0, n, lane);
   __syncthreads();
   mbar_wait_drain(&w.full, 0);
-  // rows 16 (warp % 4) on of K K^T (warps 0-3) or Q K^T: columns 8 y + 2 (lane % 4), rows lane / 4 and 8 more
-  const bool is_q = warp >= 4;
-  const int i0 = 16 * (warp & 3);
-  float acc[8][4], qq[2] = {0.f, 0.f};
+  // rows i0 on of both products: columns 8 y + 2 (lane % 4) and the next, rows lane / 4 and 8 more
+  const int i0 = 16 * warp;
+  float kk[8][4], qk[8][4], len[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int y = 0; y < 8; ++y) acc[y][0] = acc[y][1] = acc[y][2] = acc[y][3] = 0.f;
+  for (int y = 0; y < 8; ++y)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) kk[y][e] = qk[y][e] = 0.f;
 #pragma unroll
   for (int b = 0; b < KB; ++b) {
-    const uint32_t ta = s0 + ((is_q ? KB : 0) + b) * kBox, tb = s0 + b * kBox;
+    const uint32_t tb = s0 + b * kBox, ta = s0 + (KB + b) * kBox;
 #pragma unroll
-    for (int kk = 0; kk < 64; kk += 16) {
-      uint32_t fa[4];
-      ldmatrix4(ta + sw128_offset(i0 + (lane & 15), kk + 8 * (lane >> 4)), fa);
-      qq[0] += square_sum(fa[0]) + square_sum(fa[2]);
-      qq[1] += square_sum(fa[1]) + square_sum(fa[3]);
+    for (int c = 0; c < 64; c += 16) {
+      uint32_t fk[4], fq[4];
+      ldmatrix4(tb + sw128_offset(i0 + (lane & 15), c + 8 * (lane >> 4)), fk);
+      ldmatrix4(ta + sw128_offset(i0 + (lane & 15), c + 8 * (lane >> 4)), fq);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        len[e] += square_sum(fk[e]) + square_sum(fk[e + 2]);
+        len[2 + e] += square_sum(fq[e]) + square_sum(fq[e + 2]);
+      }
 #pragma unroll
       for (int y = 0; y < 8; y += 2) {
         if (8 * y > i0 + 15) continue;  // above the diagonal
         uint32_t fb[4];
-        ldmatrix4(tb + sw128_offset(8 * y + (lane & 7) + 8 * (lane >> 4), kk + 8 * ((lane >> 3) & 1)), fb);
-        mma16816(acc[y], fa, fb[0], fb[1]);
-        mma16816(acc[y + 1], fa, fb[2], fb[3]);
+        ldmatrix4(tb + sw128_offset(8 * y + (lane & 7) + 8 * (lane >> 4), c + 8 * ((lane >> 3) & 1)), fb);
+        mma16816(kk[y], fk, fb[0], fb[1]);
+        mma16816(kk[y + 1], fk, fb[2], fb[3]);
+        mma16816(qk[y], fq, fb[0], fb[1]);
+        mma16816(qk[y + 1], fq, fb[2], fb[3]);
       }
     }
   }
-  const int r0 = i0 + (lane >> 2), c0 = 2 * (lane & 3);  // the thread's values: rows r0, r0 + 8, columns 8 y + c0 and the next
+  const int r0 = i0 + (lane >> 2), c0 = 2 * (lane & 3);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {  // squared lengths, K's from the same sums
-    qq[e] += __shfl_xor_sync(0xffffffffu, qq[e], 1);
-    qq[e] += __shfl_xor_sync(0xffffffffu, qq[e], 2);
-    if ((lane & 3) == 0) (is_q ? w.rq : w.rk)[r0 + 8 * e] = p.norm ? 1.f / sqrtf(qq[e] + p.eps) : 1.f;
+  for (int e = 0; e < 4; ++e) {
+    len[e] += __shfl_xor_sync(0xffffffffu, len[e], 1);
+    len[e] += __shfl_xor_sync(0xffffffffu, len[e], 2);
+    if ((lane & 3) == 0) (e < 2 ? w.rk : w.rq)[r0 + 8 * (e & 1)] = p.norm ? 1.f / sqrtf(len[e] + p.eps) : 1.f;
   }
-  bool sent = false;
-  for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
-    if (sent && tid == 0) bulk_wait_read0();
-    __syncthreads();
-    if (warp == 0) dr_fill_rows<bf16>(p, w.rows, w.rk, w.rq, w.nan_at, h, t0, n, lane);
-    __syncthreads();
-    const float nan = __int_as_float(0x7fffffff);
-    const int nan_at = w.nan_at;
-    // e^(G_i - G_j) / |.| / |k_j| of the thread's values
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = r0 + 8 * e;
-      const float hi = w.rows.ghi[i], lo = w.rows.glo[i], ri = is_q ? w.rows.rq[i] * p.scale : w.rows.rk[i];
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const int j = 8 * y + c0;
-        float v[2] = {0.f, 0.f};
-        if (8 * y <= i0 + 15) {
-          const float2 gh = *reinterpret_cast<const float2 *>(w.rows.ghi + j), gl = *reinterpret_cast<const float2 *>(w.rows.glo + j),
-                       rk = *reinterpret_cast<const float2 *>(w.rows.rk + j);
-          v[0] = __expf((hi - gh.x) + (lo - gl.x)) * acc[y][2 * e] * (ri * rk.x);
-          v[1] = __expf((hi - gh.y) + (lo - gl.y)) * acc[y][2 * e + 1] * (ri * rk.y);
-          const int last = is_q ? i : i - 1;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (i >= nan_at && j + x < nan_at) v[x] = nan;
-            if (j + x > last || i >= n) v[x] = 0.f;
-          }
-        }
-        if (is_q) {
-          if (NP == 4)
-            put_terms(s0 + 2 * kBox, i, j, v[0], v[1]);
-          else
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(s0 + 2 * kBox + sw128_offset(i, j)), "r"(tc::pack_bf16x2(v[0], v[1])) : "memory");
-        } else {
-          *reinterpret_cast<float2 *>(&w.m[i][j]) = make_float2(v[0], v[1]);
-        }
-      }
-    }
-    const size_t at = (size_t)slot * p.H + h;
-    if (is_q) {
-      const float4 *from = reinterpret_cast<const float4 *>(&w.rows);
-      float4 *to = reinterpret_cast<float4 *>(p.rows + at);
-      for (int e = tid - 128; e < (int)(sizeof(DrRows) / 16); e += 128) to[e] = from[e];
-    } else {
-      half_sync<1>();
-      float x[16];
-      const int d0 = tid & 48, c = tid & 15;  // column c of the diagonal block from d0
-      if (tid < kDrC) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = w.m[d0 + i][d0 + c];  // zeros up to the diagonal
-#pragma unroll
-        for (int m = 1; m < 15; ++m) {
-          const float f = -w.rows.beta[d0 + m] * x[m];
-#pragma unroll
-          for (int i = m + 1; i < 16; ++i) x[i] = fmaf(f, w.m[d0 + i][d0 + m], x[i]);
-        }
-      }
-      half_sync<1>();
-      if (tid < kDrC) {
-#pragma unroll
-        for (int i = 1; i < 16; ++i) w.m[d0 + i][d0 + c] = x[i];
-      }
-      half_sync<1>();
-      below<16, 2>(w, tid >> 6 ? 32 : 0, 2 * ((tid & 63) >> 3), 2 * (tid & 7));
-      below<32, 4>(w, 0, 4 * (tid >> 4), 2 * (tid & 15));
-      for (int e = tid; e < kDrC * kDrC / 2; e += 128) {
-        const int i = e >> 5, j = 2 * (e & 31);
-        const float2 v = *reinterpret_cast<const float2 *>(&w.m[i][j]);
-        put_terms(s0, i, j, v.x, v.y);
-      }
-    }
-    fence_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      pipe::bulk_store(reinterpret_cast<uint8_t *>(p.N) + at * (4 * kDrTile), s0, NP * kBox);
-      bulk_commit();
-    }
-    sent = true;
+  __syncthreads();
+  if (warp == 0) {
+    dr_put_rows(w.rows, sums, w.rk, w.rq, p.scale, n, lane);
+    if (lane == 0) w.nan_at = sums.first_nan;
   }
-  if (tid == 0) bulk_wait0();
+  __syncthreads();
+  const int nan_at = w.nan_at;
+  const size_t at = (size_t)slot * p.H + h;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = r0 + 8 * e;
+    const float hi = w.rows.ghi[i], lo = w.rows.glo[i], rk = w.rows.rk[i], rq = w.rows.rq[i] * p.scale;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const int j = 8 * y + c0;
+      float a[2] = {0.f, 0.f}, q[2] = {0.f, 0.f};
+      if (8 * y <= i0 + 15 && i < n) {
+        const float2 gh = *reinterpret_cast<const float2 *>(w.rows.ghi + j), gl = *reinterpret_cast<const float2 *>(w.rows.glo + j),
+                     rj = *reinterpret_cast<const float2 *>(w.rows.rk + j);
+        float l[2] = {__expf((hi - gh.x) + (lo - gl.x)) * rj.x, __expf((hi - gh.y) + (lo - gl.y)) * rj.y};
+        if (nan_at < kDrC && i >= nan_at) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (j + x < nan_at) l[x] = __int_as_float(0x7fffffff);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          a[x] = kk[y][2 * e + x] * (l[x] * rk);
+          q[x] = qk[y][2 * e + x] * (l[x] * rq);
+        }
+        if (8 * y + 7 >= i0) {  // the diagonal crosses the warp's rows here
+          a[0] = j < i ? a[0] : 0.f, a[1] = j + 1 < i ? a[1] : 0.f;
+          q[0] = j <= i ? q[0] : 0.f, q[1] = j + 1 <= i ? q[1] : 0.f;
+        }
+      }
+      *reinterpret_cast<float2 *>(&w.m[i][j]) = make_float2(a[0], a[1]);
+      if (NP == 4)
+        put_terms(s0 + 2 * kBox, i, j, q[0], q[1]);
+      else
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(s0 + 2 * kBox + sw128_offset(i, j)), "r"(tc::pack_bf16x2(q[0], q[1])) : "memory");
+    }
+  }
+  {
+    const float4 *from = reinterpret_cast<const float4 *>(&w.rows);
+    float4 *to = reinterpret_cast<float4 *>(p.rows + at);
+    for (int e = tid; e < (int)(sizeof(DrRows) / 16); e += kThreads) to[e] = from[e];
+  }
+  __syncthreads();
+  {
+    float x[16];
+    const int d0 = tid & 48, c = tid & 15;  // column c of the diagonal block from d0
+    if (tid < kDrC) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = w.m[d0 + i][d0 + c];  // zeros up to the diagonal
+#pragma unroll
+      for (int m = 1; m < 15; ++m) {
+        const float f = -w.rows.beta[d0 + m] * x[m];
+#pragma unroll
+        for (int i = m + 1; i < 16; ++i) x[i] = fmaf(f, w.m[d0 + i][d0 + m], x[i]);
+      }
+      // a block is one half-warp's
+      __syncwarp();
+#pragma unroll
+      for (int i = 1; i < 16; ++i) w.m[d0 + i][d0 + c] = x[i];
+    }
+  }
+  __syncthreads();
+  {  // two blocks of 16 x 16, a half of the threads each: 2 x 2 values a thread
+    const int d0 = tid >> 6 ? 32 : 0, r = 2 * ((tid & 63) >> 3), c = 2 * (tid & 7);
+    float x[2][2], *mine = &w.m[d0 + 16 + r][d0 + c];
+    get<2, 1>(x, mine);
+    minus_product<2, 1>(x, &w.m[d0 + 16 + r][d0], w.rows.beta + d0, &w.m[d0][d0 + c], 0, 16);
+    __syncthreads();
+    put<2, 1>(x, mine);
+    __syncthreads();
+    minus_product<2, 1>(x, &w.m[d0 + 16 + r][d0 + 16], w.rows.beta + d0 + 16, &w.m[d0 + 16][d0 + c], 0, 16);
+    __syncthreads();
+    put<2, 1>(x, mine);
+  }
+  __syncthreads();
+  {  // 32 x 32: 8 values a thread.  N11 has zeros up to its diagonal, so a warp's 8 columns leave the sum's first terms out
+    const int r = lane & 7, c = 8 * warp + 2 * (lane >> 3);
+    float x[4][2];
+    get<4, 8>(x, &w.m[32 + r][c]);
+    minus_product<4, 8>(x, &w.m[32 + r][0], w.rows.beta, &w.m[0][c], 8 * warp, 32);
+    __syncthreads();
+    put<4, 8>(x, &w.m[32 + r][c]);
+  }
+  __syncthreads();
+  {  // and N22 from it, so that a warp's 8 rows leave out the last
+    const int r = 8 * warp + 4 * (lane >> 4), c = 2 * (lane & 15);
+    float x[4][2];
+    get<4, 1>(x, &w.m[32 + r][c]);
+    minus_product<4, 1>(x, &w.m[32 + r][32], w.rows.beta + 32, &w.m[32][c], 0, 8 * warp + 8);
+    __syncthreads();
+    put<4, 1>(x, &w.m[32 + r][c]);
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int e = tid; e < kDrC * kDrC / 2; e += kThreads) {
+    const int i = e >> 5, j = 2 * (e & 31);
+    const float2 v = *reinterpret_cast<const float2 *>(&w.m[i][j]);
+    put_terms(s0, i, j, v.x, v.y);
+  }
+  fence_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    pipe::bulk_store(reinterpret_cast<uint8_t *>(p.N) + at * (4 * kDrTile), s0, NP * kBox);
+    bulk_commit();
+    bulk_wait0();
+  }
 }
 
 template <int KB, int NP> void run(const DrProblem &p, cudaStream_t s) {
@@ -250,7 +276,7 @@ template <int KB, int NP> void run(const DrProblem &p, cudaStream_t s) {
     note_host_error();
     return;
   }
-  dr_prep_tc_kernel<KB, NP><<<dim3((unsigned)p.slots, (unsigned)p.Hk), kThreads, bytes, s>>>(tq, tk, p);
+  dr_prep_tc_kernel<KB, NP><<<dim3((unsigned)p.slots, (unsigned)p.H), kThreads, bytes, s>>>(tq, tk, p);
 }
 
 }  // namespace

@@ -10,23 +10,30 @@ namespace ssd {
 
 namespace {
 
-// G of one head and everything of a row, by one warp; rk, rq: 1 / |k|, 1 / |q|; first_nan: the first token whose log decay is
-// not a number, or 64
-template <typename T>
-__device__ __forceinline__ void dr_fill_rows(const DrProblem &p, DrRows &rows, const float *rk, const float *rq, int &first_nan,
-                                             int h, int t0, int n, int lane) {
+// What a head's log decays and strengths give, a warp's lane having rows 2 lane and 2 lane + 1
+struct DrSums {
+  float in[2], out[2], hi[2], lo[2], beta[2];  // e^G, e^(Gall - G), G as two values
+  float all_hi, all_lo;                        // e^Gall, likewise
+  int first_nan;                               // the first token whose log decay is not a number, or 64
+};
+template <typename T> __device__ __forceinline__ DrSums dr_sums(const DrProblem &p, int h, int t0, int n, int lane) {
   constexpr float kUnit = 4294967296.f, kLowest = -256.f;
-  const T *g = static_cast<const T *>(p.g), *b = static_cast<const T *>(p.b);
-  long long x[2];
-  float beta[2];
-  unsigned nan_lanes[2];
+  const T *g = static_cast<const T *>(p.g) + (size_t)t0 * p.gs + h, *b = static_cast<const T *>(p.b) + (size_t)t0 * p.bs + h;
+  DrSums s;
+  float v[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = 2 * lane + e;
-    const float v = i < n ? to_f<T>(g[(t0 + i) * p.gs + h]) : 0.f;
-    beta[e] = i < n ? to_f<T>(b[(t0 + i) * p.bs + h]) : 0.f;
-    x[e] = __float2ll_rn(fminf(fmaxf(v, kLowest), -kLowest) * kUnit);
-    nan_lanes[e] = __ballot_sync(0xffffffffu, v != v);
+    v[e] = i < n ? to_f<T>(g[i * p.gs]) : 0.f;
+    s.beta[e] = i < n ? to_f<T>(b[i * p.bs]) : 0.f;
+  }
+  long long x[2];
+  s.first_nan = kDrC;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    x[e] = __float2ll_rn(fminf(fmaxf(v[e], kLowest), -kLowest) * kUnit);
+    const unsigned nans = __ballot_sync(0xffffffffu, v[e] != v[e]);
+    if (nans) s.first_nan = min(s.first_nan, 2 * (__ffs(nans) - 1) + e);
   }
   x[1] += x[0];
   long long before = x[1];
@@ -37,35 +44,45 @@ __device__ __forceinline__ void dr_fill_rows(const DrProblem &p, DrRows &rows, c
   }
   const long long whole = __shfl_sync(0xffffffffu, before, 31);
   before -= x[1];
-  // the first token whose log decay is not a number: nothing that passes it is
-  int nan_at = kDrC;
-  if (nan_lanes[0]) nan_at = min(nan_at, 2 * (__ffs(nan_lanes[0]) - 1));
-  if (nan_lanes[1]) nan_at = min(nan_at, 2 * (__ffs(nan_lanes[1]) - 1) + 1);
+  // nothing that passes a log decay that is not a number is one
   const float nan = __int_as_float(0x7fffffff);
+  const bool bad = s.first_nan < kDrC;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = 2 * lane + e;
     const long long G = before + x[e];
     const float hi = __ll2float_rn(G), lo = __ll2float_rn(G - __float2ll_rn(hi));
-    const float in = expf(hi * (1.f / kUnit)) + (i >= nan_at ? nan : 0.f);
-    const float out = expf(__ll2float_rn(whole - G) * (1.f / kUnit)) + (nan_at < kDrC && i < n ? nan : 0.f);
-    const bool live = i < n;
-    rows.ghi[i] = hi * (1.f / kUnit);
-    rows.glo[i] = lo * (1.f / kUnit);
-    rows.kin[i] = live ? in * rk[i] : 0.f;
-    rows.kout[i] = live ? out * rk[i] : 0.f;
-    rows.qin[i] = live ? in * rq[i] * p.scale : 0.f;
-    rows.beta[i] = beta[e];
-    rows.rk[i] = live ? rk[i] : 0.f;
-    rows.rq[i] = live ? rq[i] : 0.f;
+    s.hi[e] = hi * (1.f / kUnit);
+    s.lo[e] = lo * (1.f / kUnit);
+    s.in[e] = i < s.first_nan ? expf(s.hi[e]) : nan;
+    s.out[e] = bad ? nan : expf(__ll2float_rn(whole - G) * (1.f / kUnit));
+  }
+  const float gall = __ll2float_rn(whole) * (1.f / kUnit), em = expm1f(gall), hi = 1.f + em;
+  s.all_hi = bad ? nan : hi;
+  // far from 1 the sum 1 + em has lost digits of e^gall, not of em
+  s.all_lo = bad ? nan : gall < -0.5f ? expf(gall) - hi : em - (hi - 1.f);
+  return s;
+}
+// The rows' factors, rk and rq being 1 / |k| and 1 / |q|; rows from n on get zeros.
+__device__ __forceinline__ void dr_put_rows(DrRows &rows, const DrSums &s, const float *rk, const float *rq, float scale, int n,
+                                            int lane) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * lane + e;
+    const float k = i < n ? rk[i] : 0.f, q = i < n ? rq[i] : 0.f;
+    rows.ghi[i] = s.hi[e];
+    rows.glo[i] = s.lo[e];
+    rows.kin[i] = i < n ? s.in[e] * k : 0.f;
+    rows.kout[i] = i < n ? s.out[e] * k : 0.f;
+    rows.qin[i] = i < n ? s.in[e] * q * scale : 0.f;
+    rows.beta[i] = s.beta[e];
+    rows.rk[i] = k;
+    rows.rq[i] = q;
   }
   if (lane == 0) {
-    const float gall = __ll2float_rn(whole) * (1.f / kUnit), em = expm1f(gall), hi = 1.f + em;
-    rows.all_hi = nan_at < kDrC ? nan : hi;
-    // hi is 0 or tiny where em is near -1: the rest is then e^gall itself
-    rows.all_lo = nan_at < kDrC ? nan : gall < -0.5f ? expf(gall) - hi : em - (hi - 1.f);
+    rows.all_hi = s.all_hi;
+    rows.all_lo = s.all_lo;
     rows.pad[0] = rows.pad[1] = 0.f;
-    first_nan = nan_at;
   }
 }
 
