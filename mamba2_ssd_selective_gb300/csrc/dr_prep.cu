@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) dr_prep_kernel(DrProblem p) {
   for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
     __syncthreads();
     if (tid < 32) {
-      const DrSums sums = dr_sums<T>(p, h, t0, n, tid);
+      const DrSums sums = dr_sums(dr_load_gates<T>(p, h, t0, n, tid), tid);
       dr_put_rows(sm.rows, sums, sm.rk, sm.rq, p.scale, n, tid);
       if (tid == 0) sm.nan_at = sums.first_nan;
     }

@@ -1,7 +1,8 @@
 // The factors of a chunk's rows (DrRows in delta.h), made by one warp.
 //
 // Sums of log decays are whole numbers of 2^-32, so that differences between tokens are exact however much was forgotten
-// before them; what is below -256 is taken as -256 (e^-256 is 0 in fp32).
+// before them; what is below -256 is taken as -256 (e^-256 is 0 in fp32).  They go to and from fp32 as a whole part and a
+// signed rest of 32 bits each: conversions of 64 bits are slow here (with them a chunk's factors took 7400 cycles).
 #pragma once
 
 #include "delta.h"
@@ -16,22 +17,37 @@ struct DrSums {
   float all_hi, all_lo;                        // e^Gall, likewise
   int first_nan;                               // the first token whose log decay is not a number, or 64
 };
-template <typename T> __device__ __forceinline__ DrSums dr_sums(const DrProblem &p, int h, int t0, int n, int lane) {
-  constexpr float kUnit = 4294967296.f, kLowest = -256.f;
+struct DrGates {
+  float g[2], b[2];
+};
+template <typename T> __device__ __forceinline__ DrGates dr_load_gates(const DrProblem &p, int h, int t0, int n, int lane) {
   const T *g = static_cast<const T *>(p.g) + (size_t)t0 * p.gs + h, *b = static_cast<const T *>(p.b) + (size_t)t0 * p.bs + h;
-  DrSums s;
-  float v[2];
+  DrGates v;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = 2 * lane + e;
-    v[e] = i < n ? to_f<T>(g[i * p.gs]) : 0.f;
-    s.beta[e] = i < n ? to_f<T>(b[i * p.bs]) : 0.f;
+    v.g[e] = i < n ? to_f<T>(g[i * p.gs]) : 0.f;
+    v.b[e] = i < n ? to_f<T>(b[i * p.bs]) : 0.f;
   }
+  return v;
+}
+// a sum as the nearest whole number and the rest
+__device__ __forceinline__ void dr_parts(long long G, float &whole, float &rest) {
+  const int I = (int)((G + 0x80000000LL) >> 32);
+  whole = (float)I;
+  rest = (float)(int)(G - ((long long)I << 32)) * (1.f / 4294967296.f);
+}
+__device__ __forceinline__ DrSums dr_sums(const DrGates &gates, int lane) {
+  constexpr float kLowest = -256.f;
+  const float *v = gates.g;
+  DrSums s;
+  s.beta[0] = gates.b[0], s.beta[1] = gates.b[1];
   long long x[2];
   s.first_nan = kDrC;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    x[e] = __float2ll_rn(fminf(fmaxf(v[e], kLowest), -kLowest) * kUnit);
+    const float c = fminf(fmaxf(v[e], kLowest), -kLowest), whole = rintf(c);
+    x[e] = ((long long)(int)whole << 32) + __float2int_rn((c - whole) * 4294967296.f);
     const unsigned nans = __ballot_sync(0xffffffffu, v[e] != v[e]);
     if (nans) s.first_nan = min(s.first_nan, 2 * (__ffs(nans) - 1) + e);
   }
@@ -51,13 +67,15 @@ template <typename T> __device__ __forceinline__ DrSums dr_sums(const DrProblem 
   for (int e = 0; e < 2; ++e) {
     const int i = 2 * lane + e;
     const long long G = before + x[e];
-    const float hi = __ll2float_rn(G), lo = __ll2float_rn(G - __float2ll_rn(hi));
-    s.hi[e] = hi * (1.f / kUnit);
-    s.lo[e] = lo * (1.f / kUnit);
-    s.in[e] = i < s.first_nan ? expf(s.hi[e]) : nan;
-    s.out[e] = bad ? nan : expf(__ll2float_rn(whole - G) * (1.f / kUnit));
+    float hi, lo;
+    dr_parts(whole - G, hi, lo);
+    s.out[e] = bad ? nan : expf(hi + lo);
+    dr_parts(G, s.hi[e], s.lo[e]);
+    s.in[e] = i < s.first_nan ? expf(s.hi[e] + s.lo[e]) : nan;
   }
-  const float gall = __ll2float_rn(whole) * (1.f / kUnit), em = expm1f(gall), hi = 1.f + em;
+  float gw, gr;
+  dr_parts(whole, gw, gr);
+  const float gall = gw + gr, em = expm1f(gall), hi = 1.f + em;
   s.all_hi = bad ? nan : hi;
   // far from 1 the sum 1 + em has lost digits of e^gall, not of em
   s.all_lo = bad ? nan : gall < -0.5f ? expf(gall) - hi : em - (hi - 1.f);
