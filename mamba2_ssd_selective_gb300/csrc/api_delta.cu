@@ -38,7 +38,7 @@ bool dr_use_tc(const ssd_delta_rule_dims *d) { return d->dtype == SSD_BF16 && la
 
 DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
   DrPlan pl{};
-  pl.tc = dr_use_tc(d) && !backward;
+  pl.tc = dr_use_tc(d);
   pl.slots = dr_slots(dr_rows(d), d->nseq, d->seqlen, d->packed != 0);
   const size_t chunks = (size_t)pl.slots * d->nheads, state = (size_t)d->headdim_k * d->headdim_v,
                tokens = (size_t)dr_rows(d) * d->nheads;
@@ -53,12 +53,13 @@ DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
   pl.N = take(chunks * (pl.tc ? 4 * kDrTile : kDrC * kDrC * 4));
   pl.P = take(pl.tc ? 0 : chunks * kDrC * kDrC * 4);
   if (backward) {
-    pl.S = take(chunks * state * 4);
-    pl.dS = take(chunks * state * 4);
-    pl.E = take(tokens * d->headdim_v * 4);
-    pl.Z = take(tokens * d->headdim_v * 4);
-    pl.dqp = take(tokens * d->headdim_k * 4);
-    pl.dkp = take(tokens * d->headdim_k * 4);
+    const size_t eb = pl.tc ? 2 : 4;
+    pl.S = take(chunks * state * eb);
+    pl.dS = take(chunks * state * eb);
+    pl.E = take(tokens * d->headdim_v * eb);
+    pl.Z = take(tokens * d->headdim_v * eb);
+    pl.dqp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
+    pl.dkp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
   }
   pl.total = off;
   return pl;
@@ -140,15 +141,22 @@ ssd_status dr_forward_impl(const DrProblem &p, bool tc, void *o, int64_t os, flo
 }
 
 template <typename T>
-ssd_status dr_backward_impl(const DrProblem &p, const void *dout, int64_t dos, const float *dfin,
+ssd_status dr_backward_impl(const DrProblem &p, bool tc, const void *dout, int64_t dos, const float *dfin,
                             const ssd_delta_rule_grads *g, cudaStream_t s) {
   const DrGrads out{g->dq, g->dk, g->dv, g->dlog_decay, g->dbeta, g->dq_tok_stride, g->dk_tok_stride, g->dv_tok_stride,
                     g->dlog_decay_tok_stride, g->dbeta_tok_stride};
-  SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, s));
-  SSD_LAUNCH("dr_chain", launch_dr_chain<T>(p, nullptr, 0, nullptr, s));
-  SSD_LAUNCH("dr_reverse", launch_dr_reverse<T>(p, dout, dos, dfin, g->dinitial_states, s));
-  SSD_LAUNCH("dr_grads", launch_dr_grads<T>(p, dout, dos, out, s));
-  SSD_LAUNCH("dr_finish", launch_dr_finish<T>(p, out, s));
+  if (tc) {
+    SSD_LAUNCH("dr_prep", launch_dr_prep_tc(p, true, s));
+    SSD_LAUNCH("dr_chain", launch_dr_tc_chain(p, nullptr, 0, nullptr, s));
+    SSD_LAUNCH("dr_reverse", launch_dr_tc_reverse(p, dout, dos, dfin, g->dinitial_states, s));
+    SSD_LAUNCH("dr_grads", launch_dr_grads_tc(p, dout, dos, out, s));
+  } else {
+    SSD_LAUNCH("dr_prep", launch_dr_prep<T>(p, s));
+    SSD_LAUNCH("dr_chain", launch_dr_chain<T>(p, nullptr, 0, nullptr, s));
+    SSD_LAUNCH("dr_reverse", launch_dr_reverse<T>(p, dout, dos, dfin, g->dinitial_states, s));
+    SSD_LAUNCH("dr_grads", launch_dr_grads<T>(p, dout, dos, out, s));
+    SSD_LAUNCH("dr_finish", launch_dr_finish<T>(p, out, s));
+  }
   return launch_status();
 }
 
@@ -265,8 +273,8 @@ ssd_status ssd_delta_rule_backward(const ssd_delta_rule_dims *dims, const ssd_de
   if (on_input(grads->dinitial_states, {in->initial_states, dfinal_states})) return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const DrProblem p = dr_problem(dims, in, &pl, static_cast<char *>(workspace));
-  return dims->dtype == SSD_BF16 ? dr_backward_impl<__nv_bfloat16>(p, dout, dout_tok_stride, dfinal_states, grads, s)
-                                 : dr_backward_impl<float>(p, dout, dout_tok_stride, dfinal_states, grads, s);
+  return dims->dtype == SSD_BF16 ? dr_backward_impl<__nv_bfloat16>(p, pl.tc, dout, dout_tok_stride, dfinal_states, grads, s)
+                                 : dr_backward_impl<float>(p, pl.tc, dout, dout_tok_stride, dfinal_states, grads, s);
 }
 
 ssd_status ssd_delta_rule_step(const ssd_delta_rule_dims *dims, const ssd_delta_rule_inputs *in, float *states,

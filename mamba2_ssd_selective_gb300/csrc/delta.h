@@ -118,6 +118,8 @@ template <typename T>
 void launch_dr_grads(const DrProblem &p, const void *dout, long long dos, const DrGrads &g, cudaStream_t s);
 // dq and dk out of their parts: summed over the states that share a head, and through the division by the length
 template <typename T> void launch_dr_finish(const DrProblem &p, const DrGrads &g, cudaStream_t s);
+// dr_grads_tc.cu: all gradients of the tensor-core path
+void launch_dr_grads_tc(const DrProblem &p, const void *dout, long long dos, const DrGrads &g, cudaStream_t s);
 // dr_step.cu
 template <typename T>
 void launch_dr_step(const DrProblem &p, void *o, long long os, float *states, int nslots, const int *slot_idx, cudaStream_t s);

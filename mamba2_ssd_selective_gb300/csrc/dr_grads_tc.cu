@@ -1,0 +1,475 @@
+// The gated delta rule's gradients on the 5th-generation tensor cores, from the states before the chunks and the
+// gradients of those behind them (dr_tc.cu), all chunks side by side.  In the tensors' own q and k (their lengths are
+// in the factors), with L_ij = e^(G_i - G_j):
+//     Wq_ij = scale L_ij / |q_i| / |k_j| (dO E^T)_ij b_j   (j <= i),    Wk_ij = -L_ij / |k_i| / |k_j| b_i (Z E^T)_ij b_j   (j < i)
+//     dq = qin dO S^T + Wq K,      dk = kout b E dS^T - kin b Z S^T + Wk K + Wq^T Q + Wk^T K
+//     dv = b Z,  dbeta = E.Z (rows),  dlog_decay: the suffix sums of q.dq - v.dv, and <S_next, dS> behind them
+// and the division by the lengths last: dq - q (q.dq) / |q|^2, likewise dk.
+//
+// Persistent CTAs; a CTA takes a chunk and a head of q and k and goes through the states that share it, dq and dk
+// staying in registers.  Lanes 0-63 of the accumulators are the rows of dO and dq, lanes 64-127 those of Z and dk:
+//     [dO; Z] S^T,   [dO; Z] E^T,   [.; E] dS^T,   [Wq; Wk] K,   [.; Wq^T Wk^T] [Q; K]
+// Warps: 0 TMA producer, 1 MMA issuer, 2-9 everything else.  A state's tensors are loaded again as soon as their products
+// are made, beside the weights, the last two products and the sums.  Operands are rounded to bf16 (the outputs are bf16).
+#include "delta.h"
+#include "tc_pipe.cuh"
+#include "tc_util.cuh"
+
+namespace ssd {
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+using namespace sm100;
+using pipe::parity;
+
+constexpr int kThreads = 320, kTeam = 256;
+constexpr uint32_t kBox = 8192;  // [64 rows x 64 columns] bf16
+constexpr uint32_t kTmA = 0, kTmC = 128, kTmW = 256, kTmB = 384, kTmCols = 512;  // products with S, dS, K; with E and, later, [Q; K]
+
+template <int KB, int VB> struct Layout {
+  static constexpr uint32_t kIn = 0;                             // dO, Z, E: boxes of each 64 columns behind one another
+  static constexpr uint32_t kS = VB * 3 * kBox, kDs = kS + KB * VB * kBox;  // boxes of 64 columns of dk, all rows
+  static constexpr uint32_t kQK = kDs + KB * VB * kBox;         // Q, K: likewise pairs
+  static constexpr uint32_t kW = kQK + KB * 2 * kBox;           // Wq, Wk
+  static constexpr uint32_t kRows = kW + 2 * kBox;
+  static constexpr uint32_t kMisc = kRows + (sizeof(DrRows) + 15) / 16 * 16;
+  static constexpr uint32_t kBar = kMisc + 4 * (64 + 128 + 128 + 16);
+  static constexpr uint32_t kEnd = kBar + 10 * 8 + 16;
+  static constexpr int kBytes = (int)kEnd + 1024;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+struct Misc {
+  float vdv[64], dot[2][64], dot2[2][64], part[16];
+};
+
+struct Args {
+  CUtensorMap q, k, dout, z, e, s, ds;
+  DrProblem p;
+  DrGrads g;
+  WaitCtl wait;
+};
+
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t par, const WaitCtl &w) {
+  const uint32_t hint = w.limit_ns < kWaitHintNs ? (uint32_t)w.limit_ns : kWaitHintNs;
+  if (__builtin_expect(mbar_try_wait_hint(bar, par, hint), 1)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < w.limit_ns) {
+    if (mbar_try_wait_hint(bar, par, hint)) return true;
+    if (*reinterpret_cast<volatile int *>(w.status) != 0) return false;
+  }
+  atomicExch(w.status, 1);
+  return false;
+}
+__device__ __forceinline__ void team_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTeam) : "memory"); }
+
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+  float x[8], y[8];
+  tc::unpack8(a, x);
+  tc::unpack8(b, y);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+  return s;
+}
+
+template <int KB, int VB>
+__global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_constant__ Args args) {
+  using L = Layout<KB, VB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = tc::aligned_smem(smem_raw);
+  const DrProblem &p = args.p;
+  const DrGrads &g = args.g;
+  const WaitCtl wait = args.wait;
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
+  uint64_t *in_full = bar, *in_free = bar + 1, *qk_full = bar + 2, *qk_free = bar + 3, *b_full = bar + 4, *w_ready = bar + 5,
+           *out_full = bar + 6, *acc_free = bar + 7, *drain = bar + 8;
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + 10 * 8);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (warp == 0 && lane < 7) prefetch_tmap(&args.q + lane);
+  if (threadIdx.x == 32) {
+    mbar_init(in_full, 1);
+    mbar_init(in_free, 9);
+    mbar_init(qk_full, 1);
+    mbar_init(qk_free, 9);
+    mbar_init(b_full, 1);
+    mbar_init(w_ready, 8);
+    mbar_init(out_full, 1);
+    mbar_init(acc_free, 8);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tslot, kTmCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
+  const uint32_t s0 = smem_u32(sm);
+  const int nunits = p.slots * p.Hk;
+  // all roles walk the same units: a chunk's heads are neighbours, so that their v, dO and states are read together
+  auto unit_at = [&](int u, int &slot, int &hk, int &t0, int &n) {
+    slot = u / p.Hk;
+    hk = u - slot * p.Hk;
+    dr_chunk(p, slot, t0, n);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t m = 0, c = 0;  // steps (a chunk and a state head), units
+      bool ok = true;
+#pragma unroll 1
+      for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
+        int slot, hk, t0, n;
+        unit_at(u, slot, hk, t0, n);
+        if (n == 0) continue;
+#pragma unroll 1
+        for (int y = 0; y < p.group && ok; ++y, ++m) {
+          const int h = hk * p.group + y;
+          const size_t at = (size_t)slot * p.H + h;
+          if (m > 0 && !wait_on(in_free, parity(m - 1), wait)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(in_full, (3 * VB + 2 * KB * VB) * kBox + (uint32_t)sizeof(DrRows));
+          for (int b = 0; b < VB; ++b) {
+            tma_load_3d(sm + L::kIn + (3 * b) * kBox, &args.dout, in_full, 64 * b, h, t0);
+            tma_load_3d(sm + L::kIn + (3 * b + 1) * kBox, &args.z, in_full, 64 * b, h, t0);
+            tma_load_3d(sm + L::kIn + (3 * b + 2) * kBox, &args.e, in_full, 64 * b, h, t0);
+          }
+          for (int b = 0; b < KB; ++b)
+            for (int v = 0; v < VB; ++v) {
+              tma_load_3d(sm + L::kS + (b * VB + v) * kBox, &args.s, in_full, 64 * b, 64 * v, (int)at);
+              tma_load_3d(sm + L::kDs + (b * VB + v) * kBox, &args.ds, in_full, 64 * b, 64 * v, (int)at);
+            }
+          pipe::bulk_load(sm + L::kRows, p.rows + at, sizeof(DrRows), in_full);
+          if (y == 0) {
+            if (c > 0 && !wait_on(qk_free, parity(c - 1), wait)) {
+              ok = false;
+              ++m;
+              break;
+            }
+            mbar_expect_tx(qk_full, 2 * KB * kBox);
+            for (int b = 0; b < KB; ++b) {
+              tma_load_3d(sm + L::kQK + (2 * b) * kBox, &args.q, qk_full, 64 * b, hk, t0);
+              tma_load_3d(sm + L::kQK + (2 * b + 1) * kBox, &args.k, qk_full, 64 * b, hk, t0);
+            }
+            ++c;
+          }
+        }
+      }
+      if (m > 0) mbar_wait_drain(in_full, parity(m - 1));
+      if (c > 0) mbar_wait_drain(qk_full, parity(c - 1));
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t el = elect_one();
+    const uint64_t dIn = desc_sw128(s0 + L::kIn, 16, 1024);                                     // K-major, 128 rows
+    const uint64_t dS = desc_sw128(s0 + L::kS, VB * kBox, 1024), dDs = desc_sw128(s0 + L::kDs, VB * kBox, 1024);
+    const uint64_t dQK = desc_sw128(s0 + L::kQK, 2 * kBox, 1024);                               // MN-major
+    const uint64_t dW = desc_sw128(s0 + L::kW, 16, 1024);
+    // transposed: lanes 64-127 are its 64 columns, lanes 0-63 those of what lies two boxes before
+    const uint64_t dWt = desc_sw128(s0 + L::kW - 2 * kBox, 2 * kBox, 1024);
+    constexpr uint32_t iB = idesc_bf16(128, 64, false, false), iN = idesc_bf16(128, 64 * KB, false, true),
+                       iT = idesc_bf16(128, 64 * KB, true, true);
+    constexpr uint64_t kB = kBox / 16;
+    uint32_t m = 0, c = 0;
+#pragma unroll 1
+    for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
+      int slot, hk, t0, n;
+      unit_at(u, slot, hk, t0, n);
+      if (n == 0) continue;
+#pragma unroll 1
+      for (int y = 0; y < p.group; ++y, ++m) {
+        wait_on(in_full, parity(m), wait);
+        if (m > 0) wait_on(acc_free, parity(m - 1), wait);
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < VB; ++b)  // [dO; Z] E^T
+          pipe::umma_k_el<4>(el, tmem + kTmB, dIn + 3 * b * kB, dIn + (3 * b + 2) * kB, pipe::kStepK, pipe::kStepK, iB, b > 0);
+        umma_commit_el(el, b_full);
+#pragma unroll
+        for (int b = 0; b < VB; ++b)  // [dO; Z] S^T
+          pipe::umma_k_el<4>(el, tmem + kTmA, dIn + 3 * b * kB, dS + b * kB, pipe::kStepK, pipe::kStepMN, iN, b > 0);
+#pragma unroll
+        for (int b = 0; b < VB; ++b)  // [Z; E] dS^T
+          pipe::umma_k_el<4>(el, tmem + kTmC, dIn + (3 * b + 1) * kB, dDs + b * kB, pipe::kStepK, pipe::kStepMN, iN, b > 0);
+        umma_commit_el(el, in_free);
+        if (y == 0) wait_on(qk_full, parity(c), wait);
+        wait_on(w_ready, parity(m), wait);
+        tc_fence_after();
+        pipe::umma_k_el<4>(el, tmem + kTmW, dW, dQK + kB, pipe::kStepK, pipe::kStepMN, iN, false);          // [Wq; Wk] K
+        pipe::umma_k_el<8>(el, tmem + kTmB, dWt, dQK, pipe::kStepMN, pipe::kStepMN, iT, false);             // [Wq^T Wk^T] [Q; K]
+        umma_commit_el(el, out_full);
+        if (y + 1 == p.group) {
+          umma_commit_el(el, qk_free);
+          ++c;
+        }
+      }
+    }
+    umma_commit_el(el, drain);
+    mbar_wait_drain(drain, 0);
+    if (m > 0) {
+      mbar_wait_drain(in_free, parity(m - 1));
+      mbar_wait_drain(b_full, parity(m - 1));
+      mbar_wait_drain(out_full, parity(m - 1));
+      mbar_wait_drain(qk_free, parity(c - 1));
+    }
+  } else {
+    // ------------------------------------------------------------ weights and gradients
+    constexpr int kCols = 32 * KB;  // columns of dk of a thread
+    const int et = threadIdx.x - 64, quad = warp & 3, sub = (warp - 2) >> 2;
+    const bool is_k = quad >= 2;                       // lanes 64-127: rows of Z and dk
+    const int i = 32 * (quad & 1) + lane;              // the thread's row
+    Misc &x = *reinterpret_cast<Misc *>(sm + L::kMisc);
+    const DrRows &rw = *reinterpret_cast<const DrRows *>(sm + L::kRows);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    uint32_t m = 0, c = 0;
+#pragma unroll 1
+    for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
+      int slot, hk, t0, n;
+      unit_at(u, slot, hk, t0, n);
+      if (n == 0) continue;
+      float acc[kCols];
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+#pragma unroll 1
+      for (int y = 0; y < p.group; ++y, ++m) {
+        const int h = hk * p.group + y;
+        wait_on(in_full, parity(m), wait);
+        // dv, dbeta, v.dv: 16 bytes of a row at a time
+#pragma unroll
+        for (int e = et; e < 64 * 8 * VB; e += kTeam) {
+          const int r = e / (8 * VB), b = e % (8 * VB) >> 3, ch = e & 7, col = 64 * b + 8 * ch;
+          float vdv = 0.f, db = 0.f;
+          if (r < n && col < p.dv) {
+            const uint4 zw = pipe::lds_sw128(s0 + L::kIn + (3 * b + 1) * kBox, r, ch), ew = pipe::lds_sw128(s0 + L::kIn + (3 * b + 2) * kBox, r, ch);
+            const uint4 vw = tc::ldg16(static_cast<const bf16 *>(p.v) + (size_t)(t0 + r) * p.vs + (size_t)h * p.dv + col);
+            db = dot8(zw, ew, 0.f);
+            float z[8], v[8];
+            tc::unpack8(zw, z);
+            tc::unpack8(vw, v);
+            const float beta = rw.beta[r];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              z[j] *= beta;
+              vdv = fmaf(v[j], z[j], vdv);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<bf16 *>(g.dv) + (size_t)(t0 + r) * g.dvs + (size_t)h * p.dv + col) = tc::pack8(z);
+          }
+#pragma unroll
+          for (int o = 4 * VB; o >= 1; o >>= 1) {
+            vdv += __shfl_xor_sync(0xffffffffu, vdv, o);
+            db += __shfl_xor_sync(0xffffffffu, db, o);
+          }
+          if (e % (8 * VB) == 0) {
+            x.vdv[r] = vdv;
+            if (r < n) static_cast<bf16 *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = __float2bfloat16_rn(db);
+          }
+        }
+        float ss = 0.f;  // <S, dS>
+#pragma unroll 4
+        for (int e = et; e < KB * VB * 512; e += kTeam) {
+          uint4 a, b;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w) : "r"(s0 + L::kS + 16 * e));
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "r"(s0 + L::kDs + 16 * e));
+          ss = dot8(a, b, ss);
+        }
+        const float all = rw.all_hi + rw.all_lo;
+        float dgall = ss * all;
+        // weights
+        const float rk_i = rw.rk[i], rq_i = rw.rq[i], beta_i = rw.beta[i];
+        const float fa = is_k ? -rw.kin[i] * beta_i : rw.qin[i], fc = rw.kout[i] * beta_i;
+        const float hi = rw.ghi[i], lo = rw.glo[i];
+        if (y == 0) {
+          if (n < kDrC) {  // rows past the end belong to another sequence
+            wait_on(qk_full, parity(c), wait);
+            for (int e = et; e < (kDrC - n) * 16 * KB; e += kTeam) {
+              const int b = e % (16 * KB), r = n + e / (16 * KB);
+              pipe::sts_u4(s0 + L::kQK + (uint32_t)(b >> 3) * kBox + sw128_offset(r, 8 * (b & 7)), make_uint4(0, 0, 0, 0));
+            }
+          }
+        }
+        wait_on(b_full, parity(m), wait);
+        tc_fence_after();
+        const float fw = is_k ? -rk_i * beta_i : rq_i * p.scale;
+        const int last = i < n ? is_k ? i - 1 : i : -1;  // the row's columns are up to this one
+#pragma unroll
+        for (int j0 = 32 * sub; j0 < 32 * sub + 32; j0 += 16) {
+          float v[16], w8[8];
+          tmem_ld16(lanes + kTmB + j0, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = j0 + e;
+            const float f = __expf((hi - rw.ghi[j]) + (lo - rw.glo[j])) * (rw.rk[j] * rw.beta[j]);
+            v[e] = j <= last ? v[e] * (f * fw) : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w8[j] = v[e + j];
+            pipe::sts_u4(s0 + L::kW + (is_k ? kBox : 0) + sw128_offset(i, j0 + e), tc::pack8(w8));
+          }
+        }
+        tc_fence_before();
+        fence_async_smem();
+        pipe::warp_arrive(w_ready);
+        pipe::warp_arrive(in_free);
+        // gradients
+        wait_on(out_full, parity(m), wait);
+        if (y == 0) wait_on(qk_full, parity(c), wait);
+        tc_fence_after();
+        float dot = 0.f;  // q.dq, or of k and what is added to the state
+#pragma unroll
+        for (int j0 = 0; j0 < kCols; j0 += 16) {
+          const int col = kCols * sub + j0;
+          float a[16], w[16], t[16];
+          tmem_ld16(lanes + kTmA + col, a);
+          tmem_ld16(lanes + kTmW + col, w);
+          const uint32_t tile = s0 + L::kQK + (2 * (col >> 6) + (is_k ? 1 : 0)) * kBox;
+          float r8[8];
+          if (is_k) {
+            tmem_ld16(lanes + kTmB + col, t);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] += t[e];
+            tmem_ld16(lanes + kTmC + col, t);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) t[e] *= fc;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            a[e] = fmaf(fa, a[e], w[e]);
+            if (is_k) a[e] += t[e];
+            acc[j0 + e] += a[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            tc::unpack8(pipe::lds_sw128(tile, i, ((col & 63) + e) >> 3), r8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot = fmaf(r8[j], is_k ? t[e + j] : a[e + j], dot);
+          }
+        }
+        tc_fence_before();
+        pipe::warp_arrive(acc_free);
+        if (!is_k) {
+          x.dot[sub][i] = dot;
+        } else if (i < n) {
+          dgall += dot;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) dgall += __shfl_xor_sync(0xffffffffu, dgall, o);
+        if (lane == 0) x.part[warp - 2] = dgall;
+        team_sync();
+        if (warp == 2) {  // suffix sums, two rows a lane
+          float d[2], end = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) end += x.part[e];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 2 * lane + e;
+            d[e] = r < n ? (x.dot[0][r] + x.dot[1][r]) - x.vdv[r] : 0.f;
+          }
+          d[0] += d[1];
+          float after = d[0];
+#pragma unroll
+          for (int o = 1; o < 32; o *= 2) {
+            const float z = __shfl_down_sync(0xffffffffu, after, o);
+            if (lane + o < 32) after += z;
+          }
+          after -= d[0];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 2 * lane + e;
+            if (r < n) static_cast<bf16 *>(g.dg)[(size_t)(t0 + r) * g.dgs + h] = __float2bfloat16_rn(d[e] + after + end);
+          }
+        }
+        team_sync();
+      }
+      // the division by the lengths, and out
+      const uint32_t tile0 = s0 + L::kQK + (is_k ? kBox : 0);
+      float f = 0.f;
+      if (p.norm) {
+        float dot = 0.f, len = 0.f, r8[8];
+#pragma unroll
+        for (int e = 0; e < kCols; e += 8) {
+          const int col = kCols * sub + e;
+          tc::unpack8(pipe::lds_sw128(tile0 + 2 * (col >> 6) * kBox, i, (col & 63) >> 3), r8);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            dot = fmaf(r8[j], acc[e + j], dot);
+            len = fmaf(r8[j], r8[j], len);
+          }
+        }
+        float(*d)[64] = is_k ? x.dot2 : x.dot;
+        d[sub][i] = dot;
+        float *l = reinterpret_cast<float *>(sm + L::kW) + (is_k ? 128 : 0);
+        l[64 * sub + i] = len;
+        team_sync();
+        f = (d[0][i] + d[1][i]) / (l[i] + l[64 + i] + p.eps);
+      }
+      const int head = hk * p.dk;
+      bf16 *out = is_k ? static_cast<bf16 *>(g.dk) + (size_t)(t0 + i) * g.dks + head : static_cast<bf16 *>(g.dq) + (size_t)(t0 + i) * g.dqs + head;
+#pragma unroll
+      for (int e = 0; e < kCols; e += 8) {
+        const int col = kCols * sub + e;
+        float v[8];
+        if (p.norm) {
+          float r8[8];
+          tc::unpack8(pipe::lds_sw128(tile0 + 2 * (col >> 6) * kBox, i, (col & 63) >> 3), r8);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = acc[e + j] - r8[j] * f;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = acc[e + j];
+        }
+        if (i < n && col < p.dk) *reinterpret_cast<uint4 *>(out + col) = tc::pack8(v);
+      }
+      pipe::warp_arrive(qk_free);
+      ++c;
+      team_sync();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmCols);
+  }
+}
+
+template <int KB, int VB> void run(Args &args, cudaStream_t s) {
+  using L = Layout<KB, VB>;
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(dr_grads_tc_kernel<KB, VB>), L::kBytes, allowed);
+  const int units = args.p.slots * args.p.Hk, sms = device_sm_count();
+  dr_grads_tc_kernel<KB, VB><<<units < sms ? units : sms, kThreads, L::kBytes, s>>>(args);
+}
+
+}  // namespace
+
+void launch_dr_grads_tc(const DrProblem &p, const void *dout, long long dos, const DrGrads &g, cudaStream_t s) {
+  Args args;
+  args.p = p;
+  args.g = g;
+  args.wait = {p.status, p.wait_ns};
+  const uint64_t es = (uint64_t)p.H * p.dv * 2, chunks = (uint64_t)p.slots * p.H;
+  if (!encode_tmap_bf16_heads(&args.q, p.q, p.dk, p.Hk, p.total, p.qs * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&args.k, p.k, p.dk, p.Hk, p.total, p.ks * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&args.dout, dout, p.dv, p.H, p.total, dos * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&args.z, p.Z, p.dv, p.H, p.total, es, kDrC) ||
+      !encode_tmap_bf16_heads(&args.e, p.E, p.dv, p.H, p.total, es, kDrC) ||
+      !encode_tmap_bf16_mats(&args.s, p.S, p.dk, p.dv, chunks) || !encode_tmap_bf16_mats(&args.ds, p.dS, p.dk, p.dv, chunks)) {
+    note_host_error();
+    return;
+  }
+  const int kb = la_tc_boxes(p.dk), vb = la_tc_boxes(p.dv);
+  if (kb == 1)
+    vb == 1 ? run<1, 1>(args, s) : run<1, 2>(args, s);
+  else
+    vb == 1 ? run<2, 1>(args, s) : run<2, 2>(args, s);
+}
+
+}  // namespace ssd
