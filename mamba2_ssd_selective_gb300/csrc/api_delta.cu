@@ -12,7 +12,7 @@ namespace {
 struct DrPlan {
   bool tc;
   int slots;
-  size_t status, rows, N, P, S, dS, E, Z, dqp, dkp, total;  // workspace offsets
+  size_t status, rows, N, P, S, dS, E, Z, dqp, dkp, dots, total;  // workspace offsets
 };
 
 long long dr_rows(const ssd_delta_rule_dims *d) { return d->packed ? d->total_tokens : (long long)d->nseq * d->seqlen; }
@@ -53,13 +53,14 @@ DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
   pl.N = take(chunks * (pl.tc ? 4 * kDrTile : kDrC * kDrC * 4));
   pl.P = take(pl.tc ? 0 : chunks * kDrC * kDrC * 4);
   if (backward) {
-    const size_t eb = pl.tc ? 2 : 4;
-    pl.S = take(chunks * state * eb);
-    pl.dS = take(chunks * state * eb);
+    const size_t eb = pl.tc ? 2 : 4, padded = (size_t)dr_padded(d->headdim_k) * dr_padded(d->headdim_v);
+    pl.S = take(pl.tc ? (chunks + (size_t)d->nseq * d->nheads) * padded * 2 : chunks * state * 4);
+    pl.dS = take(chunks * (pl.tc ? padded * 2 : state * 4));
     pl.E = take(tokens * d->headdim_v * eb);
     pl.Z = take(tokens * d->headdim_v * eb);
     pl.dqp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
     pl.dkp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
+    pl.dots = take(pl.tc ? chunks * 8 * 4 : 0);
   }
   pl.total = off;
   return pl;
@@ -128,7 +129,7 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
     auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
     p.N = at(pl->N), p.P = at(pl->P);
     p.S = at(pl->S), p.dS = at(pl->dS), p.E = at(pl->E), p.Z = at(pl->Z);
-    p.dqp = at(pl->dqp), p.dkp = at(pl->dkp);
+    p.dqp = at(pl->dqp), p.dkp = at(pl->dkp), p.dots = at(pl->dots);
   }
   return p;
 }

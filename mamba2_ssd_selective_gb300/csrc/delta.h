@@ -53,13 +53,18 @@ struct DrProblem {
   DrRows *rows;
   float *N, *P;  // CUDA cores: (64, 64) fp32, element (i, j) at 64 i + j
   // backward: the states before the chunks and the gradients of those behind them (dk, dv), E and Z (total, H, dv).
-  // Tensor cores: N's and P's two bf16 terms as four tiles of (64, 64) in the 128-byte swizzle, at N; the states
-  // (dv, dk), E and Z are bf16.
+  // Tensor cores: N's and P's two bf16 terms as four tiles of (64, 64) in the 128-byte swizzle, at N; E and Z are bf16,
+  // and so are the states, at S and dS, in blocks of 8 columns: element (m, c) of (dk, dv), both padded to 64 or 128, at
+  // (m / 8) 8 dv + 8 c + m % 8; behind the chunks' the final states of the sequences' heads.
   float *S, *dS, *E, *Z;
   float *dqp, *dkp;  // (total, H, dk): gradients of the unit q and k of each state head
+  float *dots;       // (chunk, 8): parts of <state behind the chunk, its gradient>, dv / 16 of them (dv padded)
   int *status;       // device status word, cleared by the first kernel
   unsigned long long wait_ns;
 };
+
+// padded width of a state's side
+__host__ __device__ __forceinline__ int dr_padded(int width) { return width <= 64 ? 64 : 128; }
 
 __host__ __device__ __forceinline__ int dr_slots(long long rows, int nseq, int seqlen, bool packed) {
   return packed ? (int)(rows / kDrC) + nseq : nseq * ((seqlen + kDrC - 1) / kDrC);

@@ -4,11 +4,13 @@
 //     Wq_ij = scale L_ij / |q_i| / |k_j| (dO E^T)_ij b_j   (j <= i),    Wk_ij = -L_ij / |k_i| / |k_j| b_i (Z E^T)_ij b_j   (j < i)
 //     dq = qin dO S^T + Wq K,      dk = kout b E dS^T - kin b Z S^T + Wk K + Wq^T Q + Wk^T K
 //     dv = b Z,  dbeta = E.Z (rows),  dlog_decay: the suffix sums of q.dq - v.dv, and <S_next, dS> behind them
+// (q.dq as scale e^G/|q| (dO S^T).q + sum_j Wq_ij q_i.k_j, with the weights before their rounding: the sums' terms have both
+// signs, and their errors show; <S_next, dS> is the reverse chain's, with the gradient unrounded)
 // and the division by the lengths last: dq - q (q.dq) / |q|^2, likewise dk.
 //
 // Persistent CTAs; a CTA takes a chunk and a head of q and k and goes through the states that share it, dq and dk
 // staying in registers.  Lanes 0-63 of the accumulators are the rows of dO and dq, lanes 64-127 those of Z and dk:
-//     [dO; Z] S^T,   [dO; Z] E^T,   [.; E] dS^T,   [Wq; Wk] K,   [.; Wq^T Wk^T] [Q; K]
+//     [dO; Z] S^T,   [dO; Z] E^T,   [Q; K] K^T,   [.; E] dS^T,   [Wq; Wk] K,   [.; Wq^T Wk^T] [Q; K]
 // Warps: 0 TMA producer, 1 MMA issuer, 2-9 everything else.  A state's tensors are loaded again as soon as their products
 // are made, beside the weights, the last two products and the sums.  Operands are rounded to bf16 (the outputs are bf16).
 #include "delta.h"
@@ -25,26 +27,27 @@ using pipe::parity;
 
 constexpr int kThreads = 320, kTeam = 256;
 constexpr uint32_t kBox = 8192;  // [64 rows x 64 columns] bf16
-constexpr uint32_t kTmA = 0, kTmC = 128, kTmW = 256, kTmB = 384, kTmCols = 512;  // products with S, dS, K; with E and, later, [Q; K]
+constexpr uint32_t kTmA = 0, kTmC = 128, kTmW = 256, kTmB = 384, kTmCols = 512;  // products with S, dS, K (before: Q K^T); with E and, later, [Q; K]
 
+struct Misc {
+  float vdv[64], dot[2][64], dot2[2][64];
+};
 template <int KB, int VB> struct Layout {
   static constexpr uint32_t kIn = 0;                             // dO, Z, E: boxes of each 64 columns behind one another
-  static constexpr uint32_t kS = VB * 3 * kBox, kDs = kS + KB * VB * kBox;  // boxes of 64 columns of dk, all rows
-  static constexpr uint32_t kQK = kDs + KB * VB * kBox;         // Q, K: likewise pairs
+  static constexpr uint32_t kTile = KB * VB * kBox;
+  static constexpr uint32_t kS = VB * 3 * kBox, kDs = kS + kTile;  // blocks of 8 columns of dk, all rows
+  static constexpr uint32_t kQK = kDs + kTile;         // Q, K: likewise pairs
   static constexpr uint32_t kW = kQK + KB * 2 * kBox;           // Wq, Wk
   static constexpr uint32_t kRows = kW + 2 * kBox;
   static constexpr uint32_t kMisc = kRows + (sizeof(DrRows) + 15) / 16 * 16;
-  static constexpr uint32_t kBar = kMisc + 4 * (64 + 128 + 128 + 16);
+  static constexpr uint32_t kBar = kMisc + sizeof(Misc);
   static constexpr uint32_t kEnd = kBar + 10 * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
-struct Misc {
-  float vdv[64], dot[2][64], dot2[2][64], part[16];
-};
 
 struct Args {
-  CUtensorMap q, k, dout, z, e, s, ds;
+  CUtensorMap q, k, dout, z, e;
   DrProblem p;
   DrGrads g;
   WaitCtl wait;
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
            *out_full = bar + 6, *acc_free = bar + 7, *drain = bar + 8;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + 10 * 8);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (warp == 0 && lane < 7) prefetch_tmap(&args.q + lane);
+  if (warp == 0 && lane < 5) prefetch_tmap(&args.q + lane);
   if (threadIdx.x == 32) {
     mbar_init(in_full, 1);
     mbar_init(in_free, 9);
@@ -139,11 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
             tma_load_3d(sm + L::kIn + (3 * b + 1) * kBox, &args.z, in_full, 64 * b, h, t0);
             tma_load_3d(sm + L::kIn + (3 * b + 2) * kBox, &args.e, in_full, 64 * b, h, t0);
           }
-          for (int b = 0; b < KB; ++b)
-            for (int v = 0; v < VB; ++v) {
-              tma_load_3d(sm + L::kS + (b * VB + v) * kBox, &args.s, in_full, 64 * b, 64 * v, (int)at);
-              tma_load_3d(sm + L::kDs + (b * VB + v) * kBox, &args.ds, in_full, 64 * b, 64 * v, (int)at);
-            }
+          pipe::bulk_load(sm + L::kS, reinterpret_cast<const uint8_t *>(p.S) + at * L::kTile, L::kTile, in_full);
+          pipe::bulk_load(sm + L::kDs, reinterpret_cast<const uint8_t *>(p.dS) + at * L::kTile, L::kTile, in_full);
           pipe::bulk_load(sm + L::kRows, p.rows + at, sizeof(DrRows), in_full);
           if (y == 0) {
             if (c > 0 && !wait_on(qk_free, parity(c - 1), wait)) {
@@ -167,8 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
     // ------------------------------------------------------------ MMA issuer
     const uint32_t el = elect_one();
     const uint64_t dIn = desc_sw128(s0 + L::kIn, 16, 1024);                                     // K-major, 128 rows
-    const uint64_t dS = desc_sw128(s0 + L::kS, VB * kBox, 1024), dDs = desc_sw128(s0 + L::kDs, VB * kBox, 1024);
+    const uint64_t dS = desc_blocks_mn(s0 + L::kS, 128, VB * 1024), dDs = desc_blocks_mn(s0 + L::kDs, 128, VB * 1024);
     const uint64_t dQK = desc_sw128(s0 + L::kQK, 2 * kBox, 1024);                               // MN-major
+    const uint64_t dQKk = desc_sw128(s0 + L::kQK, 16, 1024);                                    // K-major
     const uint64_t dW = desc_sw128(s0 + L::kW, 16, 1024);
     // transposed: lanes 64-127 are its 64 columns, lanes 0-63 those of what lies two boxes before
     const uint64_t dWt = desc_sw128(s0 + L::kW - 2 * kBox, 2 * kBox, 1024);
@@ -189,15 +190,21 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
 #pragma unroll
         for (int b = 0; b < VB; ++b)  // [dO; Z] E^T
           pipe::umma_k_el<4>(el, tmem + kTmB, dIn + 3 * b * kB, dIn + (3 * b + 2) * kB, pipe::kStepK, pipe::kStepK, iB, b > 0);
+        if (y == 0) {
+          wait_on(qk_full, parity(c), wait);
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int b = 0; b < KB; ++b)  // [Q; K] K^T
+          pipe::umma_k_el<4>(el, tmem + kTmW, dQKk + 2 * b * kB, dQKk + (2 * b + 1) * kB, pipe::kStepK, pipe::kStepK, iB, b > 0);
         umma_commit_el(el, b_full);
 #pragma unroll
         for (int b = 0; b < VB; ++b)  // [dO; Z] S^T
-          pipe::umma_k_el<4>(el, tmem + kTmA, dIn + 3 * b * kB, dS + b * kB, pipe::kStepK, pipe::kStepMN, iN, b > 0);
+          pipe::umma_k_el<4>(el, tmem + kTmA, dIn + 3 * b * kB, dS + b * 64, pipe::kStepK, 16, iN, b > 0);
 #pragma unroll
         for (int b = 0; b < VB; ++b)  // [Z; E] dS^T
-          pipe::umma_k_el<4>(el, tmem + kTmC, dIn + (3 * b + 1) * kB, dDs + b * kB, pipe::kStepK, pipe::kStepMN, iN, b > 0);
+          pipe::umma_k_el<4>(el, tmem + kTmC, dIn + (3 * b + 1) * kB, dDs + b * 64, pipe::kStepK, 16, iN, b > 0);
         umma_commit_el(el, in_free);
-        if (y == 0) wait_on(qk_full, parity(c), wait);
         wait_on(w_ready, parity(m), wait);
         tc_fence_after();
         pipe::umma_k_el<4>(el, tmem + kTmW, dW, dQK + kB, pipe::kStepK, pipe::kStepMN, iN, false);          // [Wq; Wk] K
@@ -269,16 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
             if (r < n) static_cast<bf16 *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = __float2bfloat16_rn(db);
           }
         }
-        float ss = 0.f;  // <S, dS>
-#pragma unroll 4
-        for (int e = et; e < KB * VB * 512; e += kTeam) {
-          uint4 a, b;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w) : "r"(s0 + L::kS + 16 * e));
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "r"(s0 + L::kDs + 16 * e));
-          ss = dot8(a, b, ss);
-        }
-        const float all = rw.all_hi + rw.all_lo;
-        float dgall = ss * all;
         // weights
         const float rk_i = rw.rk[i], rq_i = rw.rq[i], beta_i = rw.beta[i];
         const float fa = is_k ? -rw.kin[i] * beta_i : rw.qin[i], fc = rw.kout[i] * beta_i;
@@ -295,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         wait_on(b_full, parity(m), wait);
         tc_fence_after();
         const float fw = is_k ? -rk_i * beta_i : rq_i * p.scale;
+        float dot = 0.f;  // q.dq
         const int last = i < n ? is_k ? i - 1 : i : -1;  // the row's columns are up to this one
 #pragma unroll
         for (int j0 = 32 * sub; j0 < 32 * sub + 32; j0 += 16) {
@@ -305,6 +303,12 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
             const int j = j0 + e;
             const float f = __expf((hi - rw.ghi[j]) + (lo - rw.glo[j])) * (rw.rk[j] * rw.beta[j]);
             v[e] = j <= last ? v[e] * (f * fw) : 0.f;
+          }
+          if (!is_k) {
+            float qk[16];
+            tmem_ld16(lanes + kTmW + j0, qk);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) dot = j0 + e <= last ? fmaf(v[e], qk[e], dot) : dot;
           }
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
@@ -321,15 +325,23 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         wait_on(out_full, parity(m), wait);
         if (y == 0) wait_on(qk_full, parity(c), wait);
         tc_fence_after();
-        float dot = 0.f;  // q.dq, or of k and what is added to the state
+        float read = 0.f;  // (dO S^T).q
 #pragma unroll
         for (int j0 = 0; j0 < kCols; j0 += 16) {
           const int col = kCols * sub + j0;
           float a[16], w[16], t[16];
           tmem_ld16(lanes + kTmA + col, a);
           tmem_ld16(lanes + kTmW + col, w);
-          const uint32_t tile = s0 + L::kQK + (2 * (col >> 6) + (is_k ? 1 : 0)) * kBox;
-          float r8[8];
+          if (!is_k) {
+            const uint32_t tile = s0 + L::kQK + 2 * (col >> 6) * kBox;
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+              float r8[8];
+              tc::unpack8(pipe::lds_sw128(tile, i, ((col & 63) + e) >> 3), r8);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) read = fmaf(r8[j], a[e + j], read);
+            }
+          }
           if (is_k) {
             tmem_ld16(lanes + kTmB + col, t);
 #pragma unroll
@@ -344,28 +356,15 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
             if (is_k) a[e] += t[e];
             acc[j0 + e] += a[e];
           }
-#pragma unroll
-          for (int e = 0; e < 16; e += 8) {
-            tc::unpack8(pipe::lds_sw128(tile, i, ((col & 63) + e) >> 3), r8);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dot = fmaf(r8[j], is_k ? t[e + j] : a[e + j], dot);
-          }
         }
         tc_fence_before();
         pipe::warp_arrive(acc_free);
-        if (!is_k) {
-          x.dot[sub][i] = dot;
-        } else if (i < n) {
-          dgall += dot;
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) dgall += __shfl_xor_sync(0xffffffffu, dgall, o);
-        if (lane == 0) x.part[warp - 2] = dgall;
+        if (!is_k) x.dot[sub][i] = fmaf(fa, read, dot);
         team_sync();
         if (warp == 2) {  // suffix sums, two rows a lane
           float d[2], end = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) end += x.part[e];
+          for (int e = 0; e < 4 * VB; ++e) end += p.dots[((size_t)slot * p.H + h) * 8 + e];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = 2 * lane + e;
@@ -455,13 +454,12 @@ void launch_dr_grads_tc(const DrProblem &p, const void *dout, long long dos, con
   args.p = p;
   args.g = g;
   args.wait = {p.status, p.wait_ns};
-  const uint64_t es = (uint64_t)p.H * p.dv * 2, chunks = (uint64_t)p.slots * p.H;
+  const uint64_t es = (uint64_t)p.H * p.dv * 2;
   if (!encode_tmap_bf16_heads(&args.q, p.q, p.dk, p.Hk, p.total, p.qs * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.k, p.k, p.dk, p.Hk, p.total, p.ks * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.dout, dout, p.dv, p.H, p.total, dos * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.z, p.Z, p.dv, p.H, p.total, es, kDrC) ||
-      !encode_tmap_bf16_heads(&args.e, p.E, p.dv, p.H, p.total, es, kDrC) ||
-      !encode_tmap_bf16_mats(&args.s, p.S, p.dk, p.dv, chunks) || !encode_tmap_bf16_mats(&args.ds, p.dS, p.dk, p.dv, chunks)) {
+      !encode_tmap_bf16_heads(&args.e, p.E, p.dv, p.H, p.total, es, kDrC)) {
     note_host_error();
     return;
   }

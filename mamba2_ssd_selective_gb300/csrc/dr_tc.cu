@@ -114,7 +114,8 @@ struct Args {
   float *last;         // and where it ends, or null
   bf16 *out;           // o's rows
   long long os;
-  bf16 *kept;  // (chunk, dv, dk): the state before each chunk, the gradient of the one behind
+  bf16 *kept;          // the state before each chunk, the gradient of the one behind
+  const bf16 *states;  // reverse: the states
   WaitCtl wait;
 };
 
@@ -467,10 +468,20 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
 #pragma unroll
         for (int x = 0; x < kCols; ++x) S[x] = col && a0 + x < p.dk ? in[(size_t)(a0 + x) * p.dv] : 0.f;
       }
+      // the thread's 8 x 16 bytes of a kept state, 64 VB apart
+      constexpr size_t kTile = 64 * KB * 64 * VB;
+      const size_t mine = ((size_t)(a0 / 8) * (64 * VB) + c) * 8;
+      auto keep = [&](size_t at) {  // rounded as the operand's first term is
+        uint4 *to = reinterpret_cast<uint4 *>(args.kept + at * kTile + mine);
+#pragma unroll
+        for (int x = 0; x < kCols; x += 8)
+          to[(x / 8) * (64 * VB)] = make_uint4(tc::pack_bf16x2(S[x], S[x + 1]), tc::pack_bf16x2(S[x + 2], S[x + 3]),
+                                               tc::pack_bf16x2(S[x + 4], S[x + 5]), tc::pack_bf16x2(S[x + 6], S[x + 7]));
+      };
+      const size_t chunks = (size_t)p.slots * p.H;
 #pragma unroll 1
       for (int i = 0; i < nc; ++i) {
         // the state's terms as A operands: lane = column of v, bf16 pairs along dk
-        bf16 *kept = MODE == kOut ? nullptr : args.kept + ((size_t)(slot0 + chunk(i)) * p.H + h) * dd + (size_t)c * p.dk + a0;
 #pragma unroll
         for (int x = 0; x < kCols; x += 32) {
           uint32_t hi[16], lo[16];
@@ -478,16 +489,28 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           for (int e = 0; e < 16; ++e) split2(S[x + 2 * e], S[x + 2 * e + 1], hi[e], lo[e]);
           tmem_st16_async(pipe::tmem_quad(tmem + kTmS, (a0 + x) / 2), hi);
           tmem_st16_async(pipe::tmem_quad(tmem + kTmS + 64, (a0 + x) / 2), lo);
-          if (MODE != kOut && c < p.dv) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              if (a0 + x + 2 * e < p.dk)
-                *reinterpret_cast<uint4 *>(kept + x + 2 * e) = make_uint4(hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
-          }
         }
         tmem_wait_st();
         tc_fence_before();
         pipe::warp_arrive(bar.s_ready);
+        // beside the chunk's products: the state for the gradients, and its product with its gradient, the state in
+        // bf16, the gradient as it is
+        const size_t at = (size_t)(slot0 + chunk(i)) * p.H + h;
+        if (MODE != kOut) keep(at);
+        if (kRev) {
+          const uint4 *from = reinterpret_cast<const uint4 *>(args.states + (i == 0 ? chunks + item : at + p.H) * kTile + mine);
+          float dot = 0.f;
+#pragma unroll
+          for (int x = 0; x < kCols; x += 8) {
+            float v[8];
+            tc::unpack8(from[(x / 8) * (64 * VB)], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(v[e], S[x + e], dot);
+          }
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+          if (lane == 0) p.dots[at * 8 + 2 * VB * sub + quad] = dot;
+        }
         wait_full(i);
         const float all_hi = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_hi)), all_lo = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_lo));
         pipe::warp_arrive(&bar.free[i % kStages]);
@@ -502,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         }
         tc_fence_before();
       }
+      if (MODE == kStates) keep(chunks + item);
       if (args.last && c < p.dv) {
         float *out = args.last + item * dd + c;
 #pragma unroll
@@ -674,6 +698,7 @@ void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, c
   args.first = dfin;
   args.last = dinit;
   args.kept = reinterpret_cast<bf16 *>(p.dS);
+  args.states = reinterpret_cast<const bf16 *>(p.S);
   run_boxes<kReverse>(args, s);
 }
 

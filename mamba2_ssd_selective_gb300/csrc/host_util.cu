@@ -74,18 +74,6 @@ bool encode_tmap_bf16_heads(CUtensorMap *map, const void *base, uint64_t width, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_tmap_bf16_mats(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t count) {
-  EncodeTiled fn = encoder();
-  if (!fn || (reinterpret_cast<uintptr_t>(base) & 15) || (cols * 2 & 15)) return false;
-  const cuuint64_t dims[3] = {cols, rows, count};
-  const cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool encode_tmap_f32_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t rows,
                            uint64_t row_bytes, uint32_t box_rows) {
   EncodeTiled fn = encoder();

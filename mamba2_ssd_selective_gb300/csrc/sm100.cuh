@@ -434,6 +434,17 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
   return d;
 }
 
+// The same without a swizzle, for an MN-major operand of 8 x 8 blocks whose 8 K-rows of 16 bytes (8 elements along MN)
+// follow each other: k_stride = bytes between blocks along K, mn_stride along MN.
+__device__ __forceinline__ uint64_t desc_blocks_mn(uint32_t saddr, uint32_t k_stride, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((k_stride >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((mn_stride >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;  // descriptor version for the sm_100 family
+  return d;
+}
+
 // Instruction descriptor, kind::f16 with bf16 A/B and fp32 accumulation.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4)                        // D format: f32

@@ -184,10 +184,7 @@ bool encode_tmap_f32_2d(CUtensorMap *map, const void *base, uint64_t cols, uint6
 // width and rows past the last read as zeros.
 bool encode_tmap_bf16_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t rows,
                             uint64_t row_bytes, uint32_t box_rows);
-// Host: `count` row-major (rows, cols) bf16 matrices behind one another as (cols, rows, count), box 64 x 64 of one matrix,
-// 128-byte swizzle; what lies past a matrix's edges reads as zeros.
-bool encode_tmap_bf16_mats(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t count);
-// Host: the same as encode_tmap_bf16_heads for fp32, a box of 16 columns, 64-byte swizzle.
+// Host: the same for fp32, a box of 16 columns, 64-byte swizzle.
 bool encode_tmap_f32_heads(CUtensorMap *map, const void *base, uint64_t width, uint64_t heads, uint64_t rows,
                            uint64_t row_bytes, uint32_t box_rows);
 // Host: SM count of the current device (cached per device).
