@@ -60,7 +60,7 @@ DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
     pl.Z = take(tokens * d->headdim_v * eb);
     pl.dqp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
     pl.dkp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
-    pl.dots = take(pl.tc ? chunks * 8 * 4 : 0);
+    pl.dots = take(pl.tc ? chunks * 4 * 4 : 0);
   }
   pl.total = off;
   return pl;

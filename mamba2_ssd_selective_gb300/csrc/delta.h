@@ -58,7 +58,7 @@ struct DrProblem {
   // (m / 8) 8 dv + 8 c + m % 8; behind the chunks' the final states of the sequences' heads.
   float *S, *dS, *E, *Z;
   float *dqp, *dkp;  // (total, H, dk): gradients of the unit q and k of each state head
-  float *dots;       // (chunk, 8): parts of <state behind the chunk, its gradient>, dv / 16 of them (dv padded)
+  float *dots;       // (chunk, 4): parts of <state behind the chunk, its gradient>, one for each 32 columns of dv
   int *status;       // device status word, cleared by the first kernel
   unsigned long long wait_ns;
 };

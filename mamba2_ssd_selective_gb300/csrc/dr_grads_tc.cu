@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         if (warp == 2) {  // suffix sums, two rows a lane
           float d[2], end = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4 * VB; ++e) end += p.dots[((size_t)slot * p.H + h) * 8 + e];
+          for (int e = 0; e < 2 * VB; ++e) end += p.dots[((size_t)slot * p.H + h) * 4 + e];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = 2 * lane + e;

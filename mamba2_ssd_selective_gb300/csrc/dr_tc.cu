@@ -47,7 +47,8 @@ template <int KB, int VB, int MODE> struct Layout {
   static constexpr uint32_t kK = 0, kQ = KB * kBox, kV = kQ + KB * kBox, kN = kV + VB * kBox, kP = kN + 2 * kBox;
   static constexpr uint32_t kRows = kP + 2 * kBox, kStage = (kRows + sizeof(DrRows) + 1023) / 1024 * 1024;
   static constexpr uint32_t kO = kStages * kStage;  // a chunk's outputs, on their way to TMA
-  static constexpr uint32_t kBar = kO + VB * kBox;
+  static constexpr uint32_t kKept = kO + VB * kBox;  // a kept state, likewise
+  static constexpr uint32_t kBar = kKept + (MODE == kOut ? 0 : KB * VB * kBox);
   static constexpr int kNumBars = 2 * kStages + 14;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
@@ -65,6 +66,7 @@ struct Bars {
   uint64_t *w_full;       // W
   uint64_t *q_full, *q_ready;  // outputs' part of the state formed / scaled; reverse: W's part of dO formed / its terms in TMEM
   uint64_t *o_full, *o_free;   // outputs formed / read; reverse: P^T dO
+  uint64_t *s_read;            // reverse: the state's terms have been read for the product with the state
   uint64_t *drain;
   __device__ explicit Bars(uint64_t *b) {
     full = b;
@@ -80,7 +82,8 @@ struct Bars {
     q_ready = patched + 8;
     o_full = patched + 9;
     o_free = patched + 10;
-    drain = patched + 11;
+    s_read = patched + 11;
+    drain = patched + 12;
   }
 };
 
@@ -138,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
   auto chunk = [&](int i) { return kRev ? nc - 1 - i : i; };
   auto live = [&](int i) { return min(kDrC, len - chunk(i) * kDrC); };
   const int tail = kRev ? 0 : nc - 1;
+  // reverse: the state behind the i-th chunk, the final one behind all chunks' first
+  auto behind = [&](int i) { return i == 0 ? ((size_t)p.slots + seq) * p.H + h : (size_t)(slot0 + chunk(i) + 1) * p.H + h; };
   const bool partial = len % kDrC != 0;  // the tail is
 
   if (warp == 0 && lane == 0) {
@@ -163,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     mbar_init(bar.q_ready, 2 * VB);
     mbar_init(bar.o_full, 1);
     mbar_init(bar.o_free, kRev ? 4 * VB : 2 * VB);
+    mbar_init(bar.s_read, 2 * VB);
     mbar_init(bar.drain, 1);
     fence_mbar_init();
   }
@@ -183,9 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
   };
 
   // The block is launched with 768 x 80 registers; the state's warps take what the first four do not need:
-  // 128 x (48 + 2 * 80 + 2 * 96 + 80) = 61440.
+  // 128 x (32 + 2 * 80 + 2 * 104 + 80) = 61440.
   if (warp < kElemWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
@@ -205,6 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           for (int b = 0; b < VB; ++b) tma_load_3d(base + L::kV + b * kBox, &args.v, &bar.full[st], 64 * b, h, row);
           pipe::bulk_load(base + L::kRows, p.rows + at, sizeof(DrRows), &bar.full[st]);
           pipe::bulk_load(base + L::kN, tiles, kMats, &bar.full[st]);  // N's terms, P's behind them
+          if (kRev)
+            pipe::bulk_prefetch(args.states + behind(i) * (64 * KB * 64 * VB), 2 * 64 * KB * 64 * VB);
           if (MODE != kStates)
             for (int b = 0; b < KB; ++b) tma_load_3d(base + L::kQ + b * kBox, &args.q, &bar.full[st], 64 * b, hk, row);
         }
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     }
   } else if (warp < kOutWarp0) {
     // ------------------------------------------------------------ state
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     const int quad = warp & 3, sub = (warp - kStateWarp0) >> 2;
     if (quad < 2 * VB) {
       constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
@@ -471,46 +479,42 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
       // the thread's 8 x 16 bytes of a kept state, 64 VB apart
       constexpr size_t kTile = 64 * KB * 64 * VB;
       const size_t mine = ((size_t)(a0 / 8) * (64 * VB) + c) * 8;
+      constexpr int kTeam = 128 * VB;
       auto keep = [&](size_t at) {  // rounded as the operand's first term is
-        uint4 *to = reinterpret_cast<uint4 *>(args.kept + at * kTile + mine);
+        if (sub + quad == 0 && lane == 0) bulk_wait_read0();
+        role_sync<4, kTeam>();
 #pragma unroll
         for (int x = 0; x < kCols; x += 8)
-          to[(x / 8) * (64 * VB)] = make_uint4(tc::pack_bf16x2(S[x], S[x + 1]), tc::pack_bf16x2(S[x + 2], S[x + 3]),
-                                               tc::pack_bf16x2(S[x + 4], S[x + 5]), tc::pack_bf16x2(S[x + 6], S[x + 7]));
+          pipe::sts_u4(s0 + L::kKept + 2 * (uint32_t)mine + (x / 8) * (64 * VB) * 16,
+                       make_uint4(tc::pack_bf16x2(S[x], S[x + 1]), tc::pack_bf16x2(S[x + 2], S[x + 3]),
+                                  tc::pack_bf16x2(S[x + 4], S[x + 5]), tc::pack_bf16x2(S[x + 6], S[x + 7])));
+        fence_async_smem();
+        role_sync<4, kTeam>();
+        if (sub + quad == 0 && lane == 0) {
+          pipe::bulk_store(args.kept + at * kTile, s0 + L::kKept, (uint32_t)kTile * 2);
+          bulk_commit();
+        }
       };
       const size_t chunks = (size_t)p.slots * p.H;
 #pragma unroll 1
       for (int i = 0; i < nc; ++i) {
         // the state's terms as A operands: lane = column of v, bf16 pairs along dk
+        if (kRev && i > 0) {
+          wait_on(bar.s_read, parity(i - 1), wait);
+          tc_fence_after();
+        }
 #pragma unroll
-        for (int x = 0; x < kCols; x += 32) {
-          uint32_t hi[16], lo[16];
+        for (int x = 0; x < kCols; x += 16) {
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) split2(S[x + 2 * e], S[x + 2 * e + 1], hi[e], lo[e]);
-          tmem_st16_async(pipe::tmem_quad(tmem + kTmS, (a0 + x) / 2), hi);
-          tmem_st16_async(pipe::tmem_quad(tmem + kTmS + 64, (a0 + x) / 2), lo);
+          for (int e = 0; e < 8; ++e) split2(S[x + 2 * e], S[x + 2 * e + 1], hi[e], lo[e]);
+          tmem_st8_async(pipe::tmem_quad(tmem + kTmS, (a0 + x) / 2), hi);
+          tmem_st8_async(pipe::tmem_quad(tmem + kTmS + 64, (a0 + x) / 2), lo);
         }
         tmem_wait_st();
         tc_fence_before();
         pipe::warp_arrive(bar.s_ready);
-        // beside the chunk's products: the state for the gradients, and its product with its gradient, the state in
-        // bf16, the gradient as it is
-        const size_t at = (size_t)(slot0 + chunk(i)) * p.H + h;
-        if (MODE != kOut) keep(at);
-        if (kRev) {
-          const uint4 *from = reinterpret_cast<const uint4 *>(args.states + (i == 0 ? chunks + item : at + p.H) * kTile + mine);
-          float dot = 0.f;
-#pragma unroll
-          for (int x = 0; x < kCols; x += 8) {
-            float v[8];
-            tc::unpack8(from[(x / 8) * (64 * VB)], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dot = fmaf(v[e], S[x + e], dot);
-          }
-#pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-          if (lane == 0) p.dots[at * 8 + 2 * VB * sub + quad] = dot;
-        }
+        if (MODE != kOut) keep((size_t)(slot0 + chunk(i)) * p.H + h);  // beside the chunk's products
         wait_full(i);
         const float all_hi = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_hi)), all_lo = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_lo));
         pipe::warp_arrive(&bar.free[i % kStages]);
@@ -526,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         tc_fence_before();
       }
       if (MODE == kStates) keep(chunks + item);
+      if (MODE != kOut && sub + quad == 0 && lane == 0) bulk_wait0();
       if (args.last && c < p.dv) {
         float *out = args.last + item * dd + c;
 #pragma unroll
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
       if (tt == 0) bulk_wait0();
     }
   } else if (kRev) {
-    // ------------------------------------------------------------ the terms of (qin dO)^T
+    // ------------------------------------------------------------ the terms of (qin dO)^T, <state, its gradient>
     const int quad = warp & 3;
     if (quad < 2 * VB) {
       const uint32_t lr = (lane & 7) + 8 * (lane >> 4), lc = 4 * (quad & 1) + ((lane >> 3) & 1);
@@ -638,6 +643,37 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         tc_fence_before();
         pipe::warp_arrive(bar.q_ready);
         pipe::warp_arrive(&bar.free[i % kStages]);
+        // the state behind the chunk, in bf16, times its gradient's two terms
+        const uint4 *from = reinterpret_cast<const uint4 *>(args.states + behind(i) * (64 * KB * 64 * VB)) + 32 * quad + lane;
+        float dot = 0.f;
+#pragma unroll
+        for (int x = 0; x < KB; ++x) {
+          uint4 s[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] = __ldcg(from + (8 * x + e) * (64 * VB));
+          if (x == 0) {
+            wait_on(bar.s_ready, parity(i), wait);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            uint32_t hi[16], lo[16];
+            tmem_ld16_async(lanes + kTmS + 32 * x + 4 * e, hi);
+            tmem_ld16_async(lanes + kTmS + 64 + 32 * x + 4 * e, lo);
+            tmem_wait_ld(hi, lo);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t w = j % 4 == 0 ? s[e + j / 4].x : j % 4 == 1 ? s[e + j / 4].y : j % 4 == 2 ? s[e + j / 4].z : s[e + j / 4].w;
+              dot = fmaf(lo_f(w), lo_f(hi[j]) + lo_f(lo[j]), dot);
+              dot = fmaf(hi_f(w), hi_f(hi[j]) + hi_f(lo[j]), dot);
+            }
+          }
+        }
+        tc_fence_before();
+        pipe::warp_arrive(bar.s_read);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) p.dots[((size_t)(slot0 + chunk(i)) * p.H + h) * 4 + quad] = dot;
       }
     }
   }
