@@ -11,7 +11,7 @@
 // Persistent CTAs; a CTA takes a chunk and a head of q and k and goes through the states that share it, dq and dk
 // staying in registers.  Lanes 0-63 of the accumulators are the rows of dO and dq, lanes 64-127 those of Z and dk:
 //     [dO; Z] S^T,   [dO; Z] E^T,   [Q; K] K^T,   [.; E] dS^T,   [Wq; Wk] K,   [.; Wq^T Wk^T] [Q; K]
-// Warps: 0 TMA producer, 1 MMA issuer, 2-9 everything else.  A state's tensors are loaded again as soon as their products
+// Warps: 0 TMA producer, 1 MMA issuer, 2-9 weights and gradients, 10 the decays' suffix sums.  A state's tensors are loaded again as soon as their products
 // are made, beside the weights, the last two products and the sums.  Operands are rounded to bf16 (the outputs are bf16).
 #include "delta.h"
 #include "tc_pipe.cuh"
@@ -25,12 +25,17 @@ using bf16 = __nv_bfloat16;
 using namespace sm100;
 using pipe::parity;
 
-constexpr int kThreads = 320, kTeam = 256;
+constexpr int kThreads = 352, kTeam = 256;
 constexpr uint32_t kBox = 8192;  // [64 rows x 64 columns] bf16
 constexpr uint32_t kTmA = 0, kTmC = 128, kTmW = 256, kTmB = 384, kTmCols = 512;  // products with S, dS, K (before: Q K^T); with E and, later, [Q; K]
 
+// rows' sums of a step, by the step's parity: a step's are read while the next one's are made
+struct Sums {
+  float vdv[64], dot[2][64], kb[64];  // kb: beta / |k|
+};
 struct Misc {
-  float vdv[64], dot[2][64], dot2[2][64];
+  Sums sums[2];
+  float along[2][2][64], length[2][2][64];  // of dq and dk along q and k, and their lengths, by halves
 };
 template <int KB, int VB> struct Layout {
   static constexpr uint32_t kIn = 0;                             // dO, Z, E: boxes of each 64 columns behind one another
@@ -41,7 +46,7 @@ template <int KB, int VB> struct Layout {
   static constexpr uint32_t kRows = kW + 2 * kBox;
   static constexpr uint32_t kMisc = kRows + (sizeof(DrRows) + 15) / 16 * 16;
   static constexpr uint32_t kBar = kMisc + sizeof(Misc);
-  static constexpr uint32_t kEnd = kBar + 10 * 8 + 16;
+  static constexpr uint32_t kEnd = kBar + 14 * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -85,8 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
   const WaitCtl wait = args.wait;
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
   uint64_t *in_full = bar, *in_free = bar + 1, *qk_full = bar + 2, *qk_free = bar + 3, *b_full = bar + 4, *w_ready = bar + 5,
-           *out_full = bar + 6, *acc_free = bar + 7, *drain = bar + 8;
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + 10 * 8);
+           *out_full = bar + 6, *acc_free = bar + 7, *drain = bar + 8, *sums_full = bar + 9, *sums_free = bar + 11;
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + 14 * 8);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (warp == 0 && lane < 5) prefetch_tmap(&args.q + lane);
   if (threadIdx.x == 32) {
@@ -99,6 +104,10 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
     mbar_init(out_full, 1);
     mbar_init(acc_free, 8);
     mbar_init(drain, 1);
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(&sums_full[e], 8);
+      mbar_init(&sums_free[e], 1);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -224,13 +233,51 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
       mbar_wait_drain(out_full, parity(m - 1));
       mbar_wait_drain(qk_free, parity(c - 1));
     }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ suffix sums of the decays' gradients, two rows a lane
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
+      int slot, hk, t0, n;
+      unit_at(u, slot, hk, t0, n);
+      if (n == 0) continue;
+#pragma unroll 1
+      for (int y = 0; y < p.group; ++y, ++m) {
+        const int h = hk * p.group + y;
+        const Sums &x = reinterpret_cast<const Sums *>(sm + L::kMisc)[m & 1];
+        float end = lane < 2 * VB ? p.dots[((size_t)slot * p.H + h) * 4 + lane] : 0.f, d[2];
+        wait_on(&sums_full[m & 1], parity(m / 2), wait);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 2 * lane + e;
+          d[e] = r < n ? (x.dot[0][r] + x.dot[1][r]) - x.vdv[r] : 0.f;
+        }
+        pipe::warp_arrive(&sums_free[m & 1]);
+#pragma unroll
+        for (int o = VB; o >= 1; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+        end = __shfl_sync(0xffffffffu, end, 0);
+        d[0] += d[1];
+        float after = d[0];
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const float z = __shfl_down_sync(0xffffffffu, after, o);
+          if (lane + o < 32) after += z;
+        }
+        after -= d[0];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 2 * lane + e;
+          if (r < n) static_cast<bf16 *>(g.dg)[(size_t)(t0 + r) * g.dgs + h] = __float2bfloat16_rn(d[e] + after + end);
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ weights and gradients
     constexpr int kCols = 32 * KB;  // columns of dk of a thread
     const int et = threadIdx.x - 64, quad = warp & 3, sub = (warp - 2) >> 2;
     const bool is_k = quad >= 2;                       // lanes 64-127: rows of Z and dk
     const int i = 32 * (quad & 1) + lane;              // the thread's row
-    Misc &x = *reinterpret_cast<Misc *>(sm + L::kMisc);
+    Misc &misc = *reinterpret_cast<Misc *>(sm + L::kMisc);
     const DrRows &rw = *reinterpret_cast<const DrRows *>(sm + L::kRows);
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     uint32_t m = 0, c = 0;
@@ -245,37 +292,63 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
 #pragma unroll 1
       for (int y = 0; y < p.group; ++y, ++m) {
         const int h = hk * p.group + y;
-        wait_on(in_full, parity(m), wait);
-        // dv, dbeta, v.dv: 16 bytes of a row at a time
+        Sums &x = reinterpret_cast<Sums *>(sm + L::kMisc)[m & 1];
+        // what comes from global memory, before it is needed
+        constexpr int kRounds = 2 * VB;  // 16 bytes of a row a thread and round
+        uint4 vw[kRounds];
 #pragma unroll
-        for (int e = et; e < 64 * 8 * VB; e += kTeam) {
-          const int r = e / (8 * VB), b = e % (8 * VB) >> 3, ch = e & 7, col = 64 * b + 8 * ch;
-          float vdv = 0.f, db = 0.f;
+        for (int e = 0; e < kRounds; ++e) {
+          const int r = (et + kTeam * e) / (8 * VB), col = 8 * ((et + kTeam * e) % (8 * VB));
+          vw[e] = r < n && col < p.dv ? tc::ldg16(static_cast<const bf16 *>(p.v) + (size_t)(t0 + r) * p.vs + (size_t)h * p.dv + col) : make_uint4(0, 0, 0, 0);
+        }
+        if (m >= 2) wait_on(&sums_free[m & 1], parity(m / 2 - 1), wait);
+        wait_on(in_full, parity(m), wait);
+        // dv, dbeta, v.dv: the rounds side by side
+        uint4 zw[kRounds], ew[kRounds];
+        float vdv[kRounds], db[kRounds];
+#pragma unroll
+        for (int o = 0; o < kRounds; ++o) {
+          const int e = et + kTeam * o, r = e / (8 * VB), b = e % (8 * VB) >> 3;
+          const uint8_t *at = sm + L::kIn + 3 * b * kBox + sw128_offset(r, 8 * (e & 7));
+          zw[o] = *reinterpret_cast<const uint4 *>(at + kBox);
+          ew[o] = *reinterpret_cast<const uint4 *>(at + 2 * kBox);
+        }
+        if (et < 64) x.kb[et] = rw.rk[et] * rw.beta[et];
+#pragma unroll
+        for (int o = 0; o < kRounds; ++o) {
+          const int e = et + kTeam * o, r = e / (8 * VB), col = 8 * (e % (8 * VB));
+          vdv[o] = db[o] = 0.f;
           if (r < n && col < p.dv) {
-            const uint4 zw = pipe::lds_sw128(s0 + L::kIn + (3 * b + 1) * kBox, r, ch), ew = pipe::lds_sw128(s0 + L::kIn + (3 * b + 2) * kBox, r, ch);
-            const uint4 vw = tc::ldg16(static_cast<const bf16 *>(p.v) + (size_t)(t0 + r) * p.vs + (size_t)h * p.dv + col);
-            db = dot8(zw, ew, 0.f);
+            db[o] = dot8(zw[o], ew[o], 0.f);
             float z[8], v[8];
-            tc::unpack8(zw, z);
-            tc::unpack8(vw, v);
+            tc::unpack8(zw[o], z);
+            tc::unpack8(vw[o], v);
             const float beta = rw.beta[r];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               z[j] *= beta;
-              vdv = fmaf(v[j], z[j], vdv);
+              vdv[o] = fmaf(v[j], z[j], vdv[o]);
             }
             *reinterpret_cast<uint4 *>(static_cast<bf16 *>(g.dv) + (size_t)(t0 + r) * g.dvs + (size_t)h * p.dv + col) = tc::pack8(z);
           }
+        }
 #pragma unroll
-          for (int o = 4 * VB; o >= 1; o >>= 1) {
-            vdv += __shfl_xor_sync(0xffffffffu, vdv, o);
-            db += __shfl_xor_sync(0xffffffffu, db, o);
-          }
-          if (e % (8 * VB) == 0) {
-            x.vdv[r] = vdv;
-            if (r < n) static_cast<bf16 *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = __float2bfloat16_rn(db);
+        for (int z = 4 * VB; z >= 1; z >>= 1) {
+#pragma unroll
+          for (int o = 0; o < kRounds; ++o) {
+            vdv[o] += __shfl_xor_sync(0xffffffffu, vdv[o], z);
+            db[o] += __shfl_xor_sync(0xffffffffu, db[o], z);
           }
         }
+#pragma unroll
+        for (int o = 0; o < kRounds; ++o) {
+          const int e = et + kTeam * o, r = e / (8 * VB);
+          if (e % (8 * VB) == 0) {
+            x.vdv[r] = vdv[o];
+            if (r < n) static_cast<bf16 *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = __float2bfloat16_rn(db[o]);
+          }
+        }
+        team_sync();  // kb
         // weights
         const float rk_i = rw.rk[i], rq_i = rw.rq[i], beta_i = rw.beta[i];
         const float fa = is_k ? -rw.kin[i] * beta_i : rw.qin[i], fc = rw.kout[i] * beta_i;
@@ -299,10 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
           float v[16], w8[8];
           tmem_ld16(lanes + kTmB + j0, v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = j0 + e;
-            const float f = __expf((hi - rw.ghi[j]) + (lo - rw.glo[j])) * (rw.rk[j] * rw.beta[j]);
-            v[e] = j <= last ? v[e] * (f * fw) : 0.f;
+          for (int e = 0; e < 16; e += 4) {
+            const float4 gh = *reinterpret_cast<const float4 *>(rw.ghi + j0 + e), gl = *reinterpret_cast<const float4 *>(rw.glo + j0 + e),
+                         kb = *reinterpret_cast<const float4 *>(x.kb + j0 + e);
+            const float f[4] = {__expf((hi - gh.x) + (lo - gl.x)) * kb.x, __expf((hi - gh.y) + (lo - gl.y)) * kb.y,
+                                __expf((hi - gh.z) + (lo - gl.z)) * kb.z, __expf((hi - gh.w) + (lo - gl.w)) * kb.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[e + j] = j0 + e + j <= last ? v[e + j] * (f[j] * fw) : 0.f;
           }
           if (!is_k) {
             float qk[16];
@@ -360,31 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         tc_fence_before();
         pipe::warp_arrive(acc_free);
         if (!is_k) x.dot[sub][i] = fmaf(fa, read, dot);
-        team_sync();
-        if (warp == 2) {  // suffix sums, two rows a lane
-          float d[2], end = 0.f;
-#pragma unroll
-          for (int e = 0; e < 2 * VB; ++e) end += p.dots[((size_t)slot * p.H + h) * 4 + e];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 2 * lane + e;
-            d[e] = r < n ? (x.dot[0][r] + x.dot[1][r]) - x.vdv[r] : 0.f;
-          }
-          d[0] += d[1];
-          float after = d[0];
-#pragma unroll
-          for (int o = 1; o < 32; o *= 2) {
-            const float z = __shfl_down_sync(0xffffffffu, after, o);
-            if (lane + o < 32) after += z;
-          }
-          after -= d[0];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 2 * lane + e;
-            if (r < n) static_cast<bf16 *>(g.dg)[(size_t)(t0 + r) * g.dgs + h] = __float2bfloat16_rn(d[e] + after + end);
-          }
-        }
-        team_sync();
+        pipe::warp_arrive(&sums_full[m & 1]);
       }
       // the division by the lengths, and out
       const uint32_t tile0 = s0 + L::kQK + (is_k ? kBox : 0);
@@ -401,12 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
             len = fmaf(r8[j], r8[j], len);
           }
         }
-        float(*d)[64] = is_k ? x.dot2 : x.dot;
-        d[sub][i] = dot;
-        float *l = reinterpret_cast<float *>(sm + L::kW) + (is_k ? 128 : 0);
-        l[64 * sub + i] = len;
+        misc.along[is_k][sub][i] = dot;
+        misc.length[is_k][sub][i] = len;
         team_sync();
-        f = (d[0][i] + d[1][i]) / (l[i] + l[64 + i] + p.eps);
+        f = (misc.along[is_k][0][i] + misc.along[is_k][1][i]) / (misc.length[is_k][0][i] + misc.length[is_k][1][i] + p.eps);
       }
       const int head = hk * p.dk;
       bf16 *out = is_k ? static_cast<bf16 *>(g.dk) + (size_t)(t0 + i) * g.dks + head : static_cast<bf16 *>(g.dq) + (size_t)(t0 + i) * g.dqs + head;
@@ -427,7 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
       }
       pipe::warp_arrive(qk_free);
       ++c;
-      team_sync();
     }
   }
 
