@@ -35,24 +35,26 @@ struct Sums {
 };
 struct Misc {
   Sums sums[2];
-  float along[2][2][64], length[2][2][64];  // of dq and dk along q and k, and their lengths, by halves
+  float along[2][2][64];  // of dq and dk along q and k, by halves
 };
 template <int KB, int VB> struct Layout {
   static constexpr uint32_t kIn = 0;                             // dO, Z, E: boxes of each 64 columns behind one another
   static constexpr uint32_t kTile = KB * VB * kBox;
   static constexpr uint32_t kS = VB * 3 * kBox, kDs = kS + kTile;  // blocks of 8 columns of dk, all rows
   static constexpr uint32_t kQK = kDs + kTile;         // Q, K: likewise pairs
-  static constexpr uint32_t kW = kQK + KB * 2 * kBox;           // Wq, Wk
-  static constexpr uint32_t kRows = kW + 2 * kBox;
+  static constexpr uint32_t kQKs = KB * 2 * kBox;               // two buffers
+  static constexpr uint32_t kW = kQK + 2 * kQKs;                // Wq, Wk
+  static constexpr uint32_t kV = kW + 2 * kBox;
+  static constexpr uint32_t kRows = kV + VB * kBox;
   static constexpr uint32_t kMisc = kRows + (sizeof(DrRows) + 15) / 16 * 16;
   static constexpr uint32_t kBar = kMisc + sizeof(Misc);
-  static constexpr uint32_t kEnd = kBar + 14 * 8 + 16;
+  static constexpr uint32_t kEnd = kBar + 18 * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
 struct Args {
-  CUtensorMap q, k, dout, z, e;
+  CUtensorMap q, k, dout, z, e, v, dq, dk;
   DrProblem p;
   DrGrads g;
   WaitCtl wait;
@@ -89,16 +91,18 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
   const DrGrads &g = args.g;
   const WaitCtl wait = args.wait;
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
-  uint64_t *in_full = bar, *in_free = bar + 1, *qk_full = bar + 2, *qk_free = bar + 3, *b_full = bar + 4, *w_ready = bar + 5,
-           *out_full = bar + 6, *acc_free = bar + 7, *drain = bar + 8, *sums_full = bar + 9, *sums_free = bar + 11;
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + 14 * 8);
+  // rows (dO, Z, E, v, the factors) and states loaded / read; the others' names say what they are of
+  uint64_t *in_full = bar, *in_free = bar + 1, *st_full = bar + 2, *st_free = bar + 3, *b_full = bar + 4, *w_ready = bar + 5,
+           *out_full = bar + 6, *acc_free = bar + 7, *drain = bar + 8, *sums_full = bar + 9, *sums_free = bar + 11,
+           *qk_full = bar + 13, *qk_free = bar + 15;  // [2] each
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + 18 * 8);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (warp == 0 && lane < 5) prefetch_tmap(&args.q + lane);
+  if (warp == 0 && lane < 8) prefetch_tmap(&args.q + lane);
   if (threadIdx.x == 32) {
     mbar_init(in_full, 1);
     mbar_init(in_free, 9);
-    mbar_init(qk_full, 1);
-    mbar_init(qk_free, 9);
+    mbar_init(st_full, 1);
+    mbar_init(st_free, 1);
     mbar_init(b_full, 1);
     mbar_init(w_ready, 8);
     mbar_init(out_full, 1);
@@ -107,6 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
     for (int e = 0; e < 2; ++e) {
       mbar_init(&sums_full[e], 8);
       mbar_init(&sums_free[e], 1);
+      mbar_init(&qk_full[e], 1);
+      mbar_init(&qk_free[e], 9);
     }
     fence_mbar_init();
   }
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      uint32_t m = 0, c = 0;  // steps (a chunk and a state head), units
+      uint32_t m = 0, ms = 0, c = 0;  // steps (a chunk and a state head), their states' loads, units
       bool ok = true;
 #pragma unroll 1
       for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
@@ -141,36 +147,47 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         for (int y = 0; y < p.group && ok; ++y, ++m) {
           const int h = hk * p.group + y;
           const size_t at = (size_t)slot * p.H + h;
+          // a unit's q and k first: they are free the longest
+          if (y == 0) {
+            if (c >= 2 && !wait_on(&qk_free[c & 1], parity(c / 2 - 1), wait)) {
+              ok = false;
+              break;
+            }
+            uint8_t *to = sm + L::kQK + (c & 1) * L::kQKs;
+            mbar_expect_tx(&qk_full[c & 1], 2 * KB * kBox);
+            for (int b = 0; b < KB; ++b) {
+              tma_load_3d(to + (2 * b) * kBox, &args.q, &qk_full[c & 1], 64 * b, hk, t0);
+              tma_load_3d(to + (2 * b + 1) * kBox, &args.k, &qk_full[c & 1], 64 * b, hk, t0);
+            }
+            ++c;
+          }
+          if (m > 0 && !wait_on(st_free, parity(m - 1), wait)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(st_full, 2 * L::kTile);
+          pipe::bulk_load(sm + L::kS, reinterpret_cast<const uint8_t *>(p.S) + at * L::kTile, L::kTile, st_full);
+          pipe::bulk_load(sm + L::kDs, reinterpret_cast<const uint8_t *>(p.dS) + at * L::kTile, L::kTile, st_full);
+          ++ms;
           if (m > 0 && !wait_on(in_free, parity(m - 1), wait)) {
             ok = false;
             break;
           }
-          mbar_expect_tx(in_full, (3 * VB + 2 * KB * VB) * kBox + (uint32_t)sizeof(DrRows));
+          mbar_expect_tx(in_full, 4 * VB * kBox + (uint32_t)sizeof(DrRows));
+          pipe::bulk_load(sm + L::kRows, p.rows + at, sizeof(DrRows), in_full);
           for (int b = 0; b < VB; ++b) {
             tma_load_3d(sm + L::kIn + (3 * b) * kBox, &args.dout, in_full, 64 * b, h, t0);
             tma_load_3d(sm + L::kIn + (3 * b + 1) * kBox, &args.z, in_full, 64 * b, h, t0);
             tma_load_3d(sm + L::kIn + (3 * b + 2) * kBox, &args.e, in_full, 64 * b, h, t0);
-          }
-          pipe::bulk_load(sm + L::kS, reinterpret_cast<const uint8_t *>(p.S) + at * L::kTile, L::kTile, in_full);
-          pipe::bulk_load(sm + L::kDs, reinterpret_cast<const uint8_t *>(p.dS) + at * L::kTile, L::kTile, in_full);
-          pipe::bulk_load(sm + L::kRows, p.rows + at, sizeof(DrRows), in_full);
-          if (y == 0) {
-            if (c > 0 && !wait_on(qk_free, parity(c - 1), wait)) {
-              ok = false;
-              ++m;
-              break;
-            }
-            mbar_expect_tx(qk_full, 2 * KB * kBox);
-            for (int b = 0; b < KB; ++b) {
-              tma_load_3d(sm + L::kQK + (2 * b) * kBox, &args.q, qk_full, 64 * b, hk, t0);
-              tma_load_3d(sm + L::kQK + (2 * b + 1) * kBox, &args.k, qk_full, 64 * b, hk, t0);
-            }
-            ++c;
+            tma_load_3d(sm + L::kV + b * kBox, &args.v, in_full, 64 * b, h, t0);
           }
         }
       }
+      // every load issued has landed before the CTA releases its shared memory
       if (m > 0) mbar_wait_drain(in_full, parity(m - 1));
-      if (c > 0) mbar_wait_drain(qk_full, parity(c - 1));
+      if (ms > 0) mbar_wait_drain(st_full, parity(ms - 1));
+#pragma unroll 1
+      for (uint32_t x = c > 2 ? c - 2 : 0; x < c; ++x) mbar_wait_drain(&qk_full[x & 1], parity(x / 2));
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -199,28 +216,32 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
 #pragma unroll
         for (int b = 0; b < VB; ++b)  // [dO; Z] E^T
           pipe::umma_k_el<4>(el, tmem + kTmB, dIn + 3 * b * kB, dIn + (3 * b + 2) * kB, pipe::kStepK, pipe::kStepK, iB, b > 0);
+        const uint64_t qk = (uint64_t)((c & 1) * (L::kQKs / 16));
         if (y == 0) {
-          wait_on(qk_full, parity(c), wait);
+          wait_on(&qk_full[c & 1], parity(c / 2), wait);
           tc_fence_after();
         }
 #pragma unroll
         for (int b = 0; b < KB; ++b)  // [Q; K] K^T
-          pipe::umma_k_el<4>(el, tmem + kTmW, dQKk + 2 * b * kB, dQKk + (2 * b + 1) * kB, pipe::kStepK, pipe::kStepK, iB, b > 0);
+          pipe::umma_k_el<4>(el, tmem + kTmW, dQKk + qk + 2 * b * kB, dQKk + qk + (2 * b + 1) * kB, pipe::kStepK, pipe::kStepK, iB, b > 0);
         umma_commit_el(el, b_full);
+        wait_on(st_full, parity(m), wait);
+        tc_fence_after();
 #pragma unroll
         for (int b = 0; b < VB; ++b)  // [dO; Z] S^T
           pipe::umma_k_el<4>(el, tmem + kTmA, dIn + 3 * b * kB, dS + b * 64, pipe::kStepK, 16, iN, b > 0);
 #pragma unroll
         for (int b = 0; b < VB; ++b)  // [Z; E] dS^T
           pipe::umma_k_el<4>(el, tmem + kTmC, dIn + (3 * b + 1) * kB, dDs + b * 64, pipe::kStepK, 16, iN, b > 0);
+        umma_commit_el(el, st_free);
         umma_commit_el(el, in_free);
         wait_on(w_ready, parity(m), wait);
         tc_fence_after();
-        pipe::umma_k_el<4>(el, tmem + kTmW, dW, dQK + kB, pipe::kStepK, pipe::kStepMN, iN, false);          // [Wq; Wk] K
-        pipe::umma_k_el<8>(el, tmem + kTmB, dWt, dQK, pipe::kStepMN, pipe::kStepMN, iT, false);             // [Wq^T Wk^T] [Q; K]
+        pipe::umma_k_el<4>(el, tmem + kTmW, dW, dQK + qk + kB, pipe::kStepK, pipe::kStepMN, iN, false);          // [Wq; Wk] K
+        pipe::umma_k_el<8>(el, tmem + kTmB, dWt, dQK + qk, pipe::kStepMN, pipe::kStepMN, iT, false);             // [Wq^T Wk^T] [Q; K]
         umma_commit_el(el, out_full);
         if (y + 1 == p.group) {
-          umma_commit_el(el, qk_free);
+          umma_commit_el(el, &qk_free[c & 1]);
           ++c;
         }
       }
@@ -229,9 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
     mbar_wait_drain(drain, 0);
     if (m > 0) {
       mbar_wait_drain(in_free, parity(m - 1));
+      mbar_wait_drain(st_free, parity(m - 1));
       mbar_wait_drain(b_full, parity(m - 1));
       mbar_wait_drain(out_full, parity(m - 1));
-      mbar_wait_drain(qk_free, parity(c - 1));
+#pragma unroll 1
+      for (uint32_t x = c > 2 ? c - 2 : 0; x < c; ++x) mbar_wait_drain(&qk_free[x & 1], parity(x / 2));
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------ suffix sums of the decays' gradients, two rows a lane
@@ -286,79 +309,30 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
       int slot, hk, t0, n;
       unit_at(u, slot, hk, t0, n);
       if (n == 0) continue;
-      float acc[kCols];
+      const uint32_t qk0 = s0 + L::kQK + (c & 1) * L::kQKs;
+      float len = 0.f;  // 1 / |q|^2 or 1 / |k|^2
+      float acc[kCols], along = 0.f;  // along: q.dq or k.dk, the thread's part
 #pragma unroll
       for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
 #pragma unroll 1
       for (int y = 0; y < p.group; ++y, ++m) {
         const int h = hk * p.group + y;
         Sums &x = reinterpret_cast<Sums *>(sm + L::kMisc)[m & 1];
-        // what comes from global memory, before it is needed
-        constexpr int kRounds = 2 * VB;  // 16 bytes of a row a thread and round
-        uint4 vw[kRounds];
-#pragma unroll
-        for (int e = 0; e < kRounds; ++e) {
-          const int r = (et + kTeam * e) / (8 * VB), col = 8 * ((et + kTeam * e) % (8 * VB));
-          vw[e] = r < n && col < p.dv ? tc::ldg16(static_cast<const bf16 *>(p.v) + (size_t)(t0 + r) * p.vs + (size_t)h * p.dv + col) : make_uint4(0, 0, 0, 0);
-        }
         if (m >= 2) wait_on(&sums_free[m & 1], parity(m / 2 - 1), wait);
         wait_on(in_full, parity(m), wait);
-        // dv, dbeta, v.dv: the rounds side by side
-        uint4 zw[kRounds], ew[kRounds];
-        float vdv[kRounds], db[kRounds];
-#pragma unroll
-        for (int o = 0; o < kRounds; ++o) {
-          const int e = et + kTeam * o, r = e / (8 * VB), b = e % (8 * VB) >> 3;
-          const uint8_t *at = sm + L::kIn + 3 * b * kBox + sw128_offset(r, 8 * (e & 7));
-          zw[o] = *reinterpret_cast<const uint4 *>(at + kBox);
-          ew[o] = *reinterpret_cast<const uint4 *>(at + 2 * kBox);
-        }
         if (et < 64) x.kb[et] = rw.rk[et] * rw.beta[et];
-#pragma unroll
-        for (int o = 0; o < kRounds; ++o) {
-          const int e = et + kTeam * o, r = e / (8 * VB), col = 8 * (e % (8 * VB));
-          vdv[o] = db[o] = 0.f;
-          if (r < n && col < p.dv) {
-            db[o] = dot8(zw[o], ew[o], 0.f);
-            float z[8], v[8];
-            tc::unpack8(zw[o], z);
-            tc::unpack8(vw[o], v);
-            const float beta = rw.beta[r];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              z[j] *= beta;
-              vdv[o] = fmaf(v[j], z[j], vdv[o]);
-            }
-            *reinterpret_cast<uint4 *>(static_cast<bf16 *>(g.dv) + (size_t)(t0 + r) * g.dvs + (size_t)h * p.dv + col) = tc::pack8(z);
-          }
-        }
-#pragma unroll
-        for (int z = 4 * VB; z >= 1; z >>= 1) {
-#pragma unroll
-          for (int o = 0; o < kRounds; ++o) {
-            vdv[o] += __shfl_xor_sync(0xffffffffu, vdv[o], z);
-            db[o] += __shfl_xor_sync(0xffffffffu, db[o], z);
-          }
-        }
-#pragma unroll
-        for (int o = 0; o < kRounds; ++o) {
-          const int e = et + kTeam * o, r = e / (8 * VB);
-          if (e % (8 * VB) == 0) {
-            x.vdv[r] = vdv[o];
-            if (r < n) static_cast<bf16 *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = __float2bfloat16_rn(db[o]);
-          }
-        }
-        team_sync();  // kb
+        team_sync();
         // weights
         const float rk_i = rw.rk[i], rq_i = rw.rq[i], beta_i = rw.beta[i];
         const float fa = is_k ? -rw.kin[i] * beta_i : rw.qin[i], fc = rw.kout[i] * beta_i;
         const float hi = rw.ghi[i], lo = rw.glo[i];
+        len = is_k ? rk_i * rk_i : rq_i * rq_i;
         if (y == 0) {
           if (n < kDrC) {  // rows past the end belong to another sequence
-            wait_on(qk_full, parity(c), wait);
+            wait_on(&qk_full[c & 1], parity(c / 2), wait);
             for (int e = et; e < (kDrC - n) * 16 * KB; e += kTeam) {
               const int b = e % (16 * KB), r = n + e / (16 * KB);
-              pipe::sts_u4(s0 + L::kQK + (uint32_t)(b >> 3) * kBox + sw128_offset(r, 8 * (b & 7)), make_uint4(0, 0, 0, 0));
+              pipe::sts_u4(qk0 + (uint32_t)(b >> 3) * kBox + sw128_offset(r, 8 * (b & 7)), make_uint4(0, 0, 0, 0));
             }
           }
         }
@@ -396,28 +370,64 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         tc_fence_before();
         fence_async_smem();
         pipe::warp_arrive(w_ready);
+        constexpr int kRounds = 2 * VB;  // 16 bytes of a row a thread and round
+        // dv, dbeta, v.dv: the rounds side by side
+        uint4 zw[kRounds], ew[kRounds], vw[kRounds];
+        float vdv[kRounds], db[kRounds];
+#pragma unroll
+        for (int o = 0; o < kRounds; ++o) {
+          const int e = et + kTeam * o, r = e / (8 * VB), b = e % (8 * VB) >> 3;
+          const uint32_t at = sw128_offset(r, 8 * (e & 7));
+          zw[o] = *reinterpret_cast<const uint4 *>(sm + L::kIn + (3 * b + 1) * kBox + at);
+          ew[o] = *reinterpret_cast<const uint4 *>(sm + L::kIn + (3 * b + 2) * kBox + at);
+          vw[o] = *reinterpret_cast<const uint4 *>(sm + L::kV + b * kBox + at);
+        }
+#pragma unroll
+        for (int o = 0; o < kRounds; ++o) {
+          const int e = et + kTeam * o, r = e / (8 * VB), col = 8 * (e % (8 * VB));
+          vdv[o] = db[o] = 0.f;
+          if (r < n && col < p.dv) {
+            db[o] = dot8(zw[o], ew[o], 0.f);
+            float z[8], v[8];
+            tc::unpack8(zw[o], z);
+            tc::unpack8(vw[o], v);
+            const float beta = rw.beta[r];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              z[j] *= beta;
+              vdv[o] = fmaf(v[j], z[j], vdv[o]);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<bf16 *>(g.dv) + (size_t)(t0 + r) * g.dvs + (size_t)h * p.dv + col) = tc::pack8(z);
+          }
+        }
+#pragma unroll
+        for (int z = 4 * VB; z >= 1; z >>= 1) {
+#pragma unroll
+          for (int o = 0; o < kRounds; ++o) {
+            vdv[o] += __shfl_xor_sync(0xffffffffu, vdv[o], z);
+            db[o] += __shfl_xor_sync(0xffffffffu, db[o], z);
+          }
+        }
+#pragma unroll
+        for (int o = 0; o < kRounds; ++o) {
+          const int e = et + kTeam * o, r = e / (8 * VB);
+          if (e % (8 * VB) == 0) {
+            x.vdv[r] = vdv[o];
+            if (r < n) static_cast<bf16 *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = __float2bfloat16_rn(db[o]);
+          }
+        }
         pipe::warp_arrive(in_free);
         // gradients
         wait_on(out_full, parity(m), wait);
-        if (y == 0) wait_on(qk_full, parity(c), wait);
+        if (y == 0) wait_on(&qk_full[c & 1], parity(c / 2), wait);
         tc_fence_after();
-        float read = 0.f;  // (dO S^T).q
+        float read = 0.f;
 #pragma unroll
         for (int j0 = 0; j0 < kCols; j0 += 16) {
           const int col = kCols * sub + j0;
           float a[16], w[16], t[16];
           tmem_ld16(lanes + kTmA + col, a);
           tmem_ld16(lanes + kTmW + col, w);
-          if (!is_k) {
-            const uint32_t tile = s0 + L::kQK + 2 * (col >> 6) * kBox;
-#pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              float r8[8];
-              tc::unpack8(pipe::lds_sw128(tile, i, ((col & 63) + e) >> 3), r8);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) read = fmaf(r8[j], a[e + j], read);
-            }
-          }
           if (is_k) {
             tmem_ld16(lanes + kTmB + col, t);
 #pragma unroll
@@ -428,56 +438,69 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            a[e] = fmaf(fa, a[e], w[e]);
-            if (is_k) a[e] += t[e];
-            acc[j0 + e] += a[e];
+            w[e] = fmaf(fa, a[e], w[e]);
+            if (is_k) a[e] = w[e] += t[e];
+            acc[j0 + e] += w[e];
+          }
+          // (dO S^T).q, or k.dk
+          const uint32_t tile = qk0 + (2 * (col >> 6) + is_k) * kBox;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            float r8[8];
+            tc::unpack8(pipe::lds_sw128(tile, i, ((col & 63) + e) >> 3), r8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) read = fmaf(r8[j], a[e + j], read);
           }
         }
         tc_fence_before();
         pipe::warp_arrive(acc_free);
-        if (!is_k) x.dot[sub][i] = fmaf(fa, read, dot);
+        if (!is_k) x.dot[sub][i] = read = fmaf(fa, read, dot);
+        along += read;
         pipe::warp_arrive(&sums_full[m & 1]);
       }
-      // the division by the lengths, and out
-      const uint32_t tile0 = s0 + L::kQK + (is_k ? kBox : 0);
+      // the division by the lengths, and out: through the places of q and k, which nobody reads any more
+      const uint32_t tile0 = qk0 + is_k * kBox;
       float f = 0.f;
       if (p.norm) {
-        float dot = 0.f, len = 0.f, r8[8];
-#pragma unroll
-        for (int e = 0; e < kCols; e += 8) {
-          const int col = kCols * sub + e;
-          tc::unpack8(pipe::lds_sw128(tile0 + 2 * (col >> 6) * kBox, i, (col & 63) >> 3), r8);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            dot = fmaf(r8[j], acc[e + j], dot);
-            len = fmaf(r8[j], r8[j], len);
-          }
-        }
-        misc.along[is_k][sub][i] = dot;
-        misc.length[is_k][sub][i] = len;
+        misc.along[is_k][sub][i] = along;
         team_sync();
-        f = (misc.along[is_k][0][i] + misc.along[is_k][1][i]) / (misc.length[is_k][0][i] + misc.length[is_k][1][i] + p.eps);
+        f = (misc.along[is_k][0][i] + misc.along[is_k][1][i]) * len;
       }
-      const int head = hk * p.dk;
-      bf16 *out = is_k ? static_cast<bf16 *>(g.dk) + (size_t)(t0 + i) * g.dks + head : static_cast<bf16 *>(g.dq) + (size_t)(t0 + i) * g.dqs + head;
 #pragma unroll
       for (int e = 0; e < kCols; e += 8) {
         const int col = kCols * sub + e;
-        float v[8];
-        if (p.norm) {
-          float r8[8];
-          tc::unpack8(pipe::lds_sw128(tile0 + 2 * (col >> 6) * kBox, i, (col & 63) >> 3), r8);
+        const uint32_t at = tile0 + 2 * (col >> 6) * kBox + sw128_offset(i, col & 63);
+        float v[8], r8[8];
+        tc::unpack8(pipe::lds_sw128(tile0 + 2 * (col >> 6) * kBox, i, (col & 63) >> 3), r8);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = acc[e + j] - r8[j] * f;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = acc[e + j];
-        }
-        if (i < n && col < p.dk) *reinterpret_cast<uint4 *>(out + col) = tc::pack8(v);
+        for (int j = 0; j < 8; ++j) v[j] = p.norm ? acc[e + j] - r8[j] * f : acc[e + j];
+        pipe::sts_u4(at, tc::pack8(v));
       }
-      pipe::warp_arrive(qk_free);
+      fence_async_smem();
+      team_sync();
+      if (n == kDrC) {
+        if (et == 0) {
+          for (int b = 0; b < KB; ++b)
+            if (64 * b < p.dk) {
+              tma_store_3d(&args.dq, qk0 + 2 * b * kBox, 64 * b, hk, t0);
+              tma_store_3d(&args.dk, qk0 + (2 * b + 1) * kBox, 64 * b, hk, t0);
+            }
+          bulk_commit();
+          bulk_wait_read0();
+        }
+      } else {  // rows past the end belong to another sequence: row by row
+        for (int e = et; e < n * 16 * KB; e += kTeam) {
+          const int r = e / (16 * KB), b = e % (16 * KB) >> 3, ch = e & 7, col = 64 * (b >> 1) + 8 * ch;
+          if (col < p.dk) {
+            bf16 *out = b & 1 ? static_cast<bf16 *>(g.dk) + (size_t)(t0 + r) * g.dks : static_cast<bf16 *>(g.dq) + (size_t)(t0 + r) * g.dqs;
+            *reinterpret_cast<uint4 *>(out + hk * p.dk + col) = pipe::lds_sw128(qk0 + b * kBox, r, ch);
+          }
+        }
+      }
+      pipe::warp_arrive(&qk_free[c & 1]);
       ++c;
     }
+    if (et == 0) bulk_wait0();
   }
 
   tc_fence_before();
@@ -508,7 +531,10 @@ void launch_dr_grads_tc(const DrProblem &p, const void *dout, long long dos, con
       !encode_tmap_bf16_heads(&args.k, p.k, p.dk, p.Hk, p.total, p.ks * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.dout, dout, p.dv, p.H, p.total, dos * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.z, p.Z, p.dv, p.H, p.total, es, kDrC) ||
-      !encode_tmap_bf16_heads(&args.e, p.E, p.dv, p.H, p.total, es, kDrC)) {
+      !encode_tmap_bf16_heads(&args.e, p.E, p.dv, p.H, p.total, es, kDrC) ||
+      !encode_tmap_bf16_heads(&args.v, p.v, p.dv, p.H, p.total, p.vs * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&args.dq, g.dq, p.dk, p.Hk, p.total, g.dqs * 2, kDrC) ||
+      !encode_tmap_bf16_heads(&args.dk, g.dk, p.dk, p.Hk, p.total, g.dks * 2, kDrC)) {
     note_host_error();
     return;
   }
