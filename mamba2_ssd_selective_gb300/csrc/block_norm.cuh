@@ -2,12 +2,14 @@
 // bn_*.cu.
 //
 // Bytes bound them: every tensor is read and written once, a row's values wait in its threads' registers from
-// the first sum to the last store.  A row is a warp's (up to 1024 channels) or a block's.
+// the first sum to the last store.  A row is a warp's (up to 512 channels) or a block's.  Blocks whose rows can be
+// moved as whole 16-byte units go through many rows, with the next ones on their way into shared memory by bulk copies.
 #pragma once
 
 #include <type_traits>
 
 #include "block_norm.h"
+#include "tc_pipe.cuh"
 
 namespace ssd {
 
@@ -82,61 +84,138 @@ template <bool WARP> __device__ __forceinline__ float bn_sum(float v, float *buf
   return v;
 }
 
-__device__ __forceinline__ float bn_silu(float z) { return z * sigmoid_f(z); }
+// sigmoid: of bf16 values on the fast intrinsics (relative error ~1e-6; infinities of the sum give 0)
+template <typename T> __device__ __forceinline__ float bn_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+template <> __device__ __forceinline__ float bn_sigmoid<float>(float z) { return sigmoid_f(z); }
 
-template <typename T, typename R, int PER, int VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kBnWarpRows : 512) bn_forward_kernel(const BnProblem p) {
+// Where a block's rows come from: global memory, or (kRing) a ring of stages in shared memory that bulk copies fill.
+enum { kWarp, kBlock, kRing };
+struct BnTensor {
+  const void *p;
+  long long stride;
+  int eb;  // bytes of an element
+};
+template <int MODE, int NT> struct BnRows {
+  const BnTensor (&t)[NT];  // null where there is none
+  uint8_t *ring;
+  uint64_t *full;
+  int rows, C, step, stages, stage_bytes;
+  int next;  // the row that is copied next (thread 0)
+  __device__ BnRows(const BnTensor (&tensors)[NT], uint8_t *smem, int rows_, int C_, int first, int step_, int stages_)
+      : t(tensors), ring(smem + 64), full(reinterpret_cast<uint64_t *>(smem)), rows(rows_), C(C_), step(step_), stages(stages_), next(first) {
+    stage_bytes = 0;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) stage_bytes += t[i].p ? C * t[i].eb : 0;
+    if (MODE != kRing) return;
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < stages; ++s) sm100::mbar_init(&full[s], 1);
+      sm100::fence_mbar_init();
+    }
+    __syncthreads();
+    for (int s = 0; s < stages; ++s) fetch(s);
+  }
+  // the next row on its way into stage s, which every thread has read (a __syncthreads since)
+  __device__ void fetch(int s) {
+    if (MODE != kRing) return;
+    if (threadIdx.x == 0 && next < rows) {
+      sm100::mbar_expect_tx(&full[s], (uint32_t)stage_bytes);
+      uint8_t *to = ring + (size_t)s * stage_bytes;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        if (t[i].p) {
+          pipe::bulk_load(to, static_cast<const uint8_t *>(t[i].p) + (size_t)next * t[i].stride * t[i].eb, (uint32_t)(C * t[i].eb), &full[s]);
+          to += C * t[i].eb;
+        }
+    }
+    next += step;
+  }
+  // tensor `which` of a row, the it-th of the block
+  template <int N, int VEC, typename X> __device__ void get(X (&v)[N], int which, int row, int it, int tid, int team) const {
+    if (MODE == kRing) {
+      const uint8_t *from = ring + (size_t)(it % stages) * stage_bytes;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        if (i < which && t[i].p) from += C * t[i].eb;
+      bn_load<N, VEC>(v, from, 0, C, tid, team);
+    } else {
+      bn_load<N, VEC>(v, t[which].p, (size_t)row * t[which].stride, C, tid, team);
+    }
+  }
+  __device__ void wait(int it) const {
+    if (MODE == kRing) sm100::mbar_wait_drain(&full[it % stages], (it / stages) & 1);
+  }
+};
+
+template <typename T, typename R, int PER, int VEC, int MODE>
+__global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512) bn_forward_kernel(const BnProblem p, int stages) {
   constexpr int N = 8 * PER;
-  __shared__ float sums[2][32];
+  constexpr bool WARP = MODE == kWarp;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sums[4][32];
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, team = WARP ? 32 : blockDim.x;
-  const int row = WARP ? blockIdx.x * kBnWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-  if (WARP && row >= p.rows) return;
-  T x[N], z[N];
-  R res[N];
-  bn_load<N, VEC>(x, p.x, (size_t)row * p.xs, p.C, tid, team);
-  if (p.gate) bn_load<N, VEC>(z, p.z, (size_t)row * p.zs, p.C, tid, team);
-  if (p.res) bn_load<N, VEC>(res, p.res, (size_t)row * p.rs, p.C, tid, team);
-  float h[N];
+  const int first = WARP ? blockIdx.x * kBnWarpRows + (threadIdx.x >> 5) : blockIdx.x, step = WARP ? gridDim.x * kBnWarpRows : gridDim.x;
+  const float per_c = 1.f / (float)p.C;
+  const BnTensor tensors[3] = {{p.x, p.xs, sizeof(T)}, {p.gate ? p.z : nullptr, p.zs, sizeof(T)}, {p.res, p.rs, sizeof(R)}};
+  BnRows<MODE, 3> in(tensors, smem, p.rows, p.C, first, step, stages);
+  int it = 0;
+  for (int row = first; row < p.rows; row += step, ++it) {
+    T x[N], z[N];
+    R res[N];
+    in.wait(it);
+    in.template get<N, VEC>(x, 0, row, it, tid, team);
+    if (p.gate) in.template get<N, VEC>(z, 1, row, it, tid, team);
+    if (p.res) in.template get<N, VEC>(res, 2, row, it, tid, team);
+    float h[N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) h[e] = to_f<T>(x[e]);
-  if (p.post) {
-    float s = 0.f;
+    for (int e = 0; e < N; ++e) h[e] = to_f<T>(x[e]);
+    if (p.post) {
+      float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < N; ++e) s = fmaf(h[e], h[e], s);
-    const float r = 1.f / sqrtf(bn_sum<WARP>(s, sums[0]) / (float)p.C + p.eps);
-    if (tid == 0 && p.rstd_post) p.rstd_post[row] = r;
+      for (int e = 0; e < N; ++e) s = fmaf(h[e], h[e], s);
+      const float r = 1.f / sqrtf(bn_sum<WARP>(s, sums[2 * (it & 1)]) * per_c + p.eps);
+      if (tid == 0 && p.rstd_post) p.rstd_post[row] = r;
 #pragma unroll
-    for (int e = 0; e < N; ++e) h[e] *= r;
-    bn_weigh<N, VEC>(h, p.pw, p.C, tid, team);
-  }
-  if (p.gate) {
+      for (int e = 0; e < N; ++e) h[e] *= r;
+      bn_weigh<N, VEC>(h, p.pw, p.C, tid, team);
+    } else if (MODE == kRing && !p.pre) {
+      __syncthreads();
+    }
+    if (p.post || !p.pre) in.fetch(it % (MODE == kRing ? stages : 1));
+    if (p.gate) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) h[e] *= bn_silu(to_f<T>(z[e]));
-  }
-  bn_weigh<N, VEC>(h, p.sc, p.C, tid, team);
-  if (p.res) {
+      for (int e = 0; e < N; ++e) {
+        const float g = to_f<T>(z[e]);
+        h[e] *= g * bn_sigmoid<T>(g);
+      }
+    }
+    bn_weigh<N, VEC>(h, p.sc, p.C, tid, team);
+    if (p.res) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) h[e] += to_f<R>(res[e]);
-  }
-  if (p.h) bn_store<N, VEC, R>(p.h, (size_t)row * p.hs, h, p.C, tid, team);
-  if (p.pre) {
-    float s = 0.f;
+      for (int e = 0; e < N; ++e) h[e] += to_f<R>(res[e]);
+    }
+    if (p.h) bn_store<N, VEC, R>(p.h, (size_t)row * p.hs, h, p.C, tid, team);
+    if (p.pre) {
+      float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < N; ++e) s = fmaf(h[e], h[e], s);
-    const float r = 1.f / sqrtf(bn_sum<WARP>(s, sums[1]) / (float)p.C + p.eps);
-    if (tid == 0 && p.rstd_pre) p.rstd_pre[row] = r;
+      for (int e = 0; e < N; ++e) s = fmaf(h[e], h[e], s);
+      const float r = 1.f / sqrtf(bn_sum<WARP>(s, sums[2 * (it & 1) + 1]) * per_c + p.eps);
+      if (!p.post) in.fetch(it % (MODE == kRing ? stages : 1));
+      if (tid == 0 && p.rstd_pre) p.rstd_pre[row] = r;
 #pragma unroll
-    for (int e = 0; e < N; ++e) h[e] *= r;
-    bn_weigh<N, VEC>(h, p.w, p.C, tid, team);
-    bn_store<N, VEC, T>(p.y, (size_t)row * p.ys, h, p.C, tid, team);
+      for (int e = 0; e < N; ++e) h[e] *= r;
+      bn_weigh<N, VEC>(h, p.w, p.C, tid, team);
+      bn_store<N, VEC, T>(p.y, (size_t)row * p.ys, h, p.C, tid, team);
+    }
   }
 }
 
-// A block goes through rows blockIdx.x, + gridDim.x, ...; the parameters' sums stay in registers and go out once.
-// Teams of a warp: the block's warps have partial sums of their own.
-template <typename T, typename R, int PER, int VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kBnWarpRows : 512) bn_backward_kernel(const BnProblem p) {
+// The parameters' sums stay in registers and go out once: a set of partial sums for each block (teams of a warp: the
+// block's warps add up in shared memory).
+template <typename T, typename R, int PER, int VEC, int MODE>
+__global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_backward_kernel(const BnProblem p, int stages) {
   constexpr int N = 8 * PER;
+  constexpr bool WARP = MODE == kWarp;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sums[4][32];
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, team = WARP ? 32 : blockDim.x;
   const int first = WARP ? blockIdx.x * kBnWarpRows + (threadIdx.x >> 5) : blockIdx.x;
@@ -145,40 +224,48 @@ __global__ void __launch_bounds__(WARP ? 32 * kBnWarpRows : 512) bn_backward_ker
   float dpw[N], dsc[N], dw[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) dpw[e] = dsc[e] = dw[e] = 0.f;
-  const bool uses_x = p.post || p.gate || p.dsc;
-  int turn = 0;
-  for (int row = first; row < p.rows; row += step) {
+  const bool uses_x = p.post || p.gate || p.dsc, pre = p.pre && p.dy;
+  const BnTensor tensors[5] = {{uses_x ? p.x : nullptr, p.xs, sizeof(T)}, {p.gate ? p.z : nullptr, p.zs, sizeof(T)}, {pre ? p.dy : nullptr, p.dys, sizeof(T)},
+                               {pre ? p.h : nullptr, p.hs, sizeof(R)}, {p.dh, p.dhs, sizeof(R)}};
+  BnRows<MODE, 5> in(tensors, smem, p.rows, p.C, first, step, stages);
+  int it = 0;
+  for (int row = first; row < p.rows; row += step, ++it) {
     float d[N];
+    T x[N], z[N];
+    in.wait(it);
+    if (uses_x) in.template get<N, VEC>(x, 0, row, it, tid, team);
+    if (p.gate) in.template get<N, VEC>(z, 1, row, it, tid, team);
+    const float rp = p.post ? __ldg(p.rstd_post + row) : 1.f, r = pre ? __ldg(p.rstd_pre + row) : 1.f;
     {
       R dh[N];
-      if (p.dh) bn_load<N, VEC>(dh, p.dh, (size_t)row * p.dhs, p.C, tid, team);
+      if (p.dh) in.template get<N, VEC>(dh, 4, row, it, tid, team);
+      float g[N], s = 0.f;
+      R h[N];
+      if (pre) {
+        T dy[N];
+        in.template get<N, VEC>(dy, 2, row, it, tid, team);
+        in.template get<N, VEC>(h, 3, row, it, tid, team);
+#pragma unroll
+        for (int e = 0; e < N; ++e) g[e] = to_f<T>(dy[e]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[e] = fmaf(g[e], to_f<R>(h[e]) * r, dw[e]);
+        bn_weigh<N, VEC>(g, p.w, p.C, tid, team);
+#pragma unroll
+        for (int e = 0; e < N; ++e) s = fmaf(g[e], to_f<R>(h[e]), s);
+        s = bn_sum<WARP>(s, sums[2 * (it & 1)]) * per_c * r * r;
+      } else if (MODE == kRing) {
+        __syncthreads();
+      }
+      in.fetch(it % (MODE == kRing ? stages : 1));
 #pragma unroll
       for (int e = 0; e < N; ++e) d[e] = p.dh ? to_f<R>(dh[e]) : 0.f;
-    }
-    T x[N], z[N];
-    if (uses_x) bn_load<N, VEC>(x, p.x, (size_t)row * p.xs, p.C, tid, team);
-    if (p.gate) bn_load<N, VEC>(z, p.z, (size_t)row * p.zs, p.C, tid, team);
-    if (p.pre && p.dy) {
-      R h[N];
-      T dy[N];
-      bn_load<N, VEC>(h, p.h, (size_t)row * p.hs, p.C, tid, team);
-      bn_load<N, VEC>(dy, p.dy, (size_t)row * p.dys, p.C, tid, team);
-      const float r = __ldg(p.rstd_pre + row);
-      float g[N], s = 0.f;
+      if (pre) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) g[e] = to_f<T>(dy[e]);
-#pragma unroll
-      for (int e = 0; e < N; ++e) dw[e] = fmaf(g[e], to_f<R>(h[e]) * r, dw[e]);
-      bn_weigh<N, VEC>(g, p.w, p.C, tid, team);
-#pragma unroll
-      for (int e = 0; e < N; ++e) s = fmaf(g[e], to_f<R>(h[e]), s);
-      s = bn_sum<WARP>(s, sums[turn]) * per_c * r * r;
-#pragma unroll
-      for (int e = 0; e < N; ++e) d[e] = fmaf(r, g[e] - to_f<R>(h[e]) * s, d[e]);
+        for (int e = 0; e < N; ++e) d[e] = fmaf(r, g[e] - to_f<R>(h[e]) * s, d[e]);
+      }
     }
     if (p.dres) bn_store<N, VEC, R>(p.dres, (size_t)row * p.drs, d, p.C, tid, team);
     float u[N];  // the normed x, before its weight
-    const float rp = p.post ? __ldg(p.rstd_post + row) : 1.f;
     if (uses_x) {
 #pragma unroll
       for (int e = 0; e < N; ++e) u[e] = to_f<T>(x[e]) * rp;
@@ -188,20 +275,26 @@ __global__ void __launch_bounds__(WARP ? 32 * kBnWarpRows : 512) bn_backward_ker
 #pragma unroll
       for (int e = 0; e < N; ++e) t[e] = u[e];
       if (p.post) bn_weigh<N, VEC>(t, p.pw, p.C, tid, team);
-      if (p.dsc) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) dsc[e] = fmaf(d[e], p.gate ? t[e] * bn_silu(to_f<T>(z[e])) : t[e], dsc[e]);
-      }
-      bn_weigh<N, VEC>(d, p.sc, p.C, tid, team);
       if (p.gate) {
-        float dz[N];
+        float s[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] = bn_sigmoid<T>(to_f<T>(z[e]));
+        if (p.dsc) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) dsc[e] = fmaf(d[e], t[e] * (to_f<T>(z[e]) * s[e]), dsc[e]);
+        }
+        bn_weigh<N, VEC>(d, p.sc, p.C, tid, team);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const float zz = to_f<T>(z[e]), q = sigmoid_f(zz);
-          dz[e] = d[e] * t[e] * (q * (1.f + zz * (1.f - q)));
-          d[e] *= zz * q;
+          const float zz = to_f<T>(z[e]);
+          t[e] *= d[e] * (s[e] * fmaf(zz, 1.f - s[e], 1.f));
+          d[e] *= zz * s[e];
         }
-        bn_store<N, VEC, T>(p.dz, (size_t)row * p.dzs, dz, p.C, tid, team);
+        bn_store<N, VEC, T>(p.dz, (size_t)row * p.dzs, t, p.C, tid, team);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) dsc[e] = fmaf(d[e], t[e], dsc[e]);
+        bn_weigh<N, VEC>(d, p.sc, p.C, tid, team);
       }
     } else {
       bn_weigh<N, VEC>(d, p.sc, p.C, tid, team);
@@ -213,21 +306,35 @@ __global__ void __launch_bounds__(WARP ? 32 * kBnWarpRows : 512) bn_backward_ker
       bn_weigh<N, VEC>(d, p.pw, p.C, tid, team);
 #pragma unroll
       for (int e = 0; e < N; ++e) s = fmaf(d[e], u[e], s);
-      s = bn_sum<WARP>(s, sums[turn + 1]) * per_c;
+      s = bn_sum<WARP>(s, sums[2 * (it & 1) + 1]) * per_c;
 #pragma unroll
       for (int e = 0; e < N; ++e) d[e] = rp * (d[e] - u[e] * s);
     }
     bn_store<N, VEC, T>(p.dx, (size_t)row * p.dxs, d, p.C, tid, team);
-    turn ^= 2;
   }
-  const size_t set = WARP ? (size_t)first : blockIdx.x;
   auto put = [&](int which, const float *wanted, const float(&v)[N]) {
     if (!wanted) return;
-    float *to = p.part + (set * 3 + which) * p.C;
+    float *to = p.part + ((size_t)blockIdx.x * 3 + which) * p.C;
+    if (WARP) {  // one warp after another
+      float *acc = reinterpret_cast<float *>(smem);
+      for (int w = 0; w < kBnWarpRows; ++w) {
+        __syncthreads();
+        if ((int)(threadIdx.x >> 5) == w) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int c = bn_channel<VEC>(e, tid, team);
-      if (c < p.C) to[c] = v[e];
+          for (int e = 0; e < N; ++e) {
+            const int c = bn_channel<VEC>(e, tid, team);
+            if (c < p.C) acc[c] = w == 0 ? v[e] : acc[c] + v[e];
+          }
+        }
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < p.C; c += blockDim.x) to[c] = acc[c];
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int c = bn_channel<VEC>(e, tid, team);
+        if (c < p.C) to[c] = v[e];
+      }
     }
   };
   put(0, p.dpw, dpw);
@@ -235,18 +342,51 @@ __global__ void __launch_bounds__(WARP ? 32 * kBnWarpRows : 512) bn_backward_ker
   put(2, p.dw, dw);
 }
 
-template <typename T, typename R, int PER, int VEC> void run_forward(const BnProblem &p, int threads, cudaStream_t s) {
-  if (threads == 32)
-    bn_forward_kernel<T, R, PER, VEC, true><<<(p.rows + kBnWarpRows - 1) / kBnWarpRows, 32 * kBnWarpRows, 0, s>>>(p);
+// Bytes of a row that a ring would move, and how many stages of them a block may have (fewer than 2: no ring)
+template <typename T, typename R> int bn_stages(const BnProblem &p, bool backward, int blocks_per_sm, int &stage) {
+  const bool pre = p.pre && p.dy;
+  if (backward)
+    stage = p.C * ((p.post || p.gate || p.dsc ? (int)sizeof(T) : 0) + (p.gate ? (int)sizeof(T) : 0) + (pre ? (int)(sizeof(T) + sizeof(R)) : 0) + (p.dh ? (int)sizeof(R) : 0));
   else
-    bn_forward_kernel<T, R, PER, VEC, false><<<p.rows, threads, 0, s>>>(p);
+    stage = p.C * ((int)sizeof(T) * (p.gate ? 2 : 1) + (p.res ? (int)sizeof(R) : 0));
+  const int most = stage ? (220 * 1024 / blocks_per_sm - 1024) / stage : 0;
+  return most < 4 ? most : 4;
 }
-template <typename T, typename R, int PER, int VEC> void run_backward(const BnProblem &p, int threads, cudaStream_t s) {
+
+template <typename T, typename R, int PER, int VEC> void run_forward(const BnProblem &p, const BnTeam &team, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  int stage = 0;
+  const int sms = device_sm_count();
+  if (team.threads == 32) {
+    bn_forward_kernel<T, R, PER, VEC, kWarp><<<(p.rows + kBnWarpRows - 1) / kBnWarpRows, 32 * kBnWarpRows, 0, s>>>(p, 1);
+    return;
+  }
+  // two blocks of 256 threads to an SM, more of smaller ones; rows enough for some to be on their way
+  const int per_sm = team.threads > 256 ? 1 : team.threads > 128 ? 2 : 4, grid = sms * per_sm;
+  const int stages = VEC == 8 ? bn_stages<T, R>(p, false, per_sm, stage) : 0;
+  if (VEC == 8 && stages >= 2 && p.rows >= 2 * grid) {
+    allow_smem(reinterpret_cast<const void *>(bn_forward_kernel<T, R, PER, 8, kRing>), 220 * 1024, allowed);
+    bn_forward_kernel<T, R, PER, 8, kRing><<<grid, team.threads, 64 + stages * stage, s>>>(p, stages);
+  } else {
+    bn_forward_kernel<T, R, PER, VEC, kBlock><<<p.rows, team.threads, 0, s>>>(p, 1);
+  }
+}
+template <typename T, typename R, int PER, int VEC> void run_backward(const BnProblem &p, const BnTeam &team, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
   const int sets = bn_blocks(p.rows, p.C);
-  if (threads == 32)
-    bn_backward_kernel<T, R, PER, VEC, true><<<sets / kBnWarpRows, 32 * kBnWarpRows, 0, s>>>(p);
-  else
-    bn_backward_kernel<T, R, PER, VEC, false><<<sets, threads, 0, s>>>(p);
+  int stage = 0;
+  if (team.threads == 32) {
+    bn_backward_kernel<T, R, PER, VEC, kWarp><<<sets, 32 * kBnWarpRows, p.C * 4, s>>>(p, 1);
+    return;
+  }
+  const int per_sm = bn_blocks_per_sm(team);
+  const int stages = VEC == 8 ? bn_stages<T, R>(p, true, per_sm, stage) : 0;
+  if (VEC == 8 && stages >= 2 && p.rows >= 2 * sets) {
+    allow_smem(reinterpret_cast<const void *>(bn_backward_kernel<T, R, PER, 8, kRing>), 220 * 1024, allowed);
+    bn_backward_kernel<T, R, PER, 8, kRing><<<sets, team.threads, 64 + stages * stage, s>>>(p, stages);
+  } else {
+    bn_backward_kernel<T, R, PER, VEC, kBlock><<<sets, team.threads, 0, s>>>(p, 1);
+  }
 }
 
 template <typename T, typename R, int PER, class Run> void by_vec(int vec, const Run &run) {
@@ -269,12 +409,12 @@ template <typename T, typename R, class Run> void by_team(int per, int vec, cons
 }  // namespace
 
 template <typename T, typename R> void launch_bn_forward(const BnProblem &p, int vec, cudaStream_t s) {
-  const BnTeam team = bn_team(p.C);
-  by_team<T, R>(team.per, vec, [&](auto per, auto v) { run_forward<T, R, decltype(per)::value, decltype(v)::value>(p, team.threads, s); });
+  const BnTeam team = bn_team(p.C, false);
+  by_team<T, R>(team.per, vec, [&](auto per, auto v) { run_forward<T, R, decltype(per)::value, decltype(v)::value>(p, team, s); });
 }
 template <typename T, typename R> void launch_bn_backward(const BnProblem &p, int vec, cudaStream_t s) {
-  const BnTeam team = bn_team(p.C);
-  by_team<T, R>(team.per, vec, [&](auto per, auto v) { run_backward<T, R, decltype(per)::value, decltype(v)::value>(p, team.threads, s); });
+  const BnTeam team = bn_team(p.C, true);
+  by_team<T, R>(team.per, vec, [&](auto per, auto v) { run_backward<T, R, decltype(per)::value, decltype(v)::value>(p, team, s); });
 }
 
 }  // namespace ssd

@@ -35,8 +35,9 @@ struct BnProblem {
 struct BnTeam {
   int threads, per;  // per: units of 8 values a thread
 };
-BnTeam bn_team(int channels);
-int bn_blocks(int rows, int channels);  // of the backward pass: one set of partial sums each
+BnTeam bn_team(int channels, bool backward);
+int bn_blocks_per_sm(const BnTeam &team);     // of the backward pass
+int bn_blocks(int rows, int channels);        // likewise, all of them: one set of partial sums each
 
 // T: x, z, y; R: the residual stream; vec: channels that the tensors' addresses and strides allow at once (8, 2, 1)
 template <typename T, typename R> void launch_bn_forward(const BnProblem &p, int vec, cudaStream_t s);
