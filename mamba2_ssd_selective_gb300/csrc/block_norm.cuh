@@ -70,6 +70,29 @@ __device__ __forceinline__ void bn_weigh(float (&v)[N], const float *w, int C, i
   }
 }
 
+// A weight of a block that goes through many rows: in registers where HOLD says so (what bulk copies leave of the L1 cache
+// does not hold them: 16384 x 4096 forward 299 us, read again for each row)
+template <int N, int VEC, bool HOLD> struct BnWeight {
+  const float *p;
+  float v[HOLD ? N : 1];
+  __device__ BnWeight(const float *w, int C, int tid, int team) : p(w) {
+    if (!HOLD || !w) return;
+#pragma unroll
+    for (int e = 0; e < (HOLD ? N : 1); ++e) {
+      const int c = bn_channel<VEC>(e, tid, team);
+      v[e] = c < C ? __ldg(w + c) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void weigh(float (&x)[N], int C, int tid, int team) const {
+    if (!HOLD) {
+      bn_weigh<N, VEC>(x, p, C, tid, team);
+    } else if (p) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] *= v[HOLD ? e : 0];
+    }
+  }
+};
+
 // Sum over a row's threads, in a fixed order; every thread gets it.  `buf`: 32 floats that the last two sums did not use.
 template <bool WARP> __device__ __forceinline__ float bn_sum(float v, float *buf) {
 #pragma unroll
@@ -147,7 +170,7 @@ template <int MODE, int NT> struct BnRows {
 };
 
 template <typename T, typename R, int PER, int VEC, int MODE>
-__global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512) bn_forward_kernel(const BnProblem p, int stages) {
+__global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_forward_kernel(const BnProblem p, int stages) {
   constexpr int N = 8 * PER;
   constexpr bool WARP = MODE == kWarp;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -157,6 +180,8 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512) bn_for
   const float per_c = 1.f / (float)p.C;
   const BnTensor tensors[3] = {{p.x, p.xs, sizeof(T)}, {p.gate ? p.z : nullptr, p.zs, sizeof(T)}, {p.res, p.rs, sizeof(R)}};
   BnRows<MODE, 3> in(tensors, smem, p.rows, p.C, first, step, stages);
+  constexpr bool kHold = MODE == kRing && N <= 16;
+  const BnWeight<N, VEC, kHold> pw(p.pw, p.C, tid, team), sc(p.sc, p.C, tid, team), w(p.w, p.C, tid, team);
   int it = 0;
   for (int row = first; row < p.rows; row += step, ++it) {
     T x[N], z[N];
@@ -176,7 +201,7 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512) bn_for
       if (tid == 0 && p.rstd_post) p.rstd_post[row] = r;
 #pragma unroll
       for (int e = 0; e < N; ++e) h[e] *= r;
-      bn_weigh<N, VEC>(h, p.pw, p.C, tid, team);
+      pw.weigh(h, p.C, tid, team);
     } else if (MODE == kRing && !p.pre) {
       __syncthreads();
     }
@@ -188,7 +213,7 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512) bn_for
         h[e] *= g * bn_sigmoid<T>(g);
       }
     }
-    bn_weigh<N, VEC>(h, p.sc, p.C, tid, team);
+    sc.weigh(h, p.C, tid, team);
     if (p.res) {
 #pragma unroll
       for (int e = 0; e < N; ++e) h[e] += to_f<R>(res[e]);
@@ -203,7 +228,7 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512) bn_for
       if (tid == 0 && p.rstd_pre) p.rstd_pre[row] = r;
 #pragma unroll
       for (int e = 0; e < N; ++e) h[e] *= r;
-      bn_weigh<N, VEC>(h, p.w, p.C, tid, team);
+      w.weigh(h, p.C, tid, team);
       bn_store<N, VEC, T>(p.y, (size_t)row * p.ys, h, p.C, tid, team);
     }
   }
@@ -228,6 +253,8 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_
   const BnTensor tensors[5] = {{uses_x ? p.x : nullptr, p.xs, sizeof(T)}, {p.gate ? p.z : nullptr, p.zs, sizeof(T)}, {pre ? p.dy : nullptr, p.dys, sizeof(T)},
                                {pre ? p.h : nullptr, p.hs, sizeof(R)}, {p.dh, p.dhs, sizeof(R)}};
   BnRows<MODE, 5> in(tensors, smem, p.rows, p.C, first, step, stages);
+  constexpr bool kHold = MODE == kRing && N <= 8;
+  const BnWeight<N, VEC, kHold> pw(p.pw, p.C, tid, team), sc(p.sc, p.C, tid, team), w(p.w, p.C, tid, team);
   int it = 0;
   for (int row = first; row < p.rows; row += step, ++it) {
     float d[N];
@@ -249,7 +276,7 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_
         for (int e = 0; e < N; ++e) g[e] = to_f<T>(dy[e]);
 #pragma unroll
         for (int e = 0; e < N; ++e) dw[e] = fmaf(g[e], to_f<R>(h[e]) * r, dw[e]);
-        bn_weigh<N, VEC>(g, p.w, p.C, tid, team);
+        w.weigh(g, p.C, tid, team);
 #pragma unroll
         for (int e = 0; e < N; ++e) s = fmaf(g[e], to_f<R>(h[e]), s);
         s = bn_sum<WARP>(s, sums[2 * (it & 1)]) * per_c * r * r;
@@ -274,7 +301,7 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_
       float t[N];  // weighted
 #pragma unroll
       for (int e = 0; e < N; ++e) t[e] = u[e];
-      if (p.post) bn_weigh<N, VEC>(t, p.pw, p.C, tid, team);
+      if (p.post) pw.weigh(t, p.C, tid, team);
       if (p.gate) {
         float s[N];
 #pragma unroll
@@ -283,7 +310,7 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_
 #pragma unroll
           for (int e = 0; e < N; ++e) dsc[e] = fmaf(d[e], t[e] * (to_f<T>(z[e]) * s[e]), dsc[e]);
         }
-        bn_weigh<N, VEC>(d, p.sc, p.C, tid, team);
+        sc.weigh(d, p.C, tid, team);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const float zz = to_f<T>(z[e]);
@@ -294,16 +321,16 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_
       } else {
 #pragma unroll
         for (int e = 0; e < N; ++e) dsc[e] = fmaf(d[e], t[e], dsc[e]);
-        bn_weigh<N, VEC>(d, p.sc, p.C, tid, team);
+        sc.weigh(d, p.C, tid, team);
       }
     } else {
-      bn_weigh<N, VEC>(d, p.sc, p.C, tid, team);
+      sc.weigh(d, p.C, tid, team);
     }
     if (p.post) {
       float s = 0.f;
 #pragma unroll
       for (int e = 0; e < N; ++e) dpw[e] = fmaf(d[e], u[e], dpw[e]);
-      bn_weigh<N, VEC>(d, p.pw, p.C, tid, team);
+      pw.weigh(d, p.C, tid, team);
 #pragma unroll
       for (int e = 0; e < N; ++e) s = fmaf(d[e], u[e], s);
       s = bn_sum<WARP>(s, sums[2 * (it & 1) + 1]) * per_c;
