@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_
 
 // The parameters' sums stay in registers and go out once: a set of partial sums for each block (teams of a warp: the
 // block's warps add up in shared memory).
-template <typename T, typename R, int PER, int VEC, int MODE>
-__global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_backward_kernel(const BnProblem p, int stages) {
+template <typename T, typename R, int PER, int VEC, int MODE, int THREADS>
+__global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : THREADS, 1) bn_backward_kernel(const BnProblem p, int stages) {
   constexpr int N = 8 * PER;
   constexpr bool WARP = MODE == kWarp;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_
   const BnTensor tensors[5] = {{uses_x ? p.x : nullptr, p.xs, sizeof(T)}, {p.gate ? p.z : nullptr, p.zs, sizeof(T)}, {pre ? p.dy : nullptr, p.dys, sizeof(T)},
                                {pre ? p.h : nullptr, p.hs, sizeof(R)}, {p.dh, p.dhs, sizeof(R)}};
   BnRows<MODE, 5> in(tensors, smem, p.rows, p.C, first, step, stages);
-  constexpr bool kHold = MODE == kRing && N <= 8;
+  constexpr bool kHold = MODE == kRing && N * THREADS <= 16 * 256;
   const BnWeight<N, VEC, kHold> pw(p.pw, p.C, tid, team), sc(p.sc, p.C, tid, team), w(p.w, p.C, tid, team);
   int it = 0;
   for (int row = first; row < p.rows; row += step, ++it) {
@@ -398,22 +398,25 @@ template <typename T, typename R, int PER, int VEC> void run_forward(const BnPro
     bn_forward_kernel<T, R, PER, VEC, kBlock><<<p.rows, team.threads, 0, s>>>(p, 1);
   }
 }
-template <typename T, typename R, int PER, int VEC> void run_backward(const BnProblem &p, const BnTeam &team, cudaStream_t s) {
+template <typename T, typename R, int PER, int VEC, int THREADS> void run_backward_blocks(const BnProblem &p, const BnTeam &team, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
   const int sets = bn_blocks(p.rows, p.C);
   int stage = 0;
-  if (team.threads == 32) {
-    bn_backward_kernel<T, R, PER, VEC, kWarp><<<sets, 32 * kBnWarpRows, p.C * 4, s>>>(p, 1);
-    return;
-  }
-  const int per_sm = bn_blocks_per_sm(team);
-  const int stages = VEC == 8 ? bn_stages<T, R>(p, true, per_sm, stage) : 0;
+  const int stages = VEC == 8 ? bn_stages<T, R>(p, true, bn_blocks_per_sm(team), stage) : 0;
   if (VEC == 8 && stages >= 2 && p.rows >= 2 * sets) {
-    allow_smem(reinterpret_cast<const void *>(bn_backward_kernel<T, R, PER, 8, kRing>), 220 * 1024, allowed);
-    bn_backward_kernel<T, R, PER, 8, kRing><<<sets, team.threads, 64 + stages * stage, s>>>(p, stages);
+    allow_smem(reinterpret_cast<const void *>(bn_backward_kernel<T, R, PER, 8, kRing, THREADS>), 220 * 1024, allowed);
+    bn_backward_kernel<T, R, PER, 8, kRing, THREADS><<<sets, team.threads, 64 + stages * stage, s>>>(p, stages);
   } else {
-    bn_backward_kernel<T, R, PER, VEC, kBlock><<<sets, team.threads, 0, s>>>(p, 1);
+    bn_backward_kernel<T, R, PER, VEC, kBlock, THREADS><<<sets, team.threads, 0, s>>>(p, 1);
   }
+}
+template <typename T, typename R, int PER, int VEC> void run_backward(const BnProblem &p, const BnTeam &team, cudaStream_t s) {
+  if (team.threads == 32)
+    bn_backward_kernel<T, R, PER, VEC, kWarp, 256><<<bn_blocks(p.rows, p.C), 32 * kBnWarpRows, p.C * 4, s>>>(p, 1);
+  else if (team.threads <= 256)
+    run_backward_blocks<T, R, PER, VEC, 256>(p, team, s);
+  else
+    run_backward_blocks<T, R, PER, VEC, 512>(p, team, s);
 }
 
 template <typename T, typename R, int PER, class Run> void by_vec(int vec, const Run &run) {
@@ -436,11 +439,11 @@ template <typename T, typename R, class Run> void by_team(int per, int vec, cons
 }  // namespace
 
 template <typename T, typename R> void launch_bn_forward(const BnProblem &p, int vec, cudaStream_t s) {
-  const BnTeam team = bn_team(p.C, false);
+  const BnTeam team = bn_team(p.C);
   by_team<T, R>(team.per, vec, [&](auto per, auto v) { run_forward<T, R, decltype(per)::value, decltype(v)::value>(p, team, s); });
 }
 template <typename T, typename R> void launch_bn_backward(const BnProblem &p, int vec, cudaStream_t s) {
-  const BnTeam team = bn_team(p.C, true);
+  const BnTeam team = bn_team(p.C);
   by_team<T, R>(team.per, vec, [&](auto per, auto v) { run_backward<T, R, decltype(per)::value, decltype(v)::value>(p, team, s); });
 }
 

@@ -35,7 +35,7 @@ struct BnProblem {
 struct BnTeam {
   int threads, per;  // per: units of 8 values a thread
 };
-BnTeam bn_team(int channels, bool backward);
+BnTeam bn_team(int channels);
 int bn_blocks_per_sm(const BnTeam &team);     // of the backward pass
 int bn_blocks(int rows, int channels);        // likewise, all of them: one set of partial sums each
 

@@ -3,22 +3,23 @@
 
 namespace ssd {
 
-// Backward a thread has three sums for each of its channels, so that 8 are enough until a block is full.
-BnTeam bn_team(int C, bool backward) {
+// What a row costs whatever its length is shared by 16 channels a thread where it is long (gradients of 8192 x 4096: 182 us
+// with 8).
+BnTeam bn_team(int C) {
   const int units = (C + 7) / 8;
   if (units <= 32) return {32, 1};
   if (units <= 64) return {32, 2};
   auto warps = [](int n) { return (n + 31) / 32 * 32; };
-  if (units <= (backward ? 512 : 256)) return {warps(units), 1};
+  if (units <= 256) return {warps(units), 1};
   if (units <= 1024) return {warps((units + 1) / 2), 2};
   return {warps((units + 3) / 4), 4};
 }
 
-// as registers allow: some 100 a thread
-int bn_blocks_per_sm(const BnTeam &t) { return t.threads > 256 ? 1 : t.threads > 128 ? 2 : 4; }
+// as registers allow: about 100 a thread with 8 channels, 200 with 16
+int bn_blocks_per_sm(const BnTeam &t) { return t.threads > 256 || t.per > 1 ? 1 : t.threads > 128 ? 2 : 4; }
 
 int bn_blocks(int rows, int C) {
-  const BnTeam t = bn_team(C, true);
+  const BnTeam t = bn_team(C);
   // (a workspace's size may be asked for where there is no GPU: the SMs are not asked)
   const int most = 152 * (t.threads == 32 ? 2 : bn_blocks_per_sm(t)), wanted = t.threads == 32 ? (rows + 7) / 8 : rows;
   return wanted < most ? wanted : most;

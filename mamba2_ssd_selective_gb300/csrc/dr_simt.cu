@@ -23,10 +23,11 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
-// acc[i][c] += sum_k A[4 tm + i][k] B[k][2 tn + c], A's rows contiguous along k
+// acc[i][c] += sum_(k < K) A[4 tm + i][k] B[k][2 tn + c], A's rows contiguous along k
 __device__ __forceinline__ void mm_nt(float (&acc)[4][2], const float *A, int lda, const float *B, int K, int tm, int tn) {
   A += 4 * tm * lda;
   B += 2 * tn;
+#pragma unroll 2
   for (int k = 0; k < K; k += 4) {
     float4 a[4];
     float2 b[4];
@@ -41,12 +42,12 @@ __device__ __forceinline__ void mm_nt(float (&acc)[4][2], const float *A, int ld
     }
   }
 }
-// acc[i][c] += sum_j A[j][4 tm + i] B[j][2 tn + c] over the chunk's 64 rows
-__device__ __forceinline__ void mm_tn(float (&acc)[4][2], const float *A, int lda, const float *B, int tm, int tn) {
+// acc[i][c] += sum_(j >= j0) A[j][4 tm + i] B[j][2 tn + c] over the chunk's 64 rows; j0 a multiple of 8
+__device__ __forceinline__ void mm_tn(float (&acc)[4][2], const float *A, int lda, const float *B, int tm, int tn, int j0 = 0) {
   A += 4 * tm;
   B += 2 * tn;
 #pragma unroll 8
-  for (int j = 0; j < kDrC; ++j) {
+  for (int j = j0; j < kDrC; ++j) {
     const float4 a = *reinterpret_cast<const float4 *>(A + j * lda);
     const float2 b = *reinterpret_cast<const float2 *>(B + j * kCols);
     acc[0][0] = fmaf(a.x, b.x, acc[0][0]), acc[0][1] = fmaf(a.x, b.y, acc[0][1]);
@@ -84,16 +85,17 @@ struct ChainShared {
   }
 };
 
+// four threads to a row
 template <typename T>
 __device__ __forceinline__ void load_rows(float *dst, int ld, const void *src, long long stride, size_t t0, int n, int h, int dk) {
-  const int per = dk / 4;
-  const T *from = static_cast<const T *>(src) + t0 * stride + (size_t)h * dk;
-  for (int e = threadIdx.x; e < kDrC * per; e += kThreads) {
-    const int r = e / per, c = 4 * (e - r * per);
-    *reinterpret_cast<float4 *>(dst + r * ld + c) = r < n ? load4(from + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  const int r = threadIdx.x >> 2;
+  const T *from = static_cast<const T *>(src) + (t0 + r) * stride + (size_t)h * dk;
+#pragma unroll 4
+  for (int c = 4 * (threadIdx.x & 3); c < dk; c += 16)
+    *reinterpret_cast<float4 *>(dst + r * ld + c) = r < n ? load4(from + c) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 __device__ __forceinline__ void load_mat(float *dst, const float *src) {
+#pragma unroll
   for (int e = threadIdx.x; e < kDrC * kDrC / 4; e += kThreads)
     *reinterpret_cast<float4 *>(dst + (e >> 4) * kMatLd + 4 * (e & 15)) = __ldg(reinterpret_cast<const float4 *>(src) + e);
 }
@@ -136,6 +138,7 @@ __global__ void __launch_bounds__(kThreads) dr_chain_kernel(DrProblem p, T *__re
   dr_seq(p, seq, a, len, slot0);
   load_state(sm.S, p.init ? p.init + ((size_t)seq * p.H + h) * dd : nullptr, p.dk, p.dv, c0);
   const DrRows &rows = *sm.rows;
+  const int upto = 8 * (tid >> 5) + 8;  // N and P are zero right of the diagonal: the columns of the warp's 8 rows
   for (int c = 0; c * kDrC < len; ++c) {
     const size_t t0 = (size_t)a + c * kDrC, at = (size_t)(slot0 + c) * p.H + h;
     const int n = min(kDrC, len - c * kDrC);
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) dr_chain_kernel(DrProblem p, T *__re
     }
     __syncthreads();
     zero(acc);
-    mm_nt(acc, sm.N, kMatLd, sm.B1, kDrC, tm, tn);
+    mm_nt(acc, sm.N, kMatLd, sm.B1, upto, tm, tn);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * tm + i;
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) dr_chain_kernel(DrProblem p, T *__re
     }
     __syncthreads();
     if (OUT) {
-      mm_nt(acc, sm.P, kMatLd, sm.B2, kDrC, tm, tn);
+      mm_nt(acc, sm.P, kMatLd, sm.B2, upto, tm, tn);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * tm + i;
@@ -231,6 +234,7 @@ __global__ void __launch_bounds__(kThreads) dr_reverse_kernel(DrProblem p, const
   dr_seq(p, seq, a, len, slot0);
   load_state(sm.S, dfin ? dfin + ((size_t)seq * p.H + h) * dd : nullptr, p.dk, p.dv, c0);
   const DrRows &rows = *sm.rows;
+  const int from = 8 * (tid >> 5);  // N and P are zero above the diagonal: the rows of the warp's 8 columns
   for (int c = (len - 1) / kDrC; c * kDrC < len && c >= 0; --c) {
     const size_t t0 = (size_t)a + c * kDrC, at = (size_t)(slot0 + c) * p.H + h;
     const int n = min(kDrC, len - c * kDrC);
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) dr_reverse_kernel(DrProblem p, const
       d[i][0] *= rows.kout[4 * tm + i];
       d[i][1] *= rows.kout[4 * tm + i];
     }
-    mm_tn(d, sm.P, kMatLd, sm.B3, tm, tn);
+    mm_tn(d, sm.P, kMatLd, sm.B3, tm, tn, from);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * tm + i;
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) dr_reverse_kernel(DrProblem p, const
     }
     __syncthreads();
     zero(acc);
-    mm_tn(acc, sm.N, kMatLd, sm.B1, tm, tn);
+    mm_tn(acc, sm.N, kMatLd, sm.B1, tm, tn, from);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * tm + i;

@@ -240,7 +240,8 @@ def test_step_continues_a_prompt(dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 1, 1, 64, 64), (3, 4, 2, 8, 8), (2, 2, 1, 128, 40), (5, 3, 3, 256, 256),
-                                   (160, 2, 1, 64, 128), (80, 2, 2, 128, 128), (2, 1, 1, 24, 72)])
+                                   (160, 2, 1, 64, 128), (80, 2, 2, 128, 128), (2, 1, 1, 24, 72),
+                                   (310, 4, 2, 128, 128), (700, 2, 1, 40, 64)])
 @pytest.mark.parametrize("norm", [True, False])
 def test_step(shape, norm, dtype):
     n, H, K, dk, dv = shape
@@ -259,6 +260,29 @@ def test_step_without_a_slot():
     c.runner().step(*c.inputs(), states, slot_idx=torch.tensor([-1, 3, 1, 2 ** 30], dtype=torch.int32, device="cuda"), out=out)
     assert (out[[0, 1, 3]] == 0).all() and (out[2] != 0).any()
     assert (states[0] == 1).all() and (states[2] == 1).all() and (states[1] != 1).any()
+
+
+@pytest.mark.parametrize("dv", [64, 128])
+def test_step_without_a_slot_among_many(dv):
+    """The kernel of whole states: rows without a slot leave the cache alone, states of others are not touched."""
+    n, H, dk = 330, 4, 48
+    c = Case([1] * n, H, H, dk, dv, "f32", packed=False, seed=22)
+    g = torch.Generator().manual_seed(1)
+    slots = torch.randperm(400, generator=g)[:n].to(torch.int32)
+    slots[::7] = -1
+    slots[3::50] = 400
+    cache = torch.randn(400, H, dk, dv, generator=g)
+    states = cache.cuda()
+    o = c.runner().step(*c.inputs(), states, slot_idx=slots.cuda(), scale=c.scale)
+    live = (slots >= 0) & (slots < 400)
+    want, wfin = ref.delta_rule(*c.ref_inputs(), cache.double()[slots.long().clamp(0, 399)], EPS)
+    close(o[live.cuda()], want.reshape(n, -1)[live], F32, "o")
+    assert (o[~live.cuda()] == 0).all()
+    at = slots[live].long()
+    close(states[at.cuda()], wfin[live], F32, "states")
+    rest = torch.ones(400, dtype=torch.bool)
+    rest[at] = False
+    assert torch.equal(states[rest.cuda()].cpu(), cache[rest])
 
 
 def test_step_many_tokens_of_a_long_memory():
