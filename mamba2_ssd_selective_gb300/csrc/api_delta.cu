@@ -1,5 +1,7 @@
 // C ABI of the gated delta rule and of the norms around a block: argument checks, workspace carving and launch
 // sequences.  Nothing here allocates or synchronises.
+#include <cmath>
+
 #include "block_norm.h"
 #include "delta.h"
 
@@ -11,8 +13,8 @@ namespace {
 
 struct DrPlan {
   bool tc;
-  int slots;
-  size_t status, rows, N, P, S, dS, E, Z, dqp, dkp, dots, total;  // workspace offsets
+  int slots, seg, places;  // seg: chunks of a segment, 0: sequences are not cut
+  size_t seg_states, seg_sums, status, rows, N, P, S, dS, E, Z, dqp, dkp, dots, total;  // workspace offsets
 };
 
 long long dr_rows(const ssd_delta_rule_dims *d) { return d->packed ? d->total_tokens : (long long)d->nseq * d->seqlen; }
@@ -36,6 +38,29 @@ ssd_status dr_check_dims(const ssd_delta_rule_dims *d) {
 // bf16 within its widths takes the tensor-core kernels, everything else the CUDA-core ones
 bool dr_use_tc(const ssd_delta_rule_dims *d) { return d->dtype == SSD_BF16 && la_tc_envelope(d->headdim_k, d->headdim_v); }
 
+// Chunks of a segment, or 0: whether sequences are cut is a matter of their number, since a chain is an SM's however few
+// there are.  Times measured here, in us: a chunk of a chain 2.6, a chunk of a segment's sums 2.4 (there are two, for all
+// segments but the last), the scan 4 a segment, two launches more 12.  Lengths of packed sequences are not known: the
+// longest of n is taken for its mean where sequences end at random.  (A workspace's size may be asked for where there is
+// no GPU: the SMs are not asked.)
+int dr_segment_chunks(const ssd_delta_rule_dims *d) {
+  const long long sms = 152, items = (long long)d->nseq * d->nheads, n = d->nseq;
+  const double part = d->packed ? (std::log((double)n) + 0.577 + 0.5 / (double)n) / (double)n : 1.;
+  const long long chunks = (long long)((double)(d->packed ? d->total_tokens : d->seqlen) * (part < 1. ? part : 1.) / kDrC) + 1;
+  auto rounds = [&](long long x) { return (double)((x + sms - 1) / sms); };
+  double best = rounds(items) * 2.6 * (double)chunks;
+  int seg = 0;
+  for (long long k = 2; k <= 64 && 4 * k <= chunks; ++k) {
+    const long long len = (chunks + k - 1) / k;
+    const double cost = rounds(2 * items * (k - 1)) * 2.4 * (double)len + rounds(items * k) * 2.6 * (double)len + 4. * (double)k + 12.;
+    if (cost < best) {
+      best = cost;
+      seg = (int)len;
+    }
+  }
+  return seg;
+}
+
 DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
   DrPlan pl{};
   pl.tc = dr_use_tc(d);
@@ -52,6 +77,14 @@ DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
   pl.rows = take(chunks * sizeof(DrRows));
   pl.N = take(chunks * (pl.tc ? 4 * kDrTile : kDrC * kDrC * 4));
   pl.P = take(pl.tc ? 0 : chunks * kDrC * kDrC * 4);
+  if (pl.tc && !backward) pl.seg = dr_segment_chunks(d);
+  if (pl.seg) {
+    const long long n = (long long)pl.seg * kDrC, rows = dr_rows(d);
+    pl.places = (int)(d->packed ? rows / n + d->nseq : d->nseq * ((d->seqlen + n - 1) / n));
+    const size_t items = (size_t)pl.places * d->nheads;
+    pl.seg_states = take(items * state * 4);
+    pl.seg_sums = take(items * (state + (size_t)d->headdim_k * d->headdim_k) * 4);
+  }
   if (backward) {
     const size_t eb = pl.tc ? 2 : 4, padded = (size_t)dr_padded(d->headdim_k) * dr_padded(d->headdim_v);
     pl.S = take(pl.tc ? (chunks + (size_t)d->nseq * d->nheads) * padded * 2 : chunks * state * 4);
@@ -128,6 +161,8 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
     p.rows = reinterpret_cast<DrRows *>(ws + pl->rows);
     auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
     p.N = at(pl->N), p.P = at(pl->P);
+    p.seg = pl->seg, p.seg_places = pl->places;
+    p.seg_states = at(pl->seg_states), p.seg_sums = at(pl->seg_sums);
     p.S = at(pl->S), p.dS = at(pl->dS), p.E = at(pl->E), p.Z = at(pl->Z);
     p.dqp = at(pl->dqp), p.dkp = at(pl->dkp), p.dots = at(pl->dots);
   }
@@ -137,6 +172,10 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
 template <typename T>
 ssd_status dr_forward_impl(const DrProblem &p, bool tc, void *o, int64_t os, float *fin, cudaStream_t s) {
   SSD_LAUNCH("dr_prep", tc ? launch_dr_prep_tc(p, false, s) : launch_dr_prep<T>(p, s));
+  if (p.seg) {
+    SSD_LAUNCH("dr_sums", launch_dr_tc_sums(p, s));
+    SSD_LAUNCH("dr_scan", launch_dr_tc_scan(p, s));
+  }
   SSD_LAUNCH("dr_chain", tc ? launch_dr_tc_chain(p, o, os, fin, s) : launch_dr_chain<T>(p, o, os, fin, s));
   return launch_status();
 }

@@ -59,6 +59,11 @@ struct DrProblem {
   float *S, *dS, *E, *Z;
   float *dqp, *dkp;  // (total, H, dk): gradients of the unit q and k of each state head
   float *dots;       // (chunk, 4): parts of <state behind the chunk, its gradient>, one for each 32 columns of dv
+  // Tensor cores: sequences cut into segments of `seg` chunks (0: not cut), their places (dr_place0), the states before
+  // them, and for all but last ones N, the state that a segment makes of zero, and M, so that S_next = M S + N (at
+  // seg_sums: N of all places, then M)
+  int seg, seg_places;
+  float *seg_states, *seg_sums;
   int *status;       // device status word, cleared by the first kernel
   unsigned long long wait_ns;
 };
@@ -104,12 +109,47 @@ __device__ __forceinline__ void dr_chunk(const DrProblem &p, int slot, int &t0, 
   n = off < 0 || off >= len ? 0 : min(kDrC, len - (int)off);
 }
 
+// The place of a sequence's first segment, as of its first chunk; and the segment at a place: seq < 0 where there is none
+__device__ __forceinline__ int dr_place0(const DrProblem &p, int seg, int a, int s) {
+  const int n = seg * kDrC;
+  return p.cu ? a / n + s : s * ((p.seqlen + n - 1) / n);
+}
+__device__ __forceinline__ void dr_segment(const DrProblem &p, int seg, int place, int &seq, int &a, int &len, int &slot0, bool &ends) {
+  const int n = seg * kDrC;
+  if (p.cu) {
+    int lo = 0, hi = p.nseq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (min(max(__ldg(p.cu + mid), 0), p.total) / n + mid <= place)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    seq = lo;
+  } else {
+    seq = place / ((p.seqlen + n - 1) / n);
+  }
+  dr_seq(p, seq, a, len, slot0);
+  const long long off = (long long)(place - dr_place0(p, seg, a, seq)) * n;
+  if (off < 0 || (off >= len && off > 0)) {
+    seq = -1;
+    return;
+  }
+  ends = off + n >= len;
+  slot0 += (int)(off / kDrC);
+  a += (int)off;
+  len = min(n, len - (int)off);
+}
+
 // dr_prep.cu: rows' factors, N and P of every chunk
 template <typename T> void launch_dr_prep(const DrProblem &p, cudaStream_t s);
 // dr_prep_tc.cu: the same for the tensor-core chains (P's second term for backward only)
 void launch_dr_prep_tc(const DrProblem &p, bool backward, cudaStream_t s);
 // dr_tc.cu: the chains for bf16, both widths at most 128
 void launch_dr_tc_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);
+// cut sequences: the segments' M and N, then the states before them
+void launch_dr_tc_sums(const DrProblem &p, cudaStream_t s);
+void launch_dr_tc_scan(const DrProblem &p, cudaStream_t s);
 void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s);
 // dr_simt.cu: the chain of chunks (o null: only S and E, for backward), its reverse, and the gradients
 template <typename T> void launch_dr_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);

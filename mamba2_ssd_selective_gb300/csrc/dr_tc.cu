@@ -41,14 +41,14 @@ constexpr int kStages = 2;
 // of the additions (32 each), b E for the outputs or the terms of qin dO, W
 constexpr uint32_t kTmS = 0, kTmX = 128, kTmO = 192, kTmY = 256, kTmD = 320, kTmW = 384, kTmCols = 512;
 
-enum Mode { kOut, kStates, kReverse };  // outputs; states and E for the backward pass; the reverse chain
+enum Mode { kOut, kStates, kReverse, kSum };  // outputs; states and E for the backward pass; the reverse chain; only the last state
 
 template <int KB, int VB, int MODE> struct Layout {
   static constexpr uint32_t kK = 0, kQ = KB * kBox, kV = kQ + KB * kBox, kN = kV + VB * kBox, kP = kN + 2 * kBox;
   static constexpr uint32_t kRows = kP + 2 * kBox, kStage = (kRows + sizeof(DrRows) + 1023) / 1024 * 1024;
   static constexpr uint32_t kO = kStages * kStage;  // a chunk's outputs, on their way to TMA
   static constexpr uint32_t kKept = kO + VB * kBox;  // a kept state, likewise
-  static constexpr uint32_t kBar = kKept + (MODE == kOut ? 0 : KB * VB * kBox);
+  static constexpr uint32_t kBar = kKept + (MODE == kOut || MODE == kSum ? 0 : KB * VB * kBox);
   static constexpr int kNumBars = 2 * kStages + 14;
   static constexpr uint32_t kEnd = kBar + kNumBars * 8 + 16;
   static constexpr int kBytes = (int)kEnd + 1024;
@@ -120,12 +120,17 @@ struct Args {
   bf16 *kept;          // the state before each chunk, the gradient of the one behind
   const bf16 *states;  // reverse: the states
   WaitCtl wait;
+  // Sequences cut into segments of so many chunks (0: whole ones): `first` and `last` are then the segments', at their
+  // places (dr_segment), but for the last segment's of a sequence, which ends in `fin`
+  int seg, places;
+  float *fin;
+  int what;  // kSum: 0 the segment's state from zero, 1 what becomes of the unit matrix without additions, 2 both (blockIdx.y)
 };
 
 template <int KB, int VB, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constant__ Args args) {
   using L = Layout<KB, VB, MODE>;
-  constexpr bool kRev = MODE == kReverse;
+  constexpr bool kRev = MODE == kReverse, kKeeps = kRev || MODE == kStates;  // what the gradients need
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = tc::aligned_smem(smem_raw);
   const DrProblem &p = args.p;
@@ -133,9 +138,18 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
   const Bars bar(reinterpret_cast<uint64_t *>(sm + L::kBar));
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + L::kNumBars * 8);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int seq = blockIdx.x / p.H, h = blockIdx.x - seq * p.H;
-  int a, len, slot0;
-  dr_seq(p, seq, a, len, slot0);
+  const int place = blockIdx.x / p.H, h = blockIdx.x - place * p.H;
+  int seq = place, a, len, slot0;
+  bool ends = true;  // the segment is its sequence's last
+  if (args.seg)
+    dr_segment(p, args.seg, place, seq, a, len, slot0, ends);
+  else
+    dr_seq(p, seq, a, len, slot0);
+  // the places of no segment; a last segment's sum is not asked for
+  if (args.seg && (seq < 0 || (MODE == kSum && ends))) return;
+  // the unit matrix's columns are dk
+  const bool unit = MODE == kSum && (args.what == 2 ? blockIdx.y == 1 : args.what == 1);
+  const int dv = unit ? p.dk : p.dv;
   const int nc = __shfl_sync(0xffffffffu, (len + kDrC - 1) / kDrC, 0);
   // processing order: the i-th chunk, its rows
   auto chunk = [&](int i) { return kRev ? nc - 1 - i : i; };
@@ -155,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.full[i], 1);
       // the issuer's commit, the Y and state warps, the outputs' warps and those of a partial chunk where there are any
-      mbar_init(&bar.free[i], 1 + 8 * VB + (MODE == kStates ? 0 : 2 * VB) + (partial ? 2 : 0));
+      mbar_init(&bar.free[i], 1 + 8 * VB + (MODE == kOut || kRev ? 2 * VB : 0) + (partial ? 2 : 0));
     }
     mbar_init(bar.patched, 2);
     mbar_init(bar.s_ready, 4 * VB);
@@ -204,16 +218,17 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           uint8_t *base = sm + stage(i);
           const size_t at = (size_t)(slot0 + chunk(i)) * p.H + h;
           const uint8_t *tiles = reinterpret_cast<const uint8_t *>(p.N) + at * (4 * kBox);
-          constexpr uint32_t kQBytes = MODE == kStates ? 0 : KB * kBox;
-          constexpr uint32_t kMats = MODE == kOut ? 3 * kBox : MODE == kStates ? 2 * kBox : 4 * kBox;
-          mbar_expect_tx(&bar.full[st], KB * kBox + kQBytes + VB * kBox + kMats + (uint32_t)sizeof(DrRows));
+          constexpr uint32_t kQBytes = MODE == kStates || MODE == kSum ? 0 : KB * kBox;
+          constexpr uint32_t kMats = MODE == kOut ? 3 * kBox : MODE == kReverse ? 4 * kBox : 2 * kBox;
+          mbar_expect_tx(&bar.full[st], KB * kBox + kQBytes + (unit ? 0 : VB * kBox) + kMats + (uint32_t)sizeof(DrRows));
           for (int b = 0; b < KB; ++b) tma_load_3d(base + L::kK + b * kBox, &args.k, &bar.full[st], 64 * b, hk, row);
-          for (int b = 0; b < VB; ++b) tma_load_3d(base + L::kV + b * kBox, &args.v, &bar.full[st], 64 * b, h, row);
+          if (!unit)
+            for (int b = 0; b < VB; ++b) tma_load_3d(base + L::kV + b * kBox, &args.v, &bar.full[st], 64 * b, h, row);
           pipe::bulk_load(base + L::kRows, p.rows + at, sizeof(DrRows), &bar.full[st]);
           pipe::bulk_load(base + L::kN, tiles, kMats, &bar.full[st]);  // N's terms, P's behind them
           if (kRev)
             pipe::bulk_prefetch(args.states + behind(i) * (64 * KB * 64 * VB), 2 * 64 * KB * 64 * VB);
-          if (MODE != kStates)
+          if (kQBytes)
             for (int b = 0; b < KB; ++b) tma_load_3d(base + L::kQ + b * kBox, &args.q, &bar.full[st], 64 * b, hk, row);
         }
         // every load issued has landed before the CTA releases its shared memory
@@ -306,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         mbar_wait_drain(bar.x_full, parity(nc - 1));
         mbar_wait_drain(bar.n_full, parity(nc - 1));
         mbar_wait_drain(bar.w_full, parity(nc - 1));
-        if (MODE != kStates) {
+        if (MODE == kOut || kRev) {
           mbar_wait_drain(bar.q_full, parity(nc - 1));
           mbar_wait_drain(bar.o_full, parity(nc - 1));
         }
@@ -367,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
             ldmatrix4_trans(at + 16 * 128, w[4], w[5], w[6], w[7]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              y[q][2 * e] = lo_f(w[e]);
-              y[q][2 * e + 1] = hi_f(w[e]);
+              y[q][2 * e] = unit ? 0.f : lo_f(w[e]);
+              y[q][2 * e + 1] = unit ? 0.f : hi_f(w[e]);
             }
           }
         }
@@ -405,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         if (kRev) pipe::warp_arrive(bar.o_free);
         pipe::warp_arrive(bar.y_ready);
         factors(kRev ? kIn : kOutF, f);
-        if (MODE != kOut) {  // the chunk before has been read out of the staging tile
+        if (kKeeps) {  // the chunk before has been read out of the staging tile
           if (tt == 0) bulk_wait_read0();
           role_sync<2, kTeam>();
         }
@@ -430,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           tmem_st_16x128_async(at + kTmY + 32 + 16 * sub, t1);
           if (MODE == kOut) {
             tmem_st_16x128_async(at + kTmD + 16 * sub, t2);
-          } else {  // E or Z, rows of tokens, into the staging tile
+          } else if (kKeeps) {  // E or Z, rows of tokens, into the staging tile
             const int c = fc + 16 * q;
             const uint32_t to = so + (uint32_t)(c >> 6) * kBox + sw128_offset(32 * sub + fi, c & 63);
             stmatrix4_trans(to, t2[0], t2[1], t2[2], t2[3]);
@@ -441,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         tc_fence_before();
         pipe::warp_arrive(bar.d_ready);
         pipe::warp_arrive(&bar.free[i % kStages]);
-        if (MODE != kOut) {
+        if (kKeeps) {
           fence_async_smem();
           role_sync<2, kTeam>();
           const int nv = live(i);
@@ -459,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           }
         }
       }
-      if (MODE != kOut && tt == 0) bulk_wait0();
+      if (kKeeps && tt == 0) bulk_wait0();
     }
   } else if (warp < kOutWarp0) {
     // ------------------------------------------------------------ state
@@ -468,13 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     if (quad < 2 * VB) {
       constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
       const int c = 32 * quad + lane, a0 = sub * kCols;
-      const size_t dd = (size_t)p.dk * p.dv, item = (size_t)seq * p.H + h;
+      const size_t dd = (size_t)p.dk * dv, item = (size_t)place * p.H + h;
       float S[kCols];
       {
         const float *in = args.first ? args.first + item * dd + c : nullptr;
-        const bool col = in && c < p.dv;
+        const bool col = in && c < dv;
 #pragma unroll
-        for (int x = 0; x < kCols; ++x) S[x] = col && a0 + x < p.dk ? in[(size_t)(a0 + x) * p.dv] : 0.f;
+        for (int x = 0; x < kCols; ++x) S[x] = unit ? (a0 + x == c ? 1.f : 0.f) : col && a0 + x < p.dk ? in[(size_t)(a0 + x) * dv] : 0.f;
       }
       // the thread's 8 x 16 bytes of a kept state, 64 VB apart
       constexpr size_t kTile = 64 * KB * 64 * VB;
@@ -514,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         tmem_wait_st();
         tc_fence_before();
         pipe::warp_arrive(bar.s_ready);
-        if (MODE != kOut) keep((size_t)(slot0 + chunk(i)) * p.H + h);  // beside the chunk's products
+        if (kKeeps) keep((size_t)(slot0 + chunk(i)) * p.H + h);  // beside the chunk's products
         wait_full(i);
         const float all_hi = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_hi)), all_lo = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_lo));
         pipe::warp_arrive(&bar.free[i % kStages]);
@@ -529,13 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         }
         tc_fence_before();
       }
-      if (MODE == kStates) keep(chunks + item);
-      if (MODE != kOut && sub + quad == 0 && lane == 0) bulk_wait0();
-      if (args.last && c < p.dv) {
-        float *out = args.last + item * dd + c;
+      if (MODE == kStates && ends) keep(chunks + (size_t)seq * p.H + h);
+      if (kKeeps && sub + quad == 0 && lane == 0) bulk_wait0();
+      // the user's final state, or the segment's sum; M's places are behind those of all N
+      float *to = args.seg && ends ? args.fin ? args.fin + ((size_t)seq * p.H + h) * dd : nullptr
+                  : args.last      ? args.last + (unit ? (size_t)args.places * p.H * p.dk * p.dv : 0) + item * dd
+                                   : nullptr;
+      if (to && c < dv) {
 #pragma unroll
         for (int x = 0; x < kCols; ++x)
-          if (a0 + x < p.dk) out[(size_t)(a0 + x) * p.dv] = S[x];
+          if (a0 + x < p.dk) to[(size_t)(a0 + x) * dv + c] = S[x];
       }
     }
   } else if (MODE == kOut) {
@@ -690,14 +708,17 @@ template <int KB, int VB, int MODE> void run(Args &args, cudaStream_t s) {
   using L = Layout<KB, VB, MODE>;
   static std::atomic<uint64_t> allowed{0};
   allow_smem(reinterpret_cast<const void *>(dr_tc_kernel<KB, VB, MODE>), L::kBytes, allowed);
-  dr_tc_kernel<KB, VB, MODE><<<args.p.nseq * args.p.H, kThreads, L::kBytes, s>>>(args);
+  const int places = args.seg ? args.places : args.p.nseq;
+  dr_tc_kernel<KB, VB, MODE><<<dim3((unsigned)(places * args.p.H), MODE == kSum && args.what == 2 ? 2 : 1), kThreads, L::kBytes, s>>>(args);
 }
-template <int MODE> void run_boxes(Args &args, cudaStream_t s) {
-  const int kb = la_tc_boxes(args.p.dk), vb = la_tc_boxes(args.p.dv);
+template <int MODE> void run_boxes(Args &args, int kb, int vb, cudaStream_t s) {
   if (kb == 1)
     vb == 1 ? run<1, 1, MODE>(args, s) : run<1, 2, MODE>(args, s);
   else
     vb == 1 ? run<2, 1, MODE>(args, s) : run<2, 2, MODE>(args, s);
+}
+template <int MODE> void run_boxes(Args &args, cudaStream_t s) {
+  run_boxes<MODE>(args, la_tc_boxes(args.p.dk), la_tc_boxes(args.p.dv), s);
 }
 
 // the tensor maps that every chain has; v: its values or dO, with v's heads
@@ -706,6 +727,8 @@ bool fill_args(Args &args, const DrProblem &p, const void *v, long long vs, void
   args.out = static_cast<bf16 *>(out);
   args.os = os;
   args.wait = {p.status, p.wait_ns};
+  args.seg = args.places = args.what = 0;
+  args.fin = nullptr;
   if (!encode_tmap_bf16_heads(&args.q, p.q, p.dk, p.Hk, p.total, p.qs * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.k, p.k, p.dk, p.Hk, p.total, p.ks * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.v, v, p.dv, p.H, p.total, vs * 2, kDrC) ||
@@ -725,7 +748,86 @@ void launch_dr_tc_chain(const DrProblem &p, void *o, long long os, float *fin, c
   args.first = p.init;
   args.last = o ? fin : nullptr;
   args.kept = reinterpret_cast<bf16 *>(p.S);
+  if (p.seg) {
+    args.seg = p.seg;
+    args.places = p.seg_places;
+    args.first = p.seg_states;
+    args.last = nullptr;
+    args.fin = o ? fin : nullptr;
+  }
   o ? run_boxes<kOut>(args, s) : run_boxes<kStates>(args, s);
+}
+
+void launch_dr_tc_sums(const DrProblem &p, cudaStream_t s) {
+  Args args;
+  if (!fill_args(args, p, p.v, p.vs, p.E, (long long)p.H * p.dv)) return;
+  args.seg = p.seg;
+  args.places = p.seg_places;
+  args.first = nullptr;
+  args.last = p.seg_sums;
+  const int kb = la_tc_boxes(p.dk), vb = la_tc_boxes(p.dv);
+  args.what = kb == vb ? 2 : 0;
+  run_boxes<kSum>(args, kb, vb, s);
+  if (kb != vb) {
+    args.what = 1;
+    run_boxes<kSum>(args, kb, kb, s);
+  }
+}
+
+namespace {
+
+// Segments' states before their first tokens: S_next = M S + N, from the initial state on.  A block has 16 columns of a
+// state, a thread 8 of them in one row or two: M's row times the columns, which are in shared memory.
+constexpr int kScanCols = 16;
+__global__ void __launch_bounds__(256) dr_scan_kernel(DrProblem p) {
+  __shared__ __align__(16) float S[128][kScanCols];
+  const int seq = blockIdx.x / p.H, h = blockIdx.x - seq * p.H, c0 = blockIdx.y * kScanCols, dk = p.dk, dv = p.dv;
+  const int row = threadIdx.x >> 1, c = c0 + 8 * (threadIdx.x & 1);
+  const size_t dd = (size_t)dk * dv, all = (size_t)p.seg_places * p.H;
+  int a, len, slot0;
+  dr_seq(p, seq, a, len, slot0);
+  const int n = p.seg * kDrC, place0 = dr_place0(p, p.seg, a, seq), segments = len ? (len + n - 1) / n : 1;
+  const bool live = row < dk && c < dv;  // dv is a multiple of 8
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = live && p.init ? p.init[((size_t)seq * p.H + h) * dd + (size_t)row * dv + c + e] : 0.f;
+  for (int g = 0; g < segments; ++g) {
+    const size_t item = (size_t)(place0 + g) * p.H + h;
+    if (live) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p.seg_states[item * dd + (size_t)row * dv + c + e] = x[e];
+    }
+    if (g + 1 == segments) break;
+    __syncthreads();
+    if (row < 128) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) S[row][8 * (threadIdx.x & 1) + e] = x[e];
+    }
+    __syncthreads();
+    if (live) {
+      const float4 *M = reinterpret_cast<const float4 *>(p.seg_sums + all * dd + item * ((size_t)dk * dk) + (size_t)row * dk);
+      const float *N = p.seg_sums + item * dd + (size_t)row * dv + c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = N[e];
+#pragma unroll 4
+      for (int k = 0; k < dk; k += 4) {
+        const float4 m = __ldg(M + k / 4);
+        const float f[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 s0 = *reinterpret_cast<const float4 *>(&S[k + j][8 * (threadIdx.x & 1)]), s1 = *reinterpret_cast<const float4 *>(&S[k + j][8 * (threadIdx.x & 1) + 4]);
+          x[0] = fmaf(f[j], s0.x, x[0]), x[1] = fmaf(f[j], s0.y, x[1]), x[2] = fmaf(f[j], s0.z, x[2]), x[3] = fmaf(f[j], s0.w, x[3]);
+          x[4] = fmaf(f[j], s1.x, x[4]), x[5] = fmaf(f[j], s1.y, x[5]), x[6] = fmaf(f[j], s1.z, x[6]), x[7] = fmaf(f[j], s1.w, x[7]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+void launch_dr_tc_scan(const DrProblem &p, cudaStream_t s) {
+  dr_scan_kernel<<<dim3((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kScanCols - 1) / kScanCols)), 256, 0, s>>>(p);
 }
 
 void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s) {

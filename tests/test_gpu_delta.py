@@ -205,6 +205,27 @@ def test_equal_keys():
     c.check_backward()
 
 
+@pytest.mark.parametrize("lens,H,K,dk,dv,packed", [([4500], 2, 1, 64, 64, False), ([4097, 4097], 1, 1, 40, 128, False),
+                                                    ([4700], 1, 1, 128, 72, False), ([70, 0, 6000, 1], 1, 1, 64, 64, True)])
+@pytest.mark.parametrize("init", [True, False])
+def test_cut_sequences(lens, H, K, dk, dv, packed, init):
+    """Few long sequences: segments side by side."""
+    Case(lens, H, K, dk, dv, "bf16", packed, seed=13).check_forward(init)
+
+
+def test_cut_sequences_in_place():
+    """The states of cut sequences updated in place."""
+    c = Case([5000], 2, 2, 64, 64, packed=False, seed=14)
+    want, fin = c.forward()
+    r, states, o = c.runner(), c.init.cuda(), torch.empty_like(want)
+    inputs = r._inputs(*c.inputs(), c.scale, states, None)
+    keep = c.inputs()
+    for name, x in zip(("q", "k", "v", "log_decay", "beta"), keep):
+        setattr(inputs, name, x.data_ptr())
+    ssd.ssd_delta_rule_forward(r.dims, inputs, o, 128, states, r.workspace)
+    assert torch.equal(o, want) and torch.equal(states, fin)
+
+
 def test_long_memory_keeps_its_precision():
     """6000 tokens, decays of 1 - 1e-5 that are equal for all tokens: their rounding errors would add up."""
     c = Case([6000], 1, 1, 64, 64, "bf16", packed=False, seed=11, decay=torch.tensor([-1e-5]), beta=0.05)
