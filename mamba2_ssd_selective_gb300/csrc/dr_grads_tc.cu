@@ -388,10 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
           vdv[o] = db[o] = 0.f;
           if (r < n && col < p.dv) {
             db[o] = dot8(zw[o], ew[o], 0.f);
+            const float beta = rw.beta[r];
             float z[8], v[8];
             tc::unpack8(zw[o], z);
             tc::unpack8(vw[o], v);
-            const float beta = rw.beta[r];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               z[j] *= beta;

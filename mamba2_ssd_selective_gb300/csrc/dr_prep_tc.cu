@@ -78,11 +78,6 @@ template <int ROWS, int STEP> __device__ __forceinline__ void put(const float (&
   for (int e = 0; e < ROWS; ++e) *reinterpret_cast<float2 *>(m + e * STEP * kLd) = make_float2(x[e][0], x[e][1]);
 }
 
-// a pair of values as two bf16 terms
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-  hi = tc::pack_bf16x2(x, y);
-  lo = tc::pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-}
 __device__ __forceinline__ void sts(uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 
 // PT: terms of P that are wanted
@@ -206,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
         }
         *reinterpret_cast<float2 *>(&m[i][j]) = make_float2(a[0], a[1]);
         uint32_t qh, ql;
-        split2(q[0], q[1], qh, ql);
+        tc::split2(q[0], q[1], qh, ql);
         sts(row + ((y ^ (lane >> 2)) << 4), qh);  // the 128-byte swizzle: the row is lane / 4 modulo 8
         if (PT == 2) sts(row + kBox + ((y ^ (lane >> 2)) << 4), ql);
       }
@@ -275,10 +270,10 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
       const int i = e >> 3, y = e & 7;
       const float4 x0 = *reinterpret_cast<const float4 *>(&m[i][8 * y]), x1 = *reinterpret_cast<const float4 *>(&m[i][8 * y + 4]);
       uint4 hi, lo;
-      split2(x0.x, x0.y, hi.x, lo.x);
-      split2(x0.z, x0.w, hi.y, lo.y);
-      split2(x1.x, x1.y, hi.z, lo.z);
-      split2(x1.z, x1.w, hi.w, lo.w);
+      tc::split2(x0.x, x0.y, hi.x, lo.x);
+      tc::split2(x0.z, x0.w, hi.y, lo.y);
+      tc::split2(x1.x, x1.y, hi.z, lo.z);
+      tc::split2(x1.z, x1.w, hi.w, lo.w);
       const uint32_t to = s0 + kTilesN + i * 128 + ((y ^ (i & 7)) << 4);
       pipe::sts_u4(to, hi);
       pipe::sts_u4(to + kBox, lo);

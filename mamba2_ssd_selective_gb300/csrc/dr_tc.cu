@@ -89,10 +89,11 @@ struct Bars {
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-// two values as two bf16 pairs that add up to them to 16 bits
-__device__ __forceinline__ void split2(float x, float y, uint32_t &a, uint32_t &b) {
-  a = tc::pack_bf16x2(x, y);
-  b = tc::pack_bf16x2(x - lo_f(a), y - hi_f(a));
+// a packed pair likewise (tc::split2)
+__device__ __forceinline__ void split2(uint64_t v, uint32_t &a, uint32_t &b) {
+  float x, y;
+  upk2(v, x, y);
+  tc::split2(x, y, a, b);
 }
 
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t par, const WaitCtl &w) {
@@ -202,8 +203,11 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     if (partial && i == tail) wait_on(bar.patched, 0, wait);
   };
 
-  // The block is launched with 768 x 80 registers; the state's warps take what the first four do not need:
-  // 128 x (32 + 2 * 80 + 2 * 104 + 80) = 61440.
+  // The block is launched with 768 x 80 registers, 128 x 480; the warps of Y and E and the state's take what others do not
+  // need (without spills of theirs a chunk of kStates takes 2.5 us, with them 4.1).
+  constexpr bool kIdle = MODE == kStates || MODE == kSum;  // the last four warps
+  constexpr int kElemRegs = kIdle ? 88 : 80, kStateRegs = kIdle ? 120 : 104, kLastRegs = kIdle ? 32 : 80;
+  static_assert(32 + 2 * kElemRegs + 2 * kStateRegs + kLastRegs <= 480, "registers");
   if (warp < kElemWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0) {
@@ -347,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     }
   } else if (warp < kStateWarp0) {
     // ------------------------------------------------------------ Y and E
+    if (kElemRegs > 80) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kElemRegs));
     const int quad = warp & 3, sub = (warp - kElemWarp0) >> 2;
     if (quad < 2 * VB) {
       const int tok = 32 * sub + 2 * (lane & 3);  // this lane's tokens: tok + 8 m and the next
@@ -363,15 +368,19 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
       for (int i = 0; i < nc; ++i) {
         wait_full(i);
         const uint32_t rows = rows_of(i);
-        auto factors = [&](uint32_t which, float2(&f)[4]) {
+        auto factors = [&](uint32_t which, uint64_t(&f)[4]) {
 #pragma unroll
           for (int m = 0; m < 4; ++m)
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[m].x), "=f"(f[m].y) : "r"(rows + which + (tok + 8 * m) * 4));
+            asm volatile("ld.shared.b64 %0, [%1];" : "=l"(f[m]) : "r"(rows + which + (tok + 8 * m) * 4));
         };
+        constexpr uint64_t kMinus = 0x8000000080000000ull, kMinusOne = 0xbf800000bf800000ull;  // signs; -1, -1
         constexpr uint32_t kIn = offsetof(DrRows, kin), kOutF = offsetof(DrRows, kout), kBeta = offsetof(DrRows, beta);
-        float y[2][16];
-        float2 f[4], beta[4];
+        uint64_t y[2][8], f[4], beta[4];  // pairs of tokens
         factors(kRev ? kOutF : kIn, f);
+        if (!kRev) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) f[m] ^= kMinus;
+        }
         factors(kBeta, beta);
         if (!kRev) {
 #pragma unroll
@@ -381,10 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
             ldmatrix4_trans(at, w[0], w[1], w[2], w[3]);
             ldmatrix4_trans(at + 16 * 128, w[4], w[5], w[6], w[7]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              y[q][2 * e] = unit ? 0.f : lo_f(w[e]);
-              y[q][2 * e + 1] = unit ? 0.f : hi_f(w[e]);
-            }
+            for (int e = 0; e < 8; ++e) y[q][e] = unit ? 0 : pk2(lo_f(w[e]), hi_f(w[e]));
           }
         }
         wait_on(bar.x_full, parity(i), wait);
@@ -400,17 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
             tmem_ld_16x256_x4_async(at + kTmO + 32 * sub, g);
             tmem_wait_ld16(g);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[q][e] = __uint_as_float(g[e]);
+            for (int e = 0; e < 8; ++e) y[q][e] = pk2(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
           }
           tmem_wait_ld16(x);
           uint32_t t0[8], t1[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 &w = f[e >> 1], &b = beta[e >> 1];
-            float &y0 = y[q][2 * e], &y1 = y[q][2 * e + 1];
-            y0 = fmaf(kRev ? w.x : -w.x, __uint_as_float(x[2 * e]), y0);
-            y1 = fmaf(kRev ? w.y : -w.y, __uint_as_float(x[2 * e + 1]), y1);
-            split2(b.x * y0, b.y * y1, t0[e], t1[e]);
+            y[q][e] = fma2(f[e >> 1], pk2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), y[q][e]);
+            split2(mul2(beta[e >> 1], y[q][e]), t0[e], t1[e]);
           }
           tmem_st_16x128_async(at + kTmY + 16 * sub, t0);
           tmem_st_16x128_async(at + kTmY + 32 + 16 * sub, t1);
@@ -420,6 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         if (kRev) pipe::warp_arrive(bar.o_free);
         pipe::warp_arrive(bar.y_ready);
         factors(kRev ? kIn : kOutF, f);
+        if (kRev) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) f[m] ^= kMinus;
+        }
         if (kKeeps) {  // the chunk before has been read out of the staging tile
           if (tt == 0) bulk_wait_read0();
           role_sync<2, kTeam>();
@@ -435,11 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 &w = f[e >> 1], &b = beta[e >> 1];
-            const float e0 = y[q][2 * e] - __uint_as_float(x[2 * e]), e1 = y[q][2 * e + 1] - __uint_as_float(x[2 * e + 1]);
-            const float d0 = b.x * e0, d1 = b.y * e1;
-            t2[e] = MODE == kOut ? tc::pack_bf16x2(d0, d1) : tc::pack_bf16x2(e0, e1);
-            split2(kRev ? -w.x * d0 : w.x * d0, kRev ? -w.y * d1 : w.y * d1, t0[e], t1[e]);
+            const uint64_t add = fma2(pk2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kMinusOne, y[q][e]), d = mul2(beta[e >> 1], add);
+            float v0, v1;
+            upk2(MODE == kOut ? d : add, v0, v1);
+            if (MODE != kSum) t2[e] = tc::pack_bf16x2(v0, v1);
+            split2(mul2(f[e >> 1], d), t0[e], t1[e]);
           }
           tmem_st_16x128_async(at + kTmY + 16 * sub, t0);
           tmem_st_16x128_async(at + kTmY + 32 + 16 * sub, t1);
@@ -478,31 +485,40 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     }
   } else if (warp < kOutWarp0) {
     // ------------------------------------------------------------ state
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
     const int quad = warp & 3, sub = (warp - kStateWarp0) >> 2;
     if (quad < 2 * VB) {
       constexpr int kCols = 32 * KB;  // state rows (dk) of a thread
       const int c = 32 * quad + lane, a0 = sub * kCols;
       const size_t dd = (size_t)p.dk * dv, item = (size_t)place * p.H + h;
-      float S[kCols];
+      uint64_t S[kCols / 2];  // pairs along dk
       {
         const float *in = args.first ? args.first + item * dd + c : nullptr;
         const bool col = in && c < dv;
 #pragma unroll
-        for (int x = 0; x < kCols; ++x) S[x] = unit ? (a0 + x == c ? 1.f : 0.f) : col && a0 + x < p.dk ? in[(size_t)(a0 + x) * dv] : 0.f;
+        for (int x = 0; x < kCols; x += 2) {  // dk is even
+          const bool row = col && a0 + x < p.dk;
+          float v0 = row ? in[(size_t)(a0 + x) * dv] : 0.f, v1 = row ? in[(size_t)(a0 + x + 1) * dv] : 0.f;
+          if (unit) v0 = a0 + x == c ? 1.f : 0.f, v1 = a0 + x + 1 == c ? 1.f : 0.f;
+          S[x / 2] = pk2(v0, v1);
+        }
       }
       // the thread's 8 x 16 bytes of a kept state, 64 VB apart
       constexpr size_t kTile = 64 * KB * 64 * VB;
       const size_t mine = ((size_t)(a0 / 8) * (64 * VB) + c) * 8;
       constexpr int kTeam = 128 * VB;
+      auto pack = [](uint64_t v) {
+        float x, y;
+        upk2(v, x, y);
+        return tc::pack_bf16x2(x, y);
+      };
       auto keep = [&](size_t at) {  // rounded as the operand's first term is
         if (sub + quad == 0 && lane == 0) bulk_wait_read0();
         role_sync<4, kTeam>();
 #pragma unroll
         for (int x = 0; x < kCols; x += 8)
           pipe::sts_u4(s0 + L::kKept + 2 * (uint32_t)mine + (x / 8) * (64 * VB) * 16,
-                       make_uint4(tc::pack_bf16x2(S[x], S[x + 1]), tc::pack_bf16x2(S[x + 2], S[x + 3]),
-                                  tc::pack_bf16x2(S[x + 4], S[x + 5]), tc::pack_bf16x2(S[x + 6], S[x + 7])));
+                       make_uint4(pack(S[x / 2]), pack(S[x / 2 + 1]), pack(S[x / 2 + 2]), pack(S[x / 2 + 3])));
         fence_async_smem();
         role_sync<4, kTeam>();
         if (sub + quad == 0 && lane == 0) {
@@ -522,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         for (int x = 0; x < kCols; x += 16) {
           uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) split2(S[x + 2 * e], S[x + 2 * e + 1], hi[e], lo[e]);
+          for (int e = 0; e < 8; ++e) split2(S[x / 2 + e], hi[e], lo[e]);
           tmem_st8_async(pipe::tmem_quad(tmem + kTmS, (a0 + x) / 2), hi);
           tmem_st8_async(pipe::tmem_quad(tmem + kTmS + 64, (a0 + x) / 2), lo);
         }
@@ -531,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         pipe::warp_arrive(bar.s_ready);
         if (kKeeps) keep((size_t)(slot0 + chunk(i)) * p.H + h);  // beside the chunk's products
         wait_full(i);
-        const float all_hi = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_hi)), all_lo = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_lo));
+        const float ah = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_hi)), al = pipe::lds_f(rows_of(i) + offsetof(DrRows, all_lo));
+        const uint64_t all_hi = pk2(ah, ah), all_lo = pk2(al, al);
         pipe::warp_arrive(&bar.free[i % kStages]);
         wait_on(bar.w_full, parity(i), wait);
         tc_fence_after();
@@ -540,7 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           float w[16];
           tmem_ld16(pipe::tmem_quad(tmem + kTmW, a0 + x), w);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) S[x + e] = fmaf(S[x + e], all_hi, fmaf(S[x + e], all_lo, w[e]));
+          for (int e = 0; e < 8; ++e) {
+            uint64_t &s = S[x / 2 + e];
+            s = fma2(s, all_hi, fma2(s, all_lo, pk2(w[2 * e], w[2 * e + 1])));
+          }
         }
         tc_fence_before();
       }
@@ -550,12 +570,24 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
       float *to = args.seg && ends ? args.fin ? args.fin + ((size_t)seq * p.H + h) * dd : nullptr
                   : args.last      ? args.last + (unit ? (size_t)args.places * p.H * p.dk * p.dv : 0) + item * dd
                                    : nullptr;
-      if (to && c < dv) {
+      if (to && unit && c < dv) {  // M transposed, as the scan reads it
 #pragma unroll
-        for (int x = 0; x < kCols; ++x)
-          if (a0 + x < p.dk) to[(size_t)(a0 + x) * dv + c] = S[x];
+        for (int x = 0; x < kCols; x += 2)
+          if (a0 + x < p.dk) *reinterpret_cast<uint64_t *>(to + (size_t)c * p.dk + a0 + x) = S[x / 2];
+      } else if (to && c < dv) {
+#pragma unroll
+        for (int x = 0; x < kCols; x += 2) {
+          float v0, v1;
+          upk2(S[x / 2], v0, v1);
+          if (a0 + x < p.dk) {
+            to[(size_t)(a0 + x) * dv + c] = v0;
+            to[(size_t)(a0 + x + 1) * dv + c] = v1;
+          }
+        }
       }
     }
+  } else if (kIdle) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLastRegs));
   } else if (MODE == kOut) {
     // ------------------------------------------------------------ outputs
     const int quad = warp & 3, tt = threadIdx.x - 32 * kOutWarp0;
@@ -651,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
             ldmatrix4_trans(at, w[0], w[1], w[2], w[3]);
             ldmatrix4_trans(at + 16 * 128, w[4], w[5], w[6], w[7]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) split2(f[e >> 1].x * lo_f(w[e]), f[e >> 1].y * hi_f(w[e]), t0[e], t1[e]);
+            for (int e = 0; e < 8; ++e) tc::split2(f[e >> 1].x * lo_f(w[e]), f[e >> 1].y * hi_f(w[e]), t0[e], t1[e]);
             const uint32_t to = lanes + ((uint32_t)(16 * q) << 16) + kTmD + 16 * half;
             tmem_st_16x128_async(to, t0);
             tmem_st_16x128_async(to + 32, t1);
@@ -777,48 +809,56 @@ void launch_dr_tc_sums(const DrProblem &p, cudaStream_t s) {
 namespace {
 
 // Segments' states before their first tokens: S_next = M S + N, from the initial state on.  A block has 16 columns of a
-// state, a thread 8 of them in one row or two: M's row times the columns, which are in shared memory.
+// state, a thread 8 of them in one row: the warps read M, which is transposed, row by row, and the columns are in
+// shared memory.
 constexpr int kScanCols = 16;
 __global__ void __launch_bounds__(256) dr_scan_kernel(DrProblem p) {
+  extern __shared__ __align__(128) uint8_t smem[];  // two M
   __shared__ __align__(16) float S[128][kScanCols];
+  __shared__ uint64_t full[2];
   const int seq = blockIdx.x / p.H, h = blockIdx.x - seq * p.H, c0 = blockIdx.y * kScanCols, dk = p.dk, dv = p.dv;
-  const int row = threadIdx.x >> 1, c = c0 + 8 * (threadIdx.x & 1);
+  const int row = threadIdx.x & 127, half = 8 * (threadIdx.x >> 7), c = c0 + half;
   const size_t dd = (size_t)dk * dv, all = (size_t)p.seg_places * p.H;
   int a, len, slot0;
   dr_seq(p, seq, a, len, slot0);
   const int n = p.seg * kDrC, place0 = dr_place0(p, p.seg, a, seq), segments = len ? (len + n - 1) / n : 1;
   const bool live = row < dk && c < dv;  // dv is a multiple of 8
-  float x[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = live && p.init ? p.init[((size_t)seq * p.H + h) * dd + (size_t)row * dv + c + e] : 0.f;
+  float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  auto get = [&](const float *from) {
+    x[0] = reinterpret_cast<const float4 *>(from)[0], x[1] = reinterpret_cast<const float4 *>(from)[1];
+  };
+  auto put = [&](float *to) { reinterpret_cast<float4 *>(to)[0] = x[0], reinterpret_cast<float4 *>(to)[1] = x[1]; };
+  const uint32_t bytes = (uint32_t)(dk * dk * 4);
+  auto fetch = [&](int g) {  // thread 0
+    sm100::mbar_expect_tx(&full[g & 1], bytes);
+    pipe::bulk_load(smem + (g & 1) * bytes, p.seg_sums + all * dd + ((size_t)(place0 + g) * p.H + h) * ((size_t)dk * dk), bytes, &full[g & 1]);
+  };
+  if (threadIdx.x == 0) {
+    sm100::mbar_init(&full[0], 1);
+    sm100::mbar_init(&full[1], 1);
+    sm100::fence_mbar_init();
+    if (segments > 1) fetch(0);
+  }
+  __syncthreads();
+  if (live && p.init) get(p.init + ((size_t)seq * p.H + h) * dd + (size_t)row * dv + c);
   for (int g = 0; g < segments; ++g) {
     const size_t item = (size_t)(place0 + g) * p.H + h;
-    if (live) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p.seg_states[item * dd + (size_t)row * dv + c + e] = x[e];
-    }
+    if (live) put(p.seg_states + item * dd + (size_t)row * dv + c);
     if (g + 1 == segments) break;
+    __syncthreads();  // the columns and the other M are read
+    put(&S[row][half]);
+    if (threadIdx.x == 0 && g + 2 < segments) fetch(g + 1);
     __syncthreads();
-    if (row < 128) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) S[row][8 * (threadIdx.x & 1) + e] = x[e];
-    }
-    __syncthreads();
+    sm100::mbar_wait_drain(&full[g & 1], (g >> 1) & 1);
     if (live) {
-      const float4 *M = reinterpret_cast<const float4 *>(p.seg_sums + all * dd + item * ((size_t)dk * dk) + (size_t)row * dk);
-      const float *N = p.seg_sums + item * dd + (size_t)row * dv + c;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = N[e];
-#pragma unroll 4
-      for (int k = 0; k < dk; k += 4) {
-        const float4 m = __ldg(M + k / 4);
-        const float f[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 s0 = *reinterpret_cast<const float4 *>(&S[k + j][8 * (threadIdx.x & 1)]), s1 = *reinterpret_cast<const float4 *>(&S[k + j][8 * (threadIdx.x & 1) + 4]);
-          x[0] = fmaf(f[j], s0.x, x[0]), x[1] = fmaf(f[j], s0.y, x[1]), x[2] = fmaf(f[j], s0.z, x[2]), x[3] = fmaf(f[j], s0.w, x[3]);
-          x[4] = fmaf(f[j], s1.x, x[4]), x[5] = fmaf(f[j], s1.y, x[5]), x[6] = fmaf(f[j], s1.z, x[6]), x[7] = fmaf(f[j], s1.w, x[7]);
-        }
+      const float *M = reinterpret_cast<const float *>(smem + (g & 1) * bytes) + row;
+      get(p.seg_sums + item * dd + (size_t)row * dv + c);
+#pragma unroll 8
+      for (int k = 0; k < dk; ++k) {
+        const float f = M[k * dk];
+        const float4 s0 = *reinterpret_cast<const float4 *>(&S[k][half]), s1 = *reinterpret_cast<const float4 *>(&S[k][half + 4]);
+        x[0].x = fmaf(f, s0.x, x[0].x), x[0].y = fmaf(f, s0.y, x[0].y), x[0].z = fmaf(f, s0.z, x[0].z), x[0].w = fmaf(f, s0.w, x[0].w);
+        x[1].x = fmaf(f, s1.x, x[1].x), x[1].y = fmaf(f, s1.y, x[1].y), x[1].z = fmaf(f, s1.z, x[1].z), x[1].w = fmaf(f, s1.w, x[1].w);
       }
     }
   }
@@ -827,7 +867,9 @@ __global__ void __launch_bounds__(256) dr_scan_kernel(DrProblem p) {
 }  // namespace
 
 void launch_dr_tc_scan(const DrProblem &p, cudaStream_t s) {
-  dr_scan_kernel<<<dim3((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kScanCols - 1) / kScanCols)), 256, 0, s>>>(p);
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(dr_scan_kernel), 2 * 128 * 128 * 4, allowed);
+  dr_scan_kernel<<<dim3((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kScanCols - 1) / kScanCols)), 256, 2 * p.dk * p.dk * 4, s>>>(p);
 }
 
 void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s) {

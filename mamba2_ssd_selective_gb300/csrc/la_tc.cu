@@ -126,22 +126,6 @@ struct Bars {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// x minus the low (high) bf16 of w, exact where that is x's leading part: one
-// mixed-precision instruction on the FMA pipe, instead of a mask on the ALU
-__device__ __forceinline__ float minus_lo(float x, uint32_t w) {
-  float d;
-  asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %1;\n mov.b16 m, 0xbf80;\n fma.rn.f32.bf16 %0, l, m, %2;\n}"
-      : "=f"(d)
-      : "r"(w), "f"(x));
-  return d;
-}
-__device__ __forceinline__ float minus_hi(float x, uint32_t w) {
-  float d;
-  asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %1;\n mov.b16 m, 0xbf80;\n fma.rn.f32.bf16 %0, h, m, %2;\n}"
-      : "=f"(d)
-      : "r"(w), "f"(x));
-  return d;
-}
 // Two values x as three bf16 pairs that add up to them: each term is the rest's
 // leading 8 bits (cut off, so that the rest is exact and packing is a byte
 // permute), the last one rounded.
@@ -149,10 +133,10 @@ __device__ __forceinline__ void split3(uint64_t x, uint32_t &a, uint32_t &b, uin
   float f0, f1;
   upk2(x, f0, f1);
   a = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
-  f0 = minus_lo(f0, a);
-  f1 = minus_hi(f1, a);
+  f0 = tc::minus_lo(f0, a);
+  f1 = tc::minus_hi(f1, a);
   b = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
-  c = tc::pack_bf16x2(minus_lo(f0, b), minus_hi(f1, b));
+  c = tc::pack_bf16x2(tc::minus_lo(f0, b), tc::minus_hi(f1, b));
 }
 
 // The roles' loops together are more than the instruction caches hold at once, and code
