@@ -4,10 +4,12 @@
 // A block of four warps takes a chunk and a head of q and k: K K^T and Q K^T by matrix instructions, a warp's 16 rows of both
 // in its registers, for all states that share the head; A and P share their exponentials.  A warp has 8 rows of the upper
 // and 8 of the lower half, so that all warps have as much below the diagonal.
-// N = (I + A diag(b))^-1 A in blocks, without a division by b: diagonal blocks of 16 column by column, a thread to a
-// column, then twice the block below two that are done (b1, b2: theirs),
-//     N21 = M - N22 (b2 M),   M = A21 - A21 (b1 N11),
-// in place, since A's blocks are not read again.  Sums of log decays are whole numbers of 2^-32 (dr_rows.cuh).
+// N = (I + A diag(b))^-1 A in blocks of 16, without a division by b.  The diagonal's blocks column by column, a thread to a
+// column; then a warp has a column J of blocks, from the diagonal down,
+//     N_IJ = M - N_II (b_I M),    M = A_IJ - sum_(J <= K < I) A_IK (b_K N_KJ),
+// transposed, so that what a step makes is the next one's first operand as it stands in the registers.  Both operands are
+// sums of two bf16 terms, which is how N goes out too.  (With products of 16 and 32 rows in fp32 on the CUDA cores the
+// tables of 4 x 8192 tokens, 32 heads took 239 us.)
 #include "delta.h"
 #include "dr_rows.cuh"
 #include "tc_pipe.cuh"
@@ -20,20 +22,19 @@ namespace {
 using bf16 = __nv_bfloat16;
 using namespace sm100;
 
-constexpr int kThreads = 128, kLd = kDrC + 4;
+constexpr int kThreads = 128;
 constexpr uint32_t kBox = 8192;
-
 constexpr int kHeads = 2;  // whose rows' factors are made at once, by a warp each
-// The boxes of K and Q, and in their place, once their products are made, N's and P's tiles on their way out.
-constexpr uint32_t kTilesN = 0, kTilesP = 2 * kBox;
+// The boxes of K and Q, and in their place, once their products are made, N's and P's tiles on their way out; behind them
+// A's two terms, whose diagonal blocks of 16 hold A itself instead (diag_at).
+constexpr uint32_t kTilesN = 0, kTilesP = 2 * kBox, kTilesA = 4 * kBox;
 struct Work {
-  float m[kDrC][kLd];  // A, then N
   float rk[kDrC], rq[kDrC];
   DrRows rows[kHeads];
   int first_nan[kHeads];
   uint64_t full;
 };
-constexpr int kSmemBytes = 4 * (int)kBox + (int)sizeof(Work) + 1024;
+constexpr int kSmemBytes = 6 * (int)kBox + (int)sizeof(Work) + 1024;
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -47,36 +48,62 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x[r][c] -= sum_k A[r][k] b[k] B[k][c], k from k0 to k1: ROWS rows STEP apart x 2 values a thread
-template <int ROWS, int STEP>
-__device__ __forceinline__ void minus_product(float (&x)[ROWS][2], const float *A, const float *b, const float *B, int k0, int k1) {
-#pragma unroll 4
-  for (int k = k0; k < k1; k += 4) {
-    const float4 bb = *reinterpret_cast<const float4 *>(b + k);
-    float2 y[4];
+// Element (r, c) of the diagonal block from row 16 I on, in fp32: columns 0-7 in the first tile's place of the block, 8-15 in
+// the second's
+__device__ __forceinline__ uint32_t diag_at(uint32_t tiles, int I, int r, int c) {
+  const int row = 16 * I + r;
+  return tiles + (c & 8 ? kBox : 0) + row * 128 + (((2 * I + ((c & 7) >> 2)) ^ (row & 7)) << 4) + (c & 3) * 4;
+}
+// A 16 x 16 block as a result or a first operand of the matrix instruction: rows lane / 4 and 8 more, columns
+// 2 (lane % 4) and the next, [.][2..3] in the second rows, [1] 8 columns on.
+using Block = float[2][4];
+// the transpose of the block of a tile's two terms from row r0, column c0 on
+__device__ __forceinline__ void load_transposed(Block &x, uint32_t tile, int r0, int c0, int lane) {
+  const uint32_t at = tile + sw128_offset(r0 + (lane & 7) + 8 * (lane >> 4), c0 + 8 * ((lane >> 3) & 1));
+  uint32_t h[4], l[4];
+  ldmatrix4_trans(at, h[0], h[1], h[2], h[3]);
+  ldmatrix4_trans(at + kBox, l[0], l[1], l[2], l[3]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const float2 *>(B + (k + e) * kLd);
-    y[0].x *= -bb.x, y[0].y *= -bb.x, y[1].x *= -bb.y, y[1].y *= -bb.y;
-    y[2].x *= -bb.z, y[2].y *= -bb.z, y[3].x *= -bb.w, y[3].y *= -bb.w;
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const float4 a = *reinterpret_cast<const float4 *>(A + r * STEP * kLd + k);
-      x[r][0] = fmaf(a.x, y[0].x, fmaf(a.y, y[1].x, fmaf(a.z, y[2].x, fmaf(a.w, y[3].x, x[r][0]))));
-      x[r][1] = fmaf(a.x, y[0].y, fmaf(a.y, y[1].y, fmaf(a.z, y[2].y, fmaf(a.w, y[3].y, x[r][1]))));
-    }
+  for (int e = 0; e < 4; ++e) {
+    x[e >> 1][2 * (e & 1)] = __uint_as_float(h[e] << 16) + __uint_as_float(l[e] << 16);
+    x[e >> 1][2 * (e & 1) + 1] = __uint_as_float(h[e] & 0xffff0000u) + __uint_as_float(l[e] & 0xffff0000u);
   }
 }
-template <int ROWS, int STEP> __device__ __forceinline__ void get(float (&x)[ROWS][2], const float *m) {
+struct Terms {
+  uint32_t hi[4], lo[4];
+};
+// a block's columns times -b, as a first operand of two terms
+__device__ __forceinline__ void make_terms(Terms &t, const Block &x, const float *b, int lane) {
+  const float2 b0 = *reinterpret_cast<const float2 *>(b + 2 * (lane & 3)), b1 = *reinterpret_cast<const float2 *>(b + 8 + 2 * (lane & 3));
 #pragma unroll
-  for (int e = 0; e < ROWS; ++e) {
-    const float2 t = *reinterpret_cast<const float2 *>(m + e * STEP * kLd);
-    x[e][0] = t.x, x[e][1] = t.y;
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = e >> 1 ? b1 : b0;
+    tc::split2(-f.x * x[e >> 1][2 * (e & 1)], -f.y * x[e >> 1][2 * (e & 1) + 1], t.hi[e], t.lo[e]);
   }
 }
-template <int ROWS, int STEP> __device__ __forceinline__ void put(const float (&x)[ROWS][2], float *m) {
+// x += t B^T, B the block of a tile's two terms from row r0, column c0 on (what two low terms make is left out)
+__device__ __forceinline__ void add_product(Block &x, const Terms &t, uint32_t tile, int r0, int c0, int lane) {
+  const uint32_t at = tile + sw128_offset(r0 + (lane & 7) + 8 * (lane >> 4), c0 + 8 * ((lane >> 3) & 1));
+  uint32_t h[4], l[4];
+  ldmatrix4(at, h);
+  ldmatrix4(at + kBox, l);
 #pragma unroll
-  for (int e = 0; e < ROWS; ++e) *reinterpret_cast<float2 *>(m + e * STEP * kLd) = make_float2(x[e][0], x[e][1]);
+  for (int n = 0; n < 2; ++n) {
+    mma16816(x[n], t.lo, h[2 * n], h[2 * n + 1]);
+    mma16816(x[n], t.hi, l[2 * n], l[2 * n + 1]);
+    mma16816(x[n], t.hi, h[2 * n], h[2 * n + 1]);
+  }
 }
+// the block's transpose as a tile's two terms, from row r0, column c0 on
+__device__ __forceinline__ void store_transposed(const Block &x, uint32_t tile, int r0, int c0, int lane) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) tc::split2(x[e >> 1][2 * (e & 1)], x[e >> 1][2 * (e & 1) + 1], h[e], l[e]);
+  const uint32_t at = tile + sw128_offset(r0 + (lane & 7) + 8 * (lane >> 4), c0 + 8 * ((lane >> 3) & 1));
+  stmatrix4_trans(at, h[0], h[1], h[2], h[3]);
+  stmatrix4_trans(at + kBox, l[0], l[1], l[2], l[3]);
+}
+__device__ __forceinline__ float lds(uint32_t at) { return pipe::lds_f(at); }
 
 __device__ __forceinline__ void sts(uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 
@@ -86,8 +113,7 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap tk, const DrProblem p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = tc::aligned_smem(smem_raw);
-  Work &w = *reinterpret_cast<Work *>(sm + 4 * kBox);
-  float(*m)[kLd] = w.m;
+  Work &w = *reinterpret_cast<Work *>(sm + 6 * kBox);
   const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (slot == 0 && hk == 0 && tid == 0) *p.status = 0;
   int t0, n;
@@ -167,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
         if (lane == 0) w.first_nan[warp] = sums.first_nan;
       }
     }
-    if (g > 0 && tid == kThreads - 1) bulk_wait_read0();  // the last head's P has left
+    if (g > 0 && (tid == 0 || tid == kThreads - 1)) bulk_wait_read0();  // the last head's tiles have left
     __syncthreads();
     const DrRows &rows = w.rows[g % kHeads];
     const int nan_at = w.first_nan[g % kHeads];
@@ -199,7 +225,25 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
             q[0] = j <= i ? q[0] : 0.f, q[1] = j + 1 <= i ? q[1] : 0.f;
           }
         }
-        *reinterpret_cast<float2 *>(&m[i][j]) = make_float2(a[0], a[1]);
+        if (8 * y <= first) {
+          if (8 * (y & ~1) == (first & ~15)) {  // a block of the diagonal
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(diag_at(s0 + kTilesA, first >> 4, i & 15, j & 15)), "f"(a[0]), "f"(a[1]) : "memory");
+          } else {
+            uint32_t ah, al;
+            tc::split2(a[0], a[1], ah, al);
+            const uint32_t to = s0 + kTilesA + i * 128 + 2 * c0 + ((y ^ (lane >> 2)) << 4);
+            sts(to, ah);
+            sts(to + kBox, al);
+          }
+        } else {
+          if (8 * (y & ~1) == (first & ~15))  // its upper right quarter
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(diag_at(s0 + kTilesA, first >> 4, i & 15, j & 15)), "f"(0.f), "f"(0.f) : "memory");
+          if (g == 0) {  // above the diagonal N has zeros, which stay
+            const uint32_t to = s0 + kTilesN + i * 128 + 2 * c0 + ((y ^ (lane >> 2)) << 4);
+            sts(to, 0);
+            sts(to + kBox, 0);
+          }
+        }
         uint32_t qh, ql;
         tc::split2(q[0], q[1], qh, ql);
         sts(row + ((y ^ (lane >> 2)) << 4), qh);  // the 128-byte swizzle: the row is lane / 4 modulo 8
@@ -217,66 +261,48 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
       pipe::bulk_store(reinterpret_cast<uint8_t *>(p.N) + at * (4 * kDrTile) + 2 * kDrTile, s0 + kTilesP, PT * kBox);
       bulk_commit();
     }
-    if (tid < kDrC) {
+    if (tid >= kDrC) {
       float x[16];
-      const int d0 = tid & 48, c = tid & 15;  // column c of the diagonal block from d0
+      const int I = (tid >> 4) & 3, c = tid & 15;  // column c of the diagonal's block I
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = m[d0 + i][d0 + c];  // zeros up to the diagonal
+      for (int i = 0; i < 16; ++i) x[i] = lds(diag_at(s0 + kTilesA, I, i, c));  // zeros up to the diagonal
 #pragma unroll
       for (int k = 1; k < 15; ++k) {
-        const float f = -rows.beta[d0 + k] * x[k];
+        const float f = -rows.beta[16 * I + k] * x[k];
 #pragma unroll
-        for (int i = k + 1; i < 16; ++i) x[i] = fmaf(f, m[d0 + i][d0 + k], x[i]);
+        for (int i = k + 1; i < 16; ++i) x[i] = fmaf(f, lds(diag_at(s0 + kTilesA, I, i, k)), x[i]);
       }
-      __syncwarp();  // a block is one half-warp's
 #pragma unroll
-      for (int i = 1; i < 16; ++i) m[d0 + i][d0 + c] = x[i];
+      for (int i = 0; i < 16; ++i) {
+        const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]), lo = __float2bfloat16_rn(x[i] - __bfloat162float(hi));
+        uint8_t *to = sm + kTilesN + sw128_offset(16 * I + i, 16 * I + c);
+        *reinterpret_cast<__nv_bfloat16 *>(to) = hi;
+        *reinterpret_cast<__nv_bfloat16 *>(to + kBox) = lo;
+      }
     }
     __syncthreads();
-    {  // two blocks of 16 x 16, a half of the threads each: 2 x 2 values a thread
-      const int d0 = tid >> 6 ? 32 : 0, r = 2 * ((tid & 63) >> 3), c = 2 * (tid & 7);
-      float x[2][2], *mine = &m[d0 + 16 + r][d0 + c];
-      get<2, 1>(x, mine);
-      minus_product<2, 1>(x, &m[d0 + 16 + r][d0], rows.beta + d0, &m[d0][d0 + c], 0, 16);
-      __syncthreads();
-      put<2, 1>(x, mine);
-      __syncthreads();
-      minus_product<2, 1>(x, &m[d0 + 16 + r][d0 + 16], rows.beta + d0 + 16, &m[d0 + 16][d0 + c], 0, 16);
-      __syncthreads();
-      put<2, 1>(x, mine);
-    }
-    __syncthreads();
-    {  // 32 x 32: 8 values a thread.  N11 has zeros up to its diagonal, so a warp's 8 columns leave the sum's first terms out
-      const int r = lane & 7, c = 8 * warp + 2 * (lane >> 3);
-      float x[4][2];
-      get<4, 8>(x, &m[32 + r][c]);
-      minus_product<4, 8>(x, &m[32 + r][0], rows.beta, &m[0][c], 8 * warp, 32);
-      __syncthreads();
-      put<4, 8>(x, &m[32 + r][c]);
-    }
-    __syncthreads();
-    {  // and N22 from it, so that a warp's 8 rows leave out the last
-      const int r = 8 * warp + 4 * (lane >> 4), c = 2 * (lane & 15);
-      float x[4][2];
-      get<4, 1>(x, &m[32 + r][c]);
-      minus_product<4, 1>(x, &m[32 + r][32], rows.beta + 32, &m[32][c], 0, 8 * warp + 8);
-      if (tid == 0) bulk_wait_read0();  // the last head's N has left
-      __syncthreads();
-      put<4, 1>(x, &m[32 + r][c]);
-    }
-    __syncthreads();
+    {
+      const int J = warp;
+      Terms done[3];  // of -b N_KJ, transposed
+      Block x;
+      if (J < 3) {
+        load_transposed(x, s0 + kTilesN, 16 * J, 16 * J, lane);
+        make_terms(done[0], x, rows.beta + 16 * J, lane);
+      }
 #pragma unroll
-    for (int e = tid; e < kDrC * 8; e += kThreads) {  // N's terms, 8 columns at a time
-      const int i = e >> 3, y = e & 7;
-      const float4 x0 = *reinterpret_cast<const float4 *>(&m[i][8 * y]), x1 = *reinterpret_cast<const float4 *>(&m[i][8 * y + 4]);
-      uint4 hi, lo;
-      tc::split2(x0.x, x0.y, hi.x, lo.x);
-      tc::split2(x0.z, x0.w, hi.y, lo.y);
-      tc::split2(x1.x, x1.y, hi.z, lo.z);
-      tc::split2(x1.z, x1.w, hi.w, lo.w);
-      const uint32_t to = s0 + kTilesN + i * 128 + ((y ^ (i & 7)) << 4);
-      pipe::sts_u4(to, hi);
-      pipe::sts_u4(to + kBox, lo);
+      for (int d = 1; d < 4; ++d) {
+        const int I = J + d;
+        if (I < 4) {
+          load_transposed(x, s0 + kTilesA, 16 * I, 16 * J, lane);
+#pragma unroll
+          for (int e = 0; e < d; ++e) add_product(x, done[e], s0 + kTilesA, 16 * I, 16 * (J + e), lane);
+          Terms t;
+          make_terms(t, x, rows.beta + 16 * I, lane);
+          add_product(x, t, s0 + kTilesN, 16 * I, 16 * I, lane);
+          store_transposed(x, s0 + kTilesN, 16 * I, 16 * J, lane);
+          if (d < 3) make_terms(done[d], x, rows.beta + 16 * I, lane);
+        }
+      }
     }
     fence_async_smem();
     __syncthreads();
