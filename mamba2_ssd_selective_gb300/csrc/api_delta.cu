@@ -14,7 +14,7 @@ namespace {
 struct DrPlan {
   bool tc;
   int slots, seg, places;  // seg: chunks of a segment, 0: sequences are not cut
-  size_t seg_states, seg_sums, status, rows, N, P, S, dS, E, Z, dqp, dkp, dots, total;  // workspace offsets
+  size_t seg_states, seg_sums, status, rows, N, P, S, dS, E, Z, dqp, dkp, total;  // workspace offsets
 };
 
 long long dr_rows(const ssd_delta_rule_dims *d) { return d->packed ? d->total_tokens : (long long)d->nseq * d->seqlen; }
@@ -87,13 +87,12 @@ DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
   }
   if (backward) {
     const size_t eb = pl.tc ? 2 : 4, padded = (size_t)dr_padded(d->headdim_k) * dr_padded(d->headdim_v);
-    pl.S = take(pl.tc ? (chunks + (size_t)d->nseq * d->nheads) * padded * 2 : chunks * state * 4);
+    pl.S = take(chunks * (pl.tc ? padded * 2 : state * 4));
     pl.dS = take(chunks * (pl.tc ? padded * 2 : state * 4));
     pl.E = take(tokens * d->headdim_v * eb);
     pl.Z = take(tokens * d->headdim_v * eb);
     pl.dqp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
     pl.dkp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
-    pl.dots = take(pl.tc ? chunks * 4 * 4 : 0);
   }
   pl.total = off;
   return pl;
@@ -164,7 +163,7 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
     p.seg = pl->seg, p.seg_places = pl->places;
     p.seg_states = at(pl->seg_states), p.seg_sums = at(pl->seg_sums);
     p.S = at(pl->S), p.dS = at(pl->dS), p.E = at(pl->E), p.Z = at(pl->Z);
-    p.dqp = at(pl->dqp), p.dkp = at(pl->dkp), p.dots = at(pl->dots);
+    p.dqp = at(pl->dqp), p.dkp = at(pl->dkp);
   }
   return p;
 }
@@ -174,7 +173,7 @@ ssd_status dr_forward_impl(const DrProblem &p, bool tc, void *o, int64_t os, flo
   SSD_LAUNCH("dr_prep", tc ? launch_dr_prep_tc(p, false, s) : launch_dr_prep<T>(p, s));
   if (p.seg) {
     SSD_LAUNCH("dr_sums", launch_dr_tc_sums(p, s));
-    SSD_LAUNCH("dr_scan", launch_dr_tc_scan(p, s));
+    SSD_LAUNCH("dr_scan", launch_dr_tc_scan(p, fin, s));
   }
   SSD_LAUNCH("dr_chain", tc ? launch_dr_tc_chain(p, o, os, fin, s) : launch_dr_chain<T>(p, o, os, fin, s));
   return launch_status();

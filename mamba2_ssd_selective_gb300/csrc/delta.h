@@ -17,7 +17,7 @@
 //     dK = diag(e^(Gall - G)) D dS^T - diag(e^G) dV S^T + (scale dP L)^T Q + (dA L) K + (dA L)^T K
 //     dlog_decay_t = sum_{i >= t} (q_i.dq_i - v_i.dv_i) + <S_next, dS>
 // The last line: a decay at t scales all that passes from before t to t and later, and both sums count it: q.dq
-// what tokens read, v.dv what they would have read of their own chunk's additions.
+// what tokens read, v.dv what they would have read of their own chunk's additions.  (dr_grads_tc.cu counts it otherwise.)
 // q and k stay as they are (exact as bf16 operands): 1 / |q| and 1 / |k| are part of the rows' factors and of A, P.
 #pragma once
 
@@ -55,10 +55,9 @@ struct DrProblem {
   // backward: the states before the chunks and the gradients of those behind them (dk, dv), E and Z (total, H, dv).
   // Tensor cores: N's and P's two bf16 terms as four tiles of (64, 64) in the 128-byte swizzle, at N; E and Z are bf16,
   // and so are the states, at S and dS, in blocks of 8 columns: element (m, c) of (dk, dv), both padded to 64 or 128, at
-  // (m / 8) 8 dv + 8 c + m % 8; behind the chunks' the final states of the sequences' heads.
+  // (m / 8) 8 dv + 8 c + m % 8.
   float *S, *dS, *E, *Z;
   float *dqp, *dkp;  // (total, H, dk): gradients of the unit q and k of each state head
-  float *dots;       // (chunk, 4): parts of <state behind the chunk, its gradient>, one for each 32 columns of dv
   // Tensor cores: sequences cut into segments of `seg` chunks (0: not cut), their places (dr_place0), the states before
   // them, and for all but last ones N, the state that a segment makes of zero, and M, so that S_next = M S + N (at
   // seg_sums: N of all places, then M)
@@ -131,7 +130,7 @@ __device__ __forceinline__ void dr_segment(const DrProblem &p, int seg, int plac
   }
   dr_seq(p, seq, a, len, slot0);
   const long long off = (long long)(place - dr_place0(p, seg, a, seq)) * n;
-  if (off < 0 || (off >= len && off > 0)) {
+  if (off < 0 || off >= len) {  // (empty sequences have no segment either: the scan sees to their states)
     seq = -1;
     return;
   }
@@ -147,9 +146,9 @@ template <typename T> void launch_dr_prep(const DrProblem &p, cudaStream_t s);
 void launch_dr_prep_tc(const DrProblem &p, bool backward, cudaStream_t s);
 // dr_tc.cu: the chains for bf16, both widths at most 128
 void launch_dr_tc_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);
-// cut sequences: the segments' M and N, then the states before them
+// cut sequences: the segments' M and N, then the states before them, and the final ones of empty sequences
 void launch_dr_tc_sums(const DrProblem &p, cudaStream_t s);
-void launch_dr_tc_scan(const DrProblem &p, cudaStream_t s);
+void launch_dr_tc_scan(const DrProblem &p, float *fin, cudaStream_t s);
 void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s);
 // dr_simt.cu: the chain of chunks (o null: only S and E, for backward), its reverse, and the gradients
 template <typename T> void launch_dr_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);

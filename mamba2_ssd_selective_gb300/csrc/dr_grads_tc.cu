@@ -3,9 +3,13 @@
 // in the factors), with L_ij = e^(G_i - G_j):
 //     Wq_ij = scale L_ij / |q_i| / |k_j| (dO E^T)_ij b_j   (j <= i),    Wk_ij = -L_ij / |k_i| / |k_j| b_i (Z E^T)_ij b_j   (j < i)
 //     dq = qin dO S^T + Wq K,      dk = kout b E dS^T - kin b Z S^T + Wk K + Wq^T Q + Wk^T K
-//     dv = b Z,  dbeta = E.Z (rows),  dlog_decay: the suffix sums of q.dq - v.dv, and <S_next, dS> behind them
-// (q.dq as scale e^G/|q| (dO S^T).q + sum_j Wq_ij q_i.k_j, with the weights before their rounding: the sums' terms have both
-// signs, and their errors show; <S_next, dS> is the reverse chain's, with the gradient unrounded)
+//     dv = b Z,  dbeta = E.Z (rows)
+//     dlog_decay_t = sum_(i >= t) (qin q_i.(dO S^T)_i - kin b_i k_i.(Z S^T)_i) + sum_(i >= t > j) M_ij
+//                    + sum_(j < t) kout b_j k_j.(E dS^T)_j + e^Gall <S, dS>,    M = Wq o (Q K^T) + Wk o (K K^T)
+// (what passes t: what is read and written over from the state before the chunk, what tokens behind t have of tokens
+// before it, what the state behind the chunk has of them and of the state before.  delta.h's sum of q.dq - v.dv is the same, but
+// each token's own addition, which no decay touches, is in both of its terms: with operands of bf16, heads that forget
+// fast had 2% left of that difference.  The sum over pairs goes as row sums less column sums of the same fp32 M.)
 // and the division by the lengths last: dq - q (q.dq) / |q|^2, likewise dk.
 //
 // Persistent CTAs; a CTA takes a chunk and a head of q and k and goes through the states that share it, dq and dk
@@ -29,10 +33,15 @@ constexpr int kThreads = 352, kTeam = 256;
 constexpr uint32_t kBox = 8192;  // [64 rows x 64 columns] bf16
 constexpr uint32_t kTmA = 0, kTmC = 128, kTmW = 256, kTmB = 384, kTmCols = 512;  // products with S, dS, K (before: Q K^T); with E and, later, [Q; K]
 
-// rows' sums of a step, by the step's parity: a step's are read while the next one's are made
-struct Sums {
-  float vdv[64], dot[2][64], kb[64];  // kb: beta / |k|
+// sums of a step, by the step's parity: a step's are read while the next one's are made
+struct alignas(16) Sums {
+  float kb[64];         // beta / |k|
+  float row[2][2][64];  // of q's and k's halves: (dO S^T).q or (Z S^T).k with their factors, and M's row
+  float col[4][64];     // M's columns, by quarters of its rows (q's halves, then k's)
+  float add[2][64];     // k.(E dS^T) with its factors, by halves
+  float ss[8], all;     // <S, dS>, by warps; e^Gall
 };
+static_assert(sizeof(Sums) % 16 == 0, "kb is read 16 bytes at a time");
 struct Misc {
   Sums sums[2];
   float along[2][2][64];  // of dq and dk along q and k, by halves
@@ -44,8 +53,7 @@ template <int KB, int VB> struct Layout {
   static constexpr uint32_t kQK = kDs + kTile;         // Q, K: likewise pairs
   static constexpr uint32_t kQKs = KB * 2 * kBox;               // two buffers
   static constexpr uint32_t kW = kQK + 2 * kQKs;                // Wq, Wk
-  static constexpr uint32_t kV = kW + 2 * kBox;
-  static constexpr uint32_t kRows = kV + VB * kBox;
+  static constexpr uint32_t kRows = kW + 2 * kBox;
   static constexpr uint32_t kMisc = kRows + (sizeof(DrRows) + 15) / 16 * 16;
   static constexpr uint32_t kBar = kMisc + sizeof(Misc);
   static constexpr uint32_t kEnd = kBar + 18 * 8 + 16;
@@ -54,7 +62,7 @@ template <int KB, int VB> struct Layout {
 };
 
 struct Args {
-  CUtensorMap q, k, dout, z, e, v, dq, dk;
+  CUtensorMap q, k, dout, z, e, dq, dk;
   DrProblem p;
   DrGrads g;
   WaitCtl wait;
@@ -91,18 +99,18 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
   const DrGrads &g = args.g;
   const WaitCtl wait = args.wait;
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
-  // rows (dO, Z, E, v, the factors) and states loaded / read; the others' names say what they are of
+  // rows (dO, Z, E, the factors) and states loaded / read; the others' names say what they are of
   uint64_t *in_full = bar, *in_free = bar + 1, *st_full = bar + 2, *st_free = bar + 3, *b_full = bar + 4, *w_ready = bar + 5,
            *out_full = bar + 6, *acc_free = bar + 7, *drain = bar + 8, *sums_full = bar + 9, *sums_free = bar + 11,
            *qk_full = bar + 13, *qk_free = bar + 15;  // [2] each
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::kBar + 18 * 8);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (warp == 0 && lane < 8) prefetch_tmap(&args.q + lane);
+  if (warp == 0 && lane < 7) prefetch_tmap(&args.q + lane);
   if (threadIdx.x == 32) {
     mbar_init(in_full, 1);
     mbar_init(in_free, 9);
     mbar_init(st_full, 1);
-    mbar_init(st_free, 1);
+    mbar_init(st_free, 9);
     mbar_init(b_full, 1);
     mbar_init(w_ready, 8);
     mbar_init(out_full, 1);
@@ -173,13 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
             ok = false;
             break;
           }
-          mbar_expect_tx(in_full, 4 * VB * kBox + (uint32_t)sizeof(DrRows));
+          mbar_expect_tx(in_full, 3 * VB * kBox + (uint32_t)sizeof(DrRows));
           pipe::bulk_load(sm + L::kRows, p.rows + at, sizeof(DrRows), in_full);
           for (int b = 0; b < VB; ++b) {
             tma_load_3d(sm + L::kIn + (3 * b) * kBox, &args.dout, in_full, 64 * b, h, t0);
             tma_load_3d(sm + L::kIn + (3 * b + 1) * kBox, &args.z, in_full, 64 * b, h, t0);
             tma_load_3d(sm + L::kIn + (3 * b + 2) * kBox, &args.e, in_full, 64 * b, h, t0);
-            tma_load_3d(sm + L::kV + b * kBox, &args.v, in_full, 64 * b, h, t0);
           }
         }
       }
@@ -257,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
       for (uint32_t x = c > 2 ? c - 2 : 0; x < c; ++x) mbar_wait_drain(&qk_free[x & 1], parity(x / 2));
     }
   } else if (warp == 10) {
-    // ------------------------------------------------------------ suffix sums of the decays' gradients, two rows a lane
+    // ------------------------------------------------------------ sums of the decays' gradients, two rows a lane
     uint32_t m = 0;
 #pragma unroll 1
     for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
@@ -268,29 +275,37 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
       for (int y = 0; y < p.group; ++y, ++m) {
         const int h = hk * p.group + y;
         const Sums &x = reinterpret_cast<const Sums *>(sm + L::kMisc)[m & 1];
-        float end = lane < 2 * VB ? p.dots[((size_t)slot * p.H + h) * 4 + lane] : 0.f, d[2];
         wait_on(&sums_full[m & 1], parity(m / 2), wait);
+        float d[2], c[2], end = 0.f;  // what passes later tokens, and what is added before
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = 2 * lane + e;
-          d[e] = r < n ? (x.dot[0][r] + x.dot[1][r]) - x.vdv[r] : 0.f;
+          d[e] = c[e] = 0.f;
+          if (r < n) {
+            d[e] = ((x.row[0][0][r] + x.row[0][1][r]) + (x.row[1][0][r] + x.row[1][1][r])) -
+                   ((x.col[0][r] + x.col[1][r]) + (x.col[2][r] + x.col[3][r]));
+            c[e] = x.add[0][r] + x.add[1][r];
+          }
         }
-        pipe::warp_arrive(&sums_free[m & 1]);
 #pragma unroll
-        for (int o = VB; o >= 1; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
-        end = __shfl_sync(0xffffffffu, end, 0);
+        for (int e = 0; e < 8; ++e) end += x.ss[e];
+        end *= x.all;
+        pipe::warp_arrive(&sums_free[m & 1]);
         d[0] += d[1];
-        float after = d[0];
+        float after = d[0], before = c[0] + c[1];
+        const float two = before;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-          const float z = __shfl_down_sync(0xffffffffu, after, o);
+          const float z = __shfl_down_sync(0xffffffffu, after, o), w = __shfl_up_sync(0xffffffffu, before, o);
           if (lane + o < 32) after += z;
+          if (lane >= o) before += w;
         }
         after -= d[0];
+        before -= two;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = 2 * lane + e;
-          if (r < n) static_cast<bf16 *>(g.dg)[(size_t)(t0 + r) * g.dgs + h] = __float2bfloat16_rn(d[e] + after + end);
+          if (r < n) static_cast<bf16 *>(g.dg)[(size_t)(t0 + r) * g.dgs + h] = __float2bfloat16_rn((d[e] + after) + (before + (e ? c[0] : 0.f)) + end);
         }
       }
     }
@@ -321,7 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         if (m >= 2) wait_on(&sums_free[m & 1], parity(m / 2 - 1), wait);
         wait_on(in_full, parity(m), wait);
         if (et < 64) x.kb[et] = rw.rk[et] * rw.beta[et];
+        if (et == 0) x.all = rw.all_hi + rw.all_lo;
         team_sync();
+        // <S, dS>, while the first products are made
+        wait_on(st_full, parity(m), wait);
+        float ss = 0.f;
+#pragma unroll 4
+        for (int e = et; e < KB * VB * 512; e += kTeam)
+          ss = dot8(*reinterpret_cast<const uint4 *>(sm + L::kS + 16 * e), *reinterpret_cast<const uint4 *>(sm + L::kDs + 16 * e), ss);
+        pipe::warp_arrive(st_free);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (lane == 0) x.ss[warp - 2] = ss;
         // weights
         const float rk_i = rw.rk[i], rq_i = rw.rq[i], beta_i = rw.beta[i];
         const float fa = is_k ? -rw.kin[i] * beta_i : rw.qin[i], fc = rw.kout[i] * beta_i;
@@ -339,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         wait_on(b_full, parity(m), wait);
         tc_fence_after();
         const float fw = is_k ? -rk_i * beta_i : rq_i * p.scale;
-        float dot = 0.f;  // q.dq
+        float pairs = 0.f, own = 0.f;  // M's row, and q's own addition
         const int last = i < n ? is_k ? i - 1 : i : -1;  // the row's columns are up to this one
 #pragma unroll
         for (int j0 = 32 * sub; j0 < 32 * sub + 32; j0 += 16) {
@@ -354,74 +380,79 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[e + j] = j0 + e + j <= last ? v[e + j] * (f[j] * fw) : 0.f;
           }
-          if (!is_k) {
-            float qk[16];
-            tmem_ld16(lanes + kTmW + j0, qk);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) dot = j0 + e <= last ? fmaf(v[e], qk[e], dot) : dot;
-          }
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) w8[j] = v[e + j];
             pipe::sts_u4(s0 + L::kW + (is_k ? kBox : 0) + sw128_offset(i, j0 + e), tc::pack8(w8));
           }
+          {
+            float M[16];  // of columns before the row's
+            tmem_ld16(lanes + kTmW + j0, M);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p_ij = j0 + e <= last ? v[e] * M[e] : 0.f;
+              if (j0 + e == i) own = p_ij;
+              M[e] = j0 + e < i ? p_ij : 0.f;
+              pairs += M[e];
+            }
+            // column sums over the warp's rows: halves of the columns go to halves of the lanes
+#pragma unroll
+            for (int k = 16, e = 8; k >= 2; k /= 2, e /= 2)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (j < e) {
+                  const float give = lane & k ? M[j] : M[j + e], mine = lane & k ? M[j + e] : M[j];
+                  M[j] = mine + __shfl_xor_sync(0xffffffffu, give, k);
+                }
+            M[0] += __shfl_xor_sync(0xffffffffu, M[0], 1);
+            if (!(lane & 1)) x.col[quad][j0 + (lane >> 1)] = M[0];
+          }
         }
         tc_fence_before();
         fence_async_smem();
         pipe::warp_arrive(w_ready);
         constexpr int kRounds = 2 * VB;  // 16 bytes of a row a thread and round
-        // dv, dbeta, v.dv: the rounds side by side
-        uint4 zw[kRounds], ew[kRounds], vw[kRounds];
-        float vdv[kRounds], db[kRounds];
+        // dv, dbeta: the rounds side by side
+        uint4 zw[kRounds], ew[kRounds];
+        float db[kRounds];
 #pragma unroll
         for (int o = 0; o < kRounds; ++o) {
           const int e = et + kTeam * o, r = e / (8 * VB), b = e % (8 * VB) >> 3;
           const uint32_t at = sw128_offset(r, 8 * (e & 7));
           zw[o] = *reinterpret_cast<const uint4 *>(sm + L::kIn + (3 * b + 1) * kBox + at);
           ew[o] = *reinterpret_cast<const uint4 *>(sm + L::kIn + (3 * b + 2) * kBox + at);
-          vw[o] = *reinterpret_cast<const uint4 *>(sm + L::kV + b * kBox + at);
         }
 #pragma unroll
         for (int o = 0; o < kRounds; ++o) {
           const int e = et + kTeam * o, r = e / (8 * VB), col = 8 * (e % (8 * VB));
-          vdv[o] = db[o] = 0.f;
+          db[o] = 0.f;
           if (r < n && col < p.dv) {
             db[o] = dot8(zw[o], ew[o], 0.f);
             const float beta = rw.beta[r];
-            float z[8], v[8];
+            float z[8];
             tc::unpack8(zw[o], z);
-            tc::unpack8(vw[o], v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              z[j] *= beta;
-              vdv[o] = fmaf(v[j], z[j], vdv[o]);
-            }
+            for (int j = 0; j < 8; ++j) z[j] *= beta;
             *reinterpret_cast<uint4 *>(static_cast<bf16 *>(g.dv) + (size_t)(t0 + r) * g.dvs + (size_t)h * p.dv + col) = tc::pack8(z);
           }
         }
 #pragma unroll
         for (int z = 4 * VB; z >= 1; z >>= 1) {
 #pragma unroll
-          for (int o = 0; o < kRounds; ++o) {
-            vdv[o] += __shfl_xor_sync(0xffffffffu, vdv[o], z);
-            db[o] += __shfl_xor_sync(0xffffffffu, db[o], z);
-          }
+          for (int o = 0; o < kRounds; ++o) db[o] += __shfl_xor_sync(0xffffffffu, db[o], z);
         }
 #pragma unroll
         for (int o = 0; o < kRounds; ++o) {
           const int e = et + kTeam * o, r = e / (8 * VB);
-          if (e % (8 * VB) == 0) {
-            x.vdv[r] = vdv[o];
-            if (r < n) static_cast<bf16 *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = __float2bfloat16_rn(db[o]);
-          }
+          if (e % (8 * VB) == 0 && r < n) static_cast<bf16 *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = __float2bfloat16_rn(db[o]);
         }
         pipe::warp_arrive(in_free);
         // gradients
         wait_on(out_full, parity(m), wait);
         if (y == 0) wait_on(&qk_full[c & 1], parity(c / 2), wait);
         tc_fence_after();
-        float read = 0.f;
+        float read = 0.f, add = 0.f;  // (dO S^T).q or (Z S^T).k; k and what is added to the state
 #pragma unroll
         for (int j0 = 0; j0 < kCols; j0 += 16) {
           const int col = kCols * sub + j0;
@@ -439,23 +470,32 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             w[e] = fmaf(fa, a[e], w[e]);
-            if (is_k) a[e] = w[e] += t[e];
+            if (is_k) w[e] += t[e];
             acc[j0 + e] += w[e];
           }
-          // (dO S^T).q, or k.dk
           const uint32_t tile = qk0 + (2 * (col >> 6) + is_k) * kBox;
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
             float r8[8];
             tc::unpack8(pipe::lds_sw128(tile, i, ((col & 63) + e) >> 3), r8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) read = fmaf(r8[j], a[e + j], read);
+            for (int j = 0; j < 8; ++j) {
+              read = fmaf(r8[j], a[e + j], read);
+              if (is_k) {
+                add = fmaf(r8[j], t[e + j], add);
+                along = fmaf(r8[j], w[e + j], along);
+              }
+            }
           }
         }
         tc_fence_before();
         pipe::warp_arrive(acc_free);
-        if (!is_k) x.dot[sub][i] = read = fmaf(fa, read, dot);
-        along += read;
+        read = fmaf(fa, read, pairs);
+        x.row[is_k][sub][i] = read;
+        if (is_k)
+          x.add[sub][i] = add;
+        else
+          along += read + own;
         pipe::warp_arrive(&sums_full[m & 1]);
       }
       // the division by the lengths, and out: through the places of q and k, which nobody reads any more
@@ -532,7 +572,6 @@ void launch_dr_grads_tc(const DrProblem &p, const void *dout, long long dos, con
       !encode_tmap_bf16_heads(&args.dout, dout, p.dv, p.H, p.total, dos * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.z, p.Z, p.dv, p.H, p.total, es, kDrC) ||
       !encode_tmap_bf16_heads(&args.e, p.E, p.dv, p.H, p.total, es, kDrC) ||
-      !encode_tmap_bf16_heads(&args.v, p.v, p.dv, p.H, p.total, p.vs * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.dq, g.dq, p.dk, p.Hk, p.total, g.dqs * 2, kDrC) ||
       !encode_tmap_bf16_heads(&args.dk, g.dk, p.dk, p.Hk, p.total, g.dks * 2, kDrC)) {
     note_host_error();

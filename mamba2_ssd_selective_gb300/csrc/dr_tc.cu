@@ -66,7 +66,6 @@ struct Bars {
   uint64_t *w_full;       // W
   uint64_t *q_full, *q_ready;  // outputs' part of the state formed / scaled; reverse: W's part of dO formed / its terms in TMEM
   uint64_t *o_full, *o_free;   // outputs formed / read; reverse: P^T dO
-  uint64_t *s_read;            // reverse: the state's terms have been read for the product with the state
   uint64_t *drain;
   __device__ explicit Bars(uint64_t *b) {
     full = b;
@@ -82,8 +81,7 @@ struct Bars {
     q_ready = patched + 8;
     o_full = patched + 9;
     o_free = patched + 10;
-    s_read = patched + 11;
-    drain = patched + 12;
+    drain = patched + 11;
   }
 };
 
@@ -118,8 +116,7 @@ struct Args {
   float *last;         // and where it ends, or null
   bf16 *out;           // o's rows
   long long os;
-  bf16 *kept;          // the state before each chunk, the gradient of the one behind
-  const bf16 *states;  // reverse: the states
+  bf16 *kept;  // the state before each chunk, the gradient of the one behind
   WaitCtl wait;
   // Sequences cut into segments of so many chunks (0: whole ones): `first` and `last` are then the segments', at their
   // places (dr_segment), but for the last segment's of a sequence, which ends in `fin`
@@ -156,8 +153,6 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
   auto chunk = [&](int i) { return kRev ? nc - 1 - i : i; };
   auto live = [&](int i) { return min(kDrC, len - chunk(i) * kDrC); };
   const int tail = kRev ? 0 : nc - 1;
-  // reverse: the state behind the i-th chunk, the final one behind all chunks' first
-  auto behind = [&](int i) { return i == 0 ? ((size_t)p.slots + seq) * p.H + h : (size_t)(slot0 + chunk(i) + 1) * p.H + h; };
   const bool partial = len % kDrC != 0;  // the tail is
 
   if (warp == 0 && lane == 0) {
@@ -183,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     mbar_init(bar.q_ready, 2 * VB);
     mbar_init(bar.o_full, 1);
     mbar_init(bar.o_free, kRev ? 4 * VB : 2 * VB);
-    mbar_init(bar.s_read, 2 * VB);
     mbar_init(bar.drain, 1);
     fence_mbar_init();
   }
@@ -230,8 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
             for (int b = 0; b < VB; ++b) tma_load_3d(base + L::kV + b * kBox, &args.v, &bar.full[st], 64 * b, h, row);
           pipe::bulk_load(base + L::kRows, p.rows + at, sizeof(DrRows), &bar.full[st]);
           pipe::bulk_load(base + L::kN, tiles, kMats, &bar.full[st]);  // N's terms, P's behind them
-          if (kRev)
-            pipe::bulk_prefetch(args.states + behind(i) * (64 * KB * 64 * VB), 2 * 64 * KB * 64 * VB);
           if (kQBytes)
             for (int b = 0; b < KB; ++b) tma_load_3d(base + L::kQ + b * kBox, &args.q, &bar.full[st], 64 * b, hk, row);
         }
@@ -526,14 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           bulk_commit();
         }
       };
-      const size_t chunks = (size_t)p.slots * p.H;
 #pragma unroll 1
       for (int i = 0; i < nc; ++i) {
         // the state's terms as A operands: lane = column of v, bf16 pairs along dk
-        if (kRev && i > 0) {
-          wait_on(bar.s_read, parity(i - 1), wait);
-          tc_fence_after();
-        }
 #pragma unroll
         for (int x = 0; x < kCols; x += 16) {
           uint32_t hi[8], lo[8];
@@ -564,7 +551,6 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         }
         tc_fence_before();
       }
-      if (MODE == kStates && ends) keep(chunks + (size_t)seq * p.H + h);
       if (kKeeps && sub + quad == 0 && lane == 0) bulk_wait0();
       // the user's final state, or the segment's sum; M's places are behind those of all N
       float *to = args.seg && ends ? args.fin ? args.fin + ((size_t)seq * p.H + h) * dd : nullptr
@@ -655,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
       if (tt == 0) bulk_wait0();
     }
   } else if (kRev) {
-    // ------------------------------------------------------------ the terms of (qin dO)^T, <state, its gradient>
+    // ------------------------------------------------------------ the terms of (qin dO)^T
     const int quad = warp & 3;
     if (quad < 2 * VB) {
       const uint32_t lr = (lane & 7) + 8 * (lane >> 4), lc = 4 * (quad & 1) + ((lane >> 3) & 1);
@@ -693,37 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         tc_fence_before();
         pipe::warp_arrive(bar.q_ready);
         pipe::warp_arrive(&bar.free[i % kStages]);
-        // the state behind the chunk, in bf16, times its gradient's two terms
-        const uint4 *from = reinterpret_cast<const uint4 *>(args.states + behind(i) * (64 * KB * 64 * VB)) + 32 * quad + lane;
-        float dot = 0.f;
-#pragma unroll
-        for (int x = 0; x < KB; ++x) {
-          uint4 s[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] = __ldcg(from + (8 * x + e) * (64 * VB));
-          if (x == 0) {
-            wait_on(bar.s_ready, parity(i), wait);
-            tc_fence_after();
-          }
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            uint32_t hi[16], lo[16];
-            tmem_ld16_async(lanes + kTmS + 32 * x + 4 * e, hi);
-            tmem_ld16_async(lanes + kTmS + 64 + 32 * x + 4 * e, lo);
-            tmem_wait_ld(hi, lo);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const uint32_t w = j % 4 == 0 ? s[e + j / 4].x : j % 4 == 1 ? s[e + j / 4].y : j % 4 == 2 ? s[e + j / 4].z : s[e + j / 4].w;
-              dot = fmaf(lo_f(w), lo_f(hi[j]) + lo_f(lo[j]), dot);
-              dot = fmaf(hi_f(w), hi_f(hi[j]) + hi_f(lo[j]), dot);
-            }
-          }
-        }
-        tc_fence_before();
-        pipe::warp_arrive(bar.s_read);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) p.dots[((size_t)(slot0 + chunk(i)) * p.H + h) * 4 + quad] = dot;
       }
     }
   }
@@ -812,7 +767,7 @@ namespace {
 // state, a thread 8 of them in one row: the warps read M, which is transposed, row by row, and the columns are in
 // shared memory.
 constexpr int kScanCols = 16;
-__global__ void __launch_bounds__(256) dr_scan_kernel(DrProblem p) {
+__global__ void __launch_bounds__(256) dr_scan_kernel(DrProblem p, float *fin) {
   extern __shared__ __align__(128) uint8_t smem[];  // two M
   __shared__ __align__(16) float S[128][kScanCols];
   __shared__ uint64_t full[2];
@@ -821,7 +776,7 @@ __global__ void __launch_bounds__(256) dr_scan_kernel(DrProblem p) {
   const size_t dd = (size_t)dk * dv, all = (size_t)p.seg_places * p.H;
   int a, len, slot0;
   dr_seq(p, seq, a, len, slot0);
-  const int n = p.seg * kDrC, place0 = dr_place0(p, p.seg, a, seq), segments = len ? (len + n - 1) / n : 1;
+  const int n = p.seg * kDrC, place0 = dr_place0(p, p.seg, a, seq), segments = (len + n - 1) / n;
   const bool live = row < dk && c < dv;  // dv is a multiple of 8
   float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   auto get = [&](const float *from) {
@@ -841,6 +796,7 @@ __global__ void __launch_bounds__(256) dr_scan_kernel(DrProblem p) {
   }
   __syncthreads();
   if (live && p.init) get(p.init + ((size_t)seq * p.H + h) * dd + (size_t)row * dv + c);
+  if (len == 0 && fin && live) put(fin + ((size_t)seq * p.H + h) * dd + (size_t)row * dv + c);
   for (int g = 0; g < segments; ++g) {
     const size_t item = (size_t)(place0 + g) * p.H + h;
     if (live) put(p.seg_states + item * dd + (size_t)row * dv + c);
@@ -866,10 +822,10 @@ __global__ void __launch_bounds__(256) dr_scan_kernel(DrProblem p) {
 
 }  // namespace
 
-void launch_dr_tc_scan(const DrProblem &p, cudaStream_t s) {
+void launch_dr_tc_scan(const DrProblem &p, float *fin, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
   allow_smem(reinterpret_cast<const void *>(dr_scan_kernel), 2 * 128 * 128 * 4, allowed);
-  dr_scan_kernel<<<dim3((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kScanCols - 1) / kScanCols)), 256, 2 * p.dk * p.dk * 4, s>>>(p);
+  dr_scan_kernel<<<dim3((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kScanCols - 1) / kScanCols)), 256, 2 * p.dk * p.dk * 4, s>>>(p, fin);
 }
 
 void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s) {
@@ -878,7 +834,6 @@ void launch_dr_tc_reverse(const DrProblem &p, const void *dout, long long dos, c
   args.first = dfin;
   args.last = dinit;
   args.kept = reinterpret_cast<bf16 *>(p.dS);
-  args.states = reinterpret_cast<const bf16 *>(p.S);
   run_boxes<kReverse>(args, s);
 }
 

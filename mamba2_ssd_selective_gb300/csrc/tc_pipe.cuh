@@ -28,10 +28,6 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                : "memory");
 }
 
-// hint that the bytes (a multiple of 16, 16-byte aligned) will be read: into L2
-__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
 // and back, tracked by the issuing thread's bulk async-group
 __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");

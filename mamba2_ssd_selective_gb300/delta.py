@@ -276,15 +276,16 @@ class BlockNormRunner:
         return (None, 0) if x is None else _rows(x, name, self.rows, self.channels, dtype, self.device)
 
     def _inputs(self, x, z, residual, residual_there, post_weight, branch_scale, pre_weight, eps) -> SsdBlockNormInputs:
-        xp, xs = _rows(x, "x", self.rows, self.channels, self.tdtype, self.device)
+        device = self.device
+        xp, xs = _rows(x, "x", self.rows, self.channels, self.tdtype, device)
         zp, zs = self._with(z, "z", self.gate, self.tdtype)
         rp, rs = self._with(residual, "residual", residual_there, self.rdtype)
         if (post_weight is not None and not self.post_norm) or (pre_weight is not None and not self.pre_norm):
             raise ValueError("post_weight goes with post_norm, pre_weight with pre_norm")
         shape, f32 = (self.channels,), torch.float32
-        return SsdBlockNormInputs(xp, xs, zp, zs, rp, rs, _exact(post_weight, "post_weight", shape, f32, self.device),
-                                  _exact(branch_scale, "branch_scale", shape, f32, self.device),
-                                  _exact(pre_weight, "pre_weight", shape, f32, self.device), eps)
+        return SsdBlockNormInputs(xp, xs, zp, zs, rp, rs, _exact(post_weight, "post_weight", shape, f32, device),
+                                  _exact(branch_scale, "branch_scale", shape, f32, device),
+                                  _exact(pre_weight, "pre_weight", shape, f32, device), eps)
 
     def forward(self, x, *, residual=None, z=None, post_weight=None, branch_scale=None, pre_weight=None,
                 eps: float = 1e-6, h_out=None, stream=None) -> dict:
@@ -296,13 +297,18 @@ class BlockNormRunner:
                 return self.forward(x, residual=residual, z=z, post_weight=post_weight, branch_scale=branch_scale,
                                     pre_weight=pre_weight, eps=eps, h_out=h_out)
         inputs = self._inputs(x, z, residual, self.residual, post_weight, branch_scale, pre_weight, eps)
-        h = torch.empty(x.shape, dtype=self.rdtype, device=self.device) if h_out is None else h_out
-        hp, hs = _rows(h, "h_out", self.rows, self.channels, self.rdtype, self.device)
-        y = torch.empty(x.shape, dtype=self.tdtype, device=self.device) if self.pre_norm else None
-        stats = torch.empty(2, self.rows, dtype=torch.float32, device=self.device)
-        post, pre = stats[0] if self.post_norm else None, stats[1] if self.pre_norm else None
+        empty, device = torch.empty, self.device
+        if h_out is None:
+            h = empty(x.shape, dtype=self.rdtype, device=device)
+            hp, hs = h.data_ptr(), self.channels
+        else:
+            h = h_out
+            hp, hs = _rows(h, "h_out", self.rows, self.channels, self.rdtype, device)
+        y = empty(x.shape, dtype=self.tdtype, device=device) if self.pre_norm else None
+        post = empty(self.rows, dtype=torch.float32, device=device) if self.post_norm else None
+        pre = empty(self.rows, dtype=torch.float32, device=device) if self.pre_norm else None
         ssd_block_norm_forward(self.dims, inputs, hp, hs, y, self.channels, post, pre,
-                               torch._C._cuda_getCurrentRawStream(self.device.index))
+                               torch._C._cuda_getCurrentRawStream(device.index))
         return {"h": h, "y": y, "rstd_post": post, "rstd_pre": pre}
 
     def backward(self, x, h=None, *, dh=None, dy=None, z=None, post_weight=None, branch_scale=None, pre_weight=None,

@@ -149,6 +149,33 @@ def test_places_of_packed_chunks(seed):
         a += x
 
 
+@pytest.mark.parametrize("seed", range(20))
+def test_places_of_packed_segments(seed):
+    """The same for segments of n rows: start / n + s."""
+    g = torch.Generator().manual_seed(seed)
+    nseq, n = int(torch.randint(1, 20, (1,), generator=g)), 64 * int(torch.randint(1, 5, (1,), generator=g))
+    lens = torch.randint(0, 900, (nseq,), generator=g).tolist()
+    seen, a = set(), 0
+    for s, x in enumerate(lens):
+        for k in range(-(-x // n)):
+            place = a // n + s + k
+            assert place not in seen and place < sum(lens) // n + nseq
+            seen.add(place)
+        a += x
+
+
+def test_few_long_sequences_are_cut():
+    """States of segments are in the workspace exactly where cutting pays."""
+    def extra(**kw):
+        d = dr_dims(**kw)
+        chunks = d.nseq * -(-d.seqlen // 64) * d.nheads
+        return ssd.ssd_delta_rule_workspace_size(d, False) / chunks
+
+    whole = extra(nseq=40, seqlen=8192, nheads=4)
+    assert extra(nseq=1, seqlen=8192, nheads=4) > 1.05 * whole
+    assert abs(extra(nseq=1, seqlen=300, nheads=4) - whole) < 0.05 * whole
+
+
 # ---------------------------------------------------------------- block norm
 
 def bn_dims(**kw):
