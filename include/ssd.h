@@ -368,8 +368,9 @@ ssd_status ssd_group_norm_backward(const ssd_group_norm_dims *dims, const ssd_gr
  *     o_t = scale q_t S_t
  * With dims.qk_norm, q and k are divided by sqrt(|.|^2 + norm_eps) first (gradients go through the division); without
  * it the keys should be short (b |k|^2 at most 2), or states grow from token to token.
- * Sequences, cu_seqlens, empty sequences and rows outside every sequence are as in ssd_linear_attn_dims (with bounds out of
- * order what any sequence but an empty one gets is undefined, and stays inside the tensors), and so are the layouts: token-major tensors with their own token strides, heads and channels contiguous within a token,
+ * Sequences, cu_seqlens, empty sequences and rows outside every sequence are as in ssd_linear_attn_dims (with bounds out
+ * of order what any sequence but an empty one gets is undefined, and stays inside the tensors), and so are the layouts:
+ * token-major tensors with their own token strides, heads and channels contiguous within a token,
  *   q, k (T, nheads_qk * headdim_k), v, o (T, nheads * headdim_v), log_decay, beta (T, nheads)
  * all in dims.dtype; q, k, v, o 16-byte aligned with strides a multiple of 8 (bf16) or 4 (fp32) elements, log_decay and
  * beta element aligned with any stride of at least nheads.  log_decay is at most 0 (below -256 it counts as -256, which
