@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
   for (int g = 0; g < p.group; ++g) {
     const int h = hk * p.group + g;
     const size_t at = (size_t)slot * p.H + h;
+    if (g > 0 && tid == kThreads - 1) bulk_wait_read0();  // the last head's factors and P have left
     if (g % kHeads == 0) {  // the factors of the next heads
       if (g > 0 && warp < kHeads && g + warp < p.group)
         sums = dr_sums(dr_load_gates<bf16>(p, h + warp, t0, n, lane), lane);
@@ -195,23 +196,32 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
         if (lane == 0) w.first_nan[warp] = sums.first_nan;
       }
     }
-    if (g > 0 && (tid == 0 || tid == kThreads - 1)) bulk_wait_read0();  // the last head's tiles have left
     __syncthreads();
     const DrRows &rows = w.rows[g % kHeads];
     const int nan_at = w.first_nan[g % kHeads];
+    float hi[2], lo[2], rk[2], rq[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int first = e ? i1 : i0, i = first + r0;
-      const float hi = rows.ghi[i], lo = rows.glo[i], rk = rows.rk[i], rq = rows.rq[i] * p.scale;
-      const uint32_t row = s0 + kTilesP + i * 128 + 2 * c0;
+      const int i = (e ? i1 : i0) + r0;
+      hi[e] = rows.ghi[i], lo[e] = rows.glo[i], rk[e] = rows.rk[i], rq[e] = rows.rq[i] * p.scale;
+    }
 #pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const int j = 8 * y + c0;
+    for (int y = 0; y < 8; ++y) {
+      const int j = 8 * y + c0;
+      float2 gh = make_float2(0.f, 0.f), gl = gh, rj = gh;
+      if (8 * y <= i1) {
+        gh = *reinterpret_cast<const float2 *>(rows.ghi + j), gl = *reinterpret_cast<const float2 *>(rows.glo + j);
+        rj = *reinterpret_cast<const float2 *>(rows.rk + j);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int first = e ? i1 : i0, i = first + r0;
+        const bool below = 8 * y <= first, diagonal = 8 * (y & ~1) == (first & ~15);  // a block of the diagonal's 16 x 16
+        if (!below && g > 0) continue;  // zeros above the diagonal stay
+        const uint32_t at_j = i * 128 + 2 * c0 + ((y ^ (lane >> 2)) << 4);  // the 128-byte swizzle: the row is lane / 4 modulo 8
         float a[2] = {0.f, 0.f}, q[2] = {0.f, 0.f};
-        if (8 * y <= first && i < n) {
-          const float2 gh = *reinterpret_cast<const float2 *>(rows.ghi + j), gl = *reinterpret_cast<const float2 *>(rows.glo + j),
-                       rj = *reinterpret_cast<const float2 *>(rows.rk + j);
-          float l[2] = {__expf((hi - gh.x) + (lo - gl.x)) * rj.x, __expf((hi - gh.y) + (lo - gl.y)) * rj.y};
+        if (below && i < n) {
+          float l[2] = {__expf((hi[e] - gh.x) + (lo[e] - gl.x)) * rj.x, __expf((hi[e] - gh.y) + (lo[e] - gl.y)) * rj.y};
           if (nan_at < kDrC && i >= nan_at) {
 #pragma unroll
             for (int x = 0; x < 2; ++x)
@@ -219,47 +229,37 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            a[x] = kk[y][2 * e + x] * (l[x] * rk);
-            q[x] = qk[y][2 * e + x] * (l[x] * rq);
+            a[x] = kk[y][2 * e + x] * (l[x] * rk[e]);
+            q[x] = qk[y][2 * e + x] * (l[x] * rq[e]);
           }
           if (8 * y == first) {  // the diagonal's block
             a[0] = j < i ? a[0] : 0.f, a[1] = j + 1 < i ? a[1] : 0.f;
             q[0] = j <= i ? q[0] : 0.f, q[1] = j + 1 <= i ? q[1] : 0.f;
           }
         }
-        if (8 * y <= first) {
-          if (8 * (y & ~1) == (first & ~15)) {  // a block of the diagonal
-            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(diag_at(s0 + kTilesA, first >> 4, i & 15, j & 15)), "f"(a[0]), "f"(a[1]) : "memory");
-          } else {
-            uint32_t ah, al;
-            tc::split2(a[0], a[1], ah, al);
-            const uint32_t to = s0 + kTilesA + i * 128 + 2 * c0 + ((y ^ (lane >> 2)) << 4);
-            sts(to, ah);
-            sts(to + kBox, al);
-          }
-        } else {
-          if (8 * (y & ~1) == (first & ~15))  // its upper right quarter
-            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(diag_at(s0 + kTilesA, first >> 4, i & 15, j & 15)), "f"(0.f), "f"(0.f) : "memory");
-          if (g == 0) {  // above the diagonal N has zeros, which stay
-            const uint32_t to = s0 + kTilesN + i * 128 + 2 * c0 + ((y ^ (lane >> 2)) << 4);
-            sts(to, 0);
-            sts(to + kBox, 0);
-          }
+        if (diagonal) {
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(diag_at(s0 + kTilesA, first >> 4, i & 15, j & 15)), "f"(a[0]), "f"(a[1]) : "memory");
+        } else if (below) {
+          uint32_t ah, al;
+          tc::split2(a[0], a[1], ah, al);
+          sts(s0 + kTilesA + at_j, ah);
+          sts(s0 + kTilesA + at_j + kBox, al);
+        }
+        if (!below) {
+          sts(s0 + kTilesN + at_j, 0);
+          sts(s0 + kTilesN + at_j + kBox, 0);
         }
         uint32_t qh, ql;
         tc::split2(q[0], q[1], qh, ql);
-        sts(row + ((y ^ (lane >> 2)) << 4), qh);  // the 128-byte swizzle: the row is lane / 4 modulo 8
-        if (PT == 2) sts(row + kBox + ((y ^ (lane >> 2)) << 4), ql);
+        sts(s0 + kTilesP + at_j, qh);
+        if (PT == 2) sts(s0 + kTilesP + at_j + kBox, ql);
       }
     }
-    {
-      const float4 *from = reinterpret_cast<const float4 *>(&rows);
-      float4 *to = reinterpret_cast<float4 *>(p.rows + at);
-      for (int e = tid; e < (int)(sizeof(DrRows) / 16); e += kThreads) to[e] = from[e];
-    }
     fence_async_smem();
+    if (g > 0 && tid == 0) bulk_wait_read0();  // the last head's N has left
     __syncthreads();
     if (tid == kThreads - 1) {
+      pipe::bulk_store(p.rows + at, smem_u32(&rows), sizeof(DrRows));
       pipe::bulk_store(reinterpret_cast<uint8_t *>(p.N) + at * (4 * kDrTile) + 2 * kDrTile, s0 + kTilesP, PT * kBox);
       bulk_commit();
     }
