@@ -341,7 +341,7 @@ ssd_status ssd_delta_rule_step(const ssd_delta_rule_dims *dims, const ssd_delta_
 
 size_t ssd_block_norm_workspace_size(const ssd_block_norm_dims *dims) {
   if (bn_check_dims(dims) != SSD_OK) return 0;
-  return align_up((size_t)bn_blocks(dims->rows, dims->channels) * 3 * dims->channels * 4, 256);
+  return align_up((size_t)bn_blocks(dims->rows, dims->channels, 8) * 3 * dims->channels * 4, 256);
 }
 
 ssd_status ssd_block_norm_forward(const ssd_block_norm_dims *dims, const ssd_block_norm_inputs *in, void *h,
@@ -423,7 +423,7 @@ ssd_status ssd_block_norm_backward(const ssd_block_norm_dims *dims, const ssd_bl
     SSD_LAUNCH("bn_backward", (launch_bn_backward<__nv_bfloat16, float>(p, vec, s)));
   else
     SSD_LAUNCH("bn_backward", (launch_bn_backward<__nv_bfloat16, __nv_bfloat16>(p, vec, s)));
-  if (p.dpw || p.dsc || p.dw) SSD_LAUNCH("bn_sums", launch_bn_sums(p, s));
+  if (p.dpw || p.dsc || p.dw) SSD_LAUNCH("bn_sums", launch_bn_sums(p, vec, s));
   return launch_status();
 }
 

@@ -2,9 +2,9 @@
 // bn_*.cu.
 //
 // Bytes bound them: every tensor is read and written once, a row's values wait in its threads' registers from
-// the first sum to the last store.  A row is a warp's (up to 512 channels) or a block's.  Blocks whose rows can be
+// the first sum to the last store.  A row is a warp's (up to 256 channels) or a block's.  Blocks whose rows can be
 // moved as whole 16-byte units go through many rows, with the next ones on their way into shared memory by bulk copies.
-// All parts, bf16: 16384 x 4096 forward 128 us (5.2 TB/s), gradients of 8192 x 4096 with an fp32 stream 171 us (4.3 TB/s)
+// All parts, bf16: 16384 x 4096 forward 128 us (5.2 TB/s), gradients of 8192 x 4096 with an fp32 stream 174 us (4.2 TB/s)
 // and 8 us for the parameters' sums.  What is left: backward has a block of 256 threads to an SM (255 registers), whose
 // sums over the row have nothing beside them.
 #pragma once
@@ -239,8 +239,14 @@ __global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : 512, 1) bn_
 
 // The parameters' sums stay in registers and go out once: a set of partial sums for each block (teams of a warp: the
 // block's warps add up in shared memory).
+// As many blocks to an SM as bn_blocks() counts on: with the registers that the compiler takes otherwise (133 to 220) some
+// of them waited, 8192 x 1000 64 us for 48, 16384 x 256 45 for 30.  Not where channels move one by one, whose addresses take
+// up to 243: with 128 they spill, and 8192 x 1003 took 165 us for 98.
+constexpr int bn_resident(int mode, int threads, int per, int vec) {
+  return per > 1 || vec == 1 ? 1 : mode == kWarp || threads == 256 ? 2 : threads == 128 ? 4 : 1;
+}
 template <typename T, typename R, int PER, int VEC, int MODE, int THREADS>
-__global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : THREADS, 1) bn_backward_kernel(const BnProblem p, int stages) {
+__global__ void __launch_bounds__(MODE == kWarp ? 32 * kBnWarpRows : THREADS, bn_resident(MODE, THREADS, PER, VEC)) bn_backward_kernel(const BnProblem p, int stages) {
   constexpr int N = 8 * PER;
   constexpr bool WARP = MODE == kWarp;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -387,12 +393,14 @@ template <typename T, typename R, int PER, int VEC> void run_forward(const BnPro
   static std::atomic<uint64_t> allowed{0};
   int stage = 0;
   const int sms = device_sm_count();
-  if (team.threads == 32) {
-    bn_forward_kernel<T, R, PER, VEC, kWarp><<<(p.rows + kBnWarpRows - 1) / kBnWarpRows, 32 * kBnWarpRows, 0, s>>>(p, 1);
-    return;
+  if constexpr (PER == 1) {
+    if (team.threads == 32) {
+      bn_forward_kernel<T, R, 1, VEC, kWarp><<<(p.rows + kBnWarpRows - 1) / kBnWarpRows, 32 * kBnWarpRows, 0, s>>>(p, 1);
+      return;
+    }
   }
   // two blocks of 256 threads to an SM, more of smaller ones; rows enough for some to be on their way
-  const int per_sm = team.threads > 256 ? 1 : team.threads > 128 ? 2 : 4, grid = sms * per_sm;
+  const int per_sm = team.threads > 256 ? 1 : team.threads > 128 ? 2 : team.threads > 64 ? 4 : 8, grid = sms * per_sm;
   const int stages = VEC == 8 ? bn_stages<T, R>(p, false, per_sm, stage) : 0;
   if (VEC == 8 && stages >= 2 && p.rows >= 2 * grid) {
     allow_smem(reinterpret_cast<const void *>(bn_forward_kernel<T, R, PER, 8, kRing>), 220 * 1024, allowed);
@@ -403,9 +411,9 @@ template <typename T, typename R, int PER, int VEC> void run_forward(const BnPro
 }
 template <typename T, typename R, int PER, int VEC, int THREADS> void run_backward_blocks(const BnProblem &p, const BnTeam &team, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  const int sets = bn_blocks(p.rows, p.C);
+  const int sets = bn_blocks(p.rows, p.C, VEC);
   int stage = 0;
-  const int stages = VEC == 8 ? bn_stages<T, R>(p, true, bn_blocks_per_sm(team), stage) : 0;
+  const int stages = VEC == 8 ? bn_stages<T, R>(p, true, bn_blocks_per_sm(team, VEC), stage) : 0;
   if (VEC == 8 && stages >= 2 && p.rows >= 2 * sets) {
     allow_smem(reinterpret_cast<const void *>(bn_backward_kernel<T, R, PER, 8, kRing, THREADS>), 220 * 1024, allowed);
     bn_backward_kernel<T, R, PER, 8, kRing, THREADS><<<sets, team.threads, 64 + stages * stage, s>>>(p, stages);
@@ -414,12 +422,18 @@ template <typename T, typename R, int PER, int VEC, int THREADS> void run_backwa
   }
 }
 template <typename T, typename R, int PER, int VEC> void run_backward(const BnProblem &p, const BnTeam &team, cudaStream_t s) {
-  if (team.threads == 32)
-    bn_backward_kernel<T, R, PER, VEC, kWarp, 256><<<bn_blocks(p.rows, p.C), 32 * kBnWarpRows, p.C * 4, s>>>(p, 1);
-  else if (team.threads <= 256)
-    run_backward_blocks<T, R, PER, VEC, 256>(p, team, s);
-  else
+  if constexpr (PER == 1) {  // at most 2048 channels
+    if (team.threads == 32)
+      bn_backward_kernel<T, R, 1, VEC, kWarp, 256><<<bn_blocks(p.rows, p.C, VEC), 32 * kBnWarpRows, p.C * 4, s>>>(p, 1);
+    else if (VEC > 1 && team.threads <= 128)
+      run_backward_blocks<T, R, 1, VEC == 1 ? 2 : VEC, 128>(p, team, s);
+    else
+      run_backward_blocks<T, R, 1, VEC, 256>(p, team, s);
+  } else if (PER == 2 && team.threads <= 256) {
+    run_backward_blocks<T, R, 2, VEC, 256>(p, team, s);
+  } else {
     run_backward_blocks<T, R, PER, VEC, 512>(p, team, s);
+  }
 }
 
 template <typename T, typename R, int PER, class Run> void by_vec(int vec, const Run &run) {

@@ -36,12 +36,12 @@ struct BnTeam {
   int threads, per;  // per: units of 8 values a thread
 };
 BnTeam bn_team(int channels);
-int bn_blocks_per_sm(const BnTeam &team);     // of the backward pass
-int bn_blocks(int rows, int channels);        // likewise, all of them: one set of partial sums each
+int bn_blocks_per_sm(const BnTeam &team, int vec);  // of the backward pass
+int bn_blocks(int rows, int channels, int vec);     // likewise, all of them: one set of partial sums each (most with vec 8)
 
 // T: x, z, y; R: the residual stream; vec: channels that the tensors' addresses and strides allow at once (8, 2, 1)
 template <typename T, typename R> void launch_bn_forward(const BnProblem &p, int vec, cudaStream_t s);
 template <typename T, typename R> void launch_bn_backward(const BnProblem &p, int vec, cudaStream_t s);
-void launch_bn_sums(const BnProblem &p, cudaStream_t s);
+void launch_bn_sums(const BnProblem &p, int vec, cudaStream_t s);
 
 }  // namespace ssd

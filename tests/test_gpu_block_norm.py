@@ -121,6 +121,12 @@ def test_sizes(rows, C, dtype, res):
     Case(rows, C, dtype=dtype, res=res, seed=rows + C).check()
 
 
+@pytest.mark.parametrize("dtype,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,C", [(2450, 512), (2433, 264), (1300, 1000), (620, 1502), (350, 1003), (305, 2047), (2500, 248)])
+def test_blocks_that_go_through_many_rows(rows, C, dtype, res):
+    Case(rows, C, dtype=dtype, res=res, seed=rows + C).check()
+
+
 @pytest.mark.parametrize("pad", [1, 2, 6, 8])
 def test_strided_rows(pad):
     for dtype in ("bf16", "f32"):
