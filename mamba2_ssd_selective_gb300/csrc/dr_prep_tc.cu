@@ -9,7 +9,7 @@
 //     N_IJ = M - N_II (b_I M),    M = A_IJ - sum_(J <= K < I) A_IK (b_K N_KJ),
 // transposed, so that what a step makes is the next one's first operand as it stands in the registers.  Both operands are
 // sums of two bf16 terms, which is how N goes out too.
-// 4 x 8192 tokens, 16 heads of q and k for 32 states take 197 us (with products of 16 and 32 rows in fp32 on the CUDA cores
+// 4 x 8192 tokens, 16 heads of q and k for 32 states take 195 us (with products of 16 and 32 rows in fp32 on the CUDA cores
 // 239 us), their bytes 104 us at 6.8 TB/s.  What bounds it is latency: a block's steps follow one another, and registers and
 // shared memory let four blocks onto an SM (a third of the instructions that it could issue).
 #include "delta.h"
