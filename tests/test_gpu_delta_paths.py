@@ -248,6 +248,61 @@ def test_captured(which):
         assert torch.equal(x, y)
 
 
+def test_captured_calls_that_share_a_workspace():
+    """A prompt and its gradient captured from one runner, replayed in turn, with other inputs at the same places."""
+    a, b = (Case([300, 0, 77], 4, 2, 64, 128, packed=True, seed=s) for s in (51, 52))
+    r = a.runner()
+    held, do, init = [x.clone() for x in a.inputs()], a.do.cuda(), a.init.cuda()
+    kw = dict(scale=a.scale, initial_state=init, cu_seqlens=a.cu.cuda())
+    calls = (lambda: list(r.forward(*held, **kw)), lambda: list(r.backward(*held, do, **kw).values()))
+    graphs = []
+    for call in calls:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call()
+        graphs.append((graph, got))
+    for c in (a, b, a):
+        for x, y in zip((*held, do, init), (*c.inputs(), c.do.cuda(), c.init.cuda())):
+            x.copy_(y)
+        for graph, got in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for (graph, got), call in zip(graphs, calls):
+            for x, y in zip(got, call()):
+                assert torch.equal(x, y)
+
+
+def test_two_runners_at_once():
+    """Each its own workspace: prompts, gradients and norms on two streams side by side give what they give alone."""
+    cases = [Case([900, 40], 4, 2, 128, 64, packed=True, seed=s) for s in (61, 62)]
+    runners = [c.runner() for c in cases]
+    norms = [ssd.BlockNormRunner(700, 512, post_norm=True) for _ in cases]
+    x = [torch.randn(700, 512, device="cuda").bfloat16() for _ in cases]
+    args = [(c.inputs(), c.do.cuda(), dict(scale=c.scale, initial_state=c.init.cuda(), cu_seqlens=c.cu.cuda())) for c in cases]
+
+    def call(i, stream=None):
+        inputs, do, kw = args[i]
+        n = norms[i].forward(x[i], residual=x[i], stream=stream)
+        g = norms[i].backward(x[i], n["h"], dy=x[i], rstd_post=n["rstd_post"], rstd_pre=n["rstd_pre"], stream=stream)
+        return [*runners[i].forward(*inputs, stream=stream, **kw), *runners[i].backward(*inputs, do, stream=stream, **kw).values(),
+                n["h"], n["y"], g["dx"], g["dresidual"]]
+
+    want = [call(0), call(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[call(i, s) for i, s in enumerate(streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for both in got:
+        for xs, ys in zip(both, want):
+            for g, w in zip(xs, ys):
+                assert torch.equal(g, w)
+
+
 def test_a_prompt_of_one_token():
     """A runner of single tokens takes one as a prompt too, and its gradient."""
     c = Case([1, 1, 1], 2, 2, 64, 64, packed=False, seed=42)
