@@ -42,7 +42,7 @@ static_assert(sizeof(DrRows) % 16 == 0, "moved in units of 16 bytes");
 
 struct DrProblem {
   int nseq, seqlen, total, H, Hk, group, dk, dv;
-  int slots;      // places for chunks: those of sequence s start at dr_slot0
+  int slots;      // places for chunks (dr_seq says where a sequence's start)
   const int *cu;  // or null: sequences of seqlen tokens
   const void *q, *k, *v, *g, *b;
   long long qs, ks, vs, gs, bs;  // token strides (elements)
