@@ -27,7 +27,7 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
 __device__ __forceinline__ void mm_nt(float (&acc)[4][2], const float *A, int lda, const float *B, int K, int tm, int tn) {
   A += 4 * tm * lda;
   B += 2 * tn;
-#pragma unroll 2
+#pragma unroll 4
   for (int k = 0; k < K; k += 4) {
     float4 a[4];
     float2 b[4];
@@ -46,7 +46,7 @@ __device__ __forceinline__ void mm_nt(float (&acc)[4][2], const float *A, int ld
 __device__ __forceinline__ void mm_tn(float (&acc)[4][2], const float *A, int lda, const float *B, int tm, int tn, int j0 = 0) {
   A += 4 * tm;
   B += 2 * tn;
-#pragma unroll 8
+#pragma unroll 16
   for (int j = j0; j < kDrC; ++j) {
     const float4 a = *reinterpret_cast<const float4 *>(A + j * lda);
     const float2 b = *reinterpret_cast<const float2 *>(B + j * kCols);
@@ -103,6 +103,67 @@ __device__ __forceinline__ void load_factors(DrRows *dst, const DrRows *src) {
   for (int e = threadIdx.x; e < (int)(sizeof(DrRows) / 16); e += kThreads)
     reinterpret_cast<float4 *>(dst)[e] = __ldg(reinterpret_cast<const float4 *>(src) + e);
 }
+// The same in two steps, with the values in registers in between: a chunk's are on their way while the chunk before it
+// is worked on (chains of rows of at most 64 channels: beyond, registers do not hold them).  7 sequences, 5003 tokens, 12 heads
+// of 64: chains 218 and 413 us; 266 and 474 without, where of a chunk's 15000 cycles 5500 waited for its tensors.
+struct RowsAhead {
+  float4 x[4];
+  template <typename T> __device__ __forceinline__ void load(const void *src, long long stride, size_t t0, int n, int h, int dk) {
+    const int r = threadIdx.x >> 2;
+    const T *from = static_cast<const T *>(src) + (t0 + r) * stride + (size_t)h * dk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = 4 * (threadIdx.x & 3) + 16 * i;
+      x[i] = r < n && c < dk ? load4(from + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void put(float *dst, int ld, int dk) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = 4 * (threadIdx.x & 3) + 16 * i;
+      if (c < dk) *reinterpret_cast<float4 *>(dst + (threadIdx.x >> 2) * ld + c) = x[i];
+    }
+  }
+};
+struct MatAhead {
+  float4 x[4];
+  __device__ __forceinline__ void load(const float *src) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __ldg(reinterpret_cast<const float4 *>(src) + threadIdx.x + i * kThreads);
+  }
+  __device__ __forceinline__ void put(float *dst) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      *reinterpret_cast<float4 *>(dst + (e >> 4) * kMatLd + 4 * (e & 15)) = x[i];
+    }
+  }
+};
+static_assert(4 * kThreads == kDrC * kDrC / 4 && kThreads == 4 * kDrC && sizeof(DrRows) / 16 <= kThreads, "what a thread takes of a chunk");
+struct FactorsAhead {
+  float4 x;
+  __device__ __forceinline__ void load(const DrRows *src) {
+    if (threadIdx.x < sizeof(DrRows) / 16) x = __ldg(reinterpret_cast<const float4 *>(src) + threadIdx.x);
+  }
+  __device__ __forceinline__ void put(DrRows *dst) const {
+    if (threadIdx.x < sizeof(DrRows) / 16) reinterpret_cast<float4 *>(dst)[threadIdx.x] = x;
+  }
+};
+// a thread's four rows and two columns of v or do
+struct TileAhead {
+  float x[4][2];
+  template <typename T>
+  __device__ __forceinline__ void load(const void *src, long long stride, size_t t0, int n, size_t at, bool live, int tm) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * tm + i;
+      const T *from = static_cast<const T *>(src) + (t0 + r) * stride + at;
+      x[i][0] = live && r < n ? load1(from) : 0.f;
+      x[i][1] = live && r < n ? load1(from + 1) : 0.f;  // dv is even
+    }
+  }
+};
+
 // the block's columns of a state
 __device__ __forceinline__ void load_state(float *S, const float *src, int dk, int dv, int c0) {
   for (int e = threadIdx.x; e < dk * kCols; e += kThreads) {
@@ -127,7 +188,7 @@ __device__ __forceinline__ void carry(float *S, const float (&acc)[4][2], const 
 }
 
 // OUT: outputs and the final state; else the states before the chunks and E, for the backward pass
-template <typename T, bool OUT>
+template <typename T, bool OUT, bool AHEAD>
 __global__ void __launch_bounds__(kThreads) dr_chain_kernel(DrProblem p, T *__restrict__ o, long long os, float *fin) {
   extern __shared__ __align__(16) uint8_t raw[];
   const ChainShared sm(raw, p.dk);
@@ -139,29 +200,51 @@ __global__ void __launch_bounds__(kThreads) dr_chain_kernel(DrProblem p, T *__re
   load_state(sm.S, p.init ? p.init + ((size_t)seq * p.H + h) * dd : nullptr, p.dk, p.dv, c0);
   const DrRows &rows = *sm.rows;
   const int upto = 8 * (tid >> 5) + 8;  // N and P are zero right of the diagonal: the columns of the warp's 8 rows
+  RowsAhead ka, qa;
+  MatAhead na, pa;
+  FactorsAhead fa;
+  TileAhead va;
+  auto ahead = [&](int c) {
+    const size_t t0 = (size_t)a + c * kDrC, at = (size_t)(slot0 + c) * p.H + h;
+    const int n = min(kDrC, len - c * kDrC);
+    ka.load<T>(p.k, p.ks, t0, n, h / p.group, p.dk);
+    na.load(p.N + at * (kDrC * kDrC));
+    fa.load(p.rows + at);
+    va.load<T>(p.v, p.vs, t0, n, (size_t)h * p.dv + col, col < p.dv, tm);
+    if (OUT) {
+      qa.load<T>(p.q, p.qs, t0, n, h / p.group, p.dk);
+      pa.load(p.P + at * (kDrC * kDrC));
+    }
+  };
+  if (AHEAD && len > 0) ahead(0);
   for (int c = 0; c * kDrC < len; ++c) {
     const size_t t0 = (size_t)a + c * kDrC, at = (size_t)(slot0 + c) * p.H + h;
     const int n = min(kDrC, len - c * kDrC);
     __syncthreads();
-    load_rows<T>(sm.K, sm.ld, p.k, p.ks, t0, n, h / p.group, p.dk);
-    load_mat(sm.N, p.N + at * (kDrC * kDrC));
-    load_factors(sm.rows, p.rows + at);
-    if (OUT) {
-      load_rows<T>(sm.Q, sm.ld, p.q, p.qs, t0, n, h / p.group, p.dk);
-      load_mat(sm.P, p.P + at * (kDrC * kDrC));
+    if (AHEAD) {
+      ka.put(sm.K, sm.ld, p.dk);
+      na.put(sm.N);
+      fa.put(sm.rows);
+      if (OUT) {
+        qa.put(sm.Q, sm.ld, p.dk);
+        pa.put(sm.P);
+      }
     } else {
-      store_state(p.S + at * dd, sm.S, p.dk, p.dv, c0);
+      load_rows<T>(sm.K, sm.ld, p.k, p.ks, t0, n, h / p.group, p.dk);
+      load_mat(sm.N, p.N + at * (kDrC * kDrC));
+      load_factors(sm.rows, p.rows + at);
+      if (OUT) {
+        load_rows<T>(sm.Q, sm.ld, p.q, p.qs, t0, n, h / p.group, p.dk);
+        load_mat(sm.P, p.P + at * (kDrC * kDrC));
+      }
+      va.load<T>(p.v, p.vs, t0, n, (size_t)h * p.dv + col, col < p.dv, tm);
     }
+    if (!OUT) store_state(p.S + at * dd, sm.S, p.dk, p.dv, c0);
     float y[4][2], acc[4][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * tm + i;
-      const T *v = static_cast<const T *>(p.v) + (t0 + r) * p.vs + (size_t)h * p.dv + col;
-      const bool live = r < n && col < p.dv;  // dv is even
-      y[i][0] = live ? load1(v) : 0.f;
-      y[i][1] = live ? load1(v + 1) : 0.f;
-    }
+    for (int i = 0; i < 4; ++i) y[i][0] = va.x[i][0], y[i][1] = va.x[i][1];
     __syncthreads();
+    if (AHEAD && (c + 1) * kDrC < len) ahead(c + 1);
     zero(acc);
     mm_nt(acc, sm.K, sm.ld, sm.S, p.dk, tm, tn);
 #pragma unroll
@@ -222,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) dr_chain_kernel(DrProblem p, T *__re
 }
 
 // The chain backwards: Z, the gradients of the states behind the chunks and of the initial state
-template <typename T>
+template <typename T, bool AHEAD>
 __global__ void __launch_bounds__(kThreads) dr_reverse_kernel(DrProblem p, const T *__restrict__ dout, long long dos,
                                                               const float *dfin, float *dinit) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -235,27 +318,49 @@ __global__ void __launch_bounds__(kThreads) dr_reverse_kernel(DrProblem p, const
   load_state(sm.S, dfin ? dfin + ((size_t)seq * p.H + h) * dd : nullptr, p.dk, p.dv, c0);
   const DrRows &rows = *sm.rows;
   const int from = 8 * (tid >> 5);  // N and P are zero above the diagonal: the rows of the warp's 8 columns
+  RowsAhead ka, qa;
+  MatAhead na, pa;
+  FactorsAhead fa;
+  TileAhead da;
+  auto ahead = [&](int c) {
+    const size_t t0 = (size_t)a + c * kDrC, at = (size_t)(slot0 + c) * p.H + h;
+    const int n = min(kDrC, len - c * kDrC);
+    ka.load<T>(p.k, p.ks, t0, n, h / p.group, p.dk);
+    pa.load(p.P + at * (kDrC * kDrC));
+    fa.load(p.rows + at);
+    da.load<T>(dout, dos, t0, n, (size_t)h * p.dv + col, col < p.dv, tm);
+    na.load(p.N + at * (kDrC * kDrC));
+    qa.load<T>(p.q, p.qs, t0, n, h / p.group, p.dk);
+  };
+  if (AHEAD && len > 0) ahead((len - 1) / kDrC);
   for (int c = (len - 1) / kDrC; c * kDrC < len && c >= 0; --c) {
     const size_t t0 = (size_t)a + c * kDrC, at = (size_t)(slot0 + c) * p.H + h;
     const int n = min(kDrC, len - c * kDrC);
     __syncthreads();
+    if (AHEAD) {
+      ka.put(sm.K, sm.ld, p.dk);
+      qa.put(sm.Q, sm.ld, p.dk);
+      na.put(sm.N);
+      pa.put(sm.P);
+      fa.put(sm.rows);
+    } else {
+      load_rows<T>(sm.K, sm.ld, p.k, p.ks, t0, n, h / p.group, p.dk);
+      load_rows<T>(sm.Q, sm.ld, p.q, p.qs, t0, n, h / p.group, p.dk);
+      load_mat(sm.N, p.N + at * (kDrC * kDrC));
+      load_mat(sm.P, p.P + at * (kDrC * kDrC));
+      load_factors(sm.rows, p.rows + at);
+      da.load<T>(dout, dos, t0, n, (size_t)h * p.dv + col, col < p.dv, tm);
+    }
     store_state(p.dS + at * dd, sm.S, p.dk, p.dv, c0);
-    load_rows<T>(sm.K, sm.ld, p.k, p.ks, t0, n, h / p.group, p.dk);
-    load_rows<T>(sm.Q, sm.ld, p.q, p.qs, t0, n, h / p.group, p.dk);
-    load_mat(sm.N, p.N + at * (kDrC * kDrC));
-    load_mat(sm.P, p.P + at * (kDrC * kDrC));
-    load_factors(sm.rows, p.rows + at);
     float dob[4][2], d[4][2], acc[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * tm + i;
-      const T *x = dout + (t0 + r) * dos + (size_t)h * p.dv + col;
-      const bool live = r < n && col < p.dv;
-      dob[i][0] = live ? load1(x) : 0.f;
-      dob[i][1] = live ? load1(x + 1) : 0.f;
+      dob[i][0] = da.x[i][0], dob[i][1] = da.x[i][1];
       *reinterpret_cast<float2 *>(sm.B3 + r * kCols + 2 * tn) = make_float2(dob[i][0], dob[i][1]);
     }
     __syncthreads();
+    if (AHEAD && c > 0) ahead(c - 1);
     zero(d);
     mm_nt(d, sm.K, sm.ld, sm.S, p.dk, tm, tn);
 #pragma unroll
@@ -494,25 +599,33 @@ template <typename T> __global__ void __launch_bounds__(kThreads) dr_finish_kern
 
 dim3 chain_grid(const DrProblem &p) { return dim3((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kCols - 1) / kCols)); }
 
+template <typename T, bool OUT, bool AHEAD> void run_chain(const DrProblem &p, T *o, long long os, float *fin, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(dr_chain_kernel<T, OUT, AHEAD>), ChainShared::bytes(256), allowed);
+  dr_chain_kernel<T, OUT, AHEAD><<<chain_grid(p), kThreads, ChainShared::bytes(p.dk), s>>>(p, o, os, fin);
+}
+template <typename T, bool AHEAD>
+void run_reverse(const DrProblem &p, const T *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  allow_smem(reinterpret_cast<const void *>(dr_reverse_kernel<T, AHEAD>), ChainShared::bytes(256), allowed);
+  dr_reverse_kernel<T, AHEAD><<<chain_grid(p), kThreads, ChainShared::bytes(p.dk), s>>>(p, dout, dos, dfin, dinit);
+}
+constexpr int kAheadWidth = 64;  // of RowsAhead
+
 }  // namespace
 
 template <typename T> void launch_dr_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s) {
-  static std::atomic<uint64_t> allowed_out{0}, allowed_states{0};
-  const int bytes = ChainShared::bytes(p.dk), most = ChainShared::bytes(256);
-  if (o) {
-    allow_smem(reinterpret_cast<const void *>(dr_chain_kernel<T, true>), most, allowed_out);
-    dr_chain_kernel<T, true><<<chain_grid(p), kThreads, bytes, s>>>(p, static_cast<T *>(o), os, fin);
-  } else {
-    allow_smem(reinterpret_cast<const void *>(dr_chain_kernel<T, false>), most, allowed_states);
-    dr_chain_kernel<T, false><<<chain_grid(p), kThreads, bytes, s>>>(p, nullptr, 0, nullptr);
-  }
+  T *to = static_cast<T *>(o);
+  if (p.dk <= kAheadWidth)
+    o ? run_chain<T, true, true>(p, to, os, fin, s) : run_chain<T, false, true>(p, nullptr, 0, nullptr, s);
+  else
+    o ? run_chain<T, true, false>(p, to, os, fin, s) : run_chain<T, false, false>(p, nullptr, 0, nullptr, s);
 }
 
 template <typename T>
 void launch_dr_reverse(const DrProblem &p, const void *dout, long long dos, const float *dfin, float *dinit, cudaStream_t s) {
-  static std::atomic<uint64_t> allowed{0};
-  allow_smem(reinterpret_cast<const void *>(dr_reverse_kernel<T>), ChainShared::bytes(256), allowed);
-  dr_reverse_kernel<T><<<chain_grid(p), kThreads, ChainShared::bytes(p.dk), s>>>(p, static_cast<const T *>(dout), dos, dfin, dinit);
+  const T *from = static_cast<const T *>(dout);
+  p.dk <= kAheadWidth ? run_reverse<T, true>(p, from, dos, dfin, dinit, s) : run_reverse<T, false>(p, from, dos, dfin, dinit, s);
 }
 
 template <typename T>
