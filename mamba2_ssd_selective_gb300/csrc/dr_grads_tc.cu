@@ -296,15 +296,16 @@ __global__ void __launch_bounds__(kThreads, 1) dr_grads_tc_kernel(const __grid_c
         pipe::warp_arrive(&sums_free[m & 1]);
         d[0] += d[1];
         float after = d[0], before = c[0] + c[1];
-        const float two = before;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
           const float z = __shfl_down_sync(0xffffffffu, after, o), w = __shfl_up_sync(0xffffffffu, before, o);
           if (lane + o < 32) after += z;
           if (lane >= o) before += w;
         }
-        after -= d[0];
-        before -= two;
+        // without the lane's own, which may be far larger: no decay has touched what the last row adds
+        const float z = __shfl_down_sync(0xffffffffu, after, 1), w = __shfl_up_sync(0xffffffffu, before, 1);
+        after = lane < 31 ? z : 0.f;
+        before = lane > 0 ? w : 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = 2 * lane + e;
