@@ -14,7 +14,7 @@ namespace {
 struct DrPlan {
   bool tc;
   int slots, seg, places;  // seg: chunks of a segment, 0: sequences are not cut
-  size_t seg_states, seg_sums, status, rows, N, P, S, dS, E, Z, dqp, dkp, total;  // workspace offsets
+  size_t seg_states, seg_sums, status, rows, N, P, A, S, dS, E, Z, dqp, dkp, total;  // workspace offsets
 };
 
 long long dr_rows(const ssd_delta_rule_dims *d) { return d->packed ? d->total_tokens : (long long)d->nseq * d->seqlen; }
@@ -93,6 +93,7 @@ DrPlan dr_plan(const ssd_delta_rule_dims *d, bool backward) {
     pl.Z = take(tokens * d->headdim_v * eb);
     pl.dqp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
     pl.dkp = take(pl.tc ? 0 : tokens * d->headdim_k * 4);
+    pl.A = take(pl.tc ? 0 : chunks * kDrC * kDrC * 4);
   }
   pl.total = off;
   return pl;
@@ -164,6 +165,7 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
     p.seg_states = at(pl->seg_states), p.seg_sums = at(pl->seg_sums);
     p.S = at(pl->S), p.dS = at(pl->dS), p.E = at(pl->E), p.Z = at(pl->Z);
     p.dqp = at(pl->dqp), p.dkp = at(pl->dkp);
+    p.A = pl->A ? at(pl->A) : nullptr;
   }
   return p;
 }

@@ -15,9 +15,13 @@
 //     dA = -dV D^T,   dP = dO D^T (each where its matrix is not zero), and with L_ij = e^(G_i - G_j)
 //     dQ = scale diag(e^G) dO S^T + (scale dP L) K
 //     dK = diag(e^(Gall - G)) D dS^T - diag(e^G) dV S^T + (scale dP L)^T Q + (dA L) K + (dA L)^T K
-//     dlog_decay_t = sum_{i >= t} (q_i.dq_i - v_i.dv_i) + <S_next, dS>
-// The last line: a decay at t scales all that passes from before t to t and later, and both sums count it: q.dq
-// what tokens read, v.dv what they would have read of their own chunk's additions.  (dr_grads_tc.cu counts it otherwise.)
+//     dlog_decay_t = sum_{i >= t} (r_i + sum_j (M_ij - M_ji)) + sum_{j < t} w_j + e^Gall <S, dS>,   M = dP o P + dA o A (j < i)
+//     r_i = e^G_i (scale q_i.(S dO_i) - k_i.(S dV_i)),   w_j = e^(Gall - G_j) k_j.(dS D_j)
+// The last lines count what passes t, which is what a decay at t scales: what tokens from t on read and write over of the
+// state before the chunk (r), what they have of tokens before t (M: the pairs behind t cancel), and what the state behind the
+// chunk has of those (w) and of the state before it.  sum_{i >= t} (q_i.dq_i - v_i.dv_i) + <S_next, dS> is the same, but each
+// token's own addition, which no decay touches, is in both terms and leaves its rounding error: in fp32, of a
+// gradient 0.1% to 1% at log decays of -8, and 3% to 10% at -12.
 // q and k stay as they are (exact as bf16 operands): 1 / |q| and 1 / |k| are part of the rows' factors and of A, P.
 #pragma once
 
@@ -51,7 +55,7 @@ struct DrProblem {
   const float *init;
   // tables, of chunk (slot, head) at slot * H + head
   DrRows *rows;
-  float *N, *P;  // CUDA cores: (64, 64) fp32, element (i, j) at 64 i + j
+  float *N, *P, *A;  // CUDA cores: (64, 64) fp32, element (i, j) at 64 i + j; A for the gradients only, else null
   // backward: the states before the chunks and the gradients of those behind them (dk, dv), E and Z (total, H, dv).
   // Tensor cores: N's and P's two bf16 terms as four tiles of (64, 64) in the 128-byte swizzle, at N; E and Z are bf16,
   // and so are the states, at S and dS, in blocks of 8 columns: element (m, c) of (dk, dv), both padded to 64 or 128, at

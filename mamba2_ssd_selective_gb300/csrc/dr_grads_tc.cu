@@ -6,10 +6,8 @@
 //     dv = b Z,  dbeta = E.Z (rows)
 //     dlog_decay_t = sum_(i >= t) (qin q_i.(dO S^T)_i - kin b_i k_i.(Z S^T)_i) + sum_(i >= t > j) M_ij
 //                    + sum_(j < t) kout b_j k_j.(E dS^T)_j + e^Gall <S, dS>,    M = Wq o (Q K^T) + Wk o (K K^T)
-// (what passes t: what is read and written over from the state before the chunk, what tokens behind t have of tokens
-// before it, what the state behind the chunk has of them and of the state before.  delta.h's sum of q.dq - v.dv is the same, but
-// each token's own addition, which no decay touches, is in both of its terms: with operands of bf16, heads that forget
-// fast had 2% left of that difference.  The sum over pairs goes as row sums less column sums of the same fp32 M.)
+// (what passes t, as at delta.h; here the sum of q.dq - v.dv had 2% left of each token's own addition in heads that forget
+// fast, with operands of bf16.  The sum over pairs goes as row sums less column sums of the same fp32 M.)
 // and the division by the lengths last: dq - q (q.dq) / |q|^2, likewise dk.
 //
 // Persistent CTAs; a CTA takes a chunk and a head of q and k and goes through the states that share it, dq and dk

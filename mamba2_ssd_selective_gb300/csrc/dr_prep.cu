@@ -77,7 +77,9 @@ __global__ void __launch_bounds__(kThreads) dr_prep_kernel(DrProblem p) {
       if (j <= i && i >= sm.nan_at && j < sm.nan_at) l = nan;
       const float rk = sm.rows.rk[j];
       p.P[at * (kDrC * kDrC) + e] = j <= i ? l * sm.qk[i][j] * (sm.rows.rq[i] * rk * p.scale) : 0.f;
-      sm.at[j][i] = j < i ? l * sm.kk[i][j] * (sm.rows.rk[i] * rk) : 0.f;
+      const float a = j < i ? l * sm.kk[i][j] * (sm.rows.rk[i] * rk) : 0.f;
+      sm.at[j][i] = a;
+      if (p.A) p.A[at * (kDrC * kDrC) + e] = a;
     }
     const uint32_t *from = reinterpret_cast<const uint32_t *>(&sm.rows);
     uint32_t *to = reinterpret_cast<uint32_t *>(p.rows + at);

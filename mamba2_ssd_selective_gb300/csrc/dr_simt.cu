@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(kThreads) dr_reverse_kernel(DrProblem p, const
 struct GradShared {
   float stage[kGemmSmemFloats];
   float dqk[kDrC][kDrC + 1], dkk[kDrC][kDrC + 1];  // of the products q.k and k.k, decayed
-  float row[kDrC];                                 // q.dq - v.dv
-  float scratch[8];
+  float pass[kDrC], add[kDrC];                     // what passes to a row, and what a row adds to the state behind the chunk
+  float scratch[8 * kDrC];
   DrRows rows;
 };
 
@@ -420,11 +420,11 @@ __global__ void __launch_bounds__(kThreads) dr_grads_kernel(DrProblem p, const T
   const int hk = h / p.group, dk = p.dk, dv = p.dv;
   const size_t at = (size_t)slot * p.H + h, dd = (size_t)dk * dv;
   load_factors(&sm.rows, p.rows + at);
+  if (tid < kDrC) sm.pass[tid] = sm.add[tid] = 0.f;
   __syncthreads();
   const DrRows &rw = sm.rows;
   const T *q = static_cast<const T *>(p.q) + (size_t)t0 * p.qs + (size_t)hk * dk;
   const T *k = static_cast<const T *>(p.k) + (size_t)t0 * p.ks + (size_t)hk * dk;
-  const T *v = static_cast<const T *>(p.v) + (size_t)t0 * p.vs + (size_t)h * dv;
   const T *dob_ = dout + (size_t)t0 * dos + (size_t)h * dv;
   const float *E = p.E + ((size_t)t0 * p.H + h) * dv, *Z = p.Z + ((size_t)t0 * p.H + h) * dv;
   const float *S = p.S + at * dd, *dS = p.dS + at * dd;
@@ -438,10 +438,25 @@ __global__ void __launch_bounds__(kThreads) dr_grads_kernel(DrProblem p, const T
   auto q_r = [&](int j, int c) { return rw.rq[j] * load1(q + j * p.qs + c); };
   auto k_r = [&](int j, int c) { return rw.rk[j] * load1(k + j * p.ks + c); };
 
-  float acc[4][4], dgall = 0.f;
+  float acc[4][4];
   zero_acc(acc);
   gemm_tile<true, false>(acc, 0, n, 0, n, 0, dv, do_r, d_c, sm.stage);
-  float l[4][4];
+  // M: what passes from token c to a later one r.  A comes from the tables (7 sequences, 5003 tokens, 12 heads of 64: 378 us;
+  // made here again, by a product of k with k, 402)
+  float l[4][4], pairs[4][4];
+  auto add_pairs = [&](const float *table, float sign) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = tm * 4 + i, c = tn * 4;
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(table + at * (kDrC * kDrC) + r * kDrC + c));
+      const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < r && r < n) pairs[i][j] = fmaf(sign * acc[i][j], f[j], pairs[i][j]);
+    }
+  };
+  zero_acc(pairs);
+  add_pairs(p.P, 1.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -452,6 +467,7 @@ __global__ void __launch_bounds__(kThreads) dr_grads_kernel(DrProblem p, const T
     }
   zero_acc(acc);
   gemm_tile<true, false>(acc, 0, n, 0, n, 0, dv, dv_r, d_c, sm.stage);
+  add_pairs(p.A, -1.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -459,26 +475,26 @@ __global__ void __launch_bounds__(kThreads) dr_grads_kernel(DrProblem p, const T
       const int r = tm * 4 + i, c = tn * 4 + j;
       sm.dkk[r][c] = c < r ? -acc[i][j] * l[i][j] : 0.f;
     }
-  // rows: v.dv and dbeta, four threads to a row; dv itself
+  // row sums less column sums of the same values: pairs on one side of a token cancel, but for roundings of their own size
+  tile_rowsum_add(pairs, sm.pass);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) pairs[i][j] = -pairs[i][j];
+  tile_colsum_add(pairs, sm.pass, sm.scratch);
+  // rows: dbeta, four threads to a row; dv itself
   {
     const int r = tid >> 2, part = tid & 3;
-    float vdv = 0.f, db = 0.f;
+    float db = 0.f;
     if (r < n)
       for (int c = part; c < dv; c += 4) {
-        const float z = Z[r * es + c], dvc = rw.beta[r] * z;
-        vdv = fmaf(load1(v + r * p.vs + c), dvc, vdv);
+        const float z = Z[r * es + c];
         db = fmaf(E[r * es + c], z, db);
-        static_cast<T *>(g.dv)[(size_t)(t0 + r) * g.dvs + (size_t)h * dv + c] = from_f<T>(dvc);
+        static_cast<T *>(g.dv)[(size_t)(t0 + r) * g.dvs + (size_t)h * dv + c] = from_f<T>(rw.beta[r] * z);
       }
 #pragma unroll
-    for (int o = 2; o >= 1; o >>= 1) {
-      vdv += __shfl_xor_sync(0xffffffffu, vdv, o);
-      db += __shfl_xor_sync(0xffffffffu, db, o);
-    }
-    if (part == 0) {
-      sm.row[r] = -vdv;
-      if (r < n) static_cast<T *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = from_f<T>(db);
-    }
+    for (int o = 2; o >= 1; o >>= 1) db += __shfl_xor_sync(0xffffffffu, db, o);
+    if (part == 0 && r < n) static_cast<T *>(g.db)[(size_t)(t0 + r) * g.dbs + h] = from_f<T>(db);
   }
   float in_r[4], out_r[4], qin_r[4];  // e^G and e^(Gall - G) of the thread's rows, without lengths
 #pragma unroll
@@ -495,22 +511,23 @@ __global__ void __launch_bounds__(kThreads) dr_grads_kernel(DrProblem p, const T
   for (int n0 = 0; n0 < dk; n0 += kTile) {
     zero_acc(acc);
     gemm_tile<true, false>(acc, 0, n, n0, dk, 0, dv, do_r, s_c, sm.stage);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] *= qin_r[i];
-    gemm_tile<true, true>(acc, 0, n, n0, dk, 0, n, dqk_r, k_r, sm.stage);
-    float dots[4][4];
+    float dots[4][4];  // what is read of the state before the chunk, less what is written over
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = tm * 4 + i, c = n0 + tn * 4 + j;
-        const bool live = r < n && c < dk;
-        if (live) p.dqp[((size_t)(t0 + r) * p.H + h) * dk + c] = acc[i][j];
-        dots[i][j] = live ? acc[i][j] * q_r(r, c) : 0.f;
+        acc[i][j] *= qin_r[i];
+        dots[i][j] = r < n && c < dk ? acc[i][j] * q_r(r, c) : 0.f;
       }
-    tile_rowsum_add(dots, sm.row);
+    gemm_tile<true, true>(acc, 0, n, n0, dk, 0, n, dqk_r, k_r, sm.stage);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = tm * 4 + i, c = n0 + tn * 4 + j;
+        if (r < n && c < dk) p.dqp[((size_t)(t0 + r) * p.H + h) * dk + c] = acc[i][j];
+      }
     float upd[4][4];
     zero_acc(upd);
     gemm_tile<true, false>(upd, 0, n, n0, dk, 0, dv, d_r, ds_c, sm.stage);
@@ -521,10 +538,13 @@ __global__ void __launch_bounds__(kThreads) dr_grads_kernel(DrProblem p, const T
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = tm * 4 + i, c = n0 + tn * 4 + j;
-        const float u = out_r[i] * upd[i][j];
-        if (r < n && c < dk) dgall = fmaf(u, k_r(r, c), dgall);
-        acc[i][j] = u - in_r[i] * acc[i][j];
+        const float u = out_r[i] * upd[i][j], kv = r < n && c < dk ? k_r(r, c) : 0.f, over = in_r[i] * acc[i][j];
+        upd[i][j] = u * kv;
+        dots[i][j] = fmaf(-over, kv, dots[i][j]);
+        acc[i][j] = u - over;
       }
+    tile_rowsum_add(dots, sm.pass);
+    tile_rowsum_add(upd, sm.add);
     gemm_tile<false, true>(acc, 0, n, n0, dk, 0, n, dqk_t, q_r, sm.stage);
     gemm_tile<true, true>(acc, 0, n, n0, dk, 0, n, dkk_b, k_r, sm.stage);
 #pragma unroll
@@ -535,15 +555,14 @@ __global__ void __launch_bounds__(kThreads) dr_grads_kernel(DrProblem p, const T
         if (r < n && c < dk) p.dkp[((size_t)(t0 + r) * p.H + h) * dk + c] = acc[i][j];
       }
   }
-  // <S_next, dS> = e^Gall <S, dS> + sum_j k_j.(what j adds to the state).(dS)
   float ss = 0.f;
   for (int e = tid; e < (int)dd; e += kThreads) ss = fmaf(S[e], dS[e], ss);
-  dgall = fmaf(ss, rw.all_hi + rw.all_lo, dgall);
-  dgall = block_sum256(dgall, sm.scratch);
+  ss = block_sum256(ss, sm.scratch) * (rw.all_hi + rw.all_lo);
   if (tid < n) {
-    float x = dgall;
-    for (int i = n - 1; i >= tid; --i) x += sm.row[i];
-    static_cast<T *>(g.dg)[(size_t)(t0 + tid) * g.dgs + h] = from_f<T>(x);
+    float to = 0.f, behind = 0.f;
+    for (int i = n - 1; i >= tid; --i) to += sm.pass[i];
+    for (int j = 0; j < tid; ++j) behind += sm.add[j];
+    static_cast<T *>(g.dg)[(size_t)(t0 + tid) * g.dgs + h] = from_f<T>(to + behind + ss);
   }
 }
 

@@ -87,21 +87,21 @@ def check(c, lowest=None):
     return got, want
 
 
-@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 64, 64), ("bf16", 128, 128)])
+@pytest.mark.parametrize("dtype,dk,dv", [("f32", 64, 64), ("f32", 128, 40), ("bf16", 64, 64), ("bf16", 128, 128), ("bf16", 136, 64)])
 @pytest.mark.parametrize("norm", [True, False])
 def test_heads_that_forget_fast(dtype, dk, dv, norm):
     rates = torch.tensor([-0.25, -1.0, -3.0, -5.0, -8.0, -12.0, -16.0, -30.0])
     check(Case([140, 77, 1], 8, 4, dk, dv, dtype, norm=norm, seed=71, decay=rates))
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 64)])
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 136)])
 @pytest.mark.parametrize("decay", [float("-inf"), -1e30])
 def test_nothing_passes_a_head_that_forgets_everything(decay, dtype, d):
     got, want = check(Case([150, 66], 2, 1, d, 64, dtype, seed=72, decay=torch.tensor([decay])), lowest=-300.0)
     assert want.abs().max() < 1e-30 and (got == 0).all()
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 64)])
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 136)])
 def test_nothing_passes_a_reset(dtype, d):
     """Token 70 of 140 forgets everything: its gradient is what sums over its chunk's other pairs leave in fp32."""
     c = Case([140], 2, 2, d, 64, dtype, packed=False, seed=73)
