@@ -417,15 +417,15 @@ typedef struct {
 size_t ssd_delta_rule_workspace_size(const ssd_delta_rule_dims *dims, int backward);
 
 /* Forward.  final_states: the state after each sequence's last token, or NULL; it may be initial_states itself, which
- * are then updated in place.  o must not overlap an input: one that starts where an input does is refused
- * (SSD_ERR_INVALID_DIMS). */
+ * are then updated in place.  Outputs must not overlap each other or anything else that is read: one that starts where
+ * an input or another output does is refused (SSD_ERR_INVALID_DIMS). */
 ssd_status ssd_delta_rule_forward(const ssd_delta_rule_dims *dims, const ssd_delta_rule_inputs *in, void *o,
                                   int64_t o_tok_stride, float *final_states, void *workspace, size_t ws_bytes,
                                   ssd_stream_t stream);
 
 /* Backward of <do, o> + <dfinal_states, final_states> (dfinal_states NULL: zero).  do is named dout here: layout rules
- * of o.  Nothing but the inputs is needed from the forward pass.  Gradients must not overlap what is read: an output
- * that starts where an input does is refused (SSD_ERR_INVALID_DIMS). */
+ * of o.  Nothing but the inputs is needed from the forward pass.  Gradients must not overlap each other or what is read:
+ * one that starts where an input or another gradient does is refused (SSD_ERR_INVALID_DIMS). */
 ssd_status ssd_delta_rule_backward(const ssd_delta_rule_dims *dims, const ssd_delta_rule_inputs *in, const void *dout,
                                    int64_t dout_tok_stride, const float *dfinal_states,
                                    const ssd_delta_rule_grads *grads, void *workspace, size_t ws_bytes,
@@ -433,7 +433,7 @@ ssd_status ssd_delta_rule_backward(const ssd_delta_rule_dims *dims, const ssd_de
 
 /* One token of each of dims.nseq rows (dims.seqlen must be 1, dims.packed 0), against a cache of states (nslots, nheads,
  * headdim_k, headdim_v) fp32, updated in place: slots, rows without one, and refusals are those of
- * ssd_linear_attn_step.  No workspace. */
+ * ssd_linear_attn_step; o and the cache are refused where they meet each other or an input, too.  No workspace. */
 ssd_status ssd_delta_rule_step(const ssd_delta_rule_dims *dims, const ssd_delta_rule_inputs *in, float *states,
                                int32_t nslots, const int32_t *slot_idx, void *o, int64_t o_tok_stride,
                                ssd_stream_t stream);
@@ -449,7 +449,7 @@ ssd_status ssd_delta_rule_step(const ssd_delta_rule_dims *dims, const ssd_delta_
  * move as 16-byte vectors, even ones two elements at a time, others one by one.  post_weight, branch_scale, pre_weight
  * (channels) fp32, or NULL (1).  y is made of h before it is rounded.
  * h: may be NULL with pre_norm, and may be the residual itself, with its stride (the stream updated in place); other
- * outputs that start where an input does are refused (SSD_ERR_INVALID_DIMS).  rstd_post (rows) and rstd_pre (rows) fp32,
+ * outputs that start where an input or another output does are refused (SSD_ERR_INVALID_DIMS).  rstd_post (rows) and rstd_pre (rows) fp32,
  * 1 / rms, are written with their norm, each may be NULL; the backward pass reads them.
  * Envelope: at most 16384 channels and 2^30 rows, row strides below 2^31 elements; else SSD_ERR_UNSUPPORTED.  All sums
  * have a fixed order. */
@@ -481,7 +481,8 @@ typedef struct {
 } ssd_block_norm_saved;
 
 /* Gradients, written (not accumulated).  dz exactly with dims.gate, dresidual exactly with dims.residual; dresidual may
- * be dh itself, with its stride.  Parameter gradients (channels) fp32, each may be NULL; dpost_weight only with
+ * be dh itself, with its stride; else rows' gradients that start where an input does, and any two that start at the same
+ * place, are refused (SSD_ERR_INVALID_DIMS).  Parameter gradients (channels) fp32, each may be NULL; dpost_weight only with
  * post_norm, dpre_weight only with pre_norm. */
 typedef struct {
   void *dx; int64_t dx_row_stride;

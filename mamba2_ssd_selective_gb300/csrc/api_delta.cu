@@ -9,6 +9,16 @@ using namespace ssd;
 
 namespace {
 
+// two of these outputs that start at the same place, or one where one of the inputs does
+bool outputs_meet(std::initializer_list<const void *> outputs, std::initializer_list<const void *> inputs) {
+  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+    if (on_input(*o, inputs)) return true;
+    for (auto other = outputs.begin(); other != o; ++other)
+      if (*o && *o == *other) return true;
+  }
+  return false;
+}
+
 // ---------------------------------------------------------------- gated delta rule
 
 struct DrPlan {
@@ -282,7 +292,9 @@ ssd_status ssd_delta_rule_forward(const ssd_delta_rule_dims *dims, const ssd_del
   const DrPlan pl = dr_plan(dims, false);
   st = dr_check_workspace(pl, workspace, ws_bytes);
   if (st != SSD_OK) return st;
-  if (on_input(o, {in->q, in->k, in->v, in->log_decay, in->beta})) return SSD_ERR_INVALID_DIMS;
+  if (outputs_meet({o, final_states}, {in->q, in->k, in->v, in->log_decay, in->beta, in->cu_seqlens}) ||
+      on_input(o, {in->initial_states}))
+    return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const DrProblem p = dr_problem(dims, in, &pl, static_cast<char *>(workspace));
   return dims->dtype == SSD_BF16 ? dr_forward_impl<__nv_bfloat16>(p, pl.tc, o, o_tok_stride, final_states, s)
@@ -309,9 +321,9 @@ ssd_status ssd_delta_rule_backward(const ssd_delta_rule_dims *dims, const ssd_de
   const DrPlan pl = dr_plan(dims, true);
   st = dr_check_workspace(pl, workspace, ws_bytes);
   if (st != SSD_OK) return st;
-  for (const void *out : {grads->dq, grads->dk, grads->dv, grads->dlog_decay, grads->dbeta})
-    if (on_input(out, {in->q, in->k, in->v, in->log_decay, in->beta, dout})) return SSD_ERR_INVALID_DIMS;
-  if (on_input(grads->dinitial_states, {in->initial_states, dfinal_states})) return SSD_ERR_INVALID_DIMS;
+  if (outputs_meet({grads->dq, grads->dk, grads->dv, grads->dlog_decay, grads->dbeta, grads->dinitial_states},
+                   {in->q, in->k, in->v, in->log_decay, in->beta, in->initial_states, in->cu_seqlens, dout, dfinal_states}))
+    return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const DrProblem p = dr_problem(dims, in, &pl, static_cast<char *>(workspace));
   return dims->dtype == SSD_BF16 ? dr_backward_impl<__nv_bfloat16>(p, pl.tc, dout, dout_tok_stride, dfinal_states, grads, s)
@@ -331,7 +343,7 @@ ssd_status ssd_delta_rule_step(const ssd_delta_rule_dims *dims, const ssd_delta_
   if (!states) return SSD_ERR_NULL_PTR;
   if (nslots <= 0) return SSD_ERR_INVALID_DIMS;
   if (!aligned(states, 16) || !aligned(slot_idx, 4)) return SSD_ERR_ALIGNMENT;
-  if (on_input(o, {in->q, in->k, in->v, in->log_decay, in->beta})) return SSD_ERR_INVALID_DIMS;
+  if (outputs_meet({o, states}, {in->q, in->k, in->v, in->log_decay, in->beta, slot_idx})) return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const DrProblem p = dr_problem(dims, in, nullptr, nullptr);
   if (dims->dtype == SSD_BF16)
@@ -358,7 +370,8 @@ ssd_status ssd_block_norm_forward(const ssd_block_norm_dims *dims, const ssd_blo
   if (st != SSD_OK) return st;
   if ((rstd_post && !dims->post_norm) || (rstd_pre && !dims->pre_norm)) return SSD_ERR_INVALID_DIMS;
   if (!aligned(rstd_post, 4) || !aligned(rstd_pre, 4)) return SSD_ERR_ALIGNMENT;
-  if (on_input(h, {in->x, in->z}) || on_input(y, {in->x, in->z, in->residual}) || (h && h == y) ||
+  if (outputs_meet({h, y, rstd_post, rstd_pre}, {in->x, in->z, in->post_weight, in->branch_scale, in->pre_weight}) ||
+      outputs_meet({y, rstd_post, rstd_pre}, {in->residual}) ||
       (h && h == in->residual && h_row_stride != in->residual_row_stride))
     return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -400,9 +413,12 @@ ssd_status ssd_block_norm_backward(const ssd_block_norm_dims *dims, const ssd_bl
     if (!aligned(q, 4)) return SSD_ERR_ALIGNMENT;
   if (!workspace || ws_bytes < ssd_block_norm_workspace_size(dims)) return SSD_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SSD_ERR_ALIGNMENT;
-  for (const void *out : {(const void *)grads->dx, (const void *)grads->dz, (const void *)grads->dresidual})
-    if (on_input(out, {in->x, in->z, saved->h, saved->dy})) return SSD_ERR_INVALID_DIMS;
-  if (on_input(saved->dh, {grads->dx, grads->dz}) ||
+  // (the parameters' sums are written when everything has been read)
+  if (outputs_meet({grads->dx, grads->dz, grads->dresidual},
+                   {in->x, in->z, in->post_weight, in->branch_scale, in->pre_weight, saved->h, saved->dy, saved->rstd_post,
+                    saved->rstd_pre}) ||
+      outputs_meet({grads->dx, grads->dz, grads->dresidual, grads->dpost_weight, grads->dbranch_scale, grads->dpre_weight}, {}) ||
+      on_input(saved->dh, {grads->dx, grads->dz}) ||
       (on_input(saved->dh, {grads->dresidual}) && saved->dh_row_stride != grads->dresidual_row_stride))
     return SSD_ERR_INVALID_DIMS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
