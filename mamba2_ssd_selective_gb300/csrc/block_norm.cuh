@@ -4,9 +4,10 @@
 // Bytes bound them: every tensor is read and written once, a row's values wait in its threads' registers from
 // the first sum to the last store.  A row is a warp's (up to 256 channels) or a block's.  Blocks whose rows can be
 // moved as whole 16-byte units go through many rows, with the next ones on their way into shared memory by bulk copies.
-// All parts, bf16: 16384 x 4096 forward 128 us (5.2 TB/s), gradients of 8192 x 4096 with an fp32 stream 174 us (4.2 TB/s)
-// and 8 us for the parameters' sums.  What is left: backward has a block of 256 threads to an SM (255 registers), whose
-// sums over the row have nothing beside them.
+// All parts, bf16: 16384 x 4096 forward 128 us (5.2 TB/s), gradients of 8192 x 4096 with an fp32 stream 172 us, and 8 us
+// for the parameters' sums (177 together, 4.2 TB/s).  What is left: backward has a block of 256 threads to an SM (255
+// registers), whose sums over the row have nothing beside them.  From 4097 channels on it has 512 threads of 128
+// registers, which spill: 4096 x 8192 take 368 us, 6554 x 5120 426.
 #pragma once
 
 #include <type_traits>

@@ -5,8 +5,8 @@
 // Two kernels.  Many states of usual widths: a block on each SM goes through whole states, which bulk copies bring to
 // shared memory and back, two on their way in while one is worked on.  Else a block takes 64 or 32 columns of one state, the
 // layout of la_step.cu, all of a thread's elements in registers.  Between its loads and its stores stands a sum over the
-// block, so that its memory is idle for a while: 256 rows, 32 heads of 128 x 128 took 235 us with it, and take 159 us
-// (6.8 TB/s) with the first.
+// block, so that its memory is idle for a while: 256 rows, 32 heads of 128 x 128 took 235 us with it, and take 165 us
+// (6.5 TB/s) with the first.
 #include <type_traits>
 
 #include "delta.h"
