@@ -376,8 +376,10 @@ ssd_status ssd_group_norm_backward(const ssd_group_norm_dims *dims, const ssd_gr
  * beta element aligned with any stride of at least nheads.  log_decay is at most 0 (below -256 it counts as -256, which
  * forgets everything; -inf is allowed).  States (nseq, nheads, headdim_k, headdim_v) fp32, contiguous, 16-byte aligned.
  * Arithmetic: fp32.  bf16 tensors with both widths at most 128 take products of bf16 operands with fp32 sums; what ends in
- * a state is a sum of products of two bf16 terms each (states within about 3e-6 of their size; fp32 tensors: 3e-7), other
- * operands are rounded once (outputs within about 0.003 of theirs, gradients 0.004; one rounding to bf16 alone is 0.0017).
+ * a state or an output is a sum of products of two bf16 terms each (states within about 3e-6 of their size; fp32 tensors:
+ * 3e-7; outputs within their one rounding, 0.0017), operands of gradients are rounded once (0.004).  Where keys are nearly
+ * equal, additions cancel and errors add up: states 2e-5, gradients 0.01; with beta |k|^2 near 2 as well, where the rule itself
+ * magnifies errors, 1e-3 and 0.02 (fp32 tensors: 2e-5 and 4e-5).
  * A NaN or infinity in a token can reach every output of the same 64-token chunk of its own sequence and head, and those
  * of later tokens (gradients: of all tokens); other sequences are not affected.
  * Envelope: headdim_k and headdim_v multiples of 8, at most 256; otherwise as linear attention, else

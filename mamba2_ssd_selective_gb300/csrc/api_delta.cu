@@ -49,20 +49,20 @@ ssd_status dr_check_dims(const ssd_delta_rule_dims *d) {
 bool dr_use_tc(const ssd_delta_rule_dims *d) { return d->dtype == SSD_BF16 && la_tc_envelope(d->headdim_k, d->headdim_v); }
 
 // Chunks of a segment, or 0: whether sequences are cut is a matter of their number, since a chain is an SM's however few
-// there are.  Times measured here with states of 128 x 128 (and taken for narrower ones too), in us: a chunk of a chain 2.6, a chunk of a segment's sums 2.4 (there are two, for all
-// segments but the last), the scan 4 a segment, two launches more 12.  Lengths of packed sequences are not known: the
-// longest of n is taken for its mean where sequences end at random.  (A workspace's size may be asked for where there is
-// no GPU: the SMs are not asked.)
+// there are.  Times measured here with states of 128 x 128 (and taken for narrower ones too), in us: a chunk of a chain 2.7,
+// a chunk of a segment's sums 2.4 (there are two, for all segments but the last), the scan 4 a segment, two launches more
+// 12.  Lengths of packed sequences are not known: the longest of n is taken for its mean where sequences end at random.  (A
+// workspace's size may be asked for where there is no GPU: the SMs are not asked.)
 int dr_segment_chunks(const ssd_delta_rule_dims *d) {
   const long long sms = 152, items = (long long)d->nseq * d->nheads, n = d->nseq;
   const double part = d->packed ? (std::log((double)n) + 0.577 + 0.5 / (double)n) / (double)n : 1.;
   const long long chunks = (long long)((double)(d->packed ? d->total_tokens : d->seqlen) * (part < 1. ? part : 1.) / kDrC) + 1;
   auto rounds = [&](long long x) { return (double)((x + sms - 1) / sms); };
-  double best = rounds(items) * 2.6 * (double)chunks;
+  double best = rounds(items) * 2.7 * (double)chunks;
   int seg = 0;
   for (long long k = 2; k <= 64 && 4 * k <= chunks; ++k) {
     const long long len = (chunks + k - 1) / k;
-    const double cost = rounds(2 * items * (k - 1)) * 2.4 * (double)len + rounds(items * k) * 2.6 * (double)len + 4. * (double)k + 12.;
+    const double cost = rounds(2 * items * (k - 1)) * 2.4 * (double)len + rounds(items * k) * 2.7 * (double)len + 4. * (double)k + 12.;
     if (cost < best) {
       best = cost;
       seg = (int)len;
@@ -182,7 +182,7 @@ DrProblem dr_problem(const ssd_delta_rule_dims *d, const ssd_delta_rule_inputs *
 
 template <typename T>
 ssd_status dr_forward_impl(const DrProblem &p, bool tc, void *o, int64_t os, float *fin, cudaStream_t s) {
-  SSD_LAUNCH("dr_prep", tc ? launch_dr_prep_tc(p, false, s) : launch_dr_prep<T>(p, s));
+  SSD_LAUNCH("dr_prep", tc ? launch_dr_prep_tc(p, s) : launch_dr_prep<T>(p, s));
   if (p.seg) {
     SSD_LAUNCH("dr_sums", launch_dr_tc_sums(p, s));
     SSD_LAUNCH("dr_scan", launch_dr_tc_scan(p, fin, s));
@@ -197,7 +197,7 @@ ssd_status dr_backward_impl(const DrProblem &p, bool tc, const void *dout, int64
   const DrGrads out{g->dq, g->dk, g->dv, g->dlog_decay, g->dbeta, g->dq_tok_stride, g->dk_tok_stride, g->dv_tok_stride,
                     g->dlog_decay_tok_stride, g->dbeta_tok_stride};
   if (tc) {
-    SSD_LAUNCH("dr_prep", launch_dr_prep_tc(p, true, s));
+    SSD_LAUNCH("dr_prep", launch_dr_prep_tc(p, s));
     SSD_LAUNCH("dr_chain", launch_dr_tc_chain(p, nullptr, 0, nullptr, s));
     SSD_LAUNCH("dr_reverse", launch_dr_tc_reverse(p, dout, dos, dfin, g->dinitial_states, s));
     SSD_LAUNCH("dr_grads", launch_dr_grads_tc(p, dout, dos, out, s));

@@ -146,8 +146,8 @@ __device__ __forceinline__ void dr_segment(const DrProblem &p, int seg, int plac
 
 // dr_prep.cu: rows' factors, N and P of every chunk
 template <typename T> void launch_dr_prep(const DrProblem &p, cudaStream_t s);
-// dr_prep_tc.cu: the same for the tensor-core chains (P's second term for backward only)
-void launch_dr_prep_tc(const DrProblem &p, bool backward, cudaStream_t s);
+// dr_prep_tc.cu: the same for the tensor-core chains
+void launch_dr_prep_tc(const DrProblem &p, cudaStream_t s);
 // dr_tc.cu: the chains for bf16, both widths at most 128
 void launch_dr_tc_chain(const DrProblem &p, void *o, long long os, float *fin, cudaStream_t s);
 // cut sequences: the segments' M and N, then the states before them, and the final ones of empty sequences

@@ -9,8 +9,8 @@
 //     N_IJ = M - N_II (b_I M),    M = A_IJ - sum_(J <= K < I) A_IK (b_K N_KJ),
 // transposed, so that what a step makes is the next one's first operand as it stands in the registers.  Both operands are
 // sums of two bf16 terms, which is how N goes out too.
-// 4 x 8192 tokens, 16 heads of q and k for 32 states take 195 us (with products of 16 and 32 rows in fp32 on the CUDA cores
-// 239 us), their bytes 104 us at 6.8 TB/s.  What bounds it is latency: a block's steps follow one another, and registers and
+// 4 x 8192 tokens, 16 heads of q and k for 32 states take 205 us, their bytes 124 us at 6.8 TB/s (with one term of P 195 us;
+// with products of 16 and 32 rows in fp32 on the CUDA cores 239 us).  What bounds it is latency: a block's steps follow one another, and registers and
 // shared memory let four blocks onto an SM (a third of the instructions that it could issue).
 #include "delta.h"
 #include "dr_rows.cuh"
@@ -109,8 +109,7 @@ __device__ __forceinline__ float lds(uint32_t at) { return pipe::lds_f(at); }
 
 __device__ __forceinline__ void sts(uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 
-// PT: terms of P that are wanted
-template <int KB, int PT>
+template <int KB>
 __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_constant__ CUtensorMap tq,
                                                                  const __grid_constant__ CUtensorMap tk, const DrProblem p) {
   extern __shared__ uint8_t smem_raw[];
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
         uint32_t qh, ql;
         tc::split2(q[0], q[1], qh, ql);
         sts(s0 + kTilesP + at_j, qh);
-        if (PT == 2) sts(s0 + kTilesP + at_j + kBox, ql);
+        sts(s0 + kTilesP + at_j + kBox, ql);
       }
     }
     fence_async_smem();
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
     __syncthreads();
     if (tid == kThreads - 1) {
       pipe::bulk_store(p.rows + at, smem_u32(&rows), sizeof(DrRows));
-      pipe::bulk_store(reinterpret_cast<uint8_t *>(p.N) + at * (4 * kDrTile) + 2 * kDrTile, s0 + kTilesP, PT * kBox);
+      pipe::bulk_store(reinterpret_cast<uint8_t *>(p.N) + at * (4 * kDrTile) + 2 * kDrTile, s0 + kTilesP, 2 * kBox);
       bulk_commit();
     }
     if (tid >= kDrC) {
@@ -316,26 +315,21 @@ __global__ void __launch_bounds__(kThreads, 4) dr_prep_tc_kernel(const __grid_co
   if (tid == 0 || tid == kThreads - 1) bulk_wait_read0();
 }
 
-template <int KB, int PT> void run(const DrProblem &p, cudaStream_t s) {
+template <int KB> void run(const DrProblem &p, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
   constexpr int bytes = kSmemBytes;
-  allow_smem(reinterpret_cast<const void *>(dr_prep_tc_kernel<KB, PT>), bytes, allowed);
+  allow_smem(reinterpret_cast<const void *>(dr_prep_tc_kernel<KB>), bytes, allowed);
   CUtensorMap tq, tk;
   if (!encode_tmap_bf16_heads(&tq, p.q, p.dk, p.Hk, p.total, p.qs * 2, kDrC) ||
       !encode_tmap_bf16_heads(&tk, p.k, p.dk, p.Hk, p.total, p.ks * 2, kDrC)) {
     note_host_error();
     return;
   }
-  dr_prep_tc_kernel<KB, PT><<<dim3((unsigned)p.slots, (unsigned)p.Hk), kThreads, bytes, s>>>(tq, tk, p);
+  dr_prep_tc_kernel<KB><<<dim3((unsigned)p.slots, (unsigned)p.Hk), kThreads, bytes, s>>>(tq, tk, p);
 }
 
 }  // namespace
 
-void launch_dr_prep_tc(const DrProblem &p, bool backward, cudaStream_t s) {
-  if (la_tc_boxes(p.dk) == 1)
-    backward ? run<1, 2>(p, s) : run<1, 1>(p, s);
-  else
-    backward ? run<2, 2>(p, s) : run<2, 1>(p, s);
-}
+void launch_dr_prep_tc(const DrProblem &p, cudaStream_t s) { la_tc_boxes(p.dk) == 1 ? run<1>(p, s) : run<2>(p, s); }
 
 }  // namespace ssd

@@ -4,14 +4,16 @@
 // A CTA takes one sequence and head and walks its chunks.  Everything is formed transposed, so that dv (up to 128)
 // fills the accumulators' lanes and the state stays in its warps' registers (lane = dv):
 //     X^T = S^T K^T,   Y = V - kin X,   E = Y - N (b Y),   S = e^Gall S + W,   W^T = (kout b E)^T K
-//     O^T = (qin S^T Q^T) + (b E)^T P^T
+//     O^T = (qin S^T Q^T) + (b E)^T P^T                     (b E and P in two terms as well)
 // In reverse the same four steps, with the gradient of the state for the state:
 //     X^T = dS^T K^T,   dD = kout X + P^T dO,   Z = dD - N^T (b dD),   dS = e^Gall dS + W,
 //     W^T = (qin dO)^T Q - (kin b Z)^T K
 // What ends in a state is a sum in fp32, and an operand that is not a bf16 tensor of the user's is a sum of two bf16 terms
 // (16 bits; products of the two low terms are left out), which leaves a relative error of about 3e-6 in a state: 1/1000 of
 // a bf16 tensor's own rounding.  A third term would make it fp32's; it takes half as many products again of
-// X and W, twice those of N, and the columns of TMEM that W has.
+// X and W, twice those of N, and the columns of TMEM that W has.  Outputs are 0.0017 off, by their one rounding.  (With b E
+// and P in one term each they were 0.0026 off, and 0.01 where keys are nearly equal and a chunk's additions cancel; the second
+// terms, made and multiplied beside W, took 3.5% more of a chain and 5% of the tables.)
 //
 // Warps:
 //   0       TMA producer: K, Q, V (reverse: dO), and the chunk's N, P and row factors, two stages
@@ -21,8 +23,8 @@
 //   12-19   state
 //   20-23   outputs; in reverse the two terms of (qin dO)^T
 // What bounds it: the chain from state to state, its products (16 of X, 12 of N, 8 of W, 46 to 66 cycles each) and
-// five hand-offs between tensor core and warps.  4 x 8192 tokens, 32 heads of 128 (128 chains of 128 chunks): 308 us,
-// 2.4 us a chunk; 2 x 8192 tokens with the states and E kept 296 us, in reverse 384 us.  A CTA has an SM to
+// five hand-offs between tensor core and warps.  4 x 8192 tokens, 32 heads of 128 (128 chains of 128 chunks): 320 us,
+// 2.5 us a chunk; 2 x 8192 tokens with the states and E kept 296 us, in reverse 384 us.  A CTA has an SM to
 // itself (TMEM, shared memory), so fewer chains than SMs leave SMs idle: dr_segment_chunks in api_delta.cu cuts them.
 #include "delta.h"
 #include "tc_pipe.cuh"
@@ -42,7 +44,7 @@ constexpr uint32_t kBox = 8192;  // [64 rows x 64 columns] bf16
 constexpr int kStages = 2;
 
 // TMEM columns: the state's terms (64 each), X and then N's product, outputs (reverse: P^T dO), the terms of b Y and then
-// of the additions (32 each), b E for the outputs or the terms of qin dO, W
+// of the additions (32 each), those of b E for the outputs or of qin dO, W
 constexpr uint32_t kTmS = 0, kTmX = 128, kTmO = 192, kTmY = 256, kTmD = 320, kTmW = 384, kTmCols = 512;
 
 enum Mode { kOut, kStates, kReverse, kSum };  // outputs; states and E for the backward pass; the reverse chain; only the last state
@@ -67,6 +69,7 @@ struct Bars {
   uint64_t *y_ready;      // b Y's terms in TMEM
   uint64_t *n_full;       // N's product
   uint64_t *d_ready;      // the additions' terms in TMEM
+  uint64_t *e_ready;      // and those for the outputs
   uint64_t *w_full;       // W
   uint64_t *q_full, *q_ready;  // outputs' part of the state formed / scaled; reverse: W's part of dO formed / its terms in TMEM
   uint64_t *o_full, *o_free;   // outputs formed / read; reverse: P^T dO
@@ -86,6 +89,7 @@ struct Bars {
     o_full = patched + 9;
     o_free = patched + 10;
     drain = patched + 11;
+    e_ready = patched + 12;
   }
 };
 
@@ -177,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
     mbar_init(bar.y_ready, 4 * VB);
     mbar_init(bar.n_full, 1);
     mbar_init(bar.d_ready, 4 * VB);
+    mbar_init(bar.e_ready, 4 * VB);
     mbar_init(bar.w_full, 1);
     mbar_init(bar.q_full, 1);
     mbar_init(bar.q_ready, 2 * VB);
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           const size_t at = (size_t)(slot0 + chunk(i)) * p.H + h;
           const uint8_t *tiles = reinterpret_cast<const uint8_t *>(p.N) + at * (4 * kBox);
           constexpr uint32_t kQBytes = MODE == kStates || MODE == kSum ? 0 : KB * kBox;
-          constexpr uint32_t kMats = MODE == kOut ? 3 * kBox : MODE == kReverse ? 4 * kBox : 2 * kBox;
+          constexpr uint32_t kMats = MODE == kOut || MODE == kReverse ? 4 * kBox : 2 * kBox;
           mbar_expect_tx(&bar.full[st], KB * kBox + kQBytes + (unit ? 0 : VB * kBox) + kMats + (uint32_t)sizeof(DrRows));
           for (int b = 0; b < KB; ++b) tma_load_3d(base + L::kK + b * kBox, &args.k, &bar.full[st], 64 * b, hk, row);
           if (!unit)
@@ -305,8 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         umma_commit_el(el, bar.w_full);
         if (MODE == kOut) {
           wait_on(bar.q_ready, parity(i), wait);
+          wait_on(bar.e_ready, parity(i), wait);
           tc_fence_after();
           pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmD, dP + at(i), 8, pipe::kStepK, iKK, true);
+          pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmD + 32, dP + at(i), 8, pipe::kStepK, iKK, true);
+          pipe::umma_ts_k_el<4>(el, tmem + kTmO, tmem + kTmD, dP + at(i) + kB, 8, pipe::kStepK, iKK, true);
           umma_commit_el(el, bar.o_full);
         }
         umma_commit_el(el, &bar.free[i % kStages]);
@@ -438,17 +446,15 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
           uint32_t t0[8], t1[8], t2[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint64_t add = fma2(pk2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kMinusOne, y[q][e]), d = mul2(beta[e >> 1], add);
+            y[q][e] = fma2(pk2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kMinusOne, y[q][e]);
             float v0, v1;
-            upk2(MODE == kOut ? d : add, v0, v1);
-            if (MODE != kSum) t2[e] = tc::pack_bf16x2(v0, v1);
-            split2(mul2(f[e >> 1], d), t0[e], t1[e]);
+            upk2(y[q][e], v0, v1);
+            if (kKeeps) t2[e] = tc::pack_bf16x2(v0, v1);
+            split2(mul2(f[e >> 1], mul2(beta[e >> 1], y[q][e])), t0[e], t1[e]);
           }
           tmem_st_16x128_async(at + kTmY + 16 * sub, t0);
           tmem_st_16x128_async(at + kTmY + 32 + 16 * sub, t1);
-          if (MODE == kOut) {
-            tmem_st_16x128_async(at + kTmD + 16 * sub, t2);
-          } else if (kKeeps) {  // E or Z, rows of tokens, into the staging tile
+          if (kKeeps) {  // E or Z, rows of tokens, into the staging tile
             const int c = fc + 16 * q;
             const uint32_t to = so + (uint32_t)(c >> 6) * kBox + sw128_offset(32 * sub + fi, c & 63);
             stmatrix4_trans(to, t2[0], t2[1], t2[2], t2[3]);
@@ -458,6 +464,20 @@ __global__ void __launch_bounds__(kThreads, 1) dr_tc_kernel(const __grid_constan
         tmem_wait_st();
         tc_fence_before();
         pipe::warp_arrive(bar.d_ready);
+        if (MODE == kOut) {  // beside W
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t at = lanes + ((uint32_t)(16 * q) << 16);
+            uint32_t t0[8], t1[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split2(mul2(beta[e >> 1], y[q][e]), t0[e], t1[e]);
+            tmem_st_16x128_async(at + kTmD + 16 * sub, t0);
+            tmem_st_16x128_async(at + kTmD + 32 + 16 * sub, t1);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          pipe::warp_arrive(bar.e_ready);
+        }
         pipe::warp_arrive(&bar.free[i % kStages]);
         if (kKeeps) {
           fence_async_smem();
